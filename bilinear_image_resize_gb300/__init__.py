@@ -19,7 +19,8 @@ from ._native import (KIND_F32, KIND_FILTER3X3, KIND_NORMALIZE, KIND_U8, RZ_BORD
                       RZ_ERR_UNSUPPORTED, RZ_F32, RZ_LINEAR, RZ_MAX_DIM, RZ_NEAREST, RZ_NOALLOC_MAX_DIM, RZ_OK,
                       RZ_OPT_CTAS_PER_SM, RZ_OPT_GENERIC_ONLY, RZ_OPT_GRID_MODE, RZ_OPT_PDL, RZ_OPT_RING_ROWS,
                       RZ_MULTI_MAX_JOBS, RZ_OPT_F32_KERNEL, RZ_OPT_FILTER_KERNEL, RZ_OPT_L2_PREFETCH, RZ_COPY_PDL, RZ_COPY_L2_PREFETCH, RZ_FILTER_AUTO, RZ_FILTER_FP32, RZ_FILTER_TENSOR, RZ_OPT_STAGES, RZ_OPT_U8_KERNEL, RZ_U8,
-                      RzEpilogue, RzJob)
+                      RZ_ACT_GELU, RZ_ACT_NONE, RZ_ACT_SILU, RZ_BF16, RZ_F16, RzDrop, RzEpilogue, RzJob, RzMap, RzNorm,
+                      RzResample)
 
 __all__ = [
     "ResizeError", "Plan", "resize_plan_create", "resize_plan_destroy", "resize_plan_status",
@@ -38,6 +39,9 @@ __all__ = [
     "RZ_OPT_RING_ROWS", "RZ_OPT_U8_KERNEL", "RZ_OPT_L2_PREFETCH",
     "resize_copy_baseline", "RZ_COPY_PDL", "RZ_COPY_L2_PREFETCH",
     "RZ_FILTER_AUTO", "RZ_FILTER_FP32", "RZ_FILTER_TENSOR",
+    "map_group_norm", "map_group_norm_grad", "map_group_norm_workspace", "map_dropout",
+    "resize_map", "resize_map_grad", "resize_map_grad_workspace",
+    "RZ_BF16", "RZ_F16", "RZ_ACT_NONE", "RZ_ACT_SILU", "RZ_ACT_GELU",
 ]
 
 
@@ -363,6 +367,186 @@ def resize_u8_multi(jobs, njobs: int, C: int, mode: int = RZ_LINEAR, status=None
     _check(_native.load().resize_u8_multi(jobs.data_ptr() if njobs else None, njobs, C, mode,
                                           status.data_ptr() if status is not None else None, _stream(stream)),
            "resize_u8_multi")
+
+
+_MAP_DTYPES: dict = {}
+
+
+def _map_dtype(t, name: str) -> int:
+    if not _MAP_DTYPES:
+        import torch
+        _MAP_DTYPES.update({torch.float32: RZ_F32, torch.bfloat16: RZ_BF16, torch.float16: RZ_F16})
+    code = _MAP_DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _map_of(t, name: str, shape=None):
+    """((N, H, W, C), rz_map) of an (N, H, W, C) or (H, W, C) tensor whose pixels are packed; `shape`: what it must be."""
+    if t.dim() == 4:
+        N, H, W, C = t.shape
+        sn, sh, sw, sc = t.stride()
+    elif t.dim() == 3:
+        H, W, C = t.shape
+        N, sn, (sh, sw, sc) = 1, 0, t.stride()
+    else:
+        raise ValueError(f"{name}: expected NxHxWxC or HxWxC, got shape {tuple(t.shape)}")
+    if shape is not None and (N, H, W, C) != shape:
+        raise ValueError(f"{name}: shape {(N, H, W, C)}, expected {shape}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.numel() and ((C > 1 and sc != 1) or (W > 1 and sw != C)):
+        raise ValueError(f"{name}: pixels must be packed (channels last)")
+    es = t.element_size()
+    return (N, H, W, C), RzMap(t.data_ptr(), sh * es if H > 1 else W * C * es, sn * es if N > 1 else 0)
+
+
+def _floats(t, name: str, *shape):
+    """Pointer of a packed float32 CUDA tensor of that shape (None: a null pointer)."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected a contiguous float32 CUDA tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def _drop_of(drop):
+    return None if drop is None else RzDrop(float(drop[0]), int(drop[1]) & 0xFFFFFFFFFFFFFFFF,
+                                            int(drop[2]) & 0xFFFFFFFFFFFFFFFF if len(drop) > 2 else 0)
+
+
+def _workspace(workspace, nbytes: int, like, stream):
+    """The caller's workspace, or one of `nbytes` that belongs to the call's stream."""
+    import torch
+    if workspace is not None or nbytes == 0:
+        return workspace
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=like.device) if stream else torch.cuda.default_stream(like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
+def _bytes_of(workspace):
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def map_dropout(x, y, p: float, seed: int, offset: int = 0, residual=None, stream=None) -> None:
+    """y[:] = dropout(x) + residual with the counter-based mask of (p, seed,
+    offset); called on dy without a residual it is the gradient towards x.
+    Any shape, packed or in the (N, H, W, C) layout of the other maps; y may
+    be x or the residual."""
+    dtype = _map_dtype(x, "x")
+    if y.dtype != x.dtype or (residual is not None and residual.dtype != x.dtype):
+        raise ValueError("x, y and residual differ in dtype")
+    if y.shape != x.shape or (residual is not None and residual.shape != x.shape):
+        raise ValueError("x, y and residual differ in shape")
+    if all(t is None or t.is_contiguous() for t in (x, y, residual)):
+        # any shape whose elements follow one another: rows of the last dimension
+        rows = (x.numel() // x.shape[-1], 1, x.shape[-1], 1) if x.numel() and x.dim() else (1, 1, x.numel(), 1)
+        x, y, residual = (None if t is None else t.view(rows) for t in (x, y, residual))
+    shape, mx = _map_of(x, "x")
+    _, my = _map_of(y, "y")
+    mr = None if residual is None else _map_of(residual, "residual")[1]
+    _check(_native.load().map_dropout(mx, mr, my, *shape, dtype, _drop_of((p, seed, offset)), _stream(stream)),
+           "map_dropout")
+
+
+def _norm_of(shape, groups, x, act, eps):
+    return RzNorm(*shape, groups, _map_dtype(x, "x"), act, eps)
+
+
+def _norm_workspace(d) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_native.load().map_group_norm_workspace(d, ctypes.byref(n)), "map_group_norm_workspace")
+    return n.value
+
+
+def map_group_norm_workspace(x, groups: int) -> int:
+    """Bytes of workspace that map_group_norm and map_group_norm_grad need on a map like x."""
+    return _norm_workspace(_norm_of(_map_of(x, "x")[0], groups, x, RZ_ACT_NONE, 1.0))
+
+
+def map_group_norm(x, y, groups: int, gamma=None, beta=None, mean=None, rstd=None, act: int = RZ_ACT_NONE,
+                   eps: float = 1e-5, drop=None, workspace=None, stream=None) -> None:
+    """y[:] = dropout(act(group_norm(x))) on (N, H, W, C) or (H, W, C) maps.
+
+    gamma, beta: float32 (C,) or None; mean, rstd: float32 (N, groups) written
+    for the gradient, or None; act: RZ_ACT_*; drop: (p, seed, offset) or None;
+    workspace: a CUDA tensor of map_group_norm_workspace(x, groups) bytes, or
+    None to take one from torch's allocator."""
+    shape, mx = _map_of(x, "x")
+    _, my = _map_of(y, "y", shape)
+    if y.dtype != x.dtype:
+        raise ValueError("x and y differ in dtype")
+    N, C = shape[0], shape[3]
+    d = _norm_of(shape, groups, x, act, eps)
+    ws = _workspace(workspace, _norm_workspace(d) if workspace is None else 0, x, stream)
+    _check(_native.load().map_group_norm(
+        d, _drop_of(drop), mx, my, _floats(gamma, "gamma", C), _floats(beta, "beta", C),
+        _floats(mean, "mean", N, groups), _floats(rstd, "rstd", N, groups), *_bytes_of(ws), _stream(stream)),
+        "map_group_norm")
+
+
+def map_group_norm_grad(dy, x, dx, groups: int, gamma=None, beta=None, mean=None, rstd=None, dgamma=None, dbeta=None,
+                        act: int = RZ_ACT_NONE, eps: float = 1e-5, drop=None, workspace=None, stream=None) -> None:
+    """dx[:], dgamma[:] and dbeta[:] (either may be None) from dy, with the
+    arguments of the map_group_norm call and the mean and rstd it wrote."""
+    shape, mx = _map_of(x, "x")
+    _, md = _map_of(dy, "dy", shape)
+    _, mo = _map_of(dx, "dx", shape)
+    if dy.dtype != x.dtype or dx.dtype != x.dtype:
+        raise ValueError("x, dy and dx differ in dtype")
+    N, C = shape[0], shape[3]
+    d = _norm_of(shape, groups, x, act, eps)
+    ws = _workspace(workspace, _norm_workspace(d) if workspace is None else 0, x, stream)
+    _check(_native.load().map_group_norm_grad(
+        d, _drop_of(drop), md, mx, mo, _floats(gamma, "gamma", C), _floats(beta, "beta", C),
+        _floats(mean, "mean", N, groups), _floats(rstd, "rstd", N, groups), _floats(dgamma, "dgamma", C),
+        _floats(dbeta, "dbeta", C), *_bytes_of(ws), _stream(stream)), "map_group_norm_grad")
+
+
+def _resample_of(src, dst, names):
+    (Ns, H, W, C), ms = _map_of(src, names[0])
+    (N, OH, OW, C2), md = _map_of(dst, names[1])
+    if C2 != C or Ns not in (1, N):
+        raise ValueError(f"{names[0]} and {names[1]} differ in channels or images")
+    return RzResample(N, Ns, H, W, OH, OW, C, _map_dtype(dst, names[1]), _map_dtype(src, names[0])), ms, md
+
+
+def resize_map(src, dst, base=None, stream=None) -> None:
+    """dst[:] = base + the bilinear resize of src, on (N, H, W, C) or (H, W, C)
+    maps with any number of channels.  A src of one image serves every image of
+    dst (a position table); it may be float32 where dst is 16-bit."""
+    d, ms, md = _resample_of(src, dst, ("src", "dst"))
+    mb = None
+    if base is not None:
+        if base.dtype != dst.dtype:
+            raise ValueError("base and dst differ in dtype")
+        mb = _map_of(base, "base", (d.N, d.out_h, d.out_w, d.C))[1]
+    _check(_native.load().resize_map(d, ms, mb, md, _stream(stream)), "resize_map")
+
+
+def resize_map_grad_workspace(ddst, dsrc) -> int:
+    """Bytes of workspace that resize_map_grad needs for these maps."""
+    n = ctypes.c_size_t(0)
+    _check(_native.load().resize_map_grad_workspace(_resample_of(dsrc, ddst, ("dsrc", "ddst"))[0], ctypes.byref(n)),
+           "resize_map_grad_workspace")
+    return n.value
+
+
+def resize_map_grad(ddst, dsrc, workspace=None, stream=None) -> None:
+    """dsrc[:] = the gradient of resize_map towards src, from ddst; summed over
+    the images where dsrc has one."""
+    d, ms, md = _resample_of(dsrc, ddst, ("dsrc", "ddst"))
+    n = ctypes.c_size_t(0)
+    if workspace is None:
+        _check(_native.load().resize_map_grad_workspace(d, ctypes.byref(n)), "resize_map_grad_workspace")
+    ws = _workspace(workspace, n.value, ddst, stream)
+    _check(_native.load().resize_map_grad(d, md, ms, *_bytes_of(ws), _stream(stream)), "resize_map_grad")
 
 
 class Texture:

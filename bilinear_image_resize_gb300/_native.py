@@ -14,6 +14,8 @@ RZ_NEAREST = 0
 RZ_LINEAR = 1
 RZ_U8 = 0
 RZ_F32 = 1
+RZ_BF16 = 2
+RZ_F16 = 3
 RZ_EPI_NORMALIZE_NCHW = 1
 RZ_EPI_FILTER3X3 = 2
 RZ_EPI_GRAY_RGB = 3
@@ -45,6 +47,10 @@ RZ_OPT_L2_PREFETCH = 10
 RZ_FILTER_AUTO = 0
 RZ_FILTER_FP32 = 1
 RZ_FILTER_TENSOR = 2
+
+RZ_ACT_NONE = 0
+RZ_ACT_SILU = 1
+RZ_ACT_GELU = 2
 
 RZ_COPY_PDL = 1
 RZ_COPY_L2_PREFETCH = 2
@@ -90,6 +96,55 @@ class RzJob(ctypes.Structure):
 
 RZ_MULTI_MAX_JOBS = 2048
 
+
+class RzMap(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("pitch", ctypes.c_size_t),
+        ("batch_stride", ctypes.c_size_t),
+    ]
+
+
+class RzDrop(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_double),
+        ("seed", ctypes.c_size_t),
+        ("offset", ctypes.c_size_t),
+    ]
+
+
+class RzNorm(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("W", ctypes.c_int),
+        ("C", ctypes.c_int),
+        ("groups", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("act", ctypes.c_int),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class RzResample(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int),
+        ("src_n", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("W", ctypes.c_int),
+        ("out_h", ctypes.c_int),
+        ("out_w", ctypes.c_int),
+        ("C", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("src_dtype", ctypes.c_int),
+    ]
+
+
+_map = ctypes.POINTER(RzMap)
+_drop = ctypes.POINTER(RzDrop)
+_norm = ctypes.POINTER(RzNorm)
+_resample = ctypes.POINTER(RzResample)
+
 # name -> (restype, argtypes); every symbol include/gbresize.h declares
 SIGNATURES = {
     "resize_plan_create": (_i, [ctypes.POINTER(_p), _i, _i, _i, _i, _i, _p]),
@@ -117,6 +172,13 @@ SIGNATURES = {
     "resize_last_cuda_error": (_i, []),
     "resize_u8_noalloc": (_i, [_p, _sz, _p, _sz, _i, _i, _i, _i, _i, _i, _p]),
     "resize_copy_baseline": (_i, [_p, _p, _sz, _i, _p]),
+    "map_dropout": (_i, [_map, _map, _map, _i, _i, _i, _i, _i, _drop, _p]),
+    "map_group_norm_workspace": (_i, [_norm, ctypes.POINTER(_sz)]),
+    "map_group_norm": (_i, [_norm, _drop, _map, _map, _p, _p, _p, _p, _p, _sz, _p]),
+    "map_group_norm_grad": (_i, [_norm, _drop, _map, _map, _map, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "resize_map": (_i, [_resample, _map, _map, _map, _p]),
+    "resize_map_grad_workspace": (_i, [_resample, ctypes.POINTER(_sz)]),
+    "resize_map_grad": (_i, [_resample, _map, _map, _p, _sz, _p]),
 }
 
 _lib = None

@@ -1,0 +1,275 @@
+// Shared by the feature-map operators (group_norm.cu, map_dropout.cu,
+// resize_map.cu): element types, channels-last addressing, the activation
+// functions and the counter-based generator.  Maps are (N, H, W, C) with the
+// pixels of a row packed, a byte pitch between rows and a byte stride between
+// images.  All arithmetic is float32; a 16-bit result is rounded once, as it
+// is stored.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "gbresize.h"
+
+namespace rz {
+namespace maps {
+
+// ------------------------------------------------------------------ host side
+
+inline size_t dtype_size(int dtype) { return dtype == RZ_F32 ? 4 : (dtype == RZ_BF16 || dtype == RZ_F16) ? 2 : 0; }
+
+// A map's geometry as the entry points check it.
+struct Shape {
+    long long N, H, W, C;
+    size_t es;
+    size_t row() const { return static_cast<size_t>(W) * static_cast<size_t>(C) * es; }
+    bool empty() const { return N == 0 || H == 0 || W == 0; }
+    // bytes from the first to past the last element of a non-empty map
+    size_t extent(const rz_map &m) const
+    {
+        return static_cast<size_t>(N - 1) * m.batch_stride + static_cast<size_t>(H - 1) * m.pitch + row();
+    }
+};
+
+inline bool map_overlap(const rz_map &a, const Shape &sa, const rz_map &b, const Shape &sb)
+{
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.data), pb = reinterpret_cast<uintptr_t>(b.data);
+    return pa < pb + sb.extent(b) && pb < pa + sa.extent(a);
+}
+
+// Geometry limits: no negative size, C in [1, RZ_MAX_DIM], at most 2^31 - 1
+// pixels an image (the kernels count pixels in 32 bits) and 2^46 elements, so
+// that no offset wraps 64 bits.
+inline bool shape_ok(const Shape &s)
+{
+    if (s.N < 0 || s.H < 0 || s.W < 0 || s.C < 1 || s.C > RZ_MAX_DIM) return false;
+    const long long px = s.H * s.W;
+    return px <= 0x7fffffffLL && (px == 0 || s.N <= (1LL << 46) / (px * s.C));
+}
+
+// Pointer, alignment, pitch and stride of one map (of a non-empty shape).
+inline bool map_ok(const rz_map *m, const Shape &s)
+{
+    if (!m || !m->data) return false;
+    if (reinterpret_cast<uintptr_t>(m->data) % s.es || m->pitch % s.es || m->batch_stride % s.es) return false;
+    if (m->pitch > (size_t{1} << 46) || m->batch_stride > (size_t{1} << 46)) return false;
+    if (s.H > 1 && m->pitch < s.row()) return false;
+    if (s.N > 1 && m->batch_stride < static_cast<size_t>(s.H - 1) * m->pitch + s.row()) return false;
+    return true;
+}
+
+inline bool rows_joined(const rz_map &m, const Shape &s) { return s.H == 1 || m.pitch == s.row(); }
+
+// Whether every vector of `bytes` at a multiple of `bytes` from a row's start
+// is aligned.
+inline bool map_aligned(const rz_map &m, const Shape &s, size_t bytes)
+{
+    return reinterpret_cast<uintptr_t>(m.data) % bytes == 0 && (s.H == 1 || m.pitch % bytes == 0) &&
+           (s.N == 1 || m.batch_stride % bytes == 0);
+}
+
+// The same elements at the same places.
+inline bool map_same(const rz_map &a, const rz_map &b, const Shape &s)
+{
+    return a.data == b.data && (s.H == 1 || a.pitch == b.pitch) && (s.N == 1 || a.batch_stride == b.batch_stride);
+}
+
+// Launch of one kernel on `stream`; chained launches of one call are
+// programmatic dependents of their predecessors.  Returns a cudaError_t.
+template <class... P, class... A>
+inline cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, size_t smem, void *stream, A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+
+// ---------------------------------------------------------------- device side
+
+// A map as a kernel reads it; W is the number of pixels in a row, the whole
+// image where its rows follow one another without padding.
+struct View {
+    uint8_t *p;
+    long long pitch, bstride;
+};
+
+inline View view(const rz_map *m)
+{
+    return {static_cast<uint8_t *>(m->data), static_cast<long long>(m->pitch), static_cast<long long>(m->batch_stride)};
+}
+
+// Byte offset of pixel `px` of an image with W pixels a row, px_bytes each.
+__device__ __forceinline__ long long pixel_off(unsigned px, unsigned W, bool joined, long long pitch, int px_bytes)
+{
+    if (joined) return static_cast<long long>(px) * px_bytes;
+    const unsigned row = px / W;
+    return row * pitch + static_cast<long long>(px - row * W) * px_bytes;
+}
+
+// VE consecutive elements of type T, moved as one access.
+template <int BYTES> struct RawOf;
+template <> struct RawOf<2> { using type = unsigned short; };
+template <> struct RawOf<4> { using type = unsigned; };
+template <> struct RawOf<8> { using type = uint2; };
+template <> struct RawOf<16> { using type = uint4; };
+template <> struct RawOf<32> { struct alignas(16) type { uint4 a, b; }; };
+template <class T, int VE> using Raw = typename RawOf<sizeof(T) * VE>::type;
+
+__device__ __forceinline__ void unpack_pair(unsigned w, float &a, float &b, __nv_bfloat16)
+{
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack_pair(unsigned w, float &a, float &b, __half)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    a = f.x;
+    b = f.y;
+}
+__device__ __forceinline__ unsigned pack_pair(float a, float b, __nv_bfloat16)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+__device__ __forceinline__ unsigned pack_pair(float a, float b, __half)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+
+template <class T, int VE>
+__device__ __forceinline__ void unpack(const Raw<T, VE> &r, float (&f)[VE])
+{
+    if constexpr (sizeof(T) == 4) {
+        const float *s = reinterpret_cast<const float *>(&r);
+#pragma unroll
+        for (int i = 0; i < VE; i++) f[i] = s[i];
+    } else if constexpr (VE == 1) {
+        f[0] = static_cast<float>(*reinterpret_cast<const T *>(&r));
+    } else {
+        const unsigned *w = reinterpret_cast<const unsigned *>(&r);
+#pragma unroll
+        for (int i = 0; i < VE / 2; i++) unpack_pair(w[i], f[2 * i], f[2 * i + 1], T{});
+    }
+}
+
+template <class T, int VE>
+__device__ __forceinline__ Raw<T, VE> pack(const float (&f)[VE])
+{
+    Raw<T, VE> r;
+    if constexpr (sizeof(T) == 4) {
+        float *s = reinterpret_cast<float *>(&r);
+#pragma unroll
+        for (int i = 0; i < VE; i++) s[i] = f[i];
+    } else if constexpr (VE == 1) {
+        const T h = static_cast<T>(f[0]);
+        r = *reinterpret_cast<const Raw<T, VE> *>(&h);
+    } else {
+        unsigned *w = reinterpret_cast<unsigned *>(&r);
+#pragma unroll
+        for (int i = 0; i < VE / 2; i++) w[i] = pack_pair(f[2 * i], f[2 * i + 1], T{});
+    }
+    return r;
+}
+
+// Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
+// easy as 1, 2, 3", SC'11): ten rounds on the counter (block, offset) under
+// the key `seed`.  Its four words are cut into eight 16-bit lanes, lane j the
+// low or high half of word j / 2, so that one block serves eight elements:
+// 16 bits set the drop rate to 1 / 65536, which the scale takes into account,
+// and halve the generator's work, the larger part of the arithmetic.
+__device__ __forceinline__ uint4 philox(unsigned long long block, unsigned long long offset, unsigned long long seed)
+{
+    uint4 c = {static_cast<unsigned>(block), static_cast<unsigned>(block >> 32), static_cast<unsigned>(offset),
+               static_cast<unsigned>(offset >> 32)};
+    unsigned k0 = static_cast<unsigned>(seed), k1 = static_cast<unsigned>(seed >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; r++) {
+        const unsigned long long a = static_cast<unsigned long long>(c.x) * 0xD2511F53u;
+        const unsigned long long b = static_cast<unsigned long long>(c.z) * 0xCD9E8D57u;
+        c = {static_cast<unsigned>(b >> 32) ^ c.y ^ k0, static_cast<unsigned>(b),
+             static_cast<unsigned>(a >> 32) ^ c.w ^ k1, static_cast<unsigned>(a)};
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return c;
+}
+
+// The mask of a dropout: an element is kept where its 16 bits are above
+// `top` = round(65536 p) - 1, and then multiplied by `scale`.
+struct Drop {
+    unsigned long long seed, offset;
+    unsigned limit;   // top << 16 | 0xffff
+    float scale;
+};
+
+// Drop rate in 65536ths, half-up; 0 drops nothing.
+inline unsigned drop_threshold(const rz_drop *d) { return d ? static_cast<unsigned>(d->p * 65536.0 + 0.5) : 0u; }
+inline bool drop_ok(const rz_drop *d) { return !d || (d->p >= 0.0 && d->p <= 1.0); }
+inline Drop make_drop(const rz_drop *d)
+{
+    const unsigned t = drop_threshold(d);
+    if (t == 0) return {0, 0, 0, 1.0f};
+    return {d->seed, d->offset, (t - 1) << 16 | 0xffffu, t < 65536 ? static_cast<float>(65536.0 / (65536 - t)) : 0.0f};
+}
+
+// f[i] = kept ? f[i] * scale : 0 for the VE elements from `e` (a multiple of
+// VE, which divides eight).  A dropped element is 0 whatever it held.
+template <int VE>
+__device__ __forceinline__ void drop_elements(float (&f)[VE], unsigned long long e, const Drop &d)
+{
+    const uint4 c = philox(e >> 3, d.offset, d.seed);
+    if constexpr (VE == 8) {
+        const unsigned w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 0; i < 8; i++) f[i] = ((i & 1) ? w[i / 2] : w[i / 2] << 16) > d.limit ? f[i] * d.scale : 0.0f;
+    } else if constexpr (VE == 4) {
+        const bool high = e & 4;
+        const unsigned w[2] = {high ? c.z : c.x, high ? c.w : c.y};
+#pragma unroll
+        for (int i = 0; i < 4; i++) f[i] = ((i & 1) ? w[i / 2] : w[i / 2] << 16) > d.limit ? f[i] * d.scale : 0.0f;
+    } else {
+        static_assert(VE == 1, "");
+        const int j = static_cast<int>(e & 7);
+        const unsigned w = (j & 4) ? ((j & 2) ? c.w : c.z) : ((j & 2) ? c.y : c.x);
+        f[0] = ((j & 1) ? w : w << 16) > d.limit ? f[0] * d.scale : 0.0f;
+    }
+}
+
+// Activations and their derivatives.
+__device__ __forceinline__ float sigmoidf(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z)
+{
+    if constexpr (ACT == RZ_ACT_SILU) return z * sigmoidf(z);
+    if constexpr (ACT == RZ_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z)
+{
+    if constexpr (ACT == RZ_ACT_SILU) {
+        const float s = sigmoidf(z);
+        return s * fmaf(z, 1.0f - s, 1.0f);
+    }
+    if constexpr (ACT == RZ_ACT_GELU)
+        return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), fmaf(0.5f, erff(z * 0.70710678f), 0.5f));
+    return 1.0f;
+}
+
+}  // namespace maps
+}  // namespace rz

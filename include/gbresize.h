@@ -400,6 +400,134 @@ RZ_API int resize_wait_selftest(int *dev_status, int limit_us, void *stream);
 #define RZ_COPY_L2_PREFETCH 2
 RZ_API int resize_copy_baseline(const void *src, void *dst, size_t bytes, int flags, void *stream);
 
+/*
+ * ---- Feature maps -----------------------------------------------------------
+ *
+ * Operators of the models that resized frames go into, on channels-last maps
+ * (N, H, W, C) of float32, bfloat16 or float16 (RZ_F32, RZ_BF16, RZ_F16), with
+ * any C up to RZ_MAX_DIM.  A map is given by its device pointer, the byte pitch between rows
+ * (>= W * C elements; ignored for H = 1) and the byte stride between images
+ * (>= an image; ignored for N = 1), all multiples of the element size; pixels
+ * of a row are packed.  The struct itself is host memory, read during the call.
+ * Sizes are not negative, C >= 1, H * W < 2^31 and N * H * W * C <= 2^46.  Arithmetic and every sum, statistic and gradient is float32; 16-bit
+ * results are rounded once, to nearest even, as they are stored.  Results do
+ * not depend on timing: the same call gives the same bits.
+ */
+#define RZ_BF16 2
+#define RZ_F16 3
+
+typedef struct {
+    void *data;
+    size_t pitch;
+    size_t batch_stride;
+} rz_map;
+
+/*
+ * Dropout from a counter.  Element e of a map, counted in the order of its
+ * packed (N, H, W, C) layout whatever its pitches, takes 16 bits h of
+ * Philox4x32-10 (Salmon et al., SC'11) under the key `seed` (low word first)
+ * on the counter (e / 8 low, e / 8 high, offset low, offset high): with
+ * j = e % 8, the low (j even) or high (j odd) half of word j / 2.  It is kept
+ * where h >= t, t = floor(65536 p + 1/2), and then multiplied by
+ * 65536 / (65536 - t), the inverse of the rate at which it is kept; else it
+ * becomes 0, whatever it held.  The mask is never stored: a call with the same
+ * seed and offset makes it again.  0 <= p <= 1; t = 0 leaves the map as it is.
+ */
+typedef struct {
+    double p;
+    size_t seed;
+    size_t offset;
+} rz_drop;
+
+/*
+ * y = dropout(x) + residual (residual may be NULL).  The gradient towards x
+ * of an incoming dy is the same call on dy, without a residual; the one towards
+ * the residual is dy itself.  x, y and residual share the shape and dtype.  y
+ * may be x or the residual themselves (the same pointer, pitch and stride), and
+ * must not overlap them otherwise.  Asynchronous on `stream`; no allocation.
+ * An empty map is RZ_OK.
+ */
+RZ_API int map_dropout(const rz_map *x, const rz_map *residual, const rz_map *y, int N, int H, int W, int C,
+                       int dtype, const rz_drop *drop, void *stream);
+
+/*
+ * Group norm with an activation and dropout.  For image n and group g of
+ * C / groups neighbouring channels, over its M = H W C / groups values:
+ *   mean = sum x / M, rstd = 1 / sqrt(sum (x - mean)^2 / M + eps),
+ *   y = drop(act((x - mean) rstd gamma[c] + beta[c])).
+ * act: RZ_ACT_NONE, RZ_ACT_SILU (z sigmoid(z)) or RZ_ACT_GELU (z Phi(z), Phi
+ * the normal distribution function).  gamma and beta: device float[C], or NULL
+ * for 1 and 0.  mean and rstd: device float[N][groups], written for the
+ * gradient (either may be NULL).  drop: NULL for none.  C a multiple of
+ * groups; eps > 0, finite; N <= 65535 (RZ_ERR_UNSUPPORTED above).  x and y
+ * must not overlap.
+ *
+ * workspace: device memory of at least the bytes that
+ * map_group_norm_workspace gives for this descriptor (enough for the gradient
+ * too), 16-byte aligned, of any content, the call's own until the stream has
+ * passed it.  Asynchronous on `stream`; no allocation.  An empty map is RZ_OK.
+ */
+#define RZ_ACT_NONE 0
+#define RZ_ACT_SILU 1
+#define RZ_ACT_GELU 2
+typedef struct {
+    int N, H, W, C;
+    int groups;
+    int dtype;
+    int act;
+    float eps;
+} rz_norm;
+RZ_API int map_group_norm_workspace(const rz_norm *d, size_t *bytes);
+RZ_API int map_group_norm(const rz_norm *d, const rz_drop *drop, const rz_map *x, const rz_map *y, const float *gamma,
+                          const float *beta, float *mean, float *rstd, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * The gradient of map_group_norm: from dy, the call's x, gamma, beta, drop and
+ * the mean and rstd that it wrote,
+ *   dz = drop(dy) act'(z),  dbeta[c] = sum dz,  dgamma[c] = sum dz xh,
+ *   dx = rstd (gamma dz - sum_group(gamma dz) / M - xh sum_group(gamma dz xh) / M),
+ * xh = (x - mean) rstd.  dgamma and dbeta (device float[C], either may be NULL)
+ * are written, not added to; an empty map makes them 0.  dx must not overlap x
+ * or dy.  Workspace and the rest as map_group_norm.
+ */
+RZ_API int map_group_norm_grad(const rz_norm *d, const rz_drop *drop, const rz_map *dy, const rz_map *x,
+                               const rz_map *dx, const float *gamma, const float *beta, const float *mean,
+                               const float *rstd, float *dgamma, float *dbeta, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * Bilinear resize of a map under the clamp rule of resize_plan_create, with
+ * the weights of resize_f32 (u = r / den as float): dst[n] = base[n] +
+ * resize(src[n]).  No plan is needed.  src: H x W, src_n images, N or 1 (one
+ * table for every image: a learned position table brought to the grid of the
+ * images and added to them), of src_dtype, which is dtype or RZ_F32.  dst and
+ * base: N images of out_h x out_w, of dtype; base may be NULL, or dst itself
+ * (the same pointer, pitch and stride).  H, W >= 1 and H, W, out_h, out_w <=
+ * RZ_MAX_DIM.  dst overlaps neither src nor, otherwise, base.  Asynchronous on
+ * `stream`; no allocation.  An empty dst is RZ_OK.
+ */
+typedef struct {
+    int N, src_n;
+    int H, W, out_h, out_w, C;
+    int dtype, src_dtype;
+} rz_resample;
+RZ_API int resize_map(const rz_resample *d, const rz_map *src, const rz_map *base, const rz_map *dst, void *stream);
+
+/*
+ * The gradient of resize_map towards src: dsrc[n] = the transposed resize of
+ * ddst[n] (of dtype), or of the sum over the N images where src_n is 1; dsrc
+ * (of src_dtype) is written, not added to.  The gradient towards base is ddst
+ * itself.  Source pixels that no output pixel read, and all of them where ddst
+ * is empty, become 0.  Each dsrc value is summed in a fixed order.
+ * workspace: device memory of at least the bytes resize_map_grad_workspace
+ * gives (may be 0 bytes, then NULL is accepted), 16-byte aligned, of any
+ * content, the call's own until the stream has passed it.
+ */
+RZ_API int resize_map_grad_workspace(const rz_resample *d, size_t *bytes);
+RZ_API int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_map *dsrc, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static string). */
 RZ_API const char *resize_strerror(int code);
 
