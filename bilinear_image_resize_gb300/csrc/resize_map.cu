@@ -21,10 +21,12 @@ namespace {
 using namespace maps;
 
 constexpr int kMapThreads = 256;
+constexpr int kMapRun = 16;     // rows a thread walks, at most
 
 struct ResampleArgs {
     View src, base, dst;        // gradient: dst is ddst, src is dsrc; base.p null: none
     int N, src_n, H, W, OH, OW, C;
+    int run;                    // rows a thread walks
     float *sum;                 // gradient of a table: [OH][OW][C], ddst summed over the images
 };
 
@@ -63,42 +65,69 @@ __device__ __forceinline__ const Raw<T, VE> *map_at(const View &v, long long n, 
                                                 (static_cast<long long>(x) * C + c) * static_cast<int>(sizeof(T)));
 }
 
-// A thread forms one vector of channels of one output pixel: once for every
-// image where the source is one table, else for image blockIdx.z.
+// A thread forms one column of output pixels, one vector of channels wide,
+// over the block's run of rows.  It holds the horizontally interpolated values
+// of the two source rows at hand and takes the lower one over as the next
+// upper one, so an upscale reads each source row about once per run where a
+// pixel on its own would read four taps; the sampling positions of the rows
+// are formed once per block.  A table serves every image: it is interpolated
+// once and added to each image's base.
 template <class S, class T, int VE>
 __global__ void __launch_bounds__(kMapThreads) k_resize_map(const ResampleArgs a)
 {
+    __shared__ Tap taps[kMapRun];
     dev::grid_launch_dependents();
-    dev::grid_dependency_wait();
-    const int vecs = a.C / VE;
-    const long long i = blockIdx.x * static_cast<long long>(kMapThreads) + threadIdx.x;
-    if (i >= static_cast<long long>(a.OW) * vecs) return;
-    const int ox = static_cast<int>(i / vecs), c = static_cast<int>(i - static_cast<long long>(ox) * vecs) * VE;
+    const int y0 = blockIdx.y * a.run, rows = min(a.run, a.OH - y0), s = blockIdx.z;
+    if (threadIdx.x < rows) taps[threadIdx.x] = tap(y0 + threadIdx.x, a.H, a.OH);
+    __syncthreads();
+    const unsigned vecs = a.C / VE;
+    const unsigned i = blockIdx.x * kMapThreads + threadIdx.x;
+    if (i >= a.OW * vecs) return;
+    const int ox = static_cast<int>(i / vecs), c = static_cast<int>(i - ox * vecs) * VE;
     const Tap tx = tap(ox, a.W, a.OW);
-    for (int oy = blockIdx.y; oy < a.OH; oy += gridDim.y) {
-        const Tap ty = tap(oy, a.H, a.OH);
-        for (int s = blockIdx.z; s < a.src_n; s += gridDim.z) {
-            float p[VE], q[VE], out[VE];
-            unpack<S, VE>(*map_at<S, VE>(a.src, s, ty.a, tx.a, a.C, c), p);
-            unpack<S, VE>(*map_at<S, VE>(a.src, s, ty.a, tx.b, a.C, c), q);
+    const bool table = a.src_n == 1;
+    const int n0 = table ? 0 : s, n1 = table ? a.N : s + 1;
+    float up[VE], low[VE];
+    int iu = -1, il = -1;
+    const auto across = [&](int y, float (&f)[VE]) {
+        float q[VE];
+        const Raw<S, VE> ra = *map_at<S, VE>(a.src, s, y, tx.a, a.C, c), rb = *map_at<S, VE>(a.src, s, y, tx.b, a.C, c);
+        unpack<S, VE>(ra, f);
+        unpack<S, VE>(rb, q);
 #pragma unroll
-            for (int k = 0; k < VE; k++) out[k] = fmaf(tx.u, q[k] - p[k], p[k]);
-            unpack<S, VE>(*map_at<S, VE>(a.src, s, ty.b, tx.a, a.C, c), p);
-            unpack<S, VE>(*map_at<S, VE>(a.src, s, ty.b, tx.b, a.C, c), q);
+        for (int k = 0; k < VE; k++) f[k] = fmaf(tx.u, q[k] - f[k], f[k]);
+    };
+    const auto copy = [](float (&to)[VE], const float (&from)[VE]) {
 #pragma unroll
-            for (int k = 0; k < VE; k++) out[k] = fmaf(ty.u, fmaf(tx.u, q[k] - p[k], p[k]) - out[k], out[k]);
-            const int n0 = a.src_n == 1 ? 0 : s, n1 = a.src_n == 1 ? a.N : s + 1;
-            for (int n = n0; n < n1; n++) {
-                float f[VE];
+        for (int k = 0; k < VE; k++) to[k] = from[k];
+    };
+    dev::grid_dependency_wait();
+    for (int j = 0; j < rows; j++) {
+        const Tap ty = taps[j];
+        if (ty.a != iu) {
+            if (ty.a == il) copy(up, low);
+            else across(ty.a, up);
+            iu = ty.a;
+        }
+        if (ty.b != il) {
+            if (ty.b == iu) copy(low, up);
+            else across(ty.b, low);
+            il = ty.b;
+        }
+        float out[VE];
 #pragma unroll
-                for (int k = 0; k < VE; k++) f[k] = out[k];
-                if (a.base.p) {
-                    unpack<T, VE>(__ldcs(map_at<T, VE>(a.base, n, oy, ox, a.C, c)), p);
+        for (int k = 0; k < VE; k++) out[k] = fmaf(ty.u, low[k] - up[k], up[k]);
+#pragma unroll 4
+        for (int n = n0; n < n1; n++) {
+            float f[VE];
+            if (a.base.p) {
+                unpack<T, VE>(__ldcs(map_at<T, VE>(a.base, n, y0 + j, ox, a.C, c)), f);
 #pragma unroll
-                    for (int k = 0; k < VE; k++) f[k] += p[k];
-                }
-                __stcs(const_cast<Raw<T, VE> *>(map_at<T, VE>(a.dst, n, oy, ox, a.C, c)), pack<T, VE>(f));
+                for (int k = 0; k < VE; k++) f[k] += out[k];
+            } else {
+                copy(f, out);
             }
+            __stcs(const_cast<Raw<T, VE> *>(map_at<T, VE>(a.dst, n, y0 + j, ox, a.C, c)), pack<T, VE>(f));
         }
     }
 }
@@ -109,61 +138,109 @@ __global__ void __launch_bounds__(kMapThreads) k_sum_images(const ResampleArgs a
 {
     dev::grid_launch_dependents();
     dev::grid_dependency_wait();
-    const int vecs = a.C / VE;
-    const long long i = blockIdx.x * static_cast<long long>(kMapThreads) + threadIdx.x;
-    if (i >= static_cast<long long>(a.OW) * vecs) return;
-    const int ox = static_cast<int>(i / vecs), c = static_cast<int>(i - static_cast<long long>(ox) * vecs) * VE;
-    for (int oy = blockIdx.y; oy < a.OH; oy += gridDim.y) {
+    const unsigned vecs = a.C / VE;
+    const unsigned i = blockIdx.x * kMapThreads + threadIdx.x;
+    if (i >= a.OW * vecs) return;
+    const int ox = static_cast<int>(i / vecs), c = static_cast<int>(i - ox * vecs) * VE;
+    const int y0 = blockIdx.y * a.run, y1 = min(y0 + a.run, a.OH);
+    for (int oy = y0; oy < y1; oy++) {
         float s[VE];
 #pragma unroll
         for (int k = 0; k < VE; k++) s[k] = 0.0f;
+#pragma unroll 8
         for (int n = 0; n < a.N; n++) {
             float f[VE];
             unpack<T, VE>(__ldcs(map_at<T, VE>(a.dst, n, oy, ox, a.C, c)), f);
 #pragma unroll
             for (int k = 0; k < VE; k++) s[k] += f[k];
         }
-        float *out = a.sum + (static_cast<long long>(oy) * a.OW + ox) * a.C + c;
-#pragma unroll
-        for (int k = 0; k < VE; k++) out[k] = s[k];
+        *reinterpret_cast<Raw<float, VE> *>(a.sum + (static_cast<long long>(oy) * a.OW + ox) * a.C + c) =
+            pack<float, VE>(s);
     }
 }
 
-// A thread gathers one vector of channels of one source pixel.
-template <class S, class T, int VE>
+// A thread gathers one column of source pixels, one vector of channels wide,
+// over the block's run of rows.  It walks the output rows that read them: each
+// row's readers of its column are summed under the column's weights (READERS
+// of them held in registers, formed once; more only beyond a ratio of
+// READERS / 2, weighed as they come), and the sum goes to the two source rows
+// that the output row lies between, so that each output row is read once per
+// run and not once for each source row.
+template <class S, class T, int VE, int READERS>
 __global__ void __launch_bounds__(kMapThreads) k_resize_map_grad(const ResampleArgs a)
 {
+    constexpr int kTaps = 32;
+    __shared__ Tap taps[kTaps];
     dev::grid_launch_dependents();
-    dev::grid_dependency_wait();
-    const int vecs = a.C / VE;
-    const long long i = blockIdx.x * static_cast<long long>(kMapThreads) + threadIdx.x;
-    if (i >= static_cast<long long>(a.W) * vecs) return;
-    const int x = static_cast<int>(i / vecs), c = static_cast<int>(i - static_cast<long long>(x) * vecs) * VE;
+    const unsigned vecs = a.C / VE;
+    const unsigned i = blockIdx.x * kMapThreads + threadIdx.x;
+    const bool on = i < a.W * vecs;
+    const int x = on ? static_cast<int>(i / vecs) : 0, c = on ? static_cast<int>(i - x * vecs) * VE : 0;
     const int2 rx = readers(x, a.W, a.OW);
-    for (int y = blockIdx.y; y < a.H; y += gridDim.y) {
-        const int2 ry = readers(y, a.H, a.OH);
-        for (int n = blockIdx.z; n < a.src_n; n += gridDim.z) {
-            float s[VE];
+    float wx[READERS];
 #pragma unroll
-            for (int k = 0; k < VE; k++) s[k] = 0.0f;
-            for (int oy = ry.x; oy < ry.y; oy++) {
-                float h[VE];
+    for (int k = 0; k < READERS; k++) wx[k] = rx.x + k < rx.y ? tap_weight(rx.x + k, x, a.W, a.OW) : 0.0f;
+    const int y0 = blockIdx.y * a.run, y1 = min(y0 + a.run, a.H), n = blockIdx.z;
+    const int lo = readers(y0, a.H, a.OH).x, hi = readers(y1 - 1, a.H, a.OH).y;
+    dev::grid_dependency_wait();
+    float cur[VE], next[VE];   // source rows y and y + 1
+    int y = y0 - 1;
 #pragma unroll
-                for (int k = 0; k < VE; k++) h[k] = 0.0f;
-                for (int ox = rx.x; ox < rx.y; ox++) {
+    for (int k = 0; k < VE; k++) cur[k] = next[k] = 0.0f;
+    const auto flush = [&] {
+        if (on && y >= y0 && y < y1) *const_cast<Raw<S, VE> *>(map_at<S, VE>(a.src, n, y, x, a.C, c)) = pack<S, VE>(cur);
+        y++;
+#pragma unroll
+        for (int k = 0; k < VE; k++) {
+            cur[k] = next[k];
+            next[k] = 0.0f;
+        }
+    };
+    for (int base = lo; base < hi; base += kTaps) {
+        const int count = min(kTaps, hi - base);
+        __syncthreads();
+        if (threadIdx.x < count) taps[threadIdx.x] = tap(base + threadIdx.x, a.H, a.OH);
+        __syncthreads();
+        for (int j = 0; j < count; j++) {
+            float h[VE];
+#pragma unroll
+            for (int k = 0; k < VE; k++) h[k] = 0.0f;
+            if (on) {
+                const Raw<T, VE> *row = map_at<T, VE>(a.dst, n, base + j, rx.x, a.C, c);
+                Raw<T, VE> r[READERS];
+#pragma unroll
+                for (int q = 0; q < READERS; q++)
+                    if (rx.x + q < rx.y) r[q] = row[static_cast<long long>(q) * vecs];
+#pragma unroll
+                for (int q = 0; q < READERS; q++)
+                    if (rx.x + q < rx.y) {
+                        float f[VE];
+                        unpack<T, VE>(r[q], f);
+#pragma unroll
+                        for (int k = 0; k < VE; k++) h[k] = fmaf(wx[q], f[k], h[k]);
+                    }
+                for (int ox = rx.x + READERS; ox < rx.y; ox++) {
                     const float w = tap_weight(ox, x, a.W, a.OW);
                     float f[VE];
-                    unpack<T, VE>(*map_at<T, VE>(a.dst, n, oy, ox, a.C, c), f);
+                    unpack<T, VE>(row[static_cast<long long>(ox - rx.x) * vecs], f);
 #pragma unroll
                     for (int k = 0; k < VE; k++) h[k] = fmaf(w, f[k], h[k]);
                 }
-                const float w = tap_weight(oy, y, a.H, a.OH);
-#pragma unroll
-                for (int k = 0; k < VE; k++) s[k] = fmaf(w, h[k], s[k]);
             }
-            *const_cast<Raw<S, VE> *>(map_at<S, VE>(a.src, n, y, x, a.C, c)) = pack<S, VE>(s);
+            const Tap t = taps[j];
+            while (t.a > y) flush();
+            if (t.a == y) {
+                const float w = t.b == t.a ? 1.0f : 1.0f - t.u;
+#pragma unroll
+                for (int k = 0; k < VE; k++) cur[k] = fmaf(w, h[k], cur[k]);
+            }
+            if (t.b == y + 1) {
+#pragma unroll
+                for (int k = 0; k < VE; k++) next[k] = fmaf(t.u, h[k], next[k]);
+            }
         }
     }
+    while (y < y1) flush();
 }
 
 // ------------------------------------------------------------------ host side
@@ -182,7 +259,11 @@ int resample_check(const rz_resample *d, Checked *s)
     if (d->H < 1 || d->W < 1 || d->H > RZ_MAX_DIM || d->W > RZ_MAX_DIM || d->out_h > RZ_MAX_DIM ||
         d->out_w > RZ_MAX_DIM)
         return RZ_ERR_ARG;
-    return d->src_n == 1 || d->src_n == d->N ? RZ_OK : RZ_ERR_ARG;
+    if (d->src_n != 1 && d->src_n != d->N) return RZ_ERR_ARG;
+    // the grid's depth, and 32-bit column numbers
+    if (d->src_n > 65535 || static_cast<long long>(std::max(d->W, d->out_w)) * d->C > 0x7fffffffLL)
+        return RZ_ERR_UNSUPPORTED;
+    return RZ_OK;
 }
 
 void resample_fill(const rz_resample *d, ResampleArgs &a)
@@ -197,25 +278,41 @@ void resample_fill(const rz_resample *d, ResampleArgs &a)
     a.C = d->C;
 }
 
-dim3 map_grid(int W, int vecs, int rows, int images)
+// Rows a thread walks: as many as leave eight CTAs an SM, for a run reads one
+// row in `run` twice, and a launch of a few CTAs is bound by their latency.
+dim3 map_grid(int W, int vecs, int rows, int images, int *run)
 {
-    return dim3(static_cast<unsigned>((static_cast<long long>(W) * vecs + kMapThreads - 1) / kMapThreads),
-                static_cast<unsigned>(std::min(rows, 65535)), static_cast<unsigned>(std::min(images, 65535)));
+    const long long columns = (static_cast<long long>(W) * vecs + kMapThreads - 1) / kMapThreads;
+    *run = kMapRun;
+    while (*run > 1 && columns * images * ((rows + *run - 1) / *run) < 8 * 152) *run /= 2;
+    return dim3(static_cast<unsigned>(columns), static_cast<unsigned>((rows + *run - 1) / *run),
+                static_cast<unsigned>(images));
 }
 
 // Calls fn(S{}, T{}, VE) for the map types; VE is the elements of 16 bytes of
-// the wider type where `wide`.
+// the map's own type where `wide` (a float32 table is then read 32 bytes at a
+// time).
 template <class Fn>
 cudaError_t resample_dispatch(const rz_resample *d, bool wide, Fn fn)
 {
     auto width = [&](auto s, auto t) {
-        constexpr int V = 16 / static_cast<int>(sizeof(s));
+        constexpr int V = 16 / static_cast<int>(sizeof(t));
         return wide ? fn(s, t, std::integral_constant<int, V>{}) : fn(s, t, std::integral_constant<int, 1>{});
     };
     if (d->dtype == RZ_F32) return width(float{}, float{});
     if (d->dtype == RZ_BF16)
         return d->src_dtype == RZ_F32 ? width(float{}, __nv_bfloat16{}) : width(__nv_bfloat16{}, __nv_bfloat16{});
     return d->src_dtype == RZ_F32 ? width(float{}, __half{}) : width(__half{}, __half{});
+}
+
+// Readers of a source column: two where the map shrinks, then about two a
+// unit of the ratio (ends and roundings add one).
+template <class S, class T, int V>
+cudaError_t grad_launch(ResampleArgs a, void *stream)
+{
+    const dim3 grid = map_grid(a.W, a.C / V, a.H, a.src_n, &a.run);
+    const auto fn = a.OW <= 2 * a.W ? k_resize_map_grad<S, T, V, 4> : k_resize_map_grad<S, T, V, 8>;
+    return launch(fn, grid, kMapThreads, 0, stream, a);
 }
 
 int resample_status(cudaError_t e)
@@ -252,14 +349,12 @@ int resize_map(const rz_resample *d, const rz_map *src, const rz_map *base, cons
     a.src = maps::view(src);
     a.dst = maps::view(dst);
     if (base) a.base = maps::view(base);
-    const size_t ve = 16 / s.src.es;
-    const bool wide = d->C % ve == 0 && maps::map_aligned(*src, s.src, 16) &&
-                      maps::map_aligned(*dst, s.dst, ve * s.dst.es) &&
-                      (!base || maps::map_aligned(*base, s.dst, ve * s.dst.es));
+    const bool wide = d->C % (16 / s.dst.es) == 0 && maps::map_aligned(*src, s.src, 16) &&
+                      maps::map_aligned(*dst, s.dst, 16) && (!base || maps::map_aligned(*base, s.dst, 16));
     return resample_status(resample_dispatch(d, wide, [&](auto ts, auto td, auto v) {
         constexpr int V = decltype(v)::value;
-        return maps::launch(k_resize_map<decltype(ts), decltype(td), V>, map_grid(a.OW, a.C / V, a.OH, a.src_n),
-                            kMapThreads, 0, stream, a);
+        const dim3 grid = map_grid(a.OW, a.C / V, a.OH, a.src_n, &a.run);
+        return maps::launch(k_resize_map<decltype(ts), decltype(td), V>, grid, kMapThreads, 0, stream, a);
     }));
 }
 
@@ -284,14 +379,13 @@ int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_map *dsrc
     ResampleArgs a;
     resample_fill(d, a);
     a.src = maps::view(dsrc);
-    size_t ve = 16 / s.src.es;
-    bool wide = d->C % ve == 0 && maps::map_aligned(*dsrc, s.src, 16);
+    bool wide = d->C % (16 / s.dst.es) == 0 && maps::map_aligned(*dsrc, s.src, 16);
     if (s.dst.empty()) {
         a.OH = a.OW = 0;   // no reader: zeros
     } else {
         if (!maps::map_ok(ddst, s.dst) || maps::map_overlap(*ddst, s.dst, *dsrc, s.src)) return RZ_ERR_ARG;
         a.dst = maps::view(ddst);
-        wide = wide && maps::map_aligned(*ddst, s.dst, ve * s.dst.es);
+        wide = wide && maps::map_aligned(*ddst, s.dst, 16);
         const size_t need = sum_bytes(d);
         if (need) {
             if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < need) return RZ_ERR_ARG;
@@ -302,17 +396,14 @@ int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_map *dsrc
         using S = decltype(ts);
         using T = decltype(td);
         constexpr int V = decltype(v)::value;
-        ResampleArgs g = a;
         if (a.sum) {
-            const cudaError_t e = maps::launch(k_sum_images<T, V>, map_grid(a.OW, a.C / V, a.OH, 1), kMapThreads, 0,
-                                               stream, a);
+            const dim3 grid = map_grid(a.OW, a.C / V, a.OH, 1, &a.run);
+            const cudaError_t e = maps::launch(k_sum_images<T, V>, grid, kMapThreads, 0, stream, a);
             if (e != cudaSuccess) return e;
-            g.dst = {reinterpret_cast<uint8_t *>(a.sum), static_cast<long long>(sizeof(float)) * a.OW * a.C, 0};
-            return maps::launch(k_resize_map_grad<S, float, V>, map_grid(a.W, a.C / V, a.H, 1), kMapThreads, 0,
-                                stream, g);
+            a.dst = {reinterpret_cast<uint8_t *>(a.sum), static_cast<long long>(sizeof(float)) * a.OW * a.C, 0};
+            return grad_launch<S, float, (V == 1 ? 1 : 4)>(a, stream);
         }
-        return maps::launch(k_resize_map_grad<S, T, V>, map_grid(a.W, a.C / V, a.H, a.src_n), kMapThreads, 0, stream,
-                            g);
+        return grad_launch<S, T, V>(a, stream);
     }));
 }
 

@@ -504,8 +504,9 @@ RZ_API int map_group_norm_grad(const rz_norm *d, const rz_drop *drop, const rz_m
  * images and added to them), of src_dtype, which is dtype or RZ_F32.  dst and
  * base: N images of out_h x out_w, of dtype; base may be NULL, or dst itself
  * (the same pointer, pitch and stride).  H, W >= 1 and H, W, out_h, out_w <=
- * RZ_MAX_DIM.  dst overlaps neither src nor, otherwise, base.  Asynchronous on
- * `stream`; no allocation.  An empty dst is RZ_OK.
+ * RZ_MAX_DIM; more than 65535 source images, or rows of 2^31 elements, are
+ * RZ_ERR_UNSUPPORTED.  dst overlaps neither src nor, otherwise, base.
+ * Asynchronous on `stream`; no allocation.  An empty dst is RZ_OK.
  */
 typedef struct {
     int N, src_n;
