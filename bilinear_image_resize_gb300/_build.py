@@ -18,8 +18,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build_obj")
 SOURCES = ["kernels.cu", "stream.cu", "direct.cu", "filter.cu", "texture.cu", "multi.cu", "api.cu", "noalloc.cu", "baseline_copy.cu", "filter_tc.cu",
-           "group_norm.cu", "map_dropout.cu", "resize_map.cu"]
-HEADERS = [os.path.join(CSRC, "rz_internal.h"), os.path.join(CSRC, "rz_device.h"), os.path.join(CSRC, "map_ops.h"), os.path.join(INCLUDE, "gbresize.h")]
+           "group_norm.cu", "gn_cluster.cu", "gn_passes_f32.cu", "gn_passes_bf16.cu",
+           "gn_passes_f16.cu", "map_dropout.cu", "resize_map.cu"]
+HEADERS = [os.path.join(CSRC, "rz_internal.h"), os.path.join(CSRC, "rz_device.h"), os.path.join(CSRC, "map_ops.h"),
+           os.path.join(CSRC, "gn_device.h"), os.path.join(CSRC, "gn_passes.h"), os.path.join(INCLUDE, "gbresize.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "-I", INCLUDE, "-I", CSRC]

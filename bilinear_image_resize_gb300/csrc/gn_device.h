@@ -1,0 +1,208 @@
+// Group norm: what its kernels share.  group_norm.cu has the entry points and
+// the kernels for images of any size, gn_cluster.cu those that keep an image's
+// channels on chip between the statistics and their use.
+#pragma once
+
+#include <type_traits>
+
+#include "map_ops.h"
+
+namespace rz {
+
+constexpr float kLog2e = 1.44269504f;
+constexpr int kGnSms = 152;
+constexpr int kGnMaxCluster = 8;    // CTAs a cluster (the portable limit)
+
+struct GnArgs {
+    maps::View x, dy, y;        // y: the output (dx for the gradient)
+    const float *gamma, *beta;  // may be null (1 and 0)
+    float *mean, *rstd;         // [N][G]
+    float *dgamma, *dbeta;      // [C], may be null
+    int N, C, G, Cg;
+    unsigned HW, W;             // pixels an image and a row
+    int joined;                 // rows follow one another in every map
+    int act;
+    float eps, inv_m;
+    maps::Drop drop;
+    float2 *chan;               // [N][C]: {mean, squared distances}; [rows][C]: {sum dz, sum dz xh}
+    int rows;
+    // cluster kernels: groups and vectors a slab, slabs an image, CTAs a cluster, vectors a thread keeps
+    int gs, lv, slabs, cl, keep;
+    // pass kernels: chunks of an image and their pixels
+    float2 *part;               // [N][chunks][C]: a chunk's share of chan
+    int chunks;
+    unsigned chunk_px;
+};
+
+// Opts a kernel into kGnShared bytes of shared memory (two CTAs an SM), once a
+// device.
+constexpr int kGnShared = 112 * 1024;
+cudaError_t gn_shared(const void *fn);
+
+// Cluster kernels (gn_cluster.cu): whether an image's slab fits a cluster; sets
+// gs, lv, cl and keep.
+bool gn_cluster_plan(GnArgs &a, size_t es, bool grad);
+cudaError_t gn_cluster_forward(const GnArgs &a, int dtype, bool drop, void *stream);
+cudaError_t gn_cluster_backward(const GnArgs &a, int dtype, bool drop, void *stream);
+
+// Pass kernels (gn_passes.h), one translation unit a type.
+template <class T> cudaError_t gn_passes_forward(const GnArgs &a, int ve, bool drop, void *stream);
+template <class T> cudaError_t gn_passes_backward(const GnArgs &a, int ve, bool drop, void *stream);
+
+template <int V> using Int = std::integral_constant<int, V>;
+
+// Calls fn(DROP, ACT) for a call's dropout and activation.
+template <class Fn>
+cudaError_t gn_kinds(int act, bool drop, Fn fn)
+{
+    auto on = [&](auto d) {
+        if (act == RZ_ACT_SILU) return fn(d, Int<RZ_ACT_SILU>{});
+        return act == RZ_ACT_GELU ? fn(d, Int<RZ_ACT_GELU>{}) : fn(d, Int<RZ_ACT_NONE>{});
+    };
+    return drop ? on(std::true_type{}) : on(std::false_type{});
+}
+
+// VE elements as pairs, for the paired float32 instructions (half the issue
+// slots of two scalar ones); a single element leaves the second half 0.
+template <int VE> constexpr int kPairs = (VE + 1) / 2;
+
+template <class T, int VE>
+__device__ __forceinline__ void unpack2(const maps::Raw<T, VE> &r, float2 (&f)[kPairs<VE>])
+{
+    float s[2 * kPairs<VE>];
+    s[2 * kPairs<VE> - 1] = 0.0f;
+    maps::unpack<T, VE>(r, reinterpret_cast<float(&)[VE]>(s));
+#pragma unroll
+    for (int i = 0; i < kPairs<VE>; i++) f[i] = make_float2(s[2 * i], s[2 * i + 1]);
+}
+
+template <class T, int VE>
+__device__ __forceinline__ maps::Raw<T, VE> pack2(const float2 (&f)[kPairs<VE>])
+{
+    float s[2 * kPairs<VE>];
+#pragma unroll
+    for (int i = 0; i < kPairs<VE>; i++) {
+        s[2 * i] = f[i].x;
+        s[2 * i + 1] = f[i].y;
+    }
+    return maps::pack<T, VE>(reinterpret_cast<float(&)[VE]>(s));
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float2 sigmoid2(float2 z)
+{
+    const float2 t = __fmul2_rn(z, both(-kLog2e));
+    const float2 q = __fadd2_rn(make_float2(maps::exp2_approx(t.x), maps::exp2_approx(t.y)), both(1.0f));
+    return make_float2(maps::rcp_approx(q.x), maps::rcp_approx(q.y));
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_value2(float2 z)
+{
+    if constexpr (ACT == RZ_ACT_SILU) return __fmul2_rn(z, sigmoid2(z));
+    if constexpr (ACT == RZ_ACT_GELU) return make_float2(maps::gelu(z.x), maps::gelu(z.y));
+    return z;
+}
+
+// silu'(z) = s + s z (1 - s)
+template <int ACT>
+__device__ __forceinline__ float2 act_slope2(float2 z)
+{
+    if constexpr (ACT == RZ_ACT_SILU) {
+        const float2 s = sigmoid2(z);
+        return __ffma2_rn(s, __fmul2_rn(z, __ffma2_rn(s, both(-1.0f), both(1.0f))), s);
+    }
+    if constexpr (ACT == RZ_ACT_GELU) return make_float2(maps::gelu_slope(z.x), maps::gelu_slope(z.y));
+    return both(1.0f);
+}
+
+// Zeroes the dropped ones of the VE elements from `e`; the scale of the kept
+// ones is left to the caller.
+template <int VE>
+__device__ __forceinline__ void drop2(float2 (&f)[kPairs<VE>], unsigned long long e, const maps::Drop &d)
+{
+    bool keep[VE];
+    maps::kept<VE>(keep, e, d);
+#pragma unroll
+    for (int i = 0; i < VE; i++) {
+        float &v = (i & 1) ? f[i / 2].y : f[i / 2].x;
+        v = keep[i] ? v : 0.0f;
+    }
+}
+
+// The thread's vector of channels: d = x + shift, z = d a + beta, with
+// shift = -mean and a = rstd gamma.
+template <int VE>
+struct Channel {
+    float2 shift[kPairs<VE>], a[kPairs<VE>], beta[kPairs<VE>];
+};
+
+// VE channels' values from an array of them.
+template <int VE>
+__device__ __forceinline__ void gn_load(float2 (&f)[kPairs<VE>], const float *from)
+{
+    if constexpr (VE == 1) {
+        f[0] = make_float2(*from, 0.0f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VE / 4; i++) {
+            const float4 v = reinterpret_cast<const float4 *>(from)[i];
+            f[2 * i] = make_float2(v.x, v.y);
+            f[2 * i + 1] = make_float2(v.z, v.w);
+        }
+    }
+}
+template <int VE>
+__device__ __forceinline__ void gn_save(float *to, const float2 (&f)[kPairs<VE>])
+{
+    if constexpr (VE == 1) {
+        *to = f[0].x;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VE / 4; i++)
+            reinterpret_cast<float4 *>(to)[i] = make_float4(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x, f[2 * i + 1].y);
+    }
+}
+
+// One vector forward: x in, y out.
+template <class T, int VE, bool DROP, int ACT>
+__device__ __forceinline__ maps::Raw<T, VE> gn_value(const maps::Raw<T, VE> &x, const Channel<VE> &k,
+                                                     const maps::Drop &drop, unsigned long long e)
+{
+    float2 f[kPairs<VE>];
+    unpack2<T, VE>(x, f);
+#pragma unroll
+    for (int i = 0; i < kPairs<VE>; i++) {
+        f[i] = act_value2<ACT>(__ffma2_rn(__fadd2_rn(f[i], k.shift[i]), k.a[i], k.beta[i]));
+        if (DROP) f[i] = __fmul2_rn(f[i], both(drop.scale));
+    }
+    if (DROP) drop2<VE>(f, e, drop);
+    return pack2<T, VE>(f);
+}
+
+// One vector backward: x and dy in; d = x - mean and dz out, dz short of the
+// dropout's scale.
+template <class T, int VE, bool DROP, int ACT>
+__device__ __forceinline__ void gn_dz(const maps::Raw<T, VE> &x, const maps::Raw<T, VE> &dy, const Channel<VE> &k,
+                                      const maps::Drop &drop, unsigned long long e, float2 (&d)[kPairs<VE>],
+                                      float2 (&dz)[kPairs<VE>])
+{
+    unpack2<T, VE>(x, d);
+    unpack2<T, VE>(dy, dz);
+    if (DROP) drop2<VE>(dz, e, drop);
+#pragma unroll
+    for (int i = 0; i < kPairs<VE>; i++) {
+        d[i] = __fadd2_rn(d[i], k.shift[i]);
+        if (ACT != RZ_ACT_NONE) dz[i] = __fmul2_rn(dz[i], act_slope2<ACT>(__ffma2_rn(d[i], k.a[i], k.beta[i])));
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+}  // namespace rz

@@ -1,0 +1,524 @@
+// Group norm and its gradient for images of any size and layout, in passes: a
+// launch that sums each channel by chunks of an image, a small one that joins
+// the chunks, and one that applies the result.  group_norm.cu states the
+// formulas.  A map up to L2's size is read from DRAM once; cutting larger calls
+// into batches that fit L2 measured slower than reading them twice (batches of
+// 64 MB: the gradient of 4 x 512 x 512 x 128 bf16 278 us against 231 us).
+//
+// A thread keeps one vector of channels and walks pixels, so sums are taken by
+// channel whatever the group's width; groups are put together from channels at
+// the head of the applying launch.  All sums go through memory in a fixed
+// order.
+#pragma once
+
+#include "gn_device.h"
+#include "map_ops.h"
+#include "rz_device.h"
+#include "rz_internal.h"
+
+namespace rz {
+namespace {
+
+using namespace maps;
+
+constexpr int kGpThreads = 256, kGpWarps = kGpThreads / 32;
+// Pixels a thread loads ahead of using them: with 128 registers a thread two
+// CTAs are resident, and so many 16-byte loads of theirs cover DRAM's latency.
+constexpr int kGpCtas = 2, kGpStats = 8, kGpApply = 4, kGpGrad = 2;
+
+// The thread's place: vector `vec` of the block's `width`, pixel lane `lane`
+// of `lanes`; `c` its first channel, `first` the block's.
+struct GpPlace {
+    int n, first, c, width, vec, lanes, lane;
+    unsigned p0, p1;
+    bool on;
+};
+
+template <int VE>
+__device__ __forceinline__ GpPlace gp_place(const GnArgs &a)
+{
+    GpPlace t;
+    const int start = blockIdx.y * kGpThreads;
+    t.width = min(a.C / VE - start, kGpThreads);
+    t.lanes = kGpThreads / t.width;
+    t.lane = threadIdx.x / t.width;
+    t.vec = threadIdx.x - t.lane * t.width;
+    t.n = blockIdx.z;
+    t.first = start * VE;
+    t.c = t.first + t.vec * VE;
+    t.p0 = blockIdx.x * a.chunk_px;
+    t.p1 = min(a.HW, t.p0 + a.chunk_px);
+    t.on = t.lane < t.lanes;
+    return t;
+}
+
+template <class T, int VE>
+__device__ __forceinline__ const Raw<T, VE> *gp_at(const View &v, const GnArgs &a, const GpPlace &t, unsigned px)
+{
+    return reinterpret_cast<const Raw<T, VE> *>(
+        v.p + t.n * v.bstride + pixel_off(px, a.W, a.joined, v.pitch, a.C * static_cast<int>(sizeof(T))) +
+        t.c * static_cast<int>(sizeof(T)));
+}
+
+// Elements before the thread's vector of pixel px.
+__device__ __forceinline__ unsigned long long gp_element(const GnArgs &a, const GpPlace &t, unsigned px)
+{
+    return (static_cast<unsigned long long>(t.n) * a.HW + px) * a.C + t.c;
+}
+
+// A pixel's vectors as they were read.
+template <class T, int VE>
+struct One {
+    Raw<T, VE> x;
+};
+template <class T, int VE>
+struct Two {
+    Raw<T, VE> x, dy;
+};
+
+// Walks the thread's pixels, U at a time while there are U, then one by one:
+// load(pixel) and use(values, count, pixel).  The next U are read before the
+// last U are used: with sixteen warps an SM, arithmetic alone does not cover
+// DRAM's latency.
+template <int U, class Load, class Use>
+__device__ __forceinline__ void gp_walk(const GpPlace &t, Load load, Use use)
+{
+    using R = decltype(load(0u));
+    unsigned p = t.p0 + t.lane;
+    const unsigned step = U * t.lanes, reach = (U - 1) * t.lanes;
+    if (p + reach < t.p1) {
+        R now[U];
+#pragma unroll
+        for (int j = 0; j < U; j++) now[j] = load(p + j * t.lanes);
+        while (true) {
+            const unsigned q = p + step;
+            const bool more = q + reach < t.p1;
+            R next[U];
+            if (more) {
+#pragma unroll
+                for (int j = 0; j < U; j++) next[j] = load(q + j * t.lanes);
+            }
+            use(now, Int<U>{}, p);
+            p = q;
+            if (!more) break;
+#pragma unroll
+            for (int j = 0; j < U; j++) now[j] = next[j];
+        }
+    }
+    for (; p < t.p1; p += t.lanes) {
+        const R last[1] = {load(p)};
+        use(last, Int<1>{}, p);
+    }
+}
+
+__device__ __forceinline__ float2 *gp_part(const GnArgs &a, int n, int chunk)
+{
+    return a.part + (static_cast<long long>(n) * a.chunks + chunk) * a.C;
+}
+
+// One chunk's mean and sum of squared distances for every channel.  A thread
+// takes kGpStats pixels at a time: their mean, their squared distances from it,
+// and the two joined to what it holds (the pairwise update of Chan, Golub and
+// LeVeque, "Updating formulae and a pairwise algorithm for computing sample
+// variances"), so that nothing cancels where the mean is far above the
+// deviation.
+template <class T, int VE>
+__global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_stats(const GnArgs a)
+{
+    __shared__ __align__(16) float sh[kGpThreads * VE];
+    __shared__ int count[kGpThreads];
+    dev::grid_launch_dependents();
+    dev::grid_dependency_wait();
+    const GpPlace t = gp_place<VE>(a);
+    float2 mean[kPairs<VE>], m2[kPairs<VE>];
+#pragma unroll
+    for (int i = 0; i < kPairs<VE>; i++) mean[i] = m2[i] = both(0.0f);
+    int have = 0;
+    const auto take = [&](const auto &r, auto count, unsigned) {
+        constexpr int U = decltype(count)::value;
+        float2 m[kPairs<VE>], q[kPairs<VE>], f[kPairs<VE>];
+#pragma unroll
+        for (int i = 0; i < kPairs<VE>; i++) m[i] = q[i] = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < U; j++) {
+            unpack2<T, VE>(r[j].x, f);
+#pragma unroll
+            for (int i = 0; i < kPairs<VE>; i++) m[i] = __fadd2_rn(m[i], f[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPairs<VE>; i++) m[i] = __fmul2_rn(m[i], both(-1.0f / U));   // minus the mean
+#pragma unroll
+        for (int j = 0; j < U; j++) {
+            unpack2<T, VE>(r[j].x, f);
+#pragma unroll
+            for (int i = 0; i < kPairs<VE>; i++) {
+                const float2 d = __fadd2_rn(f[i], m[i]);
+                q[i] = __ffma2_rn(d, d, q[i]);
+            }
+        }
+        have += U;
+        const float share = __fdividef(static_cast<float>(U), static_cast<float>(have)), weight = share * (have - U);
+#pragma unroll
+        for (int i = 0; i < kPairs<VE>; i++) {
+            const float2 d = __fadd2_rn(m[i], mean[i]);     // what was held minus what is new
+            mean[i] = __ffma2_rn(d, both(-share), mean[i]);
+            m2[i] = __fadd2_rn(m2[i], __ffma2_rn(__fmul2_rn(d, d), both(weight), q[i]));
+        }
+    };
+    if (t.on)
+        gp_walk<kGpStats>(t, [&](unsigned px) { return One<T, VE>{*gp_at<T, VE>(a.x, a, t, px)}; }, take);
+    // join the pixel lanes, a thread to a channel: the chunk's mean, then the distances about it
+    float *mine = sh + (t.lane * t.width + t.vec) * VE;
+    if (t.on) {
+        gn_save<VE>(mine, mean);
+        if (t.vec == 0) count[t.lane] = have;
+    }
+    __syncthreads();
+    constexpr int kOwn = VE;    // channels a thread joins at most
+    float m[kOwn], q[kOwn];
+#pragma unroll
+    for (int k = 0; k < kOwn; k++) {
+        const int c = threadIdx.x + k * kGpThreads;
+        m[k] = q[k] = 0.0f;
+        if (c < t.width * VE) {
+            float s = 0.0f;
+            for (int l = 0; l < t.lanes; l++) s = fmaf(sh[l * t.width * VE + c], static_cast<float>(count[l]), s);
+            m[k] = s / (t.p1 - t.p0);
+            for (int l = 0; l < t.lanes; l++) {
+                const float d = sh[l * t.width * VE + c] - m[k];
+                q[k] = fmaf(d * d, static_cast<float>(count[l]), q[k]);
+            }
+        }
+    }
+    __syncthreads();
+    if (t.on) gn_save<VE>(mine, m2);
+    __syncthreads();
+    float2 *out = gp_part(a, blockIdx.z, blockIdx.x) + blockIdx.y * kGpThreads * VE;
+#pragma unroll
+    for (int k = 0; k < kOwn; k++) {
+        const int c = threadIdx.x + k * kGpThreads;
+        if (c < t.width * VE) {
+            for (int l = 0; l < t.lanes; l++) q[k] += sh[l * t.width * VE + c];
+            out[c] = make_float2(m[k], q[k]);
+        }
+    }
+}
+
+// The constants of the block's channels, from the groups' statistics: -mean,
+// a, beta.
+__device__ __forceinline__ void gp_constants(const GnArgs &a, const GpPlace &t, int channels, float *cst, int c, float mean,
+                                             float rstd)
+{
+    cst[c] = -mean;
+    cst[channels + c] = a.gamma ? rstd * a.gamma[t.first + c] : rstd;
+    cst[2 * channels + c] = a.beta ? a.beta[t.first + c] : 0.0f;
+}
+
+template <int VE>
+__device__ __forceinline__ void gp_channel(const GpPlace &t, const float *cst, Channel<VE> &k)
+{
+    gn_load<VE>(k.shift, cst + t.vec * VE);
+    gn_load<VE>(k.a, cst + t.width * VE + t.vec * VE);
+    gn_load<VE>(k.beta, cst + 2 * t.width * VE + t.vec * VE);
+}
+
+// For each group that the block's channels belong to, fn(g, {sum, sum}) by
+// every lane of a warp, with the sums over all its channels of get(c).
+template <class Get, class Fn>
+__device__ __forceinline__ void gp_groups(const GnArgs &a, const GpPlace &t, int channels, Get get, Fn fn)
+{
+    const int lane = threadIdx.x & 31, g1 = (t.first + channels - 1) / a.Cg;
+    for (int g = t.first / a.Cg + (threadIdx.x >> 5); g <= g1; g += kGpWarps) {
+        float2 s = make_float2(0.0f, 0.0f);
+        for (int c = g * a.Cg + lane; c < (g + 1) * a.Cg; c += 32) s = __fadd2_rn(s, get(c));
+        fn(g, make_float2(warp_sum(s.x), warp_sum(s.y)));
+    }
+}
+
+template <class T, int VE, bool DROP, int ACT>
+__global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_apply(const GnArgs a)
+{
+    extern __shared__ __align__(16) float gp_smem[];    // three constants a channel, then two statistics a group
+    dev::grid_launch_dependents();
+    const GpPlace t = gp_place<VE>(a);
+    const int channels = t.width * VE, g0 = t.first / a.Cg;
+    float2 *group = reinterpret_cast<float2 *>(gp_smem + align_up(3 * channels, 2));
+    dev::grid_dependency_wait();
+    const float2 *chan = a.chan + static_cast<long long>(t.n) * a.C;
+    const float pixels = static_cast<float>(a.HW);
+    gp_groups(
+        a, t, channels, [&](int c) { return make_float2(chan[c].x * pixels, 0.0f); },
+        [&](int g, float2 s) {
+            if ((threadIdx.x & 31) == 0) group[g - g0].x = s.x * a.inv_m;
+        });
+    __syncthreads();
+    gp_groups(
+        a, t, channels,
+        [&](int c) {
+            const float2 v = chan[c];
+            const float d = v.x - group[c / a.Cg - g0].x;
+            return make_float2(fmaf(d * d, pixels, v.y), 0.0f);
+        },
+        [&](int g, float2 s) {
+            if ((threadIdx.x & 31)) return;
+            const float rstd = 1.0f / sqrtf(fmaf(s.x, a.inv_m, a.eps));
+            group[g - g0].y = rstd;
+            if (blockIdx.x == 0 && g * a.Cg >= t.first) {
+                a.mean[t.n * a.G + g] = group[g - g0].x;
+                a.rstd[t.n * a.G + g] = rstd;
+            }
+        });
+    __syncthreads();
+    for (int c = threadIdx.x; c < channels; c += kGpThreads) {
+        const float2 v = group[(t.first + c) / a.Cg - g0];
+        gp_constants(a, t, channels, gp_smem, c, v.x, v.y);
+    }
+    __syncthreads();
+    if (!t.on) return;
+    Channel<VE> k;
+    gp_channel<VE>(t, gp_smem, k);
+    gp_walk<kGpApply>(
+        t, [&](unsigned px) { return One<T, VE>{__ldcs(gp_at<T, VE>(a.x, a, t, px))}; },
+        [&](const auto &r, auto count, unsigned p) {
+#pragma unroll
+            for (int j = 0; j < decltype(count)::value; j++) {
+                const unsigned px = p + j * t.lanes;
+                __stcs(const_cast<Raw<T, VE> *>(gp_at<T, VE>(a.y, a, t, px)),
+                       gn_value<T, VE, DROP, ACT>(r[j].x, k, a.drop, gp_element(a, t, px)));
+            }
+        });
+}
+
+// One chunk's sums of dz and dz xh for every channel.
+template <class T, int VE, bool DROP, int ACT>
+__global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_sums(const GnArgs a)
+{
+    extern __shared__ __align__(16) float gp_smem[];    // three constants a channel; then the threads' sums
+    dev::grid_launch_dependents();
+    const GpPlace t = gp_place<VE>(a);
+    const int channels = t.width * VE;
+    dev::grid_dependency_wait();
+    for (int c = threadIdx.x; c < channels; c += kGpThreads) {
+        const int g = t.n * a.G + (t.first + c) / a.Cg;
+        gp_constants(a, t, channels, gp_smem, c, a.mean[g], a.rstd[g]);
+    }
+    __syncthreads();
+    float2 s1[kPairs<VE>], s2[kPairs<VE>];
+#pragma unroll
+    for (int i = 0; i < kPairs<VE>; i++) s1[i] = s2[i] = both(0.0f);
+    if (t.on) {
+        Channel<VE> k;
+        gp_channel<VE>(t, gp_smem, k);
+        gp_walk<kGpGrad>(
+            t,
+            [&](unsigned px) {
+                return Two<T, VE>{*gp_at<T, VE>(a.x, a, t, px), *gp_at<T, VE>(a.dy, a, t, px)};
+            },
+            [&](const auto &r, auto count, unsigned p) {
+#pragma unroll
+                for (int j = 0; j < decltype(count)::value; j++) {
+                    float2 d[kPairs<VE>], dz[kPairs<VE>];
+                    gn_dz<T, VE, DROP, ACT>(r[j].x, r[j].dy, k, a.drop, gp_element(a, t, p + j * t.lanes), d, dz);
+#pragma unroll
+                    for (int i = 0; i < kPairs<VE>; i++) {
+                        s1[i] = __fadd2_rn(s1[i], dz[i]);
+                        s2[i] = __ffma2_rn(dz[i], d[i], s2[i]);
+                    }
+                }
+            });
+    }
+    float2 *out = gp_part(a, blockIdx.z, blockIdx.x) + blockIdx.y * kGpThreads * VE;
+    float u[VE];    // this thread's channels' sums of dz
+#pragma unroll
+    for (int z = 0; z < 2; z++) {
+        __syncthreads();
+        if (t.on) gn_save<VE>(gp_smem + (t.lane * t.width + t.vec) * VE, z ? s2 : s1);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < VE; k++) {
+            const int c = threadIdx.x + k * kGpThreads;
+            if (c < channels) {
+                float s = 0.0f;
+                for (int l = 0; l < t.lanes; l++) s += gp_smem[l * channels + c];
+                if (z)
+                    out[c] = make_float2(u[k] * a.drop.scale, s * a.drop.scale * a.rstd[t.n * a.G + (t.first + c) / a.Cg]);
+                else
+                    u[k] = s;
+            }
+        }
+    }
+}
+
+// dx = a dz - rstd A - rstd^2 B d; the dropout's scale, which dz lacks, goes
+// with a.
+template <class T, int VE, bool DROP, int ACT>
+__global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_dx(const GnArgs a)
+{
+    extern __shared__ __align__(16) float gp_smem[];    // five constants a channel, then two sums a group
+    dev::grid_launch_dependents();
+    const GpPlace t = gp_place<VE>(a);
+    const int channels = t.width * VE, g0 = t.first / a.Cg;
+    float2 *group = reinterpret_cast<float2 *>(gp_smem + align_up(5 * channels, 2));
+    dev::grid_dependency_wait();
+    const float2 *chan = a.chan + static_cast<long long>(t.n) * a.C;
+    gp_groups(
+        a, t, channels,
+        [&](int c) {
+            const float gamma = a.gamma ? a.gamma[c] : 1.0f;
+            return make_float2(gamma * chan[c].x, gamma * chan[c].y);
+        },
+        [&](int g, float2 s) {
+            const float r = a.rstd[t.n * a.G + g];
+            if ((threadIdx.x & 31) == 0) group[g - g0] = make_float2(-r * (s.x * a.inv_m), -r * r * (s.y * a.inv_m));
+        });
+    __syncthreads();
+    for (int c = threadIdx.x; c < channels; c += kGpThreads) {
+        const int g = (t.first + c) / a.Cg;
+        gp_constants(a, t, channels, gp_smem, c, a.mean[t.n * a.G + g], a.rstd[t.n * a.G + g]);
+        gp_smem[3 * channels + c] = group[g - g0].x;
+        gp_smem[4 * channels + c] = group[g - g0].y;
+    }
+    __syncthreads();
+    if (!t.on) return;
+    Channel<VE> k;
+    float2 k0[kPairs<VE>], k1[kPairs<VE>];
+    gp_channel<VE>(t, gp_smem, k);
+    gn_load<VE>(k0, gp_smem + 3 * channels + t.vec * VE);
+    gn_load<VE>(k1, gp_smem + 4 * channels + t.vec * VE);
+    gp_walk<kGpGrad>(
+        t,
+        [&](unsigned px) {
+            return Two<T, VE>{__ldcs(gp_at<T, VE>(a.x, a, t, px)), __ldcs(gp_at<T, VE>(a.dy, a, t, px))};
+        },
+        [&](const auto &r, auto count, unsigned p) {
+#pragma unroll
+            for (int j = 0; j < decltype(count)::value; j++) {
+                const unsigned px = p + j * t.lanes;
+                float2 d[kPairs<VE>], dz[kPairs<VE>];
+                gn_dz<T, VE, DROP, ACT>(r[j].x, r[j].dy, k, a.drop, gp_element(a, t, px), d, dz);
+#pragma unroll
+                for (int i = 0; i < kPairs<VE>; i++) {
+                    if (DROP) dz[i] = __fmul2_rn(dz[i], both(a.drop.scale));
+                    dz[i] = __ffma2_rn(d[i], k1[i], __ffma2_rn(dz[i], k.a[i], k0[i]));
+                }
+                __stcs(const_cast<Raw<T, VE> *>(gp_at<T, VE>(a.y, a, t, px)), pack2<T, VE>(dz));
+            }
+        });
+}
+
+// The chunks' shares joined, kJoinWide channels a block, the chunks over its
+// threads: forward, sets of unlike counts and means; gradient, sums.
+constexpr int kJoinThreads = 1024, kJoinWide = 16, kJoinRows = kJoinThreads / kJoinWide;
+
+template <bool GRAD>
+__global__ void __launch_bounds__(kJoinThreads) k_gp_join(const GnArgs a)
+{
+    __shared__ float2 sh[kJoinRows][kJoinWide + 1];
+    dev::grid_launch_dependents();
+    dev::grid_dependency_wait();
+    const int lane = threadIdx.x % kJoinWide, row = threadIdx.x / kJoinWide;
+    const int c = blockIdx.x * kJoinWide + lane;
+    const float2 *part = gp_part(a, blockIdx.y, 0) + c;
+    const auto pixels = [&](int k) { return static_cast<float>(min(a.chunk_px, a.HW - k * a.chunk_px)); };
+    const auto total = [&](float2 s) {
+        __syncthreads();
+        sh[row][lane] = s;
+        for (int h = kJoinRows / 2; h; h /= 2) {
+            __syncthreads();
+            if (row < h) sh[row][lane] = __fadd2_rn(sh[row][lane], sh[row + h][lane]);
+        }
+        __syncthreads();
+        return sh[0][lane];
+    };
+    float2 s = make_float2(0.0f, 0.0f);
+    if (c < a.C) {
+#pragma unroll 4
+        for (int k = row; k < a.chunks; k += kJoinRows) {
+            const float2 v = part[static_cast<long long>(k) * a.C];
+            s = GRAD ? __fadd2_rn(s, v) : make_float2(fmaf(v.x, pixels(k), s.x), 0.0f);
+        }
+    }
+    s = total(s);
+    if (!GRAD) {
+        const float mean = s.x / a.HW;
+        s = make_float2(0.0f, 0.0f);
+        if (c < a.C) {
+#pragma unroll 4
+            for (int k = row; k < a.chunks; k += kJoinRows) {
+                const float2 v = part[static_cast<long long>(k) * a.C];
+                s.y += fmaf((v.x - mean) * (v.x - mean), pixels(k), v.y);
+            }
+        }
+        s = make_float2(mean, total(s).y);
+    }
+    if (row == 0 && c < a.C) a.chan[static_cast<long long>(blockIdx.y) * a.C + c] = s;
+}
+
+// ------------------------------------------------------------------ host side
+
+template <class T, class Fn>
+cudaError_t gp_vectors(int ve, Fn fn)
+{
+    if constexpr (sizeof(T) == 2)
+        if (ve == 8) return fn(Int<8>{});
+    return ve == 4 ? fn(Int<4>{}) : fn(Int<1>{});
+}
+
+inline dim3 gp_grid(const GnArgs &a, int ve)
+{
+    return dim3(a.chunks, (a.C / ve + kGpThreads - 1) / kGpThreads, a.N);
+}
+
+inline dim3 gp_join_grid(const GnArgs &a) { return dim3((a.C + kJoinWide - 1) / kJoinWide, a.N); }
+
+// Floats of shared memory: `each` a channel and two a group, or one for each
+// thread's elements where that is more.
+inline size_t gp_shared(const GnArgs &a, int ve, int each)
+{
+    const int channels = std::min(a.C, kGpThreads * ve), groups = channels / a.Cg + 2;
+    return sizeof(float) * std::max(align_up(each * channels, 2) + 2 * groups, kGpThreads * ve);
+}
+
+inline cudaError_t gp_launch(void (*fn)(GnArgs), dim3 grid, size_t smem, void *stream, const GnArgs &a)
+{
+    const cudaError_t e = gn_shared(reinterpret_cast<const void *>(fn));
+    return e != cudaSuccess ? e : launch(fn, grid, kGpThreads, smem, stream, a);
+}
+
+}  // namespace
+
+template <class T>
+cudaError_t gn_passes_forward(const GnArgs &a, int ve, bool drop, void *stream)
+{
+    return gp_vectors<T>(ve, [&](auto v) {
+        constexpr int VE = decltype(v)::value;
+        const dim3 grid = gp_grid(a, VE);
+        cudaError_t e = launch(k_gp_stats<T, VE>, grid, kGpThreads, 0, stream, a);
+        if (e == cudaSuccess)
+            e = launch(k_gp_join<false>, gp_join_grid(a), kJoinThreads, 0, stream, a);
+        if (e != cudaSuccess) return e;
+        return gn_kinds(a.act, drop, [&](auto dr, auto act) {
+            return gp_launch(k_gp_apply<T, VE, decltype(dr)::value, decltype(act)::value>, grid, gp_shared(a, VE, 3),
+                             stream, a);
+        });
+    });
+}
+
+template <class T>
+cudaError_t gn_passes_backward(const GnArgs &a, int ve, bool drop, void *stream)
+{
+    return gp_vectors<T>(ve, [&](auto v) {
+        constexpr int VE = decltype(v)::value;
+        const dim3 grid = gp_grid(a, VE);
+        return gn_kinds(a.act, drop, [&](auto dr, auto act) {
+            constexpr bool D = decltype(dr)::value;
+            constexpr int A = decltype(act)::value;
+            cudaError_t e = gp_launch(k_gp_sums<T, VE, D, A>, grid, gp_shared(a, VE, 3), stream, a);
+            if (e == cudaSuccess)
+                e = launch(k_gp_join<true>, gp_join_grid(a), kJoinThreads, 0, stream, a);
+            return e != cudaSuccess ? e : gp_launch(k_gp_dx<T, VE, D, A>, grid, gp_shared(a, VE, 5), stream, a);
+        });
+    });
+}
+
+}  // namespace rz

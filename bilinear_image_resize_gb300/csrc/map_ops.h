@@ -184,34 +184,18 @@ __device__ __forceinline__ Raw<T, VE> pack(const float (&f)[VE])
     return r;
 }
 
-// Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
-// easy as 1, 2, 3", SC'11): ten rounds on the counter (block, offset) under
-// the key `seed`.  Its four words are cut into eight 16-bit lanes, lane j the
-// low or high half of word j / 2, so that one block serves eight elements:
-// 16 bits set the drop rate to 1 / 65536, which the scale takes into account,
-// and halve the generator's work, the larger part of the arithmetic.
-__device__ __forceinline__ uint4 philox(unsigned long long block, unsigned long long offset, unsigned long long seed)
-{
-    uint4 c = {static_cast<unsigned>(block), static_cast<unsigned>(block >> 32), static_cast<unsigned>(offset),
-               static_cast<unsigned>(offset >> 32)};
-    unsigned k0 = static_cast<unsigned>(seed), k1 = static_cast<unsigned>(seed >> 32);
-#pragma unroll
-    for (int r = 0; r < 10; r++) {
-        const unsigned long long a = static_cast<unsigned long long>(c.x) * 0xD2511F53u;
-        const unsigned long long b = static_cast<unsigned long long>(c.z) * 0xCD9E8D57u;
-        c = {static_cast<unsigned>(b >> 32) ^ c.y ^ k0, static_cast<unsigned>(b),
-             static_cast<unsigned>(a >> 32) ^ c.w ^ k1, static_cast<unsigned>(a)};
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-    return c;
-}
-
-// The mask of a dropout: an element is kept where its 16 bits are above
-// `top` = round(65536 p) - 1, and then multiplied by `scale`.
+// Dropout's mask: Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel
+// random numbers: as easy as 1, 2, 3", SC'11), ten rounds on the counter
+// (block, offset) under the key `seed`.  Its four words are cut into eight
+// 16-bit lanes, lane j the low or high half of word j / 2, so that one block
+// serves eight elements: 16 bits set the drop rate to 1 / 65536, which the
+// scale takes into account, and halve the generator's work, the larger part of
+// the arithmetic.  An element is dropped where its 16 bits are at most
+// `top` = round(65536 p) - 1, else multiplied by `scale`.
 struct Drop {
-    unsigned long long seed, offset;
-    unsigned limit;   // top << 16 | 0xffff
+    unsigned key[20];       // the rounds' keys: the same for every thread, formed on the host
+    unsigned off_lo, off_hi;
+    unsigned top;           // in both halves
     float scale;
 };
 
@@ -220,55 +204,94 @@ inline unsigned drop_threshold(const rz_drop *d) { return d ? static_cast<unsign
 inline bool drop_ok(const rz_drop *d) { return !d || (d->p >= 0.0 && d->p <= 1.0); }
 inline Drop make_drop(const rz_drop *d)
 {
+    Drop r = {};
+    r.scale = 1.0f;
     const unsigned t = drop_threshold(d);
-    if (t == 0) return {0, 0, 0, 1.0f};
-    return {d->seed, d->offset, (t - 1) << 16 | 0xffffu, t < 65536 ? static_cast<float>(65536.0 / (65536 - t)) : 0.0f};
+    if (t == 0) return r;
+    const uint64_t seed = d->seed, offset = d->offset;
+    for (unsigned i = 0; i < 10; i++) {
+        r.key[2 * i] = static_cast<unsigned>(seed) + i * 0x9E3779B9u;
+        r.key[2 * i + 1] = static_cast<unsigned>(seed >> 32) + i * 0xBB67AE85u;
+    }
+    r.off_lo = static_cast<unsigned>(offset);
+    r.off_hi = static_cast<unsigned>(offset >> 32);
+    r.top = (t - 1) * 0x10001u;
+    r.scale = t < 65536 ? static_cast<float>(65536.0 / (65536 - t)) : 0.0f;
+    return r;
 }
 
-// f[i] = kept ? f[i] * scale : 0 for the VE elements from `e` (a multiple of
-// VE, which divides eight).  A dropped element is 0 whatever it held.
-template <int VE>
-__device__ __forceinline__ void drop_elements(float (&f)[VE], unsigned long long e, const Drop &d)
+__device__ __forceinline__ uint4 philox(unsigned long long block, const Drop &d)
 {
-    const uint4 c = philox(e >> 3, d.offset, d.seed);
+    uint4 c = {static_cast<unsigned>(block), static_cast<unsigned>(block >> 32), d.off_lo, d.off_hi};
+#pragma unroll
+    for (int r = 0; r < 10; r++) {
+        const unsigned long long a = static_cast<unsigned long long>(c.x) * 0xD2511F53u;
+        const unsigned long long b = static_cast<unsigned long long>(c.z) * 0xCD9E8D57u;
+        c = {static_cast<unsigned>(b >> 32) ^ c.y ^ d.key[2 * r], static_cast<unsigned>(b),
+             static_cast<unsigned>(a >> 32) ^ c.w ^ d.key[2 * r + 1], static_cast<unsigned>(a)};
+    }
+    return c;
+}
+
+// Whether the two elements of a word are kept.
+__device__ __forceinline__ void kept_pair(unsigned w, const Drop &d, bool &lo, bool &hi)
+{
+    const unsigned limit = d.top | 0xffffu;
+    lo = w << 16 > limit;
+    hi = w > limit;
+}
+
+// Which of the VE elements from `e` (a multiple of VE, which divides eight)
+// are kept.
+template <int VE>
+__device__ __forceinline__ void kept(bool (&keep)[VE], unsigned long long e, const Drop &d)
+{
+    const uint4 c = philox(e >> 3, d);
     if constexpr (VE == 8) {
         const unsigned w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-        for (int i = 0; i < 8; i++) f[i] = ((i & 1) ? w[i / 2] : w[i / 2] << 16) > d.limit ? f[i] * d.scale : 0.0f;
+        for (int i = 0; i < 4; i++) kept_pair(w[i], d, keep[2 * i], keep[2 * i + 1]);
     } else if constexpr (VE == 4) {
         const bool high = e & 4;
-        const unsigned w[2] = {high ? c.z : c.x, high ? c.w : c.y};
-#pragma unroll
-        for (int i = 0; i < 4; i++) f[i] = ((i & 1) ? w[i / 2] : w[i / 2] << 16) > d.limit ? f[i] * d.scale : 0.0f;
+        kept_pair(high ? c.z : c.x, d, keep[0], keep[1]);
+        kept_pair(high ? c.w : c.y, d, keep[2], keep[3]);
     } else {
         static_assert(VE == 1, "");
         const int j = static_cast<int>(e & 7);
-        const unsigned w = (j & 4) ? ((j & 2) ? c.w : c.z) : ((j & 2) ? c.y : c.x);
-        f[0] = ((j & 1) ? w : w << 16) > d.limit ? f[0] * d.scale : 0.0f;
+        bool lo, hi;
+        kept_pair((j & 4) ? ((j & 2) ? c.w : c.z) : ((j & 2) ? c.y : c.x), d, lo, hi);
+        keep[0] = (j & 1) ? hi : lo;
     }
 }
 
-// Activations and their derivatives.
-__device__ __forceinline__ float sigmoidf(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
-
-template <int ACT>
-__device__ __forceinline__ float act_value(float z)
+// f[i] = kept ? f[i] * scale : 0.  A dropped element is 0 whatever it held.
+template <int VE>
+__device__ __forceinline__ void drop_elements(float (&f)[VE], unsigned long long e, const Drop &d)
 {
-    if constexpr (ACT == RZ_ACT_SILU) return z * sigmoidf(z);
-    if constexpr (ACT == RZ_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    return z;
+    bool keep[VE];
+    kept<VE>(keep, e, d);
+#pragma unroll
+    for (int i = 0; i < VE; i++) f[i] = keep[i] ? f[i] * d.scale : 0.0f;
 }
 
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z)
+__device__ __forceinline__ float exp2_approx(float v)
 {
-    if constexpr (ACT == RZ_ACT_SILU) {
-        const float s = sigmoidf(z);
-        return s * fmaf(z, 1.0f - s, 1.0f);
-    }
-    if constexpr (ACT == RZ_ACT_GELU)
-        return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), fmaf(0.5f, erff(z * 0.70710678f), 0.5f));
-    return 1.0f;
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// z Phi(z) and its derivative Phi(z) + z phi(z), Phi(z) = (1 + erf(z / sqrt 2)) / 2.
+__device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.0f + erff(z * 0.70710678f)); }
+__device__ __forceinline__ float gelu_slope(float z)
+{
+    return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), fmaf(0.5f, erff(z * 0.70710678f), 0.5f));
 }
 
 }  // namespace maps
