@@ -369,13 +369,20 @@ def resize_u8_multi(jobs, njobs: int, C: int, mode: int = RZ_LINEAR, status=None
            "resize_u8_multi")
 
 
+_torch = None
 _MAP_DTYPES: dict = {}
 
 
-def _map_dtype(t, name: str) -> int:
-    if not _MAP_DTYPES:
+def _with_torch():
+    global _torch
+    if _torch is None:
         import torch
         _MAP_DTYPES.update({torch.float32: RZ_F32, torch.bfloat16: RZ_BF16, torch.float16: RZ_F16})
+        _torch = torch
+    return _torch
+
+
+def _map_dtype(t, name: str) -> int:
     code = _MAP_DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
@@ -384,44 +391,51 @@ def _map_dtype(t, name: str) -> int:
 
 def _map_of(t, name: str, shape=None):
     """((N, H, W, C), rz_map) of an (N, H, W, C) or (H, W, C) tensor whose pixels are packed; `shape`: what it must be."""
-    if t.dim() == 4:
-        N, H, W, C = t.shape
-        sn, sh, sw, sc = t.stride()
-    elif t.dim() == 3:
+    dims = t.dim()
+    if dims == 4:
+        N, H, W, C = got = tuple(t.shape)
+    elif dims == 3:
         H, W, C = t.shape
-        N, sn, (sh, sw, sc) = 1, 0, t.stride()
+        N, got = 1, (1, H, W, C)
     else:
         raise ValueError(f"{name}: expected NxHxWxC or HxWxC, got shape {tuple(t.shape)}")
-    if shape is not None and (N, H, W, C) != shape:
-        raise ValueError(f"{name}: shape {(N, H, W, C)}, expected {shape}")
+    if shape is not None and got != shape:
+        raise ValueError(f"{name}: shape {got}, expected {shape}")
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
+    es = t.element_size()
+    if t.is_contiguous():
+        return got, RzMap(t.data_ptr(), W * C * es, H * W * C * es)
+    sn, sh, sw, sc = t.stride() if dims == 4 else (0, *t.stride())
     if t.numel() and ((C > 1 and sc != 1) or (W > 1 and sw != C)):
         raise ValueError(f"{name}: pixels must be packed (channels last)")
-    es = t.element_size()
-    return (N, H, W, C), RzMap(t.data_ptr(), sh * es if H > 1 else W * C * es, sn * es if N > 1 else 0)
+    return got, RzMap(t.data_ptr(), sh * es if H > 1 else W * C * es, sn * es if N > 1 else 0)
 
 
-def _floats(t, name: str, *shape):
+def _floats(t, name: str, shape):
     """Pointer of a packed float32 CUDA tensor of that shape (None: a null pointer)."""
     if t is None:
         return None
-    import torch
-    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not _torch.float32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: expected a contiguous float32 CUDA tensor of shape {shape}")
     return t.data_ptr()
 
 
-def _drop_of(drop):
-    return None if drop is None else RzDrop(float(drop[0]), int(drop[1]) & 0xFFFFFFFFFFFFFFFF,
-                                            int(drop[2]) & 0xFFFFFFFFFFFFFFFF if len(drop) > 2 else 0)
+def _drop_of(p, seed, offset=0) -> RzDrop:
+    return RzDrop(p, seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF)
 
 
-def _workspace(workspace, nbytes: int, like, stream):
-    """The caller's workspace, or one of `nbytes` that belongs to the call's stream."""
-    import torch
-    if workspace is not None or nbytes == 0:
-        return workspace
+def _stream_at(stream, t) -> int:
+    """The call's stream: `stream`, or the current one of the tensor's device
+    (its handle alone: a stream object costs as much as a launch)."""
+    return _torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
+
+
+def _workspace(nbytes: int, like, stream):
+    """A workspace of `nbytes` that belongs to the call's stream, from torch's allocator."""
+    torch = _torch
+    if nbytes == 0:
+        return None
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     if isinstance(stream, int):
@@ -439,24 +453,25 @@ def map_dropout(x, y, p: float, seed: int, offset: int = 0, residual=None, strea
     offset); called on dy without a residual it is the gradient towards x.
     Any shape, packed or in the (N, H, W, C) layout of the other maps; y may
     be x or the residual."""
+    _with_torch()
     dtype = _map_dtype(x, "x")
-    if y.dtype != x.dtype or (residual is not None and residual.dtype != x.dtype):
-        raise ValueError("x, y and residual differ in dtype")
-    if y.shape != x.shape or (residual is not None and residual.shape != x.shape):
-        raise ValueError("x, y and residual differ in shape")
-    if all(t is None or t.is_contiguous() for t in (x, y, residual)):
-        # any shape whose elements follow one another: rows of the last dimension
-        rows = (x.numel() // x.shape[-1], 1, x.shape[-1], 1) if x.numel() and x.dim() else (1, 1, x.numel(), 1)
-        x, y, residual = (None if t is None else t.view(rows) for t in (x, y, residual))
-    shape, mx = _map_of(x, "x")
-    _, my = _map_of(y, "y")
-    mr = None if residual is None else _map_of(residual, "residual")[1]
-    _check(_native.load().map_dropout(mx, mr, my, *shape, dtype, _drop_of((p, seed, offset)), _stream(stream)),
-           "map_dropout")
-
-
-def _norm_of(shape, groups, x, act, eps):
-    return RzNorm(*shape, groups, _map_dtype(x, "x"), act, eps)
+    both = (x, y) if residual is None else (x, y, residual)
+    for t in both[1:]:
+        if t.dtype is not x.dtype or t.shape != x.shape or not t.is_cuda:
+            raise ValueError("x, y and residual differ in dtype, shape or device")
+    if not x.is_cuda:
+        raise ValueError("x: expected a CUDA tensor")
+    if all(t.is_contiguous() for t in both):
+        # any shape whose elements follow one another: as many images of one row, of the last dimension
+        n = x.numel()
+        wide = x.shape[-1] if n and x.dim() else n
+        shape, row = (n // wide if n else 1, 1, wide, 1), wide * x.element_size()
+        maps = [RzMap(t.data_ptr(), row, row) for t in both]
+    else:
+        shape = _map_of(x, "x")[0]
+        maps = [_map_of(t, name)[1] for t, name in zip(both, ("x", "y", "residual"))]
+    _check(_native.load().map_dropout(maps[0], maps[2] if residual is not None else None, maps[1], *shape, dtype,
+                                      _drop_of(p, seed, offset), _stream_at(stream, x)), "map_dropout")
 
 
 def _norm_workspace(d) -> int:
@@ -467,7 +482,8 @@ def _norm_workspace(d) -> int:
 
 def map_group_norm_workspace(x, groups: int) -> int:
     """Bytes of workspace that map_group_norm and map_group_norm_grad need on a map like x."""
-    return _norm_workspace(_norm_of(_map_of(x, "x")[0], groups, x, RZ_ACT_NONE, 1.0))
+    _with_torch()
+    return _norm_workspace(RzNorm(*_map_of(x, "x")[0], groups, _map_dtype(x, "x"), RZ_ACT_NONE, 1.0))
 
 
 def map_group_norm(x, y, groups: int, gamma=None, beta=None, mean=None, rstd=None, act: int = RZ_ACT_NONE,
@@ -478,38 +494,43 @@ def map_group_norm(x, y, groups: int, gamma=None, beta=None, mean=None, rstd=Non
     for the gradient, or None; act: RZ_ACT_*; drop: (p, seed, offset) or None;
     workspace: a CUDA tensor of map_group_norm_workspace(x, groups) bytes, or
     None to take one from torch's allocator."""
+    _with_torch()
     shape, mx = _map_of(x, "x")
-    _, my = _map_of(y, "y", shape)
-    if y.dtype != x.dtype:
+    my = _map_of(y, "y", shape)[1]
+    if y.dtype is not x.dtype:
         raise ValueError("x and y differ in dtype")
-    N, C = shape[0], shape[3]
-    d = _norm_of(shape, groups, x, act, eps)
-    ws = _workspace(workspace, _norm_workspace(d) if workspace is None else 0, x, stream)
+    d = RzNorm(*shape, groups, _map_dtype(x, "x"), act, eps)
+    if workspace is None:
+        workspace = _workspace(_norm_workspace(d), x, stream)
+    channels, stats = (shape[3],), (shape[0], groups)
     _check(_native.load().map_group_norm(
-        d, _drop_of(drop), mx, my, _floats(gamma, "gamma", C), _floats(beta, "beta", C),
-        _floats(mean, "mean", N, groups), _floats(rstd, "rstd", N, groups), *_bytes_of(ws), _stream(stream)),
-        "map_group_norm")
+        d, None if drop is None else _drop_of(*drop), mx, my, _floats(gamma, "gamma", channels),
+        _floats(beta, "beta", channels), _floats(mean, "mean", stats), _floats(rstd, "rstd", stats),
+        *_bytes_of(workspace), _stream_at(stream, x)), "map_group_norm")
 
 
 def map_group_norm_grad(dy, x, dx, groups: int, gamma=None, beta=None, mean=None, rstd=None, dgamma=None, dbeta=None,
                         act: int = RZ_ACT_NONE, eps: float = 1e-5, drop=None, workspace=None, stream=None) -> None:
     """dx[:], dgamma[:] and dbeta[:] (either may be None) from dy, with the
     arguments of the map_group_norm call and the mean and rstd it wrote."""
+    _with_torch()
     shape, mx = _map_of(x, "x")
-    _, md = _map_of(dy, "dy", shape)
-    _, mo = _map_of(dx, "dx", shape)
-    if dy.dtype != x.dtype or dx.dtype != x.dtype:
+    md, mo = _map_of(dy, "dy", shape)[1], _map_of(dx, "dx", shape)[1]
+    if dy.dtype is not x.dtype or dx.dtype is not x.dtype:
         raise ValueError("x, dy and dx differ in dtype")
-    N, C = shape[0], shape[3]
-    d = _norm_of(shape, groups, x, act, eps)
-    ws = _workspace(workspace, _norm_workspace(d) if workspace is None else 0, x, stream)
+    d = RzNorm(*shape, groups, _map_dtype(x, "x"), act, eps)
+    if workspace is None:
+        workspace = _workspace(_norm_workspace(d), x, stream)
+    channels, stats = (shape[3],), (shape[0], groups)
     _check(_native.load().map_group_norm_grad(
-        d, _drop_of(drop), md, mx, mo, _floats(gamma, "gamma", C), _floats(beta, "beta", C),
-        _floats(mean, "mean", N, groups), _floats(rstd, "rstd", N, groups), _floats(dgamma, "dgamma", C),
-        _floats(dbeta, "dbeta", C), *_bytes_of(ws), _stream(stream)), "map_group_norm_grad")
+        d, None if drop is None else _drop_of(*drop), md, mx, mo, _floats(gamma, "gamma", channels),
+        _floats(beta, "beta", channels), _floats(mean, "mean", stats), _floats(rstd, "rstd", stats),
+        _floats(dgamma, "dgamma", channels), _floats(dbeta, "dbeta", channels), *_bytes_of(workspace),
+        _stream_at(stream, x)), "map_group_norm_grad")
 
 
 def _resample_of(src, dst, names):
+    _with_torch()
     (Ns, H, W, C), ms = _map_of(src, names[0])
     (N, OH, OW, C2), md = _map_of(dst, names[1])
     if C2 != C or Ns not in (1, N):
@@ -524,29 +545,31 @@ def resize_map(src, dst, base=None, stream=None) -> None:
     d, ms, md = _resample_of(src, dst, ("src", "dst"))
     mb = None
     if base is not None:
-        if base.dtype != dst.dtype:
+        if base.dtype is not dst.dtype:
             raise ValueError("base and dst differ in dtype")
         mb = _map_of(base, "base", (d.N, d.out_h, d.out_w, d.C))[1]
-    _check(_native.load().resize_map(d, ms, mb, md, _stream(stream)), "resize_map")
+    _check(_native.load().resize_map(d, ms, mb, md, _stream_at(stream, dst)), "resize_map")
+
+
+def _resample_workspace(d) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_native.load().resize_map_grad_workspace(d, ctypes.byref(n)), "resize_map_grad_workspace")
+    return n.value
 
 
 def resize_map_grad_workspace(ddst, dsrc) -> int:
     """Bytes of workspace that resize_map_grad needs for these maps."""
-    n = ctypes.c_size_t(0)
-    _check(_native.load().resize_map_grad_workspace(_resample_of(dsrc, ddst, ("dsrc", "ddst"))[0], ctypes.byref(n)),
-           "resize_map_grad_workspace")
-    return n.value
+    return _resample_workspace(_resample_of(dsrc, ddst, ("dsrc", "ddst"))[0])
 
 
 def resize_map_grad(ddst, dsrc, workspace=None, stream=None) -> None:
     """dsrc[:] = the gradient of resize_map towards src, from ddst; summed over
     the images where dsrc has one."""
     d, ms, md = _resample_of(dsrc, ddst, ("dsrc", "ddst"))
-    n = ctypes.c_size_t(0)
     if workspace is None:
-        _check(_native.load().resize_map_grad_workspace(d, ctypes.byref(n)), "resize_map_grad_workspace")
-    ws = _workspace(workspace, n.value, ddst, stream)
-    _check(_native.load().resize_map_grad(d, md, ms, *_bytes_of(ws), _stream(stream)), "resize_map_grad")
+        workspace = _workspace(_resample_workspace(d), ddst, stream)
+    _check(_native.load().resize_map_grad(d, md, ms, *_bytes_of(workspace), _stream_at(stream, ddst)),
+           "resize_map_grad")
 
 
 class Texture:

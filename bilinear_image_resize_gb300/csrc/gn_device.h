@@ -9,6 +9,11 @@
 
 namespace rz {
 
+using maps::both;
+using maps::kPairs;
+using maps::pack2;
+using maps::unpack2;
+
 constexpr float kLog2e = 1.44269504f;
 constexpr int kGnSms = 152;
 constexpr int kGnMaxCluster = 8;    // CTAs a cluster (the portable limit)
@@ -61,34 +66,6 @@ cudaError_t gn_kinds(int act, bool drop, Fn fn)
     };
     return drop ? on(std::true_type{}) : on(std::false_type{});
 }
-
-// VE elements as pairs, for the paired float32 instructions (half the issue
-// slots of two scalar ones); a single element leaves the second half 0.
-template <int VE> constexpr int kPairs = (VE + 1) / 2;
-
-template <class T, int VE>
-__device__ __forceinline__ void unpack2(const maps::Raw<T, VE> &r, float2 (&f)[kPairs<VE>])
-{
-    float s[2 * kPairs<VE>];
-    s[2 * kPairs<VE> - 1] = 0.0f;
-    maps::unpack<T, VE>(r, reinterpret_cast<float(&)[VE]>(s));
-#pragma unroll
-    for (int i = 0; i < kPairs<VE>; i++) f[i] = make_float2(s[2 * i], s[2 * i + 1]);
-}
-
-template <class T, int VE>
-__device__ __forceinline__ maps::Raw<T, VE> pack2(const float2 (&f)[kPairs<VE>])
-{
-    float s[2 * kPairs<VE>];
-#pragma unroll
-    for (int i = 0; i < kPairs<VE>; i++) {
-        s[2 * i] = f[i].x;
-        s[2 * i + 1] = f[i].y;
-    }
-    return maps::pack<T, VE>(reinterpret_cast<float(&)[VE]>(s));
-}
-
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 __device__ __forceinline__ float2 sigmoid2(float2 z)
 {

@@ -184,6 +184,34 @@ __device__ __forceinline__ Raw<T, VE> pack(const float (&f)[VE])
     return r;
 }
 
+// VE elements as pairs, for the paired float32 instructions (half the issue
+// slots of two scalar ones); a single element leaves the second half 0.
+template <int VE> constexpr int kPairs = (VE + 1) / 2;
+
+template <class T, int VE>
+__device__ __forceinline__ void unpack2(const Raw<T, VE> &r, float2 (&f)[kPairs<VE>])
+{
+    float s[2 * kPairs<VE>];
+    s[2 * kPairs<VE> - 1] = 0.0f;
+    unpack<T, VE>(r, reinterpret_cast<float(&)[VE]>(s));
+#pragma unroll
+    for (int i = 0; i < kPairs<VE>; i++) f[i] = make_float2(s[2 * i], s[2 * i + 1]);
+}
+
+template <class T, int VE>
+__device__ __forceinline__ Raw<T, VE> pack2(const float2 (&f)[kPairs<VE>])
+{
+    float s[2 * kPairs<VE>];
+#pragma unroll
+    for (int i = 0; i < kPairs<VE>; i++) {
+        s[2 * i] = f[i].x;
+        s[2 * i + 1] = f[i].y;
+    }
+    return pack<T, VE>(reinterpret_cast<float(&)[VE]>(s));
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // Dropout's mask: Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel
 // random numbers: as easy as 1, 2, 3", SC'11), ten rounds on the counter
 // (block, offset) under the key `seed`.  Its four words are cut into eight

@@ -22,6 +22,7 @@ using namespace maps;
 
 constexpr int kMapThreads = 256;
 constexpr int kMapRun = 16;     // rows a thread walks, at most
+constexpr int kMapImages = 4;   // images whose base a thread reads at a time
 
 struct ResampleArgs {
     View src, base, dst;        // gradient: dst is ddst, src is dsrc; base.p null: none
@@ -45,12 +46,13 @@ __device__ __forceinline__ Tap tap(int d, int n_in, int n_out)
 }
 
 // Outputs [lo, hi) that read source index s, and the weight with which d does.
-__device__ __forceinline__ long long ceil_div(long long a, long long b) { return a >= 0 ? (a + b - 1) / b : -(-a / b); }
 __device__ __forceinline__ int2 readers(int s, int n_in, int n_out)
 {
-    const long long lo = s == 0 ? 0 : ceil_div((2LL * s - 1) * n_out - n_in, 2LL * n_in);
-    const long long hi = s == n_in - 1 ? n_out : ceil_div((2LL * s + 3) * n_out - n_in, 2LL * n_in);
-    return make_int2(static_cast<int>(max(lo, 0LL)), static_cast<int>(min(hi, static_cast<long long>(n_out))));
+    // rounded up: the first d with floor(x_d) >= s - 1, and the first with floor(x_d) > s
+    const int den = 2 * n_in;
+    const int lo = s == 0 ? 0 : dev::floor_div_exact((2LL * s - 1) * n_out + n_in - 1, den);
+    const int hi = s == n_in - 1 ? n_out : dev::floor_div_exact((2LL * s + 3) * n_out + n_in - 1, den);
+    return make_int2(max(lo, 0), min(hi, n_out));
 }
 __device__ __forceinline__ float tap_weight(int d, int s, int n_in, int n_out)
 {
@@ -70,9 +72,9 @@ __device__ __forceinline__ const Raw<T, VE> *map_at(const View &v, long long n, 
 // of the two source rows at hand and takes the lower one over as the next
 // upper one, so an upscale reads each source row about once per run where a
 // pixel on its own would read four taps; the sampling positions of the rows
-// are formed once per block.  A table serves every image: it is interpolated
-// once and added to each image's base.
-template <class S, class T, int VE>
+// are formed once per block.  A table (TABLE) serves every image: it is
+// interpolated once and added to each image's base.
+template <class S, class T, int VE, bool TABLE>
 __global__ void __launch_bounds__(kMapThreads) k_resize_map(const ResampleArgs a)
 {
     __shared__ Tap taps[kMapRun];
@@ -85,50 +87,85 @@ __global__ void __launch_bounds__(kMapThreads) k_resize_map(const ResampleArgs a
     if (i >= a.OW * vecs) return;
     const int ox = static_cast<int>(i / vecs), c = static_cast<int>(i - ox * vecs) * VE;
     const Tap tx = tap(ox, a.W, a.OW);
-    const bool table = a.src_n == 1;
-    const int n0 = table ? 0 : s, n1 = table ? a.N : s + 1;
-    float up[VE], low[VE];
+    const uint8_t *src = reinterpret_cast<const uint8_t *>(map_at<S, VE>(a.src, s, 0, tx.a, a.C, c));
+    const long long far = tx.b == tx.a ? 0 : static_cast<long long>(a.C) * sizeof(S);
+    uint8_t *dst = reinterpret_cast<uint8_t *>(const_cast<Raw<T, VE> *>(map_at<T, VE>(a.dst, s, y0, ox, a.C, c)));
+    const uint8_t *add = a.base.p ? reinterpret_cast<const uint8_t *>(map_at<T, VE>(a.base, s, y0, ox, a.C, c)) : nullptr;
+    float up[VE], low[VE], step[VE];     // step = low - up
+#pragma unroll
+    for (int k = 0; k < VE; k++) low[k] = 0.0f;
     int iu = -1, il = -1;
     const auto across = [&](int y, float (&f)[VE]) {
+        const uint8_t *p = src + y * a.src.pitch;
+        const Raw<S, VE> r0 = *reinterpret_cast<const Raw<S, VE> *>(p), r1 = *reinterpret_cast<const Raw<S, VE> *>(p + far);
         float q[VE];
-        const Raw<S, VE> ra = *map_at<S, VE>(a.src, s, y, tx.a, a.C, c), rb = *map_at<S, VE>(a.src, s, y, tx.b, a.C, c);
-        unpack<S, VE>(ra, f);
-        unpack<S, VE>(rb, q);
+        unpack<S, VE>(r0, f);
+        unpack<S, VE>(r1, q);
 #pragma unroll
         for (int k = 0; k < VE; k++) f[k] = fmaf(tx.u, q[k] - f[k], f[k]);
-    };
-    const auto copy = [](float (&to)[VE], const float (&from)[VE]) {
-#pragma unroll
-        for (int k = 0; k < VE; k++) to[k] = from[k];
     };
     dev::grid_dependency_wait();
     for (int j = 0; j < rows; j++) {
         const Tap ty = taps[j];
-        if (ty.a != iu) {
-            if (ty.a == il) copy(up, low);
-            else across(ty.a, up);
-            iu = ty.a;
-        }
-        if (ty.b != il) {
-            if (ty.b == iu) copy(low, up);
-            else across(ty.b, low);
-            il = ty.b;
+        if (ty.a != iu || ty.b != il) {
+            // the lower row moves up and the next one comes in below: once, but for a run's first row and rows
+            // that a reduction skips
+            do {
+#pragma unroll
+                for (int k = 0; k < VE; k++) up[k] = low[k];
+                iu = il;
+                il = iu == ty.a ? ty.b : ty.a;
+                across(il, low);
+            } while (iu != ty.a || il != ty.b);
+#pragma unroll
+            for (int k = 0; k < VE; k++) step[k] = low[k] - up[k];
         }
         float out[VE];
 #pragma unroll
-        for (int k = 0; k < VE; k++) out[k] = fmaf(ty.u, low[k] - up[k], up[k]);
-#pragma unroll 4
-        for (int n = n0; n < n1; n++) {
-            float f[VE];
-            if (a.base.p) {
-                unpack<T, VE>(__ldcs(map_at<T, VE>(a.base, n, y0 + j, ox, a.C, c)), f);
+        for (int k = 0; k < VE; k++) out[k] = fmaf(ty.u, step[k], up[k]);
+        if (TABLE) {
+            uint8_t *to = dst;
+            const uint8_t *from = add;
+            if (add) {
+                int n = 0;
+                for (; n + kMapImages <= a.N; n += kMapImages) {
+                    Raw<T, VE> r[kMapImages];
 #pragma unroll
-                for (int k = 0; k < VE; k++) f[k] += out[k];
+                    for (int m = 0; m < kMapImages; m++)
+                        r[m] = __ldcs(reinterpret_cast<const Raw<T, VE> *>(from + m * a.base.bstride));
+#pragma unroll
+                    for (int m = 0; m < kMapImages; m++) {
+                        float f[VE];
+                        unpack<T, VE>(r[m], f);
+#pragma unroll
+                        for (int k = 0; k < VE; k++) f[k] += out[k];
+                        __stcs(reinterpret_cast<Raw<T, VE> *>(to + m * a.dst.bstride), pack<T, VE>(f));
+                    }
+                    from += kMapImages * a.base.bstride;
+                    to += kMapImages * a.dst.bstride;
+                }
+                for (; n < a.N; n++, from += a.base.bstride, to += a.dst.bstride) {
+                    float f[VE];
+                    unpack<T, VE>(__ldcs(reinterpret_cast<const Raw<T, VE> *>(from)), f);
+#pragma unroll
+                    for (int k = 0; k < VE; k++) f[k] += out[k];
+                    __stcs(reinterpret_cast<Raw<T, VE> *>(to), pack<T, VE>(f));
+                }
             } else {
-                copy(f, out);
+                const Raw<T, VE> r = pack<T, VE>(out);
+                for (int n = 0; n < a.N; n++, to += a.dst.bstride) __stcs(reinterpret_cast<Raw<T, VE> *>(to), r);
             }
-            __stcs(const_cast<Raw<T, VE> *>(map_at<T, VE>(a.dst, n, y0 + j, ox, a.C, c)), pack<T, VE>(f));
+        } else {
+            if (add) {
+                float f[VE];
+                unpack<T, VE>(__ldcs(reinterpret_cast<const Raw<T, VE> *>(add)), f);
+#pragma unroll
+                for (int k = 0; k < VE; k++) out[k] += f[k];
+            }
+            __stcs(reinterpret_cast<Raw<T, VE> *>(dst), pack<T, VE>(out));
         }
+        dst += a.dst.pitch;
+        if (add) add += a.base.pitch;
     }
 }
 
@@ -166,9 +203,16 @@ __global__ void __launch_bounds__(kMapThreads) k_sum_images(const ResampleArgs a
 // READERS / 2, weighed as they come), and the sum goes to the two source rows
 // that the output row lies between, so that each output row is read once per
 // run and not once for each source row.
+// Output rows whose readers a thread loads before it uses the first: more in
+// flight for 16-bit maps, fewer registers for the short launches of a float32
+// table's sum (upsample 2x, 8 x 128 x 128 x 256 f16: 88 us with four, 101 with
+// two; a 24 x 24 x 1024 table: 18 us with two, 23 with four).
+template <class T> constexpr int kGradRows = sizeof(T) == 2 ? 4 : 2;
+
 template <class S, class T, int VE, int READERS>
 __global__ void __launch_bounds__(kMapThreads) k_resize_map_grad(const ResampleArgs a)
 {
+    constexpr int kRows = kGradRows<T>;
     constexpr int kTaps = 32;
     __shared__ Tap taps[kTaps];
     dev::grid_launch_dependents();
@@ -177,18 +221,29 @@ __global__ void __launch_bounds__(kMapThreads) k_resize_map_grad(const ResampleA
     const bool on = i < a.W * vecs;
     const int x = on ? static_cast<int>(i / vecs) : 0, c = on ? static_cast<int>(i - x * vecs) * VE : 0;
     const int2 rx = readers(x, a.W, a.OW);
+    const int count = on ? rx.y - rx.x : 0;
+    // loads past the last reader repeat it
     float wx[READERS];
+    int off[READERS];
 #pragma unroll
-    for (int k = 0; k < READERS; k++) wx[k] = rx.x + k < rx.y ? tap_weight(rx.x + k, x, a.W, a.OW) : 0.0f;
+    for (int k = 0; k < READERS; k++) {
+        wx[k] = k < count ? tap_weight(rx.x + k, x, a.W, a.OW) : 0.0f;
+        off[k] = max(min(k, count - 1), 0) * a.C * static_cast<int>(sizeof(T));
+    }
     const int y0 = blockIdx.y * a.run, y1 = min(y0 + a.run, a.H), n = blockIdx.z;
     const int lo = readers(y0, a.H, a.OH).x, hi = readers(y1 - 1, a.H, a.OH).y;
+    const uint8_t *row = reinterpret_cast<const uint8_t *>(map_at<T, VE>(a.dst, n, lo, rx.x, a.C, c));
+    uint8_t *out = reinterpret_cast<uint8_t *>(const_cast<Raw<S, VE> *>(map_at<S, VE>(a.src, n, y0, x, a.C, c)));
     dev::grid_dependency_wait();
     float cur[VE], next[VE];   // source rows y and y + 1
     int y = y0 - 1;
 #pragma unroll
     for (int k = 0; k < VE; k++) cur[k] = next[k] = 0.0f;
     const auto flush = [&] {
-        if (on && y >= y0 && y < y1) *const_cast<Raw<S, VE> *>(map_at<S, VE>(a.src, n, y, x, a.C, c)) = pack<S, VE>(cur);
+        if (y >= y0) {
+            if (on) *reinterpret_cast<Raw<S, VE> *>(out) = pack<S, VE>(cur);
+            out += a.src.pitch;
+        }
         y++;
 #pragma unroll
         for (int k = 0; k < VE; k++) {
@@ -197,47 +252,57 @@ __global__ void __launch_bounds__(kMapThreads) k_resize_map_grad(const ResampleA
         }
     };
     for (int base = lo; base < hi; base += kTaps) {
-        const int count = min(kTaps, hi - base);
+        const int some = min(kTaps, hi - base);
         __syncthreads();
-        if (threadIdx.x < count) taps[threadIdx.x] = tap(base + threadIdx.x, a.H, a.OH);
+        if (threadIdx.x < some) taps[threadIdx.x] = tap(base + threadIdx.x, a.H, a.OH);
         __syncthreads();
-        for (int j = 0; j < count; j++) {
-            float h[VE];
+        for (int j = 0; j < some; j += kRows) {
+            Raw<T, VE> r[kRows][READERS];
+            if (count > 0) {
 #pragma unroll
-            for (int k = 0; k < VE; k++) h[k] = 0.0f;
-            if (on) {
-                const Raw<T, VE> *row = map_at<T, VE>(a.dst, n, base + j, rx.x, a.C, c);
-                Raw<T, VE> r[READERS];
+                for (int m = 0; m < kRows; m++)
+                    if (j + m < some) {
 #pragma unroll
-                for (int q = 0; q < READERS; q++)
-                    if (rx.x + q < rx.y) r[q] = row[static_cast<long long>(q) * vecs];
+                        for (int q = 0; q < READERS; q++)
+                            r[m][q] = *reinterpret_cast<const Raw<T, VE> *>(row + m * a.dst.pitch + off[q]);
+                    }
+            }
 #pragma unroll
-                for (int q = 0; q < READERS; q++)
-                    if (rx.x + q < rx.y) {
+            for (int m = 0; m < kRows; m++)
+                if (j + m < some) {
+                    float h[VE];
+#pragma unroll
+                    for (int k = 0; k < VE; k++) h[k] = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < READERS; q++) {
+                        if (q >= count) break;
                         float f[VE];
-                        unpack<T, VE>(r[q], f);
+                        unpack<T, VE>(r[m][q], f);
 #pragma unroll
                         for (int k = 0; k < VE; k++) h[k] = fmaf(wx[q], f[k], h[k]);
                     }
-                for (int ox = rx.x + READERS; ox < rx.y; ox++) {
-                    const float w = tap_weight(ox, x, a.W, a.OW);
-                    float f[VE];
-                    unpack<T, VE>(row[static_cast<long long>(ox - rx.x) * vecs], f);
+                    const Raw<T, VE> *more = reinterpret_cast<const Raw<T, VE> *>(row + m * a.dst.pitch);
+                    for (int q = READERS; q < count; q++) {
+                        const float w = tap_weight(rx.x + q, x, a.W, a.OW);
+                        float f[VE];
+                        unpack<T, VE>(more[static_cast<long long>(q) * vecs], f);
 #pragma unroll
-                    for (int k = 0; k < VE; k++) h[k] = fmaf(w, f[k], h[k]);
+                        for (int k = 0; k < VE; k++) h[k] = fmaf(w, f[k], h[k]);
+                    }
+                    const Tap t = taps[j + m];
+                    while (t.a > y && y < y1) flush();
+                    // the near row may lie before the run and the far one after it: both are then left to other blocks
+                    const float w = t.b == t.a ? 1.0f : 1.0f - t.u;
+                    if (t.a == y) {
+#pragma unroll
+                        for (int k = 0; k < VE; k++) cur[k] = fmaf(w, h[k], cur[k]);
+                    }
+                    if (t.b == y + 1) {
+#pragma unroll
+                        for (int k = 0; k < VE; k++) next[k] = fmaf(t.u, h[k], next[k]);
+                    }
                 }
-            }
-            const Tap t = taps[j];
-            while (t.a > y) flush();
-            if (t.a == y) {
-                const float w = t.b == t.a ? 1.0f : 1.0f - t.u;
-#pragma unroll
-                for (int k = 0; k < VE; k++) cur[k] = fmaf(w, h[k], cur[k]);
-            }
-            if (t.b == y + 1) {
-#pragma unroll
-                for (int k = 0; k < VE; k++) next[k] = fmaf(t.u, h[k], next[k]);
-            }
+            row += kRows * a.dst.pitch;
         }
     }
     while (y < y1) flush();
@@ -354,7 +419,9 @@ int resize_map(const rz_resample *d, const rz_map *src, const rz_map *base, cons
     return resample_status(resample_dispatch(d, wide, [&](auto ts, auto td, auto v) {
         constexpr int V = decltype(v)::value;
         const dim3 grid = map_grid(a.OW, a.C / V, a.OH, a.src_n, &a.run);
-        return maps::launch(k_resize_map<decltype(ts), decltype(td), V>, grid, kMapThreads, 0, stream, a);
+        const auto fn = a.N == a.src_n ? k_resize_map<decltype(ts), decltype(td), V, false>
+                                       : k_resize_map<decltype(ts), decltype(td), V, true>;
+        return maps::launch(fn, grid, kMapThreads, 0, stream, a);
     }));
 }
 
