@@ -31,8 +31,8 @@ struct GnArgs {
     maps::Drop drop;
     float2 *chan;               // [N][C]: {mean, squared distances}; [rows][C]: {sum dz, sum dz xh}
     int rows;
-    // cluster kernels: groups and vectors a slab, slabs an image, CTAs a cluster, vectors a thread keeps
-    int gs, lv, slabs, cl, keep;
+    // cluster kernels: groups and vectors a slab, slabs an image, CTAs a cluster, vectors a thread keeps, clusters
+    int gs, lv, slabs, cl, keep, clusters;
     // pass kernels: chunks of an image and their pixels
     float2 *part;               // [N][chunks][C]: a chunk's share of chan
     int chunks;
@@ -45,8 +45,8 @@ constexpr int kGnShared = 112 * 1024;
 cudaError_t gn_shared(const void *fn);
 
 // Cluster kernels (gn_cluster.cu): whether an image's slab fits a cluster; sets
-// gs, lv, cl and keep.
-bool gn_cluster_plan(GnArgs &a, size_t es, bool grad);
+// gs, lv, slabs, cl, keep, clusters and rows.
+cudaError_t gn_cluster_plan(GnArgs &a, size_t es, bool grad, bool *fits);
 cudaError_t gn_cluster_forward(const GnArgs &a, int dtype, bool drop, void *stream);
 cudaError_t gn_cluster_backward(const GnArgs &a, int dtype, bool drop, void *stream);
 
@@ -94,13 +94,13 @@ __device__ __forceinline__ float2 act_slope2(float2 z)
     return both(1.0f);
 }
 
-// Zeroes the dropped ones of the VE elements from `e`; the scale of the kept
-// ones is left to the caller.
+// Zeroes the dropped ones of the VE elements from lane `lane` of a block; the
+// scale of the kept ones is left to the caller.
 template <int VE>
-__device__ __forceinline__ void drop2(float2 (&f)[kPairs<VE>], unsigned long long e, const maps::Drop &d)
+__device__ __forceinline__ void drop2(float2 (&f)[kPairs<VE>], unsigned long long block, unsigned lane, const maps::Drop &d)
 {
     bool keep[VE];
-    maps::kept<VE>(keep, e, d);
+    maps::kept<VE>(keep, block, lane, d);
 #pragma unroll
     for (int i = 0; i < VE; i++) {
         float &v = (i & 1) ? f[i / 2].y : f[i / 2].x;
@@ -145,7 +145,8 @@ __device__ __forceinline__ void gn_save(float *to, const float2 (&f)[kPairs<VE>]
 // One vector forward: x in, y out.
 template <class T, int VE, bool DROP, int ACT>
 __device__ __forceinline__ maps::Raw<T, VE> gn_value(const maps::Raw<T, VE> &x, const Channel<VE> &k,
-                                                     const maps::Drop &drop, unsigned long long e)
+                                                     const maps::Drop &drop, unsigned long long block,
+                                                     unsigned lane)
 {
     float2 f[kPairs<VE>];
     unpack2<T, VE>(x, f);
@@ -154,7 +155,7 @@ __device__ __forceinline__ maps::Raw<T, VE> gn_value(const maps::Raw<T, VE> &x, 
         f[i] = act_value2<ACT>(__ffma2_rn(__fadd2_rn(f[i], k.shift[i]), k.a[i], k.beta[i]));
         if (DROP) f[i] = __fmul2_rn(f[i], both(drop.scale));
     }
-    if (DROP) drop2<VE>(f, e, drop);
+    if (DROP) drop2<VE>(f, block, lane, drop);
     return pack2<T, VE>(f);
 }
 
@@ -162,12 +163,12 @@ __device__ __forceinline__ maps::Raw<T, VE> gn_value(const maps::Raw<T, VE> &x, 
 // dropout's scale.
 template <class T, int VE, bool DROP, int ACT>
 __device__ __forceinline__ void gn_dz(const maps::Raw<T, VE> &x, const maps::Raw<T, VE> &dy, const Channel<VE> &k,
-                                      const maps::Drop &drop, unsigned long long e, float2 (&d)[kPairs<VE>],
-                                      float2 (&dz)[kPairs<VE>])
+                                      const maps::Drop &drop, unsigned long long block, unsigned lane,
+                                      float2 (&d)[kPairs<VE>], float2 (&dz)[kPairs<VE>])
 {
     unpack2<T, VE>(x, d);
     unpack2<T, VE>(dy, dz);
-    if (DROP) drop2<VE>(dz, e, drop);
+    if (DROP) drop2<VE>(dz, block, lane, drop);
 #pragma unroll
     for (int i = 0; i < kPairs<VE>; i++) {
         d[i] = __fadd2_rn(d[i], k.shift[i]);

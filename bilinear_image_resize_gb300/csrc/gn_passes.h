@@ -1,9 +1,10 @@
 // Group norm and its gradient for images of any size and layout, in passes: a
 // launch that sums each channel by chunks of an image, a small one that joins
-// the chunks, and one that applies the result.  group_norm.cu states the
-// formulas.  A map up to L2's size is read from DRAM once; cutting larger calls
-// into batches that fit L2 measured slower than reading them twice (batches of
-// 64 MB: the gradient of 4 x 512 x 512 x 128 bf16 278 us against 231 us).
+// the chunks, and one that applies the result, from the map's end backwards.
+// group_norm.cu states the formulas.  Of a map up to L2's size the second
+// reading costs no DRAM; cutting larger calls into batches that fit L2 measured
+// slower than reading them twice (batches of 64 MB: the gradient of 4 x 512 x
+// 512 x 128 bf16 278 us against 231 us).
 //
 // A thread keeps one vector of channels and walks pixels, so sums are taken by
 // channel whatever the group's width; groups are put together from channels at
@@ -34,7 +35,9 @@ struct GpPlace {
     bool on;
 };
 
-template <int VE>
+// BACK: from the last image's last chunk on, so that the pass which applies
+// begins with what the summing one has left in L2.
+template <int VE, bool BACK>
 __device__ __forceinline__ GpPlace gp_place(const GnArgs &a)
 {
     GpPlace t;
@@ -43,10 +46,10 @@ __device__ __forceinline__ GpPlace gp_place(const GnArgs &a)
     t.lanes = kGpThreads / t.width;
     t.lane = threadIdx.x / t.width;
     t.vec = threadIdx.x - t.lane * t.width;
-    t.n = blockIdx.z;
+    t.n = BACK ? gridDim.z - 1 - blockIdx.z : blockIdx.z;
     t.first = start * VE;
     t.c = t.first + t.vec * VE;
-    t.p0 = blockIdx.x * a.chunk_px;
+    t.p0 = (BACK ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * a.chunk_px;
     t.p1 = min(a.HW, t.p0 + a.chunk_px);
     t.on = t.lane < t.lanes;
     return t;
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_stats(const GnArgs a
     __shared__ int count[kGpThreads];
     dev::grid_launch_dependents();
     dev::grid_dependency_wait();
-    const GpPlace t = gp_place<VE>(a);
+    const GpPlace t = gp_place<VE, false>(a);
     float2 mean[kPairs<VE>], m2[kPairs<VE>];
 #pragma unroll
     for (int i = 0; i < kPairs<VE>; i++) mean[i] = m2[i] = both(0.0f);
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_apply(const GnArgs a
 {
     extern __shared__ __align__(16) float gp_smem[];    // three constants a channel, then two statistics a group
     dev::grid_launch_dependents();
-    const GpPlace t = gp_place<VE>(a);
+    const GpPlace t = gp_place<VE, true>(a);
     const int channels = t.width * VE, g0 = t.first / a.Cg;
     float2 *group = reinterpret_cast<float2 *>(gp_smem + align_up(3 * channels, 2));
     dev::grid_dependency_wait();
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_apply(const GnArgs a
         },
         [&](int g, float2 s) {
             if ((threadIdx.x & 31)) return;
-            const float rstd = 1.0f / sqrtf(fmaf(s.x, a.inv_m, a.eps));
+            const float rstd = rsqrtf(fmaf(s.x, a.inv_m, a.eps));
             group[g - g0].y = rstd;
             if (blockIdx.x == 0 && g * a.Cg >= t.first) {
                 a.mean[t.n * a.G + g] = group[g - g0].x;
@@ -283,8 +286,9 @@ __global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_apply(const GnArgs a
 #pragma unroll
             for (int j = 0; j < decltype(count)::value; j++) {
                 const unsigned px = p + j * t.lanes;
+                const unsigned long long e = gp_element(a, t, px);
                 __stcs(const_cast<Raw<T, VE> *>(gp_at<T, VE>(a.y, a, t, px)),
-                       gn_value<T, VE, DROP, ACT>(r[j].x, k, a.drop, gp_element(a, t, px)));
+                       gn_value<T, VE, DROP, ACT>(r[j].x, k, a.drop, e >> 3, e & 7));
             }
         });
 }
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_sums(const GnArgs a)
 {
     extern __shared__ __align__(16) float gp_smem[];    // three constants a channel; then the threads' sums
     dev::grid_launch_dependents();
-    const GpPlace t = gp_place<VE>(a);
+    const GpPlace t = gp_place<VE, false>(a);
     const int channels = t.width * VE;
     dev::grid_dependency_wait();
     for (int c = threadIdx.x; c < channels; c += kGpThreads) {
@@ -318,7 +322,8 @@ __global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_sums(const GnArgs a)
 #pragma unroll
                 for (int j = 0; j < decltype(count)::value; j++) {
                     float2 d[kPairs<VE>], dz[kPairs<VE>];
-                    gn_dz<T, VE, DROP, ACT>(r[j].x, r[j].dy, k, a.drop, gp_element(a, t, p + j * t.lanes), d, dz);
+                    const unsigned long long e = gp_element(a, t, p + j * t.lanes);
+                    gn_dz<T, VE, DROP, ACT>(r[j].x, r[j].dy, k, a.drop, e >> 3, e & 7, d, dz);
 #pragma unroll
                     for (int i = 0; i < kPairs<VE>; i++) {
                         s1[i] = __fadd2_rn(s1[i], dz[i]);
@@ -356,7 +361,7 @@ __global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_dx(const GnArgs a)
 {
     extern __shared__ __align__(16) float gp_smem[];    // five constants a channel, then two sums a group
     dev::grid_launch_dependents();
-    const GpPlace t = gp_place<VE>(a);
+    const GpPlace t = gp_place<VE, true>(a);
     const int channels = t.width * VE, g0 = t.first / a.Cg;
     float2 *group = reinterpret_cast<float2 *>(gp_smem + align_up(5 * channels, 2));
     dev::grid_dependency_wait();
@@ -395,7 +400,8 @@ __global__ void __launch_bounds__(kGpThreads, kGpCtas) k_gp_dx(const GnArgs a)
             for (int j = 0; j < decltype(count)::value; j++) {
                 const unsigned px = p + j * t.lanes;
                 float2 d[kPairs<VE>], dz[kPairs<VE>];
-                gn_dz<T, VE, DROP, ACT>(r[j].x, r[j].dy, k, a.drop, gp_element(a, t, px), d, dz);
+                const unsigned long long e = gp_element(a, t, px);
+                gn_dz<T, VE, DROP, ACT>(r[j].x, r[j].dy, k, a.drop, e >> 3, e & 7, d, dz);
 #pragma unroll
                 for (int i = 0; i < kPairs<VE>; i++) {
                     if (DROP) dz[i] = __fmul2_rn(dz[i], both(a.drop.scale));

@@ -218,9 +218,13 @@ int map_group_norm(const rz_norm *d, const rz_drop *drop, const rz_map *x, const
     a.rstd = rstd ? rstd : stat + static_cast<size_t>(a.N) * a.G;
     a.drop = maps::make_drop(drop);
     const bool dropping = maps::drop_threshold(drop) != 0;
-    if (a.joined && ve * s.es == 16 && gn_cluster_plan(a, s.es, false))
-        return gn_status(gn_cluster_forward(a, d->dtype, dropping, stream));
-    return gn_status(gn_passes(a, d->dtype, ve, dropping, false, stream));
+    bool cluster = false;
+    if (a.joined && ve * s.es == 16) {
+        const cudaError_t e = gn_cluster_plan(a, s.es, false, &cluster);
+        if (e != cudaSuccess) return gn_status(e);
+    }
+    return gn_status(cluster ? gn_cluster_forward(a, d->dtype, dropping, stream)
+                             : gn_passes(a, d->dtype, ve, dropping, false, stream));
 }
 
 int map_group_norm_grad(const rz_norm *d, const rz_drop *drop, const rz_map *dy, const rz_map *x, const rz_map *dx, const float *gamma,
@@ -266,11 +270,12 @@ int map_group_norm_grad(const rz_norm *d, const rz_drop *drop, const rz_map *dy,
     a.dbeta = dbeta;
     a.drop = maps::make_drop(drop);
     const bool dropping = maps::drop_threshold(drop) != 0;
-    cudaError_t e;
-    if (a.joined && ve * s.es == 16 && gn_cluster_plan(a, s.es, true))
-        e = gn_cluster_backward(a, d->dtype, dropping, stream);
-    else
-        e = gn_passes(a, d->dtype, ve, dropping, true, stream);
+    bool cluster = false;
+    cudaError_t e = cudaSuccess;
+    if (a.joined && ve * s.es == 16) e = gn_cluster_plan(a, s.es, true, &cluster);
+    if (e == cudaSuccess)
+        e = cluster ? gn_cluster_backward(a, d->dtype, dropping, stream)
+                    : gn_passes(a, d->dtype, ve, dropping, true, stream);
     if (e == cudaSuccess && (a.dgamma || a.dbeta))
         e = maps::launch(k_gn_params, dim3((a.C + 31) / 32), 256, 0, stream, a);
     return gn_status(e);

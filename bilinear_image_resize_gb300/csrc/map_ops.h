@@ -223,7 +223,7 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 struct Drop {
     unsigned key[20];       // the rounds' keys: the same for every thread, formed on the host
     unsigned off_lo, off_hi;
-    unsigned top;           // in both halves
+    unsigned top;           // in the high half, the low one all ones: what a kept half of a word, shifted up, is above
     float scale;
 };
 
@@ -243,7 +243,7 @@ inline Drop make_drop(const rz_drop *d)
     }
     r.off_lo = static_cast<unsigned>(offset);
     r.off_hi = static_cast<unsigned>(offset >> 32);
-    r.top = (t - 1) * 0x10001u;
+    r.top = (t - 1) << 16 | 0xffffu;
     r.scale = t < 65536 ? static_cast<float>(65536.0 / (65536 - t)) : 0.0f;
     return r;
 }
@@ -264,31 +264,28 @@ __device__ __forceinline__ uint4 philox(unsigned long long block, const Drop &d)
 // Whether the two elements of a word are kept.
 __device__ __forceinline__ void kept_pair(unsigned w, const Drop &d, bool &lo, bool &hi)
 {
-    const unsigned limit = d.top | 0xffffu;
-    lo = w << 16 > limit;
-    hi = w > limit;
+    lo = w << 16 > d.top;
+    hi = w > d.top;
 }
 
-// Which of the VE elements from `e` (a multiple of VE, which divides eight)
-// are kept.
+// Which of the VE elements from lane `lane` of a block (a multiple of VE, which
+// divides eight) are kept.
 template <int VE>
-__device__ __forceinline__ void kept(bool (&keep)[VE], unsigned long long e, const Drop &d)
+__device__ __forceinline__ void kept(bool (&keep)[VE], unsigned long long block, unsigned lane, const Drop &d)
 {
-    const uint4 c = philox(e >> 3, d);
+    const uint4 c = philox(block, d);
     if constexpr (VE == 8) {
         const unsigned w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int i = 0; i < 4; i++) kept_pair(w[i], d, keep[2 * i], keep[2 * i + 1]);
     } else if constexpr (VE == 4) {
-        const bool high = e & 4;
-        kept_pair(high ? c.z : c.x, d, keep[0], keep[1]);
-        kept_pair(high ? c.w : c.y, d, keep[2], keep[3]);
+        kept_pair(lane ? c.z : c.x, d, keep[0], keep[1]);
+        kept_pair(lane ? c.w : c.y, d, keep[2], keep[3]);
     } else {
         static_assert(VE == 1, "");
-        const int j = static_cast<int>(e & 7);
         bool lo, hi;
-        kept_pair((j & 4) ? ((j & 2) ? c.w : c.z) : ((j & 2) ? c.y : c.x), d, lo, hi);
-        keep[0] = (j & 1) ? hi : lo;
+        kept_pair((lane & 4) ? ((lane & 2) ? c.w : c.z) : ((lane & 2) ? c.y : c.x), d, lo, hi);
+        keep[0] = (lane & 1) ? hi : lo;
     }
 }
 
@@ -297,7 +294,7 @@ template <int VE>
 __device__ __forceinline__ void drop_elements(float (&f)[VE], unsigned long long e, const Drop &d)
 {
     bool keep[VE];
-    kept<VE>(keep, e, d);
+    kept<VE>(keep, e >> 3, static_cast<unsigned>(e & 7), d);
 #pragma unroll
     for (int i = 0; i < VE; i++) f[i] = keep[i] ? f[i] * d.scale : 0.0f;
 }
