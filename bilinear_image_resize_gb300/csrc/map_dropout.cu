@@ -15,50 +15,79 @@ namespace {
 using namespace maps;
 
 constexpr int kDropThreads = 256;
+constexpr int kDropVecs = 4;    // vectors a thread reads before it uses the first
 
 struct DropArgs {
     View x, r, y;               // r.p null: no residual
-    unsigned long long rows;    // N H rows, or one for the whole map
-    unsigned long long row;     // elements of a row
+    unsigned long long total;   // vectors
+    unsigned long long row;     // vectors of a row
     unsigned H;                 // rows an image
+    unsigned tail;              // elements after the last vector of maps whose elements follow one another
     Drop drop;
     int dropping;
 };
 
-// Thread i takes vectors i, i + stride, ... of the map's elements.
-template <class T, int VE>
+// One element of maps whose elements follow one another.
+template <class T, bool RESIDUAL>
+__device__ __forceinline__ void drop_one(const DropArgs &a, unsigned long long e)
+{
+    float f[1], r[1];
+    unpack<T, 1>(reinterpret_cast<const Raw<T, 1> *>(a.x.p)[e], f);
+    if (a.dropping) drop_elements<1>(f, e, a.drop);
+    if (RESIDUAL) {
+        unpack<T, 1>(reinterpret_cast<const Raw<T, 1> *>(a.r.p)[e], r);
+        f[0] += r[0];
+    }
+    reinterpret_cast<Raw<T, 1> *>(a.y.p)[e] = pack<T, 1>(f);
+}
+
+// A CTA takes kDropVecs x kDropThreads consecutive vectors.  WHOLE: the maps'
+// elements follow one another; else vectors are found by row and image.
+template <class T, int VE, bool WHOLE, bool RESIDUAL>
 __global__ void __launch_bounds__(kDropThreads) k_dropout(const DropArgs a)
 {
+    using V = Raw<T, VE>;
     dev::grid_launch_dependents();
+    const unsigned long long first = blockIdx.x * static_cast<unsigned long long>(kDropVecs * kDropThreads) + threadIdx.x;
+    const auto at = [&](const View &m, int u) {
+        const unsigned long long v = first + u * kDropThreads;
+        if (WHOLE) return reinterpret_cast<V *>(m.p) + v;
+        const unsigned long long row = v / a.row, n = row / a.H;
+        return reinterpret_cast<V *>(m.p + n * m.bstride + (row - n * a.H) * m.pitch) + (v - row * a.row);
+    };
     dev::grid_dependency_wait();
-    const unsigned long long per_row = a.row / VE, total = a.rows * per_row;
-    for (unsigned long long v = blockIdx.x * static_cast<unsigned long long>(kDropThreads) + threadIdx.x; v < total;
-         v += static_cast<unsigned long long>(gridDim.x) * kDropThreads) {
-        const unsigned long long row = a.rows == 1 ? 0 : v / per_row;
-        const unsigned long long n = a.rows == 1 ? 0 : row / a.H, h = row - n * a.H;
-        const long long j = static_cast<long long>(v - row * per_row) * VE * static_cast<long long>(sizeof(T));
-        const auto in = [&](const View &m) {
-            return reinterpret_cast<const Raw<T, VE> *>(m.p + n * m.bstride + h * m.pitch + j);
-        };
-        float f[VE];
-        unpack<T, VE>(__ldcs(in(a.x)), f);
-        if (a.dropping) drop_elements<VE>(f, v * VE, a.drop);
-        if (a.r.p) {
-            float r[VE];
-            unpack<T, VE>(__ldcs(in(a.r)), r);
+    if (WHOLE && VE > 1 && first < a.tail) drop_one<T, RESIDUAL>(a, a.total * VE + first);
+    V x[kDropVecs], r[kDropVecs];
 #pragma unroll
-            for (int i = 0; i < VE; i++) f[i] += r[i];
+    for (int u = 0; u < kDropVecs; u++)
+        if (first + u * kDropThreads < a.total) {
+            x[u] = __ldcs(at(a.x, u));
+            if (RESIDUAL) r[u] = __ldcs(at(a.r, u));
         }
-        __stcs(const_cast<Raw<T, VE> *>(in(a.y)), pack<T, VE>(f));
-    }
+#pragma unroll
+    for (int u = 0; u < kDropVecs; u++)
+        if (first + u * kDropThreads < a.total) {
+            float f[VE];
+            unpack<T, VE>(x[u], f);
+            if (a.dropping) drop_elements<VE>(f, (first + u * kDropThreads) * VE, a.drop);
+            if (RESIDUAL) {
+                float g[VE];
+                unpack<T, VE>(r[u], g);
+#pragma unroll
+                for (int i = 0; i < VE; i++) f[i] += g[i];
+            }
+            __stcs(at(a.y, u), pack<T, VE>(f));
+        }
 }
 
 template <class T, int VE>
-cudaError_t drop_launch(const DropArgs &a, void *stream)
+cudaError_t drop_launch(const DropArgs &a, bool whole, void *stream)
 {
-    const unsigned long long blocks = (a.rows * (a.row / VE) + kDropThreads - 1) / kDropThreads;
-    return launch(k_dropout<T, VE>, dim3(static_cast<unsigned>(std::min(blocks, 152ull * 64))), kDropThreads, 0,
-                  stream, a);
+    const unsigned long long blocks = std::max(1ull, (a.total + kDropVecs * kDropThreads - 1) / (kDropVecs * kDropThreads));
+    if (blocks > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+    const auto fn = whole ? (a.r.p ? k_dropout<T, VE, true, true> : k_dropout<T, VE, true, false>)
+                          : (a.r.p ? k_dropout<T, VE, false, true> : k_dropout<T, VE, false, false>);
+    return launch(fn, dim3(static_cast<unsigned>(blocks)), kDropThreads, 0, stream, a);
 }
 
 }  // namespace
@@ -85,21 +114,27 @@ int map_dropout(const rz_map *x, const rz_map *residual, const rz_map *y, int N,
     a.y = maps::view(y);
     if (residual) a.r = maps::view(residual);
     const bool one = whole(x) && whole(y) && whole(residual);
-    a.rows = one ? 1 : static_cast<unsigned long long>(s.N) * s.H;
-    a.row = static_cast<unsigned long long>(s.W) * s.C * (one ? s.N * s.H : 1);
-    a.H = one ? 1 : static_cast<unsigned>(s.H);
+    const unsigned long long row = static_cast<unsigned long long>(s.W) * s.C, all = row * s.N * s.H;
+    a.H = static_cast<unsigned>(s.H);
     a.drop = maps::make_drop(drop);
     a.dropping = maps::drop_threshold(drop) != 0;
     const int ve = 16 / static_cast<int>(s.es);
-    const bool wide = a.row % ve == 0 && maps::map_aligned(*x, s, 16) && maps::map_aligned(*y, s, 16) &&
-                      (!residual || maps::map_aligned(*residual, s, 16));
+    const auto aligned = [&](const rz_map *m) {
+        return !m || (one ? reinterpret_cast<uintptr_t>(m->data) % 16 == 0 : maps::map_aligned(*m, s, 16));
+    };
+    const bool wide = (one || row % ve == 0) && aligned(x) && aligned(y) && aligned(residual);
+    a.row = wide ? row / ve : row;
+    a.total = wide ? all / ve : all;
+    a.tail = wide ? static_cast<unsigned>(all % ve) : 0;
+    // one element at a time a map of 2^41 elements would pass the grid's width
+    if (a.total / (kDropVecs * kDropThreads) >= 0x7fffffffull) return RZ_ERR_UNSUPPORTED;
     cudaError_t e;
     if (dtype == RZ_F32)
-        e = wide ? drop_launch<float, 4>(a, stream) : drop_launch<float, 1>(a, stream);
+        e = wide ? drop_launch<float, 4>(a, one, stream) : drop_launch<float, 1>(a, one, stream);
     else if (dtype == RZ_BF16)
-        e = wide ? drop_launch<__nv_bfloat16, 8>(a, stream) : drop_launch<__nv_bfloat16, 1>(a, stream);
+        e = wide ? drop_launch<__nv_bfloat16, 8>(a, one, stream) : drop_launch<__nv_bfloat16, 1>(a, one, stream);
     else
-        e = wide ? drop_launch<__half, 8>(a, stream) : drop_launch<__half, 1>(a, stream);
+        e = wide ? drop_launch<__half, 8>(a, one, stream) : drop_launch<__half, 1>(a, one, stream);
     if (e == cudaSuccess) return RZ_OK;
     record_cuda_error(static_cast<int>(e));
     return RZ_ERR_CUDA;
