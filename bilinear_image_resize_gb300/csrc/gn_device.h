@@ -16,6 +16,7 @@ using maps::unpack2;
 
 constexpr float kLog2e = 1.44269504f;
 constexpr int kGnSms = 152;
+constexpr int kGnMaxChunks = 4 * kGnSms;  // chunks of an image, pass kernels
 constexpr int kGnMaxCluster = 8;    // CTAs a cluster (the portable limit)
 
 struct GnArgs {

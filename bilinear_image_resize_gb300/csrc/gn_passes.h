@@ -4,7 +4,13 @@
 // group_norm.cu states the formulas.  Of a map up to L2's size the second
 // reading costs no DRAM; cutting larger calls into batches that fit L2 measured
 // slower than reading them twice (batches of 64 MB: the gradient of 4 x 512 x
-// 512 x 128 bf16 278 us against 231 us).
+// 512 x 128 bf16 278 us against 231 us as it then was).
+//
+// The forward is bound by DRAM: 4 x 512 x 512 x 128 bf16 139 us, three
+// transfers of the map at 5.8 TB/s (142 us with SiLU; 181 with dropout, bound by
+// the generator's arithmetic).  The gradient is bound by how many instructions
+// its warps keep going: 8 x 128 x 128 x 512 bf16 115 us (five transfers, 5.8
+// TB/s), 116 with SiLU, 155 with dropout, which both passes make again.
 //
 // A thread keeps one vector of channels and walks pixels, so sums are taken by
 // channel whatever the group's width; groups are put together from channels at
@@ -24,11 +30,15 @@ using namespace maps;
 
 constexpr int kGpThreads = 256, kGpWarps = kGpThreads / 32;
 // Pixels a thread loads before it uses the first, and the CTAs an SM that its
-// registers are held to: the gradient wants its constants and sums in registers
-// and many loads a thread, the forward launches many warps.  4 x 512 x 512 x
-// 128 bf16 with SiLU: forward 152 us so, 164 at two CTAs an SM; gradient 246 us,
-// 267 with two pixels at a time and the next two read ahead.
-constexpr int kGpStats = 4, kGpStatsCtas = 4, kGpApply = 4, kGpApplyCtas = 4, kGpGrad = 4, kGpGradCtas = 2;
+// registers are held to: 4 x 512 x 512 x 128 bf16 with SiLU forward 152 us so,
+// 164 at two CTAs an SM, 155 with the loads through shared memory.
+constexpr int kGpStats = 4, kGpStatsCtas = 4, kGpApply = 4, kGpApplyCtas = 4;
+// The gradient, whose constants and sums fill the registers, has its loads on
+// their way in shared memory, kGpAhead pixels of x and dy a thread, and so a
+// third CTA an SM: 8 x 128 x 128 x 512 bf16 with SiLU and dropout 155 us, 171
+// with four pixels in registers and two CTAs; four CTAs spill, 183.
+constexpr int kGpAhead = 3, kGpGradCtas = 3;
+template <class V> constexpr int kGpRing = 2 * kGpAhead * kGpThreads * static_cast<int>(sizeof(V));
 
 // The thread's place: vector `vec` of the block's `width`, pixel lane `lane`
 // of `lanes`; `c` its first channel, `first` the block's.
@@ -77,10 +87,6 @@ template <class T, int VE>
 struct One {
     Raw<T, VE> x;
 };
-template <class T, int VE>
-struct Two {
-    Raw<T, VE> x, dy;
-};
 
 // Walks the thread's pixels, U at a time while there are U, then one by one:
 // load(pixel) and use(values, count, pixel).
@@ -106,6 +112,51 @@ __device__ __forceinline__ void gp_walk(const GpPlace &t, Load load, Use use)
     for (; p < t.p1; p += t.lanes) {
         const R last[1] = {load(p)};
         use(last, Int<1>{}, p);
+    }
+}
+
+// Copies a vector to the thread's own place in shared memory, asynchronously
+// where it is wide enough.
+template <class V>
+__device__ __forceinline__ void gp_copy(V *to, const V *from)
+{
+    if constexpr (sizeof(V) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dev::smem_addr(to)), "l"(from) : "memory");
+    else if constexpr (sizeof(V) >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dev::smem_addr(to)), "l"(from),
+                     "n"(sizeof(V))
+                     : "memory");
+    else
+        *to = *from;
+}
+__device__ __forceinline__ void gp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void gp_arrived()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Walks the thread's pixels with kGpAhead of them on their way into shared
+// memory: copy(slot, pixel), then use(slot, pixel, refill), which calls
+// refill() once it has read the slot.
+template <int AHEAD, class Copy, class Use>
+__device__ __forceinline__ void gp_stream(const GpPlace &t, Copy copy, Use use)
+{
+    unsigned next = t.p0 + t.lane;
+#pragma unroll
+    for (int s = 0; s < AHEAD; s++, next += t.lanes) {
+        if (next < t.p1) copy(s, next);
+        gp_commit();
+    }
+    int slot = 0;
+    for (unsigned p = t.p0 + t.lane; p < t.p1; p += t.lanes) {
+        gp_arrived<AHEAD - 1>();
+        use(slot, p, [&] {
+            if (next < t.p1) copy(slot, next);
+            gp_commit();
+        });
+        next += t.lanes;
+        slot = slot + 1 == AHEAD ? 0 : slot + 1;
     }
 }
 
@@ -292,7 +343,11 @@ __global__ void __launch_bounds__(kGpThreads, kGpApplyCtas) k_gp_apply(const GnA
 template <class T, int VE, bool DROP, int ACT>
 __global__ void __launch_bounds__(kGpThreads, kGpGradCtas) k_gp_sums(const GnArgs a)
 {
-    extern __shared__ __align__(16) float gp_smem[];    // three constants a channel; then the threads' sums
+    // vectors on their way; three constants a channel, then the threads' sums
+    extern __shared__ __align__(16) uint8_t gp_bytes[];
+    using V = Raw<T, VE>;
+    V *ring = reinterpret_cast<V *>(gp_bytes) + threadIdx.x;
+    float *gp_smem = reinterpret_cast<float *>(gp_bytes + kGpRing<V>);
     dev::grid_launch_dependents();
     const GpPlace t = gp_place<VE, false>(a);
     const int channels = t.width * VE;
@@ -308,22 +363,22 @@ __global__ void __launch_bounds__(kGpThreads, kGpGradCtas) k_gp_sums(const GnArg
     if (t.on) {
         Channel<VE> k;
         gp_channel<VE>(t, gp_smem, k);
-        gp_walk<kGpGrad>(
+        gp_stream<kGpAhead>(
             t,
-            [&](unsigned px) {
-                return Two<T, VE>{*gp_at<T, VE>(a.x, a, t, px), *gp_at<T, VE>(a.dy, a, t, px)};
+            [&](int slot, unsigned px) {
+                gp_copy(ring + 2 * slot * kGpThreads, gp_at<T, VE>(a.x, a, t, px));
+                gp_copy(ring + (2 * slot + 1) * kGpThreads, gp_at<T, VE>(a.dy, a, t, px));
             },
-            [&](const auto &r, auto count, unsigned p) {
+            [&](int slot, unsigned px, auto refill) {
+                const V x = ring[2 * slot * kGpThreads], dy = ring[(2 * slot + 1) * kGpThreads];
+                refill();
+                float2 d[kPairs<VE>], dz[kPairs<VE>];
+                const unsigned long long e = gp_element(a, t, px);
+                gn_dz<T, VE, DROP, ACT>(x, dy, k, a.drop, e >> 3, e & 7, d, dz);
 #pragma unroll
-                for (int j = 0; j < decltype(count)::value; j++) {
-                    float2 d[kPairs<VE>], dz[kPairs<VE>];
-                    const unsigned long long e = gp_element(a, t, p + j * t.lanes);
-                    gn_dz<T, VE, DROP, ACT>(r[j].x, r[j].dy, k, a.drop, e >> 3, e & 7, d, dz);
-#pragma unroll
-                    for (int i = 0; i < kPairs<VE>; i++) {
-                        s1[i] = __fadd2_rn(s1[i], dz[i]);
-                        s2[i] = __ffma2_rn(dz[i], d[i], s2[i]);
-                    }
+                for (int i = 0; i < kPairs<VE>; i++) {
+                    s1[i] = __fadd2_rn(s1[i], dz[i]);
+                    s2[i] = __ffma2_rn(dz[i], d[i], s2[i]);
                 }
             });
     }
@@ -354,7 +409,11 @@ __global__ void __launch_bounds__(kGpThreads, kGpGradCtas) k_gp_sums(const GnArg
 template <class T, int VE, bool DROP, int ACT>
 __global__ void __launch_bounds__(kGpThreads, kGpGradCtas) k_gp_dx(const GnArgs a)
 {
-    extern __shared__ __align__(16) float gp_smem[];    // five constants a channel, then two sums a group
+    // vectors on their way; five constants a channel, then two sums a group
+    extern __shared__ __align__(16) uint8_t gp_bytes[];
+    using V = Raw<T, VE>;
+    V *ring = reinterpret_cast<V *>(gp_bytes) + threadIdx.x;
+    float *gp_smem = reinterpret_cast<float *>(gp_bytes + kGpRing<V>);
     dev::grid_launch_dependents();
     const GpPlace t = gp_place<VE, true>(a);
     const int channels = t.width * VE, g0 = t.first / a.Cg;
@@ -385,72 +444,79 @@ __global__ void __launch_bounds__(kGpThreads, kGpGradCtas) k_gp_dx(const GnArgs 
     gp_channel<VE>(t, gp_smem, k);
     gn_load<VE>(k0, gp_smem + 3 * channels + t.vec * VE);
     gn_load<VE>(k1, gp_smem + 4 * channels + t.vec * VE);
-    gp_walk<kGpGrad>(
+    gp_stream<kGpAhead>(
         t,
-        [&](unsigned px) {
-            return Two<T, VE>{__ldcs(gp_at<T, VE>(a.x, a, t, px)), __ldcs(gp_at<T, VE>(a.dy, a, t, px))};
+        [&](int slot, unsigned px) {
+            gp_copy(ring + 2 * slot * kGpThreads, gp_at<T, VE>(a.x, a, t, px));
+            gp_copy(ring + (2 * slot + 1) * kGpThreads, gp_at<T, VE>(a.dy, a, t, px));
         },
-        [&](const auto &r, auto count, unsigned p) {
+        [&](int slot, unsigned px, auto refill) {
+            const V x = ring[2 * slot * kGpThreads], dy = ring[(2 * slot + 1) * kGpThreads];
+            refill();
+            float2 d[kPairs<VE>], dz[kPairs<VE>];
+            const unsigned long long e = gp_element(a, t, px);
+            gn_dz<T, VE, DROP, ACT>(x, dy, k, a.drop, e >> 3, e & 7, d, dz);
 #pragma unroll
-            for (int j = 0; j < decltype(count)::value; j++) {
-                const unsigned px = p + j * t.lanes;
-                float2 d[kPairs<VE>], dz[kPairs<VE>];
-                const unsigned long long e = gp_element(a, t, px);
-                gn_dz<T, VE, DROP, ACT>(r[j].x, r[j].dy, k, a.drop, e >> 3, e & 7, d, dz);
-#pragma unroll
-                for (int i = 0; i < kPairs<VE>; i++) {
-                    if (DROP) dz[i] = __fmul2_rn(dz[i], both(a.drop.scale));
-                    dz[i] = __ffma2_rn(d[i], k1[i], __ffma2_rn(dz[i], k.a[i], k0[i]));
-                }
-                __stcs(const_cast<Raw<T, VE> *>(gp_at<T, VE>(a.y, a, t, px)), pack2<T, VE>(dz));
+            for (int i = 0; i < kPairs<VE>; i++) {
+                if (DROP) dz[i] = __fmul2_rn(dz[i], both(a.drop.scale));
+                dz[i] = __ffma2_rn(d[i], k1[i], __ffma2_rn(dz[i], k.a[i], k0[i]));
             }
+            __stcs(const_cast<V *>(gp_at<T, VE>(a.y, a, t, px)), pack2<T, VE>(dz));
         });
 }
 
 // The chunks' shares joined, kJoinWide channels a block, the chunks over its
-// threads: forward, sets of unlike counts and means; gradient, sums.
-constexpr int kJoinThreads = 1024, kJoinWide = 16, kJoinRows = kJoinThreads / kJoinWide;
+// threads, each of which asks for all of its own at once: forward, sets of
+// unlike counts and means; gradient, sums.  A thread takes about four chunks
+// where the largest block allows it (blocks of 64 rows whatever the chunks: 16
+// x 64 x 64 x 320 forward 35 us against 30).
+constexpr int kJoinThreads = 1024, kJoinWide = 16, kJoinFew = 4;
+constexpr int kJoinEach = (kGnMaxChunks * kJoinWide + kJoinThreads - 1) / kJoinThreads;
 
 template <bool GRAD>
 __global__ void __launch_bounds__(kJoinThreads) k_gp_join(const GnArgs a)
 {
-    __shared__ float2 sh[kJoinRows][kJoinWide + 1];
+    __shared__ float2 sh[2][kJoinThreads / 32][kJoinWide];
     dev::grid_launch_dependents();
-    dev::grid_dependency_wait();
-    const int lane = threadIdx.x % kJoinWide, row = threadIdx.x / kJoinWide;
+    const int lane = threadIdx.x % kJoinWide, row = threadIdx.x / kJoinWide, rows = blockDim.x / kJoinWide;
     const int c = blockIdx.x * kJoinWide + lane;
     const float2 *part = gp_part(a, blockIdx.y, 0) + c;
-    const auto pixels = [&](int k) { return static_cast<float>(min(a.chunk_px, a.HW - k * a.chunk_px)); };
-    const auto total = [&](float2 s) {
+    // over the warp's two rows, then over the warps
+    const auto total = [&](float2 s, int z) {
+        s.x += __shfl_xor_sync(0xffffffffu, s.x, kJoinWide);
+        s.y += __shfl_xor_sync(0xffffffffu, s.y, kJoinWide);
+        if ((row & 1) == 0) sh[z][row / 2][lane] = s;
         __syncthreads();
-        sh[row][lane] = s;
-        for (int h = kJoinRows / 2; h; h /= 2) {
-            __syncthreads();
-            if (row < h) sh[row][lane] = __fadd2_rn(sh[row][lane], sh[row + h][lane]);
-        }
-        __syncthreads();
-        return sh[0][lane];
+        s = sh[z][0][lane];
+#pragma unroll 8
+        for (int w = 1; w < rows / 2; w++) s = __fadd2_rn(s, sh[z][w][lane]);
+        return s;
     };
-    float2 s = make_float2(0.0f, 0.0f);
-    if (c < a.C) {
-#pragma unroll 4
-        for (int k = row; k < a.chunks; k += kJoinRows) {
-            const float2 v = part[static_cast<long long>(k) * a.C];
-            s = GRAD ? __fadd2_rn(s, v) : make_float2(fmaf(v.x, pixels(k), s.x), 0.0f);
-        }
+    dev::grid_dependency_wait();
+    float2 v[kJoinEach];
+#pragma unroll
+    for (int k = 0; k < kJoinEach; k++) {
+        const int chunk = row + k * rows;
+        v[k] = c < a.C && chunk < a.chunks ? part[static_cast<long long>(chunk) * a.C] : make_float2(0.0f, 0.0f);
     }
-    s = total(s);
-    if (!GRAD) {
-        const float mean = s.x / a.HW;
-        s = make_float2(0.0f, 0.0f);
-        if (c < a.C) {
-#pragma unroll 4
-            for (int k = row; k < a.chunks; k += kJoinRows) {
-                const float2 v = part[static_cast<long long>(k) * a.C];
-                s.y += fmaf((v.x - mean) * (v.x - mean), pixels(k), v.y);
-            }
+    float2 s = make_float2(0.0f, 0.0f);
+    if (GRAD) {
+#pragma unroll
+        for (int k = 0; k < kJoinEach; k++) s = __fadd2_rn(s, v[k]);
+        s = total(s, 0);
+    } else {
+        float px[kJoinEach];    // the chunks' pixels; 0 past the last
+#pragma unroll
+        for (int k = 0; k < kJoinEach; k++) {
+            const int chunk = row + k * rows;
+            px[k] = chunk < a.chunks ? static_cast<float>(min(a.chunk_px, a.HW - chunk * a.chunk_px)) : 0.0f;
+            s.x = fmaf(v[k].x, px[k], s.x);
         }
-        s = make_float2(mean, total(s).y);
+        const float mean = total(s, 0).x / a.HW;
+        s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kJoinEach; k++) s.y += fmaf((v[k].x - mean) * (v[k].x - mean), px[k], v[k].y);
+        s = make_float2(mean, total(s, 1).y);
     }
     if (row == 0 && c < a.C) a.chan[static_cast<long long>(blockIdx.y) * a.C + c] = s;
 }
@@ -470,7 +536,13 @@ inline dim3 gp_grid(const GnArgs &a, int ve)
     return dim3(a.chunks, (a.C / ve + kGpThreads - 1) / kGpThreads, a.N);
 }
 
-inline dim3 gp_join_grid(const GnArgs &a) { return dim3((a.C + kJoinWide - 1) / kJoinWide, a.N); }
+template <bool GRAD>
+cudaError_t gp_join(const GnArgs &a, void *stream)
+{
+    static_assert(kJoinEach >= kJoinFew, "");
+    const int warps = std::min((a.chunks + 2 * kJoinFew - 1) / (2 * kJoinFew), kJoinThreads / 32);
+    return launch(k_gp_join<GRAD>, dim3((a.C + kJoinWide - 1) / kJoinWide, a.N), 32 * warps, 0, stream, a);
+}
 
 // Floats of shared memory: `each` a channel and two a group, or one for each
 // thread's elements where that is more.
@@ -496,7 +568,7 @@ cudaError_t gn_passes_forward(const GnArgs &a, int ve, bool drop, void *stream)
         const dim3 grid = gp_grid(a, VE);
         cudaError_t e = launch(k_gp_stats<T, VE>, grid, kGpThreads, 0, stream, a);
         if (e == cudaSuccess)
-            e = launch(k_gp_join<false>, gp_join_grid(a), kJoinThreads, 0, stream, a);
+            e = gp_join<false>(a, stream);
         if (e != cudaSuccess) return e;
         return gn_kinds(a.act, drop, [&](auto dr, auto act) {
             return gp_launch(k_gp_apply<T, VE, decltype(dr)::value, decltype(act)::value>, grid, gp_shared(a, VE, 3),
@@ -514,10 +586,11 @@ cudaError_t gn_passes_backward(const GnArgs &a, int ve, bool drop, void *stream)
         return gn_kinds(a.act, drop, [&](auto dr, auto act) {
             constexpr bool D = decltype(dr)::value;
             constexpr int A = decltype(act)::value;
-            cudaError_t e = gp_launch(k_gp_sums<T, VE, D, A>, grid, gp_shared(a, VE, 3), stream, a);
+            constexpr size_t ring = kGpRing<Raw<T, VE>>;
+            cudaError_t e = gp_launch(k_gp_sums<T, VE, D, A>, grid, ring + gp_shared(a, VE, 3), stream, a);
             if (e == cudaSuccess)
-                e = launch(k_gp_join<true>, gp_join_grid(a), kJoinThreads, 0, stream, a);
-            return e != cudaSuccess ? e : gp_launch(k_gp_dx<T, VE, D, A>, grid, gp_shared(a, VE, 5), stream, a);
+                e = gp_join<true>(a, stream);
+            return e != cudaSuccess ? e : gp_launch(k_gp_dx<T, VE, D, A>, grid, ring + gp_shared(a, VE, 5), stream, a);
         });
     });
 }

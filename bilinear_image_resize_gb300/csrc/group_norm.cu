@@ -55,14 +55,16 @@ __global__ void __launch_bounds__(256) k_gn_params(const GnArgs a)
 
 constexpr int kGnBlock = 256;   // threads of a pass kernel's CTA
 
-// Chunks of an image for the pass kernels: about four CTAs an SM over the
-// call, and at least sixteen pixels a thread.
-void gn_passes_plan(GnArgs &a, int ve)
+// Chunks of an image for the pass kernels: as many CTAs over the call as are
+// resident at once (four an SM forward, three in the gradient; two waves of the
+// gradient's measured 66 against 64 us on 16 x 64 x 64 x 320 bf16, 36 against
+// 32 on 1 x 256 x 256 x 128), and at least eight pixels a thread.
+void gn_passes_plan(GnArgs &a, int ve, bool grad)
 {
     const long long vecs = a.C / ve, blocks = (vecs + kGnBlock - 1) / kGnBlock;
     const long long lanes = kGnBlock / std::min<long long>(vecs, kGnBlock);
-    const long long want = std::max(1LL, 4LL * kGnSms / (blocks * a.N));
-    const long long chunks = std::clamp(a.HW / (16 * lanes), 1LL, want);
+    const long long want = std::max(1LL, (grad ? 3 : 4) * kGnSms / (blocks * a.N));
+    const long long chunks = std::clamp(a.HW / (8 * lanes), 1LL, std::min<long long>(want, kGnMaxChunks));
     a.chunk_px = static_cast<unsigned>((a.HW + chunks - 1) / chunks);
     a.chunks = static_cast<int>((a.HW + a.chunk_px - 1) / a.chunk_px);
 }
@@ -182,10 +184,11 @@ int map_group_norm_workspace(const rz_norm *d, size_t *bytes)
     gn_fill(d, s, a);
     // enough for every vector width, which the maps' alignment decides
     for (int ve : {8, 4, 1})
-        if (a.C % ve == 0) {
-            gn_passes_plan(a, ve);
-            *bytes = std::max(*bytes, gn_workspace(a).total);
-        }
+        for (bool grad : {false, true})
+            if (a.C % ve == 0) {
+                gn_passes_plan(a, ve, grad);
+                *bytes = std::max(*bytes, gn_workspace(a).total);
+            }
     return RZ_OK;
 }
 
@@ -205,7 +208,7 @@ int map_group_norm(const rz_norm *d, const rz_drop *drop, const rz_map *x, const
     a.y = maps::view(y);
     a.joined = maps::rows_joined(*x, s) && maps::rows_joined(*y, s);
     const int ve = gn_vector(s, x, y, nullptr);
-    gn_passes_plan(a, ve);
+    gn_passes_plan(a, ve, false);
     const GnWorkspace w = gn_workspace(a);
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < w.total) return RZ_ERR_ARG;
     uint8_t *base = static_cast<uint8_t *>(workspace);
@@ -255,7 +258,7 @@ int map_group_norm_grad(const rz_norm *d, const rz_drop *drop, const rz_map *dy,
     a.y = maps::view(dx);
     a.joined = maps::rows_joined(*x, s) && maps::rows_joined(*dy, s) && maps::rows_joined(*dx, s);
     const int ve = gn_vector(s, x, dx, dy);
-    gn_passes_plan(a, ve);
+    gn_passes_plan(a, ve, true);
     a.rows = a.N;
     const GnWorkspace w = gn_workspace(a);
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < w.total) return RZ_ERR_ARG;
