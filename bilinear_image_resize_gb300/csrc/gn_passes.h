@@ -481,15 +481,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_gp_join(const GnArgs a)
     const int lane = threadIdx.x % kJoinWide, row = threadIdx.x / kJoinWide, rows = blockDim.x / kJoinWide;
     const int c = blockIdx.x * kJoinWide + lane;
     const float2 *part = gp_part(a, blockIdx.y, 0) + c;
-    // over the warp's two rows, then over the warps
+    // over the warp's two rows, then over the warps, every other one a row
     const auto total = [&](float2 s, int z) {
         s.x += __shfl_xor_sync(0xffffffffu, s.x, kJoinWide);
         s.y += __shfl_xor_sync(0xffffffffu, s.y, kJoinWide);
         if ((row & 1) == 0) sh[z][row / 2][lane] = s;
         __syncthreads();
-        s = sh[z][0][lane];
-#pragma unroll 8
-        for (int w = 1; w < rows / 2; w++) s = __fadd2_rn(s, sh[z][w][lane]);
+        s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kJoinThreads / 64; k++) {
+            const int w = 2 * k + (row & 1);
+            if (w < rows / 2) s = __fadd2_rn(s, sh[z][w][lane]);
+        }
+        s.x += __shfl_xor_sync(0xffffffffu, s.x, kJoinWide);
+        s.y += __shfl_xor_sync(0xffffffffu, s.y, kJoinWide);
         return s;
     };
     dev::grid_dependency_wait();
