@@ -106,7 +106,7 @@ __device__ __forceinline__ int gc_count(const GnArgs &a, unsigned per_cta, int r
 
 __device__ __forceinline__ void copy16(void *to, const void *from)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dev::smem_addr(to)), "l"(from) : "memory");
+    copy_async(static_cast<uint4 *>(to), static_cast<const uint4 *>(from));
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kGcThreads, kGcCtas) k_gc_backward(const GnArg
 
 cudaError_t gc_launch(void (*fn)(GnArgs), const GnArgs &a, int smem, void *stream)
 {
-    const cudaError_t e = gn_shared(reinterpret_cast<const void *>(fn));
+    const cudaError_t e = shared_opt_in(reinterpret_cast<const void *>(fn));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.cl) * a.clusters, 1, 1);
@@ -534,12 +534,12 @@ cudaError_t gc_resident(int *clusters)
     int (&row)[kGnMaxCluster + 1] = known[dev & 63];
     if (!row[1]) {
         const auto fn = k_gc_forward<__nv_bfloat16, 8, true, RZ_ACT_SILU>;
-        e = gn_shared(reinterpret_cast<const void *>(fn));
+        e = shared_opt_in(reinterpret_cast<const void *>(fn));
         for (int cl = kGnMaxCluster; cl >= 1 && e == cudaSuccess; cl--) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(cl, 1, 1);
             cfg.blockDim = dim3(kGcThreads, 1, 1);
-            cfg.dynamicSmemBytes = kGnShared;
+            cfg.dynamicSmemBytes = kMapShared;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim = {static_cast<unsigned>(cl), 1, 1};
@@ -586,7 +586,7 @@ cudaError_t gn_cluster_plan(GnArgs &args, size_t es, bool grad, bool *fits)
         a.gs = base * m;
         if (a.lv < 2 && a.gs < a.G) break;
         const int row = kGcWarps * (32 / a.lv), rows = static_cast<int>((a.HW + row - 1) / row);
-        const int fixed = gc_bytes(a, es, grad, 0), most = (kGnShared - fixed) / (gc_bytes(a, es, grad, 1) - fixed);
+        const int fixed = gc_bytes(a, es, grad, 0), most = (kMapShared - fixed) / (gc_bytes(a, es, grad, 1) - fixed);
         a.slabs = (a.G + a.gs - 1) / a.gs;
         const long long units = static_cast<long long>(a.N) * a.slabs;
         if (units > 0x7fffffffLL) continue;

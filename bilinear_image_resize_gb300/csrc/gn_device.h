@@ -40,11 +40,6 @@ struct GnArgs {
     unsigned chunk_px;
 };
 
-// Opts a kernel into kGnShared bytes of shared memory (two CTAs an SM), once a
-// device.
-constexpr int kGnShared = 112 * 1024;
-cudaError_t gn_shared(const void *fn);
-
 // Cluster kernels (gn_cluster.cu): whether an image's slab fits a cluster; sets
 // gs, lv, slabs, cl, keep, clusters and rows.
 cudaError_t gn_cluster_plan(GnArgs &a, size_t es, bool grad, bool *fits);

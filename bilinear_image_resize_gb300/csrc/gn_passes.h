@@ -115,27 +115,6 @@ __device__ __forceinline__ void gp_walk(const GpPlace &t, Load load, Use use)
     }
 }
 
-// Copies a vector to the thread's own place in shared memory, asynchronously
-// where it is wide enough.
-template <class V>
-__device__ __forceinline__ void gp_copy(V *to, const V *from)
-{
-    if constexpr (sizeof(V) == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dev::smem_addr(to)), "l"(from) : "memory");
-    else if constexpr (sizeof(V) >= 4)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dev::smem_addr(to)), "l"(from),
-                     "n"(sizeof(V))
-                     : "memory");
-    else
-        *to = *from;
-}
-__device__ __forceinline__ void gp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void gp_arrived()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Walks the thread's pixels with kGpAhead of them on their way into shared
 // memory: copy(slot, pixel), then use(slot, pixel, refill), which calls
 // refill() once it has read the slot.
@@ -146,14 +125,14 @@ __device__ __forceinline__ void gp_stream(const GpPlace &t, Copy copy, Use use)
 #pragma unroll
     for (int s = 0; s < AHEAD; s++, next += t.lanes) {
         if (next < t.p1) copy(s, next);
-        gp_commit();
+        copies_commit();
     }
     int slot = 0;
     for (unsigned p = t.p0 + t.lane; p < t.p1; p += t.lanes) {
-        gp_arrived<AHEAD - 1>();
+        copies_left<AHEAD - 1>();
         use(slot, p, [&] {
             if (next < t.p1) copy(slot, next);
-            gp_commit();
+            copies_commit();
         });
         next += t.lanes;
         slot = slot + 1 == AHEAD ? 0 : slot + 1;
@@ -366,8 +345,8 @@ __global__ void __launch_bounds__(kGpThreads, kGpGradCtas) k_gp_sums(const GnArg
         gp_stream<kGpAhead>(
             t,
             [&](int slot, unsigned px) {
-                gp_copy(ring + 2 * slot * kGpThreads, gp_at<T, VE>(a.x, a, t, px));
-                gp_copy(ring + (2 * slot + 1) * kGpThreads, gp_at<T, VE>(a.dy, a, t, px));
+                copy_async(ring + 2 * slot * kGpThreads, gp_at<T, VE>(a.x, a, t, px));
+                copy_async(ring + (2 * slot + 1) * kGpThreads, gp_at<T, VE>(a.dy, a, t, px));
             },
             [&](int slot, unsigned px, auto refill) {
                 const V x = ring[2 * slot * kGpThreads], dy = ring[(2 * slot + 1) * kGpThreads];
@@ -447,8 +426,8 @@ __global__ void __launch_bounds__(kGpThreads, kGpGradCtas) k_gp_dx(const GnArgs 
     gp_stream<kGpAhead>(
         t,
         [&](int slot, unsigned px) {
-            gp_copy(ring + 2 * slot * kGpThreads, gp_at<T, VE>(a.x, a, t, px));
-            gp_copy(ring + (2 * slot + 1) * kGpThreads, gp_at<T, VE>(a.dy, a, t, px));
+            copy_async(ring + 2 * slot * kGpThreads, gp_at<T, VE>(a.x, a, t, px));
+            copy_async(ring + (2 * slot + 1) * kGpThreads, gp_at<T, VE>(a.dy, a, t, px));
         },
         [&](int slot, unsigned px, auto refill) {
             const V x = ring[2 * slot * kGpThreads], dy = ring[(2 * slot + 1) * kGpThreads];
@@ -559,7 +538,7 @@ inline size_t gp_shared(const GnArgs &a, int ve, int each)
 
 inline cudaError_t gp_launch(void (*fn)(GnArgs), dim3 grid, size_t smem, void *stream, const GnArgs &a)
 {
-    const cudaError_t e = gn_shared(reinterpret_cast<const void *>(fn));
+    const cudaError_t e = shared_opt_in(reinterpret_cast<const void *>(fn));
     return e != cudaSuccess ? e : launch(fn, grid, kGpThreads, smem, stream, a);
 }
 

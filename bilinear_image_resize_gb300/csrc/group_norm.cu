@@ -146,7 +146,7 @@ int gn_status(cudaError_t e)
 
 namespace rz {
 
-cudaError_t gn_shared(const void *fn)
+cudaError_t maps::shared_opt_in(const void *fn)
 {
     static std::mutex mu;
     static std::vector<std::pair<int, const void *>> ready;
@@ -156,7 +156,7 @@ cudaError_t gn_shared(const void *fn)
     std::lock_guard<std::mutex> lock(mu);
     for (const auto &r : ready)
         if (r.first == dev && r.second == fn) return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGnShared);
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, maps::kMapShared);
     if (e != cudaSuccess) return e;
     try {
         ready.emplace_back(dev, fn);

@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "gbresize.h"
+#include "rz_device.h"
 
 namespace rz {
 namespace maps {
@@ -95,6 +96,11 @@ inline cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, size_t smem,
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
 }
+
+// Opts a kernel into kMapShared bytes of shared memory (two CTAs an SM), once a
+// device (group_norm.cu).
+constexpr int kMapShared = 112 * 1024;
+cudaError_t shared_opt_in(const void *fn);
 
 // ---------------------------------------------------------------- device side
 
@@ -208,6 +214,28 @@ __device__ __forceinline__ Raw<T, VE> pack2(const float2 (&f)[kPairs<VE>])
         s[2 * i + 1] = f[i].y;
     }
     return pack<T, VE>(reinterpret_cast<float(&)[VE]>(s));
+}
+
+// Copies a vector to a place in shared memory that only this thread reads:
+// asynchronously, in the thread's open group of copies, where it is wide enough.
+template <class V>
+__device__ __forceinline__ void copy_async(V *to, const V *from)
+{
+    if constexpr (sizeof(V) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dev::smem_addr(to)), "l"(from) : "memory");
+    else if constexpr (sizeof(V) >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dev::smem_addr(to)), "l"(from),
+                     "n"(sizeof(V))
+                     : "memory");
+    else
+        *to = *from;
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until all but the last N groups have arrived.
+template <int N>
+__device__ __forceinline__ void copies_left()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }

@@ -24,10 +24,19 @@ constexpr int kMapThreads = 256;
 constexpr int kMapRun = 16;     // rows a thread walks, at most
 constexpr int kMapImages = 4;   // images whose base a thread reads at a time
 
+// Gradient: the CTAs an SM that its registers and shared memory are held to
+// (16-bit 2x as above: 64 us with three, 75 with four), the output rows whose
+// readers a thread has on their way in shared memory, and the rows that it
+// walks at most.
+template <class T, int READERS> constexpr int kGradCtas = sizeof(T) == 4 && READERS < 8 ? 4 : 3;
+template <class T, int READERS> constexpr int kGradAhead = (kGradCtas<T, READERS> == 4 ? 12 : 16) / READERS;
+constexpr int kGradRun = 32;
+
 struct ResampleArgs {
     View src, base, dst;        // gradient: dst is ddst, src is dsrc; base.p null: none
     int N, src_n, H, W, OH, OW, C;
     int run;                    // rows a thread walks
+    int ahead;                  // gradient: 1 or kGradAhead output rows on their way
     float *sum;                 // gradient of a table: [OH][OW][C], ddst summed over the images
 };
 
@@ -202,19 +211,21 @@ __global__ void __launch_bounds__(kMapThreads) k_sum_images(const ResampleArgs a
 // of them held in registers, formed once; more only beyond a ratio of
 // READERS / 2, weighed as they come), and the sum goes to the two source rows
 // that the output row lies between, so that each output row is read once per
-// run and not once for each source row.
-// Output rows whose readers a thread loads before it uses the first: more in
-// flight for 16-bit maps, fewer registers for the short launches of a float32
-// table's sum (upsample 2x, 8 x 128 x 128 x 256 f16: 88 us with four, 101 with
-// two; a 24 x 24 x 1024 table: 18 us with two, 23 with four).
-template <class T> constexpr int kGradRows = sizeof(T) == 2 ? 4 : 2;
-
+// run and not once for each source row.  The readers come through shared
+// memory, some rows ahead, in places of the thread's own: held in registers
+// they left two CTAs an SM, and the launch waited on its loads.
+// 2x, 8 x 128 x 128 x 256 f16: 64 us, 5.3 TB/s (89 us from registers); float32
+// 104 us, 6.5 TB/s; 16 images' 37 x 50 x 1024 to a table of 24 x 24: 15.5 us
+// with the sum before it.
 template <class S, class T, int VE, int READERS>
-__global__ void __launch_bounds__(kMapThreads) k_resize_map_grad(const ResampleArgs a)
+__global__ void __launch_bounds__(kMapThreads, kGradCtas<T, READERS>) k_resize_map_grad(const ResampleArgs a)
 {
-    constexpr int kRows = kGradRows<T>;
+    using V = Raw<T, VE>;
+    constexpr int kRows = kGradAhead<T, READERS>;
     constexpr int kTaps = 32;
+    extern __shared__ __align__(16) uint8_t grad_smem[];
     __shared__ Tap taps[kTaps];
+    V *ring = reinterpret_cast<V *>(grad_smem) + threadIdx.x;
     dev::grid_launch_dependents();
     const unsigned vecs = a.C / VE;
     const unsigned i = blockIdx.x * kMapThreads + threadIdx.x;
@@ -222,87 +233,90 @@ __global__ void __launch_bounds__(kMapThreads) k_resize_map_grad(const ResampleA
     const int x = on ? static_cast<int>(i / vecs) : 0, c = on ? static_cast<int>(i - x * vecs) * VE : 0;
     const int2 rx = readers(x, a.W, a.OW);
     const int count = on ? rx.y - rx.x : 0;
-    // loads past the last reader repeat it
+    const int vec_bytes = a.C * static_cast<int>(sizeof(T));    // from one reader to the next
     float wx[READERS];
-    int off[READERS];
 #pragma unroll
-    for (int k = 0; k < READERS; k++) {
-        wx[k] = k < count ? tap_weight(rx.x + k, x, a.W, a.OW) : 0.0f;
-        off[k] = max(min(k, count - 1), 0) * a.C * static_cast<int>(sizeof(T));
-    }
+    for (int k = 0; k < READERS; k++) wx[k] = k < count ? tap_weight(rx.x + k, x, a.W, a.OW) : 0.0f;
     const int y0 = blockIdx.y * a.run, y1 = min(y0 + a.run, a.H), n = blockIdx.z;
     const int lo = readers(y0, a.H, a.OH).x, hi = readers(y1 - 1, a.H, a.OH).y;
     const uint8_t *row = reinterpret_cast<const uint8_t *>(map_at<T, VE>(a.dst, n, lo, rx.x, a.C, c));
     uint8_t *out = reinterpret_cast<uint8_t *>(const_cast<Raw<S, VE> *>(map_at<S, VE>(a.src, n, y0, x, a.C, c)));
     dev::grid_dependency_wait();
-    float cur[VE], next[VE];   // source rows y and y + 1
+    constexpr int P = kPairs<VE>;
+    float2 cur[P], next[P];     // source rows y and y + 1
     int y = y0 - 1;
 #pragma unroll
-    for (int k = 0; k < VE; k++) cur[k] = next[k] = 0.0f;
+    for (int k = 0; k < P; k++) cur[k] = next[k] = both(0.0f);
     const auto flush = [&] {
         if (y >= y0) {
-            if (on) *reinterpret_cast<Raw<S, VE> *>(out) = pack<S, VE>(cur);
+            if (on) *reinterpret_cast<Raw<S, VE> *>(out) = pack2<S, VE>(cur);
             out += a.src.pitch;
         }
         y++;
 #pragma unroll
-        for (int k = 0; k < VE; k++) {
+        for (int k = 0; k < P; k++) {
             cur[k] = next[k];
-            next[k] = 0.0f;
+            next[k] = both(0.0f);
         }
     };
+    // the next row's readers, copied to the thread's places in ring slot `slot`
+    const uint8_t *ahead = row;
+    const auto copy = [&](int slot) {
+#pragma unroll
+        for (int q = 0; q < READERS; q++)
+            if (q < count)
+                copy_async(ring + (slot * READERS + q) * kMapThreads, reinterpret_cast<const V *>(ahead + q * vec_bytes));
+        ahead += a.dst.pitch;
+    };
+#pragma unroll
+    for (int m = 0; m < kRows; m++) {
+        if (m < a.ahead && lo + m < hi) copy(m);
+        copies_commit();
+    }
+    int slot = 0;
     for (int base = lo; base < hi; base += kTaps) {
         const int some = min(kTaps, hi - base);
         __syncthreads();
         if (threadIdx.x < some) taps[threadIdx.x] = tap(base + threadIdx.x, a.H, a.OH);
         __syncthreads();
-        for (int j = 0; j < some; j += kRows) {
-            Raw<T, VE> r[kRows][READERS];
-            if (count > 0) {
+        for (int j = 0; j < some; j++) {
+            float2 h[P];
 #pragma unroll
-                for (int m = 0; m < kRows; m++)
-                    if (j + m < some) {
+            for (int k = 0; k < P; k++) h[k] = both(0.0f);
+            const auto read = [&](const V &v, float w) {
+                float2 f[P];
+                unpack2<T, VE>(v, f);
 #pragma unroll
-                        for (int q = 0; q < READERS; q++)
-                            r[m][q] = *reinterpret_cast<const Raw<T, VE> *>(row + m * a.dst.pitch + off[q]);
-                    }
+                for (int k = 0; k < P; k++) h[k] = __ffma2_rn(both(w), f[k], h[k]);
+            };
+            if (a.ahead == 1)
+                copies_left<0>();
+            else
+                copies_left<kRows - 1>();
+#pragma unroll
+            for (int q = 0; q < READERS; q++) {
+                if (q >= count) break;
+                read(ring[(slot * READERS + q) * kMapThreads], wx[q]);
             }
+            if (base + j + a.ahead < hi) copy(slot);
+            copies_commit();
+            slot = slot + 1 == a.ahead ? 0 : slot + 1;
+            for (int q = READERS; q < count; q++)
+                read(*reinterpret_cast<const V *>(row + static_cast<long long>(q) * vec_bytes),
+                     tap_weight(rx.x + q, x, a.W, a.OW));
+            row += a.dst.pitch;
+            const Tap t = taps[j];
+            while (t.a > y && y < y1) flush();
+            // the near row may lie before the run and the far one after it: both are then left to other blocks
+            const float w = t.b == t.a ? 1.0f : 1.0f - t.u;
+            if (t.a == y) {
 #pragma unroll
-            for (int m = 0; m < kRows; m++)
-                if (j + m < some) {
-                    float h[VE];
+                for (int k = 0; k < P; k++) cur[k] = __ffma2_rn(both(w), h[k], cur[k]);
+            }
+            if (t.b == y + 1) {
 #pragma unroll
-                    for (int k = 0; k < VE; k++) h[k] = 0.0f;
-#pragma unroll
-                    for (int q = 0; q < READERS; q++) {
-                        if (q >= count) break;
-                        float f[VE];
-                        unpack<T, VE>(r[m][q], f);
-#pragma unroll
-                        for (int k = 0; k < VE; k++) h[k] = fmaf(wx[q], f[k], h[k]);
-                    }
-                    const Raw<T, VE> *more = reinterpret_cast<const Raw<T, VE> *>(row + m * a.dst.pitch);
-                    for (int q = READERS; q < count; q++) {
-                        const float w = tap_weight(rx.x + q, x, a.W, a.OW);
-                        float f[VE];
-                        unpack<T, VE>(more[static_cast<long long>(q) * vecs], f);
-#pragma unroll
-                        for (int k = 0; k < VE; k++) h[k] = fmaf(w, f[k], h[k]);
-                    }
-                    const Tap t = taps[j + m];
-                    while (t.a > y && y < y1) flush();
-                    // the near row may lie before the run and the far one after it: both are then left to other blocks
-                    const float w = t.b == t.a ? 1.0f : 1.0f - t.u;
-                    if (t.a == y) {
-#pragma unroll
-                        for (int k = 0; k < VE; k++) cur[k] = fmaf(w, h[k], cur[k]);
-                    }
-                    if (t.b == y + 1) {
-#pragma unroll
-                        for (int k = 0; k < VE; k++) next[k] = fmaf(t.u, h[k], next[k]);
-                    }
-                }
-            row += kRows * a.dst.pitch;
+                for (int k = 0; k < P; k++) next[k] = __ffma2_rn(both(t.u), h[k], next[k]);
+            }
         }
     }
     while (y < y1) flush();
@@ -384,14 +398,47 @@ cudaError_t resample_dispatch(const rz_resample *d, int ve, Fn fn)
     return d->src_dtype == RZ_F32 ? width(float{}, __half{}) : width(__half{}, __half{});
 }
 
+// Rows a thread of the gradient walks: the fewest row times, of the waves of
+// CTAs and what each reads, one source row's readers beyond its run and the
+// set-up, which takes about as long as kGradSetup rows (16-bit 2x as above: 64
+// us with eight rows, 68 with sixteen, whose last wave is half empty).
+constexpr int kGradSetup = 3;
+dim3 grad_grid(int W, int vecs, int rows, int images, int slots, int *run)
+{
+    const long long columns = (static_cast<long long>(W) * vecs + kMapThreads - 1) / kMapThreads;
+    long long best = 0;
+    for (int r = kGradRun; r >= 1; r /= 2) {
+        const long long ctas = columns * images * ((rows + r - 1) / r);
+        const long long cost = (ctas + slots - 1) / slots * (r + 1 + kGradSetup);
+        if (best && cost >= best) continue;
+        best = cost;
+        *run = r;
+    }
+    return dim3(static_cast<unsigned>(columns), static_cast<unsigned>((rows + *run - 1) / *run),
+                static_cast<unsigned>(images));
+}
+
 // Readers of a source column: two where the map shrinks, then about two a
-// unit of the ratio (ends and roundings add one).
-template <class S, class T, int V>
+// unit of the ratio (ends and roundings add one).  Fewer places make room for
+// more CTAs (8 x 64 x 64 x 256 float32 to 150 x 150: 36 us with six, 44 with
+// eight).
+template <class S, class T, int V, int READERS>
 cudaError_t grad_launch(ResampleArgs a, void *stream)
 {
-    const dim3 grid = map_grid(a.W, a.C / V, a.H, a.src_n, &a.run);
-    const auto fn = a.OW <= 2 * a.W ? k_resize_map_grad<S, T, V, 4> : k_resize_map_grad<S, T, V, 8>;
-    return launch(fn, grid, kMapThreads, 0, stream, a);
+    const auto fn = k_resize_map_grad<S, T, V, READERS>;
+    const dim3 grid = grad_grid(a.W, a.C / V, a.H, a.src_n, kGradCtas<T, READERS> * 152, &a.run);
+    // the few output rows of one source row: one ahead is as good, and the less shared memory a launch takes, the more
+    // of it starts under the one before (16 images' 37 x 50 x 1024 to a table of 24 x 24: 15.7 us, 19.3 with two)
+    a.ahead = a.run == 1 ? 1 : kGradAhead<T, READERS>;
+    const cudaError_t e = shared_opt_in(reinterpret_cast<const void *>(fn));
+    if (e != cudaSuccess) return e;
+    return launch(fn, grid, kMapThreads, sizeof(Raw<T, V>) * kMapThreads * READERS * a.ahead, stream, a);
+}
+template <class S, class T, int V>
+cudaError_t grad_launch(const ResampleArgs &a, void *stream)
+{
+    if (a.OW <= 2LL * a.W) return grad_launch<S, T, V, 4>(a, stream);
+    return 2LL * a.OW <= 5LL * a.W ? grad_launch<S, T, V, 6>(a, stream) : grad_launch<S, T, V, 8>(a, stream);
 }
 
 int resample_status(cudaError_t e)
