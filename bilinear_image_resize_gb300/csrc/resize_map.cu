@@ -22,6 +22,7 @@ using namespace maps;
 
 constexpr int kMapThreads = 256;
 constexpr int kMapRun = 16;     // rows a thread walks, at most
+constexpr int kMapCtas = 5;     // CTAs an SM
 constexpr int kMapImages = 4;   // images whose base a thread reads at a time
 
 // Gradient: the CTAs an SM that its registers and shared memory are held to
@@ -83,8 +84,13 @@ __device__ __forceinline__ const Raw<T, VE> *map_at(const View &v, long long n, 
 // pixel on its own would read four taps; the sampling positions of the rows
 // are formed once per block.  A table (TABLE) serves every image: it is
 // interpolated once and added to each image's base.
+// Instructions bound a 16-bit upscale, and writing a float32 one: 2x, 8 x 128 x
+// 128 x 256 bf16 67 us, 5.0 TB/s, float32 111 us, 6.0 TB/s (paired float32
+// instructions measured slower, 72 us, for the registers that pairs need).  A
+// table is bound by its images: 24 x 24 x 1024 added to 16 of 37 x 50 bf16 22
+// us, 5.6 TB/s (22.5 us with three CTAs an SM and no spills).
 template <class S, class T, int VE, bool TABLE>
-__global__ void __launch_bounds__(kMapThreads) k_resize_map(const ResampleArgs a)
+__global__ void __launch_bounds__(kMapThreads, TABLE ? 4 : kMapCtas) k_resize_map(const ResampleArgs a)
 {
     __shared__ Tap taps[kMapRun];
     dev::grid_launch_dependents();
@@ -178,7 +184,7 @@ __global__ void __launch_bounds__(kMapThreads) k_resize_map(const ResampleArgs a
     }
 }
 
-// sum[y][x][c] = the images' ddst added up in order.
+// sum[y][x][c] = the images' ddst added up in order: one pass, bound by DRAM.
 template <class T, int VE>
 __global__ void __launch_bounds__(kMapThreads) k_sum_images(const ResampleArgs a)
 {
@@ -357,8 +363,8 @@ void resample_fill(const rz_resample *d, ResampleArgs &a)
     a.C = d->C;
 }
 
-// Rows a thread walks: as many as leave eight CTAs an SM, for a run reads one
-// row in `run` twice, and a launch of a few CTAs is bound by their latency.
+// Rows a thread of a table's launches walks, whose time goes with the images of
+// each row and not with the rows: as many as leave eight CTAs an SM.
 dim3 map_grid(int W, int vecs, int rows, int images, int *run)
 {
     const long long columns = (static_cast<long long>(W) * vecs + kMapThreads - 1) / kMapThreads;
@@ -381,6 +387,28 @@ int resample_vector(const rz_resample *d, const Checked &s, const rz_map *src, c
     return 1;
 }
 
+// Rows a thread walks, at most `most`: the fewest row times, of the waves of
+// CTAs (`slots` are resident) and what each takes, one row read beyond its run
+// and the set-up, which takes about as long as kSetupRows rows (gradient of 2x,
+// 8 x 128 x 128 x 256 f16: 64 us with eight rows, 68 with sixteen, whose last
+// wave is half empty; 2x of 2 x 32 x 32 x 256 bf16 3.2 us with two, 4.1 with
+// one).
+constexpr int kSetupRows = 3;
+dim3 wave_grid(int W, int vecs, int rows, int images, int slots, int most, int *run)
+{
+    const long long columns = (static_cast<long long>(W) * vecs + kMapThreads - 1) / kMapThreads;
+    long long best = 0;
+    for (int r = most; r >= 1; r /= 2) {
+        const long long ctas = columns * images * ((rows + r - 1) / r);
+        const long long cost = (ctas + slots - 1) / slots * (r + 1 + kSetupRows);
+        if (best && cost >= best) continue;
+        best = cost;
+        *run = r;
+    }
+    return dim3(static_cast<unsigned>(columns), static_cast<unsigned>((rows + *run - 1) / *run),
+                static_cast<unsigned>(images));
+}
+
 // Calls fn(S{}, T{}, VE) for the map types.
 template <class Fn>
 cudaError_t resample_dispatch(const rz_resample *d, int ve, Fn fn)
@@ -398,26 +426,6 @@ cudaError_t resample_dispatch(const rz_resample *d, int ve, Fn fn)
     return d->src_dtype == RZ_F32 ? width(float{}, __half{}) : width(__half{}, __half{});
 }
 
-// Rows a thread of the gradient walks: the fewest row times, of the waves of
-// CTAs and what each reads, one source row's readers beyond its run and the
-// set-up, which takes about as long as kGradSetup rows (16-bit 2x as above: 64
-// us with eight rows, 68 with sixteen, whose last wave is half empty).
-constexpr int kGradSetup = 3;
-dim3 grad_grid(int W, int vecs, int rows, int images, int slots, int *run)
-{
-    const long long columns = (static_cast<long long>(W) * vecs + kMapThreads - 1) / kMapThreads;
-    long long best = 0;
-    for (int r = kGradRun; r >= 1; r /= 2) {
-        const long long ctas = columns * images * ((rows + r - 1) / r);
-        const long long cost = (ctas + slots - 1) / slots * (r + 1 + kGradSetup);
-        if (best && cost >= best) continue;
-        best = cost;
-        *run = r;
-    }
-    return dim3(static_cast<unsigned>(columns), static_cast<unsigned>((rows + *run - 1) / *run),
-                static_cast<unsigned>(images));
-}
-
 // Readers of a source column: two where the map shrinks, then about two a
 // unit of the ratio (ends and roundings add one).  Fewer places make room for
 // more CTAs (8 x 64 x 64 x 256 float32 to 150 x 150: 36 us with six, 44 with
@@ -426,7 +434,7 @@ template <class S, class T, int V, int READERS>
 cudaError_t grad_launch(ResampleArgs a, void *stream)
 {
     const auto fn = k_resize_map_grad<S, T, V, READERS>;
-    const dim3 grid = grad_grid(a.W, a.C / V, a.H, a.src_n, kGradCtas<T, READERS> * 152, &a.run);
+    const dim3 grid = wave_grid(a.W, a.C / V, a.H, a.src_n, kGradCtas<T, READERS> * 152, kGradRun, &a.run);
     // the few output rows of one source row: one ahead is as good, and the less shared memory a launch takes, the more
     // of it starts under the one before (16 images' 37 x 50 x 1024 to a table of 24 x 24: 15.7 us, 19.3 with two)
     a.ahead = a.run == 1 ? 1 : kGradAhead<T, READERS>;
@@ -478,7 +486,8 @@ int resize_map(const rz_resample *d, const rz_map *src, const rz_map *base, cons
     const int ve = resample_vector(d, s, src, dst, base);
     return resample_status(resample_dispatch(d, ve, [&](auto ts, auto td, auto v) {
         constexpr int V = decltype(v)::value;
-        const dim3 grid = map_grid(a.OW, a.C / V, a.OH, a.src_n, &a.run);
+        const dim3 grid = a.N != a.src_n ? map_grid(a.OW, a.C / V, a.OH, 1, &a.run)
+                                        : wave_grid(a.OW, a.C / V, a.OH, a.src_n, kMapCtas * 152, kMapRun, &a.run);
         const auto fn = a.N == a.src_n ? k_resize_map<decltype(ts), decltype(td), V, false>
                                        : k_resize_map<decltype(ts), decltype(td), V, true>;
         return maps::launch(fn, grid, kMapThreads, 0, stream, a);
