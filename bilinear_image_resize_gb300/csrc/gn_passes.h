@@ -8,9 +8,9 @@
 //
 // The forward is bound by DRAM: 4 x 512 x 512 x 128 bf16 139 us, three
 // transfers of the map at 5.8 TB/s (142 us with SiLU; 181 with dropout, bound by
-// the generator's arithmetic).  The gradient is bound by how many instructions
-// its warps keep going: 8 x 128 x 128 x 512 bf16 115 us (five transfers, 5.8
-// TB/s), 116 with SiLU, 155 with dropout, which both passes make again.
+// the generator's arithmetic).  The gradient is bound by the instructions that
+// its warps issue: 8 x 128 x 128 x 512 bf16 120 us (five transfers, 5.6 TB/s),
+// as much with SiLU, 142 with dropout, which both passes make again.
 //
 // A thread keeps one vector of channels and walks pixels, so sums are taken by
 // channel whatever the group's width; groups are put together from channels at
@@ -36,7 +36,8 @@ constexpr int kGpStats = 4, kGpStatsCtas = 4, kGpApply = 4, kGpApplyCtas = 4;
 // The gradient, whose constants and sums fill the registers, has its loads on
 // their way in shared memory, kGpAhead pixels of x and dy a thread, and so a
 // third CTA an SM: 8 x 128 x 128 x 512 bf16 with SiLU and dropout 155 us, 171
-// with four pixels in registers and two CTAs; four CTAs spill, 183.
+// with four pixels in registers and two CTAs; four CTAs spill, 183.  Pointers
+// that step from pixel to pixel, in place of each one's offset, took it to 142.
 constexpr int kGpAhead = 3, kGpGradCtas = 3;
 template <class V> constexpr int kGpRing = 2 * kGpAhead * kGpThreads * static_cast<int>(sizeof(V));
 
@@ -115,27 +116,65 @@ __device__ __forceinline__ void gp_walk(const GpPlace &t, Load load, Use use)
     }
 }
 
-// Walks the thread's pixels with kGpAhead of them on their way into shared
-// memory: copy(slot, pixel), then use(slot, pixel, refill), which calls
-// refill() once it has read the slot.
-template <int AHEAD, class Copy, class Use>
-__device__ __forceinline__ void gp_stream(const GpPlace &t, Copy copy, Use use)
-{
-    unsigned next = t.p0 + t.lane;
-#pragma unroll
-    for (int s = 0; s < AHEAD; s++, next += t.lanes) {
-        if (next < t.p1) copy(s, next);
-        copies_commit();
+// The thread's vector in a map, pixel after pixel; `step` bytes apart where the
+// rows follow one another.
+template <class T, int VE>
+struct GpWalker {
+    const uint8_t *at;
+    __device__ __forceinline__ GpWalker(const View &v, const GnArgs &a, const GpPlace &t, unsigned px)
+        : at(reinterpret_cast<const uint8_t *>(gp_at<T, VE>(v, a, t, px)))
+    {
     }
-    int slot = 0;
-    for (unsigned p = t.p0 + t.lane; p < t.p1; p += t.lanes) {
-        copies_left<AHEAD - 1>();
-        use(slot, p, [&] {
-            if (next < t.p1) copy(slot, next);
-            copies_commit();
-        });
+    __device__ __forceinline__ void go(const View &v, const GnArgs &a, const GpPlace &t, unsigned px, unsigned step)
+    {
+        if (a.joined)
+            at += step;
+        else
+            at = reinterpret_cast<const uint8_t *>(gp_at<T, VE>(v, a, t, px));
+    }
+    __device__ __forceinline__ Raw<T, VE> *get() const
+    {
+        return const_cast<Raw<T, VE> *>(reinterpret_cast<const Raw<T, VE> *>(at));
+    }
+};
+
+// Bytes from one of the thread's pixels to the next: at most 256 threads' vectors
+// and a pixel's channels, far below 4 GB.
+template <class T>
+__device__ __forceinline__ unsigned gp_step(const GnArgs &a, const GpPlace &t)
+{
+    return t.lanes * a.C * static_cast<unsigned>(sizeof(T));
+}
+
+// Walks the thread's pixels with kGpAhead of them, x and dy, on their way into
+// the thread's places in `ring`: use(x, dy, element, pixel).
+template <class T, int VE, class Use>
+__device__ __forceinline__ void gp_stream(const GnArgs &a, const GpPlace &t, Raw<T, VE> *ring, Use use)
+{
+    using V = Raw<T, VE>;
+    const unsigned step = gp_step<T>(a, t);
+    unsigned next = t.p0 + t.lane;
+    unsigned long long e = gp_element(a, t, next);
+    GpWalker<T, VE> x(a.x, a, t, next), dy(a.dy, a, t, next);
+    const auto copy = [&](V *to) {
+        if (next < t.p1) {
+            copy_async(to, x.get());
+            copy_async(to + kGpThreads, dy.get());
+        }
+        copies_commit();
         next += t.lanes;
-        slot = slot + 1 == AHEAD ? 0 : slot + 1;
+        x.go(a.x, a, t, next, step);
+        dy.go(a.dy, a, t, next, step);
+    };
+    V *const end = ring + 2 * kGpAhead * kGpThreads;
+    for (V *to = ring; to != end; to += 2 * kGpThreads) copy(to);
+    V *at = ring;
+    for (unsigned p = t.p0 + t.lane; p < t.p1; p += t.lanes, e += t.lanes * static_cast<unsigned>(a.C)) {
+        copies_left<kGpAhead - 1>();
+        const V vx = at[0], vd = at[kGpThreads];
+        copy(at);
+        at = at + 2 * kGpThreads == end ? ring : at + 2 * kGpThreads;
+        use(vx, vd, e, p);
     }
 }
 
@@ -342,24 +381,15 @@ __global__ void __launch_bounds__(kGpThreads, kGpGradCtas) k_gp_sums(const GnArg
     if (t.on) {
         Channel<VE> k;
         gp_channel<VE>(t, gp_smem, k);
-        gp_stream<kGpAhead>(
-            t,
-            [&](int slot, unsigned px) {
-                copy_async(ring + 2 * slot * kGpThreads, gp_at<T, VE>(a.x, a, t, px));
-                copy_async(ring + (2 * slot + 1) * kGpThreads, gp_at<T, VE>(a.dy, a, t, px));
-            },
-            [&](int slot, unsigned px, auto refill) {
-                const V x = ring[2 * slot * kGpThreads], dy = ring[(2 * slot + 1) * kGpThreads];
-                refill();
-                float2 d[kPairs<VE>], dz[kPairs<VE>];
-                const unsigned long long e = gp_element(a, t, px);
-                gn_dz<T, VE, DROP, ACT>(x, dy, k, a.drop, e >> 3, e & 7, d, dz);
+        gp_stream<T, VE>(a, t, ring, [&](const V &x, const V &dy, unsigned long long e, unsigned) {
+            float2 d[kPairs<VE>], dz[kPairs<VE>];
+            gn_dz<T, VE, DROP, ACT>(x, dy, k, a.drop, e >> 3, e & 7, d, dz);
 #pragma unroll
-                for (int i = 0; i < kPairs<VE>; i++) {
-                    s1[i] = __fadd2_rn(s1[i], dz[i]);
-                    s2[i] = __ffma2_rn(dz[i], d[i], s2[i]);
-                }
-            });
+            for (int i = 0; i < kPairs<VE>; i++) {
+                s1[i] = __fadd2_rn(s1[i], dz[i]);
+                s2[i] = __ffma2_rn(dz[i], d[i], s2[i]);
+            }
+        });
     }
     float2 *out = gp_part(a, blockIdx.z, blockIdx.x) + blockIdx.y * kGpThreads * VE;
     float u[VE];    // this thread's channels' sums of dz
@@ -423,25 +453,19 @@ __global__ void __launch_bounds__(kGpThreads, kGpGradCtas) k_gp_dx(const GnArgs 
     gp_channel<VE>(t, gp_smem, k);
     gn_load<VE>(k0, gp_smem + 3 * channels + t.vec * VE);
     gn_load<VE>(k1, gp_smem + 4 * channels + t.vec * VE);
-    gp_stream<kGpAhead>(
-        t,
-        [&](int slot, unsigned px) {
-            copy_async(ring + 2 * slot * kGpThreads, gp_at<T, VE>(a.x, a, t, px));
-            copy_async(ring + (2 * slot + 1) * kGpThreads, gp_at<T, VE>(a.dy, a, t, px));
-        },
-        [&](int slot, unsigned px, auto refill) {
-            const V x = ring[2 * slot * kGpThreads], dy = ring[(2 * slot + 1) * kGpThreads];
-            refill();
-            float2 d[kPairs<VE>], dz[kPairs<VE>];
-            const unsigned long long e = gp_element(a, t, px);
-            gn_dz<T, VE, DROP, ACT>(x, dy, k, a.drop, e >> 3, e & 7, d, dz);
+    const unsigned step = gp_step<T>(a, t);
+    GpWalker<T, VE> out(a.y, a, t, t.p0 + t.lane);
+    gp_stream<T, VE>(a, t, ring, [&](const V &x, const V &dy, unsigned long long e, unsigned px) {
+        float2 d[kPairs<VE>], dz[kPairs<VE>];
+        gn_dz<T, VE, DROP, ACT>(x, dy, k, a.drop, e >> 3, e & 7, d, dz);
 #pragma unroll
-            for (int i = 0; i < kPairs<VE>; i++) {
-                if (DROP) dz[i] = __fmul2_rn(dz[i], both(a.drop.scale));
-                dz[i] = __ffma2_rn(d[i], k1[i], __ffma2_rn(dz[i], k.a[i], k0[i]));
-            }
-            __stcs(const_cast<V *>(gp_at<T, VE>(a.y, a, t, px)), pack2<T, VE>(dz));
-        });
+        for (int i = 0; i < kPairs<VE>; i++) {
+            if (DROP) dz[i] = __fmul2_rn(dz[i], both(a.drop.scale));
+            dz[i] = __ffma2_rn(d[i], k1[i], __ffma2_rn(dz[i], k.a[i], k0[i]));
+        }
+        __stcs(out.get(), pack2<T, VE>(dz));
+        out.go(a.y, a, t, px + t.lanes, step);
+    });
 }
 
 // The chunks' shares joined, kJoinWide channels a block, the chunks over its
