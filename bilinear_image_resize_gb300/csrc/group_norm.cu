@@ -7,8 +7,8 @@
 //   A = sum gamma dz / M,  B = sum gamma dz xh / M  (over the group)
 //   dx = rstd (gamma dz - A - xh B).
 //
-// Memory bounds both: a call that reads and writes each map once is as fast as
-// it can be.  Small images are kept on chip between the two passes
+// A call's floor is each map read or written once; the arithmetic (the generator,
+// the sigmoid) comes near it or above.  Small images are kept on chip between the two passes
 // (gn_cluster.cu), others are read twice, the second time out of L2 as far as
 // it holds them (gn_passes.h).
 #include <algorithm>

@@ -1,8 +1,10 @@
 // Dropout of a channels-last map, and the add of a residual that follows it in
 // a block: y = drop(x) + residual, the mask made from a counter as the map
 // passes through (map_ops.h), never stored.  One read of each input and one
-// write: memory bounds it where the generator's arithmetic (about 70 integer
-// instructions for eight elements) stays below it.
+// write: DRAM bounds it, for the generator's arithmetic (about 70 integer
+// instructions for eight elements) fits below.  32 x 64 x 64 x 1024 bf16 with a
+// residual 115 us, 7.0 TB/s; 7 x 61 x 83 x 200 f16 7.8 us, 5.5 TB/s; a small
+// call 2 us, the launch.
 #include <algorithm>
 
 #include "map_ops.h"
@@ -15,7 +17,7 @@ namespace {
 using namespace maps;
 
 constexpr int kDropThreads = 256;
-constexpr int kDropVecs = 4;    // vectors a thread reads before it uses the first
+constexpr int kDropVecs = 4;    // vectors a thread reads before it uses the first (115 us as above, 133 with one)
 
 struct DropArgs {
     View x, r, y;               // r.p null: no residual

@@ -22,7 +22,10 @@
  *    OpenCV on GPUs", §3.1.1);
  *  - beside the method: the standalone K x K correlation over the valid
  *    region, many geometries in one launch, a texture-unit comparison path
- *    and an allocation-free uint8 entry.
+ *    and an allocation-free uint8 entry;
+ *  - on the feature maps of models that take resized frames: group norm with
+ *    an activation and dropout, dropout with a residual, and the bilinear
+ *    resize of maps and position tables, each with its gradient.
  *
  * Numerics:
  *  - uint8 bilinear is exact integer arithmetic: 11-bit weights
@@ -405,13 +408,14 @@ RZ_API int resize_copy_baseline(const void *src, void *dst, size_t bytes, int fl
  *
  * Operators of the models that resized frames go into, on channels-last maps
  * (N, H, W, C) of float32, bfloat16 or float16 (RZ_F32, RZ_BF16, RZ_F16), with
- * any C up to RZ_MAX_DIM.  A map is given by its device pointer, the byte pitch between rows
- * (>= W * C elements; ignored for H = 1) and the byte stride between images
- * (>= an image; ignored for N = 1), all multiples of the element size; pixels
- * of a row are packed.  The struct itself is host memory, read during the call.
- * Sizes are not negative, C >= 1, H * W < 2^31 and N * H * W * C <= 2^46.  Arithmetic and every sum, statistic and gradient is float32; 16-bit
- * results are rounded once, to nearest even, as they are stored.  Results do
- * not depend on timing: the same call gives the same bits.
+ * any C up to RZ_MAX_DIM.  A map is given by its device pointer, the byte pitch
+ * between rows (>= W * C elements; ignored for H = 1) and the byte stride
+ * between images (>= an image; ignored for N = 1), all multiples of the element
+ * size; pixels of a row are packed.  The struct itself is host memory, read
+ * during the call.  Sizes are not negative, C >= 1, H * W < 2^31 and
+ * N * H * W * C <= 2^46.  Arithmetic and every sum, statistic and gradient is
+ * float32; 16-bit results are rounded once, to nearest even, as they are
+ * stored.  Results do not depend on timing: the same call gives the same bits.
  */
 #define RZ_BF16 2
 #define RZ_F16 3
@@ -506,6 +510,9 @@ RZ_API int map_group_norm_grad(const rz_norm *d, const rz_drop *drop, const rz_m
  * (the same pointer, pitch and stride).  H, W >= 1 and H, W, out_h, out_w <=
  * RZ_MAX_DIM; more than 65535 source images, or rows of 2^31 elements, are
  * RZ_ERR_UNSUPPORTED.  dst overlaps neither src nor, otherwise, base.
+ * Between two taps the value is near + u (far - near), as in resize_f32: a NaN
+ * or an infinity makes every output whose taps include it a NaN or an infinity,
+ * one of weight 0 included.
  * Asynchronous on `stream`; no allocation.  An empty dst is RZ_OK.
  */
 typedef struct {
