@@ -431,21 +431,27 @@ def _stream_at(stream, t) -> int:
     return _torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
 
 
-def _workspace(nbytes: int, like, stream):
-    """A workspace of `nbytes` that belongs to the call's stream, from torch's allocator."""
-    torch = _torch
+def _with_workspace(call, workspace, query, d, like, stream) -> int:
+    """call(pointer, bytes, stream) with the given workspace, or with query(d)
+    bytes from torch's allocator that belong to the call's stream and go back
+    once it is queued (without a tensor around them, which costs as much as
+    two launches)."""
+    s = _stream_at(stream, like)
+    if workspace is not None:
+        return call(workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    nbytes = query(d)
     if nbytes == 0:
-        return None
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=like.device) if stream else torch.cuda.default_stream(like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-
-
-def _bytes_of(workspace):
-    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        return call(None, 0, s)
+    c = _torch._C
+    if like.get_device() == c._cuda_getDevice():
+        p = c._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+    else:
+        with _torch.cuda.device(like.device):
+            p = c._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+    try:
+        return call(p, nbytes, s)
+    finally:
+        c._cuda_cudaCachingAllocator_raw_delete(p)
 
 
 def map_dropout(x, y, p: float, seed: int, offset: int = 0, residual=None, stream=None) -> None:
@@ -500,13 +506,13 @@ def map_group_norm(x, y, groups: int, gamma=None, beta=None, mean=None, rstd=Non
     if y.dtype is not x.dtype:
         raise ValueError("x and y differ in dtype")
     d = RzNorm(*shape, groups, _map_dtype(x, "x"), act, eps)
-    if workspace is None:
-        workspace = _workspace(_norm_workspace(d), x, stream)
     channels, stats = (shape[3],), (shape[0], groups)
-    _check(_native.load().map_group_norm(
-        d, None if drop is None else _drop_of(*drop), mx, my, _floats(gamma, "gamma", channels),
-        _floats(beta, "beta", channels), _floats(mean, "mean", stats), _floats(rstd, "rstd", stats),
-        *_bytes_of(workspace), _stream_at(stream, x)), "map_group_norm")
+    dr = None if drop is None else _drop_of(*drop)
+    g, b = _floats(gamma, "gamma", channels), _floats(beta, "beta", channels)
+    m, r = _floats(mean, "mean", stats), _floats(rstd, "rstd", stats)
+    f = _native.load().map_group_norm
+    _check(_with_workspace(lambda w, n, st: f(d, dr, mx, my, g, b, m, r, w, n, st), workspace, _norm_workspace, d, x,
+                           stream), "map_group_norm")
 
 
 def map_group_norm_grad(dy, x, dx, groups: int, gamma=None, beta=None, mean=None, rstd=None, dgamma=None, dbeta=None,
@@ -519,14 +525,14 @@ def map_group_norm_grad(dy, x, dx, groups: int, gamma=None, beta=None, mean=None
     if dy.dtype is not x.dtype or dx.dtype is not x.dtype:
         raise ValueError("x, dy and dx differ in dtype")
     d = RzNorm(*shape, groups, _map_dtype(x, "x"), act, eps)
-    if workspace is None:
-        workspace = _workspace(_norm_workspace(d), x, stream)
     channels, stats = (shape[3],), (shape[0], groups)
-    _check(_native.load().map_group_norm_grad(
-        d, None if drop is None else _drop_of(*drop), md, mx, mo, _floats(gamma, "gamma", channels),
-        _floats(beta, "beta", channels), _floats(mean, "mean", stats), _floats(rstd, "rstd", stats),
-        _floats(dgamma, "dgamma", channels), _floats(dbeta, "dbeta", channels), *_bytes_of(workspace),
-        _stream_at(stream, x)), "map_group_norm_grad")
+    dr = None if drop is None else _drop_of(*drop)
+    g, b = _floats(gamma, "gamma", channels), _floats(beta, "beta", channels)
+    m, r = _floats(mean, "mean", stats), _floats(rstd, "rstd", stats)
+    dg, db = _floats(dgamma, "dgamma", channels), _floats(dbeta, "dbeta", channels)
+    f = _native.load().map_group_norm_grad
+    _check(_with_workspace(lambda w, n, st: f(d, dr, md, mx, mo, g, b, m, r, dg, db, w, n, st), workspace,
+                           _norm_workspace, d, x, stream), "map_group_norm_grad")
 
 
 def _resample_of(src, dst, names):
@@ -566,9 +572,8 @@ def resize_map_grad(ddst, dsrc, workspace=None, stream=None) -> None:
     """dsrc[:] = the gradient of resize_map towards src, from ddst; summed over
     the images where dsrc has one."""
     d, ms, md = _resample_of(dsrc, ddst, ("dsrc", "ddst"))
-    if workspace is None:
-        workspace = _workspace(_resample_workspace(d), ddst, stream)
-    _check(_native.load().resize_map_grad(d, md, ms, *_bytes_of(workspace), _stream_at(stream, ddst)),
+    f = _native.load().resize_map_grad
+    _check(_with_workspace(lambda w, n, st: f(d, md, ms, w, n, st), workspace, _resample_workspace, d, ddst, stream),
            "resize_map_grad")
 
 
