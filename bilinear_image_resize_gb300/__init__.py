@@ -467,17 +467,17 @@ def map_dropout(x, y, p: float, seed: int, offset: int = 0, residual=None, strea
             raise ValueError("x, y and residual differ in dtype, shape or device")
     if not x.is_cuda:
         raise ValueError("x: expected a CUDA tensor")
+    drop = _drop_of(p, seed, offset)
     if all(t.is_contiguous() for t in both):
-        # any shape whose elements follow one another: as many images of one row, of the last dimension
-        n = x.numel()
-        wide = x.shape[-1] if n and x.dim() else n
-        shape, row = (n // wide if n else 1, 1, wide, 1), wide * x.element_size()
-        maps = [RzMap(t.data_ptr(), row, row) for t in both]
+        # any shape whose elements follow one another, their number past 32 bits among them
+        r = None if residual is None else residual.data_ptr()
+        rc = _native.load().map_dropout_packed(x.data_ptr(), r, y.data_ptr(), x.numel(), dtype, drop, _stream_at(stream, x))
     else:
         shape = _map_of(x, "x")[0]
         maps = [_map_of(t, name)[1] for t, name in zip(both, ("x", "y", "residual"))]
-    _check(_native.load().map_dropout(maps[0], maps[2] if residual is not None else None, maps[1], *shape, dtype,
-                                      _drop_of(p, seed, offset), _stream_at(stream, x)), "map_dropout")
+        rc = _native.load().map_dropout(maps[0], maps[2] if residual is not None else None, maps[1], *shape, dtype, drop,
+                                        _stream_at(stream, x))
+    _check(rc, "map_dropout")
 
 
 def _norm_workspace(d) -> int:

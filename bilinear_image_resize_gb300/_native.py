@@ -173,6 +173,7 @@ SIGNATURES = {
     "resize_u8_noalloc": (_i, [_p, _sz, _p, _sz, _i, _i, _i, _i, _i, _i, _p]),
     "resize_copy_baseline": (_i, [_p, _p, _sz, _i, _p]),
     "map_dropout": (_i, [_map, _map, _map, _i, _i, _i, _i, _i, _drop, _p]),
+    "map_dropout_packed": (_i, [_p, _p, _p, _sz, _i, _drop, _p]),
     "map_group_norm_workspace": (_i, [_norm, ctypes.POINTER(_sz)]),
     "map_group_norm": (_i, [_norm, _drop, _map, _map, _p, _p, _p, _p, _p, _sz, _p]),
     "map_group_norm_grad": (_i, [_norm, _drop, _map, _map, _map, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),

@@ -6,6 +6,7 @@
 // residual 115 us, 7.0 TB/s; 7 x 61 x 83 x 200 f16 7.8 us, 5.5 TB/s; a small
 // call 2 us, the launch.
 #include <algorithm>
+#include <initializer_list>
 
 #include "map_ops.h"
 #include "rz_device.h"
@@ -92,6 +93,32 @@ cudaError_t drop_launch(const DropArgs &a, bool whole, void *stream)
     return launch(fn, dim3(static_cast<unsigned>(blocks)), kDropThreads, 0, stream, a);
 }
 
+// Launches over `all` elements of maps in rows of `row`; ONE: the maps' elements
+// follow one another, and a vector may cross rows.
+int drop_run(DropArgs &a, int dtype, bool one, bool aligned, unsigned long long row, unsigned long long all,
+             const rz_drop *drop, void *stream)
+{
+    const unsigned ve = 16 / static_cast<unsigned>(dtype_size(dtype));
+    const bool wide = (one || row % ve == 0) && aligned;
+    a.drop = make_drop(drop);
+    a.dropping = drop_threshold(drop) != 0;
+    a.row = wide ? row / ve : row;
+    a.total = wide ? all / ve : all;
+    a.tail = wide ? static_cast<unsigned>(all % ve) : 0;
+    // one element at a time a map of 2^41 elements would pass the grid's width
+    if (a.total / (kDropVecs * kDropThreads) >= 0x7fffffffull) return RZ_ERR_UNSUPPORTED;
+    cudaError_t e;
+    if (dtype == RZ_F32)
+        e = wide ? drop_launch<float, 4>(a, one, stream) : drop_launch<float, 1>(a, one, stream);
+    else if (dtype == RZ_BF16)
+        e = wide ? drop_launch<__nv_bfloat16, 8>(a, one, stream) : drop_launch<__nv_bfloat16, 1>(a, one, stream);
+    else
+        e = wide ? drop_launch<__half, 8>(a, one, stream) : drop_launch<__half, 1>(a, one, stream);
+    if (e == cudaSuccess) return RZ_OK;
+    record_cuda_error(static_cast<int>(e));
+    return RZ_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace rz
 
@@ -115,31 +142,29 @@ int map_dropout(const rz_map *x, const rz_map *residual, const rz_map *y, int N,
     a.x = maps::view(x);
     a.y = maps::view(y);
     if (residual) a.r = maps::view(residual);
-    const bool one = whole(x) && whole(y) && whole(residual);
-    const unsigned long long row = static_cast<unsigned long long>(s.W) * s.C, all = row * s.N * s.H;
     a.H = static_cast<unsigned>(s.H);
-    a.drop = maps::make_drop(drop);
-    a.dropping = maps::drop_threshold(drop) != 0;
-    const int ve = 16 / static_cast<int>(s.es);
+    const bool one = whole(x) && whole(y) && whole(residual);
     const auto aligned = [&](const rz_map *m) {
         return !m || (one ? reinterpret_cast<uintptr_t>(m->data) % 16 == 0 : maps::map_aligned(*m, s, 16));
     };
-    const bool wide = (one || row % ve == 0) && aligned(x) && aligned(y) && aligned(residual);
-    a.row = wide ? row / ve : row;
-    a.total = wide ? all / ve : all;
-    a.tail = wide ? static_cast<unsigned>(all % ve) : 0;
-    // one element at a time a map of 2^41 elements would pass the grid's width
-    if (a.total / (kDropVecs * kDropThreads) >= 0x7fffffffull) return RZ_ERR_UNSUPPORTED;
-    cudaError_t e;
-    if (dtype == RZ_F32)
-        e = wide ? drop_launch<float, 4>(a, one, stream) : drop_launch<float, 1>(a, one, stream);
-    else if (dtype == RZ_BF16)
-        e = wide ? drop_launch<__nv_bfloat16, 8>(a, one, stream) : drop_launch<__nv_bfloat16, 1>(a, one, stream);
-    else
-        e = wide ? drop_launch<__half, 8>(a, one, stream) : drop_launch<__half, 1>(a, one, stream);
-    if (e == cudaSuccess) return RZ_OK;
-    record_cuda_error(static_cast<int>(e));
-    return RZ_ERR_CUDA;
+    const unsigned long long row = static_cast<unsigned long long>(s.W) * s.C;
+    return drop_run(a, dtype, one, aligned(x) && aligned(y) && aligned(residual), row, row * s.N * s.H, drop, stream);
+}
+
+int map_dropout_packed(const void *x, const void *residual, void *y, size_t n, int dtype, const rz_drop *drop, void *stream)
+{
+    const size_t es = maps::dtype_size(dtype);
+    if (!es || n > (size_t{1} << 46) || !drop || !maps::drop_ok(drop)) return RZ_ERR_ARG;
+    if (n == 0) return RZ_OK;
+    const auto at = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
+    if (!x || !y || at(x) % es || at(y) % es || at(residual) % es) return RZ_ERR_ARG;
+    for (const void *p : {x, residual})
+        if (p && p != y && at(p) < at(y) + n * es && at(y) < at(p) + n * es) return RZ_ERR_ARG;
+    DropArgs a{};
+    a.x.p = static_cast<uint8_t *>(const_cast<void *>(x));
+    a.y.p = static_cast<uint8_t *>(y);
+    a.r.p = static_cast<uint8_t *>(const_cast<void *>(residual));
+    return drop_run(a, dtype, true, (at(x) | at(y) | at(residual)) % 16 == 0, n, n, drop, stream);
 }
 
 }  // extern "C"

@@ -455,6 +455,14 @@ RZ_API int map_dropout(const rz_map *x, const rz_map *residual, const rz_map *y,
                        int dtype, const rz_drop *drop, void *stream);
 
 /*
+ * The same on n <= 2^46 elements that follow one another, whatever their
+ * shape: element e is the e-th from the pointers.  x, y and residual (NULL for
+ * none) are device pointers of the element's alignment.
+ */
+RZ_API int map_dropout_packed(const void *x, const void *residual, void *y, size_t n, int dtype, const rz_drop *drop,
+                              void *stream);
+
+/*
  * Group norm with an activation and dropout.  For image n and group g of
  * C / groups neighbouring channels, over its M = H W C / groups values:
  *   mean = sum x / M, rstd = 1 / sqrt(sum (x - mean)^2 / M + eps),

@@ -1,0 +1,99 @@
+"""What the binding of the feature-map operators hands to the library: sizes
+past 32 bits, and what it refuses before any call.  The tensors are stand-ins
+without memory and the library's functions are recorders with the binding's
+own ctypes signatures, so nothing is launched and no GPU is needed."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class Standin:
+    """A CUDA tensor's shape, strides and type over no memory."""
+
+    def __init__(self, shape, dtype=torch.bfloat16, device=0, at=1 << 40, strides=None, cuda=True):
+        self.meta = torch.empty(shape, dtype=dtype, device="meta")
+        if strides:
+            self.meta = self.meta.as_strided(shape, strides)
+        self.dtype, self.shape, self.is_cuda, self.index, self.at = dtype, self.meta.shape, cuda, device, at
+        self.device = torch.device("cuda", device) if cuda else torch.device("cpu")
+
+    def data_ptr(self):
+        return self.at
+
+    def get_device(self):
+        return self.index if self.is_cuda else -1
+
+    def __getattr__(self, name):
+        return getattr(self.meta, name)
+
+
+@pytest.fixture
+def rz():
+    import bilinear_image_resize_gb300 as m
+    return m
+
+
+@pytest.fixture
+def calls(rz, monkeypatch):
+    """(name, arguments as the library would receive them) of every call."""
+    from bilinear_image_resize_gb300 import _native
+    made, kept = [], []
+
+    class Library:
+        pass
+
+    def recorder(name, res, args):
+        def record(*got):
+            made.append((name, got))
+            return 0
+        return ctypes.CFUNCTYPE(res, *args)(record)
+
+    lib = Library()
+    for name, (res, args) in _native.SIGNATURES.items():
+        if name.startswith(("map_", "resize_map")):
+            f = recorder(name, res, args)
+            kept.append(f)
+            setattr(lib, name, f)
+    monkeypatch.setattr(_native, "load", lambda: lib)
+    return made
+
+
+LARGE = [(1 << 32,), (1, 1 << 32), (1 << 32, 1), (64, 8192, 8192, 1), ((1 << 32) + 5,), ((1 << 32) + 5, 1), (1 << 31,),
+         ((1 << 31) + 11,), (3, (1 << 31) + 11), (1 << 16, 1 << 16, 3)]
+
+
+@pytest.mark.parametrize("shape", LARGE + [(7,), (), (3, 0), (2, 3, 5, 4, 2)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_dropout_takes_every_element_of_packed_tensors(rz, calls, shape, residual):
+    x, y, r = Standin(shape), Standin(shape, at=1 << 41), Standin(shape, at=1 << 42) if residual else None
+    rz.map_dropout(x, y, 0.5, 1, residual=r, stream=0)
+    done = 0
+    for name, a in calls:
+        if name == "map_dropout_packed":
+            assert (a[0], a[1], a[2], a[4]) == (1 << 40, (1 << 42) if residual else None, 1 << 41, 2)
+            done += a[3]
+        else:
+            n, h, w, c = a[3:7]
+            assert name == "map_dropout" and min(n, h, w, c) >= 0
+            done += n * h * w * c
+    assert done == x.numel()
+
+
+def test_packed_dropout_refuses():
+    from bilinear_image_resize_gb300 import _build, _native
+    _build.build()
+    lib, d, arg = _native.load(), _native.RzDrop(0.1, 1, 2), 1
+    x, y, r = 1 << 20, 1 << 21, 1 << 22
+
+    def drop(x=x, r=None, y=y, n=256, dtype=1, spec=d):
+        return lib.map_dropout_packed(x, r, y, n, dtype, spec, None)
+
+    for bad in (dict(x=None), dict(y=None), dict(x=x + 2), dict(y=y + 1), dict(r=r + 2), dict(dtype=0), dict(dtype=4),
+                dict(spec=None), dict(spec=_native.RzDrop(-0.1, 0, 0)), dict(spec=_native.RzDrop(float("nan"), 0, 0)),
+                dict(n=(1 << 46) + 1), dict(y=x + 1020), dict(x=y + 1020), dict(r=y + 4), dict(r=y - 4)):
+        assert drop(**bad) == arg, bad
+    # an element at a time, more than the grid's width of blocks
+    assert drop(n=1 << 42, x=(1 << 50) + 4, y=(1 << 51) + 4) == 2
+    assert drop(x=None, y=None, n=0) == 0
