@@ -389,6 +389,16 @@ def _map_dtype(t, name: str) -> int:
     return code
 
 
+#: ctypes cuts what it stores in an int to 32 bits without an error.
+_INT_MAX = 0x7FFFFFFF
+
+
+def _int(v, name: str):
+    if not -_INT_MAX <= v <= _INT_MAX:
+        raise ValueError(f"{name}: {v} does not fit 32 bits")
+    return v
+
+
 def _map_of(t, name: str, shape=None):
     """((N, H, W, C), rz_map) of an (N, H, W, C) or (H, W, C) tensor whose pixels are packed; `shape`: what it must be."""
     dims = t.dim()
@@ -401,6 +411,8 @@ def _map_of(t, name: str, shape=None):
         raise ValueError(f"{name}: expected NxHxWxC or HxWxC, got shape {tuple(t.shape)}")
     if shape is not None and got != shape:
         raise ValueError(f"{name}: shape {got}, expected {shape}")
+    if max(got) > _INT_MAX:
+        raise ValueError(f"{name}: shape {got} past 2^31 - 1")
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
     es = t.element_size()
@@ -489,7 +501,7 @@ def _norm_workspace(d) -> int:
 def map_group_norm_workspace(x, groups: int) -> int:
     """Bytes of workspace that map_group_norm and map_group_norm_grad need on a map like x."""
     _with_torch()
-    return _norm_workspace(RzNorm(*_map_of(x, "x")[0], groups, _map_dtype(x, "x"), RZ_ACT_NONE, 1.0))
+    return _norm_workspace(RzNorm(*_map_of(x, "x")[0], _int(groups, "groups"), _map_dtype(x, "x"), RZ_ACT_NONE, 1.0))
 
 
 def map_group_norm(x, y, groups: int, gamma=None, beta=None, mean=None, rstd=None, act: int = RZ_ACT_NONE,
@@ -505,7 +517,7 @@ def map_group_norm(x, y, groups: int, gamma=None, beta=None, mean=None, rstd=Non
     my = _map_of(y, "y", shape)[1]
     if y.dtype is not x.dtype:
         raise ValueError("x and y differ in dtype")
-    d = RzNorm(*shape, groups, _map_dtype(x, "x"), act, eps)
+    d = RzNorm(*shape, _int(groups, "groups"), _map_dtype(x, "x"), _int(act, "act"), eps)
     channels, stats = (shape[3],), (shape[0], groups)
     dr = None if drop is None else _drop_of(*drop)
     g, b = _floats(gamma, "gamma", channels), _floats(beta, "beta", channels)
@@ -524,7 +536,7 @@ def map_group_norm_grad(dy, x, dx, groups: int, gamma=None, beta=None, mean=None
     md, mo = _map_of(dy, "dy", shape)[1], _map_of(dx, "dx", shape)[1]
     if dy.dtype is not x.dtype or dx.dtype is not x.dtype:
         raise ValueError("x, dy and dx differ in dtype")
-    d = RzNorm(*shape, groups, _map_dtype(x, "x"), act, eps)
+    d = RzNorm(*shape, _int(groups, "groups"), _map_dtype(x, "x"), _int(act, "act"), eps)
     channels, stats = (shape[3],), (shape[0], groups)
     dr = None if drop is None else _drop_of(*drop)
     g, b = _floats(gamma, "gamma", channels), _floats(beta, "beta", channels)

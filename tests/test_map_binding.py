@@ -81,6 +81,47 @@ def test_dropout_takes_every_element_of_packed_tensors(rz, calls, shape, residua
     assert done == x.numel()
 
 
+# every size of a map past an int, and one that an int would hold as a small number
+PAST = [((1 << 32) + 2, 1, 1, 8), (1, (1 << 32) + 2, 1, 8), (1, 1, (1 << 32) + 2, 8), (1, 1, 1, (1 << 32) + 8),
+        (1, 1, 1 << 32, 8), (1 << 31, 1, 1, 8), (1, 1 << 31, 1, 8)]
+
+
+@pytest.mark.parametrize("shape", PAST)
+def test_sizes_past_an_int_are_refused(rz, calls, shape):
+    x, y = Standin(shape), Standin(shape, at=1 << 50)
+    small, g = Standin((1, 2, 2, shape[3])), Standin((shape[0], 2), torch.float32)
+    for call in (lambda: rz.map_group_norm(x, y, 2, stream=0), lambda: rz.map_group_norm_workspace(x, 2),
+                 lambda: rz.map_group_norm_grad(x, x, y, 2, mean=g, rstd=g, stream=0),
+                 lambda: rz.resize_map(x, y, stream=0), lambda: rz.resize_map(small, y, stream=0),
+                 lambda: rz.resize_map_grad(x, y, stream=0), lambda: rz.resize_map_grad(y, small, stream=0),
+                 lambda: rz.resize_map_grad_workspace(x, y)):
+        with pytest.raises(ValueError):
+            call()
+    assert not calls
+
+
+def test_strided_sizes_past_an_int_are_refused_by_dropout(rz, calls):
+    shape, strides = (2, 1 << 32, 1, 8), (16 << 32, 16, 8, 1)
+    with pytest.raises(ValueError):
+        rz.map_dropout(Standin(shape, strides=strides), Standin(shape, strides=strides, at=1 << 50), 0.5, 1, stream=0)
+    assert not calls
+
+
+@pytest.mark.parametrize("change", [dict(groups=(1 << 32) + 2), dict(groups=-(1 << 32) + 2), dict(act=(1 << 32) + 1)])
+def test_groups_and_activation_past_an_int_are_refused(rz, calls, change):
+    x, y, m = Standin((2, 4, 4, 8)), Standin((2, 4, 4, 8), at=1 << 50), Standin((2, 2), torch.float32)
+    kw = {**dict(groups=2, act=0), **change}
+    stats = {} if "groups" in change else dict(mean=m, rstd=m)
+    for call in (lambda: rz.map_group_norm(x, y, stream=0, **kw),
+                 lambda: rz.map_group_norm_grad(x, x, y, stream=0, **stats, **kw)):
+        with pytest.raises(ValueError):
+            call()
+    if "groups" in change:
+        with pytest.raises(ValueError):
+            rz.map_group_norm_workspace(x, kw["groups"])
+    assert not calls
+
+
 def test_packed_dropout_refuses():
     from bilinear_image_resize_gb300 import _build, _native
     _build.build()
