@@ -91,7 +91,9 @@ int gn_check(const rz_norm *d, Shape *s)
     if (!s->es || !shape_ok(*s) || d->groups < 1 || d->C % d->groups != 0) return RZ_ERR_ARG;
     if (d->act != RZ_ACT_NONE && d->act != RZ_ACT_SILU && d->act != RZ_ACT_GELU) return RZ_ERR_ARG;
     if (!(d->eps > 0.0f) || !(d->eps <= 3.0e38f)) return RZ_ERR_ARG;
-    return d->N > 65535 ? RZ_ERR_UNSUPPORTED : RZ_OK;
+    // the grid's depth, and statistics that the kernels number in 32 bits
+    if (d->N > 65535 || static_cast<long long>(d->N) * d->groups > 0x7fffffffLL) return RZ_ERR_UNSUPPORTED;
+    return RZ_OK;
 }
 
 void gn_fill(const rz_norm *d, const Shape &s, GnArgs &a)

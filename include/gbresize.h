@@ -471,8 +471,8 @@ RZ_API int map_dropout_packed(const void *x, const void *residual, void *y, size
  * the normal distribution function).  gamma and beta: device float[C], or NULL
  * for 1 and 0.  mean and rstd: device float[N][groups], written for the
  * gradient (either may be NULL).  drop: NULL for none.  C a multiple of
- * groups; eps > 0, finite; N <= 65535 (RZ_ERR_UNSUPPORTED above).  x and y
- * must not overlap.
+ * groups; eps > 0, finite; N <= 65535 and N * groups < 2^31 (else
+ * RZ_ERR_UNSUPPORTED).  x and y must not overlap.
  *
  * workspace: device memory of at least the bytes that
  * map_group_norm_workspace gives for this descriptor (enough for the gradient

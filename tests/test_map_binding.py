@@ -138,3 +138,20 @@ def test_packed_dropout_refuses():
     # an element at a time, more than the grid's width of blocks
     assert drop(n=1 << 42, x=(1 << 50) + 4, y=(1 << 51) + 4) == 2
     assert drop(x=None, y=None, n=0) == 0
+
+
+def test_norm_refuses_more_statistics_than_an_int_counts():
+    from bilinear_image_resize_gb300 import _build, _native
+    _build.build()
+    lib, n, unsupported = _native.load(), ctypes.c_size_t(0), 2
+    for N, C, groups in ((65535, 65536, 65536), (32768, 65536, 65536), (65535, 65536, 32768)):
+        d, m = _native.RzNorm(N, 1, 1, C, groups, 2, 0, 1e-5), _native.RzMap(1 << 40, 2 * C, 2 * C)
+        far, want = _native.RzMap(1 << 41, 2 * C, 2 * C), unsupported if N * groups > 0x7fffffff else 0
+        assert lib.map_group_norm_workspace(d, ctypes.byref(n)) == want
+        # no workspace: refused in any case
+        assert lib.map_group_norm(d, None, m, far, None, None, None, None, None, 0, None) == (want or 1)
+        assert lib.map_group_norm_grad(d, None, m, m, far, None, None, 1 << 42, 1 << 43, None, None, None, 0,
+                                       None) == (want or 1)
+    # the most that is taken: 2^31 - 2^16 statistics
+    d = _native.RzNorm(32767, 1, 1, 65536, 65536, 2, 0, 1e-5)
+    assert lib.map_group_norm_workspace(d, ctypes.byref(n)) == 0 and n.value > 8 * 32767 * 65536
