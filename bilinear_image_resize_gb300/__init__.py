@@ -424,6 +424,17 @@ def _map_of(t, name: str, shape=None):
     return got, RzMap(t.data_ptr(), sh * es if H > 1 else W * C * es, sn * es if N > 1 else 0)
 
 
+def _on_current_device(t, *others) -> None:
+    """Kernels go to the current device, so every tensor of a call has to be there (as a plan's calls have to be on
+    the plan's)."""
+    device = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != device:
+            raise ValueError("the tensors of a call are on different devices")
+    if device != _torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on device {device}, which is not the current one")
+
+
 def _floats(t, name: str, shape):
     """Pointer of a packed float32 CUDA tensor of that shape (None: a null pointer)."""
     if t is None:
@@ -455,11 +466,7 @@ def _with_workspace(call, workspace, query, d, like, stream) -> int:
     if nbytes == 0:
         return call(None, 0, s)
     c = _torch._C
-    if like.get_device() == c._cuda_getDevice():
-        p = c._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
-    else:
-        with _torch.cuda.device(like.device):
-            p = c._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+    p = c._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
     try:
         return call(p, nbytes, s)
     finally:
@@ -476,9 +483,10 @@ def map_dropout(x, y, p: float, seed: int, offset: int = 0, residual=None, strea
     both = (x, y) if residual is None else (x, y, residual)
     for t in both[1:]:
         if t.dtype is not x.dtype or t.shape != x.shape or not t.is_cuda:
-            raise ValueError("x, y and residual differ in dtype, shape or device")
+            raise ValueError("x, y and residual differ in dtype or shape, or are not CUDA tensors")
     if not x.is_cuda:
         raise ValueError("x: expected a CUDA tensor")
+    _on_current_device(x, y, residual)
     drop = _drop_of(p, seed, offset)
     if all(t.is_contiguous() for t in both):
         # any shape whose elements follow one another, their number past 32 bits among them
@@ -514,6 +522,7 @@ def map_group_norm(x, y, groups: int, gamma=None, beta=None, mean=None, rstd=Non
     None to take one from torch's allocator."""
     _with_torch()
     shape, mx = _map_of(x, "x")
+    _on_current_device(x, y, gamma, beta, mean, rstd)
     my = _map_of(y, "y", shape)[1]
     if y.dtype is not x.dtype:
         raise ValueError("x and y differ in dtype")
@@ -533,6 +542,7 @@ def map_group_norm_grad(dy, x, dx, groups: int, gamma=None, beta=None, mean=None
     arguments of the map_group_norm call and the mean and rstd it wrote."""
     _with_torch()
     shape, mx = _map_of(x, "x")
+    _on_current_device(x, dy, dx, gamma, beta, mean, rstd, dgamma, dbeta)
     md, mo = _map_of(dy, "dy", shape)[1], _map_of(dx, "dx", shape)[1]
     if dy.dtype is not x.dtype or dx.dtype is not x.dtype:
         raise ValueError("x, dy and dx differ in dtype")
@@ -561,6 +571,7 @@ def resize_map(src, dst, base=None, stream=None) -> None:
     maps with any number of channels.  A src of one image serves every image of
     dst (a position table); it may be float32 where dst is 16-bit."""
     d, ms, md = _resample_of(src, dst, ("src", "dst"))
+    _on_current_device(dst, src, base)
     mb = None
     if base is not None:
         if base.dtype is not dst.dtype:
@@ -584,6 +595,7 @@ def resize_map_grad(ddst, dsrc, workspace=None, stream=None) -> None:
     """dsrc[:] = the gradient of resize_map towards src, from ddst; summed over
     the images where dsrc has one."""
     d, ms, md = _resample_of(dsrc, ddst, ("dsrc", "ddst"))
+    _on_current_device(ddst, dsrc)
     f = _native.load().resize_map_grad
     _check(_with_workspace(lambda w, n, st: f(d, md, ms, w, n, st), workspace, _resample_workspace, d, ddst, stream),
            "resize_map_grad")

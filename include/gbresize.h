@@ -416,6 +416,8 @@ RZ_API int resize_copy_baseline(const void *src, void *dst, size_t bytes, int fl
  * N * H * W * C <= 2^46.  Arithmetic and every sum, statistic and gradient is
  * float32; 16-bit results are rounded once, to nearest even, as they are
  * stored.  Results do not depend on timing: the same call gives the same bits.
+ * Everything that a call is given, its stream among it, belongs to the current
+ * device.
  */
 #define RZ_BF16 2
 #define RZ_F16 3

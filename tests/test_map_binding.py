@@ -57,6 +57,7 @@ def calls(rz, monkeypatch):
             kept.append(f)
             setattr(lib, name, f)
     monkeypatch.setattr(_native, "load", lambda: lib)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     return made
 
 
@@ -120,6 +121,44 @@ def test_groups_and_activation_past_an_int_are_refused(rz, calls, change):
         with pytest.raises(ValueError):
             rz.map_group_norm_workspace(x, kw["groups"])
     assert not calls
+
+
+def every_call(rz):
+    """name -> (a call of the operator with the given tensors, their names, shapes and types): all that an entry takes."""
+    f32, bf16 = torch.float32, torch.bfloat16
+    x = ((2, 4, 4, 8), bf16)
+    c, s = ((8,), f32), ((2, 2), f32)
+    norm = dict(x=x, y=x, gamma=c, beta=c, mean=s, rstd=s)
+    grad = dict(dy=x, x=x, dx=x, gamma=c, beta=c, mean=s, rstd=s, dgamma=c, dbeta=c)
+    return {
+        "dropout": (lambda x, y, residual: rz.map_dropout(x, y, 0.5, 1, residual=residual, stream=0),
+                    dict(x=x, y=x, residual=x)),
+        "norm": (lambda **t: rz.map_group_norm(groups=2, stream=0, **t), norm),
+        "norm_grad": (lambda **t: rz.map_group_norm_grad(groups=2, stream=0, **t), grad),
+        "resize": (lambda **t: rz.resize_map(stream=0, **t), dict(src=((2, 2, 2, 8), bf16), dst=x, base=x)),
+        "resize_grad": (lambda **t: rz.resize_map_grad(stream=0, **t), dict(ddst=x, dsrc=((1, 2, 2, 8), f32))),
+    }
+
+
+def standins(spec, strange=None, device=0, cuda=True, home=0):
+    return {k: Standin(shape, dtype, at=(64 + i) << 40, device=device if k == strange else home, cuda=cuda or k != strange)
+            for i, (k, (shape, dtype)) in enumerate(spec.items())}
+
+
+@pytest.mark.parametrize("op", ["dropout", "norm", "norm_grad", "resize", "resize_grad"])
+def test_tensors_of_another_device_are_refused(rz, calls, op):
+    call, spec = every_call(rz)[op]
+    for name in spec:
+        for t in (standins(spec, name, device=1), standins(spec, name, cuda=False)):
+            with pytest.raises(ValueError):
+                call(**t)
+    # all of them on one that is not current
+    with pytest.raises(ValueError):
+        call(**standins(spec, home=1))
+    assert not any(n in ("map_dropout", "map_dropout_packed", "map_group_norm", "map_group_norm_grad", "resize_map",
+                         "resize_map_grad") for n, _ in calls)
+    call(**standins(spec))
+    assert calls
 
 
 def test_packed_dropout_refuses():
