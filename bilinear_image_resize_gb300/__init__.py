@@ -461,6 +461,8 @@ def _with_workspace(call, workspace, query, d, like, stream) -> int:
     two launches)."""
     s = _stream_at(stream, like)
     if workspace is not None:
+        if not (workspace.is_cuda and workspace.get_device() == like.get_device() and workspace.is_contiguous()):
+            raise ValueError("workspace: expected a contiguous CUDA tensor on the device of the others")
         return call(workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
     nbytes = query(d)
     if nbytes == 0:

@@ -161,6 +161,21 @@ def test_tensors_of_another_device_are_refused(rz, calls, op):
     assert calls
 
 
+@pytest.mark.parametrize("op", ["norm", "norm_grad", "resize_grad"])
+def test_workspaces_that_are_not_the_calls_own_memory_are_refused(rz, calls, op):
+    call, spec = every_call(rz)[op]
+    u8, n = torch.uint8, 1 << 20
+    # host memory, another device's, one byte seen n times, every other byte
+    for bad in (Standin((n,), u8, cuda=False), Standin((n,), u8, device=1), Standin((n,), u8, strides=(0,)),
+                Standin((n // 2,), u8, strides=(2,))):
+        with pytest.raises(ValueError):
+            call(**standins(spec), workspace=bad)
+    assert not calls
+    call(**standins(spec), workspace=Standin((n // 4,), torch.float32, at=1 << 50))
+    (name, got), = calls
+    assert name in ("map_group_norm", "map_group_norm_grad", "resize_map_grad") and got[-3:] == (1 << 50, n, None)
+
+
 def test_packed_dropout_refuses():
     from bilinear_image_resize_gb300 import _build, _native
     _build.build()
