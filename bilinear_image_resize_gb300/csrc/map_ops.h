@@ -52,15 +52,17 @@ inline bool shape_ok(const Shape &s)
     return px <= 0x7fffffffLL && (px == 0 || s.N <= (1LL << 46) / (px * s.C));
 }
 
-// Pointer, alignment, pitch and stride of one map (of a non-empty shape).
+// Pointer, alignment, pitch and stride of one map (of a non-empty shape).  Rows
+// and images lie within 2^60 bytes, so that neither they nor extent() wrap.
 inline bool map_ok(const rz_map *m, const Shape &s)
 {
+    constexpr size_t kMost = size_t{1} << 60;
     if (!m || !m->data) return false;
     if (reinterpret_cast<uintptr_t>(m->data) % s.es || m->pitch % s.es || m->batch_stride % s.es) return false;
     if (m->pitch > (size_t{1} << 46) || m->batch_stride > (size_t{1} << 46)) return false;
-    if (s.H > 1 && m->pitch < s.row()) return false;
-    if (s.N > 1 && m->batch_stride < static_cast<size_t>(s.H - 1) * m->pitch + s.row()) return false;
-    return true;
+    const size_t below = static_cast<size_t>(s.H - 1), before = static_cast<size_t>(s.N - 1);
+    if (below && (m->pitch < s.row() || m->pitch > kMost / below)) return false;
+    return !before || (m->batch_stride >= below * m->pitch + s.row() && m->batch_stride <= kMost / before);
 }
 
 inline bool rows_joined(const rz_map &m, const Shape &s) { return s.H == 1 || m.pitch == s.row(); }

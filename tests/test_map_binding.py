@@ -209,3 +209,21 @@ def test_norm_refuses_more_statistics_than_an_int_counts():
     # the most that is taken: 2^31 - 2^16 statistics
     d = _native.RzNorm(32767, 1, 1, 65536, 65536, 2, 0, 1e-5)
     assert lib.map_group_norm_workspace(d, ctypes.byref(n)) == 0 and n.value > 8 * 32767 * 65536
+
+
+def test_maps_whose_bytes_pass_64_bits_are_refused():
+    from bilinear_image_resize_gb300 import _build, _native
+    _build.build()
+    lib, d, arg = _native.load(), _native.RzDrop(0.1, 1, 2), 1
+    top = 1 << 46
+    # rows 2^46 bytes apart, 2^18 of them below the last: 2^64, which 64 bits hold as 0
+    tall = _native.RzMap(1 << 20, top, 16)
+    assert lib.map_dropout(tall, None, tall, 2, (1 << 18) + 1, 1, 4, 1, d, None) == arg
+    assert lib.map_dropout(tall, None, tall, 1, (1 << 18) + 1, 1, 4, 1, d, None) == arg
+    assert lib.map_dropout(_native.RzMap(1 << 20, top, 16), None, _native.RzMap((1 << 20) + 16, top, 16), 1,
+                           (1 << 18) + 1, 1, 4, 1, d, None) == arg
+    many = _native.RzMap(1 << 20, 16, top)
+    assert lib.map_dropout(many, None, many, (1 << 18) + 1, 1, 1, 4, 1, d, None) == arg
+    far = _native.RzMap(1 << 40, 16, 16 * ((1 << 18) + 1))
+    r = _native.RzResample(1, 1, 16385, 1, 16385, 1, 4, 1, 1)
+    assert lib.resize_map(r, _native.RzMap(1 << 20, top, 0), None, far, None) == arg
