@@ -15,7 +15,7 @@
 // Each map crosses DRAM once, and what bounds the kernels is the arithmetic of
 // a round's phases, at 16 warps an SM and about half of the issue slots: 64 x 32
 // x 32 x 256 bf16 forward 18 us (3.7 TB/s), 26 with SiLU and dropout, gradient
-// 33 and 43; 16 x 64 x 64 x 320 with both 36 us, where its 128 units make two
+// 32 and 42; 16 x 64 x 64 x 320 with both 36 us, where its 128 units make two
 // rounds of 76 clusters; 2 x 14 x 14 x 256 4 us, one launch's latency.  More
 // warps measured slower: ten a CTA spill (40 us at 16 x 64 x 64 x 320), and
 // three CTAs an SM keep fewer vectors each, in larger clusters.

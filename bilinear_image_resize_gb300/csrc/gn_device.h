@@ -63,6 +63,13 @@ cudaError_t gn_kinds(int act, bool drop, Fn fn)
     return drop ? on(std::true_type{}) : on(std::false_type{});
 }
 
+// 1 / (1 + 2^(-z log2 e)) by the GPU's exp2 and reciprocal.  Rounding the
+// exponent costs up to |z| units of 2^-24 of the value where z is below 0 (4 at
+// -4, 31 at -40; 2 above 0), and below -87.3 the reciprocal's subnormal becomes
+// 0, for 1.1e-36 at most.  expf and a division are within 3 units everywhere,
+// but the float32 maps that could show it took 18% longer (64 x 32 x 32 x 256
+// forward 36.8 us against 31.1, gradient 61.4 against 52.5) and 16-bit ones,
+// which cannot, 40 to 57% (16 x 64 x 64 x 320 with dropout 53.8 against 36.4).
 __device__ __forceinline__ float2 sigmoid2(float2 z)
 {
     const float2 t = __fmul2_rn(z, both(-kLog2e));

@@ -6,11 +6,12 @@
 // slower than reading them twice (batches of 64 MB: the gradient of 4 x 512 x
 // 512 x 128 bf16 278 us against 231 us as it then was).
 //
-// The forward is bound by DRAM: 4 x 512 x 512 x 128 bf16 139 us, three
-// transfers of the map at 5.8 TB/s (142 us with SiLU; 181 with dropout, bound by
+// The forward is bound by DRAM: 4 x 512 x 512 x 128 bf16 138 us, three
+// transfers of the map at 5.8 TB/s (141 us with SiLU; 180 with dropout, bound by
 // the generator's arithmetic).  The gradient is bound by the instructions that
-// its warps issue: 8 x 128 x 128 x 512 bf16 120 us (five transfers, 5.6 TB/s),
-// as much with SiLU, 142 with dropout, which both passes make again.
+// its warps issue: 8 x 128 x 128 x 512 bf16 124 us (five transfers, 5.4 TB/s),
+// as much with SiLU, 142 with dropout, which both passes make again (146 where
+// each call is made by itself and not from a graph).
 //
 // A thread keeps one vector of channels and walks pixels, so sums are taken by
 // channel whatever the group's width; groups are put together from channels at
@@ -30,8 +31,9 @@ using namespace maps;
 
 constexpr int kGpThreads = 256, kGpWarps = kGpThreads / 32;
 // Pixels a thread loads before it uses the first, and the CTAs an SM that its
-// registers are held to: 4 x 512 x 512 x 128 bf16 with SiLU forward 152 us so,
-// 164 at two CTAs an SM, 155 with the loads through shared memory.
+// registers are held to: 4 x 512 x 512 x 128 bf16 with SiLU forward 152 us so
+// (later steps took it to 141), 164 at two CTAs an SM, 155 with the loads through
+// shared memory.
 constexpr int kGpStats = 4, kGpStatsCtas = 4, kGpApply = 4, kGpApplyCtas = 4;
 // The gradient, whose constants and sums fill the registers, has its loads on
 // their way in shared memory, kGpAhead pixels of x and dy a thread, and so a

@@ -57,8 +57,8 @@ constexpr int kGnBlock = 256;   // threads of a pass kernel's CTA
 
 // Chunks of an image for the pass kernels: as many CTAs over the call as are
 // resident at once (four an SM forward, three in the gradient; two waves of the
-// gradient's measured 66 against 64 us on 16 x 64 x 64 x 320 bf16, 36 against
-// 32 on 1 x 256 x 256 x 128), and at least eight pixels a thread.
+// gradient's measured 47.0 against 42.0 us on 16 x 64 x 64 x 320 bf16, 24.8
+// against 21.4 on 1 x 256 x 256 x 128), and at least eight pixels a thread.
 void gn_passes_plan(GnArgs &a, int ve, bool grad)
 {
     const long long vecs = a.C / ve, blocks = (vecs + kGnBlock - 1) / kGnBlock;

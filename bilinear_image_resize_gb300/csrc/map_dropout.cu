@@ -3,8 +3,8 @@
 // passes through (map_ops.h), never stored.  One read of each input and one
 // write: DRAM bounds it, for the generator's arithmetic (about 70 integer
 // instructions for eight elements) fits below.  32 x 64 x 64 x 1024 bf16 with a
-// residual 115 us, 7.0 TB/s; 7 x 61 x 83 x 200 f16 7.8 us, 5.5 TB/s; a small
-// call 2 us, the launch.
+// residual 115 us, 7.0 TB/s; 7 x 61 x 83 x 200 f16 7.6 us, 5.6 TB/s (8.5 where
+// none of its maps is left in L2); a small call 1.7 us, the launch.
 #include <algorithm>
 #include <initializer_list>
 

@@ -343,6 +343,9 @@ __device__ __forceinline__ float rcp_approx(float v)
 }
 
 // z Phi(z) and its derivative Phi(z) + z phi(z), Phi(z) = (1 + erf(z / sqrt 2)) / 2.
+// The sum cancels where z is below 0, so the error is absolute there, up to 1.2e-7,
+// which is more than the value itself from z = -5.5 on.  The slope's __expf, off by
+// 2 + 0.6 z^2 units of a z phi(z) below 0.25, adds no more than that.
 __device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.0f + erff(z * 0.70710678f)); }
 __device__ __forceinline__ float gelu_slope(float z)
 {

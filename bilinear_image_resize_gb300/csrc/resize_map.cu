@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(kMapThreads) k_sum_images(const ResampleArgs a
 // memory, some rows ahead, in places of the thread's own: held in registers
 // they left two CTAs an SM, and the launch waited on its loads.
 // 2x, 8 x 128 x 128 x 256 f16: 64 us, 5.3 TB/s (89 us from registers); float32
-// 104 us, 6.5 TB/s; 16 images' 37 x 50 x 1024 to a table of 24 x 24: 15.5 us
-// with the sum before it.
+// 104 us, 6.5 TB/s; 16 images' 37 x 50 x 1024 to a table of 24 x 24: 15.4 us
+// with the sum before it (16.3 where none of the maps is left in L2).
 template <class S, class T, int VE, int READERS>
 __global__ void __launch_bounds__(kMapThreads, kGradCtas<T, READERS>) k_resize_map_grad(const ResampleArgs a)
 {
@@ -375,9 +375,9 @@ dim3 map_grid(int W, int vecs, int rows, int images, int *run)
 }
 
 // Channels a thread takes: 16 bytes of the map's own type (a float32 table is
-// then read 32 bytes at a time), or 8, 4 or one element where the number of
-// channels or an alignment allows no more (8 x 64 x 64 x C bf16 doubled: 19 us
-// at C = 320, 68 us an element at a time).
+// then read 32 bytes at a time), or 8 or 4 bytes or one element where the number
+// of channels or an alignment allows no more (8 x 64 x 64 x C bf16 doubled: 24 us
+// at C = 320, 29 at 324, 41 at 322, where an element at a time took 68).
 int resample_vector(const rz_resample *d, const Checked &s, const rz_map *src, const rz_map *a, const rz_map *b)
 {
     for (int ve = 16 / static_cast<int>(s.dst.es); ve >= 2; ve /= 2)
