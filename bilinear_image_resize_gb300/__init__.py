@@ -19,8 +19,8 @@ from ._native import (KIND_F32, KIND_FILTER3X3, KIND_NORMALIZE, KIND_U8, RZ_BORD
                       RZ_ERR_UNSUPPORTED, RZ_F32, RZ_LINEAR, RZ_MAX_DIM, RZ_NEAREST, RZ_NOALLOC_MAX_DIM, RZ_OK,
                       RZ_OPT_CTAS_PER_SM, RZ_OPT_GENERIC_ONLY, RZ_OPT_GRID_MODE, RZ_OPT_PDL, RZ_OPT_RING_ROWS,
                       RZ_MULTI_MAX_JOBS, RZ_OPT_F32_KERNEL, RZ_OPT_FILTER_KERNEL, RZ_OPT_L2_PREFETCH, RZ_COPY_PDL, RZ_COPY_L2_PREFETCH, RZ_FILTER_AUTO, RZ_FILTER_FP32, RZ_FILTER_TENSOR, RZ_OPT_STAGES, RZ_OPT_U8_KERNEL, RZ_U8,
-                      RZ_ACT_GELU, RZ_ACT_NONE, RZ_ACT_SILU, RZ_BF16, RZ_F16, RzDrop, RzEpilogue, RzJob, RzMap, RzNorm,
-                      RzResample)
+                      RZ_ACT_GELU, RZ_ACT_NONE, RZ_ACT_SILU, RZ_BF16, RZ_F16, RzBias, RzDrop, RzEpilogue, RzJob, RzLinear, RzMap, RzNorm,
+                      RzQk, RzResample)
 
 __all__ = [
     "ResizeError", "Plan", "resize_plan_create", "resize_plan_destroy", "resize_plan_status",
@@ -41,6 +41,9 @@ __all__ = [
     "RZ_FILTER_AUTO", "RZ_FILTER_FP32", "RZ_FILTER_TENSOR",
     "map_group_norm", "map_group_norm_grad", "map_group_norm_workspace", "map_dropout",
     "resize_map", "resize_map_grad", "resize_map_grad_workspace",
+    "map_linear", "map_linear_workspace", "map_linear_grad", "map_linear_grad_workspace",
+    "map_qk_norm", "map_qk_norm_grad", "map_qk_norm_grad_workspace",
+    "map_position_bias", "map_position_bias_grad", "map_position_bias_grad_workspace", "map_position_buckets",
     "RZ_BF16", "RZ_F16", "RZ_ACT_NONE", "RZ_ACT_SILU", "RZ_ACT_GELU",
 ]
 
@@ -601,6 +604,293 @@ def resize_map_grad(ddst, dsrc, workspace=None, stream=None) -> None:
     f = _native.load().resize_map_grad
     _check(_with_workspace(lambda w, n, st: f(d, md, ms, w, n, st), workspace, _resample_workspace, d, ddst, stream),
            "resize_map_grad")
+
+
+def _ints(t, name: str, shape):
+    """Pointer of a packed int32 CUDA tensor of that shape (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype is not _torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def _matrix(t, name: str, shape):
+    """(pointer, byte pitch) of a CUDA matrix of that shape with packed rows."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    rows, cols = shape
+    es = t.element_size()
+    if t.is_contiguous() or not t.numel():
+        return t.data_ptr(), cols * es
+    sr, sc = t.stride()
+    if (cols > 1 and sc != 1) or (rows > 1 and sr < cols):
+        raise ValueError(f"{name}: rows must be packed and must not overlap")
+    return t.data_ptr(), sr * es if rows > 1 else cols * es
+
+
+def _status_of(status, like):
+    if status is None:
+        return None
+    if status.dtype is not _torch.int32 or status.numel() != 1 or not status.is_cuda or \
+            status.get_device() != like.get_device():
+        raise ValueError("status: expected an int32 CUDA tensor of one element on the device of the others")
+    return status.data_ptr()
+
+
+def _linear_of(x, out, weight, act, names):
+    """rz_linear of an x (C channels) and an out (K), their maps and the weight's matrix."""
+    (N, H, W, C), mx = _map_of(x, names[0])
+    K = out.shape[-1] if out.dim() else 0
+    mo = _map_of(out, names[1], (N, H, W, K))[1]
+    if out.dtype is not x.dtype or weight.dtype is not x.dtype:
+        raise ValueError(f"{names[0]}, {names[1]} and weight differ in dtype")
+    return RzLinear(N, H, W, C, K, _map_dtype(x, names[0]), _int(act, "act")), mx, mo, *_matrix(weight, "weight", (K, C))
+
+
+def map_linear_workspace(x, y, weight, act: int = RZ_ACT_NONE) -> int:
+    """Bytes of workspace that map_linear needs for tensors like these."""
+    _with_torch()
+    d, mx, _, w, pitch = _linear_of(x, y, weight, act, ("x", "y"))
+    n = ctypes.c_size_t(0)
+    _check(_native.load().map_linear_workspace(d, mx, w, pitch, ctypes.byref(n)), "map_linear_workspace")
+    return n.value
+
+
+def map_linear(x, y, weight, bias=None, residual=None, pre=None, act: int = RZ_ACT_NONE, workspace=None, status=None,
+               stream=None) -> None:
+    """y[:] = act(x weight^T + bias) + residual on (N, H, W, C) or (H, W, C) maps.
+
+    weight: (K, C) of the maps' dtype, rows packed; bias: float32 (K,) or None;
+    residual: a map of y's shape (y itself among them) or None; pre: a map of y's
+    shape that takes x weight^T + bias for the gradient, or None; workspace: a
+    CUDA tensor of map_linear_workspace(x, y, weight, act) bytes, or None to take
+    one from torch's allocator; status: an int32 CUDA tensor of one element for
+    a kernel's time-out, or None."""
+    _with_torch()
+    d, mx, my, w, pitch = _linear_of(x, y, weight, act, ("x", "y"))
+    _on_current_device(x, y, weight, bias, residual, pre)
+    shape = (d.N, d.H, d.W, d.K)
+    mr, mp = (None if t is None else _map_of(t, n, shape)[1] for t, n in ((residual, "residual"), (pre, "pre")))
+    for t, n in ((residual, "residual"), (pre, "pre")):
+        if t is not None and t.dtype is not x.dtype:
+            raise ValueError(f"{n} and x differ in dtype")
+    b, st = _floats(bias, "bias", (d.K,)), _status_of(status, x)
+    lib = _native.load()
+
+    def query(_):
+        n = ctypes.c_size_t(0)
+        _check(lib.map_linear_workspace(d, mx, w, pitch, ctypes.byref(n)), "map_linear_workspace")
+        return n.value
+
+    _check(_with_workspace(lambda p, n, s: lib.map_linear(d, mx, w, pitch, b, mr, mp, my, p, n, st, s), workspace, query, d,
+                           x, stream), "map_linear")
+
+
+def map_linear_grad_workspace(dy, x, weight, act: int = RZ_ACT_NONE) -> int:
+    """Bytes of workspace that map_linear_grad needs for tensors like these."""
+    _with_torch()
+    d, mx, md, w, pitch = _linear_of(x, dy, weight, act, ("x", "dy"))
+    n = ctypes.c_size_t(0)
+    _check(_native.load().map_linear_grad_workspace(d, md, mx, w, pitch, ctypes.byref(n)), "map_linear_grad_workspace")
+    return n.value
+
+
+def map_linear_grad(dy, x, weight, dx=None, dweight=None, dbias=None, pre=None, act: int = RZ_ACT_NONE, workspace=None,
+                    status=None, stream=None) -> None:
+    """dx[:], dweight[:] and dbias[:] (each may be None) from dy, with the
+    arguments of the map_linear call and the pre it wrote (None without an
+    activation).  dweight: (K, C), of the maps' dtype or float32."""
+    _with_torch()
+    d, mx, md, w, pitch = _linear_of(x, dy, weight, act, ("x", "dy"))
+    _on_current_device(x, dy, weight, dx, dweight, dbias, pre)
+    mp = None if pre is None else _map_of(pre, "pre", (d.N, d.H, d.W, d.K))[1]
+    mo = None if dx is None else _map_of(dx, "dx", (d.N, d.H, d.W, d.C))[1]
+    for t, n in ((pre, "pre"), (dx, "dx")):
+        if t is not None and t.dtype is not x.dtype:
+            raise ValueError(f"{n} and x differ in dtype")
+    dw, dw_pitch, dw_type = None, 0, d.dtype
+    if dweight is not None:
+        dw_type = _map_dtype(dweight, "dweight")
+        dw, dw_pitch = _matrix(dweight, "dweight", (d.K, d.C))
+    b, st = _floats(dbias, "dbias", (d.K,)), _status_of(status, x)
+    lib = _native.load()
+
+    def query(_):
+        n = ctypes.c_size_t(0)
+        _check(lib.map_linear_grad_workspace(d, md, mx, w, pitch, ctypes.byref(n)), "map_linear_grad_workspace")
+        return n.value
+
+    _check(_with_workspace(lambda p, n, s: lib.map_linear_grad(d, md, mx, w, pitch, mp, mo, dw, dw_pitch, dw_type, b, p, n,
+                                                               st, s), workspace, query, d, x, stream), "map_linear_grad")
+
+
+def _qk_of(x, y, q_heads, k_heads, head_dim, base, row_pairs, col_pairs, scale, interleaved, eps, names):
+    """rz_qk of an x (C channels) and a y (out_C), and their maps."""
+    (N, H, W, C), mx = _map_of(x, names[0])
+    got, my = _map_of(y, names[1])
+    if got[:3] != (N, H, W):
+        raise ValueError(f"{names[1]}: shape {got}, expected {(N, H, W)} pixels")
+    if y.dtype is not x.dtype:
+        raise ValueError(f"{names[0]} and {names[1]} differ in dtype")
+    _int(head_dim, "head_dim")
+    if col_pairs is None:
+        col_pairs = head_dim // 2 - row_pairs
+    return RzQk(N, H, W, C, got[3], _int(q_heads, "q_heads"), _int(k_heads, "k_heads"), head_dim, _map_dtype(x, names[0]),
+                _int(row_pairs, "row_pairs"), _int(col_pairs, "col_pairs"), 1 if interleaved else 0, eps, base,
+                scale), mx, my
+
+
+def map_qk_norm(x, y, q_heads: int, k_heads: int, head_dim: int, gamma_q=None, gamma_k=None, positions=None,
+                base: float = 10000.0, row_pairs: int = 0, col_pairs=None, scale: float = 1.0, interleaved: bool = False,
+                eps: float = 1e-6, stream=None) -> None:
+    """y[:] = the root-mean-square norm of every query and key head of x, turned
+    by its token's position.
+
+    x: an (N, H, W, C) or (H, W, C) map whose pixels hold q_heads query heads,
+    k_heads key heads of head_dim channels, and whatever follows them, which
+    stays; y: the same pixels with at least the heads' channels (x itself among
+    others).  gamma_q, gamma_k: float32 (head_dim,) or None; positions: int32
+    (N, H, W, 2), the row and column of every token, or None for its place in
+    the map; the first row_pairs pairs turn with the row, the next col_pairs
+    (None: all others) with the column, pair j by scale * base ** (-j / pairs) a
+    step; interleaved: neighbours are pairs, else the halves of a head."""
+    _with_torch()
+    d, mx, my = _qk_of(x, y, q_heads, k_heads, head_dim, base, row_pairs, col_pairs, scale, interleaved, eps, ("x", "y"))
+    _on_current_device(x, y, gamma_q, gamma_k, positions)
+    gq, gk = _floats(gamma_q, "gamma_q", (head_dim,)), _floats(gamma_k, "gamma_k", (head_dim,))
+    at = _ints(positions, "positions", (d.N, d.H, d.W, 2))
+    _check(_native.load().map_qk_norm(d, mx, my, gq, gk, at, _stream_at(stream, x)), "map_qk_norm")
+
+
+def _qk_workspace(d) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_native.load().map_qk_norm_grad_workspace(d, ctypes.byref(n)), "map_qk_norm_grad_workspace")
+    return n.value
+
+
+def map_qk_norm_grad_workspace(dy, x, q_heads: int, k_heads: int, head_dim: int) -> int:
+    """Bytes of workspace that map_qk_norm_grad needs for these maps."""
+    _with_torch()
+    return _qk_workspace(_qk_of(x, dy, q_heads, k_heads, head_dim, 1.0, 0, 0, 1.0, False, 0.0, ("x", "dy"))[0])
+
+
+def map_qk_norm_grad(dy, x, dx, q_heads: int, k_heads: int, head_dim: int, gamma_q=None, gamma_k=None, dgamma_q=None,
+                     dgamma_k=None, positions=None, base: float = 10000.0, row_pairs: int = 0, col_pairs=None,
+                     scale: float = 1.0, interleaved: bool = False, eps: float = 1e-6, workspace=None, stream=None) -> None:
+    """dx[:], dgamma_q[:] and dgamma_k[:] (either may be None) from dy, with the
+    arguments of the map_qk_norm call.  dx: the shape of x, its channels after
+    the heads left as they are; it may be dy."""
+    _with_torch()
+    d, mx, md = _qk_of(x, dy, q_heads, k_heads, head_dim, base, row_pairs, col_pairs, scale, interleaved, eps, ("x", "dy"))
+    _on_current_device(x, dy, dx, gamma_q, gamma_k, dgamma_q, dgamma_k, positions)
+    mo = _map_of(dx, "dx", (d.N, d.H, d.W, d.C))[1]
+    if dx.dtype is not x.dtype:
+        raise ValueError("x and dx differ in dtype")
+    shape = (head_dim,)
+    gq, gk = _floats(gamma_q, "gamma_q", shape), _floats(gamma_k, "gamma_k", shape)
+    dq, dk = _floats(dgamma_q, "dgamma_q", shape), _floats(dgamma_k, "dgamma_k", shape)
+    at = _ints(positions, "positions", (d.N, d.H, d.W, 2))
+    f = _native.load().map_qk_norm_grad
+    _check(_with_workspace(lambda w, n, st: f(d, md, mx, mo, gq, gk, at, dq, dk, w, n, st), workspace, _qk_workspace, d, x,
+                           stream), "map_qk_norm_grad")
+
+
+def _matrices(t, name: str, heads: int, queries: int, keys: int):
+    """(N, rz_map) of (N, heads, queries, keys) or (heads, queries, keys) matrices with packed rows, the heads of the
+    batch at one distance from each other."""
+    dims = t.dim()
+    got = (1, *t.shape) if dims == 3 else tuple(t.shape)
+    if dims not in (3, 4) or got[1:] != (heads, queries, keys):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (N, {heads}, {queries}, {keys})")
+    if max(got) > _INT_MAX:
+        raise ValueError(f"{name}: shape {got} past 2^31 - 1")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    es, N = t.element_size(), got[0]
+    if t.is_contiguous():
+        return N, RzMap(t.data_ptr(), keys * es, queries * keys * es)
+    sn, sh, sq, sk = t.stride() if dims == 4 else (0, *t.stride())
+    if heads == 1:
+        sh = sn
+    if t.numel() and ((keys > 1 and sk != 1) or (N > 1 and heads > 1 and sn != heads * sh)):
+        raise ValueError(f"{name}: keys must be packed, and the heads of the batch evenly apart")
+    return N, RzMap(t.data_ptr(), sq * es if queries > 1 else keys * es, sh * es if N * heads > 1 else 0)
+
+
+def _bias_of(rows, cols, matrices, name, table, table_name, query, key):
+    """rz_bias with the matrices' map and the buckets' and table's pointers."""
+    (qh, qw), (kh, kw) = query, key
+    for v in (qh, qw, kh, kw):
+        _int(v, "query or key grid")
+    if table.dim() != 3:
+        raise ValueError(f"{table_name}: expected (row buckets, column buckets, heads), got {tuple(table.shape)}")
+    br, bc, heads = table.shape
+    for v in (br, bc, heads):
+        _int(v, table_name)
+    N, m = _matrices(matrices, name, heads, qh * qw, kh * kw)
+    d = RzBias(N, heads, qh, qw, kh, kw, br, bc, _map_dtype(matrices, name))
+    pr, pc = _ints(rows, "rows", (max(0, qh + kh - 1),)), _ints(cols, "cols", (max(0, qw + kw - 1),))
+    return d, m, pr, pc, _floats(table, table_name, (br, bc, heads))
+
+
+def map_position_bias(table, rows, cols, out, query, key, scores=None, stream=None) -> None:
+    """out[:] = scores + the position bias of every query and key, or the bias alone.
+
+    table: float32 (row buckets, column buckets, heads); rows, cols: int32, the
+    buckets of the offsets of rows and of columns (map_position_buckets); query,
+    key: the grids (height, width); out and scores: (N, heads, queries, keys) or
+    (heads, queries, keys), tokens numbered row by row, rows padded or not; out
+    may be scores."""
+    _with_torch()
+    d, mo, pr, pc, t = _bias_of(rows, cols, out, "out", table, "table", query, key)
+    _on_current_device(out, table, rows, cols, scores)
+    ms = None
+    if scores is not None:
+        if scores.dtype is not out.dtype or scores.shape != out.shape:
+            raise ValueError("scores and out differ in dtype or shape")
+        ms = _matrices(scores, "scores", d.heads, d.q_h * d.q_w, d.k_h * d.k_w)[1]
+    _check(_native.load().map_position_bias(d, t, pr, pc, ms, mo, _stream_at(stream, out)), "map_position_bias")
+
+
+def _bias_workspace(d) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_native.load().map_position_bias_grad_workspace(d, ctypes.byref(n)), "map_position_bias_grad_workspace")
+    return n.value
+
+
+def map_position_bias_grad_workspace(dout, dtable, query, key) -> int:
+    """Bytes of workspace that map_position_bias_grad needs for these tensors."""
+    _with_torch()
+    return _bias_workspace(_bias_of(None, None, dout, "dout", dtable, "dtable", query, key)[0])
+
+
+def map_position_bias_grad(dout, rows, cols, dtable, query, key, workspace=None, stream=None) -> None:
+    """dtable[:] = the gradient of map_position_bias towards its table, summed over the batch."""
+    _with_torch()
+    d, md, pr, pc, t = _bias_of(rows, cols, dout, "dout", dtable, "dtable", query, key)
+    _on_current_device(dout, dtable, rows, cols)
+    f = _native.load().map_position_bias_grad
+    _check(_with_workspace(lambda w, n, st: f(d, md, pr, pc, t, w, n, st), workspace, _bias_workspace, d, dout, stream),
+           "map_position_bias_grad")
+
+
+def map_position_buckets(queries: int, keys: int, exact: int, side: int, reach: int, shift: int = 0):
+    """Buckets of an axis for map_position_bias, an int32 numpy array of queries +
+    keys - 1: entry i is that of the offset i - (queries - 1) - shift, from 0 to
+    2 side - 2.  Offsets below `exact` have a bucket each, those up to `reach`
+    share the rest of `side` in steps that grow as a power."""
+    import numpy as np
+    if queries < 1 or keys < 1 or max(queries, keys) > RZ_MAX_DIM:
+        raise ValueError(f"queries and keys must be 1 to {RZ_MAX_DIM}")
+    for v, name in ((exact, "exact"), (side, "side"), (reach, "reach"), (shift, "shift")):
+        _int(v, name)
+    out = np.zeros(queries + keys - 1, np.int32)
+    _check(_native.load().map_position_buckets(queries, keys, shift, exact, side, reach, out.ctypes.data),
+           "map_position_buckets")
+    return out
 
 
 class Texture:

@@ -140,10 +140,59 @@ class RzResample(ctypes.Structure):
     ]
 
 
+class RzLinear(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("W", ctypes.c_int),
+        ("C", ctypes.c_int),
+        ("K", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("act", ctypes.c_int),
+    ]
+
+
+class RzQk(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("W", ctypes.c_int),
+        ("C", ctypes.c_int),
+        ("out_C", ctypes.c_int),
+        ("q_heads", ctypes.c_int),
+        ("k_heads", ctypes.c_int),
+        ("D", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("row_pairs", ctypes.c_int),
+        ("col_pairs", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("base", ctypes.c_double),
+        ("scale", ctypes.c_double),
+    ]
+
+
+class RzBias(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int),
+        ("heads", ctypes.c_int),
+        ("q_h", ctypes.c_int),
+        ("q_w", ctypes.c_int),
+        ("k_h", ctypes.c_int),
+        ("k_w", ctypes.c_int),
+        ("row_buckets", ctypes.c_int),
+        ("col_buckets", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+    ]
+
+
 _map = ctypes.POINTER(RzMap)
 _drop = ctypes.POINTER(RzDrop)
 _norm = ctypes.POINTER(RzNorm)
 _resample = ctypes.POINTER(RzResample)
+_linear = ctypes.POINTER(RzLinear)
+_qk = ctypes.POINTER(RzQk)
+_bias = ctypes.POINTER(RzBias)
 
 # name -> (restype, argtypes); every symbol include/gbresize.h declares
 SIGNATURES = {
@@ -180,6 +229,17 @@ SIGNATURES = {
     "resize_map": (_i, [_resample, _map, _map, _map, _p]),
     "resize_map_grad_workspace": (_i, [_resample, ctypes.POINTER(_sz)]),
     "resize_map_grad": (_i, [_resample, _map, _map, _p, _sz, _p]),
+    "map_linear_workspace": (_i, [_linear, _map, _p, _sz, ctypes.POINTER(_sz)]),
+    "map_linear": (_i, [_linear, _map, _p, _sz, _p, _map, _map, _map, _p, _sz, _p, _p]),
+    "map_linear_grad_workspace": (_i, [_linear, _map, _map, _p, _sz, ctypes.POINTER(_sz)]),
+    "map_linear_grad": (_i, [_linear, _map, _map, _p, _sz, _map, _map, _p, _sz, _i, _p, _p, _sz, _p, _p]),
+    "map_qk_norm": (_i, [_qk, _map, _map, _p, _p, _p, _p]),
+    "map_qk_norm_grad_workspace": (_i, [_qk, ctypes.POINTER(_sz)]),
+    "map_qk_norm_grad": (_i, [_qk, _map, _map, _map, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "map_position_bias": (_i, [_bias, _p, _p, _p, _map, _map, _p]),
+    "map_position_bias_grad_workspace": (_i, [_bias, ctypes.POINTER(_sz)]),
+    "map_position_bias_grad": (_i, [_bias, _map, _p, _p, _p, _p, _sz, _p]),
+    "map_position_buckets": (_i, [_i, _i, _i, _i, _i, _i, _p]),
 }
 
 _lib = None

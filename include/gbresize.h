@@ -550,6 +550,163 @@ RZ_API int resize_map_grad_workspace(const rz_resample *d, size_t *bytes);
 RZ_API int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_map *dsrc, void *workspace,
                            size_t workspace_bytes, void *stream);
 
+/*
+ * ---- Attention over a map's tokens -------------------------------------------
+ *
+ * The operators that an attention block puts around its products, on the same
+ * maps and under the same rules: one pixel is one token.
+ */
+
+/*
+ * Linear layer of a map (a 1 x 1 convolution): for every pixel
+ *   z = x W^T + b,   y = act(z) + residual,
+ * W the weight (K rows of C packed elements of the map's dtype, weight_pitch
+ * bytes apart), b float[K] or NULL, act as in map_group_norm, residual a map
+ * of y's shape or NULL.  pre: a map of y's shape that takes z, rounded, for the
+ * gradient, or NULL.  x: C channels; y, residual and pre: K.  Products are
+ * summed in float32; the result is rounded once.
+ * y may be the residual itself, and overlaps no other map; weight and b lie
+ * apart from y and pre.  K, C in [1, RZ_MAX_DIM], N * H * W < 2^31 (else
+ * RZ_ERR_UNSUPPORTED).
+ *
+ * workspace: device memory of at least the bytes that map_linear_workspace
+ * gives for maps like these (of x and weight their alignment, pitch and stride
+ * matter; the data is not touched), 16-byte aligned, of any content, the call's
+ * own until the stream has passed it.  status: a device int or NULL; a kernel
+ * whose bounded waits (1 s) run out writes RZ_ERR_TIMEOUT there and leaves the
+ * result unfinished.  Asynchronous on `stream`; no allocation.  An empty map is
+ * RZ_OK.
+ */
+typedef struct {
+    int N, H, W, C, K;
+    int dtype;
+    int act;
+} rz_linear;
+RZ_API int map_linear_workspace(const rz_linear *d, const rz_map *x, const void *weight, size_t weight_pitch,
+                                size_t *bytes);
+RZ_API int map_linear(const rz_linear *d, const rz_map *x, const void *weight, size_t weight_pitch, const float *bias,
+                      const rz_map *residual, const rz_map *pre, const rz_map *y, void *workspace,
+                      size_t workspace_bytes, int *status, void *stream);
+
+/*
+ * The gradient of map_linear from dy, the call's x and weight, and the pre that
+ * it wrote (NULL only for RZ_ACT_NONE):
+ *   dz = dy act'(pre),  dx = dz W,  dweight = dz^T x,  dbias = sum dz
+ * (pixels).  The one towards the residual is dy itself.  dx is a map like x,
+ * dweight K rows of C elements of dweight_dtype (the map's dtype or RZ_F32),
+ * dweight_pitch bytes apart, dbias device float[K]; each may be NULL, is written,
+ * not added to, and overlaps no input; an empty map makes dweight and dbias 0.
+ * Sums run in a fixed order.  Workspace, status and the rest as map_linear.
+ */
+RZ_API int map_linear_grad_workspace(const rz_linear *d, const rz_map *dy, const rz_map *x, const void *weight,
+                                     size_t weight_pitch, size_t *bytes);
+RZ_API int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x, const void *weight,
+                           size_t weight_pitch, const rz_map *pre, const rz_map *dx, void *dweight,
+                           size_t dweight_pitch, int dweight_dtype, float *dbias, void *workspace,
+                           size_t workspace_bytes, int *status, void *stream);
+
+/*
+ * Norm of queries and keys with the position rotation.  x holds, for each
+ * pixel, q_heads query heads and then k_heads key heads of D channels; the
+ * channels after them (values) are neither read nor written.  With g the
+ * query heads' or key heads' gamma (device float[D], NULL for 1), a head v is
+ *   u = v g / sqrt(sum v^2 / D + eps),
+ * and pair j < row_pairs + col_pairs of u is turned by an angle:
+ *   (a, b) -> (a cos - b sin, a sin + b cos),
+ *   angle = row scale base^(-j / row_pairs)                    j < row_pairs,
+ *   angle = col scale base^(-(j - row_pairs) / col_pairs)      after them;
+ * further pairs stay.  Pair j is (u[j], u[j + D / 2]), or (u[2j], u[2j + 1])
+ * where `interleaved` is set.  (row, col) is the pixel's place in its image, or
+ * positions[n][h][w] (device int[N][H][W][2]) where that is given; any int.
+ * Angles are reduced to a turn exactly, in 64-bit integers, whatever the
+ * position: they are off by 2^-24 of half a turn at most, their cosines and
+ * sines by 3e-7.
+ * x has C channels, y has out_C, either at least (q_heads + k_heads) D.
+ * D even, 2 <= D <= 256; one head at least; eps >= 0, base > 0 and scale
+ * finite; row_pairs + col_pairs <= D / 2.  A head of zeros gives zeros where
+ * eps > 0.  y may be x itself, and must not overlap it otherwise.
+ * Asynchronous on `stream`; no allocation.  An empty map is RZ_OK.
+ */
+typedef struct {
+    int N, H, W;
+    int C, out_C;
+    int q_heads, k_heads, D;
+    int dtype;
+    int row_pairs, col_pairs, interleaved;
+    float eps;
+    double base, scale;
+} rz_qk;
+RZ_API int map_qk_norm(const rz_qk *d, const rz_map *x, const rz_map *y, const float *gamma_q, const float *gamma_k,
+                       const int *positions, void *stream);
+
+/*
+ * The gradient of map_qk_norm from dy (out_C channels), the call's x, gammas and
+ * positions: with du = dy turned back, r = 1 / sqrt(sum v^2 / D + eps), h = v r,
+ *   dgamma[c] = sum du h over pixels and heads,   t = gamma du,
+ *   dx = r (t - h sum(t h) / D).
+ * dx has C channels; the ones after the heads are left as they are.  dgamma_q
+ * and dgamma_k (device float[D], either may be NULL) are written, not added to;
+ * an empty map, or no head of the kind, makes them 0.  dx may be dy itself, and
+ * overlaps neither dy otherwise nor x.  Sums run in a fixed order.
+ * workspace: device memory of at least the bytes map_qk_norm_grad_workspace
+ * gives, 16-byte aligned, of any content, the call's own until the stream has
+ * passed it.
+ */
+RZ_API int map_qk_norm_grad_workspace(const rz_qk *d, size_t *bytes);
+RZ_API int map_qk_norm_grad(const rz_qk *d, const rz_map *dy, const rz_map *x, const rz_map *dx, const float *gamma_q,
+                            const float *gamma_k, const int *positions, float *dgamma_q, float *dgamma_k,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Learned relative position bias by buckets.  Queries lie on a grid of q_h x q_w
+ * and keys on one of k_h x k_w, numbered row by row; table is device
+ * float[row_buckets][col_buckets][heads]; rows (device int[q_h + k_h - 1]) and
+ * cols (device int[q_w + k_w - 1]) give the bucket of each offset of an axis:
+ * entry i is that of key - query = i - (q - 1).
+ *   out[n][a][q][k] = scores[n][a][q][k] + table[rows(q, k)][cols(q, k)][a],
+ * or the table's value alone where scores is NULL.  A pair with a bucket outside
+ * the table has bias 0.  The sum is float32 and rounded once; -infinity in a
+ * masked place stays.
+ * The maps are matrices: batch n, head a is image n * heads + a, query q its row
+ * q, with k_h * k_w packed elements (pitch: bytes between queries, stride: bytes
+ * between heads).  N * heads <= 2^24, at most RZ_MAX_DIM keys and as many
+ * queries, at most 2^22 buckets.  out may be scores itself, and must not
+ * overlap it otherwise.  Asynchronous on `stream`; no allocation.  An empty
+ * result is RZ_OK.
+ */
+typedef struct {
+    int N, heads;
+    int q_h, q_w, k_h, k_w;
+    int row_buckets, col_buckets;
+    int dtype;
+} rz_bias;
+RZ_API int map_position_bias(const rz_bias *d, const float *table, const int *rows, const int *cols,
+                             const rz_map *scores, const rz_map *out, void *stream);
+
+/*
+ * The gradient of map_position_bias towards its table from dout: dtable[r][c][a]
+ * = the sum of dout[n][a][q][k] over the batch and the pairs of bucket (r, c),
+ * written, not added to; 0 where there is none.  (The one towards scores is
+ * dout itself.)  Sums run in a fixed order.  Workspace as above.
+ */
+RZ_API int map_position_bias_grad_workspace(const rz_bias *d, size_t *bytes);
+RZ_API int map_position_bias_grad(const rz_bias *d, const rz_map *dout, const int *rows, const int *cols,
+                                  float *dtable, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Host only: the buckets of one axis, out[queries + keys - 1], for the two calls
+ * above.  The offset of entry i is d = i - (queries - 1) - shift (shift: the
+ * place of query 0 among the keys).  With m = |d|, its bucket is
+ * side - 1 + b (d > 0) or side - 1 - b (d < 0), where b = m for m < exact, and
+ *   b = min(side - 1, exact + floor((side - exact) log(m / exact) / log(reach / exact)))
+ * from there on: offsets below `exact` have a bucket each, those up to `reach`
+ * share side - exact of them in steps that grow as a power; there are
+ * 2 side - 1 buckets.  Borders are exact: they are compared in integers where
+ * float64 could not tell.  1 <= exact <= side <= 1024, reach > exact;
+ * queries, keys in [1, RZ_MAX_DIM]; |shift| and reach at most RZ_MAX_DIM.
+ */
+RZ_API int map_position_buckets(int queries, int keys, int shift, int exact, int side, int reach, int *out);
+
 /* Human-readable name of a status code (static string). */
 RZ_API const char *resize_strerror(int code);
 

@@ -1,0 +1,284 @@
+"""Linear layer of a map with bias, activation and residual, and its gradient,
+against the 64-bit forms."""
+import numpy as np
+import pytest
+
+import map_reference as ref
+import token_reference as tok
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+ACTS = {"none": 0, "silu": 1, "gelu": 2}
+TYPES = ["f32", "bf16", "f16"]
+
+
+@pytest.fixture(scope="module")
+def rz():
+    import __graft_entry__
+    __graft_entry__.build()
+    import bilinear_image_resize_gb300 as m
+    torch.cuda.set_device(0)
+    return m
+
+
+def values(shape, dtype, seed, scale=1.0):
+    return tok.rounded(np.random.default_rng(seed).normal(size=shape) * scale, dtype)
+
+
+def matrix(a, dtype, pad=0, offset=0, fill=0.0):
+    """A matrix with `pad` elements after each row, from element `offset` of a flat buffer."""
+    rows, cols = a.shape
+    flat = torch.full((offset + rows * (cols + pad) + 64,), fill, dtype=getattr(torch, tok.TORCH[dtype]), device="cuda")
+    view = torch.as_strided(flat, (rows, cols), (cols + pad, 1), offset)
+    view.copy_(torch.from_numpy(np.ascontiguousarray(a)).to(view.dtype))
+    return view, flat
+
+
+def check(got, want, bound, what):
+    err = np.abs(ref.host(got) - want)
+    assert np.all(err <= bound), (what, float((err / np.maximum(bound, 1e-300)).max()))
+
+
+def forward(rz, shape, K, dtype, kind, bias=True, residual=False, pre=False, layout={}, pad=0, offset=0, seed=1, in_place=False,
+            **kw):
+    C = shape[3]
+    x, w = values(shape, dtype, seed), values((K, C), dtype, seed + 1, C ** -0.5)
+    b = values(K, "f32", seed + 2, 0.3) if bias else None
+    r = values((*shape[:3], K), dtype, seed + 3) if residual else None
+    xv, _ = ref.device_map(x, dtype, **layout)
+    wv, _ = matrix(w, dtype, pad, offset)
+    yv, flat = ref.device_map(np.zeros((*shape[:3], K)) if not in_place else r, dtype, fill=-3.0, **layout)
+    rv = None if r is None else yv if in_place else ref.device_map(r, dtype, **layout)[0]
+    pv, pflat = ref.device_map(np.zeros((*shape[:3], K)), dtype, fill=-3.0, **layout) if pre else (None, None)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rz.map_linear(xv, yv, wv, None if b is None else torch.from_numpy(b).float().cuda(), residual=rv, pre=pv, act=ACTS[kind],
+                  status=status, **kw)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    ty, tz = tok.linear_bounds(x, w, b, kind, r, dtype)
+    want, z = tok.linear(x, w, b, kind, r)
+    check(yv, want, ty, "y")
+    assert ref.outside_untouched(flat, yv, -3.0)
+    if pre:
+        check(pv, z, tz, "pre")
+        assert ref.outside_untouched(pflat, pv, -3.0)
+    return yv
+
+
+def gradient(rz, shape, K, dtype, kind, layout={}, pad=0, offset=0, seed=11, wdtype=None, parts="xwb", **kw):
+    C = shape[3]
+    wdtype = wdtype or dtype
+    x, w = values(shape, dtype, seed), values((K, C), dtype, seed + 1, C ** -0.5)
+    dy, pre = values((*shape[:3], K), dtype, seed + 2), values((*shape[:3], K), dtype, seed + 3, 1.5)
+    xv, dv, pv = (ref.device_map(a, dtype, **layout)[0] for a in (x, dy, pre))
+    wv, _ = matrix(w, dtype, pad, offset)
+    ov, oflat = ref.device_map(np.zeros(shape), dtype, fill=-3.0, **layout)
+    gv, gflat = matrix(np.zeros((K, C)), wdtype, pad, offset, -3.0)
+    gv.fill_(7.0)
+    db = torch.full((K,), 9.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rz.map_linear_grad(dv, xv, wv, ov if "x" in parts else None, gv if "w" in parts else None, db if "b" in parts else None,
+                       pre=None if kind == "none" else pv, act=ACTS[kind], status=status, **kw)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    dx, dw, dbias, _ = tok.linear_grad(dy, x, w, pre, kind)
+    tx, tw, tb = tok.linear_grad_bounds(dy, x, w, pre, kind, dtype, wdtype)
+    if "x" in parts:
+        check(ov, dx, tx, "dx")
+    if "w" in parts:
+        check(gv, dw, tw, "dweight")
+    if "b" in parts:
+        check(db, dbias, tb, "dbias")
+    assert ref.outside_untouched(oflat, ov, -3.0) and ref.outside_untouched(gflat, gv, -3.0)
+    return ov, gv, db
+
+
+# (N, H, W, C), K: one value; one pixel; widths of one; widths that fill no vector, no tile; tiles just filled and just passed
+SHAPES = [((1, 1, 1, 1), 1), ((1, 1, 1, 640), 96), ((1, 1, 1, 37), 5), ((2, 1, 1, 256), 130), ((7, 1, 1, 512), 64),
+          ((9, 1, 1, 72), 1000), ((2, 3, 5, 1), 7), ((2, 3, 5, 9), 1), ((1, 8, 16, 64), 64), ((1, 9, 15, 65), 63),
+          ((3, 13, 11, 96), 250), ((2, 16, 16, 128), 256), ((1, 17, 31, 200), 322), ((1, 1, 130, 264), 520),
+          ((1, 40, 33, 16), 24), ((1, 1, 300, 1030), 8)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape, K", SHAPES)
+def test_forward(rz, shape, K, dtype):
+    forward(rz, shape, K, dtype, "gelu", residual=True, pre=True)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape, K", SHAPES)
+def test_gradient(rz, shape, K, dtype):
+    gradient(rz, shape, K, dtype, "silu")
+
+
+@pytest.mark.parametrize("kind", list(ACTS))
+@pytest.mark.parametrize("bias, residual, pre", [(True, False, False), (False, True, False), (False, False, True)])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape, K", [((2, 9, 15, 72), 136), ((3, 1, 1, 72), 136), ((2, 9, 15, 21), 33)])
+def test_epilogues(rz, kind, bias, residual, pre, dtype, shape, K):
+    forward(rz, shape, K, dtype, kind, bias, residual, pre)
+
+
+@pytest.mark.parametrize("kind", list(ACTS))
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape, K", [((2, 9, 15, 72), 136), ((3, 1, 1, 72), 136), ((2, 9, 15, 21), 33)])
+def test_slopes(rz, kind, dtype, shape, K):
+    gradient(rz, shape, K, dtype, kind)
+
+
+@pytest.mark.parametrize("parts", ["x", "w", "b", "xw", "wb", "xb"])
+@pytest.mark.parametrize("kind", ["none", "gelu"])
+def test_parts_of_the_gradient(rz, parts, kind):
+    gradient(rz, (2, 9, 15, 72), 136, "bf16", kind, parts=parts)
+
+
+# padded rows, gaps between images, starts that no vector is aligned to
+LAYOUTS = [dict(pad=16), dict(gap=64), dict(pad=8, gap=24), dict(offset=1), dict(pad=4, offset=4), dict(pad=1)]
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("K", [64, 50])
+def test_layouts(rz, layout, dtype, K):
+    forward(rz, (2, 11, 13, 32), K, dtype, "silu", residual=True, pre=True, layout=layout)
+    gradient(rz, (2, 11, 13, 32), K, dtype, "gelu", layout)
+
+
+@pytest.mark.parametrize("pad, offset", [(8, 0), (0, 1), (3, 2), (8, 8)])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", [(2, 11, 13, 40), (1, 1, 2, 40)])
+def test_weights_with_padding(rz, pad, offset, dtype, shape):
+    forward(rz, shape, 56, dtype, "none", pad=pad, offset=offset)
+    gradient(rz, shape, 56, dtype, "none", pad=pad, offset=offset)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("kind", ["none", "silu"])
+def test_weight_gradient_in_float32(rz, dtype, kind):
+    gradient(rz, (2, 9, 15, 72), 136, dtype, kind, wdtype="f32")
+
+
+@pytest.mark.parametrize("shape, K", [((2, 9, 15, 72), 136), ((4, 1, 1, 72), 136)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_residual_in_place(rz, shape, K, dtype):
+    forward(rz, shape, K, dtype, "none", residual=True, in_place=True)
+
+
+# sums over many pixels, many terms, and more tiles than there are processors
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape, K", [((1, 64, 160, 24), 40), ((1, 5, 50, 4096), 72), ((2, 96, 100, 136), 328)])
+def test_larger(rz, shape, K, dtype):
+    forward(rz, shape, K, dtype, "silu", residual=True, pre=True)
+    gradient(rz, shape, K, dtype, "gelu")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape, K", [((2, 9, 15, 72), 136), ((1, 40, 50, 200), 72), ((3, 1, 1, 512), 136)])
+def test_same_bits_every_time(rz, shape, K, dtype):
+    a = forward(rz, shape, K, dtype, "gelu").clone()
+    g = [t.clone() for t in gradient(rz, shape, K, dtype, "gelu")]
+    for _ in range(3):
+        assert torch.equal(a, forward(rz, shape, K, dtype, "gelu"))
+        assert all(torch.equal(u, v) for u, v in zip(g, gradient(rz, shape, K, dtype, "gelu")))
+
+
+@pytest.mark.parametrize("shape, K", [((2, 9, 15, 72), 136), ((1, 40, 50, 200), 72), ((3, 1, 1, 512), 136)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_other_stream_and_given_workspace(rz, shape, K, dtype):
+    x = torch.zeros(shape, dtype=getattr(torch, tok.TORCH[dtype]), device="cuda")
+    y = torch.zeros((*shape[:3], K), dtype=x.dtype, device="cuda")
+    w = torch.zeros((K, shape[3]), dtype=x.dtype, device="cuda")
+    n = max(rz.map_linear_workspace(x, y, w, act=1), rz.map_linear_grad_workspace(y, x, w, act=1))
+    work = torch.full((n + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        forward(rz, shape, K, dtype, "silu", workspace=work[:n], stream=s)
+        gradient(rz, shape, K, dtype, "silu", workspace=work[:n], stream=s)
+    assert bool((work[n:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("shape, K", [((2, 9, 15, 72), 136), ((1, 40, 50, 200), 72), ((3, 1, 1, 512), 136)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_and_replayed(rz, shape, K, dtype):
+    C = shape[3]
+    t = getattr(torch, tok.TORCH[dtype])
+    x, dy, pre = (torch.zeros(s, dtype=t, device="cuda") for s in (shape, (*shape[:3], K), (*shape[:3], K)))
+    w, y, dx = torch.zeros((K, C), dtype=t, device="cuda"), torch.zeros_like(dy), torch.zeros_like(x)
+    dw, db = torch.zeros_like(w), torch.zeros(K, device="cuda")
+    fw = torch.empty(max(16, rz.map_linear_workspace(x, y, w, act=2)), dtype=torch.uint8, device="cuda")
+    gw = torch.empty(max(16, rz.map_linear_grad_workspace(dy, x, w, act=2)), dtype=torch.uint8, device="cuda")
+
+    def step():
+        rz.map_linear(x, y, w, pre=pre, act=2, workspace=fw)
+        rz.map_linear_grad(dy, x, w, dx, dw, db, pre=pre, act=2, workspace=gw)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed in (1, 2):
+        vx, vw, vd = values(shape, dtype, seed), values((K, C), dtype, seed + 5, C ** -0.5), values((*shape[:3], K), dtype, seed + 7)
+        for a, v in ((x, vx), (w, vw), (dy, vd)):
+            a.copy_(torch.from_numpy(v).to(t))
+        g.replay()
+        torch.cuda.synchronize()
+        check(y, tok.linear(vx, vw, None, "gelu")[0], tok.linear_bounds(vx, vw, None, "gelu", None, dtype)[0], "y")
+        p = ref.host(pre)
+        want = tok.linear_grad(vd, vx, vw, p, "gelu")
+        for a, v, b, name in zip((dx, dw, db), want, tok.linear_grad_bounds(vd, vx, vw, p, "gelu", dtype, dtype), ("dx", "dw", "db")):
+            check(a, v, b, name)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_values_that_are_not_finite_stay_in_their_rows(rz, dtype):
+    shape, K = (1, 9, 17, 72), 136
+    x, w = values(shape, dtype, 3), values((K, 72), dtype, 4, 0.1)
+    xv, wv = (torch.from_numpy(a).to(getattr(torch, tok.TORCH[dtype])).cuda() for a in (x, w))
+    xv[0, 2, 3, 7] = float("nan")
+    xv[0, 5, 1, 0] = float("inf")
+    y = torch.empty((1, 9, 17, K), dtype=xv.dtype, device="cuda")
+    rz.map_linear(xv, y, wv)
+    bad = torch.zeros((1, 9, 17), dtype=torch.bool)
+    bad[0, 2, 3] = bad[0, 5, 1] = True
+    assert not bool(torch.isfinite(y.cpu()[bad]).any())
+    assert bool(torch.isfinite(y.cpu()[~bad]).all())
+
+
+def test_empty_maps(rz):
+    for shape in ((0, 3, 3, 16), (2, 0, 3, 16), (2, 3, 0, 16)):
+        x, y = torch.empty(shape, device="cuda"), torch.empty((*shape[:3], 24), device="cuda")
+        w, dw, db = torch.ones((24, 16), device="cuda"), torch.full((24, 16), 5.0, device="cuda"), torch.full((24,), 5.0, device="cuda")
+        rz.map_linear(x, y, w)
+        rz.map_linear_grad(y, x, w, torch.empty_like(x), dw, db)
+        assert float(dw.abs().max()) == 0 and float(db.abs().max()) == 0
+
+
+@pytest.mark.parametrize("kind", list(ACTS))
+def test_gradient_against_differences(rz, kind):
+    """d(sum of dy y) along random directions, by central differences of the float32 forward, in float64."""
+    shape, K, h = (2, 5, 7, 24), 40, 2.0 ** -6
+    x, w, b, dy = (values(s, "f32", i) for i, s in enumerate((shape, (K, 24), (K,), (*shape[:3], K))))
+    gpu = lambda a: torch.from_numpy(a).float().cuda()    # noqa: E731
+    y, pre = torch.empty((*shape[:3], K), device="cuda"), torch.empty((*shape[:3], K), device="cuda")
+    dx, dw, db = torch.empty(shape, device="cuda"), torch.empty((K, 24), device="cuda"), torch.empty(K, device="cuda")
+    rz.map_linear(gpu(x), y, gpu(w), gpu(b), pre=pre, act=ACTS[kind])
+    rz.map_linear_grad(gpu(dy), gpu(x), gpu(w), dx, dw, db, pre=pre, act=ACTS[kind])
+    rng = np.random.default_rng(7)
+    for k, (v, g) in enumerate(((x, dx), (w, dw), (b, db))):
+        d = rng.normal(size=v.shape)
+        d /= np.linalg.norm(d)
+        sums = []
+        for s in (1, -1):
+            a = [x, w, b]
+            a[k] = tok.rounded(v + s * h * d, "f32")
+            rz.map_linear(gpu(a[0]), y, gpu(a[1]), gpu(a[2]), act=ACTS[kind])
+            sums.append(float((ref.host(y) * dy).sum()))
+        slope = (sums[0] - sums[1]) / (2 * h)
+        # float32 forwards: 88 U of each |y| before the division by 2 h, random over the sum's n terms (six deviations); the
+        # third derivative's h^2 / 6 of a smooth sum: 1e-3 of its size
+        noise = 6 * 88 * 2.0 ** -24 * np.linalg.norm(ref.host(y) * dy) / h + 1e-3 * np.linalg.norm(ref.host(g))
+        assert abs(slope - float((ref.host(g) * d).sum())) <= noise
