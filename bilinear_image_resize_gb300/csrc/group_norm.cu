@@ -148,7 +148,7 @@ int gn_status(cudaError_t e)
 
 namespace rz {
 
-cudaError_t maps::shared_opt_in(const void *fn)
+cudaError_t maps::shared_opt_in(const void *fn, int bytes)
 {
     static std::mutex mu;
     static std::vector<std::pair<int, const void *>> ready;
@@ -158,7 +158,7 @@ cudaError_t maps::shared_opt_in(const void *fn)
     std::lock_guard<std::mutex> lock(mu);
     for (const auto &r : ready)
         if (r.first == dev && r.second == fn) return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, maps::kMapShared);
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     try {
         ready.emplace_back(dev, fn);

@@ -1,130 +1,181 @@
 // Linear layer of a map with its epilogue, and its gradient:
 //   z = x W^T + b,  y = act(z) + residual;
 //   dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum dz.
+// The products run on the tensor cores (linear_tc.cu), which take 16-bit
+// operands whose rows TMA can address (16-byte pitch and start).  What is not of
+// that kind is laid out first: float32 as three bfloat16 planes, rows of odd
+// widths or with gaps as packed ones; so is dz, in one pass that also adds up its
+// columns.  Sums too long for few tiles are cut into runs that a last kernel joins
+// in order.
 #include <algorithm>
 #include <cmath>
 
-#include "map_ops.h"
+#include "linear.h"
 #include "rz_device.h"
 #include "rz_internal.h"
 
 namespace rz {
 namespace {
 
-using namespace maps;
+using namespace lin;
 using dev::grid_dependency_wait;
 using dev::grid_launch_dependents;
 
-// A matrix inside a map or a weight: row r at row_off(r), its columns packed.
-struct Rows {
-    View v;
-    unsigned HW, W;     // pixels of an image and of its rows (HW 0: rows `pitch` apart)
-    int joined, bytes;  // a row's bytes where the map's rows are joined
+constexpr int kLinSms = 152;
+constexpr int kPackThreads = 256;
+constexpr int kPackWarps = kPackThreads / 32;
+
+// Rows of a map or weight, times act'(slope) if there is one, laid out for the
+// tensor cores: 16-bit rows of `pitch` bytes, float32 as three planes of bfloat16
+// (each the leading 8 bits of what is left: together all 24).  And their column
+// sums, by chunks of rows.
+struct PackArgs {
+    Rows in, slope;
+    uint8_t *to;            // null: sums only
+    long long pitch, plane;
+    float *sums;            // [chunks][C], or null
+    unsigned M, C;
+    unsigned chunk;         // rows of a CTA
+    int lanes;              // lanes side by side in a row, eight columns each
+    int has_slope, act, wide;
 };
 
-__device__ __forceinline__ long long row_off(const Rows &m, unsigned r)
-{
-    if (!m.HW) return r * m.v.pitch;
-    const unsigned n = r / m.HW;
-    return n * m.v.bstride + pixel_off(r - n * m.HW, m.W, m.joined != 0, m.v.pitch, m.bytes);
-}
 template <class T>
-__device__ __forceinline__ float element(const Rows &m, unsigned r, unsigned c)
+__device__ __forceinline__ void load8(const uint8_t *at, int left, bool wide, float (&f)[8])
 {
-    return static_cast<float>(reinterpret_cast<const T *>(m.v.p + row_off(m, r))[c]);
-}
-template <class T>
-__device__ __forceinline__ void put(const Rows &m, unsigned r, unsigned c, float v)
-{
-    reinterpret_cast<T *>(m.v.p + row_off(m, r))[c] = static_cast<T>(v);
-}
-
-__device__ __forceinline__ float activated(float z, int act)
-{
-    if (act == RZ_ACT_SILU) return z < -87.3f ? 0.0f : z * rcp_approx(1.0f + exp2_approx(-1.44269504f * z));
-    return act == RZ_ACT_GELU ? gelu(z) : z;
-}
-__device__ __forceinline__ float act_slope(float z, int act)
-{
-    if (act == RZ_ACT_SILU) {
-        const float s = z < -87.3f ? 0.0f : rcp_approx(1.0f + exp2_approx(-1.44269504f * z));
-        return s * fmaf(z, 1.0f - s, 1.0f);
+    if (wide && left >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = __ldcs(reinterpret_cast<const float4 *>(at)), b = __ldcs(reinterpret_cast<const float4 *>(at) + 1);
+            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        } else {
+            unpack<T, 8>(__ldcs(reinterpret_cast<const uint4 *>(at)), f);
+        }
+        return;
     }
-    return act == RZ_ACT_GELU ? gelu_slope(z) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) f[i] = i < left ? static_cast<float>(reinterpret_cast<const T *>(at)[i]) : 0.0f;
 }
 
-// D[m][n] = sum_k A(m, k) B(n, k), an element read by its row and column: of a
-// transposed operand k is the row.  64 x 64 a CTA, 16 terms at a time.
-struct SimpleArgs {
-    Rows a, b, out, pre, residual, slope;   // slope: pre of A, which A is multiplied by act' of
-    const float *bias;
-    unsigned M, N, K;
-    int a_turned, b_turned, act, has_pre, has_residual, has_slope;
-};
-
-template <class T, class O>
-__global__ void __launch_bounds__(256) k_linear_simple(const __grid_constant__ SimpleArgs p)
+// The leading 8 bits of v, cut, so that what is left has its sign and no value
+// becomes infinite.
+__device__ __forceinline__ float leading(float v)
 {
-    __shared__ float sa[16][65], sb[16][65];
+    return v != v ? v : __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_constant__ PackArgs a)
+{
+    __shared__ float sh[kPackWarps][256];
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rows = 32 / a.lanes, sub = lane % a.lanes, down = lane / a.lanes;
+    const unsigned c = (blockIdx.x * a.lanes + sub) * 8;
+    const int left = static_cast<int>(a.C) - static_cast<int>(c);
+    const unsigned r0 = blockIdx.y * a.chunk, r1 = min(a.M, r0 + a.chunk);
+    float s[8] = {};
+    grid_dependency_wait();
+    if (left > 0) {
+#pragma unroll 2
+        for (unsigned r = r0 + warp * rows + down; r < r1; r += kPackWarps * rows) {
+            float f[8];
+            load8<T>(a.in.v.p + row_off(a.in, r) + static_cast<long long>(c) * sizeof(T), left, a.wide, f);
+            if (a.has_slope) {
+                float z[8];
+                load8<T>(a.slope.v.p + row_off(a.slope, r) + static_cast<long long>(c) * sizeof(T), left, a.wide, z);
+#pragma unroll
+                for (int i = 0; i < 8; i++) f[i] *= act_slope(z[i], a.act);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (i < left) s[i] += f[i];
+            if (!a.to) continue;
+            uint8_t *at = a.to + r * a.pitch + c * 2;
+            if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<uint4 *>(at) = pack<T, 8>(f);
+            } else {
+#pragma unroll
+                for (int p = 0; p < 3; p++) {
+                    float h[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        h[i] = leading(f[i]);
+                        f[i] -= h[i];
+                    }
+                    *reinterpret_cast<uint4 *>(at + p * a.plane) = pack<__nv_bfloat16, 8>(h);
+                }
+            }
+        }
+    }
+    if (!a.sums) return;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        for (int o = a.lanes; o < 32; o <<= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+        if (down == 0) sh[warp][sub * 8 + i] = s[i];
+    }
+    __syncthreads();
+    const unsigned col = blockIdx.x * a.lanes * 8 + threadIdx.x;
+    if (static_cast<int>(threadIdx.x) >= a.lanes * 8 || col >= a.C) return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kPackWarps; w++) sum += sh[w][threadIdx.x];
+    a.sums[static_cast<long long>(blockIdx.y) * a.C + col] = sum;
+}
+
+// dbias: the chunks' sums, 32 columns a block, each of its warps a chunk in
+// eight, joined in order.
+__global__ void __launch_bounds__(256) k_linear_sums(const float *sums, unsigned chunks, unsigned C, float *dbias)
+{
+    __shared__ float sh[8][32];
     grid_launch_dependents();
     grid_dependency_wait();
-    const unsigned tiles_n = (p.N + 63) / 64, m0 = blockIdx.x / tiles_n * 64, n0 = blockIdx.x % tiles_n * 64;
-    const unsigned tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (unsigned k0 = 0; k0 < p.K; k0 += 16) {
-        for (unsigned i = threadIdx.x; i < 1024; i += 256) {
-            const unsigned k = i % 16, r = i / 16;
-            float a = 0.0f, b = 0.0f;
-            if (k0 + k < p.K && m0 + r < p.M) {
-                const unsigned row = p.a_turned ? k0 + k : m0 + r, col = p.a_turned ? m0 + r : k0 + k;
-                a = element<T>(p.a, row, col);
-                if (p.has_slope) a *= act_slope(element<T>(p.slope, row, col), p.act);
-            }
-            if (k0 + k < p.K && n0 + r < p.N)
-                b = p.b_turned ? element<T>(p.b, k0 + k, n0 + r) : element<T>(p.b, n0 + r, k0 + k);
-            sa[k][r] = a;
-            sb[k][r] = b;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 16; k++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], acc[i][j]);
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; i++)
-        for (int j = 0; j < 4; j++) {
-            const unsigned m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= p.M || n >= p.N) continue;
-            float z = acc[i][j];
-            if (!p.has_slope) {
-                if (p.bias) z += p.bias[n];
-                if (p.has_pre) put<T>(p.pre, m, n, z);
-                z = activated(z, p.act);
-                if (p.has_residual) z += element<T>(p.residual, m, n);
-            }
-            put<O>(p.out, m, n, z);
-        }
-}
-
-// Column sums of dz, a column a warp.
-template <class T>
-__global__ void __launch_bounds__(256) k_linear_sums(const __grid_constant__ SimpleArgs p, float *dbias)
-{
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const unsigned c = blockIdx.x * 8 + threadIdx.x / 32;
-    if (c >= p.N) return;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const unsigned c = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    for (unsigned r = threadIdx.x % 32; r < p.M; r += 32) {
-        float v = element<T>(p.a, r, c);
-        if (p.has_slope) v *= act_slope(element<T>(p.slope, r, c), p.act);
-        s += v;
+    if (c < C) {
+#pragma unroll 8
+        for (unsigned r = w; r < chunks; r += 8) s += sums[static_cast<long long>(r) * C + c];
     }
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (threadIdx.x % 32 == 0) dbias[c] = s;
+    sh[w][lane] = s;
+    __syncthreads();
+    if (w || c >= C) return;
+#pragma unroll
+    for (int i = 1; i < 8; i++) s += sh[i][lane];
+    dbias[c] = s;
+}
+
+// The runs of a product joined in order, and its epilogue.
+struct JoinArgs {
+    Finish f;
+    const float *part;
+    unsigned pitch;         // floats, a multiple of VE
+    int splits;
+};
+
+template <class T>
+__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ JoinArgs a)
+{
+    constexpr int VE = 16 / sizeof(T);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const unsigned vecs = a.pitch / VE;
+    const unsigned long long id = blockIdx.x * 256ull + threadIdx.x;
+    const unsigned m = static_cast<unsigned>(id / vecs), n = static_cast<unsigned>(id % vecs) * VE;
+    if (m >= a.f.M || n >= a.f.N) return;
+    float z[VE] = {}, b[VE];
+    for (int r = 0; r < a.splits; r++) {
+        const float *from = a.part + (static_cast<long long>(r) * a.f.M + m) * a.pitch + n;
+#pragma unroll
+        for (int q = 0; q < VE; q += 4) {
+            const float4 v = __ldcs(reinterpret_cast<const float4 *>(from + q));
+            z[q] += v.x;
+            z[q + 1] += v.y;
+            z[q + 2] += v.z;
+            z[q + 3] += v.w;
+        }
+    }
+    bias_of<VE>(a.f, n, b);
+    finish<T, VE>(a.f, m, n, z, b);
 }
 
 // ------------------------------------------------------------------ host side
@@ -147,6 +198,7 @@ int lin_check(const rz_linear *d, LinPlan *p)
     return RZ_OK;
 }
 
+// A map's rows are pixels; where they are evenly apart, `HW` is 0.
 Rows rows_of(const rz_map *m, const Shape &s)
 {
     Rows r{};
@@ -155,6 +207,11 @@ Rows rows_of(const rz_map *m, const Shape &s)
     r.joined = rows_joined(*m, s);
     r.HW = static_cast<unsigned>(s.H * s.W);
     r.W = static_cast<unsigned>(s.W);
+    if (r.joined && (s.N == 1 || m->batch_stride == s.H * s.row())) {
+        r.HW = 0;
+        r.v.pitch = r.bytes;
+        r.v.bstride = 0;
+    }
     return r;
 }
 Rows rows_of(const void *p, size_t pitch)
@@ -168,9 +225,9 @@ bool matrix_ok(const void *p, size_t pitch, long long rows, long long cols, size
 {
     const size_t row = static_cast<size_t>(cols) * es;
     return p && reinterpret_cast<uintptr_t>(p) % es == 0 && pitch % es == 0 && (rows == 1 || pitch >= row) &&
-           pitch <= (size_t{1} << 40);
+           pitch <= (size_t{1} << 39);
 }
-// The bytes of a matrix and of a map, for overlaps.
+// The bytes of a matrix or a map, for overlaps.
 struct Range {
     uintptr_t from, to;
 };
@@ -193,22 +250,213 @@ int lin_status(cudaError_t e)
     return RZ_ERR_CUDA;
 }
 
-template <class T, class O = T>
-cudaError_t simple(const SimpleArgs &p, void *stream)
+size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+// A matrix as an operand: itself where TMA can address it, else its place in the
+// workspace.
+struct Laid {
+    Rows in;
+    unsigned rows, cols;
+    int dtype;
+    bool direct;
+    size_t pitch, plane, bytes;     // of the layout in the workspace; bytes 0: direct
+    size_t at = 0;
+};
+Laid lay(const Rows &in, unsigned rows, unsigned cols, int dtype, bool changed)
 {
-    const long long tiles = static_cast<long long>((p.M + 63) / 64) * ((p.N + 63) / 64);
-    if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch(k_linear_simple<T, O>, dim3(static_cast<unsigned>(tiles)), 256, 0, stream, p);
+    Laid l{};
+    l.in = in;
+    l.rows = rows;
+    l.cols = cols;
+    l.dtype = dtype;
+    l.direct = dtype != RZ_F32 && !changed && !in.HW && reinterpret_cast<uintptr_t>(in.v.p) % 16 == 0 &&
+               (rows == 1 || in.v.pitch % 16 == 0);
+    if (l.direct) {
+        l.pitch = rows == 1 ? up(2 * static_cast<size_t>(cols), 16) : static_cast<size_t>(in.v.pitch);
+        return l;
+    }
+    l.pitch = up(cols, 8) * 2;
+    l.plane = l.pitch * rows;
+    l.bytes = l.plane * (dtype == RZ_F32 ? 3 : 1);
+    return l;
 }
+// rows, terms: of the product; turned: the memory's rows are its terms.
+Operand operand(const Laid &l, const uint8_t *workspace, bool turned)
+{
+    Operand o{};
+    o.p = l.direct ? l.in.v.p : workspace + l.at;
+    o.pitch = l.pitch;
+    o.plane = l.plane;
+    o.rows = turned ? l.cols : l.rows;
+    o.terms = turned ? l.rows : l.cols;
+    o.planes = l.dtype == RZ_F32 ? 3 : 1;
+    o.turned = turned;
+    o.bf16 = l.dtype != RZ_F16;
+    return o;
+}
+
+// Tile width and runs of a product, by an estimate in clocks: a stage's products
+// (or its loads, on narrow tiles), a tile's epilogue, and the join of its runs.
+struct Cut {
+    int tile_n, splits;
+    unsigned pitch;
+    size_t bytes;
+};
+Cut cut(unsigned M, unsigned N, unsigned terms, int dtype)
+{
+    const long long chunks = static_cast<long long>((terms + 63) / 64) * (dtype == RZ_F32 ? 6 : 1);
+    Cut best{};
+    double least = 0.0;
+    const unsigned pitch = static_cast<unsigned>(up(N, 8));
+    for (int tile = 256; tile >= 64; tile /= 2) {
+        if (tile > 64 && N <= static_cast<unsigned>(tile) / 2) continue;
+        const double stage = tile == 256 ? 560 : tile == 128 ? 340 : 240;
+        const long long tiles = static_cast<long long>((M + 127) / 128) * ((N + tile - 1) / tile);
+        for (int want = 1; want <= 64 && want <= chunks; want++) {
+            const long long run = (chunks + want - 1) / want;
+            const int splits = static_cast<int>((chunks + run - 1) / run);
+            if (splits != want) continue;
+            const double waves = static_cast<double>((tiles * splits + kLinSms - 1) / kLinSms);
+            double t = waves * run * stage + 3000 + 6.0 * tile;
+            if (splits > 1) t += 5000 + 4.0 * M * pitch * (splits + 1) / 3000.0;
+            if (!best.tile_n || t < least) {
+                least = t;
+                best = {tile, splits, pitch, splits > 1 ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
+            }
+        }
+    }
+    return best;
+}
+
+cudaError_t pack_rows(const Laid &l, const Rows *slope, int act, float *sums, unsigned chunks, uint8_t *workspace, void *stream)
+{
+    PackArgs a{};
+    a.in = l.in;
+    if (slope) a.slope = *slope;
+    a.has_slope = slope != nullptr;
+    a.act = act;
+    a.to = l.bytes ? workspace + l.at : nullptr;
+    a.pitch = static_cast<long long>(l.pitch);
+    a.plane = static_cast<long long>(l.plane);
+    a.sums = sums;
+    a.M = l.rows;
+    a.C = l.cols;
+    const unsigned vecs = (l.cols + 7) / 8;
+    a.lanes = 1;
+    while (a.lanes < 32 && static_cast<unsigned>(a.lanes) < vecs) a.lanes *= 2;
+    a.chunk = (l.rows + chunks - 1) / chunks;
+    const size_t es = dtype_size(l.dtype);
+    const auto wide = [&](const Rows &r) {
+        return reinterpret_cast<uintptr_t>(r.v.p) % 16 == 0 && r.v.pitch % 16 == 0 && r.v.bstride % 16 == 0 &&
+               (!r.HW || r.bytes % 16 == 0);
+    };
+    a.wide = l.cols * es % 16 == 0 && wide(l.in) && (!slope || wide(*slope));
+    const dim3 grid((vecs + a.lanes - 1) / a.lanes, (l.rows + a.chunk - 1) / a.chunk);
+    if (l.dtype == RZ_F32) return launch(k_linear_pack<float>, grid, kPackThreads, 0, stream, a);
+    if (l.dtype == RZ_BF16) return launch(k_linear_pack<__nv_bfloat16>, grid, kPackThreads, 0, stream, a);
+    return launch(k_linear_pack<__half>, grid, kPackThreads, 0, stream, a);
+}
+// Chunks of rows of a pass over a matrix: about four CTAs an SM, at least 16 rows each.
+unsigned pack_chunks(unsigned rows, unsigned cols)
+{
+    const unsigned vecs = (cols + 7) / 8, blocks = (vecs + 31) / 32;
+    const unsigned want = std::max(1u, 4 * kLinSms / blocks);
+    const unsigned n = std::clamp((rows + 15) / 16, 1u, std::min(want, 65535u));
+    const unsigned chunk = (rows + n - 1) / n;
+    return (rows + chunk - 1) / chunk;
+}
+
 template <class T>
-cudaError_t simple_to(const SimpleArgs &p, int out, void *stream)
+cudaError_t join_launch(const JoinArgs &a, void *stream)
 {
-    return out == RZ_F32 ? simple<T, float>(p, stream) : simple<T>(p, stream);
+    const unsigned long long n = static_cast<unsigned long long>(a.f.M) * (a.pitch / (16 / sizeof(T)));
+    return launch(k_linear_join<T>, dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream, a);
 }
-cudaError_t simple_of(const SimpleArgs &p, int dtype, int out, void *stream)
+
+cudaError_t product(const Operand &a, const Operand &b, const Finish &f, int out_dtype, const Cut &c, float *part, int *status,
+                    void *stream)
 {
-    if (dtype == RZ_F32) return simple<float>(p, stream);
-    return dtype == RZ_BF16 ? simple_to<__nv_bfloat16>(p, out, stream) : simple_to<__half>(p, out, stream);
+    Product p{};
+    p.a = a;
+    p.b = b;
+    p.f = f;
+    p.out_dtype = out_dtype;
+    p.splits = c.splits;
+    p.part = part;
+    p.part_pitch = c.pitch;
+    p.tile_n = c.tile_n;
+    p.status = status;
+    cudaError_t e = launch_product(p, stream);
+    if (e != cudaSuccess || c.splits == 1) return e;
+    const JoinArgs j{f, part, c.pitch, c.splits};
+    if (out_dtype == RZ_F32) return join_launch<float>(j, stream);
+    return out_dtype == RZ_BF16 ? join_launch<__nv_bfloat16>(j, stream) : join_launch<__half>(j, stream);
+}
+
+Finish finish_of(const Rows &out, unsigned M, unsigned N, const Rows *pre, const Rows *residual)
+{
+    Finish f{};
+    f.out = out;
+    f.M = M;
+    f.N = N;
+    f.has_pre = pre != nullptr;
+    f.has_residual = residual != nullptr;
+    if (pre) f.pre = *pre;
+    if (residual) f.residual = *residual;
+    f.wide = 1;
+    for (const Rows *r : {&out, pre, residual})
+        if (r && (reinterpret_cast<uintptr_t>(r->v.p) % 16 || r->v.pitch % 16 || r->v.bstride % 16 || (r->HW && r->bytes % 16)))
+            f.wide = 0;
+    return f;
+}
+
+// What a forward call lays out, and where in its workspace.
+struct Forward {
+    Laid x, w;
+    Cut c;
+    size_t part, total;
+};
+Forward plan_forward(const rz_linear *d, const LinPlan &p, const rz_map *x, const void *weight, size_t weight_pitch)
+{
+    Forward f{};
+    f.x = lay(rows_of(x, p.x), p.P, static_cast<unsigned>(d->C), d->dtype, false);
+    f.w = lay(rows_of(weight, weight_pitch), static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), d->dtype, false);
+    f.c = cut(p.P, static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), d->dtype);
+    f.w.at = up(f.x.bytes, 256);
+    f.part = f.w.at + up(f.w.bytes, 256);
+    f.total = f.part + f.c.bytes;
+    return f;
+}
+
+// The same of a gradient call.
+struct Backward {
+    Laid dz, x, w;
+    Cut cx, cw;
+    unsigned chunks;
+    size_t sums, part, total;
+};
+Backward plan_backward(const rz_linear *d, const LinPlan &p, const rz_map *dy, const rz_map *x, const void *weight,
+                       size_t weight_pitch)
+{
+    const unsigned C = static_cast<unsigned>(d->C), K = static_cast<unsigned>(d->K);
+    Backward b{};
+    b.dz = lay(rows_of(dy, p.y), p.P, K, d->dtype, d->act != RZ_ACT_NONE);
+    b.x = lay(rows_of(x, p.x), p.P, C, d->dtype, false);
+    b.w = lay(rows_of(weight, weight_pitch), K, C, d->dtype, false);
+    b.cx = cut(p.P, C, K, d->dtype);
+    b.cw = cut(K, C, p.P, d->dtype);
+    b.chunks = pack_chunks(p.P, K);
+    b.x.at = up(b.dz.bytes, 256);
+    b.w.at = b.x.at + up(b.x.bytes, 256);
+    b.sums = b.w.at + up(b.w.bytes, 256);
+    b.part = b.sums + up(sizeof(float) * b.chunks * static_cast<size_t>(K), 256);
+    b.total = b.part + std::max(b.cx.bytes, b.cw.bytes);
+    return b;
+}
+
+bool workspace_ok(const void *p, size_t bytes, size_t need)
+{
+    return need == 0 || (p && reinterpret_cast<uintptr_t>(p) % 16 == 0 && bytes >= need);
 }
 
 }  // namespace
@@ -226,6 +474,7 @@ int map_linear_workspace(const rz_linear *d, const rz_map *x, const void *weight
     *bytes = 0;
     if (p.x.empty()) return RZ_OK;
     if (!maps::map_ok(x, p.x) || !matrix_ok(weight, weight_pitch, d->K, d->C, p.x.es)) return RZ_ERR_ARG;
+    *bytes = plan_forward(d, p, x, weight, weight_pitch).total;
     return RZ_OK;
 }
 
@@ -250,20 +499,21 @@ int map_linear(const rz_linear *d, const rz_map *x, const void *weight, size_t w
             (residual && meet(rp, range_of(*residual, p.y))))
             return RZ_ERR_ARG;
     }
-    SimpleArgs s{};
-    s.a = rows_of(x, p.x);
-    s.b = rows_of(weight, weight_pitch);
-    s.out = rows_of(y, p.y);
-    s.M = p.P;
-    s.N = static_cast<unsigned>(d->K);
-    s.K = static_cast<unsigned>(d->C);
-    s.bias = bias;
-    s.act = d->act;
-    if (pre) s.pre = rows_of(pre, p.y);
-    if (residual) s.residual = rows_of(residual, p.y);
-    s.has_pre = pre != nullptr;
-    s.has_residual = residual != nullptr;
-    return lin_status(simple_of(s, d->dtype, d->dtype, stream));
+    const Forward f = plan_forward(d, p, x, weight, weight_pitch);
+    if (!workspace_ok(workspace, workspace_bytes, f.total)) return RZ_ERR_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    cudaError_t e = cudaSuccess;
+    for (const Laid *l : {&f.w, &f.x})
+        if (l->bytes && e == cudaSuccess) e = pack_rows(*l, nullptr, 0, nullptr, pack_chunks(l->rows, l->cols), ws, stream);
+    if (e != cudaSuccess) return lin_status(e);
+    Rows rr, rp;
+    if (residual) rr = rows_of(residual, p.y);
+    if (pre) rp = rows_of(pre, p.y);
+    Finish out = finish_of(rows_of(y, p.y), p.P, static_cast<unsigned>(d->K), pre ? &rp : nullptr, residual ? &rr : nullptr);
+    out.bias = bias;
+    out.act = d->act;
+    return lin_status(product(operand(f.x, ws, false), operand(f.w, ws, false), out, d->dtype, f.c,
+                              reinterpret_cast<float *>(ws + f.part), status, stream));
 }
 
 int map_linear_grad_workspace(const rz_linear *d, const rz_map *dy, const rz_map *x, const void *weight, size_t weight_pitch,
@@ -276,6 +526,7 @@ int map_linear_grad_workspace(const rz_linear *d, const rz_map *dy, const rz_map
     if (p.x.empty()) return RZ_OK;
     if (!maps::map_ok(x, p.x) || !maps::map_ok(dy, p.y) || !matrix_ok(weight, weight_pitch, d->K, d->C, p.x.es))
         return RZ_ERR_ARG;
+    *bytes = plan_backward(d, p, dy, x, weight, weight_pitch).total;
     return RZ_OK;
 }
 
@@ -313,42 +564,35 @@ int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x, const
         for (int j = 0; j < i; j++)
             if (meet(out[i], out[j])) return RZ_ERR_ARG;
     }
-    SimpleArgs s{};
-    s.a = rows_of(dy, p.y);
-    s.act = d->act;
-    s.has_slope = d->act != RZ_ACT_NONE;
-    if (s.has_slope) s.slope = rows_of(pre, p.y);
+    const Backward b = plan_backward(d, p, dy, x, weight, weight_pitch);
+    if (!workspace_ok(workspace, workspace_bytes, b.total)) return RZ_ERR_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    float *sums = reinterpret_cast<float *>(ws + b.sums), *part = reinterpret_cast<float *>(ws + b.part);
     cudaError_t e = cudaSuccess;
-    if (dx) {
-        SimpleArgs q = s;
-        q.b = rows_of(weight, weight_pitch);
-        q.b_turned = 1;
-        q.out = rows_of(dx, p.x);
-        q.M = p.P;
-        q.N = static_cast<unsigned>(d->C);
-        q.K = static_cast<unsigned>(d->K);
-        e = simple_of(q, d->dtype, d->dtype, stream);
+    if (dbias || (b.dz.bytes && (dx || dweight))) {
+        Rows slope;
+        const bool sloped = d->act != RZ_ACT_NONE;
+        if (sloped) slope = rows_of(pre, p.y);
+        Laid dz = b.dz;
+        if (!dx && !dweight) dz.bytes = 0;
+        e = pack_rows(dz, sloped ? &slope : nullptr, d->act, dbias ? sums : nullptr, b.chunks, ws, stream);
+        if (dbias && e == cudaSuccess)
+            e = maps::launch(k_linear_sums, dim3((d->K + 31) / 32), 256, 0, stream, sums, b.chunks, static_cast<unsigned>(d->K), dbias);
+    }
+    if (dx && e == cudaSuccess) {
+        if (b.w.bytes) e = pack_rows(b.w, nullptr, 0, nullptr, pack_chunks(b.w.rows, b.w.cols), ws, stream);
+        if (e == cudaSuccess)
+            e = product(operand(b.dz, ws, false), operand(b.w, ws, true),
+                        finish_of(rows_of(dx, p.x), p.P, static_cast<unsigned>(d->C), nullptr, nullptr), d->dtype, b.cx, part,
+                        status, stream);
     }
     if (dweight && e == cudaSuccess) {
-        SimpleArgs q = s;
-        q.a_turned = q.b_turned = 1;
-        q.b = rows_of(x, p.x);
-        q.out = rows_of(dweight, dweight_pitch);
-        q.M = static_cast<unsigned>(d->K);
-        q.N = static_cast<unsigned>(d->C);
-        q.K = p.P;
-        e = simple_of(q, d->dtype, dweight_dtype, stream);
-    }
-    if (dbias && e == cudaSuccess) {
-        s.M = p.P;
-        s.N = static_cast<unsigned>(d->K);
-        const dim3 grid((s.N + 7) / 8);
-        if (d->dtype == RZ_F32)
-            e = maps::launch(k_linear_sums<float>, grid, 256, 0, stream, s, dbias);
-        else if (d->dtype == RZ_BF16)
-            e = maps::launch(k_linear_sums<__nv_bfloat16>, grid, 256, 0, stream, s, dbias);
-        else
-            e = maps::launch(k_linear_sums<__half>, grid, 256, 0, stream, s, dbias);
+        if (b.x.bytes) e = pack_rows(b.x, nullptr, 0, nullptr, pack_chunks(b.x.rows, b.x.cols), ws, stream);
+        if (e == cudaSuccess)
+            e = product(operand(b.dz, ws, true), operand(b.x, ws, true),
+                        finish_of(rows_of(dweight, dweight_pitch), static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), nullptr,
+                                  nullptr),
+                        dweight_dtype, b.cw, part, status, stream);
     }
     return lin_status(e);
 }
