@@ -84,7 +84,11 @@ __global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_const
                 float z[8];
                 load8<T>(a.slope.v.p + row_off(a.slope, r) + static_cast<long long>(c) * sizeof(T), left, a.wide, z);
 #pragma unroll
-                for (int i = 0; i < 8; i++) f[i] *= act_slope(z[i], a.act);
+                for (int i = 0; i < 8; i += 2) {
+                    const float2 d = act_slope<T>(make_float2(z[i], z[i + 1]), a.act);
+                    f[i] *= d.x;
+                    f[i + 1] *= d.y;
+                }
             }
 #pragma unroll
             for (int i = 0; i < 8; i++)
@@ -152,30 +156,38 @@ struct JoinArgs {
     int splits;
 };
 
-template <class T>
+template <class T, int ACT, bool WIDE>
 __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ JoinArgs a)
 {
-    constexpr int VE = 16 / sizeof(T);
+    constexpr int VE = WIDE ? 16 / sizeof(T) : 1;
     grid_launch_dependents();
     grid_dependency_wait();
-    const unsigned vecs = a.pitch / VE;
+    const unsigned vecs = a.f.N / VE;
     const unsigned long long id = blockIdx.x * 256ull + threadIdx.x;
-    const unsigned m = static_cast<unsigned>(id / vecs), n = static_cast<unsigned>(id % vecs) * VE;
-    if (m >= a.f.M || n >= a.f.N) return;
-    float z[VE] = {}, b[VE];
-    for (int r = 0; r < a.splits; r++) {
-        const float *from = a.part + (static_cast<long long>(r) * a.f.M + m) * a.pitch + n;
+    const unsigned m = static_cast<unsigned>(id / vecs), n = static_cast<unsigned>(id - static_cast<unsigned long long>(m) * vecs) * VE;
+    if (m >= a.f.M) return;
+    const float *from = a.part + static_cast<long long>(m) * a.pitch + n;
+    const long long run = static_cast<long long>(a.f.M) * a.pitch;
+    if constexpr (WIDE) {
+        float2 z[VE / 2] = {}, b[VE / 2];
+#pragma unroll 4
+        for (int r = 0; r < a.splits; r++, from += run)
 #pragma unroll
-        for (int q = 0; q < VE; q += 4) {
-            const float4 v = __ldcs(reinterpret_cast<const float4 *>(from + q));
-            z[q] += v.x;
-            z[q + 1] += v.y;
-            z[q + 2] += v.z;
-            z[q + 3] += v.w;
-        }
+            for (int q = 0; q < VE; q += 4) {
+                const float4 v = __ldcs(reinterpret_cast<const float4 *>(from + q));
+                z[q / 2] = __fadd2_rn(z[q / 2], make_float2(v.x, v.y));
+                z[q / 2 + 1] = __fadd2_rn(z[q / 2 + 1], make_float2(v.z, v.w));
+            }
+        bias_of<VE>(a.f, n, b);
+        Raw<T, VE> r{};
+        if (a.f.has_residual) r = *vec_at<T, VE>(a.f.residual, m, n);
+        finish<T, VE, ACT>(a.f, m, n, z, b, r);
+    } else {
+        float z[1] = {0.0f};
+#pragma unroll 4
+        for (int r = 0; r < a.splits; r++, from += run) z[0] += __ldcs(from);
+        finish_column<T, ACT, 1>(a.f, m, n, z, a.f.bias ? __ldg(a.f.bias + n) : 0.0f);
     }
-    bias_of<VE>(a.f, n, b);
-    finish<T, VE>(a.f, m, n, z, b);
 }
 
 // ------------------------------------------------------------------ host side
@@ -298,7 +310,7 @@ Operand operand(const Laid &l, const uint8_t *workspace, bool turned)
 // Tile width and runs of a product, by an estimate in clocks: a stage's products
 // (or its loads, on narrow tiles), a tile's epilogue, and the join of its runs.
 struct Cut {
-    int tile_n, splits;
+    int tile_n, pair, splits;
     unsigned pitch;
     size_t bytes;
 };
@@ -308,23 +320,26 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype)
     Cut best{};
     double least = 0.0;
     const unsigned pitch = static_cast<unsigned>(up(N, 8));
-    for (int tile = 256; tile >= 64; tile /= 2) {
-        if (tile > 64 && N <= static_cast<unsigned>(tile) / 2) continue;
-        const double stage = tile == 256 ? 560 : tile == 128 ? 340 : 240;
-        const long long tiles = static_cast<long long>((M + 127) / 128) * ((N + tile - 1) / tile);
-        for (int want = 1; want <= 64 && want <= chunks; want++) {
-            const long long run = (chunks + want - 1) / want;
-            const int splits = static_cast<int>((chunks + run - 1) / run);
-            if (splits != want) continue;
-            const double waves = static_cast<double>((tiles * splits + kLinSms - 1) / kLinSms);
-            double t = waves * run * stage + 3000 + 6.0 * tile;
-            if (splits > 1) t += 5000 + 4.0 * M * pitch * (splits + 1) / 3000.0;
-            if (!best.tile_n || t < least) {
-                least = t;
-                best = {tile, splits, pitch, splits > 1 ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
+    for (int pair = 0; pair < 2; pair++)
+        for (int tile = 256; tile >= (pair ? 128 : 64); tile /= 2) {
+            if ((tile > 64 && N <= static_cast<unsigned>(tile) / 2) || (pair && M <= 128)) continue;
+            const double stage = pair ? (tile == 256 ? 540 : 300) : tile == 256 ? 700 : tile == 128 ? 380 : 240;
+            const long long rows = pair ? 256 : 128, slots = pair ? kLinSms / 2 : kLinSms;
+            const long long tiles = (M + rows - 1) / rows * ((N + tile - 1) / tile);
+            for (int want = 1; want <= 64 && want <= chunks; want++) {
+                const long long run = (chunks + want - 1) / want;
+                const int splits = static_cast<int>((chunks + run - 1) / run);
+                if (splits != want) continue;
+                const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
+                double t = waves * run * stage + 3000 + 12.0 * tile;
+                if (splits > 1) t += 5000 + 4.0 * M * pitch * (splits + 1) / 3000.0;
+                if (!best.tile_n || t < least) {
+                    least = t;
+                    best = {tile, pair, splits, pitch, splits > 1 ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
+                }
+                if (waves > 8) break;
             }
         }
-    }
     return best;
 }
 
@@ -366,11 +381,18 @@ unsigned pack_chunks(unsigned rows, unsigned cols)
     return (rows + chunk - 1) / chunk;
 }
 
-template <class T>
+template <class T, int ACT>
 cudaError_t join_launch(const JoinArgs &a, void *stream)
 {
-    const unsigned long long n = static_cast<unsigned long long>(a.f.M) * (a.pitch / (16 / sizeof(T)));
-    return launch(k_linear_join<T>, dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream, a);
+    const unsigned long long n = static_cast<unsigned long long>(a.f.M) * (a.f.wide ? a.f.N / (16 / sizeof(T)) : a.f.N);
+    return launch(a.f.wide ? k_linear_join<T, ACT, true> : k_linear_join<T, ACT, false>,
+                  dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream, a);
+}
+template <class T>
+cudaError_t join_of(const JoinArgs &a, void *stream)
+{
+    if (a.f.act == RZ_ACT_SILU) return join_launch<T, RZ_ACT_SILU>(a, stream);
+    return a.f.act == RZ_ACT_GELU ? join_launch<T, RZ_ACT_GELU>(a, stream) : join_launch<T, RZ_ACT_NONE>(a, stream);
 }
 
 cudaError_t product(const Operand &a, const Operand &b, const Finish &f, int out_dtype, const Cut &c, float *part, int *status,
@@ -385,15 +407,16 @@ cudaError_t product(const Operand &a, const Operand &b, const Finish &f, int out
     p.part = part;
     p.part_pitch = c.pitch;
     p.tile_n = c.tile_n;
+    p.pair = c.pair;
     p.status = status;
     cudaError_t e = launch_product(p, stream);
     if (e != cudaSuccess || c.splits == 1) return e;
     const JoinArgs j{f, part, c.pitch, c.splits};
-    if (out_dtype == RZ_F32) return join_launch<float>(j, stream);
-    return out_dtype == RZ_BF16 ? join_launch<__nv_bfloat16>(j, stream) : join_launch<__half>(j, stream);
+    if (out_dtype == RZ_F32) return join_of<float>(j, stream);
+    return out_dtype == RZ_BF16 ? join_of<__nv_bfloat16>(j, stream) : join_of<__half>(j, stream);
 }
 
-Finish finish_of(const Rows &out, unsigned M, unsigned N, const Rows *pre, const Rows *residual)
+Finish finish_of(const Rows &out, unsigned M, unsigned N, int dtype, const Rows *pre, const Rows *residual)
 {
     Finish f{};
     f.out = out;
@@ -403,7 +426,7 @@ Finish finish_of(const Rows &out, unsigned M, unsigned N, const Rows *pre, const
     f.has_residual = residual != nullptr;
     if (pre) f.pre = *pre;
     if (residual) f.residual = *residual;
-    f.wide = 1;
+    f.wide = N * dtype_size(dtype) % 16 == 0;
     for (const Rows *r : {&out, pre, residual})
         if (r && (reinterpret_cast<uintptr_t>(r->v.p) % 16 || r->v.pitch % 16 || r->v.bstride % 16 || (r->HW && r->bytes % 16)))
             f.wide = 0;
@@ -509,7 +532,7 @@ int map_linear(const rz_linear *d, const rz_map *x, const void *weight, size_t w
     Rows rr, rp;
     if (residual) rr = rows_of(residual, p.y);
     if (pre) rp = rows_of(pre, p.y);
-    Finish out = finish_of(rows_of(y, p.y), p.P, static_cast<unsigned>(d->K), pre ? &rp : nullptr, residual ? &rr : nullptr);
+    Finish out = finish_of(rows_of(y, p.y), p.P, static_cast<unsigned>(d->K), d->dtype, pre ? &rp : nullptr, residual ? &rr : nullptr);
     out.bias = bias;
     out.act = d->act;
     return lin_status(product(operand(f.x, ws, false), operand(f.w, ws, false), out, d->dtype, f.c,
@@ -583,15 +606,15 @@ int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x, const
         if (b.w.bytes) e = pack_rows(b.w, nullptr, 0, nullptr, pack_chunks(b.w.rows, b.w.cols), ws, stream);
         if (e == cudaSuccess)
             e = product(operand(b.dz, ws, false), operand(b.w, ws, true),
-                        finish_of(rows_of(dx, p.x), p.P, static_cast<unsigned>(d->C), nullptr, nullptr), d->dtype, b.cx, part,
+                        finish_of(rows_of(dx, p.x), p.P, static_cast<unsigned>(d->C), d->dtype, nullptr, nullptr), d->dtype, b.cx, part,
                         status, stream);
     }
     if (dweight && e == cudaSuccess) {
         if (b.x.bytes) e = pack_rows(b.x, nullptr, 0, nullptr, pack_chunks(b.x.rows, b.x.cols), ws, stream);
         if (e == cudaSuccess)
             e = product(operand(b.dz, ws, true), operand(b.x, ws, true),
-                        finish_of(rows_of(dweight, dweight_pitch), static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), nullptr,
-                                  nullptr),
+                        finish_of(rows_of(dweight, dweight_pitch), static_cast<unsigned>(d->K), static_cast<unsigned>(d->C),
+                                  dweight_dtype, nullptr, nullptr),
                         dweight_dtype, b.cw, part, status, stream);
     }
     return lin_status(e);

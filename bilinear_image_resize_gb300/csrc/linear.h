@@ -25,18 +25,62 @@ __device__ __forceinline__ long long row_off(const Rows &m, unsigned r)
     return n * m.v.bstride + pixel_off(r - n * m.HW, m.W, m.joined != 0, m.v.pitch, m.bytes);
 }
 
-__device__ __forceinline__ float activated(float z, int act)
+// The activations.  float32 results take the exact forms.  16-bit ones, which are
+// rounded to 2^-9 or 2^-12 of their size, take GELU from Abramowitz and Stegun's
+// 7.1.26, two elements at a time: with a = |z|, t = 1 / (1 + p a / sqrt 2),
+//   Phi(-a) = (a1 t + ... + a5 t^5) exp(-z^2 / 2) / 2,  |error| < 7.5e-8,
+//   GELU(z) = max(z, 0) - a Phi(-a),
+// nine instructions an element where erff takes thirty: on a product of 1024
+// terms those cost more than the product (617 against 330 us on 65536 x 1024 x 4096).
+// Infinities: a is cut at 1e4, where Phi(-a) is 0; the rest passes them and NaN on.
+__device__ __forceinline__ float2 lower_tail(float2 z, float2 &a, float2 &e)
 {
-    if (act == RZ_ACT_SILU) return z < -87.3f ? 0.0f : z * rcp_approx(1.0f + exp2_approx(-1.44269504f * z));
-    return act == RZ_ACT_GELU ? gelu(z) : z;
+    a = make_float2(fminf(fabsf(z.x), 1.0e4f), fminf(fabsf(z.y), 1.0e4f));
+    const float2 d = __ffma2_rn(a, both(0.3275911f * 0.70710678f), both(1.0f));
+    const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    float2 p = __ffma2_rn(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+    p = __ffma2_rn(t, p, both(0.5f * 1.421413741f));
+    p = __ffma2_rn(t, p, both(0.5f * -0.284496736f));
+    p = __ffma2_rn(t, p, both(0.5f * 0.254829592f));
+    const float2 x = __fmul2_rn(__fmul2_rn(a, a), both(-0.72134752f));
+    e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+    return __fmul2_rn(__fmul2_rn(t, p), e);
 }
-__device__ __forceinline__ float act_slope(float z, int act)
+template <class T, int ACT>
+__device__ __forceinline__ float2 activated(float2 z)
+{
+    if constexpr (ACT == RZ_ACT_SILU) {
+        const float2 x = __fmul2_rn(z, both(-1.44269504f));
+        const float2 d = __fadd2_rn(make_float2(exp2_approx(x.x), exp2_approx(x.y)), both(1.0f));
+        const float2 y = __fmul2_rn(z, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+        return make_float2(z.x < -87.3f ? 0.0f : y.x, z.y < -87.3f ? 0.0f : y.y);
+    } else if constexpr (ACT == RZ_ACT_GELU) {
+        if constexpr (sizeof(T) == 4) return make_float2(gelu(z.x), gelu(z.y));
+        float2 a, e;
+        const float2 q = lower_tail(z, a, e);
+        const float2 m = __ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), both(0.5f), __fmul2_rn(z, both(0.5f)));
+        return __ffma2_rn(make_float2(-a.x, -a.y), q, m);
+    } else {
+        return z;
+    }
+}
+// Their derivatives; GELU's is Phi(z) + z phi(z).
+template <class T>
+__device__ __forceinline__ float2 act_slope(float2 z, int act)
 {
     if (act == RZ_ACT_SILU) {
-        const float s = z < -87.3f ? 0.0f : rcp_approx(1.0f + exp2_approx(-1.44269504f * z));
-        return s * fmaf(z, 1.0f - s, 1.0f);
+        const float2 x = __fmul2_rn(z, both(-1.44269504f));
+        const float2 d = __fadd2_rn(make_float2(exp2_approx(x.x), exp2_approx(x.y)), both(1.0f));
+        const float2 s = make_float2(z.x < -87.3f ? 0.0f : rcp_approx(d.x), z.y < -87.3f ? 0.0f : rcp_approx(d.y));
+        return __fmul2_rn(s, __ffma2_rn(z, __ffma2_rn(s, both(-1.0f), both(1.0f)), both(1.0f)));
     }
-    return act == RZ_ACT_GELU ? gelu_slope(z) : 1.0f;
+    if (act != RZ_ACT_GELU) return both(1.0f);
+    if constexpr (sizeof(T) == 4) return make_float2(gelu_slope(z.x), gelu_slope(z.y));
+    float2 a, e;
+    const float2 q = lower_tail(z, a, e);
+    const float2 up = __ffma2_rn(q, both(-1.0f), both(1.0f));
+    const float2 phi = make_float2(z.x > 0.0f ? up.x : q.x, z.y > 0.0f ? up.y : q.y);
+    return __ffma2_rn(__fmul2_rn(z, both(0.39894228f)), e, phi);
 }
 
 // What becomes of z = a row of a matrix times one of another: out = act(z + bias)
@@ -46,62 +90,62 @@ struct Finish {
     const float *bias;
     unsigned M, N;      // rows and columns of out
     int has_pre, has_residual, act;
-    int wide;           // whole vectors of 16 bytes are aligned in out, pre and residual
+    int wide;           // out, pre and residual are made of whole aligned vectors of 16 bytes
 };
 
-// Columns n .. n + VE - 1 of row m, within the matrix (the last of them may not
-// be); b: their bias.
 template <class T, int VE>
-__device__ __forceinline__ void finish(const Finish &f, unsigned m, unsigned n, float (&z)[VE], const float (&b)[VE])
+__device__ __forceinline__ Raw<T, VE> *vec_at(const Rows &r, unsigned m, unsigned n)
 {
-    using V = Raw<T, VE>;
-    using E = Raw<T, 1>;
-    const bool vec = f.wide && n + VE <= f.N;
-    const int left = static_cast<int>(min(static_cast<unsigned>(VE), f.N - n));
-    const auto store = [&](const Rows &to) {
-        uint8_t *at = to.v.p + row_off(to, m) + static_cast<long long>(n) * sizeof(T);
-        if (vec) {
-            *reinterpret_cast<V *>(at) = pack<T, VE>(z);
-            return;
-        }
+    return reinterpret_cast<Raw<T, VE> *>(r.v.p + row_off(r, m) + static_cast<long long>(n) * sizeof(T));
+}
+// Columns n .. n + VE - 1 of row m, a vector of each matrix; b: their bias, r: the
+// residual's vector.
+template <class T, int VE, int ACT>
+__device__ __forceinline__ void finish(const Finish &f, unsigned m, unsigned n, float2 (&z)[VE / 2], const float2 (&b)[VE / 2],
+                                       const Raw<T, VE> &r)
+{
 #pragma unroll
-        for (int i = 0; i < VE; i++)
-            if (i < left) {
-                const float one[1] = {z[i]};
-                reinterpret_cast<E *>(at)[i] = pack<T, 1>(one);
-            }
-    };
+    for (int i = 0; i < VE / 2; i++) z[i] = __fadd2_rn(z[i], b[i]);
+    if (f.has_pre) *vec_at<T, VE>(f.pre, m, n) = pack2<T, VE>(z);
 #pragma unroll
-    for (int i = 0; i < VE; i++) z[i] += b[i];
-    if (f.has_pre) store(f.pre);
-    if (f.act != RZ_ACT_NONE)
-#pragma unroll
-        for (int i = 0; i < VE; i++) z[i] = activated(z[i], f.act);
+    for (int i = 0; i < VE / 2; i++) z[i] = activated<T, ACT>(z[i]);
     if (f.has_residual) {
-        const uint8_t *at = f.residual.v.p + row_off(f.residual, m) + static_cast<long long>(n) * sizeof(T);
-        float r[VE] = {};
-        if (vec) {
-            unpack<T, VE>(*reinterpret_cast<const V *>(at), r);
-        } else {
+        float2 add[VE / 2];
+        unpack2<T, VE>(r, add);
 #pragma unroll
-            for (int i = 0; i < VE; i++)
-                if (i < left) {
-                    float one[1];
-                    unpack<T, 1>(reinterpret_cast<const E *>(at)[i], one);
-                    r[i] = one[0];
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < VE; i++) z[i] += r[i];
+        for (int i = 0; i < VE / 2; i++) z[i] = __fadd2_rn(z[i], add[i]);
     }
-    store(f.out);
+    *vec_at<T, VE>(f.out, m, n) = pack2<T, VE>(z);
+}
+// Element n of rows m .. m + U - 1 (as far as the matrix has them), where vectors do
+// not fit: the residual's elements are asked for before the first is used.
+template <class T, int ACT, int U>
+__device__ __forceinline__ void finish_column(const Finish &f, unsigned m, unsigned n, const float (&z)[U], float b)
+{
+    using E = Raw<T, 1>;
+    const auto at = [&](const Rows &r, unsigned row) { return reinterpret_cast<E *>(r.v.p + row_off(r, row)) + n; };
+    float r[U][1];
+    if (f.has_residual)
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (m + u < f.M) unpack<T, 1>(*at(f.residual, m + u), r[u]);
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        if (m + u >= f.M) break;
+        float v[1] = {z[u] + b};
+        if (f.has_pre) *at(f.pre, m + u) = pack<T, 1>(v);
+        v[0] = activated<T, ACT>(both(v[0])).x;
+        if (f.has_residual) v[0] += r[u][0];
+        *at(f.out, m + u) = pack<T, 1>(v);
+    }
 }
 
 template <int VE>
-__device__ __forceinline__ void bias_of(const Finish &f, unsigned n, float (&b)[VE])
+__device__ __forceinline__ void bias_of(const Finish &f, unsigned n, float2 (&b)[VE / 2])
 {
 #pragma unroll
-    for (int i = 0; i < VE; i++) b[i] = f.bias && n + i < f.N ? __ldg(f.bias + n + i) : 0.0f;
+    for (int i = 0; i < VE / 2; i++)
+        b[i] = f.bias ? make_float2(__ldg(f.bias + n + 2 * i), __ldg(f.bias + n + 2 * i + 1)) : both(0.0f);
 }
 
 // One operand of a product on the tensor cores: its rows (M or N of the product)
@@ -125,7 +169,8 @@ struct Product {
     int splits;
     float *part;
     unsigned part_pitch;    // floats
-    int tile_n;             // 64, 128 or 256
+    int tile_n;             // 64 (without a pair), 128 or 256
+    int pair;               // two CTAs work on a tile of 256 rows, else one on 128
     int *status;
 };
 cudaError_t launch_product(const Product &p, void *stream);
