@@ -1,7 +1,7 @@
 // The linear layer's products on the fifth-generation tensor cores.
 //
-// A CTA computes 128 x tile_n of D = A B^T, 64 terms at a time: one thread asks
-// for both operands' tiles by TMA, into a ring of stages in the 128-byte swizzle;
+// A CTA computes 128 x tile_n of D = A B^T, 64 terms at a time: two threads ask
+// for the operands' tiles by TMA, into a ring of stages in the 128-byte swizzle;
 // one thread issues four tcgen05.mma (16 terms each) a stage, accumulating in
 // tensor memory; sixteen warps take finished tiles out of it.  Tensor memory holds
 // two tiles, so that one is stored while the next is computed.  CTAs are
@@ -36,9 +36,9 @@ constexpr int kTerms = 64;                      // terms of a stage: 128 bytes, 
 constexpr int kTileM = 128;
 constexpr int kBytesA = kTileM * kTerms * 2;
 constexpr int kEpiWarps = 16;
-constexpr int kThreads = 128 + 32 * kEpiWarps;  // producer, issuer, two idle warps; the epilogue's begin at a multiple of four
-constexpr int kStagePitch = 20;                 // floats of a row on its way out: 16 columns and a gap, so that rows differ in their banks
-constexpr int kStageBytes = kEpiWarps * 32 * kStagePitch * 4;
+constexpr int kThreads = 128 + 32 * kEpiWarps;  // loads of A, issuer, tensor memory, loads of B; the epilogue's begin at a multiple of four
+constexpr int kStagePitch = 48;                 // bytes of a row on its way out: 32 and a gap, so that rows differ in their banks
+constexpr int kStageBytes = kEpiWarps * 32 * kStagePitch;
 constexpr int kShare = 64;                      // most columns of a tile that are one epilogue warp's
 constexpr int kSmem = 227 * 1024;
 constexpr int kStatic = kEpiWarps * kShare * 4 + 512;   // the kernel's own variables
@@ -53,6 +53,7 @@ struct TcArgs {
     int tile_n, stages;
     int chunks, all_chunks, run;        // 64-term chunks of a plane product, of all of them, and of a run
     int planes;
+    unsigned group;                     // rows of tiles that are walked together
     int a_turned, b_turned;
     unsigned idesc;
     int *status;
@@ -127,6 +128,7 @@ __device__ __forceinline__ void commit(uint64_t *bar)
                      : "memory");
 }
 
+// Columns addr .. of this warp's 32 lanes of tensor memory, a row a thread.
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -137,6 +139,79 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[16])
                  : "memory");
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(addr)
+                 : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// A wait of at most a second that leaves no gap between its attempts.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int *status)
+{
+    if (dev::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = dev::global_ns();
+    while (!dev::mbar_try_wait(bar, parity))
+        if (dev::global_ns() - t0 > kWaitLimitNs) {
+            if (status) atomicExch(status, RZ_ERR_TIMEOUT);
+            return false;
+        }
+    return true;
+}
+
+// 32 rows of 32 bytes each through a warp's stage, which turns a row a thread into
+// consecutive bytes of a row for consecutive threads and back: lane / 2 + 16 k is
+// the row of a lane's k-th 16 bytes, lane % 2 their half of it.
+__device__ __forceinline__ void stage_row(uint8_t *stage, const uint4 (&v)[2])
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    reinterpret_cast<uint4 *>(stage + lane * kStagePitch)[0] = v[0];
+    reinterpret_cast<uint4 *>(stage + lane * kStagePitch)[1] = v[1];
+    __syncwarp();
+}
+__device__ __forceinline__ uint4 staged(const uint8_t *stage, int k)
+{
+    const int lane = threadIdx.x & 31;
+    return *reinterpret_cast<const uint4 *>(stage + (lane / 2 + 16 * k) * kStagePitch + lane % 2 * 16);
+}
+
+// A row a thread of PC = 32 / sizeof(T) columns to a matrix: rows from m, columns
+// from n, as far as it reaches; whole vectors or element by element.
+template <class T>
+__device__ __forceinline__ void emit(const Rows &to, const Finish &f, unsigned m, unsigned n, uint8_t *stage,
+                                     const float2 (&z)[16 / sizeof(T)])
+{
+    constexpr int PC = 32 / sizeof(T), VE = PC / 2;
+    using E = Raw<T, 1>;
+    const int lane = threadIdx.x & 31;
+    uint4 v[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        float2 part[VE / 2];
+#pragma unroll
+        for (int i = 0; i < VE / 2; i++) part[i] = z[h * VE / 2 + i];
+        v[h] = pack2<T, VE>(part);
+    }
+    stage_row(stage, v);
+    if (f.wide) {
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const unsigned r = m + lane / 2 + 16 * k, c = n + lane % 2 * VE;
+            if (r < f.M && c < f.N) *vec_at<T, VE>(to, r, c) = staged(stage, k);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < PC; k++) {
+            const int r = k * (32 / PC) + lane / PC, c = lane % PC;
+            if (m + r < f.M && n + c < f.N)
+                *reinterpret_cast<E *>(to.v.p + row_off(to, m + r) + static_cast<long long>(n + c) * sizeof(T)) =
+                    *reinterpret_cast<const E *>(stage + r * kStagePitch + c * sizeof(T));
+        }
+    }
+}
 
 // A tile's place and the chunks of its run.
 struct Tile {
@@ -146,10 +221,11 @@ struct Tile {
 __device__ __forceinline__ Tile tile_at(const TcArgs &a, unsigned t)
 {
     Tile r;
-    r.n = t % a.tiles_n;
-    const unsigned q = t / a.tiles_n;
-    r.m = q % a.tiles_m;
-    r.run = q / a.tiles_m;
+    const unsigned all = a.tiles_m * a.tiles_n, x = t % all, per = a.group * a.tiles_n;
+    const unsigned g = x / per, y = x - g * per, rows = min(a.group, a.tiles_m - g * a.group);
+    r.run = t / all;
+    r.m = g * a.group + y % rows;
+    r.n = y / rows;
     r.first = static_cast<int>(r.run) * a.run;
     r.last = min(a.all_chunks, r.first + a.run);
     return r;
@@ -215,39 +291,44 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
     const uint32_t tmem = tmem_slot;
     grid_dependency_wait();
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 3) {
+        // warp 0 asks for A's tiles, warp 3 for B's: one thread for both spends longer on a stage's requests than the
+        // products take (its waits for a free stage were a fifth of its time)
         if (lane == 0) {
+            const bool of_b = warp == 3;
+            const CUtensorMap *map = of_b ? &map_b : &map_a;
+            const int turned = of_b ? a.b_turned : a.a_turned, boxes = turned ? (of_b ? rows_b : kTileM) : 64;
+            const uint32_t to = ring + (of_b ? kBytesA : 0);
+            const uint32_t bars = CG == 1 ? smem_addr(full) : in_cta(smem_addr(full), 0);
             int s = 0;
             uint32_t phase = 0;
             bool ok = true;
             unsigned asked = 0;
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step) {
                 const Tile w = tile_at(a, t);
+                const int row = of_b ? static_cast<int>(w.n * a.tile_n + rank * rows_b) : static_cast<int>((w.m * CG + rank) * kTileM);
+                int j = w.first / a.chunks, k0 = (w.first - j * a.chunks) * kTerms, pa, pb;
+                planes_of(a.planes, j, pa, pb);
                 for (int c = w.first; c < w.last; c++) {
-                    ok = dev::mbar_wait_bounded(empty + s, phase ^ 1, a.status);
+                    ok = wait_for(empty + s, phase ^ 1, a.status);
                     if (!ok) break;
-                    const int j = c / a.chunks, k0 = (c - j * a.chunks) * kTerms;
-                    int pa, pb;
-                    planes_of(a.planes, j, pa, pb);
-                    const uint32_t sa = ring + s * stage_bytes, sb = sa + kBytesA;
-                    if (rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
-                    const uint32_t bar = CG == 1 ? smem_addr(full + s) : in_cta(smem_addr(full + s), 0);
-                    const int m0 = (w.m * CG + rank) * kTileM, n0 = w.n * a.tile_n + rank * rows_b;
-                    if (a.a_turned) {
-                        load_box<CG>(&map_a, sa, bar, m0, k0, pa);
-                        load_box<CG>(&map_a, sa + 8192, bar, m0 + 64, k0, pa);
+                    if (!of_b && rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
+                    const uint32_t at = to + s * stage_bytes, bar = bars + 8 * s;
+                    const int plane = of_b ? pb : pa;
+                    if (turned) {
+                        for (int i = 0; i < boxes; i += 64) load_box<CG>(map, at + i * 128, bar, row + i, k0, plane);
                     } else {
-                        load_box<CG>(&map_a, sa, bar, k0, m0, pa);
-                    }
-                    if (a.b_turned) {
-                        for (int i = 0; i < rows_b; i += 64) load_box<CG>(&map_b, sb + i * 128, bar, n0 + i, k0, pb);
-                    } else {
-                        load_box<CG>(&map_b, sb, bar, k0, n0, pb);
+                        load_box<CG>(map, at, bar, k0, row, plane);
                     }
                     asked++;
                     if (++s == a.stages) {
                         s = 0;
                         phase ^= 1;
+                    }
+                    k0 += kTerms;
+                    if (k0 >= a.chunks * kTerms) {
+                        k0 = 0;
+                        planes_of(a.planes, ++j, pa, pb);
                     }
                 }
             }
@@ -256,7 +337,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             if (!ok && rank == 0)
                 for (unsigned i = 0; i < min(asked, static_cast<unsigned>(a.stages)); i++) {
                     const unsigned at = asked - 1 - i;
-                    dev::mbar_wait_bounded(full + at % a.stages, at / a.stages & 1, a.status);
+                    wait_for(full + at % a.stages, at / a.stages & 1, a.status);
                 }
         }
     } else if (warp == 1) {
@@ -265,19 +346,20 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             uint32_t phase = 0;
             bool ok = true;
             unsigned i = 0;
+            const uint64_t desc_a = tile_desc(ring, a.a_turned), desc_b = tile_desc(ring + kBytesA, a.b_turned);
             const uint32_t step_a = (a.a_turned ? 2048 : 32) >> 4, step_b = (a.b_turned ? 2048 : 32) >> 4;
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
                 const Tile w = tile_at(a, t);
                 const uint32_t acc = tmem + (i & 1) * 256;
-                ok = dev::mbar_wait_bounded(taken + (i & 1), (i >> 1 & 1) ^ 1, a.status);
+                ok = wait_for(taken + (i & 1), (i >> 1 & 1) ^ 1, a.status);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 for (int c = w.first; c < w.last; c++) {
-                    ok = dev::mbar_wait_bounded(full + s, phase, a.status);
+                    ok = wait_for(full + s, phase, a.status);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t sa = ring + s * stage_bytes;
-                    const uint64_t da = tile_desc(sa, a.a_turned), db = tile_desc(sa + kBytesA, a.b_turned);
+                    const uint32_t at = static_cast<uint32_t>(s * stage_bytes) >> 4;   // the ring lies below 2^18: no carry leaves the address
+                    const uint64_t da = desc_a + at, db = desc_b + at;
 #pragma unroll
                     for (uint32_t k = 0; k < kTerms / 16; k++)
                         mma<CG>(acc, da + k * step_a, db + k * step_b, a.idesc, c > w.first || k > 0);
@@ -291,12 +373,11 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             }
         }
     } else if (warp >= 4) {
-        // four warps share 32 rows, a quarter of the columns each, 16 at a time: out of tensor memory a lane has a row
-        // of them, on the way to memory (through `stage`) a vector of each of the rows below
-        constexpr int VE = 16 / sizeof(T), per_row = 16 / VE, rows = 32 / per_row, steps = 32 / rows;
-        using V = Raw<T, VE>;
-        const int e = warp - 4, quarter = warp & 3, cols = a.tile_n / 4, down = lane / per_row, sub = lane % per_row * VE;
-        float *stage = reinterpret_cast<float *>(raw + pad + a.stages * stage_bytes) + e * 32 * kStagePitch;
+        // four warps share 32 rows of the tile, a quarter of its columns each, 32 bytes of the result's rows at a time
+        constexpr int PC = 32 / sizeof(T), VE = PC / 2;
+        using E = Raw<T, 1>;
+        const int e = warp - 4, quarter = warp & 3, cols = a.tile_n / 4;
+        uint8_t *stage = raw + pad + a.stages * stage_bytes + e * 32 * kStagePitch;
         unsigned i = 0;
         bool ok = true;
         for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
@@ -309,23 +390,24 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                 for (int c = lane; c < cols; c += 32) bias[e][c] = a.f.bias && n0 + c < a.f.N ? __ldg(a.f.bias + n0 + c) : 0.0f;
                 __syncwarp();
             }
-            V next[steps] = {};
-            const bool reads = !a.part && a.f.wide && a.f.has_residual;
+            uint4 next[2] = {};
+            const bool adds = !a.part && a.f.has_residual, ahead = adds && a.f.wide;
             const auto residuals = [&](unsigned n) {
 #pragma unroll
-                for (int k = 0; k < steps; k++)
-                    if (m0 + k * rows + down < a.f.M && n + sub < a.f.N)
-                        next[k] = *vec_at<T, VE>(a.f.residual, m0 + k * rows + down, n + sub);
+                for (int k = 0; k < 2; k++) {
+                    const unsigned r = m0 + lane / 2 + 16 * k, c = n + lane % 2 * VE;
+                    if (r < a.f.M && c < a.f.N) next[k] = *vec_at<T, VE>(a.f.residual, r, c);
+                }
             };
-            if (reads) residuals(n0);
-            ok = dev::mbar_wait_bounded(done + (i & 1), i >> 1 & 1, a.status);
+            if (ahead) residuals(n0);
+            ok = wait_for(done + (i & 1), i >> 1 & 1, a.status);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + from;
-            for (int c0 = 0; c0 < cols; c0 += 16) {
-                uint32_t v[16];
+            for (int c0 = 0; c0 < cols; c0 += PC) {
+                uint32_t v[PC];
                 tmem_load(acc + c0, v);
-                if (c0 + 16 >= cols) {
+                if (c0 + PC >= cols) {
                     // this warp's share of the tile is in registers
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                     if (lane == 0) {
@@ -336,60 +418,71 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                     }
                 }
                 const unsigned n = n0 + c0;
-                if (n >= a.f.N) continue;
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    *reinterpret_cast<uint4 *>(stage + lane * kStagePitch + 4 * k) =
-                        make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                __syncwarp();
+                if (n >= a.f.N || m0 >= a.f.M) continue;
                 if (a.part) {
-                    // a float32 row of the run's part: 16 columns, 4 lanes a row
-                    float *to = a.part + (static_cast<long long>(w.run) * a.f.M + m0) * a.part_pitch + n;
-                    const int c = lane % 4 * 4;
+                    // float32 rows of the run's part
+                    float *to = a.part + static_cast<long long>(w.run) * a.f.M * a.part_pitch;
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const int r = k * 8 + lane / 4;
-                        if (m0 + r < a.f.M && n + c < a.part_pitch)
-                            *reinterpret_cast<float4 *>(to + static_cast<long long>(r) * a.part_pitch + c) =
-                                *reinterpret_cast<const float4 *>(stage + r * kStagePitch + c);
-                    }
-                } else if (a.f.wide) {
-                    V now[steps];
+                    for (int h = 0; h < PC; h += 8) {
+                        const uint4 row[2] = {make_uint4(v[h], v[h + 1], v[h + 2], v[h + 3]),
+                                              make_uint4(v[h + 4], v[h + 5], v[h + 6], v[h + 7])};
+                        stage_row(stage, row);
 #pragma unroll
-                    for (int k = 0; k < steps; k++) now[k] = next[k];
-                    if (reads && c0 + 16 < cols) residuals(n + 16);
-                    if (n + sub < a.f.N) {
-                        float2 b[VE / 2];
-#pragma unroll
-                        for (int q = 0; q < VE; q += 4) {
-                            const float4 v4 = *reinterpret_cast<const float4 *>(&bias[e][c0 + sub + q]);
-                            b[q / 2] = make_float2(v4.x, v4.y);
-                            b[q / 2 + 1] = make_float2(v4.z, v4.w);
-                        }
-#pragma unroll
-                        for (int k = 0; k < steps; k++) {
-                            const int r = k * rows + down;
-                            float2 z[VE / 2];
-#pragma unroll
-                            for (int q = 0; q < VE; q += 4) {
-                                const float4 v4 = *reinterpret_cast<const float4 *>(stage + r * kStagePitch + sub + q);
-                                z[q / 2] = make_float2(v4.x, v4.y);
-                                z[q / 2 + 1] = make_float2(v4.z, v4.w);
-                            }
-                            if (m0 + r < a.f.M) finish<T, VE, ACT>(a.f, m0 + r, n + sub, z, b, now[k]);
+                        for (int k = 0; k < 2; k++) {
+                            const unsigned r = m0 + lane / 2 + 16 * k, c = n + h + lane % 2 * 4;
+                            if (r < a.f.M && c < a.part_pitch)
+                                *reinterpret_cast<uint4 *>(to + static_cast<long long>(r) * a.part_pitch + c) = staged(stage, k);
                         }
                     }
-                } else if (n + lane % 16 < a.f.N) {
-                    const int c = lane % 16;
-#pragma unroll 1
-                    for (int r = lane / 16 * 16; r < lane / 16 * 16 + 16 && m0 + r < a.f.M; r += 8) {
-                        float z[8];
+                    continue;
+                }
+                float2 add[PC / 2];
+                if (adds) {
+                    if (ahead) {
+                        const uint4 now[2] = {next[0], next[1]};
+                        if (c0 + PC < cols) residuals(n + PC);
+                        __syncwarp();
 #pragma unroll
-                        for (int u = 0; u < 8; u++) z[u] = stage[(r + u) * kStagePitch + c];
-                        finish_column<T, ACT, 8>(a.f, m0 + r, n + c, z, bias[e][c0 + c]);
+                        for (int k = 0; k < 2; k++)
+                            *reinterpret_cast<uint4 *>(stage + (lane / 2 + 16 * k) * kStagePitch + lane % 2 * 16) = now[k];
+                    } else {
+                        E now[PC];
+#pragma unroll
+                        for (int k = 0; k < PC; k++) {
+                            const unsigned r = m0 + k * (32 / PC) + lane / PC, c = n + lane % PC;
+                            now[k] = r < a.f.M && c < a.f.N
+                                         ? *reinterpret_cast<const E *>(a.f.residual.v.p + row_off(a.f.residual, r) +
+                                                                        static_cast<long long>(c) * sizeof(T))
+                                         : E{};
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < PC; k++)
+                            *reinterpret_cast<E *>(stage + (k * (32 / PC) + lane / PC) * kStagePitch + lane % PC * sizeof(T)) = now[k];
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        float2 half[VE / 2];
+                        unpack2<T, VE>(reinterpret_cast<const Raw<T, VE> *>(stage + lane * kStagePitch)[h], half);
+#pragma unroll
+                        for (int q = 0; q < VE / 2; q++) add[h * VE / 2 + q] = half[q];
                     }
                 }
+                float2 z[PC / 2];
+#pragma unroll
+                for (int q = 0; q < PC; q += 4) {
+                    const float4 b = *reinterpret_cast<const float4 *>(&bias[e][c0 + q]);
+                    z[q / 2] = __fadd2_rn(make_float2(__uint_as_float(v[q]), __uint_as_float(v[q + 1])), make_float2(b.x, b.y));
+                    z[q / 2 + 1] = __fadd2_rn(make_float2(__uint_as_float(v[q + 2]), __uint_as_float(v[q + 3])), make_float2(b.z, b.w));
+                }
+                if (a.f.has_pre) emit<T>(a.f.pre, a.f, m0, n, stage, z);
+#pragma unroll
+                for (int q = 0; q < PC / 2; q++) z[q] = activated<T, ACT>(z[q]);
+                if (adds)
+#pragma unroll
+                    for (int q = 0; q < PC / 2; q++) z[q] = __fadd2_rn(z[q], add[q]);
+                emit<T>(a.f.out, a.f, m0, n, stage, z);
             }
         }
     }
@@ -491,6 +584,10 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     a.tiles_m = (p.f.M + cg * kTileM - 1) / (cg * kTileM);
     a.tiles_n = (p.f.N + p.tile_n - 1) / p.tile_n;
     a.planes = p.a.planes;
+    // Tiles of a row next to each other read its A at once, and B out of L2 where that holds it (65536 x 1024 x 4096: 341 us,
+    // rows of tiles in groups of eight 373).  A larger B is read once for eight rows of tiles (8192 x 8192 x 8192: 611 us, by
+    // single rows 650).
+    a.group = 2.0 * p.f.N * p.b.terms * p.b.planes > 48e6 ? 8 : 1;
     a.chunks = static_cast<int>((p.a.terms + kTerms - 1) / kTerms);
     a.all_chunks = a.chunks * (a.planes == 1 ? 1 : 6);
     a.run = (a.all_chunks + p.splits - 1) / p.splits;
