@@ -55,6 +55,7 @@ struct TcArgs {
     int planes;
     unsigned group;                     // rows of tiles that are walked together
     int a_turned, b_turned;
+    int a_merged, b_merged;             // a turned operand's rows come in one box
     unsigned idesc;
     int *status;
 };
@@ -62,17 +63,17 @@ struct TcArgs {
 // CG: CTAs that work on one tile, 1 or a pair.  A box of this CTA's share, counted
 // by the barrier at `bar` (of a pair, its first CTA's: an address in the cluster).
 template <int CG>
-__device__ __forceinline__ void load_box(const CUtensorMap *map, uint32_t to, uint32_t bar, int x, int y, int plane)
+__device__ __forceinline__ void load_box(const CUtensorMap *map, uint32_t to, uint32_t bar, int x, int y, int z, int plane)
 {
     if constexpr (CG == 1)
-        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                     "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
-                     "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(plane), "r"(bar)
+        asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
+                     "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(plane), "r"(bar)
                      : "memory");
     else
-        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-                     "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
-                     "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(plane), "r"(bar)
+        asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                     "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
+                     "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(plane), "r"(bar)
                      : "memory");
 }
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
@@ -297,7 +298,8 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
         if (lane == 0) {
             const bool of_b = warp == 3;
             const CUtensorMap *map = of_b ? &map_b : &map_a;
-            const int turned = of_b ? a.b_turned : a.a_turned, boxes = turned ? (of_b ? rows_b : kTileM) : 64;
+            const int turned = of_b ? a.b_turned : a.a_turned, merged = of_b ? a.b_merged : a.a_merged;
+            const int rows = of_b ? rows_b : kTileM;
             const uint32_t to = ring + (of_b ? kBytesA : 0);
             const uint32_t bars = CG == 1 ? smem_addr(full) : in_cta(smem_addr(full), 0);
             int s = 0;
@@ -315,11 +317,12 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                     if (!of_b && rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
                     const uint32_t at = to + s * stage_bytes, bar = bars + 8 * s;
                     const int plane = of_b ? pb : pa;
-                    if (turned) {
-                        for (int i = 0; i < boxes; i += 64) load_box<CG>(map, at + i * 128, bar, row + i, k0, plane);
-                    } else {
-                        load_box<CG>(map, at, bar, k0, row, plane);
-                    }
+                    if (!turned)
+                        load_box<CG>(map, at, bar, k0, row, 0, plane);
+                    else if (merged)
+                        load_box<CG>(map, at, bar, 0, k0, row / 64, plane);
+                    else
+                        for (int i = 0; i < rows; i += 64) load_box<CG>(map, at + i * 128, bar, row + i, k0, 0, plane);
                     asked++;
                     if (++s == a.stages) {
                         s = 0;
@@ -518,16 +521,21 @@ EncodeFn encoder()
     return fn;
 }
 
-// The operand's tensor map: boxes of 64 packed elements by `box` memory rows;
-// what lies outside the matrix reads as 0.
-bool encode(const Operand &o, unsigned box, CUtensorMap *map)
+// The operand's tensor map; what lies outside the matrix reads as 0.  By terms: boxes
+// of 64 terms by `share` rows.  Turned: boxes of 64 rows by 64 terms, as many side
+// by side as the share has where the matrix is made of them (a thread asks for a
+// box in about the time of a stage's products, so two take longer than those: 345
+// against 3xx us on the weight gradient of 65536 x 1024 x 4096).
+bool encode(const Operand &o, unsigned share, CUtensorMap *map, int *merged)
 {
     std::memset(map, 0, sizeof(*map));
-    const cuuint64_t inner = o.turned ? o.rows : o.terms, outer = o.turned ? o.terms : o.rows;
-    const cuuint64_t dims[3] = {inner, outer, static_cast<cuuint64_t>(o.planes)};
-    const cuuint64_t strides[2] = {o.pitch, o.planes > 1 ? o.plane : o.pitch};
-    const cuuint32_t boxes[3] = {kTerms, box, 1}, steps[3] = {1, 1, 1};
-    return encoder()(map, o.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(o.p),
+    *merged = o.turned && o.rows % kTerms == 0;
+    const cuuint64_t outer = o.turned ? o.terms : o.rows;
+    const cuuint64_t dims[4] = {o.turned ? (*merged ? kTerms : o.rows) : o.terms, outer, *merged ? o.rows / kTerms : 1u,
+                                static_cast<cuuint64_t>(o.planes)};
+    const cuuint64_t strides[3] = {o.pitch, *merged ? 2 * kTerms : o.pitch, o.planes > 1 ? o.plane : o.pitch};
+    const cuuint32_t boxes[4] = {kTerms, o.turned ? kTerms : share, *merged ? share / kTerms : 1u, 1}, steps[4] = {1, 1, 1, 1};
+    return encoder()(map, o.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(o.p),
                      dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -572,15 +580,14 @@ cudaError_t tc_launch_of(const TcArgs &a, const CUtensorMap &ma, const CUtensorM
 cudaError_t lin::launch_product(const Product &p, void *stream)
 {
     if (!encoder()) return cudaErrorNotSupported;
+    const int cg = p.pair ? 2 : 1;
     CUtensorMap ma, mb;
-    if (!encode(p.a, p.a.turned ? kTerms : kTileM, &ma) || !encode(p.b, p.b.turned ? kTerms : p.tile_n / (p.pair ? 2 : 1), &mb))
-        return cudaErrorInvalidValue;
     TcArgs a{};
+    if (!encode(p.a, kTileM, &ma, &a.a_merged) || !encode(p.b, p.tile_n / cg, &mb, &a.b_merged)) return cudaErrorInvalidValue;
     a.f = p.f;
     a.part = p.splits > 1 ? p.part : nullptr;
     a.part_pitch = p.part_pitch;
     a.tile_n = p.tile_n;
-    const int cg = p.pair ? 2 : 1;
     a.tiles_m = (p.f.M + cg * kTileM - 1) / (cg * kTileM);
     a.tiles_n = (p.f.N + p.tile_n - 1) / p.tile_n;
     a.planes = p.a.planes;
