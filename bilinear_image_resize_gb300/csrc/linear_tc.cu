@@ -84,7 +84,9 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
 }
 __device__ __forceinline__ void arrive_in_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    // what it orders is reads of tensor memory, which have their own fence: a release in the cluster would wait for the
+    // thread's stores to memory
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cluster_sync()
 {
