@@ -53,6 +53,7 @@ struct PbArgs {
     View scores, out;           // gradient: out is dout
     const float *table;
     float *sums;                // gradient: the units' offset sums
+    float *dense;               // gradient: their totals, [head][row offset][column offset]
     int tq, tk, tx;             // a tile: query rows, key rows, key columns
     int gx, gn;                 // gradient: query columns and batch entries of a unit
     int nq, nk, nx, ngx, ngn;   // tiles and groups along each
@@ -184,6 +185,41 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_whole(const __grid_constant
     }
 }
 
+// s += the vectors at `row`, `count` of them `step` bytes apart, eight read before
+// the first is added.  Of the last few that are missing the last one is read again
+// and not added: a load under a condition waits for the one before it.
+template <class T, int VE>
+__device__ __forceinline__ void add_rows(const uint8_t *row, long long step, int count, float (&s)[VE])
+{
+    using V = Raw<T, VE>;
+    constexpr int B = 8;
+    V x[B];
+    float f[VE];
+    for (; count >= B; count -= B) {
+#pragma unroll
+        for (int u = 0; u < B; u++, row += step) x[u] = __ldcs(reinterpret_cast<const V *>(row));
+#pragma unroll
+        for (int u = 0; u < B; u++) {
+            unpack<T, VE>(x[u], f);
+#pragma unroll
+            for (int j = 0; j < VE; j++) s[j] += f[j];
+        }
+    }
+    if (count <= 0) return;
+#pragma unroll
+    for (int u = 0; u < B; u++) {
+        x[u] = __ldcs(reinterpret_cast<const V *>(row));
+        if (u + 1 < count) row += step;
+    }
+#pragma unroll
+    for (int u = 0; u < B; u++) {
+        unpack<T, VE>(x[u], f);
+#pragma unroll
+        for (int j = 0; j < VE; j++)
+            if (u < count) s[j] += f[j];
+    }
+}
+
 // Gradient: a unit is one head, a tile of rows and keys, gx query columns and gn
 // batch entries; D[e][kx - qx] of it in shared memory, then in its place of `sums`:
 // [head][iq][ik][e][ix][column group][batch group][column], each of full tile size.
@@ -194,7 +230,6 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_whole(const __grid_constant
 template <class T, int VE>
 __global__ void __launch_bounds__(kPbThreads) k_bias_grad(const __grid_constant__ PbArgs a)
 {
-    using V = Raw<T, VE>;
     extern __shared__ float D[];
     grid_launch_dependents();
     unsigned b = blockIdx.x;
@@ -219,7 +254,7 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_grad(const __grid_constant_
     const int sub = subs > 1 ? threadIdx.x / places : 0, first = subs > 1 ? threadIdx.x - sub * places : threadIdx.x;
     const int stride = subs > 1 ? places : kPbThreads;
     for (int qx = g0; qx < g1; qx++) {
-        const long long down = a.out.pitch * a.g.q[1], side = static_cast<long long>(a.g.k[1]) * sizeof(T);
+        const long long side = static_cast<long long>(a.g.k[1]) * sizeof(T), step = a.out.pitch * a.g.q[1] + side;
         for (int p0 = 0; p0 < places; p0 += stride) {
             const int p = p0 + first;
             float s[2][VE];
@@ -233,18 +268,8 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_grad(const __grid_constant_
                     const uint8_t *at = a.out.p + (static_cast<long long>(n) * a.g.heads + head) * a.out.bstride +
                                         (static_cast<long long>(q0) * a.g.q[1] + qx) * a.out.pitch +
                                         (static_cast<long long>(k0 + m) * a.g.k[1] + x0 + v * VE) * sizeof(T);
-#pragma unroll
-                    for (int half = 0; half < 2; half++) {
-                        const int from = half ? wrap : 0, to = half ? nq : wrap;
-                        const uint8_t *row = at + from * (down + side) - (half ? nk * side : 0);
-#pragma unroll 8
-                        for (int i = from; i < to; i++, row += down + side) {
-                            float f[VE];
-                            unpack<T, VE>(__ldcs(reinterpret_cast<const V *>(row)), f);
-#pragma unroll
-                            for (int j = 0; j < VE; j++) s[half][j] += f[j];
-                        }
-                    }
+                    add_rows<T, VE>(at, step, wrap, s[0]);
+                    add_rows<T, VE>(at + wrap * step - nk * side, step, nq - wrap, s[1]);
                 }
             }
             const int c = v * VE + (g1 - 1 - qx);
@@ -270,7 +295,45 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_grad(const __grid_constant_
     }
 }
 
-// A bucket of a head a warp: its offsets' sums over the units that have them.
+// An offset of a head a thread: its sums over the units that have it, in their order.
+__global__ void __launch_bounds__(kPbThreads) k_bias_dense(const __grid_constant__ PbArgs a)
+{
+    grid_launch_dependents();
+    const int down = a.g.q[0] + a.g.k[0] - 1, wide = a.g.q[1] + a.g.k[1] - 1;
+    const long long id = static_cast<long long>(blockIdx.x) * kPbThreads + threadIdx.x;
+    const int off = static_cast<int>(id % wide);
+    const long long up = id / wide;
+    const int ry = static_cast<int>(up % down), head = static_cast<int>(up / down);
+    if (head >= a.g.heads) return;
+    const int rows = a.tq + a.tk - 1, cols = a.gx + a.tx - 1, groups = a.nx * a.ngx * a.ngn;
+    grid_dependency_wait();
+    float s = 0.0f;
+    for (int iq = 0; iq < a.nq; iq++) {
+        const int q1 = min(a.g.q[0], iq * a.tq + a.tq), nq = q1 - iq * a.tq;
+        // the tiles of keys that a row offset ry meets: e = below - k0 of nq + nk - 1 rows
+        const int below = ry - (a.g.q[0] - 1) + (q1 - 1);
+        const int first = max(0, (below - (nq + a.tk - 2) + a.tk - 1) / a.tk), last = min(a.nk - 1, below / a.tk);
+        if (below < 0) continue;
+        for (int ik = first; ik <= last; ik++) {
+            const int k0 = ik * a.tk, e = below - k0;
+            if (e >= nq + min(a.g.k[0], k0 + a.tk) - k0 - 1) continue;
+            const float *row = a.sums + ((static_cast<long long>(head) * a.nq + iq) * a.nk + ik) * rows * groups * cols +
+                               static_cast<long long>(e) * groups * cols;
+            for (int ix = 0; ix < a.nx; ix++) {
+                const int x0 = ix * a.tx, nx = min(a.g.k[1], x0 + a.tx) - x0;
+#pragma unroll 8
+                for (int i = 0; i < a.ngx * a.ngn; i++) {
+                    const int ig = i / a.ngn, g0 = ig * a.gx, g1 = min(a.g.q[1], g0 + a.gx);
+                    const int c = off - x0 + (g1 - 1) - (a.g.q[1] - 1);
+                    if (c >= 0 && c < (g1 - g0) + nx - 1) s += row[(static_cast<long long>(ix) * a.ngx * a.ngn + i) * cols + c];
+                }
+            }
+        }
+    }
+    a.dense[id] = s;
+}
+
+// A bucket of a head a warp: the sums of its offsets.
 __global__ void __launch_bounds__(kPbThreads) k_bias_fold(const __grid_constant__ PbArgs a, float *dtable)
 {
     grid_launch_dependents();
@@ -281,36 +344,22 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_fold(const __grid_constant_
     const int b1 = static_cast<int>(bucket % a.g.buckets[1]);
     const long long b0 = bucket / a.g.buckets[1];
     if (b0 >= a.g.buckets[0]) return;
-    const int rows = a.tq + a.tk - 1, cols = a.gx + a.tx - 1, groups = a.nx * a.ngx * a.ngn;
+    const int down = a.g.q[0] + a.g.k[0] - 1, wide = a.g.q[1] + a.g.k[1] - 1;
     grid_dependency_wait();
+    const float *from = a.dense + static_cast<long long>(head) * down * wide;
     float s = 0.0f;
-    for (int iq = 0; iq < a.nq; iq++)
-        for (int ik = 0; ik < a.nk; ik++) {
-            const int q1 = min(a.g.q[0], iq * a.tq + a.tq), nq = q1 - iq * a.tq, nk = min(a.g.k[0], ik * a.tk + a.tk) - ik * a.tk;
-            const float *tile = a.sums + ((static_cast<long long>(head) * a.nq + iq) * a.nk + ik) * rows * groups * cols;
-            const int *lut = a.g.lut[0] + ik * a.tk - (q1 - 1) + a.g.q[0] - 1;
-            const auto add = [&](int e, int from, int step) {
-                const float *row = tile + static_cast<long long>(e) * groups * cols;
-                for (int i = from; i < groups * cols; i += step) {
-                    const int group = i / cols, c = i - group * cols;
-                    const int gxn = group / a.ngn, ix = gxn / a.ngx, ig = gxn - ix * a.ngx;
-                    const int g1 = min(a.g.q[1], ig * a.gx + a.gx), x1 = min(a.g.k[1], ix * a.tx + a.tx);
-                    const int off = c + ix * a.tx - (g1 - 1) + a.g.q[1] - 1;
-                    // past the unit's last offset, where its columns or keys end early
-                    if (c >= (g1 - ig * a.gx) + (x1 - ix * a.tx) - 1) continue;
-                    if (__ldg(a.g.lut[1] + off) == b1) s += row[i];
-                }
-            };
-            for (int e0 = 0; e0 < nq + nk - 1; e0 += 32) {
-                const bool has = e0 + lane < nq + nk - 1 && __ldg(lut + e0 + lane) == b0;
-                if (groups * cols <= 8) {       // rows of a few sums: one a lane
-                    if (has) add(e0 + lane, 0, 1);
-                } else {
-                    for (unsigned left = __ballot_sync(0xffffffffu, has); left; left &= left - 1)
-                        add(e0 + __ffs(left) - 1, lane, 32);
-                }
-            }
+    const auto add = [&](int r, int c0, int step) {
+        for (int c = c0; c < wide; c += step)
+            if (__ldg(a.g.lut[1] + c) == b1) s += from[static_cast<long long>(r) * wide + c];
+    };
+    for (int r0 = 0; r0 < down; r0 += 32) {
+        const bool has = r0 + lane < down && __ldg(a.g.lut[0] + r0 + lane) == b0;
+        if (wide <= 8) {        // rows of a few offsets: one a lane
+            if (has) add(r0 + lane, 0, 1);
+        } else {
+            for (unsigned left = __ballot_sync(0xffffffffu, has); left; left &= left - 1) add(r0 + __ffs(left) - 1, lane, 32);
         }
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) dtable[b0 * a.g.step[0] + b1 * a.g.step[1] + head] = s;
@@ -396,11 +445,11 @@ void pb_plan_grad(PbArgs &a)
         a.tq = std::min(a.g.q[0], a.g.k[0] - (ceil_div(a.g.k[0], a.tk) - 1) * a.tk);
     };
     rows();
-    a.tx = std::min(a.g.k[1], 256);
-    a.gx = std::min(a.g.q[1], 256);
+    a.tx = std::min(a.g.k[1], 128);
+    a.gx = std::min(a.g.q[1], 128);
     const auto panel = [&] { return static_cast<long long>(a.tq + a.tk - 1) * (a.gx + a.tx - 1); };
     // a unit's columns first, then its rows
-    while (panel() > kPbFloats / 2 && a.gx > 1) a.gx = (a.gx + 1) / 2;
+    while (panel() > kPbFloats && a.gx > 32) a.gx = (a.gx + 1) / 2;
     while (panel() > kPbFloats && most > 8) {
         most /= 2;
         rows();
@@ -417,11 +466,18 @@ void pb_plan_grad(PbArgs &a)
 }
 
 long long pb_units(const PbArgs &a) { return static_cast<long long>(a.nk) * a.nx * a.ngx * a.nq * a.ngn * a.g.heads; }
-size_t pb_bytes(const PbArgs &a)
+// The workspace: the units' sums, then their totals.
+size_t pb_dense_at(const PbArgs &a)
 {
-    return sizeof(float) * static_cast<size_t>(pb_units(a)) * static_cast<size_t>(a.tq + a.tk - 1) *
-           static_cast<size_t>(a.gx + a.tx - 1);
+    return (sizeof(float) * static_cast<size_t>(pb_units(a)) * static_cast<size_t>(a.tq + a.tk - 1) *
+                static_cast<size_t>(a.gx + a.tx - 1) + 255) / 256 * 256;
 }
+long long pb_offsets(const PbArgs &a)
+{
+    return static_cast<long long>(a.g.q[0] + a.g.k[0] - 1) * (a.g.q[1] + a.g.k[1] - 1) * a.g.heads;
+}
+size_t pb_bytes(const PbArgs &a) { return pb_dense_at(a) + sizeof(float) * static_cast<size_t>(pb_offsets(a)); }
+bool pb_too_many(const PbArgs &a) { return pb_units(a) > 0x7fffffffLL || pb_offsets(a) / kPbThreads >= 0x7fffffffLL; }
 
 int pb_status(cudaError_t e)
 {
@@ -518,7 +574,7 @@ int map_position_bias_grad_workspace(const rz_bias *d, size_t *bytes)
     PbArgs a{};
     pb_grid(d, nullptr, nullptr, a.g);
     pb_plan_grad(a);
-    if (pb_units(a) > 0x7fffffffLL) return RZ_ERR_UNSUPPORTED;
+    if (pb_too_many(a)) return RZ_ERR_UNSUPPORTED;
     *bytes = pb_bytes(a);
     return RZ_OK;
 }
@@ -538,10 +594,11 @@ int map_position_bias_grad(const rz_bias *d, const rz_map *dout, const int *rows
     PbArgs a{};
     pb_grid(d, rows, cols, a.g);
     pb_plan_grad(a);
-    if (pb_units(a) > 0x7fffffffLL) return RZ_ERR_UNSUPPORTED;
+    if (pb_too_many(a)) return RZ_ERR_UNSUPPORTED;
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < pb_bytes(a)) return RZ_ERR_ARG;
     a.out = maps::view(dout);
     a.sums = static_cast<float *>(workspace);
+    a.dense = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + pb_dense_at(a));
     // the widest vectors that every row, key row and tile of columns is made of
     int ve = 16 / static_cast<int>(s.es);
     while (ve > 1 && (a.g.k[1] % ve || a.tx % ve || !maps::map_aligned(*dout, s, ve * s.es))) ve /= 2;
@@ -552,6 +609,9 @@ int map_position_bias_grad(const rz_bias *d, const rz_map *dout, const int *rows
         e = pb_grad_of<__nv_bfloat16>(a, ve, stream);
     else
         e = pb_grad_of<__half>(a, ve, stream);
+    if (e == cudaSuccess)
+        e = maps::launch(k_bias_dense, dim3(static_cast<unsigned>((pb_offsets(a) + kPbThreads - 1) / kPbThreads)), kPbThreads, 0,
+                         stream, a);
     if (e == cudaSuccess)
         e = maps::launch(k_bias_fold, dim3(static_cast<unsigned>((buckets * d->heads + kPbWarps - 1) / kPbWarps)), kPbThreads, 0,
                          stream, a, dtable);
