@@ -192,7 +192,7 @@ template <class T, int VE>
 __device__ __forceinline__ void add_rows(const uint8_t *row, long long step, int count, float (&s)[VE])
 {
     using V = Raw<T, VE>;
-    constexpr int B = 8;
+    constexpr int B = VE <= 2 ? 16 : 8;
     V x[B];
     float f[VE];
     for (; count >= B; count -= B) {
@@ -320,13 +320,16 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_dense(const __grid_constant
             const float *row = a.sums + ((static_cast<long long>(head) * a.nq + iq) * a.nk + ik) * rows * groups * cols +
                                static_cast<long long>(e) * groups * cols;
             for (int ix = 0; ix < a.nx; ix++) {
-                const int x0 = ix * a.tx, nx = min(a.g.k[1], x0 + a.tx) - x0;
+                // column groups with this offset: from the first with a column g < q and g + at >= 0, to the last whose
+                // first column has g + at < nx; its place in a group's sums is at + the group's last column
+                const int x0 = ix * a.tx, nx = min(a.g.k[1], x0 + a.tx) - x0, at = off - x0 - (a.g.q[1] - 1);
+                if (at + a.g.q[1] < 1 || at >= nx) continue;
+                const int from = at < 0 ? -at / a.gx : 0, to = min(a.ngx, (nx - at + a.gx - 1) / a.gx);
+                const float *group = row + static_cast<long long>(ix) * a.ngx * a.ngn * cols + at - 1;
+                for (int i = 0; i < a.ngn; i++, group += cols)
 #pragma unroll 8
-                for (int i = 0; i < a.ngx * a.ngn; i++) {
-                    const int ig = i / a.ngn, g0 = ig * a.gx, g1 = min(a.g.q[1], g0 + a.gx);
-                    const int c = off - x0 + (g1 - 1) - (a.g.q[1] - 1);
-                    if (c >= 0 && c < (g1 - g0) + nx - 1) s += row[(static_cast<long long>(ix) * a.ngx * a.ngn + i) * cols + c];
-                }
+                    for (int ig = from; ig < to; ig++)
+                        s += group[static_cast<long long>(ig) * a.ngn * cols + min(a.g.q[1], ig * a.gx + a.gx)];
             }
         }
     }
