@@ -30,114 +30,114 @@ constexpr int kQkSms = 152;
 constexpr int kQkThreads = 256;
 constexpr int kQkWarps = kQkThreads / 32;
 constexpr int kQkMaxD = 256;
-constexpr int kQkBlocks = 4 * kQkSms;   // most CTAs of a gradient call, each with a row of partial sums
+constexpr int kQkBlocks = 4 * kQkSms;   // most CTAs of a call, each of a gradient's with a row of partial sums
 
 struct QkArgs {
     View x, y, dy;              // forward: x -> y; gradient: x, dy -> y
-    const float *gq, *gk;
+    const float *g[2];          // of queries and keys
     const int *pos;             // null: the pixel's place
-    float *part;                // gradient: [blocks][D] partial sums, or null
-    unsigned tokens, HW, W;
+    float *part;                // gradient: [blocks][2][D] partial sums, or null
+    unsigned tokens, H, W;
     int x_px, y_px, dy_px;      // bytes of a pixel
-    int x_joined, y_joined, dy_joined;
-    int q_heads, k_heads, D;
+    int q_heads, heads, D;
     int lanes;                  // lanes of a head's group
     int chunks;                 // runs of heads a token is cut into, for calls of few tokens
-    unsigned q_blocks;          // CTAs of the query heads; the others take the key heads
-    int row_pairs, pairs;
+    int row_pairs;
     float eps, inv_d;
     unsigned long long turn[kQkMaxD / 2];   // a position step's angle in 2^-64 turns
 };
 
 // Cosine and sine of position * turn: the product's low 64 bits are the angle
-// modulo a turn, exactly; its top 32 bits go on as a signed float.
+// modulo a turn, exactly; its top 32 bits go on as a signed float.  16-bit results
+// take the GPU's approximate functions, off by 2^-21.2 in [-pi, pi].
+template <class T>
 __device__ __forceinline__ void turned(int p, unsigned long long turn, float &c, float &s)
 {
     const unsigned long long f = static_cast<unsigned long long>(static_cast<long long>(p)) * turn;
-    sincospif(static_cast<float>(static_cast<int>(f >> 32)) * 0x1p-31f, &s, &c);
+    const float half_turns = static_cast<float>(static_cast<int>(f >> 32)) * 0x1p-31f;
+    if constexpr (sizeof(T) == 4)
+        sincospif(half_turns, &s, &c);
+    else
+        __sincosf(half_turns * 3.14159265f, &s, &c);
 }
 
-__device__ __forceinline__ long long token_off(unsigned n, unsigned px, const View &v, unsigned W, int joined, int bytes)
-{
-    return n * v.bstride + pixel_off(px, W, joined != 0, v.pitch, bytes);
-}
-
-// VE: elements of a vector, NV: vectors a lane holds of each half.  INTER: pairs
-// are neighbours.  A lane's pairs are (lo[i], hi[i]), or, of neighbours, those
-// inside lo and then those inside hi (VE 1: lo and hi are neighbours).
+// A head's vectors as pairs' members, two pairs at a time.  VE: elements of a
+// vector; INTER: pairs are neighbours.  Pair i of a lane is (lo[i], hi[i]), or, of
+// neighbours, those inside lo and then those inside hi (VE 1: lo and hi are
+// neighbours).
 template <int VE, bool INTER>
-__device__ __forceinline__ void to_pairs(const float (&lo)[VE], const float (&hi)[VE], float (&a)[VE], float (&b)[VE])
+__device__ __forceinline__ void to_pairs(const float (&lo)[VE], const float (&hi)[VE], float2 (&a)[kPairs<VE>], float2 (&b)[kPairs<VE>])
 {
 #pragma unroll
-    for (int i = 0; i < VE; i++) {
-        if (INTER && VE > 1) {
-            a[i] = i < VE / 2 ? lo[(2 * i) % VE] : hi[(2 * i) % VE];
-            b[i] = i < VE / 2 ? lo[(2 * i) % VE + 1] : hi[(2 * i) % VE + 1];
+    for (int i = 0; i < kPairs<VE>; i++) {
+        if constexpr (VE == 1) {
+            a[i] = make_float2(lo[0], 0.0f);
+            b[i] = make_float2(hi[0], 0.0f);
+        } else if constexpr (INTER) {
+            const float(&v)[VE] = i < VE / 4 ? lo : hi;
+            const int k = 4 * i % VE;
+            a[i] = make_float2(v[k], v[k + 2]);
+            b[i] = make_float2(v[k + 1], v[k + 3]);
         } else {
-            a[i] = lo[i];
-            b[i] = hi[i];
+            a[i] = make_float2(lo[2 * i], lo[2 * i + 1]);
+            b[i] = make_float2(hi[2 * i], hi[2 * i + 1]);
         }
     }
 }
 template <int VE, bool INTER>
-__device__ __forceinline__ void from_pairs(const float (&a)[VE], const float (&b)[VE], float (&lo)[VE], float (&hi)[VE])
+__device__ __forceinline__ void from_pairs(const float2 (&a)[kPairs<VE>], const float2 (&b)[kPairs<VE>], float (&lo)[VE], float (&hi)[VE])
 {
 #pragma unroll
-    for (int i = 0; i < VE; i++) {
-        if (INTER && VE > 1) {
-            lo[i] = (i & 1) ? b[i / 2] : a[i / 2];
-            hi[i] = (i & 1) ? b[VE / 2 + i / 2] : a[VE / 2 + i / 2];
+    for (int i = 0; i < kPairs<VE>; i++) {
+        if constexpr (VE == 1) {
+            lo[0] = a[i].x;
+            hi[0] = b[i].x;
+        } else if constexpr (INTER) {
+            float(&v)[VE] = i < VE / 4 ? lo : hi;
+            const int k = 4 * i % VE;
+            v[k] = a[i].x;
+            v[k + 1] = b[i].x;
+            v[k + 2] = a[i].y;
+            v[k + 3] = b[i].y;
         } else {
-            lo[i] = a[i];
-            hi[i] = b[i];
+            lo[2 * i] = a[i].x;
+            lo[2 * i + 1] = a[i].y;
+            hi[2 * i] = b[i].x;
+            hi[2 * i + 1] = b[i].y;
         }
     }
 }
 
-// What a lane holds of every head: the channels of its vectors, their gammas and
-// its pairs' numbers.
-template <class T, int VE, int NV, bool INTER>
+// What a lane has of every head: vector v of its first half begins at channel
+// lo(v), the matching one of the second half at hi(v).
+template <int VE, bool INTER>
 struct QkLane {
-    int lo[NV], hi[NV], pair[NV];   // first channel of either vector; the first pair (of hi's half where INTER: + half / 2)
-    bool on[NV];
-    float ga[NV][VE], gb[NV][VE];
-    float cs[NV][VE], sn[NV][VE];
-
-    __device__ __forceinline__ void place(int sub, int lanes, int half)
+    int sub, lanes, half;
+    __device__ __forceinline__ int idx(int v) const { return sub + v * lanes; }
+    __device__ __forceinline__ bool on(int v) const { return idx(v) * VE < half; }
+    __device__ __forceinline__ int lo(int v) const { return INTER && VE == 1 ? 2 * idx(v) : idx(v) * VE; }
+    __device__ __forceinline__ int hi(int v) const { return INTER && VE == 1 ? 2 * idx(v) + 1 : half + idx(v) * VE; }
+    // The lane's entries of a table with one for each pair: those of VE pairs in a
+    // row, or, of neighbours, of half as many inside each vector.
+    __device__ __forceinline__ void pairs(const float *t, int v, float2 (&out)[kPairs<VE>]) const
     {
+        if constexpr (VE == 1) {
+            out[0] = make_float2(t[idx(v)], 0.0f);
+        } else {
 #pragma unroll
-        for (int v = 0; v < NV; v++) {
-            const int idx = sub + v * lanes;
-            on[v] = idx * VE < half;
-            lo[v] = INTER && VE == 1 ? 2 * idx : idx * VE;
-            hi[v] = INTER && VE == 1 ? 2 * idx + 1 : half + idx * VE;
-            pair[v] = INTER && VE > 1 ? idx * VE / 2 : idx * VE;
-        }
-    }
-    __device__ __forceinline__ void gammas(const float *g)
-    {
-#pragma unroll
-        for (int v = 0; v < NV; v++) {
-            float l[VE], h[VE];
-#pragma unroll
-            for (int i = 0; i < VE; i++) {
-                l[i] = g && on[v] ? g[lo[v] + i] : 1.0f;
-                h[i] = g && on[v] ? g[hi[v] + i] : 1.0f;
+            for (int i = 0; i < VE / 2; i += 2) {
+                const int at = !INTER ? idx(v) * VE + 2 * i : i < VE / 4 ? idx(v) * VE / 2 + 2 * i : (half + idx(v) * VE) / 2 + 2 * i - VE / 2;
+                if constexpr (VE == 4 && INTER) {
+                    const int second = (half + idx(v) * VE) / 2;
+                    out[0] = *reinterpret_cast<const float2 *>(t + idx(v) * VE / 2);
+                    out[1] = *reinterpret_cast<const float2 *>(t + second);
+                } else {
+                    const float4 q = *reinterpret_cast<const float4 *>(t + at);
+                    out[i] = make_float2(q.x, q.y);
+                    out[i + 1] = make_float2(q.z, q.w);
+                }
             }
-            to_pairs<VE, INTER>(l, h, ga[v], gb[v]);
         }
-    }
-    __device__ __forceinline__ void angles(const unsigned long long *turn, int row, int col, int row_pairs, int half)
-    {
-#pragma unroll
-        for (int v = 0; v < NV; v++)
-#pragma unroll
-            for (int i = 0; i < VE; i++) {
-                int j = pair[v] + i;
-                if (INTER && VE > 1 && i >= VE / 2) j += (half - VE) / 2;
-                if (!on[v]) j = 0;
-                turned(j < row_pairs ? row : col, turn[j], cs[v][i], sn[v][i]);
-            }
     }
 };
 
@@ -147,134 +147,247 @@ __device__ __forceinline__ float group_sum(float v, int lanes)
     return v;
 }
 
-// One warp takes a token's heads (or a run of them) at a time, U groups' vectors
-// read before the first is used.
+// Tables of a token, an entry for each pair.  Forward, for queries and keys each,
+// gamma and the turn as one: cos ga, -sin gb, sin ga, cos gb.  Gradient: cos, sin,
+// -sin.  (Gamma by pairs' members follows the tables.)
+constexpr int kQkTables = 8, kQkGradTables = 3;
+__host__ __device__ constexpr int qk_row(int half) { return (half + 3) / 4 * 4; }
+
+// A warp takes a token (or a run of the heads of few tokens) at a time: while its
+// first vectors are on their way it works out the token's turns, once for all of
+// its heads, into shared memory of its own.  U: groups' vectors read before the
+// first is used.
 template <class T, int VE, int NV, bool INTER, bool GRAD, int U>
-__global__ void __launch_bounds__(kQkThreads) k_qk_norm(const __grid_constant__ QkArgs a)
+__global__ void __launch_bounds__(kQkThreads, NV == 1 ? (GRAD ? 2 : 4) : 1) k_qk_norm(const __grid_constant__ QkArgs a)
 {
     using V = Raw<T, VE>;
+    constexpr int P = kPairs<VE>;
+    extern __shared__ float4 shared[];
     __shared__ unsigned long long turn[kQkMaxD / 2];
-    __shared__ float sums[GRAD ? kQkWarps : 1][GRAD ? kQkMaxD : 1];
     grid_launch_dependents();
-    const int half = a.D / 2;
+    const int half = a.D / 2, row = qk_row(half);
     for (int i = threadIdx.x; i < half; i += kQkThreads) turn[i] = a.turn[i];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool keys = blockIdx.x >= a.q_blocks;
-    const unsigned block = keys ? blockIdx.x - a.q_blocks : blockIdx.x;
-    const unsigned blocks = keys ? gridDim.x - a.q_blocks : a.q_blocks;
-    const int heads = keys ? a.k_heads : a.q_heads, first = keys ? a.q_heads : 0;
     const int lanes = a.lanes, at_once = 32 / lanes, group = lane / lanes;
-    QkLane<T, VE, NV, INTER> k;
-    k.place(lane & (lanes - 1), lanes, half);
-    __syncthreads();
+    const QkLane<VE, INTER> k{lane & (lanes - 1), lanes, half};
+    float *tables = reinterpret_cast<float *>(shared) + warp * (GRAD ? kQkGradTables : kQkTables) * row;
+    float *gammas = reinterpret_cast<float *>(shared) + kQkWarps * (GRAD ? kQkGradTables : kQkTables) * row;    // [part][member][row]
     grid_dependency_wait();
-    k.gammas(keys ? a.gk : a.gq);
-    float da[NV][VE], db[NV][VE];
+    for (int i = threadIdx.x; i < 4 * half; i += kQkThreads) {
+        const int part = i / (2 * half), member = i / half % 2, j = i % half;
+        const float *g = a.g[part];
+        gammas[(i / half) * row + j] = g ? g[INTER ? 2 * j + member : j + member * half] : 1.0f;
+    }
+    __syncthreads();
+    float2 da[GRAD ? 2 : 1][NV][P], db[GRAD ? 2 : 1][NV][P];
     if (GRAD) {
 #pragma unroll
-        for (int v = 0; v < NV; v++)
+        for (int part = 0; part < 2; part++)
 #pragma unroll
-            for (int i = 0; i < VE; i++) da[v][i] = db[v][i] = 0.0f;
+            for (int v = 0; v < NV; v++)
+#pragma unroll
+                for (int i = 0; i < P; i++) da[part][v][i] = db[part][v][i] = both(0.0f);
     }
-    const int chunk = (heads + a.chunks - 1) / a.chunks;
+    const int chunk = (a.heads + a.chunks - 1) / a.chunks;
     const unsigned long long items = static_cast<unsigned long long>(a.tokens) * a.chunks;
-    for (unsigned long long item = static_cast<unsigned long long>(block) * kQkWarps + warp; item < items;
-         item += static_cast<unsigned long long>(blocks) * kQkWarps) {
-        const unsigned t = static_cast<unsigned>(a.chunks == 1 ? item : item / a.chunks);
-        const int h0 = static_cast<int>(item - static_cast<unsigned long long>(t) * a.chunks) * chunk;
-        const int h1 = min(heads, h0 + chunk);
-        const unsigned n = t / a.HW, px = t - n * a.HW;
-        const uint8_t *xt = a.x.p + token_off(n, px, a.x, a.W, a.x_joined, a.x_px);
-        const uint8_t *dt = GRAD ? a.dy.p + token_off(n, px, a.dy, a.W, a.dy_joined, a.dy_px) : nullptr;
-        uint8_t *yt = a.y.p + token_off(n, px, a.y, a.W, a.y_joined, a.y_px);
-        bool ready = false;
-        for (int h = h0; h < h1; h += U * at_once) {
-            V x[U][NV][2], d[GRAD ? U : 1][NV][2];
+    const unsigned step = gridDim.x * kQkWarps;
+    // the token's place, stepped on: n, h, w
+    unsigned n = 0, h = 0, w = 0;
+    const auto place = [&](unsigned t) {
+        const unsigned r = t / a.W;
+        w = t - r * a.W;
+        n = r / a.H;
+        h = r - n * a.H;
+    };
+    unsigned dn, dh, dw;
+    place(step);
+    dn = n, dh = h, dw = w;
+    bool first = true;
+    for (unsigned long long item = static_cast<unsigned long long>(blockIdx.x) * kQkWarps + warp; item < items; item += step) {
+        unsigned t;
+        int h0 = 0, h1 = a.heads;
+        if (a.chunks == 1) {
+            t = static_cast<unsigned>(item);
+            if (first) {
+                place(t);
+            } else {
+                w += dw;
+                h += dh + (w >= a.W ? 1 : 0);
+                if (w >= a.W) w -= a.W;
+                n += dn + (h >= a.H ? 1 : 0);
+                if (h >= a.H) h -= a.H;
+            }
+            first = false;
+        } else {
+            t = static_cast<unsigned>(item / a.chunks);
+            h0 = static_cast<int>(item - static_cast<unsigned long long>(t) * a.chunks) * chunk;
+            h1 = min(a.heads, h0 + chunk);
+            place(t);
+        }
+        const auto at = [&](const View &m, int px) { return m.p + n * m.bstride + h * m.pitch + static_cast<long long>(w) * px; };
+        const uint8_t *xt = at(a.x, a.x_px), *dt = GRAD ? at(a.dy, a.dy_px) : nullptr;
+        uint8_t *yt = at(a.y, a.y_px);
+        V x[U][NV][2], d[GRAD ? U : 1][NV][2];
+        const auto read = [&](int from, int to) {
 #pragma unroll
             for (int u = 0; u < U; u++)
 #pragma unroll
                 for (int v = 0; v < NV; v++) {
-                    const int hd = h + u * at_once + group;
-                    const long long off = static_cast<long long>(first + hd) * a.D;
-                    if (hd < h1 && k.on[v]) {
-                        x[u][v][0] = __ldcs(reinterpret_cast<const V *>(xt + (off + k.lo[v]) * sizeof(T)));
-                        x[u][v][1] = __ldcs(reinterpret_cast<const V *>(xt + (off + k.hi[v]) * sizeof(T)));
+                    const int hd = from + u * at_once + group;
+                    const int lo = (hd * a.D + k.lo(v)) * static_cast<int>(sizeof(T)), hi = (hd * a.D + k.hi(v)) * static_cast<int>(sizeof(T));
+                    if (hd < to && k.on(v)) {
+                        x[u][v][0] = __ldcs(reinterpret_cast<const V *>(xt + lo));
+                        x[u][v][1] = __ldcs(reinterpret_cast<const V *>(xt + hi));
                         if (GRAD) {
-                            d[u][v][0] = __ldcs(reinterpret_cast<const V *>(dt + (off + k.lo[v]) * sizeof(T)));
-                            d[u][v][1] = __ldcs(reinterpret_cast<const V *>(dt + (off + k.hi[v]) * sizeof(T)));
+                            d[u][v][0] = __ldcs(reinterpret_cast<const V *>(dt + lo));
+                            d[u][v][1] = __ldcs(reinterpret_cast<const V *>(dt + hi));
                         }
                     } else {
                         x[u][v][0] = x[u][v][1] = V{};
                         if (GRAD) d[u][v][0] = d[u][v][1] = V{};
                     }
                 }
-            if (!ready) {
-                // under the first vectors' flight
-                const unsigned prow = px / a.W;
-                int row = static_cast<int>(prow), col = static_cast<int>(px - prow * a.W);
-                if (a.pos) {
-                    const int2 p = reinterpret_cast<const int2 *>(a.pos)[t];
-                    row = p.x;
-                    col = p.y;
+        };
+        const auto pairs_of = [&](const V(&raw)[2], float2(&pa)[P], float2(&pb)[P]) {
+            float lo[VE], hi[VE];
+            unpack<T, VE>(raw[0], lo);
+            unpack<T, VE>(raw[1], hi);
+            to_pairs<VE, INTER>(lo, hi, pa, pb);
+        };
+        const auto write = [&](int hd, int v, const float2(&pa)[P], const float2(&pb)[P]) {
+            float lo[VE], hi[VE];
+            from_pairs<VE, INTER>(pa, pb, lo, hi);
+            *reinterpret_cast<V *>(yt + (hd * a.D + k.lo(v)) * static_cast<int>(sizeof(T))) = pack<T, VE>(lo);
+            *reinterpret_cast<V *>(yt + (hd * a.D + k.hi(v)) * static_cast<int>(sizeof(T))) = pack<T, VE>(hi);
+        };
+        const int first_to = GRAD ? min(h1, max(h0, a.q_heads)) : h1;   // the gradient takes queries and keys one after another
+        read(h0, GRAD && h0 >= a.q_heads ? h1 : first_to);
+        // the turns, under the vectors' flight
+        int2 p = make_int2(static_cast<int>(h), static_cast<int>(w));
+        if (a.pos) p = __ldg(reinterpret_cast<const int2 *>(a.pos) + t);
+        __syncwarp();
+        for (int j = lane; j < half; j += 32) {
+            float c, s;
+            turned<T>(j < a.row_pairs ? p.x : p.y, turn[j], c, s);
+            if (GRAD) {
+                tables[j] = c;
+                tables[row + j] = s;
+                tables[2 * row + j] = -s;
+            } else {
+#pragma unroll
+                for (int part = 0; part < 2; part++) {
+                    const float ga = gammas[2 * part * row + j], gb = gammas[(2 * part + 1) * row + j];
+                    float *to = tables + part * 4 * row + j;
+                    to[0] = c * ga;
+                    to[row] = -s * gb;
+                    to[2 * row] = s * ga;
+                    to[3 * row] = c * gb;
                 }
-                k.angles(turn, row, col, a.row_pairs, half);
-                ready = true;
             }
+        }
+        __syncwarp();
+        if constexpr (!GRAD) {
+            for (int from = h0; from < h1; from += U * at_once) {
+                if (from != h0) read(from, h1);
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                if (h + u * at_once >= h1) break;   // the same for the whole warp
-                const int hd = h + u * at_once + group;
-                const long long off = static_cast<long long>(first + hd) * a.D;
-                float xa[NV][VE], xb[NV][VE], wa[NV][VE], wb[NV][VE];
-                float s1 = 0.0f, s2 = 0.0f;
+                for (int u = 0; u < U; u++) {
+                    if (from + u * at_once >= h1) break;    // the same for the whole warp
+                    const int hd = from + u * at_once + group;
+                    float2 xa[NV][P], xb[NV][P], s = both(0.0f);
 #pragma unroll
-                for (int v = 0; v < NV; v++) {
-                    float lo[VE], hi[VE];
-                    unpack<T, VE>(x[u][v][0], lo);
-                    unpack<T, VE>(x[u][v][1], hi);
-                    to_pairs<VE, INTER>(lo, hi, xa[v], xb[v]);
+                    for (int v = 0; v < NV; v++) {
+                        pairs_of(x[u][v], xa[v], xb[v]);
 #pragma unroll
-                    for (int i = 0; i < VE; i++) s1 = fmaf(xa[v][i], xa[v][i], fmaf(xb[v][i], xb[v][i], s1));
-                    if (GRAD) {
-                        float ya[VE], yb[VE];
-                        unpack<T, VE>(d[u][v][0], lo);
-                        unpack<T, VE>(d[u][v][1], hi);
-                        to_pairs<VE, INTER>(lo, hi, ya, yb);
+                        for (int i = 0; i < P; i++) s = __ffma2_rn(xa[v][i], xa[v][i], __ffma2_rn(xb[v][i], xb[v][i], s));
+                    }
+                    const float r = rsqrtf(fmaf(group_sum(s.x + s.y, lanes), a.inv_d, a.eps));
+                    const float *tab = tables + (hd < a.q_heads ? 0 : 4 * row);
 #pragma unroll
-                        for (int i = 0; i < VE; i++) {
-                            // turned back; dg's term lacks r, w has gamma
-                            wa[v][i] = fmaf(ya[i], k.cs[v][i], yb[i] * k.sn[v][i]);
-                            wb[v][i] = fmaf(yb[i], k.cs[v][i], -ya[i] * k.sn[v][i]);
-                            s2 = fmaf(wa[v][i] * k.ga[v][i], xa[v][i], fmaf(wb[v][i] * k.gb[v][i], xb[v][i], s2));
-                        }
+                    for (int v = 0; v < NV; v++) {
+                        if (hd >= h1 || !k.on(v)) continue;
+                        float2 t[P], oa[P], ob[P];
+                        k.pairs(tab, v, t);
+#pragma unroll
+                        for (int i = 0; i < P; i++) oa[i] = __fmul2_rn(xa[v][i], t[i]);
+                        k.pairs(tab + row, v, t);
+#pragma unroll
+                        for (int i = 0; i < P; i++) oa[i] = __fmul2_rn(__ffma2_rn(xb[v][i], t[i], oa[i]), both(r));
+                        k.pairs(tab + 2 * row, v, t);
+#pragma unroll
+                        for (int i = 0; i < P; i++) ob[i] = __fmul2_rn(xa[v][i], t[i]);
+                        k.pairs(tab + 3 * row, v, t);
+#pragma unroll
+                        for (int i = 0; i < P; i++) ob[i] = __fmul2_rn(__ffma2_rn(xb[v][i], t[i], ob[i]), both(r));
+                        write(hd, v, oa, ob);
                     }
                 }
-                s1 = group_sum(s1, lanes);
-                if (GRAD) s2 = group_sum(s2, lanes);
-                const float r = rsqrtf(fmaf(s1, a.inv_d, a.eps));
-                const float m = GRAD ? r * r * r * (s2 * a.inv_d) : 0.0f;
+            }
+        } else {
 #pragma unroll
-                for (int v = 0; v < NV; v++) {
-                    float oa[VE], ob[VE], lo[VE], hi[VE];
+            for (int part = 0; part < 2; part++) {
+                const int p0 = part ? max(h0, a.q_heads) : h0, p1 = part ? h1 : min(h1, a.q_heads);
+                for (int from = p0; from < p1; from += U * at_once) {
+                    if (from != h0) read(from, p1);
 #pragma unroll
-                    for (int i = 0; i < VE; i++) {
-                        if (GRAD) {
-                            if (hd < h1) {      // r of a lane without a head is not finite for eps 0
-                                da[v][i] = fmaf(wa[v][i] * xa[v][i], r, da[v][i]);
-                                db[v][i] = fmaf(wb[v][i] * xb[v][i], r, db[v][i]);
+                    for (int u = 0; u < U; u++) {
+                        if (from + u * at_once >= p1) break;
+                        const int hd = from + u * at_once + group;
+                        float2 xa[NV][P], xb[NV][P], wa[NV][P], wb[NV][P], s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+                        for (int v = 0; v < NV; v++) {
+                            float2 ya[P], yb[P], t[P];
+                            pairs_of(x[u][v], xa[v], xb[v]);
+                            pairs_of(d[u][v], ya, yb);
+#pragma unroll
+                            for (int i = 0; i < P; i++) {
+                                s1 = __ffma2_rn(xa[v][i], xa[v][i], __ffma2_rn(xb[v][i], xb[v][i], s1));
+                                wa[v][i] = wb[v][i] = both(0.0f);
                             }
-                            oa[i] = fmaf(wa[v][i] * k.ga[v][i], r, -xa[v][i] * m);
-                            ob[i] = fmaf(wb[v][i] * k.gb[v][i], r, -xb[v][i] * m);
-                        } else {
-                            const float ua = xa[v][i] * r * k.ga[v][i], ub = xb[v][i] * r * k.gb[v][i];
-                            oa[i] = fmaf(ua, k.cs[v][i], -ub * k.sn[v][i]);
-                            ob[i] = fmaf(ua, k.sn[v][i], ub * k.cs[v][i]);
+                            if (!k.on(v)) continue;
+                            // turned back
+                            k.pairs(tables, v, t);
+#pragma unroll
+                            for (int i = 0; i < P; i++) {
+                                wa[v][i] = __fmul2_rn(ya[i], t[i]);
+                                wb[v][i] = __fmul2_rn(yb[i], t[i]);
+                            }
+                            k.pairs(tables + row, v, t);
+#pragma unroll
+                            for (int i = 0; i < P; i++) wa[v][i] = __ffma2_rn(yb[i], t[i], wa[v][i]);
+                            k.pairs(tables + 2 * row, v, t);
+#pragma unroll
+                            for (int i = 0; i < P; i++) wb[v][i] = __ffma2_rn(ya[i], t[i], wb[v][i]);
+                            // dgamma's terms lack r: wa xa, wb xb, which times gamma are those of the other sum
+                            k.pairs(gammas + 2 * part * row, v, t);
+#pragma unroll
+                            for (int i = 0; i < P; i++) s2 = __ffma2_rn(__fmul2_rn(wa[v][i], xa[v][i]), t[i], s2);
+                            k.pairs(gammas + (2 * part + 1) * row, v, t);
+#pragma unroll
+                            for (int i = 0; i < P; i++) s2 = __ffma2_rn(__fmul2_rn(wb[v][i], xb[v][i]), t[i], s2);
                         }
-                    }
-                    if (hd < h1 && k.on[v]) {
-                        from_pairs<VE, INTER>(oa, ob, lo, hi);
-                        *reinterpret_cast<V *>(yt + (off + k.lo[v]) * sizeof(T)) = pack<T, VE>(lo);
-                        *reinterpret_cast<V *>(yt + (off + k.hi[v]) * sizeof(T)) = pack<T, VE>(hi);
+                        const float sum1 = group_sum(s1.x + s1.y, lanes), sum2 = group_sum(s2.x + s2.y, lanes);
+                        const float r = rsqrtf(fmaf(sum1, a.inv_d, a.eps)), m = r * r * r * (sum2 * a.inv_d);
+#pragma unroll
+                        for (int v = 0; v < NV; v++) {
+                            // r of a group without a head is not finite for eps 0
+                            if (hd >= p1 || !k.on(v)) continue;
+                            float2 t[P];
+                            k.pairs(gammas + 2 * part * row, v, t);
+#pragma unroll
+                            for (int i = 0; i < P; i++) {
+                                const float2 wr = __fmul2_rn(wa[v][i], both(r));
+                                da[part][v][i] = __ffma2_rn(wr, xa[v][i], da[part][v][i]);
+                                wa[v][i] = __ffma2_rn(wr, t[i], __fmul2_rn(xa[v][i], both(-m)));
+                            }
+                            k.pairs(gammas + (2 * part + 1) * row, v, t);
+#pragma unroll
+                            for (int i = 0; i < P; i++) {
+                                const float2 wr = __fmul2_rn(wb[v][i], both(r));
+                                db[part][v][i] = __ffma2_rn(wr, xb[v][i], db[part][v][i]);
+                                wb[v][i] = __ffma2_rn(wr, t[i], __fmul2_rn(xb[v][i], both(-m)));
+                            }
+                            write(hd, v, wa[v], wb[v]);
+                        }
                     }
                 }
             }
@@ -282,48 +395,54 @@ __global__ void __launch_bounds__(kQkThreads) k_qk_norm(const __grid_constant__ 
     }
     if constexpr (GRAD) {
         if (!a.part) return;
-        // the groups of a warp, then the warps in order
-#pragma unroll
-        for (int v = 0; v < NV; v++) {
-            float lo[VE], hi[VE];
-#pragma unroll
-            for (int i = 0; i < VE; i++)
-                for (int o = lanes; o < 32; o <<= 1) {
-                    da[v][i] += __shfl_xor_sync(0xffffffffu, da[v][i], o);
-                    db[v][i] += __shfl_xor_sync(0xffffffffu, db[v][i], o);
-                }
-            from_pairs<VE, INTER>(da[v], db[v], lo, hi);
-            if (group == 0 && k.on[v])
-#pragma unroll
-                for (int i = 0; i < VE; i++) {
-                    sums[warp][k.lo[v] + i] = lo[i];
-                    sums[warp][k.hi[v] + i] = hi[i];
-                }
-        }
+        // the groups of a warp, then the warps in order; a warp's sums lie where its tables were
         __syncthreads();
-        for (int c = threadIdx.x; c < a.D; c += kQkThreads) {
-            float s = 0.0f;
+        float *sums = reinterpret_cast<float *>(shared);    // [warp][D]
 #pragma unroll
-            for (int w = 0; w < kQkWarps; w++) s += sums[w][c];
-            a.part[static_cast<long long>(blockIdx.x) * a.D + c] = s;
+        for (int part = 0; part < 2; part++) {
+#pragma unroll
+            for (int v = 0; v < NV; v++) {
+                float lo[VE], hi[VE];
+#pragma unroll
+                for (int i = 0; i < P; i++)
+                    for (int o = lanes; o < 32; o <<= 1) {
+                        float2 &pa = da[part][v][i], &pb = db[part][v][i];
+                        pa = __fadd2_rn(pa, make_float2(__shfl_xor_sync(0xffffffffu, pa.x, o), __shfl_xor_sync(0xffffffffu, pa.y, o)));
+                        pb = __fadd2_rn(pb, make_float2(__shfl_xor_sync(0xffffffffu, pb.x, o), __shfl_xor_sync(0xffffffffu, pb.y, o)));
+                    }
+                from_pairs<VE, INTER>(da[part][v], db[part][v], lo, hi);
+                if (group == 0 && k.on(v))
+#pragma unroll
+                    for (int i = 0; i < VE; i++) {
+                        sums[warp * a.D + k.lo(v) + i] = lo[i];
+                        sums[warp * a.D + k.hi(v) + i] = hi[i];
+                    }
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.D; c += kQkThreads) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kQkWarps; i++) s += sums[i * a.D + c];
+                a.part[(static_cast<long long>(blockIdx.x) * 2 + part) * a.D + c] = s;
+            }
+            __syncthreads();
         }
     }
 }
 
 // dgamma of the queries (blockIdx.y 0) and keys: the CTAs' sums, 32 channels a
 // block, each of its warps a row in eight, joined in order.
-__global__ void __launch_bounds__(256) k_qk_params(const float *part, unsigned q_blocks, unsigned blocks, int D, float *dq,
-                                                   float *dk)
+__global__ void __launch_bounds__(256) k_qk_params(const float *part, unsigned blocks, int D, float *dq, float *dk)
 {
     __shared__ float sh[8][32];
     grid_launch_dependents();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    const unsigned from = blockIdx.y ? q_blocks : 0, to = blockIdx.y ? blocks : q_blocks;
     float s = 0.0f;
     if (c < D) {
-#pragma unroll 8
-        for (unsigned r = from + w; r < to; r += 8) s += part[static_cast<long long>(r) * D + c];
+        const float *from = part + static_cast<long long>(blockIdx.y) * D + c;
+#pragma unroll 16
+        for (unsigned r = w; r < blocks; r += 8) s += from[static_cast<long long>(r) * 2 * D];
     }
     sh[w][lane] = s;
     __syncthreads();
@@ -347,7 +466,6 @@ int qk_check(const rz_qk *d, QkPlan *p)
     const size_t es = dtype_size(d->dtype);
     p->x = {d->N, d->H, d->W, d->C, es};
     p->y = {d->N, d->H, d->W, d->out_C, es};
-    p->workspace = sizeof(float) * static_cast<size_t>(kQkBlocks) * kQkMaxD;
     if (!es || !shape_ok(p->x) || !shape_ok(p->y)) return RZ_ERR_ARG;
     if (d->q_heads < 0 || d->k_heads < 0 || d->q_heads > RZ_MAX_DIM || d->k_heads > RZ_MAX_DIM) return RZ_ERR_ARG;
     if (d->q_heads + d->k_heads < 1 || d->D < 2 || d->D > kQkMaxD || d->D % 2) return RZ_ERR_ARG;
@@ -357,6 +475,7 @@ int qk_check(const rz_qk *d, QkPlan *p)
         return RZ_ERR_ARG;
     if (!(d->eps >= 0.0f) || !(d->eps <= 3.0e38f) || !(d->base > 0.0) || !std::isfinite(d->base) || !std::isfinite(d->scale))
         return RZ_ERR_ARG;
+    p->workspace = sizeof(float) * 2 * static_cast<size_t>(kQkBlocks) * d->D;
     // tokens are numbered in 32 bits
     if (!p->x.empty() && static_cast<long long>(d->N) > 0x7fffffffLL / (p->x.H * p->x.W)) return RZ_ERR_UNSUPPORTED;
     return RZ_OK;
@@ -374,42 +493,35 @@ unsigned long long turn_of(double base, double scale, int j, int pairs)
 template <class T, int VE, int NV, bool GRAD>
 cudaError_t qk_launch(const QkArgs &a, bool inter, unsigned blocks, void *stream)
 {
-    constexpr int U = NV > 1 ? 1 : GRAD ? 2 : 4;
+    constexpr int U = NV > 1 ? 1 : 2;
     const auto fn = inter ? k_qk_norm<T, VE, NV, true, GRAD, U> : k_qk_norm<T, VE, NV, false, GRAD, U>;
-    return launch(fn, dim3(blocks), kQkThreads, 0, stream, a);
+    const size_t smem = sizeof(float) * qk_row(a.D / 2) * (kQkWarps * (GRAD ? kQkGradTables : kQkTables) + 4);
+    return launch(fn, dim3(blocks), kQkThreads, std::max(smem, sizeof(float) * kQkWarps * a.D), stream, a);
 }
 
 template <class T, bool GRAD>
-cudaError_t qk_dispatch(QkArgs &a, const rz_qk *d, int ve, unsigned *total, void *stream)
+cudaError_t qk_dispatch(QkArgs &a, const rz_qk *d, int ve, unsigned *blocks, void *stream)
 {
     constexpr int W = 16 / sizeof(T);
-    const int half = d->D / 2, vecs = half / ve;
+    const int vecs = (d->D / 2 + ve - 1) / ve;
     int lanes = 1;
     while (lanes < vecs && lanes < 32) lanes *= 2;
     a.lanes = lanes;
-    const int u = ve == 1 ? 1 : GRAD ? 2 : 4, heads = a.q_heads + a.k_heads;
-    // about two CTAs' worth of warps an SM before a token's heads stay in one warp
+    // calls of few tokens cut a token's heads, down to one step a warp, until there are two CTAs' warps an SM
     a.chunks = 1;
-    const int most = (std::max(a.q_heads, a.k_heads) * lanes + 32 * u - 1) / (32 * u);
+    const int most = (a.heads * lanes + 31) / 32;
     while (a.chunks < most && static_cast<long long>(a.tokens) * a.chunks < 2 * kQkSms * kQkWarps) a.chunks++;
-    const unsigned long long need =
-        (static_cast<unsigned long long>(a.tokens) * a.chunks + kQkWarps - 1) / kQkWarps;
-    // CTAs are shared out by heads
-    const auto share = [&](int h) {
-        if (!h) return 0u;
-        const unsigned long long s = std::max(1ull, static_cast<unsigned long long>(kQkBlocks - 1) * h / heads);
-        return static_cast<unsigned>(std::min(need, s));
-    };
-    a.q_blocks = share(a.q_heads);
-    const unsigned blocks = *total = a.q_blocks + share(a.k_heads);
-    if (ve == W) return qk_launch<T, W, 1, GRAD>(a, d->interleaved != 0, blocks, stream);
-    if (sizeof(T) == 2 && ve == 4) return qk_launch<T, 4, 1, GRAD>(a, d->interleaved != 0, blocks, stream);
-    return qk_launch<T, 1, 4, GRAD>(a, d->interleaved != 0, blocks, stream);
+    const unsigned long long need = (static_cast<unsigned long long>(a.tokens) * a.chunks + kQkWarps - 1) / kQkWarps;
+    *blocks = static_cast<unsigned>(std::min<unsigned long long>(need, GRAD ? 2 * kQkSms : kQkBlocks));
+    const bool inter = d->interleaved != 0;
+    if (ve == W) return qk_launch<T, W, 1, GRAD>(a, inter, *blocks, stream);
+    if (sizeof(T) == 2 && ve == 4) return qk_launch<T, 4, 1, GRAD>(a, inter, *blocks, stream);
+    return qk_launch<T, 1, 4, GRAD>(a, inter, *blocks, stream);
 }
 
 template <bool GRAD>
 int qk_run(const rz_qk *d, const QkPlan &p, const rz_map *x, const rz_map *dy, const rz_map *y, const float *gamma_q,
-           const float *gamma_k, const int *positions, float *part, unsigned *q_blocks, unsigned *blocks, void *stream)
+           const float *gamma_k, const int *positions, float *part, unsigned *blocks, void *stream)
 {
     QkArgs a{};
     a.x = view(x);
@@ -418,28 +530,24 @@ int qk_run(const rz_qk *d, const QkPlan &p, const rz_map *x, const rz_map *dy, c
     const auto px = [](const Shape &s) { return static_cast<int>(s.C * s.es); };
     a.x_px = px(p.x);
     a.y_px = px(sy);
-    a.x_joined = rows_joined(*x, p.x);
-    a.y_joined = rows_joined(*y, sy);
     if (GRAD) {
         a.dy = view(dy);
         a.dy_px = px(p.y);
-        a.dy_joined = rows_joined(*dy, p.y);
     }
-    a.gq = gamma_q;
-    a.gk = gamma_k;
+    a.g[0] = gamma_q;
+    a.g[1] = gamma_k;
     a.pos = positions;
     a.part = part;
-    a.HW = static_cast<unsigned>(p.x.H * p.x.W);
+    a.H = static_cast<unsigned>(p.x.H);
     a.W = static_cast<unsigned>(p.x.W);
-    a.tokens = static_cast<unsigned>(d->N) * a.HW;
+    a.tokens = static_cast<unsigned>(d->N) * a.H * a.W;
     a.q_heads = d->q_heads;
-    a.k_heads = d->k_heads;
+    a.heads = d->q_heads + d->k_heads;
     a.D = d->D;
     a.row_pairs = d->row_pairs;
-    a.pairs = d->row_pairs + d->col_pairs;
     a.eps = d->eps;
     a.inv_d = 1.0f / static_cast<float>(d->D);
-    for (int j = 0; j < a.pairs; j++)
+    for (int j = 0; j < d->row_pairs + d->col_pairs; j++)
         a.turn[j] = j < d->row_pairs ? turn_of(d->base, d->scale, j, d->row_pairs)
                                      : turn_of(d->base, d->scale, j - d->row_pairs, d->col_pairs);
     const auto fits = [&](int ve) {
@@ -456,7 +564,6 @@ int qk_run(const rz_qk *d, const QkPlan &p, const rz_map *x, const rz_map *dy, c
         e = qk_dispatch<__nv_bfloat16, GRAD>(a, d, ve, blocks, stream);
     else
         e = qk_dispatch<__half, GRAD>(a, d, ve, blocks, stream);
-    *q_blocks = a.q_blocks;
     if (e != cudaSuccess) {
         record_cuda_error(static_cast<int>(e));
         return RZ_ERR_CUDA;
@@ -483,8 +590,8 @@ int map_qk_norm(const rz_qk *d, const rz_map *x, const rz_map *y, const float *g
     if (!floats_ok(gamma_q) || !floats_ok(gamma_k) || reinterpret_cast<uintptr_t>(positions) % 8) return RZ_ERR_ARG;
     const bool same = d->C == d->out_C && maps::map_same(*x, *y, p.x);
     if (!same && maps::map_overlap(*x, p.x, *y, p.y)) return RZ_ERR_ARG;
-    unsigned qb, b;
-    return qk_run<false>(d, p, x, nullptr, y, gamma_q, gamma_k, positions, nullptr, &qb, &b, stream);
+    unsigned blocks;
+    return qk_run<false>(d, p, x, nullptr, y, gamma_q, gamma_k, positions, nullptr, &blocks, stream);
 }
 
 int map_qk_norm_grad_workspace(const rz_qk *d, size_t *bytes)
@@ -504,7 +611,7 @@ int map_qk_norm_grad(const rz_qk *d, const rz_map *dy, const rz_map *x, const rz
     if (const int rc = qk_check(d, &p)) return rc;
     if (!floats_ok(gamma_q) || !floats_ok(gamma_k) || !floats_ok(dgamma_q) || !floats_ok(dgamma_k)) return RZ_ERR_ARG;
     const bool sums = dgamma_q || dgamma_k;
-    unsigned qb = 0, blocks = 0;
+    unsigned blocks = 0;
     if (!p.x.empty()) {
         if (!maps::map_ok(x, p.x) || !maps::map_ok(dy, p.y) || !maps::map_ok(dx, p.x)) return RZ_ERR_ARG;
         if (reinterpret_cast<uintptr_t>(positions) % 8) return RZ_ERR_ARG;
@@ -512,13 +619,13 @@ int map_qk_norm_grad(const rz_qk *d, const rz_map *dy, const rz_map *x, const rz
         if ((!same && maps::map_overlap(*dx, p.x, *dy, p.y)) || maps::map_overlap(*dx, p.x, *x, p.x)) return RZ_ERR_ARG;
         if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < p.workspace) return RZ_ERR_ARG;
         const int rc = qk_run<true>(d, p, x, dy, dx, gamma_q, gamma_k, positions,
-                                    sums ? static_cast<float *>(workspace) : nullptr, &qb, &blocks, stream);
+                                    sums ? static_cast<float *>(workspace) : nullptr, &blocks, stream);
         if (rc) return rc;
     }
     if (!sums) return RZ_OK;
     const dim3 grid((d->D + 31) / 32, 2);
-    const cudaError_t e = maps::launch(k_qk_params, grid, 256, 0, stream, static_cast<const float *>(workspace), qb, blocks,
-                                       d->D, dgamma_q, dgamma_k);
+    const cudaError_t e = maps::launch(k_qk_params, grid, 256, 0, stream, static_cast<const float *>(workspace), blocks, d->D,
+                                       dgamma_q, dgamma_k);
     if (e == cudaSuccess) return RZ_OK;
     record_cuda_error(static_cast<int>(e));
     return RZ_ERR_CUDA;
