@@ -190,6 +190,85 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Joi
     }
 }
 
+// Few rows of x, one token's for instance: the weight is all there is to read, so
+// no tile is staged.  A warp takes two columns of the result, its lanes the terms, a
+// vector of each at a time; `share` warps of a CTA share a column pair's terms where
+// there are few of them.  Up to ROWS rows of x (blockIdx.y counts them off) meet
+// each vector of the weight.
+struct RowsArgs {
+    Rows x, w;
+    Finish f;
+    unsigned C;
+    int share;
+};
+constexpr int kRowsColumns = 2;
+
+template <class T, int ACT, int ROWS, bool WIDE>
+__global__ void __launch_bounds__(256) k_linear_rows(const __grid_constant__ RowsArgs a)
+{
+    constexpr int VE = WIDE ? 16 / sizeof(T) : 1, P = kPairs<VE>, N = kRowsColumns;
+    using V = Raw<T, VE>;
+    __shared__ float sh[8][N * ROWS];
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned pair = (blockIdx.x * 8 + warp) / a.share, n0 = pair * N, m0 = blockIdx.y * ROWS;
+    const int part = warp % a.share;
+    const uint8_t *w[N], *x[ROWS];
+#pragma unroll
+    for (int j = 0; j < N; j++) w[j] = a.w.v.p + row_off(a.w, min(n0 + j, a.f.N - 1));
+#pragma unroll
+    for (int r = 0; r < ROWS; r++) x[r] = a.x.v.p + row_off(a.x, min(m0 + r, a.f.M - 1));
+    float2 s[N][ROWS];
+#pragma unroll
+    for (int j = 0; j < N; j++)
+#pragma unroll
+        for (int r = 0; r < ROWS; r++) s[j][r] = both(0.0f);
+    grid_dependency_wait();
+    const unsigned vecs = a.C / VE;
+#pragma unroll(ROWS > 2 ? 2 : 4)
+    for (unsigned v = part * 32 + lane; v < vecs; v += 32 * a.share) {
+        V wr[N], xr[ROWS];
+#pragma unroll
+        for (int j = 0; j < N; j++) wr[j] = __ldcs(reinterpret_cast<const V *>(w[j]) + v);
+#pragma unroll
+        for (int r = 0; r < ROWS; r++) xr[r] = reinterpret_cast<const V *>(x[r])[v];
+        float2 wf[N][P];
+#pragma unroll
+        for (int j = 0; j < N; j++) unpack2<T, VE>(wr[j], wf[j]);
+#pragma unroll
+        for (int r = 0; r < ROWS; r++) {
+            float2 xf[P];
+            unpack2<T, VE>(xr[r], xf);
+#pragma unroll
+            for (int j = 0; j < N; j++)
+#pragma unroll
+                for (int i = 0; i < P; i++) s[j][r] = __ffma2_rn(wf[j][i], xf[i], s[j][r]);
+        }
+    }
+    // a lane keeps the sum of column lane / ROWS, row lane % ROWS
+    float z = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; j++)
+#pragma unroll
+        for (int r = 0; r < ROWS; r++) {
+            float t = s[j][r].x + s[j][r].y;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            if (lane == j * ROWS + r) z = t;
+        }
+    if (a.share > 1) {
+        if (lane < N * ROWS) sh[warp][lane] = z;
+        __syncthreads();
+        if (part) return;
+        if (lane < N * ROWS)
+            for (int i = 1; i < a.share; i++) z += sh[warp + i][lane];
+    }
+    const unsigned n = n0 + lane / ROWS, m = m0 + lane % ROWS;
+    if (lane >= N * ROWS || n >= a.f.N || m >= a.f.M) return;
+    const float one[1] = {z};
+    finish_column<T, ACT, 1>(a.f, m, n, one, a.f.bias ? __ldg(a.f.bias + n) : 0.0f);
+}
+
 // ------------------------------------------------------------------ host side
 
 struct LinPlan {
@@ -433,6 +512,53 @@ Finish finish_of(const Rows &out, unsigned M, unsigned N, int dtype, const Rows 
     return f;
 }
 
+// Whether a call of M rows is k_linear_rows's, which reads the weight once for eight of them.
+bool is_few(unsigned M, unsigned N, unsigned C, int dtype)
+{
+    const double read = static_cast<double>((M + 7) / 8) * N * C;
+    return M <= 8 || (M <= 32 && read <= (dtype == RZ_F32 ? 4.2e6 : 2.1e6));
+}
+
+template <class T, int ACT, int ROWS>
+cudaError_t rows_launch(const RowsArgs &a, bool wide, void *stream)
+{
+    const unsigned pairs = (a.f.N + kRowsColumns - 1) / kRowsColumns;
+    const dim3 grid((pairs * a.share + 7) / 8, (a.f.M + ROWS - 1) / ROWS);
+    return launch(wide ? k_linear_rows<T, ACT, ROWS, true> : k_linear_rows<T, ACT, ROWS, false>, grid, 256, 0, stream, a);
+}
+template <class T, int ACT>
+cudaError_t rows_of_act(const RowsArgs &a, bool wide, void *stream)
+{
+    if (a.f.M == 1) return rows_launch<T, ACT, 1>(a, wide, stream);
+    if (a.f.M == 2) return rows_launch<T, ACT, 2>(a, wide, stream);
+    return a.f.M <= 4 ? rows_launch<T, ACT, 4>(a, wide, stream) : rows_launch<T, ACT, 8>(a, wide, stream);
+}
+template <class T>
+cudaError_t rows_of_type(const RowsArgs &a, bool wide, void *stream)
+{
+    if (a.f.act == RZ_ACT_SILU) return rows_of_act<T, RZ_ACT_SILU>(a, wide, stream);
+    return a.f.act == RZ_ACT_GELU ? rows_of_act<T, RZ_ACT_GELU>(a, wide, stream) : rows_of_act<T, RZ_ACT_NONE>(a, wide, stream);
+}
+cudaError_t few_rows(const Rows &x, const Rows &w, const Finish &f, unsigned C, int dtype, void *stream)
+{
+    RowsArgs a{};
+    a.x = x;
+    a.w = w;
+    a.f = f;
+    a.C = C;
+    const size_t es = dtype_size(dtype);
+    const auto aligned = [](const Rows &r) {
+        return reinterpret_cast<uintptr_t>(r.v.p) % 16 == 0 && r.v.pitch % 16 == 0 && r.v.bstride % 16 == 0 && (!r.HW || r.bytes % 16 == 0);
+    };
+    const bool wide = C * es % 16 == 0 && aligned(x) && aligned(w);
+    // warps until there are sixteen an SM, but at least two vectors a lane
+    const unsigned vecs = wide ? static_cast<unsigned>(C * es / 16) : C;
+    a.share = 1;
+    while (a.share < 8 && (f.N + 1) / 2 * a.share < 16 * kLinSms && vecs >= 128u * a.share) a.share *= 2;
+    if (dtype == RZ_F32) return rows_of_type<float>(a, wide, stream);
+    return dtype == RZ_BF16 ? rows_of_type<__nv_bfloat16>(a, wide, stream) : rows_of_type<__half>(a, wide, stream);
+}
+
 // What a forward call lays out, and where in its workspace.
 struct Forward {
     Laid x, w;
@@ -442,6 +568,7 @@ struct Forward {
 Forward plan_forward(const rz_linear *d, const LinPlan &p, const rz_map *x, const void *weight, size_t weight_pitch)
 {
     Forward f{};
+    if (is_few(p.P, static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), d->dtype)) return f;
     f.x = lay(rows_of(x, p.x), p.P, static_cast<unsigned>(d->C), d->dtype, false);
     f.w = lay(rows_of(weight, weight_pitch), static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), d->dtype, false);
     f.c = cut(p.P, static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), d->dtype);
@@ -525,16 +652,18 @@ int map_linear(const rz_linear *d, const rz_map *x, const void *weight, size_t w
     const Forward f = plan_forward(d, p, x, weight, weight_pitch);
     if (!workspace_ok(workspace, workspace_bytes, f.total)) return RZ_ERR_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    cudaError_t e = cudaSuccess;
-    for (const Laid *l : {&f.w, &f.x})
-        if (l->bytes && e == cudaSuccess) e = pack_rows(*l, nullptr, 0, nullptr, pack_chunks(l->rows, l->cols), ws, stream);
-    if (e != cudaSuccess) return lin_status(e);
     Rows rr, rp;
     if (residual) rr = rows_of(residual, p.y);
     if (pre) rp = rows_of(pre, p.y);
     Finish out = finish_of(rows_of(y, p.y), p.P, static_cast<unsigned>(d->K), d->dtype, pre ? &rp : nullptr, residual ? &rr : nullptr);
     out.bias = bias;
     out.act = d->act;
+    if (is_few(p.P, static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), d->dtype))
+        return lin_status(few_rows(rows_of(x, p.x), rows_of(weight, weight_pitch), out, static_cast<unsigned>(d->C), d->dtype, stream));
+    cudaError_t e = cudaSuccess;
+    for (const Laid *l : {&f.w, &f.x})
+        if (l->bytes && e == cudaSuccess) e = pack_rows(*l, nullptr, 0, nullptr, pack_chunks(l->rows, l->cols), ws, stream);
+    if (e != cudaSuccess) return lin_status(e);
     return lin_status(product(operand(f.x, ws, false), operand(f.w, ws, false), out, d->dtype, f.c,
                               reinterpret_cast<float *>(ws + f.part), status, stream));
 }
