@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Joi
     const long long run = static_cast<long long>(a.f.M) * a.pitch;
     if constexpr (WIDE) {
         float2 z[VE / 2] = {}, b[VE / 2];
-#pragma unroll 4
+#pragma unroll 8
         for (int r = 0; r < a.splits; r++, from += run)
 #pragma unroll
             for (int q = 0; q < VE; q += 4) {
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Joi
         finish<T, VE, ACT>(a.f, m, n, z, b, r);
     } else {
         float z[1] = {0.0f};
-#pragma unroll 4
+#pragma unroll 8
         for (int r = 0; r < a.splits; r++, from += run) z[0] += __ldcs(from);
         finish_column<T, ACT, 1>(a.f, m, n, z, a.f.bias ? __ldg(a.f.bias + n) : 0.0f);
     }
@@ -386,8 +386,12 @@ Operand operand(const Laid &l, const uint8_t *workspace, bool turned)
     return o;
 }
 
-// Tile width and runs of a product, by an estimate in clocks: a stage's products
-// (or its loads, on narrow tiles), a tile's epilogue, and the join of its runs.
+// Tile width, CTAs of a tile and runs of a product, by an estimate in clocks of
+// what was measured: a stage (what reaches an SM from L2, 64 bytes a clock, bounds
+// it on every tile: 256 columns of a pair 690, of one CTA 780, narrower ones 560 to
+// 590), a wave's beginning and end, and the join of runs, which pays for long sums
+// of few tiles (50000 pixels' gradient of a 64 x 64 weight: 211 us in one run, 18 in
+// 32; of 32768 pixels' 1024 x 1024 one: 162 and, in 4, 50).
 struct Cut {
     int tile_n, pair, splits;
     unsigned pitch;
@@ -402,7 +406,7 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype)
     for (int pair = 0; pair < 2; pair++)
         for (int tile = 256; tile >= (pair ? 128 : 64); tile /= 2) {
             if ((tile > 64 && N <= static_cast<unsigned>(tile) / 2) || (pair && M <= 128)) continue;
-            const double stage = pair ? (tile == 256 ? 540 : 300) : tile == 256 ? 700 : tile == 128 ? 380 : 240;
+            const double stage = tile == 256 ? (pair ? 690 : 780) : tile == 128 ? (pair ? 590 : 580) : 560;
             const long long rows = pair ? 256 : 128, slots = pair ? kLinSms / 2 : kLinSms;
             const long long tiles = (M + rows - 1) / rows * ((N + tile - 1) / tile);
             for (int want = 1; want <= 64 && want <= chunks; want++) {
@@ -410,13 +414,13 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype)
                 const int splits = static_cast<int>((chunks + run - 1) / run);
                 if (splits != want) continue;
                 const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
-                double t = waves * run * stage + 3000 + 12.0 * tile;
-                if (splits > 1) t += 5000 + 4.0 * M * pitch * (splits + 1) / 3000.0;
+                double t = waves * (run * stage + 2500) + 4.0 * tile;
+                if (splits > 1) t += 6500 + 170.0 * splits + 4.0 * M * pitch * (splits + 1) / 2500.0;
                 if (!best.tile_n || t < least) {
                     least = t;
                     best = {tile, pair, splits, pitch, splits > 1 ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
                 }
-                if (waves > 8) break;
+                if (waves > 3) break;
             }
         }
     return best;

@@ -527,7 +527,7 @@ EncodeFn encoder()
 // of 64 terms by `share` rows.  Turned: boxes of 64 rows by 64 terms, as many side
 // by side as the share has where the matrix is made of them (a thread asks for a
 // box in about the time of a stage's products, so two take longer than those: 345
-// against 3xx us on the weight gradient of 65536 x 1024 x 4096).
+// against 331 us on the weight gradient of 65536 x 1024 x 4096).
 bool encode(const Operand &o, unsigned share, CUtensorMap *map, int *merged)
 {
     std::memset(map, 0, sizeof(*map));
