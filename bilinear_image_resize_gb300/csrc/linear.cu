@@ -37,23 +37,26 @@ struct PackArgs {
     unsigned M, C;
     unsigned chunk;         // rows of a CTA
     int lanes;              // lanes side by side in a row, eight columns each
-    int has_slope, act, wide;
+    int has_slope, act;
 };
 
-template <class T>
-__device__ __forceinline__ void load8(const uint8_t *at, int left, bool wide, float (&f)[8])
+// Eight elements: as they come, or with those past the row's end 0.
+template <class T, bool WIDE>
+__device__ __forceinline__ void load8(const uint8_t *at, int left, Raw<T, 8> &r)
 {
-    if (wide && left >= 8) {
+    if constexpr (WIDE) {
         if constexpr (sizeof(T) == 4) {
-            const float4 a = __ldcs(reinterpret_cast<const float4 *>(at)), b = __ldcs(reinterpret_cast<const float4 *>(at) + 1);
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+            r.a = __ldcs(reinterpret_cast<const uint4 *>(at));
+            r.b = __ldcs(reinterpret_cast<const uint4 *>(at) + 1);
         } else {
-            unpack<T, 8>(__ldcs(reinterpret_cast<const uint4 *>(at)), f);
+            r = __ldcs(reinterpret_cast<const uint4 *>(at));
         }
-        return;
-    }
+    } else {
+        float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) f[i] = i < left ? static_cast<float>(reinterpret_cast<const T *>(at)[i]) : 0.0f;
+        for (int i = 0; i < 8; i++) f[i] = i < left ? static_cast<float>(reinterpret_cast<const T *>(at)[i]) : 0.0f;
+        r = pack<T, 8>(f);
+    }
 }
 
 // The leading 8 bits of v, cut, so that what is left has its sign and no value
@@ -63,50 +66,62 @@ __device__ __forceinline__ float leading(float v)
     return v != v ? v : __uint_as_float(__float_as_uint(v) & 0xffff0000u);
 }
 
-template <class T>
+template <class T, bool WIDE>
 __global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_constant__ PackArgs a)
 {
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;       // rows read before the first is used
     __shared__ float sh[kPackWarps][256];
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rows = 32 / a.lanes, sub = lane % a.lanes, down = lane / a.lanes;
     const unsigned c = (blockIdx.x * a.lanes + sub) * 8;
     const int left = static_cast<int>(a.C) - static_cast<int>(c);
-    const unsigned r0 = blockIdx.y * a.chunk, r1 = min(a.M, r0 + a.chunk);
+    const unsigned r0 = blockIdx.y * a.chunk, r1 = min(a.M, r0 + a.chunk), step = kPackWarps * rows;
     float s[8] = {};
     grid_dependency_wait();
     if (left > 0) {
-#pragma unroll 2
-        for (unsigned r = r0 + warp * rows + down; r < r1; r += kPackWarps * rows) {
-            float f[8];
-            load8<T>(a.in.v.p + row_off(a.in, r) + static_cast<long long>(c) * sizeof(T), left, a.wide, f);
-            if (a.has_slope) {
-                float z[8];
-                load8<T>(a.slope.v.p + row_off(a.slope, r) + static_cast<long long>(c) * sizeof(T), left, a.wide, z);
+        for (unsigned r = r0 + warp * rows + down; r < r1; r += U * step) {
+            Raw<T, 8> in[U], slope[U];
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const float2 d = act_slope<T>(make_float2(z[i], z[i + 1]), a.act);
-                    f[i] *= d.x;
-                    f[i + 1] *= d.y;
-                }
+            for (int u = 0; u < U; u++) {
+                // past the last row: that one again, and not used
+                const unsigned ru = min(r + u * step, r1 - 1);
+                load8<T, WIDE>(a.in.v.p + row_off(a.in, ru) + static_cast<long long>(c) * sizeof(T), left, in[u]);
+                if (a.has_slope) load8<T, WIDE>(a.slope.v.p + row_off(a.slope, ru) + static_cast<long long>(c) * sizeof(T), left, slope[u]);
             }
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (i < left) s[i] += f[i];
-            if (!a.to) continue;
-            uint8_t *at = a.to + r * a.pitch + c * 2;
-            if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<uint4 *>(at) = pack<T, 8>(f);
-            } else {
+            for (int u = 0; u < U; u++) {
+                if (r + u * step >= r1) break;
+                float f[8];
+                unpack<T, 8>(in[u], f);
+                if (a.has_slope) {
+                    float z[8];
+                    unpack<T, 8>(slope[u], z);
 #pragma unroll
-                for (int p = 0; p < 3; p++) {
-                    float h[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        h[i] = leading(f[i]);
-                        f[i] -= h[i];
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 d = act_slope<T>(make_float2(z[i], z[i + 1]), a.act);
+                        f[i] *= d.x;
+                        f[i + 1] *= d.y;
                     }
-                    *reinterpret_cast<uint4 *>(at + p * a.plane) = pack<__nv_bfloat16, 8>(h);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (WIDE || i < left) s[i] += f[i];
+                if (!a.to) continue;
+                uint8_t *at = a.to + (r + u * step) * a.pitch + c * 2;
+                if constexpr (sizeof(T) == 2) {
+                    *reinterpret_cast<uint4 *>(at) = pack<T, 8>(f);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < 3; p++) {
+                        float h[8];
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            h[i] = leading(f[i]);
+                            f[i] -= h[i];
+                        }
+                        *reinterpret_cast<uint4 *>(at + p * a.plane) = pack<__nv_bfloat16, 8>(h);
+                    }
                 }
             }
         }
@@ -443,16 +458,16 @@ cudaError_t pack_rows(const Laid &l, const Rows *slope, int act, float *sums, un
     a.lanes = 1;
     while (a.lanes < 32 && static_cast<unsigned>(a.lanes) < vecs) a.lanes *= 2;
     a.chunk = (l.rows + chunks - 1) / chunks;
-    const size_t es = dtype_size(l.dtype);
-    const auto wide = [&](const Rows &r) {
+    const auto wide = [](const Rows &r) {
         return reinterpret_cast<uintptr_t>(r.v.p) % 16 == 0 && r.v.pitch % 16 == 0 && r.v.bstride % 16 == 0 &&
                (!r.HW || r.bytes % 16 == 0);
     };
-    a.wide = l.cols * es % 16 == 0 && wide(l.in) && (!slope || wide(*slope));
+    const bool vectors = l.cols % 8 == 0 && wide(l.in) && (!slope || wide(*slope));
     const dim3 grid((vecs + a.lanes - 1) / a.lanes, (l.rows + a.chunk - 1) / a.chunk);
-    if (l.dtype == RZ_F32) return launch(k_linear_pack<float>, grid, kPackThreads, 0, stream, a);
-    if (l.dtype == RZ_BF16) return launch(k_linear_pack<__nv_bfloat16>, grid, kPackThreads, 0, stream, a);
-    return launch(k_linear_pack<__half>, grid, kPackThreads, 0, stream, a);
+    const auto fn = l.dtype == RZ_F32    ? (vectors ? k_linear_pack<float, true> : k_linear_pack<float, false>)
+                    : l.dtype == RZ_BF16 ? (vectors ? k_linear_pack<__nv_bfloat16, true> : k_linear_pack<__nv_bfloat16, false>)
+                                         : (vectors ? k_linear_pack<__half, true> : k_linear_pack<__half, false>);
+    return launch(fn, grid, kPackThreads, 0, stream, a);
 }
 // Chunks of rows of a pass over a matrix: about four CTAs an SM, at least 16 rows each.
 unsigned pack_chunks(unsigned rows, unsigned cols)
