@@ -572,7 +572,7 @@ RZ_API int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_ma
  * workspace: device memory of at least the bytes that map_linear_workspace
  * gives for maps like these (of x and weight their alignment, pitch and stride
  * matter; the data is not touched), 16-byte aligned, of any content, the call's
- * own until the stream has passed it.  status: a device int or NULL; a kernel
+ * own until the stream has passed it; up to eight pixels need none.  status: a device int or NULL; a kernel
  * whose bounded waits (1 s) run out writes RZ_ERR_TIMEOUT there and leaves the
  * result unfinished.  Asynchronous on `stream`; no allocation.  An empty map is
  * RZ_OK.
