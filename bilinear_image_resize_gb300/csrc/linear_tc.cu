@@ -3,7 +3,7 @@
 // A CTA computes 128 x tile_n of D = A B^T, 64 terms at a time: two threads ask
 // for the operands' tiles by TMA, into a ring of stages in the 128-byte swizzle;
 // one thread issues four tcgen05.mma (16 terms each) a stage, accumulating in
-// tensor memory; sixteen warps take finished tiles out of it.  Tensor memory holds
+// tensor memory; eight warps take finished tiles out of it.  Tensor memory holds
 // two tiles, so that one is stored while the next is computed.  CTAs are
 // persistent and take tiles in turn, those of one row of tiles next to each
 // other, so that their rows of A come from L2.
@@ -35,20 +35,20 @@ using dev::smem_addr;
 constexpr int kTerms = 64;                      // terms of a stage: 128 bytes, the swizzle's width
 constexpr int kTileM = 128;
 constexpr int kBytesA = kTileM * kTerms * 2;
-constexpr int kEpiWarps = 16;
+constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;  // loads of A, issuer, tensor memory, loads of B; the epilogue's begin at a multiple of four
-constexpr int kStagePitch = 48;                 // bytes of a row on its way out: 32 and a gap, so that rows differ in their banks
-constexpr int kStageBytes = kEpiWarps * 32 * kStagePitch;
-constexpr int kShare = 64;                      // most columns of a tile that are one epilogue warp's
+constexpr int kBlockRow = 64;                   // bytes of a row of a block on its way out, 32 rows a block
+constexpr int kBlockBytes = 32 * kBlockRow;
+constexpr int kWarpBytes = 2 * kBlockBytes;     // an epilogue warp's two blocks
+constexpr int kOutBytes = kEpiWarps * kWarpBytes;
+constexpr int kStagePitch = 48;                 // without TMA: bytes of a row on its way out, 32 and a gap, so that rows differ in their banks
 constexpr int kSmem = 227 * 1024;
-constexpr int kStatic = kEpiWarps * kShare * 4 + 512;   // the kernel's own variables
+constexpr int kStatic = 512;    // the kernel's own variables
 constexpr int kRing = 8;
 constexpr int kSms = 152;
 
 struct TcArgs {
     Finish f;
-    float *part;
-    unsigned part_pitch;
     unsigned tiles_m, tiles_n, tiles;   // tiles: of all runs
     int tile_n, stages;
     int chunks, all_chunks, run;        // 64-term chunks of a plane product, of all of them, and of a run
@@ -142,15 +142,6 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[16])
                  : "memory");
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[8])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "r"(addr)
-                 : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
 // A wait of at most a second that leaves no gap between its attempts.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int *status)
 {
@@ -164,25 +155,82 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int *st
     return true;
 }
 
-// 32 rows of 32 bytes each through a warp's stage, which turns a row a thread into
-// consecutive bytes of a row for consecutive threads and back: lane / 2 + 16 k is
-// the row of a lane's k-th 16 bytes, lane % 2 their half of it.
-__device__ __forceinline__ void stage_row(uint8_t *stage, const uint4 (&v)[2])
+// Bias of 16 columns from n, as far as the matrix has them.
+__device__ __forceinline__ void add_bias(const Finish &f, bool vectors, unsigned n, float2 (&z)[8])
 {
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
-    reinterpret_cast<uint4 *>(stage + lane * kStagePitch)[0] = v[0];
-    reinterpret_cast<uint4 *>(stage + lane * kStagePitch)[1] = v[1];
-    __syncwarp();
-}
-__device__ __forceinline__ uint4 staged(const uint8_t *stage, int k)
-{
-    const int lane = threadIdx.x & 31;
-    return *reinterpret_cast<const uint4 *>(stage + (lane / 2 + 16 * k) * kStagePitch + lane % 2 * 16);
+    if (!f.bias) return;
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const unsigned c = n + 4 * q;
+        if (vectors && c + 4 <= f.N) {
+            b = __ldg(reinterpret_cast<const float4 *>(f.bias + c));
+        } else {
+            if (c < f.N) b.x = __ldg(f.bias + c);
+            if (c + 1 < f.N) b.y = __ldg(f.bias + c + 1);
+            if (c + 2 < f.N) b.z = __ldg(f.bias + c + 2);
+            if (c + 3 < f.N) b.w = __ldg(f.bias + c + 3);
+        }
+        z[2 * q] = __fadd2_rn(z[2 * q], make_float2(b.x, b.y));
+        z[2 * q + 1] = __fadd2_rn(z[2 * q + 1], make_float2(b.z, b.w));
+    }
 }
 
-// A row a thread of PC = 32 / sizeof(T) columns to a matrix: rows from m, columns
-// from n, as far as it reaches; whole vectors or element by element.
+// By TMA: a row a thread of 16 columns, the half `sub` of a block's row where they
+// are 16-bit, to and from a block in the 64-byte swizzle (16 bytes at `c` of row r are
+// at c ^ (r / 2) % 4, so that eight rows differ in their banks).
+template <class T>
+__device__ __forceinline__ void block_write(uint8_t *block, int sub, const float2 (&z)[8])
+{
+    constexpr int VE = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 16 / VE; h++) {
+        float2 v[VE / 2];
+#pragma unroll
+        for (int i = 0; i < VE / 2; i++) v[i] = z[h * VE / 2 + i];
+        const int c = sub * (16 / VE) + h;
+        *reinterpret_cast<Raw<T, VE> *>(block + lane * kBlockRow + ((c ^ (lane >> 1 & 3)) << 4)) = pack2<T, VE>(v);
+    }
+}
+template <class T>
+__device__ __forceinline__ void block_add(const uint8_t *block, int sub, float2 (&z)[8])
+{
+    constexpr int VE = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 16 / VE; h++) {
+        float2 v[VE / 2];
+        const int c = sub * (16 / VE) + h;
+        unpack2<T, VE>(*reinterpret_cast<const Raw<T, VE> *>(block + lane * kBlockRow + ((c ^ (lane >> 1 & 3)) << 4)), v);
+#pragma unroll
+        for (int i = 0; i < VE / 2; i++) z[h * VE / 2 + i] = __fadd2_rn(z[h * VE / 2 + i], v[i]);
+    }
+}
+// A filled block on its way to memory, clipped to the matrix.
+__device__ __forceinline__ void block_store(const CUtensorMap *map, const uint8_t *block, int n, int m, int run)
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(n), "r"(m), "r"(run), "r"(smem_addr(block))
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+// Until all but the last LEFT of this thread's blocks have been read.
+template <int LEFT>
+__device__ __forceinline__ void blocks_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+}
+
+// Without TMA: 32 rows of 32 bytes each through a warp's stage, which turns a row a
+// thread into consecutive bytes of a row for consecutive threads: lane / 2 + 16 k is
+// the row of a lane's k-th 16 bytes, lane % 2 their half of it.  PC = 32 / sizeof(T)
+// columns from n, as far as the matrix reaches; whole vectors or element by element.
 template <class T>
 __device__ __forceinline__ void emit(const Rows &to, const Finish &f, unsigned m, unsigned n, uint8_t *stage,
                                      const float2 (&z)[16 / sizeof(T)])
@@ -190,20 +238,22 @@ __device__ __forceinline__ void emit(const Rows &to, const Finish &f, unsigned m
     constexpr int PC = 32 / sizeof(T), VE = PC / 2;
     using E = Raw<T, 1>;
     const int lane = threadIdx.x & 31;
-    uint4 v[2];
+    __syncwarp();
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         float2 part[VE / 2];
 #pragma unroll
         for (int i = 0; i < VE / 2; i++) part[i] = z[h * VE / 2 + i];
-        v[h] = pack2<T, VE>(part);
+        reinterpret_cast<Raw<T, VE> *>(stage + lane * kStagePitch)[h] = pack2<T, VE>(part);
     }
-    stage_row(stage, v);
+    __syncwarp();
     if (f.wide) {
 #pragma unroll
         for (int k = 0; k < 2; k++) {
             const unsigned r = m + lane / 2 + 16 * k, c = n + lane % 2 * VE;
-            if (r < f.M && c < f.N) *vec_at<T, VE>(to, r, c) = staged(stage, k);
+            if (r < f.M && c < f.N)
+                *vec_at<T, VE>(to, r, c) =
+                    *reinterpret_cast<const Raw<T, VE> *>(stage + (lane / 2 + 16 * k) * kStagePitch + lane % 2 * 16);
         }
     } else {
 #pragma unroll
@@ -213,6 +263,48 @@ __device__ __forceinline__ void emit(const Rows &to, const Finish &f, unsigned m
                 *reinterpret_cast<E *>(to.v.p + row_off(to, m + r) + static_cast<long long>(n + c) * sizeof(T)) =
                     *reinterpret_cast<const E *>(stage + r * kStagePitch + c * sizeof(T));
         }
+    }
+}
+// z += the residual, PC columns from n of a row a thread.
+template <class T>
+__device__ __forceinline__ void absorb(const Finish &f, unsigned m, unsigned n, uint8_t *stage, float2 (&z)[16 / sizeof(T)])
+{
+    constexpr int PC = 32 / sizeof(T), VE = PC / 2;
+    using E = Raw<T, 1>;
+    using V = Raw<T, VE>;
+    const int lane = threadIdx.x & 31;
+    const Rows &from = f.residual;
+    if (f.wide) {
+        V now[2];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const unsigned r = m + lane / 2 + 16 * k, c = n + lane % 2 * VE;
+            now[k] = V{};
+            if (r < f.M && c < f.N) now[k] = *vec_at<T, VE>(from, r, c);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; k++) *reinterpret_cast<V *>(stage + (lane / 2 + 16 * k) * kStagePitch + lane % 2 * 16) = now[k];
+    } else {
+        E now[PC];
+#pragma unroll
+        for (int k = 0; k < PC; k++) {
+            const unsigned r = m + k * (32 / PC) + lane / PC, c = n + lane % PC;
+            now[k] = r < f.M && c < f.N ? *reinterpret_cast<const E *>(from.v.p + row_off(from, r) + static_cast<long long>(c) * sizeof(T))
+                                        : E{};
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < PC; k++)
+            *reinterpret_cast<E *>(stage + (k * (32 / PC) + lane / PC) * kStagePitch + lane % PC * sizeof(T)) = now[k];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        float2 half[VE / 2];
+        unpack2<T, VE>(reinterpret_cast<const V *>(stage + lane * kStagePitch)[h], half);
+#pragma unroll
+        for (int q = 0; q < VE / 2; q++) z[h * VE / 2 + q] = __fadd2_rn(z[h * VE / 2 + q], half[q]);
     }
 }
 
@@ -246,14 +338,17 @@ __device__ __forceinline__ void planes_of(int planes, int j, int &a, int &b)
     b = 0x010210 >> (4 * j) & 0xf;
 }
 
-template <class T, int ACT, int CG>
+// BULK: results leave, and residuals come, by TMA (map_out; map_aux: the residual's or
+// pre's); else by loads and stores.
+template <class T, int ACT, int CG, bool BULK>
 __global__ void __launch_bounds__(kThreads, 1)
-k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b)
+k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+            const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_aux)
 {
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[kRing], empty[kRing], done[2], taken[2];
     __shared__ uint32_t tmem_slot;
-    __shared__ alignas(16) float bias[kEpiWarps][kShare];
+    __shared__ uint64_t came[kEpiWarps][2];     // a residual's block, each of a warp's two
     const uint32_t pad = (1024 - (smem_addr(raw) & 1023)) & 1023;
     const uint32_t ring = smem_addr(raw) + pad;
     const int rows_b = a.tile_n / CG;     // this CTA's share of B's rows
@@ -271,6 +366,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
         for (int i = 0; i < 2; i++) {
             dev::mbar_init(done + i, 1);
             dev::mbar_init(taken + i, kEpiWarps * CG);
+            for (int e = 0; e < kEpiWarps; e++) dev::mbar_init(&came[e][i], 1);
         }
         dev::fence_mbar_init();
     }
@@ -378,116 +474,127 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             }
         }
     } else if (warp >= 4) {
-        // four warps share 32 rows of the tile, a quarter of its columns each, 32 bytes of the result's rows at a time
-        constexpr int PC = 32 / sizeof(T), VE = PC / 2;
-        using E = Raw<T, 1>;
-        const int e = warp - 4, quarter = warp & 3, cols = a.tile_n / 4;
-        uint8_t *stage = raw + pad + a.stages * stage_bytes + e * 32 * kStagePitch;
+        // two warps share 32 rows of the tile, half of its columns each
+        const int e = warp - 4, quarter = warp & 3, cols = a.tile_n / 2;
+        uint8_t *out = raw + pad + a.stages * stage_bytes + e * kWarpBytes;
+        const bool vectors = (reinterpret_cast<uintptr_t>(a.f.bias) & 15) == 0;
         unsigned i = 0;
         bool ok = true;
-        for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
-            const Tile w = tile_at(a, t);
-            const unsigned m0 = (w.m * CG + rank) * kTileM + 32 * quarter, from = (e >> 2) * cols;
-            const unsigned n0 = w.n * a.tile_n + from;
-            // what does not wait for the product: its columns' bias, the first residuals
-            if (!a.part) {
-                __syncwarp();
-                for (int c = lane; c < cols; c += 32) bias[e][c] = a.f.bias && n0 + c < a.f.N ? __ldg(a.f.bias + n0 + c) : 0.0f;
-                __syncwarp();
+        const auto give_back = [&] {
+            // this warp's share of the tile is in registers
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            if (lane == 0) {
+                if constexpr (CG == 1)
+                    dev::mbar_arrive(taken + (i & 1));
+                else
+                    arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), 0));
             }
-            uint4 next[2] = {};
-            const bool adds = !a.part && a.f.has_residual, ahead = adds && a.f.wide;
-            const auto residuals = [&](unsigned n) {
+        };
+        const auto columns = [&](uint32_t at, float2(&z)[8]) {
+            uint32_t v[16];
+            tmem_load(at, v);
 #pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const unsigned r = m0 + lane / 2 + 16 * k, c = n + lane % 2 * VE;
-                    if (r < a.f.M && c < a.f.N) next[k] = *vec_at<T, VE>(a.f.residual, r, c);
+            for (int q = 0; q < 8; q++) z[q] = make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
+        };
+        if constexpr (BULK) {
+            // Blocks of 64 bytes by 32 rows, in two places in turn: a residual's block comes into the place that its result
+            // leaves from, the next one's while this one is worked on.
+            constexpr int BC = kBlockRow / sizeof(T), SUBS = BC / 16;
+            const int blocks = cols / BC;
+            int flip = 0;
+            uint32_t phases = 0;
+            for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
+                const Tile w = tile_at(a, t);
+                const unsigned m0 = (w.m * CG + rank) * kTileM + 32 * quarter, n0 = w.n * a.tile_n + (e >> 2) * cols;
+                const int live = m0 < a.f.M && n0 < a.f.N ? min(blocks, static_cast<int>((a.f.N - n0 + BC - 1) / BC)) : 0;
+                const auto fetch = [&](int b, int place) {
+                    uint64_t *bar = &came[e][place];
+                    dev::mbar_arrive_expect_tx(bar, kBlockBytes);
+                    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(out + place * kBlockBytes)),
+                                 "l"(reinterpret_cast<uint64_t>(&map_aux)), "r"(static_cast<int>(n0) + b * BC),
+                                 "r"(static_cast<int>(m0)), "r"(0), "r"(smem_addr(bar))
+                                 : "memory");
+                };
+                if (a.f.has_residual && live && lane == 0) {
+                    blocks_read<1>();
+                    fetch(0, flip);
                 }
-            };
-            if (ahead) residuals(n0);
-            ok = wait_for(done + (i & 1), i >> 1 & 1, a.status);
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + from;
-            for (int c0 = 0; c0 < cols; c0 += PC) {
-                uint32_t v[PC];
-                tmem_load(acc + c0, v);
-                if (c0 + PC >= cols) {
-                    // this warp's share of the tile is in registers
-                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                    if (lane == 0) {
-                        if constexpr (CG == 1)
-                            dev::mbar_arrive(taken + (i & 1));
-                        else
-                            arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), 0));
+                ok = wait_for(done + (i & 1), i >> 1 & 1, a.status);
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + (e >> 2) * cols;
+                for (int b = 0; b < blocks; b++) {
+                    float2 z[SUBS][8];
+#pragma unroll
+                    for (int q = 0; q < SUBS; q++) columns(acc + b * BC + 16 * q, z[q]);
+                    if (b == blocks - 1) give_back();
+                    if (b >= live) continue;
+                    const int n = static_cast<int>(n0) + b * BC;
+                    if (a.f.has_residual && b + 1 < live && lane == 0) {
+                        blocks_read<0>();
+                        fetch(b + 1, flip ^ 1);
                     }
-                }
-                const unsigned n = n0 + c0;
-                if (n >= a.f.N || m0 >= a.f.M) continue;
-                if (a.part) {
-                    // float32 rows of the run's part
-                    float *to = a.part + static_cast<long long>(w.run) * a.f.M * a.part_pitch;
 #pragma unroll
-                    for (int h = 0; h < PC; h += 8) {
-                        const uint4 row[2] = {make_uint4(v[h], v[h + 1], v[h + 2], v[h + 3]),
-                                              make_uint4(v[h + 4], v[h + 5], v[h + 6], v[h + 7])};
-                        stage_row(stage, row);
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            const unsigned r = m0 + lane / 2 + 16 * k, c = n + h + lane % 2 * 4;
-                            if (r < a.f.M && c < a.part_pitch)
-                                *reinterpret_cast<uint4 *>(to + static_cast<long long>(r) * a.part_pitch + c) = staged(stage, k);
-                        }
-                    }
-                    continue;
-                }
-                float2 add[PC / 2];
-                if (adds) {
-                    if (ahead) {
-                        const uint4 now[2] = {next[0], next[1]};
-                        if (c0 + PC < cols) residuals(n + PC);
+                    for (int q = 0; q < SUBS; q++) add_bias(a.f, vectors, n + 16 * q, z[q]);
+                    if (a.f.has_pre) {
+                        if (lane == 0) blocks_read<1>();
                         __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < 2; k++)
-                            *reinterpret_cast<uint4 *>(stage + (lane / 2 + 16 * k) * kStagePitch + lane % 2 * 16) = now[k];
+                        for (int q = 0; q < SUBS; q++) block_write<T>(out + flip * kBlockBytes, q, z[q]);
+                        block_store(&map_aux, out + flip * kBlockBytes, n, static_cast<int>(m0), 0);
+                        flip ^= 1;
+                    }
+#pragma unroll
+                    for (int q = 0; q < SUBS; q++)
+#pragma unroll
+                        for (int j = 0; j < 8; j++) z[q][j] = activated<T, ACT>(z[q][j]);
+                    uint8_t *block = out + flip * kBlockBytes;
+                    if (a.f.has_residual) {
+                        ok = __all_sync(0xffffffffu, wait_for(&came[e][flip], phases >> flip & 1, a.status));
+                        if (!ok) break;
+                        phases ^= 1u << flip;
+#pragma unroll
+                        for (int q = 0; q < SUBS; q++) block_add<T>(block, q, z[q]);
                     } else {
-                        E now[PC];
-#pragma unroll
-                        for (int k = 0; k < PC; k++) {
-                            const unsigned r = m0 + k * (32 / PC) + lane / PC, c = n + lane % PC;
-                            now[k] = r < a.f.M && c < a.f.N
-                                         ? *reinterpret_cast<const E *>(a.f.residual.v.p + row_off(a.f.residual, r) +
-                                                                        static_cast<long long>(c) * sizeof(T))
-                                         : E{};
-                        }
+                        if (lane == 0) blocks_read<1>();
                         __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < PC; k++)
-                            *reinterpret_cast<E *>(stage + (k * (32 / PC) + lane / PC) * kStagePitch + lane % PC * sizeof(T)) = now[k];
                     }
-                    __syncwarp();
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        float2 half[VE / 2];
-                        unpack2<T, VE>(reinterpret_cast<const Raw<T, VE> *>(stage + lane * kStagePitch)[h], half);
+                    for (int q = 0; q < SUBS; q++) block_write<T>(block, q, z[q]);
+                    block_store(&map_out, block, n, static_cast<int>(m0), static_cast<int>(w.run));
+                    flip ^= 1;
+                }
+            }
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        } else {
+            constexpr int PC = 32 / sizeof(T);
+            for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
+                const Tile w = tile_at(a, t);
+                const unsigned m0 = (w.m * CG + rank) * kTileM + 32 * quarter, n0 = w.n * a.tile_n + (e >> 2) * cols;
+                ok = wait_for(done + (i & 1), i >> 1 & 1, a.status);
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + (e >> 2) * cols;
+                for (int c0 = 0; c0 < cols; c0 += 16) {
+                    float2 z[8];
+                    columns(acc + c0, z);
+                    if (c0 + 16 >= cols) give_back();
+                    const unsigned n = n0 + c0;
+                    if (n >= a.f.N || m0 >= a.f.M) continue;
+                    add_bias(a.f, vectors, n, z);
 #pragma unroll
-                        for (int q = 0; q < VE / 2; q++) add[h * VE / 2 + q] = half[q];
+                    for (int h = 0; h < 16; h += PC) {
+                        float2 part[PC / 2];
+#pragma unroll
+                        for (int q = 0; q < PC / 2; q++) part[q] = z[h / 2 + q];
+                        if (a.f.has_pre) emit<T>(a.f.pre, a.f, m0, n + h, out, part);
+#pragma unroll
+                        for (int q = 0; q < PC / 2; q++) part[q] = activated<T, ACT>(part[q]);
+                        if (a.f.has_residual) absorb<T>(a.f, m0, n + h, out, part);
+                        emit<T>(a.f.out, a.f, m0, n + h, out, part);
                     }
                 }
-                float2 z[PC / 2];
-#pragma unroll
-                for (int q = 0; q < PC; q += 4) {
-                    const float4 b = *reinterpret_cast<const float4 *>(&bias[e][c0 + q]);
-                    z[q / 2] = __fadd2_rn(make_float2(__uint_as_float(v[q]), __uint_as_float(v[q + 1])), make_float2(b.x, b.y));
-                    z[q / 2 + 1] = __fadd2_rn(make_float2(__uint_as_float(v[q + 2]), __uint_as_float(v[q + 3])), make_float2(b.z, b.w));
-                }
-                if (a.f.has_pre) emit<T>(a.f.pre, a.f, m0, n, stage, z);
-#pragma unroll
-                for (int q = 0; q < PC / 2; q++) z[q] = activated<T, ACT>(z[q]);
-                if (adds)
-#pragma unroll
-                    for (int q = 0; q < PC / 2; q++) z[q] = __fadd2_rn(z[q], add[q]);
-                emit<T>(a.f.out, a.f, m0, n, stage, z);
             }
         }
     }
@@ -542,15 +649,35 @@ bool encode(const Operand &o, unsigned share, CUtensorMap *map, int *merged)
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, int ACT, int CG>
-cudaError_t tc_launch(const TcArgs &a, const CUtensorMap &ma, const CUtensorMap &mb, void *stream)
+// A result's (or residual's, or pre's) tensor map: blocks of 64 bytes by 32 rows, of
+// `runs` matrices one after another.
+bool encode_out(const Rows &r, unsigned M, unsigned N, int dtype, int runs, size_t run_bytes, CUtensorMap *map)
 {
-    const auto fn = k_linear_tc<T, ACT, CG>;
+    std::memset(map, 0, sizeof(*map));
+    const size_t es = dtype_size(dtype), pitch = M == 1 && runs == 1 ? N * es : static_cast<size_t>(r.v.pitch);
+    const cuuint64_t dims[3] = {N, M, static_cast<cuuint64_t>(runs)};
+    const cuuint64_t strides[2] = {pitch, runs > 1 ? run_bytes : pitch};
+    const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(kBlockRow / es), 32, 1}, steps[3] = {1, 1, 1};
+    const CUtensorMapDataType type = dtype == RZ_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == RZ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return encoder()(map, type, 3, r.v.p, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+    CUtensorMap a, b, out, aux;
+};
+
+template <class T, int ACT, int CG, bool BULK>
+cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
+{
+    const auto fn = k_linear_tc<T, ACT, CG, BULK>;
     if (const cudaError_t e = shared_opt_in(reinterpret_cast<const void *>(fn), kSmem - kStatic)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CG * std::min<unsigned>(a.tiles, kSms / CG));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = 1024 + a.stages * static_cast<size_t>(kBytesA + a.tile_n / CG * kTerms * 2) + kStageBytes;
+    cfg.dynamicSmemBytes = 1024 + a.stages * static_cast<size_t>(kBytesA + a.tile_n / CG * kTerms * 2) + kOutBytes;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -560,21 +687,20 @@ cudaError_t tc_launch(const TcArgs &a, const CUtensorMap &ma, const CUtensorMap 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 1 ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, fn, a, ma, mb);
+    return cudaLaunchKernelEx(&cfg, fn, a, m.a, m.b, m.out, m.aux);
 }
 
-template <class T, int CG>
-cudaError_t tc_launch_act(const TcArgs &a, const CUtensorMap &ma, const CUtensorMap &mb, void *stream)
+template <class T, int CG, bool BULK>
+cudaError_t tc_launch_act(const TcArgs &a, const Maps &m, void *stream)
 {
-    // runs of a sum are finished where they are joined
-    const int act = a.part ? RZ_ACT_NONE : a.f.act;
-    if (act == RZ_ACT_SILU) return tc_launch<T, RZ_ACT_SILU, CG>(a, ma, mb, stream);
-    return act == RZ_ACT_GELU ? tc_launch<T, RZ_ACT_GELU, CG>(a, ma, mb, stream) : tc_launch<T, RZ_ACT_NONE, CG>(a, ma, mb, stream);
+    if (a.f.act == RZ_ACT_SILU) return tc_launch<T, RZ_ACT_SILU, CG, BULK>(a, m, stream);
+    return a.f.act == RZ_ACT_GELU ? tc_launch<T, RZ_ACT_GELU, CG, BULK>(a, m, stream) : tc_launch<T, RZ_ACT_NONE, CG, BULK>(a, m, stream);
 }
 template <class T>
-cudaError_t tc_launch_of(const TcArgs &a, const CUtensorMap &ma, const CUtensorMap &mb, int pair, void *stream)
+cudaError_t tc_launch_of(const TcArgs &a, const Maps &m, int pair, bool bulk, void *stream)
 {
-    return pair ? tc_launch_act<T, 2>(a, ma, mb, stream) : tc_launch_act<T, 1>(a, ma, mb, stream);
+    if (bulk) return pair ? tc_launch_act<T, 2, true>(a, m, stream) : tc_launch_act<T, 1, true>(a, m, stream);
+    return pair ? tc_launch_act<T, 2, false>(a, m, stream) : tc_launch_act<T, 1, false>(a, m, stream);
 }
 
 }  // namespace
@@ -583,12 +709,32 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
 {
     if (!encoder()) return cudaErrorNotSupported;
     const int cg = p.pair ? 2 : 1;
-    CUtensorMap ma, mb;
+    Maps m;
     TcArgs a{};
-    if (!encode(p.a, kTileM, &ma, &a.a_merged) || !encode(p.b, p.tile_n / cg, &mb, &a.b_merged)) return cudaErrorInvalidValue;
+    if (!encode(p.a, kTileM, &m.a, &a.a_merged) || !encode(p.b, p.tile_n / cg, &m.b, &a.b_merged)) return cudaErrorInvalidValue;
     a.f = p.f;
-    a.part = p.splits > 1 ? p.part : nullptr;
-    a.part_pitch = p.part_pitch;
+    int dtype = p.out_dtype;
+    bool bulk = true;
+    if (p.splits > 1) {
+        // runs of a sum leave as they are, float32; k_linear_join finishes them
+        dtype = RZ_F32;
+        a.f = Finish{};
+        a.f.M = p.f.M;
+        a.f.N = p.f.N;
+        a.f.out.v = {reinterpret_cast<uint8_t *>(p.part), static_cast<long long>(p.part_pitch) * 4, 0};
+        if (!encode_out(a.f.out, a.f.M, a.f.N, dtype, p.splits, static_cast<size_t>(p.part_pitch) * 4 * a.f.M, &m.out))
+            return cudaErrorInvalidValue;
+        m.aux = m.out;
+    } else {
+        // pre and a residual at once would need a third place for their blocks; and TMA clips a row to whole 16 bytes
+        const auto fits = [&](const Rows &r) {
+            return !r.HW && reinterpret_cast<uintptr_t>(r.v.p) % 16 == 0 && (a.f.M == 1 || r.v.pitch % 16 == 0);
+        };
+        const Rows &aux = a.f.has_residual ? a.f.residual : a.f.has_pre ? a.f.pre : a.f.out;
+        bulk = a.f.N * dtype_size(dtype) % 16 == 0 && fits(a.f.out) && fits(aux) && !(a.f.has_residual && a.f.has_pre);
+        if (bulk) bulk = encode_out(a.f.out, a.f.M, a.f.N, dtype, 1, 0, &m.out) && encode_out(aux, a.f.M, a.f.N, dtype, 1, 0, &m.aux);
+        if (!bulk) m.out = m.aux = m.a;     // not read
+    }
     a.tile_n = p.tile_n;
     a.tiles_m = (p.f.M + cg * kTileM - 1) / (cg * kTileM);
     a.tiles_n = (p.f.N + p.tile_n - 1) / p.tile_n;
@@ -603,15 +749,15 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     const unsigned long long tiles = static_cast<unsigned long long>(a.tiles_m) * a.tiles_n * p.splits;
     if (tiles > 0x7fffffffull) return cudaErrorInvalidConfiguration;
     a.tiles = static_cast<unsigned>(tiles);
-    a.stages = std::min(kRing, (kSmem - kStatic - 1024 - kStageBytes) / (kBytesA + p.tile_n / cg * kTerms * 2));
+    a.stages = std::min(kRing, (kSmem - kStatic - 1024 - kOutBytes) / (kBytesA + p.tile_n / cg * kTerms * 2));
     a.a_turned = p.a.turned;
     a.b_turned = p.b.turned;
     const unsigned type = p.a.bf16 ? 1u : 0u;
     a.idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<unsigned>(p.a.turned) << 15) |
               (static_cast<unsigned>(p.b.turned) << 16) | (static_cast<unsigned>(p.tile_n >> 3) << 17) | (static_cast<unsigned>(cg * kTileM >> 4) << 24);
     a.status = p.status;
-    if (p.out_dtype == RZ_F32) return tc_launch_of<float>(a, ma, mb, p.pair, stream);
-    return p.out_dtype == RZ_BF16 ? tc_launch_of<__nv_bfloat16>(a, ma, mb, p.pair, stream) : tc_launch_of<__half>(a, ma, mb, p.pair, stream);
+    if (dtype == RZ_F32) return tc_launch_of<float>(a, m, p.pair, bulk, stream);
+    return dtype == RZ_BF16 ? tc_launch_of<__nv_bfloat16>(a, m, p.pair, bulk, stream) : tc_launch_of<__half>(a, m, p.pair, bulk, stream);
 }
 
 }  // namespace rz
