@@ -35,13 +35,18 @@ using dev::smem_addr;
 constexpr int kTerms = 64;                      // terms of a stage: 128 bytes, the swizzle's width
 constexpr int kTileM = 128;
 constexpr int kBytesA = kTileM * kTerms * 2;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 128 + 32 * kEpiWarps;  // loads of A, issuer, tensor memory, loads of B; the epilogue's begin at a multiple of four
+// Warps that take tiles out: eight with TMA, sixteen where loads and stores have to
+// be waited for (5883 x 96 x 250 float32 with a residual: 17 us, with eight 31).
+__host__ __device__ constexpr int epi_warps(bool bulk) { return bulk ? 8 : 16; }
+// Loads of A, issuer, tensor memory, loads of B; the epilogue's begin at a multiple of four.
+__host__ __device__ constexpr int tc_threads(bool bulk) { return 128 + 32 * epi_warps(bulk); }
 constexpr int kBlockRow = 64;                   // bytes of a row of a block on its way out, 32 rows a block
 constexpr int kBlockBytes = 32 * kBlockRow;
 constexpr int kWarpBytes = 2 * kBlockBytes;     // an epilogue warp's two blocks
-constexpr int kOutBytes = kEpiWarps * kWarpBytes;
+constexpr int kOutBytes = epi_warps(true) * kWarpBytes;
 constexpr int kStagePitch = 48;                 // without TMA: bytes of a row on its way out, 32 and a gap, so that rows differ in their banks
+constexpr int kShare = 64;                      // most columns of a tile that are one of sixteen warps'
+static_assert(epi_warps(false) * (32 * kStagePitch + kShare * 4) <= kOutBytes, "");
 constexpr int kSmem = 227 * 1024;
 constexpr int kStatic = 512;    // the kernel's own variables
 constexpr int kRing = 8;
@@ -131,7 +136,9 @@ __device__ __forceinline__ void commit(uint64_t *bar)
                      : "memory");
 }
 
-// Columns addr .. of this warp's 32 lanes of tensor memory, a row a thread.
+// Sixteen columns from addr of this warp's 32 lanes of tensor memory, a row a
+// thread; they are there after tmem_wait, which the registers pass through so that
+// no use of them moves before it.
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -140,8 +147,16 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[16])
                    "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
                  : "r"(addr)
                  : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+
 // A wait of at most a second that leaves no gap between its attempts.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int *status)
 {
@@ -265,48 +280,59 @@ __device__ __forceinline__ void emit(const Rows &to, const Finish &f, unsigned m
         }
     }
 }
-// z += the residual, PC columns from n of a row a thread.
+// The residual of PC columns from n: as a lane reads them, and turned through the
+// stage into a row a thread and added to z.
 template <class T>
-__device__ __forceinline__ void absorb(const Finish &f, unsigned m, unsigned n, uint8_t *stage, float2 (&z)[16 / sizeof(T)])
-{
-    constexpr int PC = 32 / sizeof(T), VE = PC / 2;
+struct Residual {
+    static constexpr int PC = 32 / sizeof(T), VE = PC / 2;
     using E = Raw<T, 1>;
     using V = Raw<T, VE>;
-    const int lane = threadIdx.x & 31;
-    const Rows &from = f.residual;
-    if (f.wide) {
-        V now[2];
+    V vec[2];
+    E one[PC];
+
+    __device__ __forceinline__ void read(const Finish &f, unsigned m, unsigned n)
+    {
+        const int lane = threadIdx.x & 31;
+        const Rows &from = f.residual;
+        if (f.wide) {
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
-            const unsigned r = m + lane / 2 + 16 * k, c = n + lane % 2 * VE;
-            now[k] = V{};
-            if (r < f.M && c < f.N) now[k] = *vec_at<T, VE>(from, r, c);
+            for (int k = 0; k < 2; k++) {
+                const unsigned r = m + lane / 2 + 16 * k, c = n + lane % 2 * VE;
+                vec[k] = V{};
+                if (r < f.M && c < f.N) vec[k] = *vec_at<T, VE>(from, r, c);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < PC; k++) {
+                const unsigned r = m + k * (32 / PC) + lane / PC, c = n + lane % PC;
+                one[k] = E{};
+                if (r < f.M && c < f.N)
+                    one[k] = *reinterpret_cast<const E *>(from.v.p + row_off(from, r) + static_cast<long long>(c) * sizeof(T));
+            }
+        }
+    }
+    __device__ __forceinline__ void add(const Finish &f, uint8_t *stage, float2 (&z)[PC / 2]) const
+    {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+        if (f.wide) {
+#pragma unroll
+            for (int k = 0; k < 2; k++) *reinterpret_cast<V *>(stage + (lane / 2 + 16 * k) * kStagePitch + lane % 2 * 16) = vec[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < PC; k++)
+                *reinterpret_cast<E *>(stage + (k * (32 / PC) + lane / PC) * kStagePitch + lane % PC * sizeof(T)) = one[k];
         }
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 2; k++) *reinterpret_cast<V *>(stage + (lane / 2 + 16 * k) * kStagePitch + lane % 2 * 16) = now[k];
-    } else {
-        E now[PC];
+        for (int h = 0; h < 2; h++) {
+            float2 half[VE / 2];
+            unpack2<T, VE>(reinterpret_cast<const V *>(stage + lane * kStagePitch)[h], half);
 #pragma unroll
-        for (int k = 0; k < PC; k++) {
-            const unsigned r = m + k * (32 / PC) + lane / PC, c = n + lane % PC;
-            now[k] = r < f.M && c < f.N ? *reinterpret_cast<const E *>(from.v.p + row_off(from, r) + static_cast<long long>(c) * sizeof(T))
-                                        : E{};
+            for (int q = 0; q < VE / 2; q++) z[h * VE / 2 + q] = __fadd2_rn(z[h * VE / 2 + q], half[q]);
         }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < PC; k++)
-            *reinterpret_cast<E *>(stage + (k * (32 / PC) + lane / PC) * kStagePitch + lane % PC * sizeof(T)) = now[k];
     }
-    __syncwarp();
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-        float2 half[VE / 2];
-        unpack2<T, VE>(reinterpret_cast<const V *>(stage + lane * kStagePitch)[h], half);
-#pragma unroll
-        for (int q = 0; q < VE / 2; q++) z[h * VE / 2 + q] = __fadd2_rn(z[h * VE / 2 + q], half[q]);
-    }
-}
+};
 
 // A tile's place and the chunks of its run.
 struct Tile {
@@ -341,14 +367,15 @@ __device__ __forceinline__ void planes_of(int planes, int j, int &a, int &b)
 // BULK: results leave, and residuals come, by TMA (map_out; map_aux: the residual's or
 // pre's); else by loads and stores.
 template <class T, int ACT, int CG, bool BULK>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(tc_threads(BULK), 1)
 k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_aux)
 {
+    constexpr int kEpiWarps = epi_warps(BULK);
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[kRing], empty[kRing], done[2], taken[2];
     __shared__ uint32_t tmem_slot;
-    __shared__ uint64_t came[kEpiWarps][2];     // a residual's block, each of a warp's two
+    __shared__ uint64_t came[epi_warps(true)][2];     // a residual's block, each of a warp's two
     const uint32_t pad = (1024 - (smem_addr(raw) & 1023)) & 1023;
     const uint32_t ring = smem_addr(raw) + pad;
     const int rows_b = a.tile_n / CG;     // this CTA's share of B's rows
@@ -366,7 +393,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
         for (int i = 0; i < 2; i++) {
             dev::mbar_init(done + i, 1);
             dev::mbar_init(taken + i, kEpiWarps * CG);
-            for (int e = 0; e < kEpiWarps; e++) dev::mbar_init(&came[e][i], 1);
+            for (int e = 0; e < epi_warps(true); e++) dev::mbar_init(&came[e][i], 1);
         }
         dev::fence_mbar_init();
     }
@@ -474,9 +501,9 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             }
         }
     } else if (warp >= 4) {
-        // two warps share 32 rows of the tile, half of its columns each
-        const int e = warp - 4, quarter = warp & 3, cols = a.tile_n / 2;
-        uint8_t *out = raw + pad + a.stages * stage_bytes + e * kWarpBytes;
+        // two (four) warps share 32 rows of the tile, half (a quarter) of its columns each
+        const int e = warp - 4, quarter = warp & 3, cols = a.tile_n / (kEpiWarps / 4);
+        uint8_t *out = raw + pad + a.stages * stage_bytes + e * (BULK ? kWarpBytes : 32 * kStagePitch);
         const bool vectors = (reinterpret_cast<uintptr_t>(a.f.bias) & 15) == 0;
         unsigned i = 0;
         bool ok = true;
@@ -490,9 +517,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                     arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), 0));
             }
         };
-        const auto columns = [&](uint32_t at, float2(&z)[8]) {
-            uint32_t v[16];
-            tmem_load(at, v);
+        const auto floats = [](const uint32_t(&v)[16], float2(&z)[8]) {
 #pragma unroll
             for (int q = 0; q < 8; q++) z[q] = make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
         };
@@ -524,11 +549,22 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + (e >> 2) * cols;
+                // a block's columns are asked for while the one before is worked on
+                uint32_t v[SUBS][16];
+#pragma unroll
+                for (int q = 0; q < SUBS; q++) tmem_load(acc + 16 * q, v[q]);
                 for (int b = 0; b < blocks; b++) {
                     float2 z[SUBS][8];
 #pragma unroll
-                    for (int q = 0; q < SUBS; q++) columns(acc + b * BC + 16 * q, z[q]);
-                    if (b == blocks - 1) give_back();
+                    for (int q = 0; q < SUBS; q++) {
+                        tmem_wait(v[q]);
+                        floats(v[q], z[q]);
+                    }
+                    if (b == blocks - 1)
+                        give_back();
+                    else
+#pragma unroll
+                        for (int q = 0; q < SUBS; q++) tmem_load(acc + (b + 1) * BC + 16 * q, v[q]);
                     if (b >= live) continue;
                     const int n = static_cast<int>(n0) + b * BC;
                     if (a.f.has_residual && b + 1 < live && lane == 0) {
@@ -569,31 +605,57 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         } else {
             constexpr int PC = 32 / sizeof(T);
+            float *bias = reinterpret_cast<float *>(raw + pad + a.stages * stage_bytes + kEpiWarps * 32 * kStagePitch) + e * kShare;
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
                 const Tile w = tile_at(a, t);
                 const unsigned m0 = (w.m * CG + rank) * kTileM + 32 * quarter, n0 = w.n * a.tile_n + (e >> 2) * cols;
+                // the columns' bias before the tile is done; residuals a step ahead
+                __syncwarp();
+                for (int c = lane; c < cols; c += 32) bias[c] = a.f.bias && n0 + c < a.f.N ? __ldg(a.f.bias + n0 + c) : 0.0f;
+                __syncwarp();
+                Residual<T> even, odd;      // two that take turns: a copy would wait for what is on its way
+                if (a.f.has_residual) {
+                    even.read(a.f, m0, n0);
+                    // the rest on its way to L2, a row a lane
+                    if (m0 + lane < a.f.M && n0 < a.f.N) {
+                        const uint8_t *at = a.f.residual.v.p + row_off(a.f.residual, m0 + lane);
+                        const unsigned to = min(n0 + cols, a.f.N) * sizeof(T);
+                        for (unsigned o = n0 * sizeof(T); o < to; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + o));
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + to - 1));
+                    }
+                }
                 ok = wait_for(done + (i & 1), i >> 1 & 1, a.status);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + (e >> 2) * cols;
-                for (int c0 = 0; c0 < cols; c0 += 16) {
-                    float2 z[8];
-                    columns(acc + c0, z);
-                    if (c0 + 16 >= cols) give_back();
-                    const unsigned n = n0 + c0;
-                    if (n >= a.f.N || m0 >= a.f.M) continue;
-                    add_bias(a.f, vectors, n, z);
-#pragma unroll
-                    for (int h = 0; h < 16; h += PC) {
-                        float2 part[PC / 2];
-#pragma unroll
-                        for (int q = 0; q < PC / 2; q++) part[q] = z[h / 2 + q];
-                        if (a.f.has_pre) emit<T>(a.f.pre, a.f, m0, n + h, out, part);
-#pragma unroll
-                        for (int q = 0; q < PC / 2; q++) part[q] = activated<T, ACT>(part[q]);
-                        if (a.f.has_residual) absorb<T>(a.f, m0, n + h, out, part);
-                        emit<T>(a.f.out, a.f, m0, n + h, out, part);
+                float2 z[8];
+                const auto part = [&](int c, const Residual<T> &now, Residual<T> &next) {
+                    if (c % 16 == 0) {
+                        uint32_t v[16];
+                        tmem_load(acc + c, v);
+                        tmem_wait(v);
+                        floats(v, z);
+                        if (c + 16 >= cols) give_back();
                     }
+                    const unsigned n = n0 + c;
+                    if (n >= a.f.N || m0 >= a.f.M) return;
+                    if (a.f.has_residual && c + PC < cols) next.read(a.f, m0, n + PC);
+                    float2 y[PC / 2];
+#pragma unroll
+                    for (int q = 0; q < PC / 2; q += 2) {
+                        const float4 b = *reinterpret_cast<const float4 *>(bias + c + 2 * q);
+                        y[q] = __fadd2_rn(PC == 8 && c % 16 ? z[(q + 4) % 8] : z[q], make_float2(b.x, b.y));
+                        y[q + 1] = __fadd2_rn(PC == 8 && c % 16 ? z[(q + 5) % 8] : z[q + 1], make_float2(b.z, b.w));
+                    }
+                    if (a.f.has_pre) emit<T>(a.f.pre, a.f, m0, n, out, y);
+#pragma unroll
+                    for (int q = 0; q < PC / 2; q++) y[q] = activated<T, ACT>(y[q]);
+                    if (a.f.has_residual) now.add(a.f, out, y);
+                    emit<T>(a.f.out, a.f, m0, n, out, y);
+                };
+                for (int c = 0; c < cols; c += 2 * PC) {
+                    part(c, even, odd);
+                    if (c + PC < cols) part(c + PC, odd, even);
                 }
             }
         }
@@ -676,7 +738,7 @@ cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
     if (const cudaError_t e = shared_opt_in(reinterpret_cast<const void *>(fn), kSmem - kStatic)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CG * std::min<unsigned>(a.tiles, kSms / CG));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(tc_threads(BULK));
     cfg.dynamicSmemBytes = 1024 + a.stages * static_cast<size_t>(kBytesA + a.tile_n / CG * kTerms * 2) + kOutBytes;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
