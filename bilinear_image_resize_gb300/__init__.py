@@ -650,13 +650,27 @@ def _linear_of(x, out, weight, act, names):
     return RzLinear(N, H, W, C, K, _map_dtype(x, names[0]), _int(act, "act")), mx, mo, *_matrix(weight, "weight", (K, C))
 
 
-def map_linear_workspace(x, y, weight, act: int = RZ_ACT_NONE) -> int:
-    """Bytes of workspace that map_linear needs for tensors like these."""
-    _with_torch()
-    d, mx, _, w, pitch = _linear_of(x, y, weight, act, ("x", "y"))
+def _linear_args(x, y, weight, residual, pre, act):
+    """map_linear's descriptor, maps and weight: what its workspace goes by, in its C order."""
+    d, mx, my, w, pitch = _linear_of(x, y, weight, act, ("x", "y"))
+    shape = (d.N, d.H, d.W, d.K)
+    mr = None if residual is None else _map_of(residual, "residual", shape)[1]
+    mp = None if pre is None else _map_of(pre, "pre", shape)[1]
+    if (mr is not None and residual.dtype is not x.dtype) or (mp is not None and pre.dtype is not x.dtype):
+        raise ValueError("x, residual and pre differ in dtype")
+    return d, mx, w, pitch, mr, mp, my
+
+
+def _linear_query(args) -> int:
     n = ctypes.c_size_t(0)
-    _check(_native.load().map_linear_workspace(d, mx, w, pitch, ctypes.byref(n)), "map_linear_workspace")
+    _check(_native.load().map_linear_workspace(*args, ctypes.byref(n)), "map_linear_workspace")
     return n.value
+
+
+def map_linear_workspace(x, y, weight, residual=None, pre=None, act: int = RZ_ACT_NONE) -> int:
+    """Bytes of workspace that map_linear needs for these tensors."""
+    _with_torch()
+    return _linear_query(_linear_args(x, y, weight, residual, pre, act))
 
 
 def map_linear(x, y, weight, bias=None, residual=None, pre=None, act: int = RZ_ACT_NONE, workspace=None, status=None,
@@ -666,39 +680,46 @@ def map_linear(x, y, weight, bias=None, residual=None, pre=None, act: int = RZ_A
     weight: (K, C) of the maps' dtype, rows packed; bias: float32 (K,) or None;
     residual: a map of y's shape (y itself among them) or None; pre: a map of y's
     shape that takes x weight^T + bias for the gradient, or None; workspace: a
-    CUDA tensor of map_linear_workspace(x, y, weight, act) bytes, or None to take
-    one from torch's allocator; status: an int32 CUDA tensor of one element for
-    a kernel's time-out, or None."""
+    CUDA tensor of map_linear_workspace bytes, or None to take one from torch's
+    allocator; status: an int32 CUDA tensor of one element for a kernel's
+    time-out, or None."""
     _with_torch()
-    d, mx, my, w, pitch = _linear_of(x, y, weight, act, ("x", "y"))
+    args = _linear_args(x, y, weight, residual, pre, act)
+    d, mx, w, pitch, mr, mp, my = args
     _on_current_device(x, y, weight, bias, residual, pre)
-    shape = (d.N, d.H, d.W, d.K)
-    mr = None if residual is None else _map_of(residual, "residual", shape)[1]
-    mp = None if pre is None else _map_of(pre, "pre", shape)[1]
-    if (mr is not None and residual.dtype is not x.dtype) or (mp is not None and pre.dtype is not x.dtype):
-        raise ValueError("x, residual and pre differ in dtype")
     b, st = _floats(bias, "bias", (d.K,)), None if status is None else _status_of(status, x)
-    lib = _native.load()
+    f = _native.load().map_linear
     if workspace is None and d.N * d.H * d.W <= 8:      # needs none
-        _check(lib.map_linear(d, mx, w, pitch, b, mr, mp, my, None, 0, st, _stream_at(stream, x)), "map_linear")
+        _check(f(d, mx, w, pitch, b, mr, mp, my, None, 0, st, _stream_at(stream, x)), "map_linear")
         return
-
-    def query(_):
-        n = ctypes.c_size_t(0)
-        _check(lib.map_linear_workspace(d, mx, w, pitch, ctypes.byref(n)), "map_linear_workspace")
-        return n.value
-
-    _check(_with_workspace(lambda p, n, s: lib.map_linear(d, mx, w, pitch, b, mr, mp, my, p, n, st, s), workspace, query, d,
-                           x, stream), "map_linear")
+    _check(_with_workspace(lambda p, n, s: f(d, mx, w, pitch, b, mr, mp, my, p, n, st, s), workspace, _linear_query, args, x,
+                           stream), "map_linear")
 
 
-def map_linear_grad_workspace(dy, x, weight, act: int = RZ_ACT_NONE) -> int:
-    """Bytes of workspace that map_linear_grad needs for tensors like these."""
-    _with_torch()
+def _linear_grad_args(dy, x, weight, dx, dweight, pre, act):
+    """The same of map_linear_grad."""
     d, mx, md, w, pitch = _linear_of(x, dy, weight, act, ("x", "dy"))
+    mp = None if pre is None else _map_of(pre, "pre", (d.N, d.H, d.W, d.K))[1]
+    mo = None if dx is None else _map_of(dx, "dx", (d.N, d.H, d.W, d.C))[1]
+    if (mp is not None and pre.dtype is not x.dtype) or (mo is not None and dx.dtype is not x.dtype):
+        raise ValueError("x, pre and dx differ in dtype")
+    dw, dw_pitch, dw_type = None, 0, d.dtype
+    if dweight is not None:
+        dw_type = _map_dtype(dweight, "dweight")
+        dw, dw_pitch = _matrix(dweight, "dweight", (d.K, d.C))
+    return d, md, mx, w, pitch, mp, mo, dw, dw_pitch, dw_type
+
+
+def _linear_grad_query(args) -> int:
     n = ctypes.c_size_t(0)
-    _check(_native.load().map_linear_grad_workspace(d, md, mx, w, pitch, ctypes.byref(n)), "map_linear_grad_workspace")
+    _check(_native.load().map_linear_grad_workspace(*args, ctypes.byref(n)), "map_linear_grad_workspace")
     return n.value
+
+
+def map_linear_grad_workspace(dy, x, weight, dx=None, dweight=None, pre=None, act: int = RZ_ACT_NONE) -> int:
+    """Bytes of workspace that map_linear_grad needs for these tensors (with or without dbias)."""
+    _with_torch()
+    return _linear_grad_query(_linear_grad_args(dy, x, weight, dx, dweight, pre, act))
 
 
 def map_linear_grad(dy, x, weight, dx=None, dweight=None, dbias=None, pre=None, act: int = RZ_ACT_NONE, workspace=None,
@@ -707,27 +728,12 @@ def map_linear_grad(dy, x, weight, dx=None, dweight=None, dbias=None, pre=None, 
     arguments of the map_linear call and the pre it wrote (None without an
     activation).  dweight: (K, C), of the maps' dtype or float32."""
     _with_torch()
-    d, mx, md, w, pitch = _linear_of(x, dy, weight, act, ("x", "dy"))
+    args = _linear_grad_args(dy, x, weight, dx, dweight, pre, act)
     _on_current_device(x, dy, weight, dx, dweight, dbias, pre)
-    mp = None if pre is None else _map_of(pre, "pre", (d.N, d.H, d.W, d.K))[1]
-    mo = None if dx is None else _map_of(dx, "dx", (d.N, d.H, d.W, d.C))[1]
-    for t, n in ((pre, "pre"), (dx, "dx")):
-        if t is not None and t.dtype is not x.dtype:
-            raise ValueError(f"{n} and x differ in dtype")
-    dw, dw_pitch, dw_type = None, 0, d.dtype
-    if dweight is not None:
-        dw_type = _map_dtype(dweight, "dweight")
-        dw, dw_pitch = _matrix(dweight, "dweight", (d.K, d.C))
-    b, st = _floats(dbias, "dbias", (d.K,)), _status_of(status, x)
-    lib = _native.load()
-
-    def query(_):
-        n = ctypes.c_size_t(0)
-        _check(lib.map_linear_grad_workspace(d, md, mx, w, pitch, ctypes.byref(n)), "map_linear_grad_workspace")
-        return n.value
-
-    _check(_with_workspace(lambda p, n, s: lib.map_linear_grad(d, md, mx, w, pitch, mp, mo, dw, dw_pitch, dw_type, b, p, n,
-                                                               st, s), workspace, query, d, x, stream), "map_linear_grad")
+    b, st = _floats(dbias, "dbias", (args[0].K,)), None if status is None else _status_of(status, x)
+    f = _native.load().map_linear_grad
+    _check(_with_workspace(lambda p, n, s: f(*args, b, p, n, st, s), workspace, _linear_grad_query, args, x, stream),
+           "map_linear_grad")
 
 
 def _qk_of(x, y, q_heads, k_heads, head_dim, base, row_pairs, col_pairs, scale, interleaved, eps, names):

@@ -229,9 +229,9 @@ SIGNATURES = {
     "resize_map": (_i, [_resample, _map, _map, _map, _p]),
     "resize_map_grad_workspace": (_i, [_resample, ctypes.POINTER(_sz)]),
     "resize_map_grad": (_i, [_resample, _map, _map, _p, _sz, _p]),
-    "map_linear_workspace": (_i, [_linear, _map, _p, _sz, ctypes.POINTER(_sz)]),
+    "map_linear_workspace": (_i, [_linear, _map, _p, _sz, _map, _map, _map, ctypes.POINTER(_sz)]),
     "map_linear": (_i, [_linear, _map, _p, _sz, _p, _map, _map, _map, _p, _sz, _p, _p]),
-    "map_linear_grad_workspace": (_i, [_linear, _map, _map, _p, _sz, ctypes.POINTER(_sz)]),
+    "map_linear_grad_workspace": (_i, [_linear, _map, _map, _p, _sz, _map, _map, _p, _sz, _i, ctypes.POINTER(_sz)]),
     "map_linear_grad": (_i, [_linear, _map, _map, _p, _sz, _map, _map, _p, _sz, _i, _p, _p, _sz, _p, _p]),
     "map_qk_norm": (_i, [_qk, _map, _map, _p, _p, _p, _p]),
     "map_qk_norm_grad_workspace": (_i, [_qk, ctypes.POINTER(_sz)]),

@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(256) k_linear_sums(const float *sums, unsigned
     dbias[c] = s;
 }
 
-// The runs of a product joined in order, and its epilogue.
+// The runs of a product joined in order, and its epilogue; a run alone where its
+// result's rows are not TMA's to write.
 struct JoinArgs {
     Finish f;
     const float *part;
@@ -171,37 +172,64 @@ struct JoinArgs {
     int splits;
 };
 
-template <class T, int ACT, bool WIDE>
+constexpr int kJoinUnits = 4;   // units a thread has in flight where vectors do not fit
+
+// UNIT: elements taken at once, a vector, a pair or one.
+template <class T, int ACT, int UNIT>
 __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ JoinArgs a)
 {
-    constexpr int VE = WIDE ? 16 / sizeof(T) : 1;
+    constexpr bool WIDE = UNIT * sizeof(T) == 16;
+    constexpr int U = WIDE ? 1 : kJoinUnits;
     grid_launch_dependents();
     grid_dependency_wait();
-    const unsigned vecs = a.f.N / VE;
-    const unsigned long long id = blockIdx.x * 256ull + threadIdx.x;
-    const unsigned m = static_cast<unsigned>(id / vecs), n = static_cast<unsigned>(id - static_cast<unsigned long long>(m) * vecs) * VE;
-    if (m >= a.f.M) return;
-    const float *from = a.part + static_cast<long long>(m) * a.pitch + n;
+    // a block's first unit by 64-bit division, the others from there
+    const unsigned units = a.f.N / UNIT;
+    const unsigned long long base = static_cast<unsigned long long>(blockIdx.x) * (256 * U);
+    const unsigned m0 = static_cast<unsigned>(base / units), n0 = static_cast<unsigned>(base - static_cast<unsigned long long>(m0) * units);
     const long long run = static_cast<long long>(a.f.M) * a.pitch;
     if constexpr (WIDE) {
-        float2 z[VE / 2] = {}, b[VE / 2];
+        const unsigned q0 = n0 + threadIdx.x, m = m0 + q0 / units, n = q0 % units * UNIT;
+        if (m >= a.f.M) return;
+        const float *from = a.part + static_cast<long long>(m) * a.pitch + n;
+        float2 z[UNIT / 2] = {}, b[UNIT / 2];
 #pragma unroll 8
         for (int r = 0; r < a.splits; r++, from += run)
 #pragma unroll
-            for (int q = 0; q < VE; q += 4) {
+            for (int q = 0; q < UNIT; q += 4) {
                 const float4 v = __ldcs(reinterpret_cast<const float4 *>(from + q));
                 z[q / 2] = __fadd2_rn(z[q / 2], make_float2(v.x, v.y));
                 z[q / 2 + 1] = __fadd2_rn(z[q / 2 + 1], make_float2(v.z, v.w));
             }
-        bias_of<VE>(a.f, n, b);
-        Raw<T, VE> r{};
-        if (a.f.has_residual) r = *vec_at<T, VE>(a.f.residual, m, n);
-        finish<T, VE, ACT>(a.f, m, n, z, b, r);
+        bias_of<UNIT>(a.f, n, b);
+        Raw<T, UNIT> r{};
+        if (a.f.has_residual) r = *vec_at<T, UNIT>(a.f.residual, m, n);
+        finish<T, UNIT, ACT>(a.f, m, n, z, b, r);
     } else {
-        float z[1] = {0.0f};
-#pragma unroll 8
-        for (int r = 0; r < a.splits; r++, from += run) z[0] += __ldcs(from);
-        finish_column<T, ACT, 1>(a.f, m, n, z, a.f.bias ? __ldg(a.f.bias + n) : 0.0f);
+        unsigned m[U], n[U];
+        const float *from[U];
+        float2 z[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const unsigned q = n0 + threadIdx.x + 256 * u;
+            m[u] = m0 + q / units;
+            n[u] = q % units * UNIT;
+            // past the last: that one again, and not stored
+            from[u] = a.part + static_cast<long long>(min(m[u], a.f.M - 1)) * a.pitch + n[u];
+            z[u] = both(0.0f);
+        }
+#pragma unroll 2
+        for (int r = 0; r < a.splits; r++)
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                if (UNIT == 2)
+                    z[u] = __fadd2_rn(z[u], __ldcs(reinterpret_cast<const float2 *>(from[u])));
+                else
+                    z[u].x += __ldcs(from[u]);
+                from[u] += run;
+            }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (m[u] < a.f.M) finish_unit<T, ACT, UNIT>(a.f, m[u], n[u], z[u]);
     }
 }
 
@@ -280,8 +308,7 @@ __global__ void __launch_bounds__(256) k_linear_rows(const __grid_constant__ Row
     }
     const unsigned n = n0 + lane / ROWS, m = m0 + lane % ROWS;
     if (lane >= N * ROWS || n >= a.f.N || m >= a.f.M) return;
-    const float one[1] = {z};
-    finish_column<T, ACT, 1>(a.f, m, n, one, a.f.bias ? __ldg(a.f.bias + n) : 0.0f);
+    finish_unit<T, ACT, 1>(a.f, m, n, make_float2(z, 0.0f));
 }
 
 // ------------------------------------------------------------------ host side
@@ -412,7 +439,8 @@ struct Cut {
     unsigned pitch;
     size_t bytes;
 };
-Cut cut(unsigned M, unsigned N, unsigned terms, int dtype)
+// through: a single run goes through the workspace as well.
+Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, bool through)
 {
     const long long chunks = static_cast<long long>((terms + 63) / 64) * (dtype == RZ_F32 ? 6 : 1);
     Cut best{};
@@ -430,10 +458,11 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype)
                 if (splits != want) continue;
                 const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
                 double t = waves * (run * stage + 2500) + 4.0 * tile;
-                if (splits > 1) t += 6500 + 170.0 * splits + 4.0 * M * pitch * (splits + 1) / 2500.0;
+                const bool joined = splits > 1 || through;
+                if (joined) t += 6500 + 170.0 * splits + 4.0 * M * pitch * (splits + 1) / 2500.0;
                 if (!best.tile_n || t < least) {
                     least = t;
-                    best = {tile, pair, splits, pitch, splits > 1 ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
+                    best = {tile, pair, splits, pitch, joined ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
                 }
                 if (waves > 3) break;
             }
@@ -482,9 +511,19 @@ unsigned pack_chunks(unsigned rows, unsigned cols)
 template <class T, int ACT>
 cudaError_t join_launch(const JoinArgs &a, void *stream)
 {
-    const unsigned long long n = static_cast<unsigned long long>(a.f.M) * (a.f.wide ? a.f.N / (16 / sizeof(T)) : a.f.N);
-    return launch(a.f.wide ? k_linear_join<T, ACT, true> : k_linear_join<T, ACT, false>,
-                  dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream, a);
+    constexpr int VE = 16 / sizeof(T);
+    // pairs: rows of them, two elements' alignment everywhere
+    bool even = a.f.N % 2 == 0;
+    for (const Rows *r : {&a.f.out, a.f.has_pre ? &a.f.pre : nullptr, a.f.has_residual ? &a.f.residual : nullptr})
+        if (r && (reinterpret_cast<uintptr_t>(r->v.p) | static_cast<uintptr_t>(r->v.pitch) | static_cast<uintptr_t>(r->v.bstride) |
+                  static_cast<uintptr_t>(r->HW ? r->bytes : 0)) % (2 * sizeof(T)))
+            even = false;
+    const unsigned unit = a.f.wide ? VE : even ? 2 : 1;
+    const unsigned long long n = static_cast<unsigned long long>(a.f.M) * (a.f.N / unit), block = 256ull * (a.f.wide ? 1 : kJoinUnits);
+    const unsigned long long blocks = (n + block - 1) / block;
+    if (blocks > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+    const auto fn = a.f.wide ? k_linear_join<T, ACT, VE> : even ? k_linear_join<T, ACT, 2> : k_linear_join<T, ACT, 1>;
+    return launch(fn, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, a);
 }
 template <class T>
 cudaError_t join_of(const JoinArgs &a, void *stream)
@@ -502,13 +541,13 @@ cudaError_t product(const Operand &a, const Operand &b, const Finish &f, int out
     p.f = f;
     p.out_dtype = out_dtype;
     p.splits = c.splits;
-    p.part = part;
+    p.part = c.bytes ? part : nullptr;
     p.part_pitch = c.pitch;
     p.tile_n = c.tile_n;
     p.pair = c.pair;
     p.status = status;
     cudaError_t e = launch_product(p, stream);
-    if (e != cudaSuccess || c.splits == 1) return e;
+    if (e != cudaSuccess || !c.bytes) return e;
     const JoinArgs j{f, part, c.pitch, c.splits};
     if (out_dtype == RZ_F32) return join_of<float>(j, stream);
     return out_dtype == RZ_BF16 ? join_of<__nv_bfloat16>(j, stream) : join_of<__half>(j, stream);
@@ -580,17 +619,27 @@ cudaError_t few_rows(const Rows &x, const Rows &w, const Finish &f, unsigned C, 
 
 // What a forward call lays out, and where in its workspace.
 struct Forward {
+    bool few;
     Laid x, w;
+    Finish out;
     Cut c;
     size_t part, total;
 };
-Forward plan_forward(const rz_linear *d, const LinPlan &p, const rz_map *x, const void *weight, size_t weight_pitch)
+Forward plan_forward(const rz_linear *d, const LinPlan &p, const rz_map *x, const void *weight, size_t weight_pitch, const rz_map *y,
+                     const rz_map *pre, const rz_map *residual)
 {
+    const unsigned C = static_cast<unsigned>(d->C), K = static_cast<unsigned>(d->K);
     Forward f{};
-    if (is_few(p.P, static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), d->dtype)) return f;
-    f.x = lay(rows_of(x, p.x), p.P, static_cast<unsigned>(d->C), d->dtype, false);
-    f.w = lay(rows_of(weight, weight_pitch), static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), d->dtype, false);
-    f.c = cut(p.P, static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), d->dtype);
+    Rows rp, rr;
+    if (pre) rp = rows_of(pre, p.y);
+    if (residual) rr = rows_of(residual, p.y);
+    f.out = finish_of(rows_of(y, p.y), p.P, K, d->dtype, pre ? &rp : nullptr, residual ? &rr : nullptr);
+    f.out.act = d->act;
+    f.few = is_few(p.P, K, C, d->dtype);
+    f.x = lay(rows_of(x, p.x), p.P, C, d->dtype, false);
+    f.w = lay(rows_of(weight, weight_pitch), K, C, d->dtype, false);
+    if (f.few) return f;
+    f.c = cut(p.P, K, C, d->dtype, !direct_out(f.out, d->dtype));
     f.w.at = up(f.x.bytes, 256);
     f.part = f.w.at + up(f.w.bytes, 256);
     f.total = f.part + f.c.bytes;
@@ -600,20 +649,30 @@ Forward plan_forward(const rz_linear *d, const LinPlan &p, const rz_map *x, cons
 // The same of a gradient call.
 struct Backward {
     Laid dz, x, w;
+    Finish dx, dw;
     Cut cx, cw;
     unsigned chunks;
     size_t sums, part, total;
 };
-Backward plan_backward(const rz_linear *d, const LinPlan &p, const rz_map *dy, const rz_map *x, const void *weight,
-                       size_t weight_pitch)
+Backward plan_backward(const rz_linear *d, const LinPlan &p, const rz_map *dy, const rz_map *x, const void *weight, size_t weight_pitch,
+                       const rz_map *dx, const void *dweight, size_t dweight_pitch, int dweight_dtype)
 {
     const unsigned C = static_cast<unsigned>(d->C), K = static_cast<unsigned>(d->K);
     Backward b{};
     b.dz = lay(rows_of(dy, p.y), p.P, K, d->dtype, d->act != RZ_ACT_NONE);
+    if (!dx && !dweight) b.dz.bytes = 0;
     b.x = lay(rows_of(x, p.x), p.P, C, d->dtype, false);
+    if (!dweight) b.x.bytes = 0;
     b.w = lay(rows_of(weight, weight_pitch), K, C, d->dtype, false);
-    b.cx = cut(p.P, C, K, d->dtype);
-    b.cw = cut(K, C, p.P, d->dtype);
+    if (!dx) b.w.bytes = 0;
+    if (dx) {
+        b.dx = finish_of(rows_of(dx, p.x), p.P, C, d->dtype, nullptr, nullptr);
+        b.cx = cut(p.P, C, K, d->dtype, !direct_out(b.dx, d->dtype));
+    }
+    if (dweight) {
+        b.dw = finish_of(rows_of(dweight, dweight_pitch), K, C, dweight_dtype, nullptr, nullptr);
+        b.cw = cut(K, C, p.P, d->dtype, !direct_out(b.dw, dweight_dtype));
+    }
     b.chunks = pack_chunks(p.P, K);
     b.x.at = up(b.dz.bytes, 256);
     b.w.at = b.x.at + up(b.x.bytes, 256);
@@ -633,17 +692,44 @@ bool workspace_ok(const void *p, size_t bytes, size_t need)
 
 using namespace rz;
 
+namespace rz {
+namespace {
+
+int forward_check(const rz_linear *d, LinPlan *p, const rz_map *x, const void *weight, size_t weight_pitch, const rz_map *residual,
+                  const rz_map *pre, const rz_map *y)
+{
+    if (const int rc = lin_check(d, p)) return rc;
+    if (p->x.empty()) return RZ_OK;
+    const auto map = [](const rz_map *m, const Shape &s) { return !m || map_ok(m, s); };
+    if (!x || !y || !map(x, p->x) || !map(y, p->y) || !map(residual, p->y) || !map(pre, p->y)) return RZ_ERR_ARG;
+    return matrix_ok(weight, weight_pitch, d->K, d->C, p->x.es) ? RZ_OK : RZ_ERR_ARG;
+}
+
+int backward_check(const rz_linear *d, LinPlan *p, const rz_map *dy, const rz_map *x, const void *weight, size_t weight_pitch,
+                   const rz_map *pre, const rz_map *dx, const void *dweight, size_t dweight_pitch, int dweight_dtype)
+{
+    if (const int rc = lin_check(d, p)) return rc;
+    if (dweight && ((dweight_dtype != d->dtype && dweight_dtype != RZ_F32) ||
+                    !matrix_ok(dweight, dweight_pitch, d->K, d->C, dtype_size(dweight_dtype))))
+        return RZ_ERR_ARG;
+    if (p->x.empty()) return RZ_OK;
+    if (!map_ok(x, p->x) || !map_ok(dy, p->y) || (dx && !map_ok(dx, p->x))) return RZ_ERR_ARG;
+    if (d->act != RZ_ACT_NONE ? !map_ok(pre, p->y) : pre && !map_ok(pre, p->y)) return RZ_ERR_ARG;
+    return matrix_ok(weight, weight_pitch, d->K, d->C, p->x.es) ? RZ_OK : RZ_ERR_ARG;
+}
+
+}  // namespace
+}  // namespace rz
+
 extern "C" {
 
-int map_linear_workspace(const rz_linear *d, const rz_map *x, const void *weight, size_t weight_pitch, size_t *bytes)
+int map_linear_workspace(const rz_linear *d, const rz_map *x, const void *weight, size_t weight_pitch, const rz_map *residual,
+                         const rz_map *pre, const rz_map *y, size_t *bytes)
 {
     LinPlan p;
-    const int rc = bytes ? lin_check(d, &p) : RZ_ERR_ARG;
+    const int rc = bytes ? forward_check(d, &p, x, weight, weight_pitch, residual, pre, y) : RZ_ERR_ARG;
     if (rc) return rc;
-    *bytes = 0;
-    if (p.x.empty()) return RZ_OK;
-    if (!maps::map_ok(x, p.x) || !matrix_ok(weight, weight_pitch, d->K, d->C, p.x.es)) return RZ_ERR_ARG;
-    *bytes = plan_forward(d, p, x, weight, weight_pitch).total;
+    *bytes = p.x.empty() ? 0 : plan_forward(d, p, x, weight, weight_pitch, y, pre, residual).total;
     return RZ_OK;
 }
 
@@ -652,11 +738,8 @@ int map_linear(const rz_linear *d, const rz_map *x, const void *weight, size_t w
                void *stream)
 {
     LinPlan p;
-    if (const int rc = lin_check(d, &p)) return rc;
+    if (const int rc = forward_check(d, &p, x, weight, weight_pitch, residual, pre, y)) return rc;
     if (p.x.empty()) return RZ_OK;
-    const auto map = [](const rz_map *m, const maps::Shape &s) { return !m || maps::map_ok(m, s); };
-    if (!x || !y || !map(x, p.x) || !map(y, p.y) || !map(residual, p.y) || !map(pre, p.y)) return RZ_ERR_ARG;
-    if (!matrix_ok(weight, weight_pitch, d->K, d->C, p.x.es)) return RZ_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(bias) % 4 || reinterpret_cast<uintptr_t>(status) % 4) return RZ_ERR_ARG;
     const Range ry = range_of(*y, p.y), rx = range_of(*x, p.x), rw = range_of(weight, weight_pitch, d->K, d->C, p.x.es);
     const Range rb{reinterpret_cast<uintptr_t>(bias), reinterpret_cast<uintptr_t>(bias) + (bias ? 4 * size_t(d->K) : 0)};
@@ -668,36 +751,27 @@ int map_linear(const rz_linear *d, const rz_map *x, const void *weight, size_t w
             (residual && meet(rp, range_of(*residual, p.y))))
             return RZ_ERR_ARG;
     }
-    const Forward f = plan_forward(d, p, x, weight, weight_pitch);
+    Forward f = plan_forward(d, p, x, weight, weight_pitch, y, pre, residual);
     if (!workspace_ok(workspace, workspace_bytes, f.total)) return RZ_ERR_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    Rows rr, rp;
-    if (residual) rr = rows_of(residual, p.y);
-    if (pre) rp = rows_of(pre, p.y);
-    Finish out = finish_of(rows_of(y, p.y), p.P, static_cast<unsigned>(d->K), d->dtype, pre ? &rp : nullptr, residual ? &rr : nullptr);
-    out.bias = bias;
-    out.act = d->act;
-    if (is_few(p.P, static_cast<unsigned>(d->K), static_cast<unsigned>(d->C), d->dtype))
-        return lin_status(few_rows(rows_of(x, p.x), rows_of(weight, weight_pitch), out, static_cast<unsigned>(d->C), d->dtype, stream));
+    f.out.bias = bias;
+    if (f.few) return lin_status(few_rows(f.x.in, f.w.in, f.out, static_cast<unsigned>(d->C), d->dtype, stream));
     cudaError_t e = cudaSuccess;
     for (const Laid *l : {&f.w, &f.x})
         if (l->bytes && e == cudaSuccess) e = pack_rows(*l, nullptr, 0, nullptr, pack_chunks(l->rows, l->cols), ws, stream);
     if (e != cudaSuccess) return lin_status(e);
-    return lin_status(product(operand(f.x, ws, false), operand(f.w, ws, false), out, d->dtype, f.c,
+    return lin_status(product(operand(f.x, ws, false), operand(f.w, ws, false), f.out, d->dtype, f.c,
                               reinterpret_cast<float *>(ws + f.part), status, stream));
 }
 
 int map_linear_grad_workspace(const rz_linear *d, const rz_map *dy, const rz_map *x, const void *weight, size_t weight_pitch,
+                              const rz_map *pre, const rz_map *dx, const void *dweight, size_t dweight_pitch, int dweight_dtype,
                               size_t *bytes)
 {
     LinPlan p;
-    const int rc = bytes ? lin_check(d, &p) : RZ_ERR_ARG;
+    const int rc = bytes ? backward_check(d, &p, dy, x, weight, weight_pitch, pre, dx, dweight, dweight_pitch, dweight_dtype) : RZ_ERR_ARG;
     if (rc) return rc;
-    *bytes = 0;
-    if (p.x.empty()) return RZ_OK;
-    if (!maps::map_ok(x, p.x) || !maps::map_ok(dy, p.y) || !matrix_ok(weight, weight_pitch, d->K, d->C, p.x.es))
-        return RZ_ERR_ARG;
-    *bytes = plan_backward(d, p, dy, x, weight, weight_pitch).total;
+    *bytes = p.x.empty() ? 0 : plan_backward(d, p, dy, x, weight, weight_pitch, dx, dweight, dweight_pitch, dweight_dtype).total;
     return RZ_OK;
 }
 
@@ -706,11 +780,8 @@ int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x, const
                     void *workspace, size_t workspace_bytes, int *status, void *stream)
 {
     LinPlan p;
-    if (const int rc = lin_check(d, &p)) return rc;
-    const size_t dw_es = maps::dtype_size(dweight_dtype);
-    if (dweight && ((dweight_dtype != d->dtype && dweight_dtype != RZ_F32) ||
-                    !matrix_ok(dweight, dweight_pitch, d->K, d->C, dw_es)))
-        return RZ_ERR_ARG;
+    if (const int rc = backward_check(d, &p, dy, x, weight, weight_pitch, pre, dx, dweight, dweight_pitch, dweight_dtype)) return rc;
+    const size_t dw_es = dweight ? maps::dtype_size(dweight_dtype) : 0;
     if (reinterpret_cast<uintptr_t>(dbias) % 4 || reinterpret_cast<uintptr_t>(status) % 4) return RZ_ERR_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (p.x.empty()) {
@@ -719,9 +790,6 @@ int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x, const
         if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, 4 * static_cast<size_t>(d->K), st);
         return lin_status(e);
     }
-    if (!maps::map_ok(x, p.x) || !maps::map_ok(dy, p.y) || (dx && !maps::map_ok(dx, p.x))) return RZ_ERR_ARG;
-    if (d->act != RZ_ACT_NONE ? !maps::map_ok(pre, p.y) : pre && !maps::map_ok(pre, p.y)) return RZ_ERR_ARG;
-    if (!matrix_ok(weight, weight_pitch, d->K, d->C, p.x.es)) return RZ_ERR_ARG;
     // no output meets an input or another output
     Range in[4] = {range_of(*x, p.x), range_of(*dy, p.y), range_of(weight, weight_pitch, d->K, d->C, p.x.es), {}}, out[3];
     int nin = 3, nout = 0;
@@ -735,35 +803,28 @@ int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x, const
         for (int j = 0; j < i; j++)
             if (meet(out[i], out[j])) return RZ_ERR_ARG;
     }
-    const Backward b = plan_backward(d, p, dy, x, weight, weight_pitch);
+    const Backward b = plan_backward(d, p, dy, x, weight, weight_pitch, dx, dweight, dweight_pitch, dweight_dtype);
     if (!workspace_ok(workspace, workspace_bytes, b.total)) return RZ_ERR_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *sums = reinterpret_cast<float *>(ws + b.sums), *part = reinterpret_cast<float *>(ws + b.part);
     cudaError_t e = cudaSuccess;
-    if (dbias || (b.dz.bytes && (dx || dweight))) {
+    if (dbias || b.dz.bytes) {
         Rows slope;
         const bool sloped = d->act != RZ_ACT_NONE;
         if (sloped) slope = rows_of(pre, p.y);
-        Laid dz = b.dz;
-        if (!dx && !dweight) dz.bytes = 0;
-        e = pack_rows(dz, sloped ? &slope : nullptr, d->act, dbias ? sums : nullptr, b.chunks, ws, stream);
+        e = pack_rows(b.dz, sloped ? &slope : nullptr, d->act, dbias ? sums : nullptr, b.chunks, ws, stream);
         if (dbias && e == cudaSuccess)
             e = maps::launch(k_linear_sums, dim3((d->K + 31) / 32), 256, 0, stream, sums, b.chunks, static_cast<unsigned>(d->K), dbias);
     }
     if (dx && e == cudaSuccess) {
         if (b.w.bytes) e = pack_rows(b.w, nullptr, 0, nullptr, pack_chunks(b.w.rows, b.w.cols), ws, stream);
         if (e == cudaSuccess)
-            e = product(operand(b.dz, ws, false), operand(b.w, ws, true),
-                        finish_of(rows_of(dx, p.x), p.P, static_cast<unsigned>(d->C), d->dtype, nullptr, nullptr), d->dtype, b.cx, part,
-                        status, stream);
+            e = product(operand(b.dz, ws, false), operand(b.w, ws, true), b.dx, d->dtype, b.cx, part, status, stream);
     }
     if (dweight && e == cudaSuccess) {
         if (b.x.bytes) e = pack_rows(b.x, nullptr, 0, nullptr, pack_chunks(b.x.rows, b.x.cols), ws, stream);
         if (e == cudaSuccess)
-            e = product(operand(b.dz, ws, true), operand(b.x, ws, true),
-                        finish_of(rows_of(dweight, dweight_pitch), static_cast<unsigned>(d->K), static_cast<unsigned>(d->C),
-                                  dweight_dtype, nullptr, nullptr),
-                        dweight_dtype, b.cw, part, status, stream);
+            e = product(operand(b.dz, ws, true), operand(b.x, ws, true), b.dw, dweight_dtype, b.cw, part, status, stream);
     }
     return lin_status(e);
 }

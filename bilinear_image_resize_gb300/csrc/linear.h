@@ -117,27 +117,29 @@ __device__ __forceinline__ void finish(const Finish &f, unsigned m, unsigned n, 
     }
     *vec_at<T, VE>(f.out, m, n) = pack2<T, VE>(z);
 }
-// Element n of rows m .. m + U - 1 (as far as the matrix has them), where vectors do
-// not fit: the residual's elements are asked for before the first is used.
-template <class T, int ACT, int U>
-__device__ __forceinline__ void finish_column(const Finish &f, unsigned m, unsigned n, const float (&z)[U], float b)
+// UNIT elements, one or an aligned pair, where vectors do not fit.
+template <class T, int ACT, int UNIT>
+__device__ __forceinline__ void finish_unit(const Finish &f, unsigned m, unsigned n, float2 z)
 {
-    using E = Raw<T, 1>;
-    const auto at = [&](const Rows &r, unsigned row) { return reinterpret_cast<E *>(r.v.p + row_off(r, row)) + n; };
-    float r[U][1];
-    if (f.has_residual)
-#pragma unroll
-        for (int u = 0; u < U; u++)
-            if (m + u < f.M) unpack<T, 1>(*at(f.residual, m + u), r[u]);
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-        if (m + u >= f.M) break;
-        float v[1] = {z[u] + b};
-        if (f.has_pre) *at(f.pre, m + u) = pack<T, 1>(v);
-        v[0] = activated<T, ACT>(both(v[0])).x;
-        if (f.has_residual) v[0] += r[u][0];
-        *at(f.out, m + u) = pack<T, 1>(v);
+    using V = Raw<T, UNIT>;
+    const auto at = [&](const Rows &r) { return vec_at<T, UNIT>(r, m, n); };
+    const auto packed = [](float2 v) {
+        float e[UNIT];
+        e[0] = v.x;
+        if (UNIT == 2) e[UNIT - 1] = v.y;
+        return pack<T, UNIT>(e);
+    };
+    V r{};
+    if (f.has_residual) r = *at(f.residual);
+    if (f.bias) z = __fadd2_rn(z, make_float2(__ldg(f.bias + n), UNIT == 2 ? __ldg(f.bias + n + 1) : 0.0f));
+    if (f.has_pre) *at(f.pre) = packed(z);
+    z = activated<T, ACT>(z);
+    if (f.has_residual) {
+        float e[UNIT];
+        unpack<T, UNIT>(r, e);
+        z = __fadd2_rn(z, make_float2(e[0], UNIT == 2 ? e[UNIT - 1] : 0.0f));
     }
+    *at(f.out) = packed(z);
 }
 
 template <int VE>
@@ -160,8 +162,9 @@ struct Operand {
     int bf16;
 };
 
-// D = A B^T over the terms.  parts > 1: the terms are cut into so many runs, whose
-// float32 sums go to part[run][M][pitch_n] for k_linear_join.
+// D = A B^T over the terms.  part: the terms are cut into `splits` runs, whose float32
+// sums go to part[run][M][part_pitch] for k_linear_join; else (one run) the kernel
+// itself finishes them, where direct_out says that it can.
 struct Product {
     Operand a, b;
     Finish f;
@@ -173,6 +176,7 @@ struct Product {
     int pair;               // two CTAs work on a tile of 256 rows, else one on 128
     int *status;
 };
+bool direct_out(const Finish &f, int dtype);
 cudaError_t launch_product(const Product &p, void *stream);
 
 }  // namespace lin

@@ -35,18 +35,10 @@ using dev::smem_addr;
 constexpr int kTerms = 64;                      // terms of a stage: 128 bytes, the swizzle's width
 constexpr int kTileM = 128;
 constexpr int kBytesA = kTileM * kTerms * 2;
-// Warps that take tiles out: eight with TMA, sixteen where loads and stores have to
-// be waited for (5883 x 96 x 250 float32 with a residual: 17 us, with eight 31).
-__host__ __device__ constexpr int epi_warps(bool bulk) { return bulk ? 8 : 16; }
-// Loads of A, issuer, tensor memory, loads of B; the epilogue's begin at a multiple of four.
-__host__ __device__ constexpr int tc_threads(bool bulk) { return 128 + 32 * epi_warps(bulk); }
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;  // loads of A, issuer, tensor memory, loads of B; the epilogue's begin at a multiple of four
 constexpr int kBlockRow = 64;                   // bytes of a row of a block on its way out, 32 rows a block
 constexpr int kBlockBytes = 32 * kBlockRow;
-constexpr int kWarpBytes = 2 * kBlockBytes;     // an epilogue warp's two blocks
-constexpr int kOutBytes = epi_warps(true) * kWarpBytes;
-constexpr int kStagePitch = 48;                 // without TMA: bytes of a row on its way out, 32 and a gap, so that rows differ in their banks
-constexpr int kShare = 64;                      // most columns of a tile that are one of sixteen warps'
-static_assert(epi_warps(false) * (32 * kStagePitch + kShare * 4) <= kOutBytes, "");
 constexpr int kSmem = 227 * 1024;
 constexpr int kStatic = 512;    // the kernel's own variables
 constexpr int kRing = 8;
@@ -61,6 +53,7 @@ struct TcArgs {
     unsigned group;                     // rows of tiles that are walked together
     int a_turned, b_turned;
     int a_merged, b_merged;             // a turned operand's rows come in one box
+    int places;                         // an epilogue warp's blocks
     unsigned idesc;
     int *status;
 };
@@ -170,30 +163,9 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int *st
     return true;
 }
 
-// Bias of 16 columns from n, as far as the matrix has them.
-__device__ __forceinline__ void add_bias(const Finish &f, bool vectors, unsigned n, float2 (&z)[8])
-{
-    if (!f.bias) return;
-#pragma unroll
-    for (int q = 0; q < 4; q++) {
-        float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const unsigned c = n + 4 * q;
-        if (vectors && c + 4 <= f.N) {
-            b = __ldg(reinterpret_cast<const float4 *>(f.bias + c));
-        } else {
-            if (c < f.N) b.x = __ldg(f.bias + c);
-            if (c + 1 < f.N) b.y = __ldg(f.bias + c + 1);
-            if (c + 2 < f.N) b.z = __ldg(f.bias + c + 2);
-            if (c + 3 < f.N) b.w = __ldg(f.bias + c + 3);
-        }
-        z[2 * q] = __fadd2_rn(z[2 * q], make_float2(b.x, b.y));
-        z[2 * q + 1] = __fadd2_rn(z[2 * q + 1], make_float2(b.z, b.w));
-    }
-}
-
-// By TMA: a row a thread of 16 columns, the half `sub` of a block's row where they
-// are 16-bit, to and from a block in the 64-byte swizzle (16 bytes at `c` of row r are
-// at c ^ (r / 2) % 4, so that eight rows differ in their banks).
+// A row a thread of 16 columns, the half `sub` of a block's row where they are
+// 16-bit, to and from a block in the 64-byte swizzle (16 bytes at `c` of row r are at
+// c ^ (r / 2) % 4, so that eight rows differ in their banks).
 template <class T>
 __device__ __forceinline__ void block_write(uint8_t *block, int sub, const float2 (&z)[8])
 {
@@ -242,98 +214,6 @@ __device__ __forceinline__ void blocks_read()
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
 }
 
-// Without TMA: 32 rows of 32 bytes each through a warp's stage, which turns a row a
-// thread into consecutive bytes of a row for consecutive threads: lane / 2 + 16 k is
-// the row of a lane's k-th 16 bytes, lane % 2 their half of it.  PC = 32 / sizeof(T)
-// columns from n, as far as the matrix reaches; whole vectors or element by element.
-template <class T>
-__device__ __forceinline__ void emit(const Rows &to, const Finish &f, unsigned m, unsigned n, uint8_t *stage,
-                                     const float2 (&z)[16 / sizeof(T)])
-{
-    constexpr int PC = 32 / sizeof(T), VE = PC / 2;
-    using E = Raw<T, 1>;
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-        float2 part[VE / 2];
-#pragma unroll
-        for (int i = 0; i < VE / 2; i++) part[i] = z[h * VE / 2 + i];
-        reinterpret_cast<Raw<T, VE> *>(stage + lane * kStagePitch)[h] = pack2<T, VE>(part);
-    }
-    __syncwarp();
-    if (f.wide) {
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            const unsigned r = m + lane / 2 + 16 * k, c = n + lane % 2 * VE;
-            if (r < f.M && c < f.N)
-                *vec_at<T, VE>(to, r, c) =
-                    *reinterpret_cast<const Raw<T, VE> *>(stage + (lane / 2 + 16 * k) * kStagePitch + lane % 2 * 16);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < PC; k++) {
-            const int r = k * (32 / PC) + lane / PC, c = lane % PC;
-            if (m + r < f.M && n + c < f.N)
-                *reinterpret_cast<E *>(to.v.p + row_off(to, m + r) + static_cast<long long>(n + c) * sizeof(T)) =
-                    *reinterpret_cast<const E *>(stage + r * kStagePitch + c * sizeof(T));
-        }
-    }
-}
-// The residual of PC columns from n: as a lane reads them, and turned through the
-// stage into a row a thread and added to z.
-template <class T>
-struct Residual {
-    static constexpr int PC = 32 / sizeof(T), VE = PC / 2;
-    using E = Raw<T, 1>;
-    using V = Raw<T, VE>;
-    V vec[2];
-    E one[PC];
-
-    __device__ __forceinline__ void read(const Finish &f, unsigned m, unsigned n)
-    {
-        const int lane = threadIdx.x & 31;
-        const Rows &from = f.residual;
-        if (f.wide) {
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const unsigned r = m + lane / 2 + 16 * k, c = n + lane % 2 * VE;
-                vec[k] = V{};
-                if (r < f.M && c < f.N) vec[k] = *vec_at<T, VE>(from, r, c);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < PC; k++) {
-                const unsigned r = m + k * (32 / PC) + lane / PC, c = n + lane % PC;
-                one[k] = E{};
-                if (r < f.M && c < f.N)
-                    one[k] = *reinterpret_cast<const E *>(from.v.p + row_off(from, r) + static_cast<long long>(c) * sizeof(T));
-            }
-        }
-    }
-    __device__ __forceinline__ void add(const Finish &f, uint8_t *stage, float2 (&z)[PC / 2]) const
-    {
-        const int lane = threadIdx.x & 31;
-        __syncwarp();
-        if (f.wide) {
-#pragma unroll
-            for (int k = 0; k < 2; k++) *reinterpret_cast<V *>(stage + (lane / 2 + 16 * k) * kStagePitch + lane % 2 * 16) = vec[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < PC; k++)
-                *reinterpret_cast<E *>(stage + (k * (32 / PC) + lane / PC) * kStagePitch + lane % PC * sizeof(T)) = one[k];
-        }
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            float2 half[VE / 2];
-            unpack2<T, VE>(reinterpret_cast<const V *>(stage + lane * kStagePitch)[h], half);
-#pragma unroll
-            for (int q = 0; q < VE / 2; q++) z[h * VE / 2 + q] = __fadd2_rn(z[h * VE / 2 + q], half[q]);
-        }
-    }
-};
-
 // A tile's place and the chunks of its run.
 struct Tile {
     unsigned m, n, run;
@@ -364,18 +244,16 @@ __device__ __forceinline__ void planes_of(int planes, int j, int &a, int &b)
     b = 0x010210 >> (4 * j) & 0xf;
 }
 
-// BULK: results leave, and residuals come, by TMA (map_out; map_aux: the residual's or
-// pre's); else by loads and stores.
-template <class T, int ACT, int CG, bool BULK>
-__global__ void __launch_bounds__(tc_threads(BULK), 1)
+template <class T, int ACT, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
 k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-            const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_aux)
+            const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
+            const __grid_constant__ CUtensorMap map_residual)
 {
-    constexpr int kEpiWarps = epi_warps(BULK);
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[kRing], empty[kRing], done[2], taken[2];
     __shared__ uint32_t tmem_slot;
-    __shared__ uint64_t came[epi_warps(true)][2];     // a residual's block, each of a warp's two
+    __shared__ uint64_t came[kEpiWarps][2];     // a residual's block, each of a warp's two
     const uint32_t pad = (1024 - (smem_addr(raw) & 1023)) & 1023;
     const uint32_t ring = smem_addr(raw) + pad;
     const int rows_b = a.tile_n / CG;     // this CTA's share of B's rows
@@ -393,7 +271,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
         for (int i = 0; i < 2; i++) {
             dev::mbar_init(done + i, 1);
             dev::mbar_init(taken + i, kEpiWarps * CG);
-            for (int e = 0; e < epi_warps(true); e++) dev::mbar_init(&came[e][i], 1);
+            for (int e = 0; e < kEpiWarps; e++) dev::mbar_init(&came[e][i], 1);
         }
         dev::fence_mbar_init();
     }
@@ -501,164 +379,116 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             }
         }
     } else if (warp >= 4) {
-        // two (four) warps share 32 rows of the tile, half (a quarter) of its columns each
-        const int e = warp - 4, quarter = warp & 3, cols = a.tile_n / (kEpiWarps / 4);
-        uint8_t *out = raw + pad + a.stages * stage_bytes + e * (BULK ? kWarpBytes : 32 * kStagePitch);
-        const bool vectors = (reinterpret_cast<uintptr_t>(a.f.bias) & 15) == 0;
+        // Two warps share 32 rows of the tile, half of its columns each.  Results leave and residuals come by TMA in blocks of
+        // 64 bytes by 32 rows, in two places in turn: a residual's block comes into the place that its result leaves from,
+        // the next one's while this one is worked on.  (Loads and stores of a warp's own took the data path of shared
+        // memory for 58% of a call's time, and it is what the products are fed through: 325 against 303 us on 65536 x 1024 x
+        // 4096.)  With a residual, pre has a third place.
+        constexpr int BC = kBlockRow / sizeof(T), SUBS = BC / 16;
+        const int e = warp - 4, quarter = warp & 3, cols = a.tile_n / 2, blocks = cols / BC;
+        uint8_t *out = raw + pad + a.stages * stage_bytes + e * a.places * kBlockBytes;
+        int flip = 0;
+        uint32_t phases = 0;
         unsigned i = 0;
         bool ok = true;
-        const auto give_back = [&] {
-            // this warp's share of the tile is in registers
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            if (lane == 0) {
-                if constexpr (CG == 1)
-                    dev::mbar_arrive(taken + (i & 1));
-                else
-                    arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), 0));
+        for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
+            const Tile w = tile_at(a, t);
+            const unsigned m0 = (w.m * CG + rank) * kTileM + 32 * quarter, n0 = w.n * a.tile_n + (e >> 2) * cols;
+            const int live = m0 < a.f.M && n0 < a.f.N ? min(blocks, static_cast<int>((a.f.N - n0 + BC - 1) / BC)) : 0;
+            const auto fetch = [&](int b, int place) {
+                uint64_t *bar = &came[e][place];
+                dev::mbar_arrive_expect_tx(bar, kBlockBytes);
+                asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                             "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(out + place * kBlockBytes)),
+                             "l"(reinterpret_cast<uint64_t>(&map_residual)), "r"(static_cast<int>(n0) + b * BC),
+                             "r"(static_cast<int>(m0)), "r"(0), "r"(smem_addr(bar))
+                             : "memory");
+            };
+            // what does not wait for the tile: its first residual, and bias, four columns a lane
+            if (a.f.has_residual && live && lane == 0) {
+                blocks_read<1>();
+                fetch(0, flip);
             }
-        };
-        const auto floats = [](const uint32_t(&v)[16], float2(&z)[8]) {
+            float bias[4] = {};
+            if (a.f.bias)
 #pragma unroll
-            for (int q = 0; q < 8; q++) z[q] = make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
-        };
-        if constexpr (BULK) {
-            // Blocks of 64 bytes by 32 rows, in two places in turn: a residual's block comes into the place that its result
-            // leaves from, the next one's while this one is worked on.
-            constexpr int BC = kBlockRow / sizeof(T), SUBS = BC / 16;
-            const int blocks = cols / BC;
-            int flip = 0;
-            uint32_t phases = 0;
-            for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
-                const Tile w = tile_at(a, t);
-                const unsigned m0 = (w.m * CG + rank) * kTileM + 32 * quarter, n0 = w.n * a.tile_n + (e >> 2) * cols;
-                const int live = m0 < a.f.M && n0 < a.f.N ? min(blocks, static_cast<int>((a.f.N - n0 + BC - 1) / BC)) : 0;
-                const auto fetch = [&](int b, int place) {
-                    uint64_t *bar = &came[e][place];
-                    dev::mbar_arrive_expect_tx(bar, kBlockBytes);
-                    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(out + place * kBlockBytes)),
-                                 "l"(reinterpret_cast<uint64_t>(&map_aux)), "r"(static_cast<int>(n0) + b * BC),
-                                 "r"(static_cast<int>(m0)), "r"(0), "r"(smem_addr(bar))
-                                 : "memory");
-                };
-                if (a.f.has_residual && live && lane == 0) {
-                    blocks_read<1>();
-                    fetch(0, flip);
+                for (int q = 0; q < 4; q++)
+                    if (4 * lane + q < cols && n0 + 4 * lane + q < a.f.N) bias[q] = __ldg(a.f.bias + n0 + 4 * lane + q);
+            ok = wait_for(done + (i & 1), i >> 1 & 1, a.status);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + (e >> 2) * cols;
+            // a block's columns are asked for while the one before is worked on
+            uint32_t v[SUBS][16];
+#pragma unroll
+            for (int q = 0; q < SUBS; q++) tmem_load(acc + 16 * q, v[q]);
+            for (int b = 0; b < blocks; b++) {
+                float2 z[SUBS][8];
+#pragma unroll
+                for (int q = 0; q < SUBS; q++) {
+                    tmem_wait(v[q]);
+#pragma unroll
+                    for (int j = 0; j < 8; j++) z[q][j] = make_float2(__uint_as_float(v[q][2 * j]), __uint_as_float(v[q][2 * j + 1]));
                 }
-                ok = wait_for(done + (i & 1), i >> 1 & 1, a.status);
-                if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + (e >> 2) * cols;
-                // a block's columns are asked for while the one before is worked on
-                uint32_t v[SUBS][16];
+                if (b + 1 < blocks) {
 #pragma unroll
-                for (int q = 0; q < SUBS; q++) tmem_load(acc + 16 * q, v[q]);
-                for (int b = 0; b < blocks; b++) {
-                    float2 z[SUBS][8];
-#pragma unroll
-                    for (int q = 0; q < SUBS; q++) {
-                        tmem_wait(v[q]);
-                        floats(v[q], z[q]);
+                    for (int q = 0; q < SUBS; q++) tmem_load(acc + (b + 1) * BC + 16 * q, v[q]);
+                } else {
+                    // this warp's share of the tile is in registers
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    if (lane == 0) {
+                        if constexpr (CG == 1)
+                            dev::mbar_arrive(taken + (i & 1));
+                        else
+                            arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), 0));
                     }
-                    if (b == blocks - 1)
-                        give_back();
-                    else
-#pragma unroll
-                        for (int q = 0; q < SUBS; q++) tmem_load(acc + (b + 1) * BC + 16 * q, v[q]);
-                    if (b >= live) continue;
-                    const int n = static_cast<int>(n0) + b * BC;
-                    if (a.f.has_residual && b + 1 < live && lane == 0) {
-                        blocks_read<0>();
-                        fetch(b + 1, flip ^ 1);
-                    }
-#pragma unroll
-                    for (int q = 0; q < SUBS; q++) add_bias(a.f, vectors, n + 16 * q, z[q]);
-                    if (a.f.has_pre) {
-                        if (lane == 0) blocks_read<1>();
-                        __syncwarp();
-#pragma unroll
-                        for (int q = 0; q < SUBS; q++) block_write<T>(out + flip * kBlockBytes, q, z[q]);
-                        block_store(&map_aux, out + flip * kBlockBytes, n, static_cast<int>(m0), 0);
-                        flip ^= 1;
-                    }
+                }
+                if (b >= live) continue;
+                const int n = static_cast<int>(n0) + b * BC;
+                if (a.f.has_residual && b + 1 < live && lane == 0) {
+                    blocks_read<0>();
+                    fetch(b + 1, flip ^ 1);
+                }
+                if (a.f.bias)
 #pragma unroll
                     for (int q = 0; q < SUBS; q++)
 #pragma unroll
-                        for (int j = 0; j < 8; j++) z[q][j] = activated<T, ACT>(z[q][j]);
-                    uint8_t *block = out + flip * kBlockBytes;
-                    if (a.f.has_residual) {
-                        ok = __all_sync(0xffffffffu, wait_for(&came[e][flip], phases >> flip & 1, a.status));
-                        if (!ok) break;
-                        phases ^= 1u << flip;
-#pragma unroll
-                        for (int q = 0; q < SUBS; q++) block_add<T>(block, q, z[q]);
-                    } else {
-                        if (lane == 0) blocks_read<1>();
-                        __syncwarp();
-                    }
+                        for (int j = 0; j < 8; j++) {
+                            const int from = (b * BC + 16 * q) / 4 + j / 2;
+                            z[q][j] = __fadd2_rn(z[q][j], make_float2(__shfl_sync(0xffffffffu, bias[j % 2 * 2], from),
+                                                                      __shfl_sync(0xffffffffu, bias[j % 2 * 2 + 1], from)));
+                        }
+                if (a.f.has_pre) {
+                    uint8_t *block = out + (a.f.has_residual ? 2 : flip) * kBlockBytes;
+                    if (lane == 0) blocks_read<1>();
+                    __syncwarp();
 #pragma unroll
                     for (int q = 0; q < SUBS; q++) block_write<T>(block, q, z[q]);
-                    block_store(&map_out, block, n, static_cast<int>(m0), static_cast<int>(w.run));
-                    flip ^= 1;
+                    block_store(&map_pre, block, n, static_cast<int>(m0), 0);
+                    if (!a.f.has_residual) flip ^= 1;
                 }
-            }
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        } else {
-            constexpr int PC = 32 / sizeof(T);
-            float *bias = reinterpret_cast<float *>(raw + pad + a.stages * stage_bytes + kEpiWarps * 32 * kStagePitch) + e * kShare;
-            for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
-                const Tile w = tile_at(a, t);
-                const unsigned m0 = (w.m * CG + rank) * kTileM + 32 * quarter, n0 = w.n * a.tile_n + (e >> 2) * cols;
-                // the columns' bias before the tile is done; residuals a step ahead
-                __syncwarp();
-                for (int c = lane; c < cols; c += 32) bias[c] = a.f.bias && n0 + c < a.f.N ? __ldg(a.f.bias + n0 + c) : 0.0f;
-                __syncwarp();
-                Residual<T> even, odd;      // two that take turns: a copy would wait for what is on its way
+#pragma unroll
+                for (int q = 0; q < SUBS; q++)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) z[q][j] = activated<T, ACT>(z[q][j]);
+                uint8_t *block = out + flip * kBlockBytes;
                 if (a.f.has_residual) {
-                    even.read(a.f, m0, n0);
-                    // the rest on its way to L2, a row a lane
-                    if (m0 + lane < a.f.M && n0 < a.f.N) {
-                        const uint8_t *at = a.f.residual.v.p + row_off(a.f.residual, m0 + lane);
-                        const unsigned to = min(n0 + cols, a.f.N) * sizeof(T);
-                        for (unsigned o = n0 * sizeof(T); o < to; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + o));
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + to - 1));
-                    }
-                }
-                ok = wait_for(done + (i & 1), i >> 1 & 1, a.status);
-                if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + (e >> 2) * cols;
-                float2 z[8];
-                const auto part = [&](int c, const Residual<T> &now, Residual<T> &next) {
-                    if (c % 16 == 0) {
-                        uint32_t v[16];
-                        tmem_load(acc + c, v);
-                        tmem_wait(v);
-                        floats(v, z);
-                        if (c + 16 >= cols) give_back();
-                    }
-                    const unsigned n = n0 + c;
-                    if (n >= a.f.N || m0 >= a.f.M) return;
-                    if (a.f.has_residual && c + PC < cols) next.read(a.f, m0, n + PC);
-                    float2 y[PC / 2];
+                    ok = __all_sync(0xffffffffu, wait_for(&came[e][flip], phases >> flip & 1, a.status));
+                    if (!ok) break;
+                    phases ^= 1u << flip;
 #pragma unroll
-                    for (int q = 0; q < PC / 2; q += 2) {
-                        const float4 b = *reinterpret_cast<const float4 *>(bias + c + 2 * q);
-                        y[q] = __fadd2_rn(PC == 8 && c % 16 ? z[(q + 4) % 8] : z[q], make_float2(b.x, b.y));
-                        y[q + 1] = __fadd2_rn(PC == 8 && c % 16 ? z[(q + 5) % 8] : z[q + 1], make_float2(b.z, b.w));
-                    }
-                    if (a.f.has_pre) emit<T>(a.f.pre, a.f, m0, n, out, y);
-#pragma unroll
-                    for (int q = 0; q < PC / 2; q++) y[q] = activated<T, ACT>(y[q]);
-                    if (a.f.has_residual) now.add(a.f, out, y);
-                    emit<T>(a.f.out, a.f, m0, n, out, y);
-                };
-                for (int c = 0; c < cols; c += 2 * PC) {
-                    part(c, even, odd);
-                    if (c + PC < cols) part(c + PC, odd, even);
+                    for (int q = 0; q < SUBS; q++) block_add<T>(block, q, z[q]);
+                } else {
+                    if (lane == 0) blocks_read<1>();
+                    __syncwarp();
                 }
+#pragma unroll
+                for (int q = 0; q < SUBS; q++) block_write<T>(block, q, z[q]);
+                block_store(&map_out, block, n, static_cast<int>(m0), static_cast<int>(w.run));
+                flip ^= 1;
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
@@ -716,7 +546,7 @@ bool encode(const Operand &o, unsigned share, CUtensorMap *map, int *merged)
 bool encode_out(const Rows &r, unsigned M, unsigned N, int dtype, int runs, size_t run_bytes, CUtensorMap *map)
 {
     std::memset(map, 0, sizeof(*map));
-    const size_t es = dtype_size(dtype), pitch = M == 1 && runs == 1 ? N * es : static_cast<size_t>(r.v.pitch);
+    const size_t es = dtype_size(dtype), pitch = r.v.pitch % 16 ? N * es : static_cast<size_t>(r.v.pitch);    // of one row it is any
     const cuuint64_t dims[3] = {N, M, static_cast<cuuint64_t>(runs)};
     const cuuint64_t strides[2] = {pitch, runs > 1 ? run_bytes : pitch};
     const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(kBlockRow / es), 32, 1}, steps[3] = {1, 1, 1};
@@ -728,18 +558,19 @@ bool encode_out(const Rows &r, unsigned M, unsigned N, int dtype, int runs, size
 }
 
 struct Maps {
-    CUtensorMap a, b, out, aux;
+    CUtensorMap a, b, out, pre, residual;
 };
 
-template <class T, int ACT, int CG, bool BULK>
+template <class T, int ACT, int CG>
 cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
 {
-    const auto fn = k_linear_tc<T, ACT, CG, BULK>;
+    const auto fn = k_linear_tc<T, ACT, CG>;
     if (const cudaError_t e = shared_opt_in(reinterpret_cast<const void *>(fn), kSmem - kStatic)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CG * std::min<unsigned>(a.tiles, kSms / CG));
-    cfg.blockDim = dim3(tc_threads(BULK));
-    cfg.dynamicSmemBytes = 1024 + a.stages * static_cast<size_t>(kBytesA + a.tile_n / CG * kTerms * 2) + kOutBytes;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = 1024 + a.stages * static_cast<size_t>(kBytesA + a.tile_n / CG * kTerms * 2) +
+                           static_cast<size_t>(kEpiWarps) * a.places * kBlockBytes;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -749,23 +580,31 @@ cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 1 ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, fn, a, m.a, m.b, m.out, m.aux);
+    return cudaLaunchKernelEx(&cfg, fn, a, m.a, m.b, m.out, m.pre, m.residual);
 }
 
-template <class T, int CG, bool BULK>
+template <class T, int CG>
 cudaError_t tc_launch_act(const TcArgs &a, const Maps &m, void *stream)
 {
-    if (a.f.act == RZ_ACT_SILU) return tc_launch<T, RZ_ACT_SILU, CG, BULK>(a, m, stream);
-    return a.f.act == RZ_ACT_GELU ? tc_launch<T, RZ_ACT_GELU, CG, BULK>(a, m, stream) : tc_launch<T, RZ_ACT_NONE, CG, BULK>(a, m, stream);
+    if (a.f.act == RZ_ACT_SILU) return tc_launch<T, RZ_ACT_SILU, CG>(a, m, stream);
+    return a.f.act == RZ_ACT_GELU ? tc_launch<T, RZ_ACT_GELU, CG>(a, m, stream) : tc_launch<T, RZ_ACT_NONE, CG>(a, m, stream);
 }
 template <class T>
-cudaError_t tc_launch_of(const TcArgs &a, const Maps &m, int pair, bool bulk, void *stream)
+cudaError_t tc_launch_of(const TcArgs &a, const Maps &m, int pair, void *stream)
 {
-    if (bulk) return pair ? tc_launch_act<T, 2, true>(a, m, stream) : tc_launch_act<T, 1, true>(a, m, stream);
-    return pair ? tc_launch_act<T, 2, false>(a, m, stream) : tc_launch_act<T, 1, false>(a, m, stream);
+    return pair ? tc_launch_act<T, 2>(a, m, stream) : tc_launch_act<T, 1>(a, m, stream);
 }
 
 }  // namespace
+
+bool lin::direct_out(const Finish &f, int dtype)
+{
+    const auto fits = [&](const Rows &r) {
+        return !r.HW && reinterpret_cast<uintptr_t>(r.v.p) % 16 == 0 && (f.M == 1 || r.v.pitch % 16 == 0);
+    };
+    // TMA clips a row to whole 16 bytes
+    return f.N * dtype_size(dtype) % 16 == 0 && fits(f.out) && (!f.has_pre || fits(f.pre)) && (!f.has_residual || fits(f.residual));
+}
 
 cudaError_t lin::launch_product(const Product &p, void *stream)
 {
@@ -776,27 +615,20 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     if (!encode(p.a, kTileM, &m.a, &a.a_merged) || !encode(p.b, p.tile_n / cg, &m.b, &a.b_merged)) return cudaErrorInvalidValue;
     a.f = p.f;
     int dtype = p.out_dtype;
-    bool bulk = true;
-    if (p.splits > 1) {
-        // runs of a sum leave as they are, float32; k_linear_join finishes them
+    if (p.part) {
+        // runs of a sum, and what TMA cannot write, leave as they are, float32; k_linear_join finishes them
         dtype = RZ_F32;
         a.f = Finish{};
         a.f.M = p.f.M;
         a.f.N = p.f.N;
         a.f.out.v = {reinterpret_cast<uint8_t *>(p.part), static_cast<long long>(p.part_pitch) * 4, 0};
-        if (!encode_out(a.f.out, a.f.M, a.f.N, dtype, p.splits, static_cast<size_t>(p.part_pitch) * 4 * a.f.M, &m.out))
-            return cudaErrorInvalidValue;
-        m.aux = m.out;
-    } else {
-        // pre and a residual at once would need a third place for their blocks; and TMA clips a row to whole 16 bytes
-        const auto fits = [&](const Rows &r) {
-            return !r.HW && reinterpret_cast<uintptr_t>(r.v.p) % 16 == 0 && (a.f.M == 1 || r.v.pitch % 16 == 0);
-        };
-        const Rows &aux = a.f.has_residual ? a.f.residual : a.f.has_pre ? a.f.pre : a.f.out;
-        bulk = a.f.N * dtype_size(dtype) % 16 == 0 && fits(a.f.out) && fits(aux) && !(a.f.has_residual && a.f.has_pre);
-        if (bulk) bulk = encode_out(a.f.out, a.f.M, a.f.N, dtype, 1, 0, &m.out) && encode_out(aux, a.f.M, a.f.N, dtype, 1, 0, &m.aux);
-        if (!bulk) m.out = m.aux = m.a;     // not read
     }
+    if (!encode_out(a.f.out, a.f.M, a.f.N, dtype, p.splits, static_cast<size_t>(p.part_pitch) * 4 * a.f.M, &m.out))
+        return cudaErrorInvalidValue;
+    m.pre = m.residual = m.out;     // where there is none
+    if (a.f.has_pre && !encode_out(a.f.pre, a.f.M, a.f.N, dtype, 1, 0, &m.pre)) return cudaErrorInvalidValue;
+    if (a.f.has_residual && !encode_out(a.f.residual, a.f.M, a.f.N, dtype, 1, 0, &m.residual)) return cudaErrorInvalidValue;
+    a.places = a.f.has_pre && a.f.has_residual ? 3 : 2;
     a.tile_n = p.tile_n;
     a.tiles_m = (p.f.M + cg * kTileM - 1) / (cg * kTileM);
     a.tiles_n = (p.f.N + p.tile_n - 1) / p.tile_n;
@@ -811,15 +643,15 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     const unsigned long long tiles = static_cast<unsigned long long>(a.tiles_m) * a.tiles_n * p.splits;
     if (tiles > 0x7fffffffull) return cudaErrorInvalidConfiguration;
     a.tiles = static_cast<unsigned>(tiles);
-    a.stages = std::min(kRing, (kSmem - kStatic - 1024 - kOutBytes) / (kBytesA + p.tile_n / cg * kTerms * 2));
+    a.stages = std::min(kRing, (kSmem - kStatic - 1024 - kEpiWarps * a.places * kBlockBytes) / (kBytesA + p.tile_n / cg * kTerms * 2));
     a.a_turned = p.a.turned;
     a.b_turned = p.b.turned;
     const unsigned type = p.a.bf16 ? 1u : 0u;
     a.idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<unsigned>(p.a.turned) << 15) |
               (static_cast<unsigned>(p.b.turned) << 16) | (static_cast<unsigned>(p.tile_n >> 3) << 17) | (static_cast<unsigned>(cg * kTileM >> 4) << 24);
     a.status = p.status;
-    if (dtype == RZ_F32) return tc_launch_of<float>(a, m, p.pair, bulk, stream);
-    return dtype == RZ_BF16 ? tc_launch_of<__nv_bfloat16>(a, m, p.pair, bulk, stream) : tc_launch_of<__half>(a, m, p.pair, bulk, stream);
+    if (dtype == RZ_F32) return tc_launch_of<float>(a, m, p.pair, stream);
+    return dtype == RZ_BF16 ? tc_launch_of<__nv_bfloat16>(a, m, p.pair, stream) : tc_launch_of<__half>(a, m, p.pair, stream);
 }
 
 }  // namespace rz

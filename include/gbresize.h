@@ -570,11 +570,13 @@ RZ_API int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_ma
  * RZ_ERR_UNSUPPORTED).
  *
  * workspace: device memory of at least the bytes that map_linear_workspace
- * gives for maps like these (of x and weight their alignment, pitch and stride
- * matter; the data is not touched), 16-byte aligned, of any content, the call's
- * own until the stream has passed it; up to eight pixels need none.  status: a device int or NULL; a kernel
- * whose bounded waits (1 s) run out writes RZ_ERR_TIMEOUT there and leaves the
- * result unfinished.  Asynchronous on `stream`; no allocation.  An empty map is
+ * gives for these maps and weight (their alignment, pitch and stride matter; the
+ * data is not touched), 16-byte aligned, of any content, the call's own until the
+ * stream has passed it; up to eight pixels need none.  Maps and weights whose rows
+ * begin and end at multiples of 16 bytes, evenly apart, are read and written where
+ * they lie; others pass through the workspace.  status: a device int or NULL; a
+ * kernel whose bounded waits (1 s) run out writes RZ_ERR_TIMEOUT there and leaves
+ * the result unfinished.  Asynchronous on `stream`; no allocation.  An empty map is
  * RZ_OK.
  */
 typedef struct {
@@ -583,7 +585,7 @@ typedef struct {
     int act;
 } rz_linear;
 RZ_API int map_linear_workspace(const rz_linear *d, const rz_map *x, const void *weight, size_t weight_pitch,
-                                size_t *bytes);
+                                const rz_map *residual, const rz_map *pre, const rz_map *y, size_t *bytes);
 RZ_API int map_linear(const rz_linear *d, const rz_map *x, const void *weight, size_t weight_pitch, const float *bias,
                       const rz_map *residual, const rz_map *pre, const rz_map *y, void *workspace,
                       size_t workspace_bytes, int *status, void *stream);
@@ -599,7 +601,8 @@ RZ_API int map_linear(const rz_linear *d, const rz_map *x, const void *weight, s
  * Sums run in a fixed order.  Workspace, status and the rest as map_linear.
  */
 RZ_API int map_linear_grad_workspace(const rz_linear *d, const rz_map *dy, const rz_map *x, const void *weight,
-                                     size_t weight_pitch, size_t *bytes);
+                                     size_t weight_pitch, const rz_map *pre, const rz_map *dx, const void *dweight,
+                                     size_t dweight_pitch, int dweight_dtype, size_t *bytes);
 RZ_API int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x, const void *weight,
                            size_t weight_pitch, const rz_map *pre, const rz_map *dx, void *dweight,
                            size_t dweight_pitch, int dweight_dtype, float *dbias, void *workspace,

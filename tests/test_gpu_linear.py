@@ -190,7 +190,7 @@ def test_other_stream_and_given_workspace(rz, shape, K, dtype):
     x = torch.zeros(shape, dtype=getattr(torch, tok.TORCH[dtype]), device="cuda")
     y = torch.zeros((*shape[:3], K), dtype=x.dtype, device="cuda")
     w = torch.zeros((K, shape[3]), dtype=x.dtype, device="cuda")
-    n = max(rz.map_linear_workspace(x, y, w, act=1), rz.map_linear_grad_workspace(y, x, w, act=1))
+    n = max(rz.map_linear_workspace(x, y, w, act=1), rz.map_linear_grad_workspace(y, x, w, x, w, pre=y, act=1))
     work = torch.full((n + 64,), 0xA5, dtype=torch.uint8, device="cuda")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -208,8 +208,8 @@ def test_captured_and_replayed(rz, shape, K, dtype):
     x, dy, pre = (torch.zeros(s, dtype=t, device="cuda") for s in (shape, (*shape[:3], K), (*shape[:3], K)))
     w, y, dx = torch.zeros((K, C), dtype=t, device="cuda"), torch.zeros_like(dy), torch.zeros_like(x)
     dw, db = torch.zeros_like(w), torch.zeros(K, device="cuda")
-    fw = torch.empty(max(16, rz.map_linear_workspace(x, y, w, act=2)), dtype=torch.uint8, device="cuda")
-    gw = torch.empty(max(16, rz.map_linear_grad_workspace(dy, x, w, act=2)), dtype=torch.uint8, device="cuda")
+    fw = torch.empty(max(16, rz.map_linear_workspace(x, y, w, pre=pre, act=2)), dtype=torch.uint8, device="cuda")
+    gw = torch.empty(max(16, rz.map_linear_grad_workspace(dy, x, w, dx, dw, pre, act=2)), dtype=torch.uint8, device="cuda")
 
     def step():
         rz.map_linear(x, y, w, pre=pre, act=2, workspace=fw)
