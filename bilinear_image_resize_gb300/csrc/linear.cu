@@ -439,10 +439,15 @@ struct Cut {
     unsigned pitch;
     size_t bytes;
 };
-// through: a single run goes through the workspace as well.
-Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, bool through)
+// through: a single run goes through the workspace as well.  A run is as long as its
+// accumulator's cut sums allow, n 1e-9 for n terms: float32 inputs 768 (8e-7, about
+// what float32 arithmetic leaves), 16-bit ones 2048 for a float32 result, else 16384.
+Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool through)
 {
-    const long long chunks = static_cast<long long>((terms + 63) / 64) * (dtype == RZ_F32 ? 6 : 1);
+    const long long chunks = (terms + 63) / 64;
+    const int products = dtype == RZ_F32 ? 6 : 1;
+    const long long longest = dtype == RZ_F32 ? 12 : out_dtype == RZ_F32 ? 32 : 256;
+    const int fewest = static_cast<int>((chunks + longest - 1) / longest);
     Cut best{};
     double least = 0.0;
     const unsigned pitch = static_cast<unsigned>(up(N, 8));
@@ -452,12 +457,12 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, bool through)
             const double stage = tile == 256 ? (pair ? 690 : 780) : tile == 128 ? (pair ? 590 : 580) : 560;
             const long long rows = pair ? 256 : 128, slots = pair ? kLinSms / 2 : kLinSms;
             const long long tiles = (M + rows - 1) / rows * ((N + tile - 1) / tile);
-            for (int want = 1; want <= 64 && want <= chunks; want++) {
+            for (int want = fewest; want < fewest + 64 && want <= chunks; want++) {
                 const long long run = (chunks + want - 1) / want;
                 const int splits = static_cast<int>((chunks + run - 1) / run);
-                if (splits != want) continue;
+                if (splits != want && want != fewest) continue;
                 const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
-                double t = waves * (run * stage + 2500) + 4.0 * tile;
+                double t = waves * (run * products * stage + 2500) + 4.0 * tile;
                 const bool joined = splits > 1 || through;
                 if (joined) t += 6500 + 170.0 * splits + 4.0 * M * pitch * (splits + 1) / 2500.0;
                 if (!best.tile_n || t < least) {
@@ -639,7 +644,7 @@ Forward plan_forward(const rz_linear *d, const LinPlan &p, const rz_map *x, cons
     f.x = lay(rows_of(x, p.x), p.P, C, d->dtype, false);
     f.w = lay(rows_of(weight, weight_pitch), K, C, d->dtype, false);
     if (f.few) return f;
-    f.c = cut(p.P, K, C, d->dtype, !direct_out(f.out, d->dtype));
+    f.c = cut(p.P, K, C, d->dtype, d->dtype, !direct_out(f.out, d->dtype));
     f.w.at = up(f.x.bytes, 256);
     f.part = f.w.at + up(f.w.bytes, 256);
     f.total = f.part + f.c.bytes;
@@ -667,11 +672,11 @@ Backward plan_backward(const rz_linear *d, const LinPlan &p, const rz_map *dy, c
     if (!dx) b.w.bytes = 0;
     if (dx) {
         b.dx = finish_of(rows_of(dx, p.x), p.P, C, d->dtype, nullptr, nullptr);
-        b.cx = cut(p.P, C, K, d->dtype, !direct_out(b.dx, d->dtype));
+        b.cx = cut(p.P, C, K, d->dtype, d->dtype, !direct_out(b.dx, d->dtype));
     }
     if (dweight) {
         b.dw = finish_of(rows_of(dweight, dweight_pitch), K, C, dweight_dtype, nullptr, nullptr);
-        b.cw = cut(K, C, p.P, d->dtype, !direct_out(b.dw, dweight_dtype));
+        b.cw = cut(K, C, p.P, d->dtype, dweight_dtype, !direct_out(b.dw, dweight_dtype));
     }
     b.chunks = pack_chunks(p.P, K);
     b.x.at = up(b.dz.bytes, 256);

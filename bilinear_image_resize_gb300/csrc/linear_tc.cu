@@ -14,6 +14,10 @@
 // the leading bits of what the ones before it leave; of the nine products of
 // planes the six with i + j <= 2 are summed, the smallest first, in the one
 // accumulator: the others are below 2^-23 of |a| |b|.
+//
+// The accumulator cuts what it adds (it does not round): a sum of n terms ends up
+// smaller by about n 1e-9 of its size.  So long sums are cut into runs, which
+// k_linear_join adds up in rounded arithmetic.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -48,7 +52,7 @@ struct TcArgs {
     Finish f;
     unsigned tiles_m, tiles_n, tiles;   // tiles: of all runs
     int tile_n, stages;
-    int chunks, all_chunks, run;        // 64-term chunks of a plane product, of all of them, and of a run
+    int chunks, run;                    // 64-term chunks, and of a run
     int planes;
     unsigned group;                     // rows of tiles that are walked together
     int a_turned, b_turned;
@@ -214,10 +218,10 @@ __device__ __forceinline__ void blocks_read()
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
 }
 
-// A tile's place and the chunks of its run.
+// A tile's place and the chunks of its run, each once for every product of planes.
 struct Tile {
     unsigned m, n, run;
-    int first, last;
+    int first, last, stages;
 };
 __device__ __forceinline__ Tile tile_at(const TcArgs &a, unsigned t)
 {
@@ -228,7 +232,8 @@ __device__ __forceinline__ Tile tile_at(const TcArgs &a, unsigned t)
     r.m = g * a.group + y % rows;
     r.n = y / rows;
     r.first = static_cast<int>(r.run) * a.run;
-    r.last = min(a.all_chunks, r.first + a.run);
+    r.last = min(a.chunks, r.first + a.run);
+    r.stages = (r.last - r.first) * (a.planes == 1 ? 1 : 6);
     return r;
 }
 
@@ -239,7 +244,7 @@ __device__ __forceinline__ void planes_of(int planes, int j, int &a, int &b)
         a = b = 0;
         return;
     }
-    // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
+    // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0); past the last, none
     a = 0x001012 >> (4 * j) & 0xf;
     b = 0x010210 >> (4 * j) & 0xf;
 }
@@ -312,9 +317,9 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step) {
                 const Tile w = tile_at(a, t);
                 const int row = of_b ? static_cast<int>(w.n * a.tile_n + rank * rows_b) : static_cast<int>((w.m * CG + rank) * kTileM);
-                int j = w.first / a.chunks, k0 = (w.first - j * a.chunks) * kTerms, pa, pb;
+                int j = 0, k0 = w.first * kTerms, pa, pb;
                 planes_of(a.planes, j, pa, pb);
-                for (int c = w.first; c < w.last; c++) {
+                for (int c = 0; c < w.stages; c++) {
                     ok = wait_for(empty + s, phase ^ 1, a.status);
                     if (!ok) break;
                     if (!of_b && rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
@@ -332,8 +337,8 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                         phase ^= 1;
                     }
                     k0 += kTerms;
-                    if (k0 >= a.chunks * kTerms) {
-                        k0 = 0;
+                    if (k0 >= w.last * kTerms) {
+                        k0 = w.first * kTerms;
                         planes_of(a.planes, ++j, pa, pb);
                     }
                 }
@@ -360,7 +365,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                 ok = wait_for(taken + (i & 1), (i >> 1 & 1) ^ 1, a.status);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (int c = w.first; c < w.last; c++) {
+                for (int c = 0; c < w.stages; c++) {
                     ok = wait_for(full + s, phase, a.status);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -368,7 +373,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                     const uint64_t da = desc_a + at, db = desc_b + at;
 #pragma unroll
                     for (uint32_t k = 0; k < kTerms / 16; k++)
-                        mma<CG>(acc, da + k * step_a, db + k * step_b, a.idesc, c > w.first || k > 0);
+                        mma<CG>(acc, da + k * step_a, db + k * step_b, a.idesc, c > 0 || k > 0);
                     commit<CG>(empty + s);
                     if (++s == a.stages) {
                         s = 0;
@@ -638,8 +643,7 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     // single rows 650).
     a.group = 2.0 * p.f.N * p.b.terms * p.b.planes > 48e6 ? 8 : 1;
     a.chunks = static_cast<int>((p.a.terms + kTerms - 1) / kTerms);
-    a.all_chunks = a.chunks * (a.planes == 1 ? 1 : 6);
-    a.run = (a.all_chunks + p.splits - 1) / p.splits;
+    a.run = (a.chunks + p.splits - 1) / p.splits;
     const unsigned long long tiles = static_cast<unsigned long long>(a.tiles_m) * a.tiles_n * p.splits;
     if (tiles > 0x7fffffffull) return cudaErrorInvalidConfiguration;
     a.tiles = static_cast<unsigned>(tiles);
