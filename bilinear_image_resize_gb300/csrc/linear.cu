@@ -37,7 +37,13 @@ struct PackArgs {
     unsigned M, C;
     unsigned chunk;         // rows of a CTA
     int lanes;              // lanes side by side in a row, eight columns each
-    int has_slope, act;
+    int has_slope, act, wide;
+    unsigned blocks, across;    // CTAs, and of them along a row
+};
+// The matrices of a call in one launch, their CTAs one after another.
+struct PackJobs {
+    PackArgs job[3];
+    int count;
 };
 
 // Eight elements: as they come, or with those past the row's end 0.
@@ -67,18 +73,15 @@ __device__ __forceinline__ float leading(float v)
 }
 
 template <class T, bool WIDE>
-__global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_constant__ PackArgs a)
+__device__ __forceinline__ void pack_block(const PackArgs &a, unsigned bx, unsigned by, float (&sh)[kPackWarps][256])
 {
     constexpr int U = sizeof(T) == 2 ? 4 : 2;       // rows read before the first is used
-    __shared__ float sh[kPackWarps][256];
-    grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rows = 32 / a.lanes, sub = lane % a.lanes, down = lane / a.lanes;
-    const unsigned c = (blockIdx.x * a.lanes + sub) * 8;
+    const unsigned c = (bx * a.lanes + sub) * 8;
     const int left = static_cast<int>(a.C) - static_cast<int>(c);
-    const unsigned r0 = blockIdx.y * a.chunk, r1 = min(a.M, r0 + a.chunk), step = kPackWarps * rows;
+    const unsigned r0 = by * a.chunk, r1 = min(a.M, r0 + a.chunk), step = kPackWarps * rows;
     float s[8] = {};
-    grid_dependency_wait();
     if (left > 0) {
         for (unsigned r = r0 + warp * rows + down; r < r1; r += U * step) {
             Raw<T, 8> in[U], slope[U];
@@ -133,12 +136,32 @@ __global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_const
         if (down == 0) sh[warp][sub * 8 + i] = s[i];
     }
     __syncthreads();
-    const unsigned col = blockIdx.x * a.lanes * 8 + threadIdx.x;
+    const unsigned col = bx * a.lanes * 8 + threadIdx.x;
     if (static_cast<int>(threadIdx.x) >= a.lanes * 8 || col >= a.C) return;
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kPackWarps; w++) sum += sh[w][threadIdx.x];
-    a.sums[static_cast<long long>(blockIdx.y) * a.C + col] = sum;
+    a.sums[static_cast<long long>(by) * a.C + col] = sum;
+}
+
+// WIDE: of every job.  ONE: a single one, whose arguments need no index (32768 x 1024
+// with a slope: 34.5 us, 40 where they do).
+template <class T, bool WIDE, bool ONE>
+__global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_constant__ PackJobs jobs)
+{
+    __shared__ float sh[kPackWarps][256];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    unsigned b = blockIdx.x;
+    int j = 0;
+    if (!ONE)
+        while (j + 1 < jobs.count && b >= jobs.job[j].blocks) b -= jobs.job[j++].blocks;
+    const PackArgs &a = jobs.job[ONE ? 0 : j];
+    const unsigned by = b / a.across, bx = b - by * a.across;
+    if (WIDE || a.wide)
+        pack_block<T, true>(a, bx, by, sh);
+    else
+        pack_block<T, false>(a, bx, by, sh);
 }
 
 // dbias: the chunks' sums, 32 columns a block, each of its warps a chunk in
@@ -475,9 +498,10 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool t
     return best;
 }
 
-cudaError_t pack_rows(const Laid &l, const Rows *slope, int act, float *sums, unsigned chunks, uint8_t *workspace, void *stream)
+// One more matrix to lay out.
+void add_job(PackJobs &jobs, const Laid &l, const Rows *slope, int act, float *sums, unsigned chunks, uint8_t *workspace)
 {
-    PackArgs a{};
+    PackArgs &a = jobs.job[jobs.count++];
     a.in = l.in;
     if (slope) a.slope = *slope;
     a.has_slope = slope != nullptr;
@@ -496,12 +520,26 @@ cudaError_t pack_rows(const Laid &l, const Rows *slope, int act, float *sums, un
         return reinterpret_cast<uintptr_t>(r.v.p) % 16 == 0 && r.v.pitch % 16 == 0 && r.v.bstride % 16 == 0 &&
                (!r.HW || r.bytes % 16 == 0);
     };
-    const bool vectors = l.cols % 8 == 0 && wide(l.in) && (!slope || wide(*slope));
-    const dim3 grid((vecs + a.lanes - 1) / a.lanes, (l.rows + a.chunk - 1) / a.chunk);
-    const auto fn = l.dtype == RZ_F32    ? (vectors ? k_linear_pack<float, true> : k_linear_pack<float, false>)
-                    : l.dtype == RZ_BF16 ? (vectors ? k_linear_pack<__nv_bfloat16, true> : k_linear_pack<__nv_bfloat16, false>)
-                                         : (vectors ? k_linear_pack<__half, true> : k_linear_pack<__half, false>);
-    return launch(fn, grid, kPackThreads, 0, stream, a);
+    a.wide = l.cols % 8 == 0 && wide(l.in) && (!slope || wide(*slope));
+    a.across = (vecs + a.lanes - 1) / a.lanes;
+    a.blocks = a.across * ((l.rows + a.chunk - 1) / a.chunk);
+}
+cudaError_t pack_launch(const PackJobs &jobs, int dtype, void *stream)
+{
+    if (!jobs.count) return cudaSuccess;
+    unsigned blocks = 0;
+    bool wide = true;
+    for (int i = 0; i < jobs.count; i++) {
+        blocks += jobs.job[i].blocks;
+        wide = wide && jobs.job[i].wide;
+    }
+    const auto of = [&](auto t) {
+        using T = decltype(t);
+        if (!wide) return k_linear_pack<T, false, false>;
+        return jobs.count == 1 ? k_linear_pack<T, true, true> : k_linear_pack<T, true, false>;
+    };
+    const auto fn = dtype == RZ_F32 ? of(float{}) : dtype == RZ_BF16 ? of(__nv_bfloat16{}) : of(__half{});
+    return launch(fn, dim3(blocks), kPackThreads, 0, stream, jobs);
 }
 // Chunks of rows of a pass over a matrix: about four CTAs an SM, at least 16 rows each.
 unsigned pack_chunks(unsigned rows, unsigned cols)
@@ -761,10 +799,10 @@ int map_linear(const rz_linear *d, const rz_map *x, const void *weight, size_t w
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     f.out.bias = bias;
     if (f.few) return lin_status(few_rows(f.x.in, f.w.in, f.out, static_cast<unsigned>(d->C), d->dtype, stream));
-    cudaError_t e = cudaSuccess;
-    for (const Laid *l : {&f.w, &f.x})
-        if (l->bytes && e == cudaSuccess) e = pack_rows(*l, nullptr, 0, nullptr, pack_chunks(l->rows, l->cols), ws, stream);
-    if (e != cudaSuccess) return lin_status(e);
+    PackJobs jobs{};
+    for (const Laid *l : {&f.x, &f.w})
+        if (l->bytes) add_job(jobs, *l, nullptr, 0, nullptr, pack_chunks(l->rows, l->cols), ws);
+    if (const cudaError_t e = pack_launch(jobs, d->dtype, stream)) return lin_status(e);
     return lin_status(product(operand(f.x, ws, false), operand(f.w, ws, false), f.out, d->dtype, f.c,
                               reinterpret_cast<float *>(ws + f.part), status, stream));
 }
@@ -812,25 +850,22 @@ int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x, const
     if (!workspace_ok(workspace, workspace_bytes, b.total)) return RZ_ERR_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *sums = reinterpret_cast<float *>(ws + b.sums), *part = reinterpret_cast<float *>(ws + b.part);
-    cudaError_t e = cudaSuccess;
+    PackJobs jobs{};
     if (dbias || b.dz.bytes) {
         Rows slope;
         const bool sloped = d->act != RZ_ACT_NONE;
         if (sloped) slope = rows_of(pre, p.y);
-        e = pack_rows(b.dz, sloped ? &slope : nullptr, d->act, dbias ? sums : nullptr, b.chunks, ws, stream);
-        if (dbias && e == cudaSuccess)
-            e = maps::launch(k_linear_sums, dim3((d->K + 31) / 32), 256, 0, stream, sums, b.chunks, static_cast<unsigned>(d->K), dbias);
+        add_job(jobs, b.dz, sloped ? &slope : nullptr, d->act, dbias ? sums : nullptr, b.chunks, ws);
     }
-    if (dx && e == cudaSuccess) {
-        if (b.w.bytes) e = pack_rows(b.w, nullptr, 0, nullptr, pack_chunks(b.w.rows, b.w.cols), ws, stream);
-        if (e == cudaSuccess)
-            e = product(operand(b.dz, ws, false), operand(b.w, ws, true), b.dx, d->dtype, b.cx, part, status, stream);
-    }
-    if (dweight && e == cudaSuccess) {
-        if (b.x.bytes) e = pack_rows(b.x, nullptr, 0, nullptr, pack_chunks(b.x.rows, b.x.cols), ws, stream);
-        if (e == cudaSuccess)
-            e = product(operand(b.dz, ws, true), operand(b.x, ws, true), b.dw, dweight_dtype, b.cw, part, status, stream);
-    }
+    for (const Laid *l : {&b.x, &b.w})
+        if (l->bytes) add_job(jobs, *l, nullptr, 0, nullptr, pack_chunks(l->rows, l->cols), ws);
+    cudaError_t e = pack_launch(jobs, d->dtype, stream);
+    if (dbias && e == cudaSuccess)
+        e = maps::launch(k_linear_sums, dim3((d->K + 31) / 32), 256, 0, stream, sums, b.chunks, static_cast<unsigned>(d->K), dbias);
+    if (dx && e == cudaSuccess)
+        e = product(operand(b.dz, ws, false), operand(b.w, ws, true), b.dx, d->dtype, b.cx, part, status, stream);
+    if (dweight && e == cudaSuccess)
+        e = product(operand(b.dz, ws, true), operand(b.x, ws, true), b.dw, dweight_dtype, b.cw, part, status, stream);
     return lin_status(e);
 }
 

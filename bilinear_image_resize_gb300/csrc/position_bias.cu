@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_whole(const __grid_constant
     grid_launch_dependents();
     const int head = blockIdx.x % a.g.heads, group = blockIdx.x / a.g.heads;
     const int lk = a.g.k[0] * a.g.k[1], lq = a.g.q[0] * a.g.q[1];
+    const int n0 = group * a.gn, n1 = min(a.g.N, n0 + a.gn);
     grid_dependency_wait();
     for (int i = threadIdx.x; i < lq * lk; i += kPbThreads) {
         const int q = i / lk, k = i - q * lk, qy = q / a.g.q[1], ky = k / a.g.k[1];
@@ -177,7 +178,6 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_whole(const __grid_constant
                                    (k - ky * a.g.k[1]) - (q - qy * a.g.q[1]) + a.g.q[1] - 1);
     }
     __syncthreads();
-    const int n0 = group * a.gn, n1 = min(a.g.N, n0 + a.gn);
     for (int n = n0 + (threadIdx.x >> 5); n < n1; n += kPbWarps) {
         const long long image = static_cast<long long>(n) * a.g.heads + head;
         stream_row<T, WIDE, SCORES>(a.out.p + image * a.out.bstride,
@@ -351,16 +351,35 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_fold(const __grid_constant_
     grid_dependency_wait();
     const float *from = a.dense + static_cast<long long>(head) * down * wide;
     float s = 0.0f;
-    const auto add = [&](int r, int c0, int step) {
-        for (int c = c0; c < wide; c += step)
-            if (__ldg(a.g.lut[1] + c) == b1) s += from[static_cast<long long>(r) * wide + c];
-    };
-    for (int r0 = 0; r0 < down; r0 += 32) {
-        const bool has = r0 + lane < down && __ldg(a.g.lut[0] + r0 + lane) == b0;
-        if (wide <= 8) {        // rows of a few offsets: one a lane
-            if (has) add(r0 + lane, 0, 1);
-        } else {
-            for (unsigned left = __ballot_sync(0xffffffffu, has); left; left &= left - 1) add(r0 + __ffs(left) - 1, lane, 32);
+    if (wide <= 8) {            // rows of a few offsets: one a lane
+        for (int r = lane; r < down; r += 32)
+            if (__ldg(a.g.lut[0] + r) == b0)
+                for (int c = 0; c < wide; c++)
+                    if (__ldg(a.g.lut[1] + c) == b1) s += from[static_cast<long long>(r) * wide + c];
+    } else {
+        // the bucket's rows, four of them asked for at once (past the last that one again, and not added)
+        for (int c0 = 0; c0 < wide; c0 += 32) {
+            const bool mine = c0 + lane < wide && __ldg(a.g.lut[1] + c0 + lane) == b1;
+            if (!__any_sync(0xffffffffu, mine)) continue;
+            const float *column = from + min(c0 + lane, wide - 1);
+            for (int r0 = 0; r0 < down; r0 += 32) {
+                unsigned left = __ballot_sync(0xffffffffu, r0 + lane < down && __ldg(a.g.lut[0] + r0 + lane) == b0);
+                while (left) {
+                    int r[4], n = 0;
+                    float v[4];
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        r[u] = left ? r0 + __ffs(left) - 1 : r[u ? u - 1 : 0];
+                        n += left != 0;
+                        left &= left - 1;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; u++) v[u] = column[static_cast<long long>(r[u]) * wide];
+#pragma unroll
+                    for (int u = 0; u < 4; u++)
+                        if (mine && u < n) s += v[u];
+                }
+            }
         }
     }
 #pragma unroll
