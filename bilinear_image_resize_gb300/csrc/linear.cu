@@ -453,19 +453,20 @@ Operand operand(const Laid &l, const uint8_t *workspace, bool turned)
 
 // Tile width, CTAs of a tile and runs of a product, by an estimate in clocks of
 // what was measured: a stage (what reaches an SM from L2, 64 bytes a clock, bounds
-// it on every tile: 256 columns of a pair 690, of one CTA 780, narrower ones 560 to
-// 590), a wave's beginning and end, and the join of runs, which pays for long sums
+// it on every tile: 256 columns of a pair 690, 720 where both operands are turned and
+// 640 where two pairs then share one, of one CTA 780, narrower ones 560 to 590), a wave's beginning and end, and the join of runs, which pays for long sums
 // of few tiles (50000 pixels' gradient of a 64 x 64 weight: 211 us in one run, 18 in
 // 32; of 32768 pixels' 1024 x 1024 one: 162 and, in 4, 50).
 struct Cut {
-    int tile_n, pair, splits;
+    int tile_n, pairs, splits;
     unsigned pitch;
     size_t bytes;
 };
 // through: a single run goes through the workspace as well.  A run is as long as its
 // accumulator's cut sums allow, n 1e-9 for n terms: float32 inputs 768 (8e-7, about
 // what float32 arithmetic leaves), 16-bit ones 2048 for a float32 result, else 16384.
-Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool through)
+// turned: both operands are.
+Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool through, bool turned)
 {
     const long long chunks = (terms + 63) / 64;
     const int products = dtype == RZ_F32 ? 6 : 1;
@@ -474,12 +475,14 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool t
     Cut best{};
     double least = 0.0;
     const unsigned pitch = static_cast<unsigned>(up(N, 8));
-    for (int pair = 0; pair < 2; pair++)
-        for (int tile = 256; tile >= (pair ? 128 : 64); tile /= 2) {
-            if ((tile > 64 && N <= static_cast<unsigned>(tile) / 2) || (pair && M <= 128)) continue;
-            const double stage = tile == 256 ? (pair ? 690 : 780) : tile == 128 ? (pair ? 590 : 580) : 560;
-            const long long rows = pair ? 256 : 128, slots = pair ? kLinSms / 2 : kLinSms;
-            const long long tiles = (M + rows - 1) / rows * ((N + tile - 1) / tile);
+    for (int pairs = 0; pairs < 3; pairs++)
+        for (int tile = 256; tile >= (pairs ? 128 : 64); tile /= 2) {
+            const long long across = (N + tile - 1) / tile;
+            if ((tile > 64 && N <= static_cast<unsigned>(tile) / 2) || (pairs && M <= 128)) continue;
+            if (pairs == 2 && (!turned || tile < 256 || across % 2)) continue;
+            const double stage = tile < 256 ? (tile == 64 ? 560 : pairs ? 590 : 580) : pairs == 2 ? 640 : !pairs ? 780 : turned ? 720 : 690;
+            const long long rows = pairs ? 256 : 128, slots = pairs == 2 ? kQuads : pairs ? kLinSms / 2 : kLinSms;
+            const long long tiles = (M + rows - 1) / rows * (pairs == 2 ? across / 2 : across);
             for (int want = fewest; want < fewest + 64 && want <= chunks; want++) {
                 const long long run = (chunks + want - 1) / want;
                 const int splits = static_cast<int>((chunks + run - 1) / run);
@@ -490,7 +493,7 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool t
                 if (joined) t += 6500 + 170.0 * splits + 4.0 * M * pitch * (splits + 1) / 2500.0;
                 if (!best.tile_n || t < least) {
                     least = t;
-                    best = {tile, pair, splits, pitch, joined ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
+                    best = {tile, pairs, splits, pitch, joined ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
                 }
                 if (waves > 3) break;
             }
@@ -587,7 +590,7 @@ cudaError_t product(const Operand &a, const Operand &b, const Finish &f, int out
     p.part = c.bytes ? part : nullptr;
     p.part_pitch = c.pitch;
     p.tile_n = c.tile_n;
-    p.pair = c.pair;
+    p.pairs = c.pairs;
     p.status = status;
     cudaError_t e = launch_product(p, stream);
     if (e != cudaSuccess || !c.bytes) return e;
@@ -682,7 +685,7 @@ Forward plan_forward(const rz_linear *d, const LinPlan &p, const rz_map *x, cons
     f.x = lay(rows_of(x, p.x), p.P, C, d->dtype, false);
     f.w = lay(rows_of(weight, weight_pitch), K, C, d->dtype, false);
     if (f.few) return f;
-    f.c = cut(p.P, K, C, d->dtype, d->dtype, !direct_out(f.out, d->dtype));
+    f.c = cut(p.P, K, C, d->dtype, d->dtype, !direct_out(f.out, d->dtype), false);
     f.w.at = up(f.x.bytes, 256);
     f.part = f.w.at + up(f.w.bytes, 256);
     f.total = f.part + f.c.bytes;
@@ -710,11 +713,11 @@ Backward plan_backward(const rz_linear *d, const LinPlan &p, const rz_map *dy, c
     if (!dx) b.w.bytes = 0;
     if (dx) {
         b.dx = finish_of(rows_of(dx, p.x), p.P, C, d->dtype, nullptr, nullptr);
-        b.cx = cut(p.P, C, K, d->dtype, d->dtype, !direct_out(b.dx, d->dtype));
+        b.cx = cut(p.P, C, K, d->dtype, d->dtype, !direct_out(b.dx, d->dtype), false);
     }
     if (dweight) {
         b.dw = finish_of(rows_of(dweight, dweight_pitch), K, C, dweight_dtype, nullptr, nullptr);
-        b.cw = cut(K, C, p.P, d->dtype, dweight_dtype, !direct_out(b.dw, dweight_dtype));
+        b.cw = cut(K, C, p.P, d->dtype, dweight_dtype, !direct_out(b.dw, dweight_dtype), true);
     }
     b.chunks = pack_chunks(p.P, K);
     b.x.at = up(b.dz.bytes, 256);

@@ -4,7 +4,12 @@
 // for the operands' tiles by TMA, into a ring of stages in the 128-byte swizzle;
 // one thread issues four tcgen05.mma (16 terms each) a stage, accumulating in
 // tensor memory; eight warps take finished tiles out of it.  Tensor memory holds
-// two tiles, so that one is stored while the next is computed.  CTAs are
+// two tiles, so that one is stored while the next is computed.  A pair of CTAs
+// computes 256 x tile_n, each with its half of A's rows and of B's; two pairs next to
+// each other may share A, each of their CTAs loading half of what it needs for both
+// (multicast), which pays where both operands are turned: their boxes cost L2 more,
+// and in a sustained run power (8192^3: 660 against 540 us; products by rows of A are
+// the same either way or lose the SMs that no cluster of four reaches).  CTAs are
 // persistent and take tiles in turn, those of one row of tiles next to each
 // other, so that their rows of A come from L2.
 //
@@ -78,6 +83,16 @@ __device__ __forceinline__ void load_box(const CUtensorMap *map, uint32_t to, ui
                      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(plane), "r"(bar)
                      : "memory");
 }
+// The same into the places of every CTA of the mask, counted by the first CTA of each
+// one's pair.
+__device__ __forceinline__ void load_shared_box(const CUtensorMap *map, uint32_t to, uint32_t bar, int x, int y, int z, int plane,
+                                                uint16_t mask)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(to),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(plane), "r"(bar), "h"(mask)
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
 {
     uint32_t r;
@@ -119,9 +134,9 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
                      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
                      : "memory");
 }
-// One arrival at the barrier (of a pair: at both CTAs') once the products so far are done.
+// One arrival at the barrier (of a pair: at those of the CTAs of `mask`) once the products so far are done.
 template <int CG>
-__device__ __forceinline__ void commit(uint64_t *bar)
+__device__ __forceinline__ void commit(uint64_t *bar, uint16_t mask)
 {
     if constexpr (CG == 1)
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
@@ -129,7 +144,7 @@ __device__ __forceinline__ void commit(uint64_t *bar)
     else
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
                          smem_addr(bar)),
-                     "h"(static_cast<uint16_t>(3))
+                     "h"(mask)
                      : "memory");
 }
 
@@ -223,14 +238,15 @@ struct Tile {
     unsigned m, n, run;
     int first, last, stages;
 };
-__device__ __forceinline__ Tile tile_at(const TcArgs &a, unsigned t)
+template <int PAIRS>
+__device__ __forceinline__ Tile tile_at(const TcArgs &a, unsigned t, uint32_t pair)
 {
     Tile r;
     const unsigned all = a.tiles_m * a.tiles_n, x = t % all, per = a.group * a.tiles_n;
     const unsigned g = x / per, y = x - g * per, rows = min(a.group, a.tiles_m - g * a.group);
     r.run = t / all;
     r.m = g * a.group + y % rows;
-    r.n = y / rows;
+    r.n = y / rows * PAIRS + pair;
     r.first = static_cast<int>(r.run) * a.run;
     r.last = min(a.chunks, r.first + a.run);
     r.stages = (r.last - r.first) * (a.planes == 1 ? 1 : 6);
@@ -249,7 +265,7 @@ __device__ __forceinline__ void planes_of(int planes, int j, int &a, int &b)
     b = 0x010210 >> (4 * j) & 0xf;
 }
 
-template <class T, int ACT, int CG>
+template <class T, int ACT, int CG, int PAIRS>
 __global__ void __launch_bounds__(kThreads, 1)
 k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
@@ -263,15 +279,17 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
     const uint32_t ring = smem_addr(raw) + pad;
     const int rows_b = a.tile_n / CG;     // this CTA's share of B's rows
     const int stage_bytes = kBytesA + rows_b * kTerms * 2;
-    uint32_t rank = 0;
-    if constexpr (CG == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    const unsigned first_tile = blockIdx.x / CG, tile_step = gridDim.x / CG;
+    // place in the cluster, and in the pair; the pair's first CTA
+    uint32_t place = 0;
+    if constexpr (CG == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(place));
+    const uint32_t rank = place & 1, leader = place & ~1u, pair = place >> 1;
+    const unsigned first_tile = blockIdx.x / (CG * PAIRS), tile_step = gridDim.x / (CG * PAIRS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; i++) {
             dev::mbar_init(full + i, 1);
-            dev::mbar_init(empty + i, 1);
+            dev::mbar_init(empty + i, PAIRS);
         }
         for (int i = 0; i < 2; i++) {
             dev::mbar_init(done + i, 1);
@@ -309,13 +327,14 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             const int turned = of_b ? a.b_turned : a.a_turned, merged = of_b ? a.b_merged : a.a_merged;
             const int rows = of_b ? rows_b : kTileM;
             const uint32_t to = ring + (of_b ? kBytesA : 0);
-            const uint32_t bars = CG == 1 ? smem_addr(full) : in_cta(smem_addr(full), 0);
+            const uint32_t bars = CG == 1 ? smem_addr(full) : in_cta(smem_addr(full), leader);
+            const uint16_t both_pairs = static_cast<uint16_t>(5u << rank);
             int s = 0;
             uint32_t phase = 0;
             bool ok = true;
             unsigned asked = 0;
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step) {
-                const Tile w = tile_at(a, t);
+                const Tile w = tile_at<PAIRS>(a, t, pair);
                 const int row = of_b ? static_cast<int>(w.n * a.tile_n + rank * rows_b) : static_cast<int>((w.m * CG + rank) * kTileM);
                 int j = 0, k0 = w.first * kTerms, pa, pb;
                 planes_of(a.planes, j, pa, pb);
@@ -325,7 +344,9 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                     if (!of_b && rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
                     const uint32_t at = to + s * stage_bytes, bar = bars + 8 * s;
                     const int plane = of_b ? pb : pa;
-                    if (!turned)
+                    if (PAIRS == 2 && !of_b)  // turned; this pair's half of the rows, for both
+                        load_shared_box(map, at + pair * 8192, bar, row + pair * 64, k0, 0, plane, both_pairs);
+                    else if (!turned)
                         load_box<CG>(map, at, bar, k0, row, 0, plane);
                     else if (merged)
                         load_box<CG>(map, at, bar, 0, k0, row / 64, plane);
@@ -360,7 +381,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             const uint64_t desc_a = tile_desc(ring, a.a_turned), desc_b = tile_desc(ring + kBytesA, a.b_turned);
             const uint32_t step_a = (a.a_turned ? 2048 : 32) >> 4, step_b = (a.b_turned ? 2048 : 32) >> 4;
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
-                const Tile w = tile_at(a, t);
+                const Tile w = tile_at<PAIRS>(a, t, pair);
                 const uint32_t acc = tmem + (i & 1) * 256;
                 ok = wait_for(taken + (i & 1), (i >> 1 & 1) ^ 1, a.status);
                 if (!ok) break;
@@ -374,13 +395,13 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
 #pragma unroll
                     for (uint32_t k = 0; k < kTerms / 16; k++)
                         mma<CG>(acc, da + k * step_a, db + k * step_b, a.idesc, c > 0 || k > 0);
-                    commit<CG>(empty + s);
+                    commit<CG>(empty + s, PAIRS == 2 ? 15 : 3);
                     if (++s == a.stages) {
                         s = 0;
                         phase ^= 1;
                     }
                 }
-                if (ok) commit<CG>(done + (i & 1));
+                if (ok) commit<CG>(done + (i & 1), static_cast<uint16_t>(3u << leader));
             }
         }
     } else if (warp >= 4) {
@@ -397,7 +418,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
         unsigned i = 0;
         bool ok = true;
         for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
-            const Tile w = tile_at(a, t);
+            const Tile w = tile_at<PAIRS>(a, t, pair);
             const unsigned m0 = (w.m * CG + rank) * kTileM + 32 * quarter, n0 = w.n * a.tile_n + (e >> 2) * cols;
             const int live = m0 < a.f.M && n0 < a.f.N ? min(blocks, static_cast<int>((a.f.N - n0 + BC - 1) / BC)) : 0;
             const auto fetch = [&](int b, int place) {
@@ -445,7 +466,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                         if constexpr (CG == 1)
                             dev::mbar_arrive(taken + (i & 1));
                         else
-                            arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), 0));
+                            arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), leader));
                     }
                 }
                 if (b >= live) continue;
@@ -566,13 +587,13 @@ struct Maps {
     CUtensorMap a, b, out, pre, residual;
 };
 
-template <class T, int ACT, int CG>
+template <class T, int ACT, int CG, int PAIRS>
 cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
 {
-    const auto fn = k_linear_tc<T, ACT, CG>;
+    const auto fn = k_linear_tc<T, ACT, CG, PAIRS>;
     if (const cudaError_t e = shared_opt_in(reinterpret_cast<const void *>(fn), kSmem - kStatic)) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CG * std::min<unsigned>(a.tiles, kSms / CG));
+    cfg.gridDim = dim3(CG * PAIRS * std::min<unsigned>(a.tiles, PAIRS == 2 ? kQuads : kSms / CG));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = 1024 + a.stages * static_cast<size_t>(kBytesA + a.tile_n / CG * kTerms * 2) +
                            static_cast<size_t>(kEpiWarps) * a.places * kBlockBytes;
@@ -581,7 +602,7 @@ cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = CG * PAIRS;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 1 ? 1 : 2;
@@ -591,13 +612,14 @@ cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
 template <class T, int CG>
 cudaError_t tc_launch_act(const TcArgs &a, const Maps &m, void *stream)
 {
-    if (a.f.act == RZ_ACT_SILU) return tc_launch<T, RZ_ACT_SILU, CG>(a, m, stream);
-    return a.f.act == RZ_ACT_GELU ? tc_launch<T, RZ_ACT_GELU, CG>(a, m, stream) : tc_launch<T, RZ_ACT_NONE, CG>(a, m, stream);
+    if (a.f.act == RZ_ACT_SILU) return tc_launch<T, RZ_ACT_SILU, CG, 1>(a, m, stream);
+    return a.f.act == RZ_ACT_GELU ? tc_launch<T, RZ_ACT_GELU, CG, 1>(a, m, stream) : tc_launch<T, RZ_ACT_NONE, CG, 1>(a, m, stream);
 }
 template <class T>
-cudaError_t tc_launch_of(const TcArgs &a, const Maps &m, int pair, void *stream)
+cudaError_t tc_launch_of(const TcArgs &a, const Maps &m, int pairs, void *stream)
 {
-    return pair ? tc_launch_act<T, 2>(a, m, stream) : tc_launch_act<T, 1>(a, m, stream);
+    if (pairs == 2) return tc_launch<T, RZ_ACT_NONE, 2, 2>(a, m, stream);
+    return pairs ? tc_launch_act<T, 2>(a, m, stream) : tc_launch_act<T, 1>(a, m, stream);
 }
 
 }  // namespace
@@ -614,10 +636,12 @@ bool lin::direct_out(const Finish &f, int dtype)
 cudaError_t lin::launch_product(const Product &p, void *stream)
 {
     if (!encoder()) return cudaErrorNotSupported;
-    const int cg = p.pair ? 2 : 1;
+    const int cg = p.pairs ? 2 : 1;
     Maps m;
     TcArgs a{};
-    if (!encode(p.a, kTileM, &m.a, &a.a_merged) || !encode(p.b, p.tile_n / cg, &m.b, &a.b_merged)) return cudaErrorInvalidValue;
+    if (p.pairs == 2 && (!p.a.turned || p.f.act != RZ_ACT_NONE)) return cudaErrorInvalidValue;
+    if (!encode(p.a, p.pairs == 2 ? kTileM / 2 : kTileM, &m.a, &a.a_merged) || !encode(p.b, p.tile_n / cg, &m.b, &a.b_merged))
+        return cudaErrorInvalidValue;
     a.f = p.f;
     int dtype = p.out_dtype;
     if (p.part) {
@@ -637,6 +661,7 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     a.tile_n = p.tile_n;
     a.tiles_m = (p.f.M + cg * kTileM - 1) / (cg * kTileM);
     a.tiles_n = (p.f.N + p.tile_n - 1) / p.tile_n;
+    if (p.pairs == 2) a.tiles_n = (a.tiles_n + 1) / 2;
     a.planes = p.a.planes;
     // Tiles of a row next to each other read its A at once, and B out of L2 where that holds it (65536 x 1024 x 4096: 341 us,
     // rows of tiles in groups of eight 373).  A larger B is read once for eight rows of tiles (8192 x 8192 x 8192: 611 us, by
@@ -654,8 +679,8 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     a.idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<unsigned>(p.a.turned) << 15) |
               (static_cast<unsigned>(p.b.turned) << 16) | (static_cast<unsigned>(p.tile_n >> 3) << 17) | (static_cast<unsigned>(cg * kTileM >> 4) << 24);
     a.status = p.status;
-    if (dtype == RZ_F32) return tc_launch_of<float>(a, m, p.pair, stream);
-    return dtype == RZ_BF16 ? tc_launch_of<__nv_bfloat16>(a, m, p.pair, stream) : tc_launch_of<__half>(a, m, p.pair, stream);
+    if (dtype == RZ_F32) return tc_launch_of<float>(a, m, p.pairs, stream);
+    return dtype == RZ_BF16 ? tc_launch_of<__nv_bfloat16>(a, m, p.pairs, stream) : tc_launch_of<__half>(a, m, p.pairs, stream);
 }
 
 }  // namespace rz
