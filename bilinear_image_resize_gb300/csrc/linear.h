@@ -64,10 +64,13 @@ __device__ __forceinline__ float2 activated(float2 z)
         return z;
     }
 }
-// Their derivatives; GELU's is Phi(z) + z phi(z).
+// Their derivatives; GELU's is Phi(z) + z phi(z).  From 1e4 on they are 0 or 1, of an
+// infinite z (a float16 pre past its type's range) as well; NaN stays.
+__device__ __forceinline__ float within(float z) { return z > 1.0e4f ? 1.0e4f : z < -1.0e4f ? -1.0e4f : z; }
 template <class T>
 __device__ __forceinline__ float2 act_slope(float2 z, int act)
 {
+    z = make_float2(within(z.x), within(z.y));
     if (act == RZ_ACT_SILU) {
         const float2 x = __fmul2_rn(z, both(-1.44269504f));
         const float2 d = __fadd2_rn(make_float2(exp2_approx(x.x), exp2_approx(x.y)), both(1.0f));

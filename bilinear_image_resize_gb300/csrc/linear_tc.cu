@@ -414,7 +414,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
         const int e = warp - 4, quarter = warp & 3, cols = a.tile_n / 2, blocks = cols / BC;
         uint8_t *out = raw + pad + a.stages * stage_bytes + e * a.places * kBlockBytes;
         int flip = 0;
-        uint32_t phases = 0;
+        uint32_t phases = 0, coming = 0;        // a bit of each place: its barrier's phase, and whether a residual is on its way
         unsigned i = 0;
         bool ok = true;
         for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
@@ -423,6 +423,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             const int live = m0 < a.f.M && n0 < a.f.N ? min(blocks, static_cast<int>((a.f.N - n0 + BC - 1) / BC)) : 0;
             const auto fetch = [&](int b, int place) {
                 uint64_t *bar = &came[e][place];
+                coming |= 1u << place;
                 dev::mbar_arrive_expect_tx(bar, kBlockBytes);
                 asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
                              "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(out + place * kBlockBytes)),
@@ -502,6 +503,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                     ok = __all_sync(0xffffffffu, wait_for(&came[e][flip], phases >> flip & 1, a.status));
                     if (!ok) break;
                     phases ^= 1u << flip;
+                    coming &= ~(1u << flip);
 #pragma unroll
                     for (int q = 0; q < SUBS; q++) block_add<T>(block, q, z[q]);
                 } else {
@@ -514,7 +516,11 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                 flip ^= 1;
             }
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane == 0) {
+            for (int place = 0; place < 2; place++)
+                if (coming >> place & 1) wait_for(&came[e][place], phases >> place & 1, a.status);
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();

@@ -499,11 +499,16 @@ long long pb_offsets(const PbArgs &a)
     return static_cast<long long>(a.g.q[0] + a.g.k[0] - 1) * (a.g.q[1] + a.g.k[1] - 1) * a.g.heads;
 }
 size_t pb_bytes(const PbArgs &a) { return pb_dense_at(a) + sizeof(float) * static_cast<size_t>(pb_offsets(a)); }
-bool pb_too_many(const PbArgs &a) { return pb_units(a) > 0x7fffffffLL || pb_offsets(a) / kPbThreads >= 0x7fffffffLL; }
+bool pb_too_many(const PbArgs &a)
+{
+    const long long entries = static_cast<long long>(a.g.buckets[0]) * a.g.buckets[1] * a.g.heads;
+    return pb_units(a) > 0x7fffffffLL || pb_offsets(a) / kPbThreads >= 0x7fffffffLL || entries / kPbWarps >= 0x7fffffffLL;
+}
 
 int pb_status(cudaError_t e)
 {
     if (e == cudaSuccess) return RZ_OK;
+    if (e == cudaErrorNotSupported) return RZ_ERR_UNSUPPORTED;
     record_cuda_error(static_cast<int>(e));
     return RZ_ERR_CUDA;
 }
@@ -529,7 +534,7 @@ cudaError_t pb_forward(PbArgs &a, bool whole, void *stream)
     }
     pb_plan_forward(a);
     const long long blocks = static_cast<long long>(a.nk) * a.nx * a.g.q[1] * a.nq * a.g.heads * a.ngn;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (blocks > 0x7fffffffLL) return cudaErrorNotSupported;
     return pb_launch(k_bias<T, WIDE, SCORES>, blocks, bytes(static_cast<long long>(a.tq + a.tk - 1) * a.tx), stream, a);
 }
 

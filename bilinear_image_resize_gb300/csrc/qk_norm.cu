@@ -49,7 +49,7 @@ struct QkArgs {
 
 // Cosine and sine of position * turn: the product's low 64 bits are the angle
 // modulo a turn, exactly; its top 32 bits go on as a signed float.  16-bit results
-// take the GPU's approximate functions, off by 2^-21.2 in [-pi, pi].
+// take the GPU's approximate functions, off by 2^-21.2 in [-pi, pi] (with the angle's rounding 7e-7).
 template <class T>
 __device__ __forceinline__ void turned(int p, unsigned long long turn, float &c, float &s)
 {
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kQkThreads, NV == 1 ? 2 : 1) k_qk_grad(const _
                 }
                 place = place + 1 == kPlaces ? 0 : place + 1;
                 const float sum1 = group_sum(s1.x + s1.y, lanes), sum2 = group_sum(s2.x + s2.y, lanes);
-                const float r = rsqrtf(fmaf(sum1, a.inv_d, a.eps)), m = r * r * r * (sum2 * a.inv_d);
+                const float r = rsqrtf(fmaf(sum1, a.inv_d, a.eps)), m = sum2 * a.inv_d * r * r * r;    // r^3 alone may pass the range
 #pragma unroll
                 for (int v = 0; v < NV; v++) {
                     // r of a group without a head is not finite for eps 0

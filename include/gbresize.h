@@ -564,7 +564,10 @@ RZ_API int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_ma
  * bytes apart), b float[K] or NULL, act as in map_group_norm, residual a map
  * of y's shape or NULL.  pre: a map of y's shape that takes z, rounded, for the
  * gradient, or NULL.  x: C channels; y, residual and pre: K.  Products are
- * summed in float32; the result is rounded once.
+ * summed in float32; the result is rounded once.  float32 products are off by
+ * about 1e-6 of the sum of their terms' magnitudes; GELU of 16-bit maps by 7.5e-8 |z|
+ * before it is rounded.  A value that is not finite reaches the results of its own
+ * row or column alone; an infinity of float32 maps may come out as NaN.
  * y may be the residual itself, and overlaps no other map; weight and b lie
  * apart from y and pre.  K, C in [1, RZ_MAX_DIM], N * H * W < 2^31 (else
  * RZ_ERR_UNSUPPORTED).
@@ -598,7 +601,9 @@ RZ_API int map_linear(const rz_linear *d, const rz_map *x, const void *weight, s
  * dweight K rows of C elements of dweight_dtype (the map's dtype or RZ_F32),
  * dweight_pitch bytes apart, dbias device float[K]; each may be NULL, is written,
  * not added to, and overlaps no input; an empty map makes dweight and dbias 0.
- * Sums run in a fixed order.  Workspace, status and the rest as map_linear.
+ * Sums run in a fixed order, in float32; dz of 16-bit maps enters dx and dweight as
+ * a value of its type (rounded once where there is an activation), dbias as float32.
+ * Workspace, status and the rest as map_linear.
  */
 RZ_API int map_linear_grad_workspace(const rz_linear *d, const rz_map *dy, const rz_map *x, const void *weight,
                                      size_t weight_pitch, const rz_map *pre, const rz_map *dx, const void *dweight,
@@ -620,10 +625,10 @@ RZ_API int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x
  *   angle = col scale base^(-(j - row_pairs) / col_pairs)      after them;
  * further pairs stay.  Pair j is (u[j], u[j + D / 2]), or (u[2j], u[2j + 1])
  * where `interleaved` is set.  (row, col) is the pixel's place in its image, or
- * positions[n][h][w] (device int[N][H][W][2]) where that is given; any int.
- * Angles are reduced to a turn exactly, in 64-bit integers, whatever the
- * position: they are off by 2^-24 of half a turn at most, their cosines and
- * sines by 3e-7.
+ * positions[n][h][w] (device int[N][H][W][2], 8-byte aligned) where that is given;
+ * any int.  Angles are reduced to a turn exactly, in 64-bit integers, whatever the
+ * position: they are off by 2^-24 of half a turn at most, their cosines and sines
+ * by 3e-7 for float32 maps, by 7e-7 for 16-bit ones.
  * x has C channels, y has out_C, either at least (q_heads + k_heads) D.
  * D even, 2 <= D <= 256; one head at least; eps >= 0, base > 0 and scale
  * finite; row_pairs + col_pairs <= D / 2.  A head of zeros gives zeros where
@@ -690,7 +695,8 @@ RZ_API int map_position_bias(const rz_bias *d, const float *table, const int *ro
  * The gradient of map_position_bias towards its table from dout: dtable[r][c][a]
  * = the sum of dout[n][a][q][k] over the batch and the pairs of bucket (r, c),
  * written, not added to; 0 where there is none.  (The one towards scores is
- * dout itself.)  Sums run in a fixed order.  Workspace as above.
+ * dout itself.)  Sums run in a fixed order.  Workspace as above.  Past 2^34 table
+ * entries RZ_ERR_UNSUPPORTED.
  */
 RZ_API int map_position_bias_grad_workspace(const rz_bias *d, size_t *bytes);
 RZ_API int map_position_bias_grad(const rz_bias *d, const rz_map *dout, const int *rows, const int *cols,

@@ -167,6 +167,16 @@ def test_position_bias_refuses(lib, nat):
         assert n.value == 0
 
 
+def test_position_bias_past_the_grid(lib, nat):
+    """A table of more entries than a launch has warps, and more rows and heads than it has blocks."""
+    d, n = nat.RzBias(N=1, heads=1 << 13, q_h=1, q_w=1, k_h=1, k_w=1, row_buckets=1 << 11, col_buckets=1 << 11, dtype=1), ctypes.c_size_t(7)
+    one = nat.RzMap(1 << 20, 4, 4)
+    assert lib.map_position_bias_grad_workspace(d, ctypes.byref(n)) == UNSUPPORTED
+    assert lib.map_position_bias_grad(d, one, 1 << 23, 1 << 24, 1 << 22, 1 << 30, 1 << 30, None) == UNSUPPORTED
+    d = nat.RzBias(N=1, heads=1 << 16, q_h=1, q_w=1 << 16, k_h=2, k_w=1, row_buckets=1, col_buckets=1, dtype=1)
+    assert lib.map_position_bias(d, 1 << 22, 1 << 23, 1 << 24, None, nat.RzMap(1 << 40, 8, 1 << 19), None) == UNSUPPORTED
+
+
 def test_buckets_match_the_definition(lib):
     import bilinear_image_resize_gb300 as rz
     rng = random.Random(1)
