@@ -166,24 +166,33 @@ __global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_const
 
 // dbias: the chunks' sums, 32 columns a block, each of its warps a chunk in
 // eight, joined in order.
-__global__ void __launch_bounds__(256) k_linear_sums(const float *sums, unsigned chunks, unsigned C, float *dbias)
+struct Sums {
+    const float *from;
+    float *to;              // null: none
+    unsigned chunks, C;
+};
+__device__ __forceinline__ void sum_columns(const Sums &a, unsigned block)
 {
     __shared__ float sh[8][32];
-    grid_launch_dependents();
-    grid_dependency_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const unsigned c = blockIdx.x * 32 + lane;
+    const unsigned c = block * 32 + lane;
     float s = 0.0f;
-    if (c < C) {
-#pragma unroll 8
-        for (unsigned r = w; r < chunks; r += 8) s += sums[static_cast<long long>(r) * C + c];
+    if (c < a.C) {
+#pragma unroll 16
+        for (unsigned r = w; r < a.chunks; r += 8) s += a.from[static_cast<long long>(r) * a.C + c];
     }
     sh[w][lane] = s;
     __syncthreads();
-    if (w || c >= C) return;
+    if (w || c >= a.C) return;
 #pragma unroll
     for (int i = 1; i < 8; i++) s += sh[i][lane];
-    dbias[c] = s;
+    a.to[c] = s;
+}
+__global__ void __launch_bounds__(256) k_linear_sums(const __grid_constant__ Sums a)
+{
+    grid_launch_dependents();
+    grid_dependency_wait();
+    sum_columns(a, blockIdx.x);
 }
 
 // The runs of a product joined in order, and its epilogue; a run alone where its
@@ -193,6 +202,8 @@ struct JoinArgs {
     const float *part;
     unsigned pitch;         // floats, a multiple of VE
     int splits;
+    unsigned blocks;        // those after them sum the bias's columns (a launch less: 134 -> NEW us on 32768 x 1024 x 1024)
+    Sums sums;
 };
 
 constexpr int kJoinUnits = 4;   // units a thread has in flight where vectors do not fit
@@ -205,6 +216,10 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Joi
     constexpr int U = WIDE ? 1 : kJoinUnits;
     grid_launch_dependents();
     grid_dependency_wait();
+    if (blockIdx.x >= a.blocks) {
+        sum_columns(a.sums, blockIdx.x - a.blocks);
+        return;
+    }
     // a block's first unit by 64-bit division, the others from there
     const unsigned units = a.f.N / UNIT;
     const unsigned long long base = static_cast<unsigned long long>(blockIdx.x) * (256 * U);
@@ -475,27 +490,37 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool t
     Cut best{};
     double least = 0.0;
     const unsigned pitch = static_cast<unsigned>(up(N, 8));
+    const double of_split = 170.0 + 4.0 * M * pitch / 2500.0;
     for (int pairs = 0; pairs < 3; pairs++)
         for (int tile = 256; tile >= (pairs ? 128 : 64); tile /= 2) {
             const long long across = (N + tile - 1) / tile;
             if ((tile > 64 && N <= static_cast<unsigned>(tile) / 2) || (pairs && M <= 128)) continue;
             if (pairs == 2 && (!turned || tile < 256 || across % 2)) continue;
             const double stage = tile < 256 ? (tile == 64 ? 560 : pairs ? 590 : 580) : pairs == 2 ? 640 : !pairs ? 780 : turned ? 720 : 690;
-            const long long rows = pairs ? 256 : 128, slots = pairs == 2 ? kQuads : pairs ? kLinSms / 2 : kLinSms;
-            const long long tiles = (M + rows - 1) / rows * (pairs == 2 ? across / 2 : across);
-            for (int want = fewest; want < fewest + 64 && want <= chunks; want++) {
+            const int rows = pairs ? 256 : 128, slots = pairs == 2 ? kQuads : pairs ? kLinSms / 2 : kLinSms;
+            const long long tiles = static_cast<long long>((M + rows - 1ull) / rows) * (pairs == 2 ? across / 2 : across);
+            const auto consider = [&](long long want) {
+                want = std::min<long long>(std::max<long long>(want, fewest), chunks);
                 const long long run = (chunks + want - 1) / want;
                 const int splits = static_cast<int>((chunks + run - 1) / run);
-                if (splits != want && want != fewest) continue;
                 const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
                 double t = waves * (run * products * stage + 2500) + 4.0 * tile;
                 const bool joined = splits > 1 || through;
-                if (joined) t += 6500 + 170.0 * splits + 4.0 * M * pitch * (splits + 1) / 2500.0;
+                if (joined) t += 6500 + of_split * splits + 4.0 * M * pitch / 2500.0;
                 if (!best.tile_n || t < least) {
                     least = t;
                     best = {tile, pairs, splits, pitch, joined ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
                 }
-                if (waves > 3) break;
+            };
+            consider(fewest);
+            consider(fewest + 1);
+            // of the runs that make one wave, two or three: as many as there can be, or those whose joins cost what they save
+            for (int waves = 1; waves <= 3; waves++) {
+                const long long most = std::min<long long>(waves * static_cast<long long>(slots) / tiles, fewest + 63);
+                if (most <= fewest) continue;
+                consider(most);
+                const long long even = std::lround(std::sqrt(waves * static_cast<double>(chunks) * products * stage / of_split));
+                if (even < most) consider(even);
             }
         }
     return best;
@@ -555,7 +580,7 @@ unsigned pack_chunks(unsigned rows, unsigned cols)
 }
 
 template <class T, int ACT>
-cudaError_t join_launch(const JoinArgs &a, void *stream)
+cudaError_t join_launch(JoinArgs a, void *stream)
 {
     constexpr int VE = 16 / sizeof(T);
     // pairs: rows of them, two elements' alignment everywhere
@@ -566,10 +591,11 @@ cudaError_t join_launch(const JoinArgs &a, void *stream)
             even = false;
     const unsigned unit = a.f.wide ? VE : even ? 2 : 1;
     const unsigned long long n = static_cast<unsigned long long>(a.f.M) * (a.f.N / unit), block = 256ull * (a.f.wide ? 1 : kJoinUnits);
-    const unsigned long long blocks = (n + block - 1) / block;
-    if (blocks > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+    const unsigned long long blocks = (n + block - 1) / block, columns = a.sums.to ? (a.sums.C + 31) / 32 : 0;
+    if (blocks + columns > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+    a.blocks = static_cast<unsigned>(blocks);
     const auto fn = a.f.wide ? k_linear_join<T, ACT, VE> : even ? k_linear_join<T, ACT, 2> : k_linear_join<T, ACT, 1>;
-    return launch(fn, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, a);
+    return launch(fn, dim3(static_cast<unsigned>(blocks + columns)), 256, 0, stream, a);
 }
 template <class T>
 cudaError_t join_of(const JoinArgs &a, void *stream)
@@ -579,7 +605,7 @@ cudaError_t join_of(const JoinArgs &a, void *stream)
 }
 
 cudaError_t product(const Operand &a, const Operand &b, const Finish &f, int out_dtype, const Cut &c, float *part, int *status,
-                    void *stream)
+                    void *stream, const Sums &sums = {})
 {
     Product p{};
     p.a = a;
@@ -594,7 +620,7 @@ cudaError_t product(const Operand &a, const Operand &b, const Finish &f, int out
     p.status = status;
     cudaError_t e = launch_product(p, stream);
     if (e != cudaSuccess || !c.bytes) return e;
-    const JoinArgs j{f, part, c.pitch, c.splits};
+    const JoinArgs j{f, part, c.pitch, c.splits, 0, sums};
     if (out_dtype == RZ_F32) return join_of<float>(j, stream);
     return out_dtype == RZ_BF16 ? join_of<__nv_bfloat16>(j, stream) : join_of<__half>(j, stream);
 }
@@ -863,12 +889,17 @@ int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x, const
     for (const Laid *l : {&b.x, &b.w})
         if (l->bytes) add_job(jobs, *l, nullptr, 0, nullptr, pack_chunks(l->rows, l->cols), ws);
     cudaError_t e = pack_launch(jobs, d->dtype, stream);
-    if (dbias && e == cudaSuccess)
-        e = maps::launch(k_linear_sums, dim3((d->K + 31) / 32), 256, 0, stream, sums, b.chunks, static_cast<unsigned>(d->K), dbias);
+    // dbias in the last join that there is, else by itself
+    const Sums columns{sums, dbias, b.chunks, static_cast<unsigned>(d->K)};
+    const bool with_w = dbias && dweight && b.cw.bytes, with_x = dbias && !with_w && dx && b.cx.bytes;
     if (dx && e == cudaSuccess)
-        e = product(operand(b.dz, ws, false), operand(b.w, ws, true), b.dx, d->dtype, b.cx, part, status, stream);
+        e = product(operand(b.dz, ws, false), operand(b.w, ws, true), b.dx, d->dtype, b.cx, part, status, stream,
+                    with_x ? columns : Sums{});
     if (dweight && e == cudaSuccess)
-        e = product(operand(b.dz, ws, true), operand(b.x, ws, true), b.dw, dweight_dtype, b.cw, part, status, stream);
+        e = product(operand(b.dz, ws, true), operand(b.x, ws, true), b.dw, dweight_dtype, b.cw, part, status, stream,
+                    with_w ? columns : Sums{});
+    if (dbias && !with_w && !with_x && e == cudaSuccess)
+        e = maps::launch(k_linear_sums, dim3((columns.C + 31) / 32), 256, 0, stream, columns);
     return lin_status(e);
 }
 
