@@ -169,6 +169,14 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&v)[16])
                  : "memory");
 }
 
+// True in one lane of a warp, the same one every time.
+__device__ __forceinline__ bool elected()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // A wait of at most a second that leaves no gap between its attempts.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int *status)
 {
@@ -284,7 +292,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
     if constexpr (CG == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(place));
     const uint32_t rank = place & 1, leader = place & ~1u, pair = place >> 1;
     const unsigned first_tile = blockIdx.x / (CG * PAIRS), tile_step = gridDim.x / (CG * PAIRS);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     grid_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; i++) {
@@ -321,7 +329,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
     if (warp == 0 || warp == 3) {
         // warp 0 asks for A's tiles, warp 3 for B's: one thread for both spends longer on a stage's requests than the
         // products take (its waits for a free stage were a fifth of its time)
-        if (lane == 0) {
+        {
             const bool of_b = warp == 3;
             const CUtensorMap *map = of_b ? &map_b : &map_a;
             const int turned = of_b ? a.b_turned : a.a_turned, merged = of_b ? a.b_merged : a.a_merged;
@@ -339,19 +347,22 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                 int j = 0, k0 = w.first * kTerms, pa, pb;
                 planes_of(a.planes, j, pa, pb);
                 for (int c = 0; c < w.stages; c++) {
-                    ok = wait_for(empty + s, phase ^ 1, a.status);
+                    ok = __all_sync(0xffffffffu, wait_for(empty + s, phase ^ 1, a.status));
                     if (!ok) break;
-                    if (!of_b && rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
                     const uint32_t at = to + s * stage_bytes, bar = bars + 8 * s;
                     const int plane = of_b ? pb : pa;
-                    if (PAIRS == 2 && !of_b)  // turned; this pair's half of the rows, for both
-                        load_shared_box(map, at + pair * 8192, bar, row + pair * 64, k0, 0, plane, both_pairs);
-                    else if (!turned)
-                        load_box<CG>(map, at, bar, k0, row, 0, plane);
-                    else if (merged)
-                        load_box<CG>(map, at, bar, 0, k0, row / 64, plane);
-                    else
-                        for (int i = 0; i < rows; i += 64) load_box<CG>(map, at + i * 128, bar, row + i, k0, 0, plane);
+                    if (elected()) {
+                        if (!of_b && rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
+                        if (PAIRS == 2 && !of_b)  // turned; this pair's half of the rows, for both
+                            load_shared_box(map, at + pair * 8192, bar, row + pair * 64, k0, 0, plane, both_pairs);
+                        else if (!turned)
+                            load_box<CG>(map, at, bar, k0, row, 0, plane);
+                        else if (merged)
+                            load_box<CG>(map, at, bar, 0, k0, row / 64, plane);
+                        else
+                            for (int i = 0; i < rows; i += 64) load_box<CG>(map, at + i * 128, bar, row + i, k0, 0, plane);
+                    }
+                    __syncwarp();
                     asked++;
                     if (++s == a.stages) {
                         s = 0;
@@ -373,7 +384,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                 }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int s = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -383,25 +394,29 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
                 const Tile w = tile_at<PAIRS>(a, t, pair);
                 const uint32_t acc = tmem + (i & 1) * 256;
-                ok = wait_for(taken + (i & 1), (i >> 1 & 1) ^ 1, a.status);
+                ok = __all_sync(0xffffffffu, wait_for(taken + (i & 1), (i >> 1 & 1) ^ 1, a.status));
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 for (int c = 0; c < w.stages; c++) {
-                    ok = wait_for(full + s, phase, a.status);
+                    ok = __all_sync(0xffffffffu, wait_for(full + s, phase, a.status));
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t at = static_cast<uint32_t>(s * stage_bytes) >> 4;   // the ring lies below 2^18: no carry leaves the address
                     const uint64_t da = desc_a + at, db = desc_b + at;
+                    if (elected()) {
 #pragma unroll
-                    for (uint32_t k = 0; k < kTerms / 16; k++)
-                        mma<CG>(acc, da + k * step_a, db + k * step_b, a.idesc, c > 0 || k > 0);
-                    commit<CG>(empty + s, PAIRS == 2 ? 15 : 3);
+                        for (uint32_t k = 0; k < kTerms / 16; k++)
+                            mma<CG>(acc, da + k * step_a, db + k * step_b, a.idesc, c > 0 || k > 0);
+                        commit<CG>(empty + s, PAIRS == 2 ? 15 : 3);
+                    }
+                    __syncwarp();
                     if (++s == a.stages) {
                         s = 0;
                         phase ^= 1;
                     }
                 }
-                if (ok) commit<CG>(done + (i & 1), static_cast<uint16_t>(3u << leader));
+                if (ok && elected()) commit<CG>(done + (i & 1), static_cast<uint16_t>(3u << leader));
+                __syncwarp();
             }
         }
     } else if (warp >= 4) {
