@@ -49,9 +49,18 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;  // loads of A, issuer, tensor me
 constexpr int kBlockRow = 64;                   // bytes of a row of a block on its way out, 32 rows a block
 constexpr int kBlockBytes = 32 * kBlockRow;
 constexpr int kSmem = 227 * 1024;
-constexpr int kStatic = 512;    // the kernel's own variables
 constexpr int kRing = 8;
 constexpr int kSms = 152;
+
+// What lies in shared memory before the ring, which begins at a multiple of 1024: the kernel's own variables, then
+// bias of two tiles.
+struct alignas(16) Vars {
+    uint64_t full[kRing], empty[kRing], done[2], taken[2];
+    uint64_t came[kEpiWarps][2];    // a residual's block, each of a warp's two
+    uint32_t tmem;
+};
+constexpr int kBias = 2 * 256 * sizeof(float);
+constexpr int kHead = (static_cast<int>(sizeof(Vars)) + kBias + 1023) / 1024 * 1024;
 
 struct TcArgs {
     Finish f;
@@ -279,11 +288,11 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
             const __grid_constant__ CUtensorMap map_residual)
 {
-    extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[kRing], empty[kRing], done[2], taken[2];
-    __shared__ uint32_t tmem_slot;
-    __shared__ uint64_t came[kEpiWarps][2];     // a residual's block, each of a warp's two
-    const uint32_t pad = (1024 - (smem_addr(raw) & 1023)) & 1023;
+    extern __shared__ __align__(16) uint8_t raw[];
+    __shared__ Vars vars;
+    uint64_t *const full = vars.full, *const empty = vars.empty, *const done = vars.done, *const taken = vars.taken;
+    auto &came = vars.came;
+    const uint32_t pad = kBias + ((1024 - ((smem_addr(raw) + kBias) & 1023)) & 1023);
     const uint32_t ring = smem_addr(raw) + pad;
     const int rows_b = a.tile_n / CG;     // this CTA's share of B's rows
     const int stage_bytes = kBytesA + rows_b * kTerms * 2;
@@ -308,12 +317,12 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
     }
     if (warp == 2) {
         if constexpr (CG == 1) {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&vars.tmem)),
                          "r"(512u)
                          : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         } else {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&vars.tmem)),
                          "r"(512u)
                          : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -323,7 +332,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = vars.tmem;
     grid_dependency_wait();
 
     if (warp == 0 || warp == 3) {
@@ -456,9 +465,16 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
 #pragma unroll
                 for (int q = 0; q < 4; q++)
                     if (4 * lane + q < cols && n0 + 4 * lane + q < a.f.N) bias[q] = __ldg(a.f.bias + n0 + 4 * lane + q);
-            ok = wait_for(done + (i & 1), i >> 1 & 1, a.status);
+            ok = __all_sync(0xffffffffu, wait_for(done + (i & 1), i >> 1 & 1, a.status));
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            // the four warps of these columns write the same; none still reads what they held two tiles ago, which all had
+            // taken before this tile was begun
+            float4 *const columns = reinterpret_cast<float4 *>(raw) + (i & 1) * 64 + (e >> 2) * 32;
+            if (a.f.bias) {
+                columns[lane] = make_float4(bias[0], bias[1], bias[2], bias[3]);
+                __syncwarp();
+            }
             const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + (e >> 2) * cols;
             // a block's columns are asked for while the one before is worked on
             uint32_t v[SUBS][16];
@@ -472,12 +488,23 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
 #pragma unroll
                     for (int j = 0; j < 8; j++) z[q][j] = make_float2(__uint_as_float(v[q][2 * j]), __uint_as_float(v[q][2 * j + 1]));
                 }
-                if (b + 1 < blocks) {
+                if (b + 1 < blocks)
 #pragma unroll
                     for (int q = 0; q < SUBS; q++) tmem_load(acc + (b + 1) * BC + 16 * q, v[q]);
-                } else {
-                    // this warp's share of the tile is in registers
+                // (read by four columns: by shuffles, one a column, they took the data path of shared memory for 18 us of 368)
+                if (a.f.bias && b < live)
+#pragma unroll
+                    for (int q = 0; q < SUBS; q++)
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            const float4 c = columns[(b * BC + 16 * q) / 4 + j / 2];
+                            z[q][j] = __fadd2_rn(z[q][j], make_float2(c.x, c.y));
+                            z[q][j + 1] = __fadd2_rn(z[q][j + 1], make_float2(c.z, c.w));
+                        }
+                if (b + 1 == blocks) {
+                    // this warp's share of the tile is in registers, its bias read
                     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
                     if (lane == 0) {
                         if constexpr (CG == 1)
                             dev::mbar_arrive(taken + (i & 1));
@@ -491,15 +518,6 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                     blocks_read<0>();
                     fetch(b + 1, flip ^ 1);
                 }
-                if (a.f.bias)
-#pragma unroll
-                    for (int q = 0; q < SUBS; q++)
-#pragma unroll
-                        for (int j = 0; j < 8; j++) {
-                            const int from = (b * BC + 16 * q) / 4 + j / 2;
-                            z[q][j] = __fadd2_rn(z[q][j], make_float2(__shfl_sync(0xffffffffu, bias[j % 2 * 2], from),
-                                                                      __shfl_sync(0xffffffffu, bias[j % 2 * 2 + 1], from)));
-                        }
                 if (a.f.has_pre) {
                     uint8_t *block = out + (a.f.has_residual ? 2 : flip) * kBlockBytes;
                     if (lane == 0) blocks_read<1>();
@@ -612,11 +630,11 @@ template <class T, int ACT, int CG, int PAIRS>
 cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
 {
     const auto fn = k_linear_tc<T, ACT, CG, PAIRS>;
-    if (const cudaError_t e = shared_opt_in(reinterpret_cast<const void *>(fn), kSmem - kStatic)) return e;
+    if (const cudaError_t e = shared_opt_in(reinterpret_cast<const void *>(fn), kSmem - sizeof(Vars))) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CG * PAIRS * std::min<unsigned>(a.tiles, PAIRS == 2 ? kQuads : kSms / CG));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = 1024 + a.stages * static_cast<size_t>(kBytesA + a.tile_n / CG * kTerms * 2) +
+    cfg.dynamicSmemBytes = kHead - sizeof(Vars) + a.stages * static_cast<size_t>(kBytesA + a.tile_n / CG * kTerms * 2) +
                            static_cast<size_t>(kEpiWarps) * a.places * kBlockBytes;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
@@ -693,7 +711,7 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     const unsigned long long tiles = static_cast<unsigned long long>(a.tiles_m) * a.tiles_n * p.splits;
     if (tiles > 0x7fffffffull) return cudaErrorInvalidConfiguration;
     a.tiles = static_cast<unsigned>(tiles);
-    a.stages = std::min(kRing, (kSmem - kStatic - 1024 - kEpiWarps * a.places * kBlockBytes) / (kBytesA + p.tile_n / cg * kTerms * 2));
+    a.stages = std::min(kRing, (kSmem - kHead - kEpiWarps * a.places * kBlockBytes) / (kBytesA + p.tile_n / cg * kTerms * 2));
     a.a_turned = p.a.turned;
     a.b_turned = p.b.turned;
     const unsigned type = p.a.bf16 ? 1u : 0u;
