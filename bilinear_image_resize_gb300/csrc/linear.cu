@@ -467,11 +467,11 @@ Operand operand(const Laid &l, const uint8_t *workspace, bool turned)
 }
 
 // Tile width, CTAs of a tile and runs of a product, by an estimate in clocks of
-// what was measured: a stage (what reaches an SM from L2, 64 bytes a clock, bounds
-// it on every tile: 256 columns of a pair 690, 720 where both operands are turned and
-// 640 where two pairs then share one, of one CTA 780, narrower ones 560 to 590), a wave's beginning and end, and the join of runs, which pays for long sums
-// of few tiles (50000 pixels' gradient of a 64 x 64 weight: 211 us in one run, 18 in
-// 32; of 32768 pixels' 1024 x 1024 one: 162 and, in 4, 50).
+// what was measured (19456 x 1024, 1024 and 4096 terms): a stage of 64 terms takes 590
+// on 256 columns of a pair of CTAs and 320 on 128, 510 on 256 where two pairs share
+// an operand, 650, 390 and 335 on 256, 128 and 64 of one CTA; and the join of runs,
+// which pays for long sums of few tiles (50000 pixels' gradient of a 64 x 64 weight:
+// 211 us in one run, 18 in 32; of 32768 pixels' 1024 x 1024 one: 162 and, in 4, 50).
 struct Cut {
     int tile_n, pairs, splits;
     unsigned pitch;
@@ -496,7 +496,7 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool t
             const long long across = (N + tile - 1) / tile;
             if ((tile > 64 && N <= static_cast<unsigned>(tile) / 2) || (pairs && M <= 128)) continue;
             if (pairs == 2 && (!turned || tile < 256 || across % 2)) continue;
-            const double stage = tile < 256 ? (tile == 64 ? 560 : pairs ? 590 : 580) : pairs == 2 ? 640 : !pairs ? 780 : turned ? 720 : 690;
+            const double stage = tile == 64 ? 335 : tile == 128 ? (pairs ? 320 : 390) : pairs == 2 ? 510 : pairs ? 590 : 650;
             const int rows = pairs ? 256 : 128, slots = pairs == 2 ? kQuads : pairs ? kLinSms / 2 : kLinSms;
             const long long tiles = static_cast<long long>((M + rows - 1ull) / rows) * (pairs == 2 ? across / 2 : across);
             const auto consider = [&](long long want) {
@@ -504,9 +504,9 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool t
                 const long long run = (chunks + want - 1) / want;
                 const int splits = static_cast<int>((chunks + run - 1) / run);
                 const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
-                double t = waves * (run * products * stage + 2500) + 4.0 * tile;
+                double t = waves * (run * products * stage + 300) + 8.0 * tile + (pairs ? 1000 : 0);
                 const bool joined = splits > 1 || through;
-                if (joined) t += 6500 + of_split * splits + 4.0 * M * pitch / 2500.0;
+                if (joined) t += 4500 + of_split * splits + 4.0 * M * pitch / 2500.0;
                 if (!best.tile_n || t < least) {
                     least = t;
                     best = {tile, pairs, splits, pitch, joined ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
