@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
+#include <type_traits>
 #include <vector>
 
 #include "map_ops.h"
@@ -205,19 +206,27 @@ __device__ __forceinline__ void add_rows(const uint8_t *row, long long step, int
             for (int j = 0; j < VE; j++) s[j] += f[j];
         }
     }
-    if (count <= 0) return;
+    const auto rest = [&](auto size) {
+        constexpr int L = decltype(size)::value;
 #pragma unroll
-    for (int u = 0; u < B; u++) {
-        x[u] = __ldcs(reinterpret_cast<const V *>(row));
-        if (u + 1 < count) row += step;
-    }
+        for (int u = 0; u < L; u++) {
+            x[u] = __ldcs(reinterpret_cast<const V *>(row));
+            if (u + 1 < count) row += step;
+        }
 #pragma unroll
-    for (int u = 0; u < B; u++) {
-        unpack<T, VE>(x[u], f);
+        for (int u = 0; u < L; u++) {
+            unpack<T, VE>(x[u], f);
 #pragma unroll
-        for (int j = 0; j < VE; j++)
-            if (u < count) s[j] += f[j];
-    }
+            for (int j = 0; j < VE; j++)
+                if (u < count) s[j] += f[j];
+        }
+    };
+    // half a batch where that is enough: of loads of up to four bytes (of more, four of them wait as long as eight)
+    constexpr int R = VE * sizeof(T) <= 4 ? B / 2 : B;
+    if (R < B && count > R)
+        rest(std::integral_constant<int, B>{});
+    else if (count > 0)
+        rest(std::integral_constant<int, R>{});
 }
 
 // Gradient: a unit is one head, a tile of rows and keys, gx query columns and gn
@@ -352,10 +361,17 @@ __global__ void __launch_bounds__(kPbThreads) k_bias_fold(const __grid_constant_
     const float *from = a.dense + static_cast<long long>(head) * down * wide;
     float s = 0.0f;
     if (wide <= 8) {            // rows of a few offsets: one a lane
-        for (int r = lane; r < down; r += 32)
-            if (__ldg(a.g.lut[0] + r) == b0)
-                for (int c = 0; c < wide; c++)
-                    if (__ldg(a.g.lut[1] + c) == b1) s += from[static_cast<long long>(r) * wide + c];
+        unsigned mine = 0;
+        for (int c = 0; c < wide; c++) mine |= (__ldg(a.g.lut[1] + c) == b1 ? 1u : 0u) << c;
+        for (; mine; mine &= mine - 1) {
+            const float *column = from + __ffs(mine) - 1;
+#pragma unroll 8
+            for (int r = lane; r < down; r += 32) {
+                // read whether it is the bucket's or not: a load under a condition waits for the one before it
+                const float v = column[static_cast<long long>(r) * wide];
+                s += __ldg(a.g.lut[0] + r) == b0 ? v : 0.0f;
+            }
+        }
     } else {
         // the bucket's rows, four of them asked for at once (past the last that one again, and not added)
         for (int c0 = 0; c0 < wide; c0 += 32) {
@@ -485,6 +501,12 @@ void pb_plan_grad(PbArgs &a)
     const int split = static_cast<int>(std::clamp<long long>(want / (units() * a.ngx), 1, a.g.N));
     a.gn = ceil_div(a.g.N, split);
     a.ngn = ceil_div(a.g.N, a.gn);
+    // long sequences of few heads: fewer query rows a unit (2 x 8 heads of 4096 to 4096: 440 us, in units
+    // of 2048 rows 4900)
+    while (units() * a.ngx * a.ngn < want / 2 && a.tq > 32) {
+        a.tq = (a.tq + 1) / 2;
+        pb_count(a);
+    }
 }
 
 long long pb_units(const PbArgs &a) { return static_cast<long long>(a.nk) * a.nx * a.ngx * a.nq * a.ngn * a.g.heads; }
