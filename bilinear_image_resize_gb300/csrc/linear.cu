@@ -275,7 +275,9 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Joi
 // no tile is staged.  A warp takes two columns of the result, its lanes the terms, a
 // vector of each at a time; `share` warps of a CTA share a column pair's terms where
 // there are few of them.  Up to ROWS rows of x (blockIdx.y counts them off) meet
-// each vector of the weight.
+// each vector of the weight.  One row, 4096 x 1024 bf16: 2.8 us in a stream of calls
+// that leave the weight in L2, 4 from DRAM (2.1 TB/s): a launch and one chain of loads
+// and shuffles.
 struct RowsArgs {
     Rows x, w;
     Finish f;
@@ -468,20 +470,19 @@ Operand operand(const Laid &l, const uint8_t *workspace, bool turned)
 
 // Tile width, CTAs of a tile and runs of a product, by an estimate in clocks of
 // what was measured (19456 x 1024, 1024 and 4096 terms): a stage of 64 terms takes 590
-// on 256 columns of a pair of CTAs and 320 on 128, 510 on 256 where two pairs share
-// an operand, 650, 390 and 335 on 256, 128 and 64 of one CTA; and the join of runs,
-// which pays for long sums of few tiles (50000 pixels' gradient of a 64 x 64 weight:
-// 211 us in one run, 18 in 32; of 32768 pixels' 1024 x 1024 one: 162 and, in 4, 50).
+// on 256 columns of a pair of CTAs and 320 on 128, 650, 390 and 335 on 256, 128 and
+// 64 of one CTA; and the join of runs, which pays for long sums of few tiles (50000
+// pixels' gradient of a 64 x 64 weight: 211 us in one run, 18 in 32; of 32768 pixels'
+// 1024 x 1024 one: 162 and, in 4, 50).
 struct Cut {
-    int tile_n, pairs, splits;
+    int tile_n, pair, splits;
     unsigned pitch;
     size_t bytes;
 };
 // through: a single run goes through the workspace as well.  A run is as long as its
 // accumulator's cut sums allow, n 1e-9 for n terms: float32 inputs 768 (8e-7, about
 // what float32 arithmetic leaves), 16-bit ones 2048 for a float32 result, else 16384.
-// turned: both operands are.
-Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool through, bool turned)
+Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool through)
 {
     const long long chunks = (terms + 63) / 64;
     const int products = dtype == RZ_F32 ? 6 : 1;
@@ -491,25 +492,24 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool t
     double least = 0.0;
     const unsigned pitch = static_cast<unsigned>(up(N, 8));
     const double of_split = 170.0 + 4.0 * M * pitch / 2500.0;
-    for (int pairs = 0; pairs < 3; pairs++)
-        for (int tile = 256; tile >= (pairs ? 128 : 64); tile /= 2) {
+    for (int pair = 0; pair < 2; pair++)
+        for (int tile = 256; tile >= (pair ? 128 : 64); tile /= 2) {
             const long long across = (N + tile - 1) / tile;
-            if ((tile > 64 && N <= static_cast<unsigned>(tile) / 2) || (pairs && M <= 128)) continue;
-            if (pairs == 2 && (!turned || tile < 256 || across % 2)) continue;
-            const double stage = tile == 64 ? 335 : tile == 128 ? (pairs ? 320 : 390) : pairs == 2 ? 510 : pairs ? 590 : 650;
-            const int rows = pairs ? 256 : 128, slots = pairs == 2 ? kQuads : pairs ? kLinSms / 2 : kLinSms;
-            const long long tiles = static_cast<long long>((M + rows - 1ull) / rows) * (pairs == 2 ? across / 2 : across);
+            if ((tile > 64 && N <= static_cast<unsigned>(tile) / 2) || (pair && M <= 128)) continue;
+            const double stage = tile == 64 ? 335 : tile == 128 ? (pair ? 320 : 390) : pair ? 590 : 650;
+            const int rows = pair ? 256 : 128, slots = pair ? kLinSms / 2 : kLinSms;
+            const long long tiles = static_cast<long long>((M + rows - 1ull) / rows) * across;
             const auto consider = [&](long long want) {
                 want = std::min<long long>(std::max<long long>(want, fewest), chunks);
                 const long long run = (chunks + want - 1) / want;
                 const int splits = static_cast<int>((chunks + run - 1) / run);
                 const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
-                double t = waves * (run * products * stage + 300) + 8.0 * tile + (pairs ? 1000 : 0);
+                double t = waves * (run * products * stage + 300) + 8.0 * tile + (pair ? 1000 : 0);
                 const bool joined = splits > 1 || through;
                 if (joined) t += 4500 + of_split * splits + 4.0 * M * pitch / 2500.0;
                 if (!best.tile_n || t < least) {
                     least = t;
-                    best = {tile, pairs, splits, pitch, joined ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
+                    best = {tile, pair, splits, pitch, joined ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
                 }
             };
             consider(fewest);
@@ -616,7 +616,7 @@ cudaError_t product(const Operand &a, const Operand &b, const Finish &f, int out
     p.part = c.bytes ? part : nullptr;
     p.part_pitch = c.pitch;
     p.tile_n = c.tile_n;
-    p.pairs = c.pairs;
+    p.pair = c.pair;
     p.status = status;
     cudaError_t e = launch_product(p, stream);
     if (e != cudaSuccess || !c.bytes) return e;
@@ -642,7 +642,10 @@ Finish finish_of(const Rows &out, unsigned M, unsigned N, int dtype, const Rows 
     return f;
 }
 
-// Whether a call of M rows is k_linear_rows's, which reads the weight once for eight of them.
+// Whether a call of M rows is k_linear_rows's, which reads the weight once for eight of
+// them.  K x C, rows / tiles in us: 16-bit, 16 rows, 256 x 256 2.2 / 3.2, 1024 x 1024 3.7 / 5.4,
+// 4096 x 1024 11.5 / 7.0; 32 rows 2.4 / 3.2, 6.7 / 5.6, 20.6 / 6.5; float32, 16 rows 2.7 /
+// 8.2, 6.1 / 11.1, 14.5 / 22.6; 32 rows 2.7 / 8.2, 10.9 / 10.1, 25.3 / 17.3.
 bool is_few(unsigned M, unsigned N, unsigned C, int dtype)
 {
     const double read = static_cast<double>((M + 7) / 8) * N * C;
@@ -681,10 +684,11 @@ cudaError_t few_rows(const Rows &x, const Rows &w, const Finish &f, unsigned C, 
         return reinterpret_cast<uintptr_t>(r.v.p) % 16 == 0 && r.v.pitch % 16 == 0 && r.v.bstride % 16 == 0 && (!r.HW || r.bytes % 16 == 0);
     };
     const bool wide = C * es % 16 == 0 && aligned(x) && aligned(w);
-    // warps until there are sixteen an SM, but at least two vectors a lane
+    // warps until there are sixteen an SM, but at least a vector a lane (one row, 1, 2, 4 and 8 warps: 1024 x 4096 5.8, 3.9, 3.1
+    // and 2.8 us; 1024 x 1024 2.4, 2.1, 1.9 and 1.9; 4096 x 1024 3.0, 2.8, 3.8 and 4.7; 256 x 256 1.4, 1.6, 1.6 and 1.6)
     const unsigned vecs = wide ? static_cast<unsigned>(C * es / 16) : C;
     a.share = 1;
-    while (a.share < 8 && (f.N + 1) / 2 * a.share < 16 * kLinSms && vecs >= 128u * a.share) a.share *= 2;
+    while (a.share < 8 && (f.N + 1) / 2 * a.share < 16 * kLinSms && vecs >= 64u * a.share) a.share *= 2;
     if (dtype == RZ_F32) return rows_of_type<float>(a, wide, stream);
     return dtype == RZ_BF16 ? rows_of_type<__nv_bfloat16>(a, wide, stream) : rows_of_type<__half>(a, wide, stream);
 }
@@ -711,7 +715,7 @@ Forward plan_forward(const rz_linear *d, const LinPlan &p, const rz_map *x, cons
     f.x = lay(rows_of(x, p.x), p.P, C, d->dtype, false);
     f.w = lay(rows_of(weight, weight_pitch), K, C, d->dtype, false);
     if (f.few) return f;
-    f.c = cut(p.P, K, C, d->dtype, d->dtype, !direct_out(f.out, d->dtype), false);
+    f.c = cut(p.P, K, C, d->dtype, d->dtype, !direct_out(f.out, d->dtype));
     f.w.at = up(f.x.bytes, 256);
     f.part = f.w.at + up(f.w.bytes, 256);
     f.total = f.part + f.c.bytes;
@@ -739,11 +743,11 @@ Backward plan_backward(const rz_linear *d, const LinPlan &p, const rz_map *dy, c
     if (!dx) b.w.bytes = 0;
     if (dx) {
         b.dx = finish_of(rows_of(dx, p.x), p.P, C, d->dtype, nullptr, nullptr);
-        b.cx = cut(p.P, C, K, d->dtype, d->dtype, !direct_out(b.dx, d->dtype), false);
+        b.cx = cut(p.P, C, K, d->dtype, d->dtype, !direct_out(b.dx, d->dtype));
     }
     if (dweight) {
         b.dw = finish_of(rows_of(dweight, dweight_pitch), K, C, dweight_dtype, nullptr, nullptr);
-        b.cw = cut(K, C, p.P, d->dtype, dweight_dtype, !direct_out(b.dw, dweight_dtype), true);
+        b.cw = cut(K, C, p.P, d->dtype, dweight_dtype, !direct_out(b.dw, dweight_dtype));
     }
     b.chunks = pack_chunks(p.P, K);
     b.x.at = up(b.dz.bytes, 256);

@@ -157,8 +157,6 @@ __device__ __forceinline__ void bias_of(const Finish &f, unsigned n, float2 (&b)
         b[i] = f.bias ? make_float2(__ldg(f.bias + n + 2 * i), __ldg(f.bias + n + 2 * i + 1)) : both(0.0f);
 }
 
-constexpr int kQuads = 36;      // clusters of four CTAs that a GPU holds at once; more than that would only wait
-
 // One operand of a product on the tensor cores: its rows (M or N of the product)
 // and the terms of the sum, 16-bit, in `planes` matrices one after another.
 struct Operand {
@@ -182,7 +180,7 @@ struct Product {
     float *part;
     unsigned part_pitch;    // floats
     int tile_n;             // 64 (without a pair), 128 or 256
-    int pairs;              // 0: a CTA works on a tile of 128 rows; 1: a pair on one of 256; 2: two pairs on two that share A's rows
+    int pair;               // two CTAs work on a tile of 256 rows, else one on 128
     int *status;
 };
 bool direct_out(const Finish &f, int dtype);

@@ -1,17 +1,22 @@
 // The linear layer's products on the fifth-generation tensor cores.
 //
-// A CTA computes 128 x tile_n of D = A B^T, 64 terms at a time: two threads ask
+// A CTA computes 128 x tile_n of D = A B^T, 64 terms at a time: two warps ask
 // for the operands' tiles by TMA, into a ring of stages in the 128-byte swizzle;
-// one thread issues four tcgen05.mma (16 terms each) a stage, accumulating in
-// tensor memory; eight warps take finished tiles out of it.  Tensor memory holds
+// one warp issues four tcgen05.mma (16 terms each) a stage, accumulating in
+// tensor memory; eight warps take finished tiles out of it.  The first three run
+// whole, with one elected lane for the requests, so that addresses and descriptors
+// stay in uniform registers: by one thread in a branch of its own the issue took as
+// long as the products, and longer under a busy epilogue (65536 x 1024 x 4096 with
+// bias and GELU: 400 us, 368 so).  Tensor memory holds
 // two tiles, so that one is stored while the next is computed.  A pair of CTAs
-// computes 256 x tile_n, each with its half of A's rows and of B's; two pairs next to
-// each other may share A, each of their CTAs loading half of what it needs for both
-// (multicast), which pays where both operands are turned: their boxes cost L2 more,
-// and in a sustained run power (8192^3: 660 against 540 us; products by rows of A are
-// the same either way or lose the SMs that no cluster of four reaches).  CTAs are
+// computes 256 x tile_n, each with its half of A's rows and of B's.  CTAs are
 // persistent and take tiles in turn, those of one row of tiles next to each
 // other, so that their rows of A come from L2.
+//
+// What bounds it: products of 65536 x 1024 x 4096 (bf16) run at the power limit,
+// 1530 to 1690 TFLOP/s (325 us sustained, 294 alone; with bias and GELU 354 and 303), a
+// stage in 530 clocks of the 512 that its products take; a short call by its launch,
+// first stages and last epilogue, about 5 us.
 //
 // An operand may be stored by rows of the product (its terms packed) or by terms
 // (its rows packed, as W in dz W and both in dz^T x): the matrix descriptors say
@@ -92,16 +97,6 @@ __device__ __forceinline__ void load_box(const CUtensorMap *map, uint32_t to, ui
                      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(plane), "r"(bar)
                      : "memory");
 }
-// The same into the places of every CTA of the mask, counted by the first CTA of each
-// one's pair.
-__device__ __forceinline__ void load_shared_box(const CUtensorMap *map, uint32_t to, uint32_t bar, int x, int y, int z, int plane,
-                                                uint16_t mask)
-{
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 "
-                 "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(to),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(plane), "r"(bar), "h"(mask)
-                 : "memory");
-}
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
 {
     uint32_t r;
@@ -143,9 +138,9 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
                      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
                      : "memory");
 }
-// One arrival at the barrier (of a pair: at those of the CTAs of `mask`) once the products so far are done.
+// One arrival at the barrier (of a pair: at both CTAs') once the products so far are done.
 template <int CG>
-__device__ __forceinline__ void commit(uint64_t *bar, uint16_t mask)
+__device__ __forceinline__ void commit(uint64_t *bar)
 {
     if constexpr (CG == 1)
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
@@ -153,7 +148,7 @@ __device__ __forceinline__ void commit(uint64_t *bar, uint16_t mask)
     else
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
                          smem_addr(bar)),
-                     "h"(mask)
+                     "h"(static_cast<uint16_t>(3))
                      : "memory");
 }
 
@@ -255,15 +250,14 @@ struct Tile {
     unsigned m, n, run;
     int first, last, stages;
 };
-template <int PAIRS>
-__device__ __forceinline__ Tile tile_at(const TcArgs &a, unsigned t, uint32_t pair)
+__device__ __forceinline__ Tile tile_at(const TcArgs &a, unsigned t)
 {
     Tile r;
     const unsigned all = a.tiles_m * a.tiles_n, x = t % all, per = a.group * a.tiles_n;
     const unsigned g = x / per, y = x - g * per, rows = min(a.group, a.tiles_m - g * a.group);
     r.run = t / all;
     r.m = g * a.group + y % rows;
-    r.n = y / rows * PAIRS + pair;
+    r.n = y / rows;
     r.first = static_cast<int>(r.run) * a.run;
     r.last = min(a.chunks, r.first + a.run);
     r.stages = (r.last - r.first) * (a.planes == 1 ? 1 : 6);
@@ -282,7 +276,7 @@ __device__ __forceinline__ void planes_of(int planes, int j, int &a, int &b)
     b = 0x010210 >> (4 * j) & 0xf;
 }
 
-template <class T, int ACT, int CG, int PAIRS>
+template <class T, int ACT, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
@@ -296,17 +290,15 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
     const uint32_t ring = smem_addr(raw) + pad;
     const int rows_b = a.tile_n / CG;     // this CTA's share of B's rows
     const int stage_bytes = kBytesA + rows_b * kTerms * 2;
-    // place in the cluster, and in the pair; the pair's first CTA
-    uint32_t place = 0;
-    if constexpr (CG == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(place));
-    const uint32_t rank = place & 1, leader = place & ~1u, pair = place >> 1;
-    const unsigned first_tile = blockIdx.x / (CG * PAIRS), tile_step = gridDim.x / (CG * PAIRS);
+    uint32_t rank = 0;
+    if constexpr (CG == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const unsigned first_tile = blockIdx.x / CG, tile_step = gridDim.x / CG;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     grid_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; i++) {
             dev::mbar_init(full + i, 1);
-            dev::mbar_init(empty + i, PAIRS);
+            dev::mbar_init(empty + i, 1);
         }
         for (int i = 0; i < 2; i++) {
             dev::mbar_init(done + i, 1);
@@ -336,22 +328,21 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
     grid_dependency_wait();
 
     if (warp == 0 || warp == 3) {
-        // warp 0 asks for A's tiles, warp 3 for B's: one thread for both spends longer on a stage's requests than the
-        // products take (its waits for a free stage were a fifth of its time)
+        // warp 0 asks for A's tiles, warp 3 for B's: one for both spends longer on a stage's requests than the products
+        // take (its waits for a free stage were a fifth of its time)
         {
             const bool of_b = warp == 3;
             const CUtensorMap *map = of_b ? &map_b : &map_a;
             const int turned = of_b ? a.b_turned : a.a_turned, merged = of_b ? a.b_merged : a.a_merged;
             const int rows = of_b ? rows_b : kTileM;
             const uint32_t to = ring + (of_b ? kBytesA : 0);
-            const uint32_t bars = CG == 1 ? smem_addr(full) : in_cta(smem_addr(full), leader);
-            const uint16_t both_pairs = static_cast<uint16_t>(5u << rank);
+            const uint32_t bars = CG == 1 ? smem_addr(full) : in_cta(smem_addr(full), 0);
             int s = 0;
             uint32_t phase = 0;
             bool ok = true;
             unsigned asked = 0;
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step) {
-                const Tile w = tile_at<PAIRS>(a, t, pair);
+                const Tile w = tile_at(a, t);
                 const int row = of_b ? static_cast<int>(w.n * a.tile_n + rank * rows_b) : static_cast<int>((w.m * CG + rank) * kTileM);
                 int j = 0, k0 = w.first * kTerms, pa, pb;
                 planes_of(a.planes, j, pa, pb);
@@ -362,9 +353,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                     const int plane = of_b ? pb : pa;
                     if (elected()) {
                         if (!of_b && rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
-                        if (PAIRS == 2 && !of_b)  // turned; this pair's half of the rows, for both
-                            load_shared_box(map, at + pair * 8192, bar, row + pair * 64, k0, 0, plane, both_pairs);
-                        else if (!turned)
+                        if (!turned)
                             load_box<CG>(map, at, bar, k0, row, 0, plane);
                         else if (merged)
                             load_box<CG>(map, at, bar, 0, k0, row / 64, plane);
@@ -401,7 +390,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             const uint64_t desc_a = tile_desc(ring, a.a_turned), desc_b = tile_desc(ring + kBytesA, a.b_turned);
             const uint32_t step_a = (a.a_turned ? 2048 : 32) >> 4, step_b = (a.b_turned ? 2048 : 32) >> 4;
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
-                const Tile w = tile_at<PAIRS>(a, t, pair);
+                const Tile w = tile_at(a, t);
                 const uint32_t acc = tmem + (i & 1) * 256;
                 ok = __all_sync(0xffffffffu, wait_for(taken + (i & 1), (i >> 1 & 1) ^ 1, a.status));
                 if (!ok) break;
@@ -410,13 +399,14 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                     ok = __all_sync(0xffffffffu, wait_for(full + s, phase, a.status));
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t at = static_cast<uint32_t>(s * stage_bytes) >> 4;   // the ring lies below 2^18: no carry leaves the address
+                    // the ring lies below 2^18: no carry leaves the address
+                    const uint32_t at = static_cast<uint32_t>(s * stage_bytes) >> 4;
                     const uint64_t da = desc_a + at, db = desc_b + at;
                     if (elected()) {
 #pragma unroll
                         for (uint32_t k = 0; k < kTerms / 16; k++)
                             mma<CG>(acc, da + k * step_a, db + k * step_b, a.idesc, c > 0 || k > 0);
-                        commit<CG>(empty + s, PAIRS == 2 ? 15 : 3);
+                        commit<CG>(empty + s);
                     }
                     __syncwarp();
                     if (++s == a.stages) {
@@ -424,7 +414,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                         phase ^= 1;
                     }
                 }
-                if (ok && elected()) commit<CG>(done + (i & 1), static_cast<uint16_t>(3u << leader));
+                if (ok && elected()) commit<CG>(done + (i & 1));
                 __syncwarp();
             }
         }
@@ -442,7 +432,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
         unsigned i = 0;
         bool ok = true;
         for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
-            const Tile w = tile_at<PAIRS>(a, t, pair);
+            const Tile w = tile_at(a, t);
             const unsigned m0 = (w.m * CG + rank) * kTileM + 32 * quarter, n0 = w.n * a.tile_n + (e >> 2) * cols;
             const int live = m0 < a.f.M && n0 < a.f.N ? min(blocks, static_cast<int>((a.f.N - n0 + BC - 1) / BC)) : 0;
             const auto fetch = [&](int b, int place) {
@@ -509,7 +499,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                         if constexpr (CG == 1)
                             dev::mbar_arrive(taken + (i & 1));
                         else
-                            arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), leader));
+                            arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), 0));
                     }
                 }
                 if (b >= live) continue;
@@ -626,13 +616,13 @@ struct Maps {
     CUtensorMap a, b, out, pre, residual;
 };
 
-template <class T, int ACT, int CG, int PAIRS>
+template <class T, int ACT, int CG>
 cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
 {
-    const auto fn = k_linear_tc<T, ACT, CG, PAIRS>;
+    const auto fn = k_linear_tc<T, ACT, CG>;
     if (const cudaError_t e = shared_opt_in(reinterpret_cast<const void *>(fn), kSmem - sizeof(Vars))) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CG * PAIRS * std::min<unsigned>(a.tiles, PAIRS == 2 ? kQuads : kSms / CG));
+    cfg.gridDim = dim3(CG * std::min<unsigned>(a.tiles, kSms / CG));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kHead - sizeof(Vars) + a.stages * static_cast<size_t>(kBytesA + a.tile_n / CG * kTerms * 2) +
                            static_cast<size_t>(kEpiWarps) * a.places * kBlockBytes;
@@ -641,7 +631,7 @@ cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG * PAIRS;
+    attr[1].val.clusterDim.x = CG;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 1 ? 1 : 2;
@@ -651,14 +641,13 @@ cudaError_t tc_launch(const TcArgs &a, const Maps &m, void *stream)
 template <class T, int CG>
 cudaError_t tc_launch_act(const TcArgs &a, const Maps &m, void *stream)
 {
-    if (a.f.act == RZ_ACT_SILU) return tc_launch<T, RZ_ACT_SILU, CG, 1>(a, m, stream);
-    return a.f.act == RZ_ACT_GELU ? tc_launch<T, RZ_ACT_GELU, CG, 1>(a, m, stream) : tc_launch<T, RZ_ACT_NONE, CG, 1>(a, m, stream);
+    if (a.f.act == RZ_ACT_SILU) return tc_launch<T, RZ_ACT_SILU, CG>(a, m, stream);
+    return a.f.act == RZ_ACT_GELU ? tc_launch<T, RZ_ACT_GELU, CG>(a, m, stream) : tc_launch<T, RZ_ACT_NONE, CG>(a, m, stream);
 }
 template <class T>
-cudaError_t tc_launch_of(const TcArgs &a, const Maps &m, int pairs, void *stream)
+cudaError_t tc_launch_of(const TcArgs &a, const Maps &m, int pair, void *stream)
 {
-    if (pairs == 2) return tc_launch<T, RZ_ACT_NONE, 2, 2>(a, m, stream);
-    return pairs ? tc_launch_act<T, 2>(a, m, stream) : tc_launch_act<T, 1>(a, m, stream);
+    return pair ? tc_launch_act<T, 2>(a, m, stream) : tc_launch_act<T, 1>(a, m, stream);
 }
 
 }  // namespace
@@ -675,12 +664,10 @@ bool lin::direct_out(const Finish &f, int dtype)
 cudaError_t lin::launch_product(const Product &p, void *stream)
 {
     if (!encoder()) return cudaErrorNotSupported;
-    const int cg = p.pairs ? 2 : 1;
+    const int cg = p.pair ? 2 : 1;
     Maps m;
     TcArgs a{};
-    if (p.pairs == 2 && (!p.a.turned || p.f.act != RZ_ACT_NONE)) return cudaErrorInvalidValue;
-    if (!encode(p.a, p.pairs == 2 ? kTileM / 2 : kTileM, &m.a, &a.a_merged) || !encode(p.b, p.tile_n / cg, &m.b, &a.b_merged))
-        return cudaErrorInvalidValue;
+    if (!encode(p.a, kTileM, &m.a, &a.a_merged) || !encode(p.b, p.tile_n / cg, &m.b, &a.b_merged)) return cudaErrorInvalidValue;
     a.f = p.f;
     int dtype = p.out_dtype;
     if (p.part) {
@@ -700,7 +687,6 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     a.tile_n = p.tile_n;
     a.tiles_m = (p.f.M + cg * kTileM - 1) / (cg * kTileM);
     a.tiles_n = (p.f.N + p.tile_n - 1) / p.tile_n;
-    if (p.pairs == 2) a.tiles_n = (a.tiles_n + 1) / 2;
     a.planes = p.a.planes;
     // Tiles of a row next to each other read its A at once, and B out of L2 where that holds it (65536 x 1024 x 4096: 341 us,
     // rows of tiles in groups of eight 373).  A larger B is read once for eight rows of tiles (8192 x 8192 x 8192: 611 us, by
@@ -716,10 +702,11 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     a.b_turned = p.b.turned;
     const unsigned type = p.a.bf16 ? 1u : 0u;
     a.idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<unsigned>(p.a.turned) << 15) |
-              (static_cast<unsigned>(p.b.turned) << 16) | (static_cast<unsigned>(p.tile_n >> 3) << 17) | (static_cast<unsigned>(cg * kTileM >> 4) << 24);
+              (static_cast<unsigned>(p.b.turned) << 16) | (static_cast<unsigned>(p.tile_n >> 3) << 17) |
+              (static_cast<unsigned>(cg * kTileM >> 4) << 24);
     a.status = p.status;
-    if (dtype == RZ_F32) return tc_launch_of<float>(a, m, p.pairs, stream);
-    return dtype == RZ_BF16 ? tc_launch_of<__nv_bfloat16>(a, m, p.pairs, stream) : tc_launch_of<__half>(a, m, p.pairs, stream);
+    if (dtype == RZ_F32) return tc_launch_of<float>(a, m, p.pair, stream);
+    return dtype == RZ_BF16 ? tc_launch_of<__nv_bfloat16>(a, m, p.pair, stream) : tc_launch_of<__half>(a, m, p.pair, stream);
 }
 
 }  // namespace rz

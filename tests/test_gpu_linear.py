@@ -169,7 +169,8 @@ def test_residual_in_place(rz, shape, K, dtype):
 # sums over many pixels, many terms, and more tiles than there are processors
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape, K", [((1, 64, 160, 24), 40), ((1, 5, 50, 4096), 72), ((2, 96, 100, 136), 328), ((2, 64, 65, 520), 520),
-                                      ((1, 60, 70, 1030), 264), ((1, 40, 50, 640), 1000)])
+                                      ((1, 60, 70, 1030), 264), ((1, 40, 50, 640), 1000), ((1, 50, 60, 512), 512),
+                                      ((1, 30, 40, 1024), 1024)])
 def test_larger(rz, shape, K, dtype):
     forward(rz, shape, K, dtype, "silu", residual=True, pre=True)
     gradient(rz, shape, K, dtype, "gelu")
