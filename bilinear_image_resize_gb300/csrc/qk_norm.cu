@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kQkThreads, NV == 1 ? 4 : 1) k_qk_norm(const _
 // kind.  A step's vectors are copied into places in shared memory that only their
 // lane reads, kQkAhead steps before they are used, across tokens: in registers the
 // four vectors of two steps left 16 warps an SM waiting a memory's latency for
-// each (16 x 37 x 50 tokens of 20 heads of 128, f16: 106 us).
+// each (16 x 37 x 50 tokens of 20 heads of 128, f16: 106 us; so 85 us, 5.3 TB/s).
 constexpr int kQkAhead = 3;
 
 template <class T, int VE, int NV, bool INTER>

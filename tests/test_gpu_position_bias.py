@@ -116,13 +116,13 @@ LAYOUTS = [dict(pad=16), dict(gap=64), dict(pad=7), dict(offset=1), dict(pad=3, 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("N, query, key", [(2, (5, 8), (5, 8)), (9, (3, 3), (3, 3)), (2, (1, 20), (1, 33))])
+@pytest.mark.parametrize("N, query, key", [(2, (5, 8), (5, 8)), (9, (3, 3), (3, 3)), (2, (1, 20), (1, 33)), (60, (3, 3), (3, 3))])
 def test_layouts(rz, layout, dtype, N, query, key):
     both(rz, N, 2, query, key, dtype, layout=layout)
     both(rz, N, 2, query, key, dtype, layout=layout, in_place=True)
 
 
-@pytest.mark.parametrize("N", [1, 9])
+@pytest.mark.parametrize("N", [1, 9, 60])
 def test_scores_that_begin_elsewhere_in_their_vectors(rz, N):
     query = key = (5, 8)
     rule = (4, 6, 20)
@@ -135,7 +135,7 @@ def test_scores_that_begin_elsewhere_in_their_vectors(rz, N):
     assert np.all(np.abs(ref.host(out) - want) <= ref.stored(want, 2.0 ** -24 * np.abs(want), "bf16"))
 
 
-@pytest.mark.parametrize("N", [1, 9])
+@pytest.mark.parametrize("N", [1, 9, 40])
 def test_buckets_outside_the_table_have_no_bias(rz, N):
     rng = np.random.default_rng(3)
     rows, cols = rng.integers(-3, 14, 6 + 5 - 1), rng.integers(-3, 14, 4 + 7 - 1)

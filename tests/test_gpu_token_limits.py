@@ -123,7 +123,7 @@ def test_qk_norm_of_images_far_apart(rz):
 
 
 @pytest.mark.parametrize("rows_apart", [False, True])
-@pytest.mark.parametrize("N", [1, 9])
+@pytest.mark.parametrize("N", [1, 9, 40])
 def test_position_bias_of_matrices_far_apart(rz, N, rows_apart):
     query, key, heads, R = (5, 8), (5, 8), 3, 11
     rule = (4, 6, 20)
