@@ -14,7 +14,7 @@
 // other, so that their rows of A come from L2.
 //
 // What bounds it: products of 65536 x 1024 x 4096 (bf16) run at the power limit,
-// 1530 to 1690 TFLOP/s (325 us sustained, 294 alone; with bias and GELU 354 and 303), a
+// 1550 to 1690 TFLOP/s (325 us sustained, 294 alone; with bias and GELU 354 and 303), a
 // stage in 530 clocks of the 512 that its products take; a short call by its launch,
 // first stages and last epilogue, about 5 us.
 //

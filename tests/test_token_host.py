@@ -111,13 +111,13 @@ def test_linear_grad_refuses(lib, nat):
 def test_qk_norm_refuses(lib, nat):
     good = dict(N=2, H=4, W=4, C=96, out_C=64, q_heads=1, k_heads=1, D=32, dtype=2, row_pairs=8, col_pairs=8, interleaved=0, eps=1e-6,
                 base=100.0, scale=1.0)
-    x, y = nat.RzMap(1 << 20, 768, 3072), nat.RzMap(1 << 21, 512, 2048)
+    x, y = nat.RzMap(1 << 20, 768, 3840), nat.RzMap(1 << 21, 512, 2048)
     n, ws = ctypes.c_size_t(7), 1 << 30
 
     def call(x=x, y=y, gq=None, gk=None, at=None, **change):
         return lib.map_qk_norm(nat.RzQk(**{**good, **change}), x, y, gq, gk, at, None)
 
-    def grad(dy=y, x=x, dx=nat.RzMap(1 << 22, 768, 3072), gq=None, gk=None, at=None, dq=1 << 23, dk=None, work=ws, size=1 << 30, **change):
+    def grad(dy=y, x=x, dx=nat.RzMap(1 << 22, 768, 3840), gq=None, gk=None, at=None, dq=1 << 23, dk=None, work=ws, size=1 << 30, **change):
         return lib.map_qk_norm_grad(nat.RzQk(**{**good, **change}), dy, x, dx, gq, gk, at, dq, dk, work, size, None)
 
     inf, nan = float("inf"), float("nan")
@@ -125,7 +125,7 @@ def test_qk_norm_refuses(lib, nat):
                    dict(C=63), dict(out_C=63), dict(row_pairs=-1), dict(col_pairs=-1), dict(row_pairs=9), dict(row_pairs=17, col_pairs=0),
                    dict(eps=-1.0), dict(eps=nan), dict(eps=inf), dict(base=0.0), dict(base=-2.0), dict(base=inf), dict(base=nan),
                    dict(scale=inf), dict(scale=nan), dict(dtype=0), dict(dtype=5), dict(N=-1), dict(q_heads=1 << 30),
-                   dict(x=None), dict(x=nat.RzMap(1 << 20, 766, 3072)), dict(x=nat.RzMap((1 << 20) + 1, 768, 3072)), dict(gq=2), dict(gk=1), dict(at=4)):
+                   dict(x=None), dict(x=nat.RzMap(1 << 20, 766, 3840)), dict(x=nat.RzMap((1 << 20) + 1, 768, 3840)), dict(gq=2), dict(gk=1), dict(at=4)):
         assert call(**change) == ARG and grad(**change) == ARG, change
     assert call(y=None) == ARG and call(y=nat.RzMap((1 << 20) + 64, 512, 2048)) == ARG
     assert call(y=x) == ARG                       # the same place, but other channels
@@ -133,7 +133,7 @@ def test_qk_norm_refuses(lib, nat):
     assert call(x=nat.RzMap(1 << 40, 1024, 1 << 18), y=nat.RzMap(1 << 50, 1024, 1 << 18), **many) == UNSUPPORTED
     assert lib.map_qk_norm_grad_workspace(nat.RzQk(**good), None) == ARG and lib.map_qk_norm_grad_workspace(None, ctypes.byref(n)) == ARG
     assert lib.map_qk_norm_grad_workspace(nat.RzQk(**good), ctypes.byref(n)) == 0 and n.value >= 4 * 2 * 32
-    for change in (dict(dy=None), dict(dx=None), dict(dx=x), dict(dx=nat.RzMap((1 << 21) + 64, 768, 3072)), dict(dq=2), dict(dk=6),
+    for change in (dict(dy=None), dict(dx=None), dict(dx=x), dict(dx=nat.RzMap((1 << 21) + 64, 768, 3840)), dict(dq=2), dict(dk=6),
                    dict(work=None), dict(work=ws + 8), dict(size=16)):
         assert grad(**change) == ARG, change
     assert call(N=0, x=None, y=None) == 0 and grad(N=0, dy=None, x=None, dx=None, dq=None, work=None, size=0) == 0
