@@ -22,7 +22,8 @@ SOURCES = ["kernels.cu", "stream.cu", "direct.cu", "filter.cu", "texture.cu", "m
            "gn_passes_f16.cu", "map_dropout.cu", "resize_map.cu",
            "linear.cu", "linear_tc.cu", "qk_norm.cu", "position_bias.cu"]
 HEADERS = [os.path.join(CSRC, "rz_internal.h"), os.path.join(CSRC, "rz_device.h"), os.path.join(CSRC, "map_ops.h"),
-           os.path.join(CSRC, "gn_device.h"), os.path.join(CSRC, "gn_passes.h"), os.path.join(CSRC, "linear.h"), os.path.join(INCLUDE, "gbresize.h")]
+           os.path.join(CSRC, "gn_device.h"), os.path.join(CSRC, "gn_passes.h"), os.path.join(CSRC, "linear.h"),
+           os.path.join(CSRC, "token_rules.h"), os.path.join(INCLUDE, "gbresize.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "-I", INCLUDE, "-I", CSRC]

@@ -18,6 +18,7 @@
 #include "map_ops.h"
 #include "rz_device.h"
 #include "rz_internal.h"
+#include "token_rules.h"
 
 namespace rz {
 namespace {
@@ -26,7 +27,7 @@ using namespace maps;
 using dev::grid_dependency_wait;
 using dev::grid_launch_dependents;
 
-constexpr int kQkSms = 152;
+constexpr int kQkSms = rules::kSms;
 constexpr int kQkThreads = 256;
 constexpr int kQkWarps = kQkThreads / 32;
 constexpr int kQkMaxD = 256;
@@ -41,7 +42,7 @@ struct QkArgs {
     int x_px, y_px, dy_px;      // bytes of a pixel
     int q_heads, heads, D;
     int lanes;                  // lanes of a head's group
-    int chunks;                 // runs of heads a token is cut into, for calls of few tokens
+    int chunks, chunk;          // runs of heads a token is cut into, for calls of few tokens, and the heads of a run
     int row_pairs;
     float eps, inv_d;
     unsigned long long turn[kQkMaxD / 2];   // a position step's angle in 2^-64 turns
@@ -212,9 +213,8 @@ struct QkWalk {
         const unsigned t = token(a);
         place(a, t);
         if (a.chunks > 1) {
-            const int chunk = (a.heads + a.chunks - 1) / a.chunks;
-            h0 = static_cast<int>(item - static_cast<unsigned long long>(t) * a.chunks) * chunk;
-            h1 = min(a.heads, h0 + chunk);
+            h0 = static_cast<int>(item - static_cast<unsigned long long>(t) * a.chunks) * a.chunk;
+            h1 = min(a.heads, h0 + a.chunk);
         }
     }
     __device__ __forceinline__ void next(const QkArgs &a)
@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(kQkThreads, NV == 1 ? 4 : 1) k_qk_norm(const _
 }
 
 // The gradient: the same walk, a step of a warp being one group of heads of one
-// kind.  A step's vectors are copied into places in shared memory that only their
+// kind.  (Every item has a step: two walks count the places, one as it fills them
+// and one as it uses them.)  A step's vectors are copied into places in shared memory that only their
 // lane reads, kQkAhead steps before they are used, across tokens: in registers the
 // four vectors of two steps left 16 warps an SM waiting a memory's latency for
 // each (16 x 37 x 50 tokens of 20 heads of 128, f16: 106 us; so 85 us, 5.3 TB/s).
@@ -606,10 +607,9 @@ cudaError_t qk_dispatch(QkArgs &a, const rz_qk *d, int ve, unsigned *blocks, voi
     int lanes = 1;
     while (lanes < vecs && lanes < 32) lanes *= 2;
     a.lanes = lanes;
-    // calls of few tokens cut a token's heads, down to one step a warp, until there are two CTAs' warps an SM
-    a.chunks = 1;
-    const int most = (a.heads * lanes + 31) / 32;
-    while (a.chunks < most && static_cast<long long>(a.tokens) * a.chunks < 2 * kQkSms * kQkWarps) a.chunks++;
+    const rules::Runs runs = rules::head_runs(a.heads, lanes, a.tokens, kQkWarps);
+    a.chunks = runs.chunks;
+    a.chunk = runs.chunk;
     const unsigned long long need = (static_cast<unsigned long long>(a.tokens) * a.chunks + kQkWarps - 1) / kQkWarps;
     *blocks = static_cast<unsigned>(std::min<unsigned long long>(need, GRAD ? 2 * kQkSms : kQkBlocks));
     const bool inter = d->interleaved != 0;

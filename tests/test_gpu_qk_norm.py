@@ -240,3 +240,17 @@ def test_gradient_against_differences(rz):
         # 25 U of each |y| before the division by 2 h, six deviations of the sum; a smooth sum's third derivative, 1e-3
         noise = 6 * 25 * 2.0 ** -24 * np.linalg.norm(ref.host(y) * dy) / h + 1e-3 * np.linalg.norm(ref.host(g))
         assert abs(slope - float((ref.host(g) * d).sum())) <= noise
+
+
+# a few hundred tokens, whose heads are cut into runs that no whole number of warps takes: a warp's second item is another
+# token's run (the cut into whole runs once left empty ones, after which the gradient read vectors of another step)
+@pytest.mark.parametrize("grid, heads, D, dtype", [((1, 16, 16), (12, 12), 128, "f32"), ((1, 30, 30), (2, 2), 256, "f32"),
+                                                   ((1, 14, 14), (16, 16), 128, "f32"), ((2, 12, 12), (32, 8), 64, "f32"),
+                                                   ((1, 17, 17), (32, 8), 128, "bf16"), ((1, 14, 14), (16, 16), 256, "bf16"),
+                                                   ((1, 16, 16), (16, 16), 256, "f16"), ((1, 16, 18), (20, 20), 128, "f16"),
+                                                   ((3, 8, 17), (4, 3), 24, "f16"), ((2, 19, 16), (5, 2), 100, "f32")])
+@pytest.mark.parametrize("inter", [False, True])
+def test_some_hundred_tokens(rz, grid, heads, D, dtype, inter):
+    first = both(rz, grid, heads, D, dtype, D // 4, D // 2 - D // 4, inter)
+    again = both(rz, grid, heads, D, dtype, D // 4, D // 2 - D // 4, inter)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
