@@ -344,13 +344,14 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step) {
                 const Tile w = tile_at(a, t);
                 const int row = of_b ? static_cast<int>(w.n * a.tile_n + rank * rows_b) : static_cast<int>((w.m * CG + rank) * kTileM);
-                int j = 0, k0 = w.first * kTerms, pa, pb;
+                // (counted in chunks: past the last one's terms may lie 2^31)
+                int j = 0, chunk = w.first, pa, pb;
                 planes_of(a.planes, j, pa, pb);
                 for (int c = 0; c < w.stages; c++) {
                     ok = __all_sync(0xffffffffu, wait_for(empty + s, phase ^ 1, a.status));
                     if (!ok) break;
                     const uint32_t at = to + s * stage_bytes, bar = bars + 8 * s;
-                    const int plane = of_b ? pb : pa;
+                    const int plane = of_b ? pb : pa, k0 = chunk * kTerms;
                     if (elected()) {
                         if (!of_b && rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
                         if (!turned)
@@ -366,9 +367,8 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                         s = 0;
                         phase ^= 1;
                     }
-                    k0 += kTerms;
-                    if (k0 >= w.last * kTerms) {
-                        k0 = w.first * kTerms;
+                    if (++chunk == w.last) {
+                        chunk = w.first;
                         planes_of(a.planes, ++j, pa, pb);
                     }
                 }

@@ -217,3 +217,25 @@ def test_slopes_of_infinite_sums(rz, dtype, act):
     pre[..., 0] = float("nan")
     rz.map_linear_grad(dy, x, w, dbias=db, pre=pre, act=act)
     assert bool(torch.isnan(db[0])) and db[1:].cpu().tolist() == [0.0, -3.0, 0.0]
+
+
+def test_weight_gradient_of_the_most_pixels(rz):
+    """2^31 - 1 of them: the last 64 terms of the sum end at 2^31."""
+    P, C = (1 << 31) - 1, 8
+    torch.cuda.empty_cache()
+    x, dy = (torch.zeros((1, 1, P, C), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    # whole numbers at the beginning, in the middle and at the end: their sums are exact
+    want = torch.zeros((C, C), dtype=torch.float64)
+    rng = np.random.default_rng(3)
+    for at in (0, 1 << 30, P - 130, P - 64):
+        n = min(100, P - at)
+        a, b = (torch.from_numpy(rng.integers(-8, 9, size=(n, C))).double() for _ in range(2))
+        x[0, 0, at:at + n], dy[0, 0, at:at + n] = a.to("cuda", torch.bfloat16), b.to("cuda", torch.bfloat16)
+    for at in (0, 1 << 30, P - 130):
+        want += dy[0, 0, at:at + 130].double().cpu().T @ x[0, 0, at:at + 130].double().cpu()
+    dw, db = torch.empty((C, C), device="cuda"), torch.empty(C, device="cuda")
+    rz.map_linear_grad(dy, x, torch.zeros((C, C), dtype=torch.bfloat16, device="cuda"), None, dw, db)
+    assert torch.equal(dw.double().cpu(), want)
+    assert torch.equal(db.double().cpu(), sum(dy[0, 0, at:at + 130].double().cpu().sum(0) for at in (0, 1 << 30, P - 130)))
+    del x, dy
+    torch.cuda.empty_cache()
