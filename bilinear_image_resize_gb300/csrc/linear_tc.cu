@@ -37,6 +37,7 @@
 #include "linear.h"
 #include "rz_device.h"
 #include "rz_internal.h"
+#include "token_rules.h"
 
 namespace rz {
 namespace {
@@ -181,13 +182,13 @@ __device__ __forceinline__ bool elected()
     return r != 0;
 }
 
-// A wait of at most a second that leaves no gap between its attempts.
+// A wait of at most a second of the kernel's own time that leaves no gap between its attempts.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int *status)
 {
     if (dev::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = dev::global_ns();
+    rules::WaitClock clock(dev::global_ns());
     while (!dev::mbar_try_wait(bar, parity))
-        if (dev::global_ns() - t0 > kWaitLimitNs) {
+        if (clock.over(dev::global_ns(), kWaitLimitNs)) {
             if (status) atomicExch(status, RZ_ERR_TIMEOUT);
             return false;
         }

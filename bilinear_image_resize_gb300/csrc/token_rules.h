@@ -1,9 +1,31 @@
-// What the operators around attention work out on the host, in plain C++: the
-// host tests compile this file by itself.
+// What the operators around attention work out in plain C++, on the host but for
+// the waits' clock: the host tests compile this file by itself.
 #pragma once
+
+#ifdef __CUDACC__
+#define RZ_BOTH __host__ __device__ __forceinline__
+#else
+#define RZ_BOTH inline
+#endif
 
 namespace rz {
 namespace rules {
+
+// The clock of a bounded wait, in nanoseconds.  A wait looks again at least every
+// millisecond while its kernel runs; what lies between two looks counts as ten at
+// most, so that the time slices of other programs, in which nothing that it waits
+// for can happen either, do not use up its limit.
+struct WaitClock {
+    unsigned long long last, waited = 0;
+    RZ_BOTH explicit WaitClock(unsigned long long now) : last(now) {}
+    RZ_BOTH bool over(unsigned long long now, unsigned long long limit)
+    {
+        const unsigned long long step = now - last, most = 10000000ull;
+        last = now;
+        waited += step < most ? step : most;
+        return waited > limit;
+    }
+};
 
 constexpr int kSms = 152;
 

@@ -30,6 +30,14 @@ int bad_runs(int heads, int lanes, int most, int warps)
     }
     return bad;
 }
+// looks of a wait that began at times[0] until it gives up, at most n - 1; 0: it does not
+int looks(const unsigned long long *times, int n, unsigned long long limit)
+{
+    WaitClock clock(times[0]);
+    for (int i = 1; i < n; i++)
+        if (clock.over(times[i], limit)) return i;
+    return 0;
+}
 
 }
 """
@@ -83,3 +91,21 @@ def test_runs_are_copied_as_they_are_used(rules, q, k, lanes, tokens):
             for p0, p1 in ((h0, min(h1, q)), (max(h0, q), h1)):
                 used += [(item, f) for f in range(p0, p1, at_once)]
         assert copied == used
+
+
+def looks(rules, times, limit=10 ** 9):
+    return rules.looks((ctypes.c_ulonglong * len(times))(*times), len(times), ctypes.c_ulonglong(limit))
+
+
+def test_a_wait_gives_up_after_a_second_of_its_own(rules):
+    ms = 10 ** 6
+    times = [5 + i * ms // 2 for i in range(2100)]
+    assert looks(rules, times) == 2001                        # looks every half millisecond
+    # another program's slice of 1.5 s, and one of an hour, between two looks: neither uses the second up
+    away = [5, 5 + ms, 5 + ms + 1500 * ms, 5 + 3_600_000 * ms]
+    away += [away[-1] + i * ms // 2 for i in range(1, 500)]
+    assert looks(rules, away) == 0
+    # but a wait whose looks are always late ends too, after a hundred of them
+    assert looks(rules, [i * 3000 * ms for i in range(200)]) == 101
+    # a clock that passes 2^64: look i is at 5 ns + (i - 1) ms, which passes 50 ms with the 51st
+    assert looks(rules, [(1 << 64) - 5] + [i * ms for i in range(100)], 50 * ms) == 51
