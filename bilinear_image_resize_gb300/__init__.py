@@ -640,6 +640,37 @@ def _status_of(status, like):
     return status.data_ptr()
 
 
+_waits = {}     # device -> a word of pinned host memory, its address
+
+
+def _capturing(stream) -> bool:
+    c = _torch.cuda
+    if stream is None:
+        return c.is_current_stream_capturing()
+    with c.stream(c.ExternalStream(_stream(stream))):
+        return c.is_current_stream_capturing()
+
+
+def _status_at(status, like, stream, where: str):
+    """Where a call's kernels report a time-out: the caller's word, or one of the
+    binding's that the host can read without waiting for the device.  What an
+    earlier call has left in that one is raised here."""
+    if status is not None:
+        return _status_of(status, like)
+    device = like.get_device()
+    word = _waits.get(device)
+    if word is None:
+        if not _torch.cuda.is_available() or _capturing(stream):     # nothing is pinned during a capture
+            return None
+        kept = _torch.zeros(1, dtype=_torch.int32, pin_memory=True)
+        word = _waits.setdefault(device, (ctypes.c_int.from_address(kept.data_ptr()), kept.data_ptr(), kept))
+    code = word[0].value
+    if code:
+        word[0].value = 0
+        raise ResizeError(code, f"{where}: an earlier map_linear or map_linear_grad was left unfinished")
+    return word[1]
+
+
 def _linear_of(x, out, weight, act, names):
     """rz_linear of an x (C channels) and an out (K), their maps and the weight's matrix."""
     (N, H, W, C), mx = _map_of(x, names[0])
@@ -681,13 +712,15 @@ def map_linear(x, y, weight, bias=None, residual=None, pre=None, act: int = RZ_A
     residual: a map of y's shape (y itself among them) or None; pre: a map of y's
     shape that takes x weight^T + bias for the gradient, or None; workspace: a
     CUDA tensor of map_linear_workspace bytes, or None to take one from torch's
-    allocator; status: an int32 CUDA tensor of one element for a kernel's
-    time-out, or None."""
+    allocator; status: an int32 CUDA tensor of one element that takes
+    RZ_ERR_TIMEOUT where a kernel's wait runs out and the result is left
+    unfinished, or None: the next map_linear or map_linear_grad on the device
+    that is called without one then raises ResizeError."""
     _with_torch()
     args = _linear_args(x, y, weight, residual, pre, act)
     d, mx, w, pitch, mr, mp, my = args
     _on_current_device(x, y, weight, bias, residual, pre)
-    b, st = _floats(bias, "bias", (d.K,)), None if status is None else _status_of(status, x)
+    b, st = _floats(bias, "bias", (d.K,)), _status_at(status, x, stream, "map_linear")
     f = _native.load().map_linear
     if workspace is None and d.N * d.H * d.W <= 8:      # needs none
         _check(f(d, mx, w, pitch, b, mr, mp, my, None, 0, st, _stream_at(stream, x)), "map_linear")
@@ -730,7 +763,7 @@ def map_linear_grad(dy, x, weight, dx=None, dweight=None, dbias=None, pre=None, 
     _with_torch()
     args = _linear_grad_args(dy, x, weight, dx, dweight, pre, act)
     _on_current_device(x, dy, weight, dx, dweight, dbias, pre)
-    b, st = _floats(dbias, "dbias", (args[0].K,)), None if status is None else _status_of(status, x)
+    b, st = _floats(dbias, "dbias", (args[0].K,)), _status_at(status, x, stream, "map_linear_grad")
     f = _native.load().map_linear_grad
     _check(_with_workspace(lambda p, n, s: f(*args, b, p, n, st, s), workspace, _linear_grad_query, args, x, stream),
            "map_linear_grad")

@@ -189,7 +189,7 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int *st
     rules::WaitClock clock(dev::global_ns());
     while (!dev::mbar_try_wait(bar, parity))
         if (clock.over(dev::global_ns(), kWaitLimitNs)) {
-            if (status) atomicExch(status, RZ_ERR_TIMEOUT);
+            if (status) *static_cast<volatile int *>(status) = RZ_ERR_TIMEOUT;     // every writer's value; the word may lie on the host
             return false;
         }
     return true;

@@ -284,3 +284,38 @@ def test_gradient_against_differences(rz, kind):
         # third derivative's h^2 / 6 of a smooth sum: 1e-3 of its size
         noise = 6 * 88 * 2.0 ** -24 * np.linalg.norm(ref.host(y) * dy) / h + 1e-3 * np.linalg.norm(ref.host(g))
         assert abs(slope - float((ref.host(g) * d).sum())) <= noise
+
+
+def test_calls_without_a_status_word_report_to_the_bindings_own(rz):
+    x, w = torch.ones((1, 4, 8, 16), device="cuda"), torch.ones((24, 16), device="cuda")
+    y, dw = torch.empty((1, 4, 8, 24), device="cuda"), torch.empty((24, 16), device="cuda")
+    rz.map_linear(x, y, w)
+    word, at, kept = rz._waits[0]
+    assert at == kept.data_ptr() and kept.is_pinned() and word.value == 0
+    # the device can write it where the host reads it
+    device_view = torch.tensor([7], dtype=torch.int32, device="cuda")
+    kept.copy_(device_view)
+    torch.cuda.synchronize()
+    with pytest.raises(rz.ResizeError, match="earlier"):
+        rz.map_linear_grad(y, x, w, None, dw)
+    rz.map_linear_grad(y, x, w, None, dw)
+    torch.cuda.synchronize()
+    assert word.value == 0 and float(dw[0, 0]) == 32 * 16
+    s = torch.cuda.Stream()
+    assert not rz._capturing(None) and not rz._capturing(s) and not rz._capturing(s.cuda_stream)
+    with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
+        assert rz._capturing(None) and rz._capturing(s)
+        rz.map_linear(x, y, w)
+
+
+def test_first_call_inside_a_capture(rz, monkeypatch):
+    monkeypatch.setattr(rz, "_waits", {})
+    x, w, y = (torch.ones(s, device="cuda") for s in ((1, 4, 8, 16), (24, 16), (1, 4, 8, 24)))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rz.map_linear(x, y, w)
+    assert not rz._waits
+    y.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert bool((y == 16).all())

@@ -155,3 +155,26 @@ def test_few_pixels_ask_for_no_workspace(rz, calls):              # noqa: F811
     rz.map_linear(Standin((8, 1, 1, 16)), Standin((8, 1, 1, 16), at=1 << 45), Standin((16, 16), at=1 << 46), stream=0)
     (name, got), = calls
     assert name == "map_linear" and got[8:10] == (None, 0)
+
+
+@pytest.mark.parametrize("op", ["linear", "linear_grad"])
+def test_a_time_out_of_an_earlier_call_is_raised(rz, calls, monkeypatch, op):    # noqa: F811
+    """Without a status word of the caller's, calls hand on the binding's own one of the device."""
+    import ctypes
+    from bilinear_image_resize_gb300 import _native
+    call, spec = every_call(rz)[op]
+    word = ctypes.c_int(0)
+    monkeypatch.setitem(rz._waits, 0, (word, ctypes.addressof(word), word))
+    monkeypatch.setattr(_native.load(), "resize_strerror", lambda code: b"timeout", raising=False)
+    call(**standins(spec))
+    assert ctypes.addressof(word) in calls[-1][1]
+    word.value = rz.RZ_ERR_TIMEOUT                            # as a kernel leaves it
+    before = len([n for n, _ in calls if n in LAUNCHES])
+    with pytest.raises(rz.ResizeError, match="earlier") as e:
+        call(**standins(spec))
+    assert e.value.code == rz.RZ_ERR_TIMEOUT and word.value == 0
+    assert len([n for n, _ in calls if n in LAUNCHES]) == before
+    call(**standins(spec))                                    # told once
+    word.value = rz.RZ_ERR_TIMEOUT
+    call(**standins(spec), status=Standin((1,), INT, at=1 << 51))     # the caller's own word: theirs to look at
+    assert (1 << 51) in calls[-1][1] and word.value == rz.RZ_ERR_TIMEOUT
