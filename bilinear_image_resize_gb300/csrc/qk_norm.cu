@@ -49,8 +49,9 @@ struct QkArgs {
 };
 
 // Cosine and sine of position * turn: the product's low 64 bits are the angle
-// modulo a turn, exactly; its top 32 bits go on as a signed float.  16-bit results
-// take the GPU's approximate functions, off by 2^-21.2 in [-pi, pi] (with the angle's rounding 7e-7).
+// modulo a turn, off by what the step is (2^-63 of a turn) for each position; its top
+// 32 bits go on as a signed float.  16-bit results take the GPU's approximate
+// functions, off by 2^-21.2 in [-pi, pi] (with the angle's rounding 7e-7).
 template <class T>
 __device__ __forceinline__ void turned(int p, unsigned long long turn, float &c, float &s)
 {
@@ -574,15 +575,6 @@ int qk_check(const rz_qk *d, QkPlan *p)
     return RZ_OK;
 }
 
-// Turns of a position step in 2^-64, whole turns left out.
-unsigned long long turn_of(double base, double scale, int j, int pairs)
-{
-    const double f = scale * std::pow(base, -static_cast<double>(j) / pairs) * 0.15915494309189533577;
-    if (!std::isfinite(f)) return 0;
-    const double frac = f - std::floor(f);
-    return frac < 1.0 ? static_cast<unsigned long long>(std::ldexp(frac, 64)) : 0ull;
-}
-
 template <class T, int VE, int NV, bool GRAD>
 cudaError_t qk_launch(const QkArgs &a, bool inter, unsigned blocks, void *stream)
 {
@@ -646,9 +638,8 @@ int qk_run(const rz_qk *d, const QkPlan &p, const rz_map *x, const rz_map *dy, c
     a.row_pairs = d->row_pairs;
     a.eps = d->eps;
     a.inv_d = 1.0f / static_cast<float>(d->D);
-    for (int j = 0; j < d->row_pairs + d->col_pairs; j++)
-        a.turn[j] = j < d->row_pairs ? turn_of(d->base, d->scale, j, d->row_pairs)
-                                     : turn_of(d->base, d->scale, j - d->row_pairs, d->col_pairs);
+    rules::turns_of(d->base, d->scale, d->row_pairs, a.turn);
+    rules::turns_of(d->base, d->scale, d->col_pairs, a.turn + d->row_pairs);
     const auto fits = [&](int ve) {
         const size_t b = ve * p.x.es;
         return d->D / 2 % ve == 0 && a.x_px % b == 0 && a.y_px % b == 0 && map_aligned(*x, p.x, b) && map_aligned(*y, sy, b) &&

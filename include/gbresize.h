@@ -628,9 +628,10 @@ RZ_API int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x
  * further pairs stay.  Pair j is (u[j], u[j + D / 2]), or (u[2j], u[2j + 1])
  * where `interleaved` is set.  (row, col) is the pixel's place in its image, or
  * positions[n][h][w] (device int[N][H][W][2], 8-byte aligned) where that is given;
- * any int.  Angles are reduced to a turn exactly, in 64-bit integers, whatever the
- * position: they are off by 2^-24 of half a turn at most, their cosines and sines
- * by 3e-7 for float32 maps, by 7e-7 for 16-bit ones.
+ * any int.  A step is held to 2^-63 of a turn and angles are reduced to a turn in
+ * 64-bit integers: they are off by 2^-24 of half a turn at most whatever the position
+ * (|scale| below 2^32), their cosines and sines by 3e-7 for float32 maps, by 7e-7 for
+ * 16-bit ones.
  * x has C channels, y has out_C, either at least (q_heads + k_heads) D.
  * D even, 2 <= D <= 256; one head at least; eps >= 0, base > 0 and scale
  * finite; row_pairs + col_pairs <= D / 2.  A head of zeros gives zeros where

@@ -254,3 +254,34 @@ def test_some_hundred_tokens(rz, grid, heads, D, dtype, inter):
     first = both(rz, grid, heads, D, dtype, D // 4, D // 2 - D // 4, inter)
     again = both(rz, grid, heads, D, dtype, D // 4, D // 2 - D // 4, inter)
     assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("base, scale", [(10000.0, 1.0), (500000.0, 9.0), (100.0, -1000.0), (10.0, 0.125)])
+def test_any_int_position(rz, dtype, base, scale):
+    """The whole range of int, and steps of many turns: the angle is good to 2^-24 of half a turn all the same."""
+    N, H, W, q, k, D, rows = 2, 3, 8, 2, 1, 32, 7
+    rng = np.random.default_rng(11)
+    p = rng.integers(-(1 << 31), 1 << 31, size=(N, H, W, 2))
+    p[0, 0, 0], p[0, 0, 1], p[0, 0, 2] = (-(1 << 31), (1 << 31) - 1), ((1 << 31) - 1, -(1 << 31)), (0, -1)
+    x, dy = values((N, H, W, 96), dtype, 1), values((N, H, W, 96), dtype, 2)
+    xv, dv = (torch.from_numpy(a).to(getattr(torch, tok.TORCH[dtype])).cuda() for a in (x, dy))
+    y, dx, dq = torch.empty_like(xv), torch.empty_like(xv), torch.empty(D, device="cuda")
+    turn = dict(positions=torch.from_numpy(p.astype(np.int32)).cuda(), base=base, row_pairs=rows, scale=scale)
+    rz.map_qk_norm(xv, y, q, k, D, **turn)
+    rz.map_qk_norm_grad(dv, xv, dx, q, k, D, dgamma_q=dq, **turn)
+    t = tok.exact_angles(N, H, W, D, p, base, rows, D // 2 - rows, scale)
+    one = np.ones(D)
+    want, err = tok.qk_norm(x, q, k, D, one, one, t, False, EPS)
+    gx, gq, _, ex, eq, _ = tok.qk_norm_grad(dy, x, q, k, D, one, one, t, False, EPS)
+    if dtype != "f32":      # 16-bit maps' cosines and sines: 7e-7, six units of 2^-24 more than the bounds have
+        more = 6 * 2.0 ** -24
+        r = 1 / np.sqrt((x.reshape(N, H, W, 3, D) ** 2).mean(-1, keepdims=True) + EPS)
+        spread = tok.pair_sum(dy.reshape(N, H, W, 3, D), False)
+        h = np.abs(x.reshape(N, H, W, 3, D) * r)
+        err = err + more * tok.pair_sum((x.reshape(N, H, W, 3, D) * r), False).reshape(err.shape)
+        ex = ex + more * (r * spread + r * h * (spread * h).mean(-1, keepdims=True)).reshape(ex.shape)
+        eq = eq + more * (spread * h)[..., :q, :].sum((0, 1, 2, 3))
+    check(y, want, ref.stored(want, err, dtype), "y")
+    check(dx, gx, ref.stored(gx, ex, dtype), "dx")
+    check(dq, gq, eq + 2.0 ** -24 * np.abs(gq), "dgamma_q")

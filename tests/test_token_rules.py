@@ -2,11 +2,14 @@
 compiled by itself and asked for its answers."""
 import ctypes
 import os
+import random
 import shutil
 import subprocess
+from fractions import Fraction
 
 import pytest
 
+import token_reference as tok
 from conftest import ROOT
 
 SOURCE = r"""
@@ -30,6 +33,12 @@ int bad_runs(int heads, int lanes, int most, int warps)
     }
     return bad;
 }
+unsigned long long turn(double base, double scale, int j, int pairs)
+{
+    unsigned long long all[128];
+    turns_of(base, scale, pairs, all);
+    return all[j];
+}
 // looks of a wait that began at times[0] until it gives up, at most n - 1; 0: it does not
 int looks(const unsigned long long *times, int n, unsigned long long limit)
 {
@@ -51,9 +60,12 @@ def rules(tmp_path_factory):
     at = tmp_path_factory.mktemp("rules")
     (at / "rules.cpp").write_text(SOURCE)
     csrc = os.path.join(ROOT, "bilinear_image_resize_gb300", "csrc")
-    subprocess.run([cc, "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I", csrc, str(at / "rules.cpp"), "-o",
+    subprocess.run([cc, "-std=c++17", "-O3", "-Wall", "-Werror", "-shared", "-fPIC", "-I", csrc, str(at / "rules.cpp"), "-o",
                     str(at / "rules.so")], check=True)
-    return ctypes.CDLL(str(at / "rules.so"))
+    lib = ctypes.CDLL(str(at / "rules.so"))
+    lib.turn.restype = ctypes.c_ulonglong
+    lib.turn.argtypes = [ctypes.c_double, ctypes.c_double, ctypes.c_int, ctypes.c_int]
+    return lib
 
 
 @pytest.mark.parametrize("lanes", [1, 2, 4, 8, 16, 32])
@@ -109,3 +121,25 @@ def test_a_wait_gives_up_after_a_second_of_its_own(rules):
     assert looks(rules, [i * 3000 * ms for i in range(200)]) == 101
     # a clock that passes 2^64: look i is at 5 ns + (i - 1) ms, which passes 50 ms with the 51st
     assert looks(rules, [(1 << 64) - 5] + [i * ms for i in range(100)], 50 * ms) == 51
+
+
+def test_steps_of_positions_are_exact_turns(rules):
+    """In 2^-64 of a turn, against sixty digits: within two of them and 2^-92 of the step, so that 2^31 positions stay within 2^-31."""
+    rng = random.Random(4)
+    cases = [(base, scale, j, pairs) for base in (10000.0, 500000.0, 100.0, 1.0, 2.0, 0.5) for scale in (1.0, -1.0, 9.0, 1000.0, 0.125)
+             for pairs in (1, 2, 16, 37, 64, 128) for j in sorted({0, 1, pairs // 2, pairs - 1}) if j < pairs]
+    cases += [(10.0 ** rng.uniform(-300, 300), rng.choice([-1, 1]) * 10.0 ** rng.uniform(-20, 20), rng.randrange(128), 128) for _ in range(200)]
+    cases += [(rng.uniform(1, 1e6), rng.uniform(-1e6, 1e6), rng.randrange(p), p) for p in (3, 5, 24, 100, 127) for _ in range(40)]
+    for base, scale, j, pairs in cases:
+        step = tok.step_in_turns(base, scale, j, pairs)
+        if abs(step) > 1 << 28:
+            continue                                          # less than 2^-63 is left of a turn
+        off = (Fraction(rules.turn(base, scale, j, pairs), 1 << 64) - step) % 1
+        off = min(off, 1 - off)
+        assert off <= Fraction(2, 1 << 64) + abs(step) / (1 << 92), (base, scale, j, pairs, float(off * 2 ** 64))
+
+
+def test_steps_past_the_range(rules):
+    assert rules.turn(1e-300, 1e300, 127, 128) == 0 and rules.turn(5e-324, 1.0, 1, 2) >= 0
+    assert rules.turn(1e-300, -1e300, 0, 1) >= 0 and rules.turn(1e308, 1e-300, 127, 128) == 0
+    assert rules.turn(1.0, 0.0, 3, 7) == 0

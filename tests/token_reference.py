@@ -82,6 +82,38 @@ def angles(N, H, W, D, positions, base, row_pairs, col_pairs, scale):
     return a
 
 
+def step_in_turns(base, scale, j, pairs):
+    """scale base^(-j / pairs) / (2 pi) as a fraction, from a hundred digits."""
+    from decimal import Context, Decimal
+    from fractions import Fraction
+    c = Context(prec=100)
+    # pi by Machin's formula
+    def arc(n):
+        t, s, k = Fraction(1, n), Fraction(0), 0
+        while t.denominator < 10 ** 110 * max(1, t.numerator):
+            s += t / (2 * k + 1) * (-1) ** k
+            t /= n * n
+            k += 1
+        return s
+    pi = 4 * (4 * arc(5) - arc(239))
+    y = c.exp(c.multiply(c.ln(Decimal(base)), c.divide(Decimal(-j), Decimal(pairs))))
+    return Fraction(scale) * Fraction(y) / (2 * pi)
+
+
+def exact_angles(N, H, W, D, positions, base, row_pairs, col_pairs, scale):
+    """`angles` for positions of any size, reduced to within half a turn before they are rounded."""
+    from fractions import Fraction
+    steps = [step_in_turns(base, scale, j, row_pairs) for j in range(row_pairs)]
+    steps += [step_in_turns(base, scale, j, col_pairs) for j in range(col_pairs)]
+    a = np.zeros((N, H, W, 1, D // 2), np.longdouble)
+    for at in np.ndindex(N, H, W):
+        for j, step in enumerate(steps):
+            t = int(positions[at][0 if j < row_pairs else 1]) * step
+            t -= round(t)
+            a[at][0, j] = 2 * np.longdouble(np.pi) * np.longdouble(float(t))
+    return a
+
+
 def _split(v, inter):
     return (v[..., 0::2], v[..., 1::2]) if inter else (v[..., :v.shape[-1] // 2], v[..., v.shape[-1] // 2:])
 
