@@ -26,12 +26,13 @@ __device__ __forceinline__ long long row_off(const Rows &m, unsigned r)
 }
 
 // The activations.  float32 results take the exact forms.  16-bit ones, which are
-// rounded to 2^-9 or 2^-12 of their size, take GELU from the lower tail of the normal
+// rounded to 2^-8 or 2^-11 of their size, take GELU from the lower tail of the normal
 // distribution, two elements at a time: with a = |z|,
 //   Phi(-a) = 2^(r(a) - a^2 log2(e) / 2),   GELU(z) = max(z, 0) - a Phi(-a),
-// r a polynomial of degree 6 for a <= 6, fitted so that Phi(-a) is off by 2.9e-4 of
-// itself at most and by (10 + 3 a) 2^-26 where that is less; it stays where it is
-// from there on, where Phi(-a) < 1e-9.  One function of the special unit and seven
+// r a polynomial of degree 6 for a <= 6, fitted so that Phi(-a) is off by 3e-4 of
+// itself at most and by (25 + 3 a) 2^-26 where that is less (of which the fit has 13 + 3 a,
+// the float32 steps 4, the power, off by 2^-22, 8); it stays where it is from there on,
+// where Phi(-a) < 1e-9.  One function of the special unit and seven
 // packed products an element pair; erff takes thirty instructions an element, which
 // on a product of 1024 terms cost more than the product (617 against 330 us on 65536 x
 // 1024 x 4096).  Infinities: a is cut at 1e4, where Phi(-a) is 0; the rest passes them

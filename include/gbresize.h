@@ -566,7 +566,8 @@ RZ_API int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_ma
  * gradient, or NULL.  x: C channels; y, residual and pre: K.  Products are
  * summed in float32; the result is rounded once.  float32 products are off by
  * about 1e-6 of the sum of their terms' magnitudes; GELU of 16-bit maps by
- * (10 + 3 |z|) |z| / 2^26 before it is rounded.  A value that is not finite
+ * (25 + 3 |z|) |z| / 2^26 before it is rounded, and below 0 by 3e-4 of itself where
+ * that is less.  A value that is not finite
  * reaches the results of its own row or column alone; an infinity of float32 maps
  * may come out as NaN.
  * y may be the residual itself, and overlaps no other map; weight and b lie

@@ -319,3 +319,67 @@ def test_first_call_inside_a_capture(rz, monkeypatch):
     g.replay()
     torch.cuda.synchronize()
     assert bool((y == 16).all())
+
+
+def gelu_border(dtype, k):
+    """Float32 z whose GELU lies (k + 3 |z|) |z| / 2^26 or just more from where its rounding changes, on either side, and what
+    it rounds to: an error of that size turns the rounding."""
+    import scipy.special as sp
+
+    def f(z):
+        return z * sp.ndtr(z)
+
+    t = getattr(torch, tok.TORCH[dtype])
+    rng = np.random.default_rng(9)
+    found = []
+    # an interval of z, whether GELU rises there, and borders: the middles of neighbours of the type
+    for lo, hi, rises in ((2.0 ** -9, 7.0, True), (-0.7, -(2.0 ** -9), True), (-3.0, -0.8, False)):
+        one = np.sign(lo) * 2.0 ** rng.uniform(*np.sort(np.log2(np.abs([lo, hi]))), 12000)
+        g = torch.unique(torch.from_numpy(f(one)).to(t))
+        border = ((g.double() + (g.view(torch.int16) + 1).view(t).double()) / 2).numpy()
+        for side in (-1, 1):
+            a, b = np.full(border.shape, lo), np.full(border.shape, hi)
+            for _ in range(200):
+                m = (a + b) / 2
+                above = f(m) - side * (k + 3 * np.abs(m)) * np.abs(m) / 2 ** 26 > border
+                up = above == rises
+                a, b = np.where(up, a, m), np.where(up, m, b)
+            z = ((a + b) / 2).astype(np.float32)
+            # the next float32 on the far side of the margin
+            for _ in range(4):
+                z64 = z.astype(np.float64)
+                margin = side * (f(z64) - border) - (k + 3 * np.abs(z64)) * np.abs(z64) / 2 ** 26
+                away = np.float32(np.inf if (side > 0) == rises else -np.inf)
+                z = np.where(margin < 0, np.nextafter(z, away), z)
+            z64 = z.astype(np.float64)
+            margin = side * (f(z64) - border) - (k + 3 * np.abs(z64)) * np.abs(z64) / 2 ** 26
+            good = (margin >= 0) & (margin < 4 * np.abs(z64) / 2 ** 24) & (z64 > lo) & (z64 < hi)
+            found.append(z64[good])
+    z = np.unique(np.concatenate(found))
+    return z, torch.from_numpy(f(z)).to(t).double().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("pixels", [1, 40])
+def test_gelu_of_16_bit_maps_is_as_good_as_stated(rz, dtype, pixels):
+    """(25 + 3 |z|) |z| / 2^26 before the rounding: z by way of the bias."""
+    z, want = gelu_border(dtype, 25)
+    assert z.size > (200 if dtype == "bf16" else 4000)
+    t = getattr(torch, tok.TORCH[dtype])
+    y = torch.empty((1, 1, pixels, z.size), dtype=t, device="cuda")
+    rz.map_linear(torch.zeros((1, 1, pixels, 8), dtype=t, device="cuda"), y, torch.zeros((z.size, 8), dtype=t, device="cuda"),
+                  torch.from_numpy(z).float().cuda(), act=ACTS["gelu"])
+    assert np.array_equal(ref.host(y), np.broadcast_to(want, y.shape))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gelu_of_16_bit_maps_far_below_zero(rz, dtype):
+    """3e-4 of the tail before the rounding."""
+    import scipy.special as sp
+    z = -np.linspace(2.0, 5.9, 60000).astype(np.float32).astype(np.float64)
+    t = getattr(torch, tok.TORCH[dtype])
+    y = torch.empty((1, 1, 1, z.size), dtype=t, device="cuda")
+    rz.map_linear(torch.zeros((1, 1, 1, 8), dtype=t, device="cuda"), y, torch.zeros((z.size, 8), dtype=t, device="cuda"),
+                  torch.from_numpy(z).float().cuda(), act=ACTS["gelu"])
+    want = z * sp.ndtr(z)
+    check(y, want, ref.stored(want, 3e-4 * np.abs(want), dtype), "y")
