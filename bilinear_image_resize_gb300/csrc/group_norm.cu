@@ -14,13 +14,12 @@
 #include <algorithm>
 #include <initializer_list>
 #include <mutex>
-#include <utility>
-#include <vector>
 
 #include "gn_device.h"
 #include "map_ops.h"
 #include "rz_device.h"
 #include "rz_internal.h"
+#include "token_rules.h"
 
 namespace rz {
 namespace {
@@ -151,21 +150,14 @@ namespace rz {
 cudaError_t maps::shared_opt_in(const void *fn, int bytes)
 {
     static std::mutex mu;
-    static std::vector<std::pair<int, const void *>> ready;
+    static rules::Granted granted;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
-    for (const auto &r : ready)
-        if (r.first == dev && r.second == fn) return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    try {
-        ready.emplace_back(dev, fn);
-    } catch (...) {
-        // not remembered: asked for again by the next call
-    }
-    return cudaSuccess;
+    return static_cast<cudaError_t>(granted.have(dev, fn, bytes, [fn](int n) {
+        return static_cast<int>(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, n));
+    }));
 }
 
 }  // namespace rz

@@ -99,7 +99,7 @@ inline cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, size_t smem,
     return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
 }
 
-// Opts a kernel into `bytes` of shared memory, once a device (group_norm.cu); the
+// Opts a kernel into at least `bytes` of shared memory, once a device (group_norm.cu); the
 // default lets two CTAs an SM have as much.
 constexpr int kMapShared = 112 * 1024;
 cudaError_t shared_opt_in(const void *fn, int bytes = kMapShared);

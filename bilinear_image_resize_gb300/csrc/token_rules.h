@@ -1,8 +1,9 @@
-// What the operators around attention work out in plain C++, on the host but for
+// What the map operators work out in plain C++, on the host but for
 // the waits' clock: the host tests compile this file by itself.
 #pragma once
 
 #include <cmath>
+#include <vector>
 
 #ifdef __CUDACC__
 #define RZ_BOTH __host__ __device__ __forceinline__
@@ -30,6 +31,39 @@ struct WaitClock {
 };
 
 constexpr int kSms = 152;
+
+// The shared memory that kernels have been opted into, by device; grant(bytes) asks
+// for it and gives 0, or an error that is handed on.  A kernel that asks for more
+// than it was given asks again.
+class Granted {
+    struct Entry {
+        int device;
+        const void *fn;
+        int bytes;
+    };
+    std::vector<Entry> entries;
+
+public:
+    template <class F>
+    int have(int device, const void *fn, int bytes, const F &grant)
+    {
+        Entry *found = nullptr;
+        for (Entry &e : entries)
+            if (e.device == device && e.fn == fn) found = &e;
+        if (found && found->bytes >= bytes) return 0;
+        if (const int error = grant(bytes)) return error;
+        if (found) {
+            found->bytes = bytes;
+            return 0;
+        }
+        try {
+            entries.push_back({device, fn, bytes});
+        } catch (...) {
+            // not remembered: asked for again by the next call
+        }
+        return 0;
+    }
+};
 
 // How the norm of queries and keys cuts a token's heads, where there are few tokens:
 // into more runs, down to one step a warp, until there are two CTAs' warps an SM.

@@ -1,4 +1,4 @@
-"""What the operators around attention work out on the host (csrc/token_rules.h),
+"""What the map operators work out in plain C++ (csrc/token_rules.h),
 compiled by itself and asked for its answers."""
 import ctypes
 import os
@@ -13,6 +13,7 @@ import token_reference as tok
 from conftest import ROOT
 
 SOURCE = r"""
+#include <cstddef>
 #include "token_rules.h"
 using namespace rz::rules;
 extern "C" {
@@ -38,6 +39,21 @@ unsigned long long turn(double base, double scale, int j, int pairs)
     unsigned long long all[128];
     turns_of(base, scale, pairs, all);
     return all[j];
+}
+// asks for (device, function, bytes) three ints at a time; the device `failing` refuses. asked[i]: bytes that call i asked for, 0 none,
+// -1 refused
+void grants(const int *calls, int n, int failing, int *asked)
+{
+    Granted g;
+    for (int i = 0; i < n; i++) {
+        const int *c = calls + 3 * i;
+        asked[i] = 0;
+        if (g.have(c[0], reinterpret_cast<const void *>(static_cast<size_t>(c[1])), c[2], [&](int bytes) {
+                asked[i] = bytes;
+                return c[0] == failing ? 7 : 0;
+            }) == 7)
+            asked[i] = -1;
+    }
 }
 // looks of a wait that began at times[0] until it gives up, at most n - 1; 0: it does not
 int looks(const unsigned long long *times, int n, unsigned long long limit)
@@ -143,3 +159,11 @@ def test_steps_past_the_range(rules):
     assert rules.turn(1e-300, 1e300, 127, 128) == 0 and rules.turn(5e-324, 1.0, 1, 2) >= 0
     assert rules.turn(1e-300, -1e300, 0, 1) >= 0 and rules.turn(1e308, 1e-300, 127, 128) == 0
     assert rules.turn(1.0, 0.0, 3, 7) == 0
+
+
+def test_shared_memory_is_asked_for_once_and_again_for_more(rules):
+    calls = [(0, 1, 100), (0, 1, 100), (0, 1, 90), (0, 1, 120), (0, 1, 100), (0, 1, 120), (0, 2, 100), (1, 1, 100), (1, 1, 121), (2, 1, 50), (2, 1, 50)]
+    flat = (ctypes.c_int * (3 * len(calls)))(*(v for c in calls for v in c))
+    asked = (ctypes.c_int * len(calls))()
+    rules.grants(flat, len(calls), 2, asked)
+    assert list(asked) == [100, 0, 0, 120, 0, 0, 100, 100, 121, -1, -1]
