@@ -5,7 +5,7 @@
 // operands whose rows TMA can address (16-byte pitch and start).  What is not of
 // that kind is laid out first: float32 as three bfloat16 planes, rows of odd
 // widths or with gaps as packed ones; so is dz, in one pass that also adds up its
-// columns.  Sums too long for few tiles are cut into runs that a last kernel joins
+// columns.  Sums too long for few tiles are cut into parts that a last kernel joins
 // in order.
 #include <algorithm>
 #include <cmath>
@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(256) k_linear_sums(const __grid_constant__ Sum
     sum_columns(a, blockIdx.x);
 }
 
-// The runs of a product joined in order, and its epilogue; a run alone where its
-// result's rows are not TMA's to write.
+// The parts of a product joined in order, and its epilogue; one alone where its sums
+// took several runs, or its result's rows are not TMA's to write.
 struct JoinArgs {
     Finish f;
     const float *part;
     unsigned pitch;         // floats, a multiple of VE
-    int splits;
+    int parts;
     unsigned blocks;        // those after them sum the bias's columns (a launch of 5 us less)
     Sums sums;
 };
@@ -224,14 +224,14 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Joi
     const unsigned units = a.f.N / UNIT;
     const unsigned long long base = static_cast<unsigned long long>(blockIdx.x) * (256 * U);
     const unsigned m0 = static_cast<unsigned>(base / units), n0 = static_cast<unsigned>(base - static_cast<unsigned long long>(m0) * units);
-    const long long run = static_cast<long long>(a.f.M) * a.pitch;
+    const long long step = static_cast<long long>(a.f.M) * a.pitch;
     if constexpr (WIDE) {
         const unsigned q0 = n0 + threadIdx.x, m = m0 + q0 / units, n = q0 % units * UNIT;
         if (m >= a.f.M) return;
         const float *from = a.part + static_cast<long long>(m) * a.pitch + n;
         float2 z[UNIT / 2] = {}, b[UNIT / 2];
 #pragma unroll 8
-        for (int r = 0; r < a.splits; r++, from += run)
+        for (int r = 0; r < a.parts; r++, from += step)
 #pragma unroll
             for (int q = 0; q < UNIT; q += 4) {
                 const float4 v = __ldcs(reinterpret_cast<const float4 *>(from + q));
@@ -256,14 +256,14 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ Joi
             z[u] = both(0.0f);
         }
 #pragma unroll 2
-        for (int r = 0; r < a.splits; r++)
+        for (int r = 0; r < a.parts; r++)
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 if (UNIT == 2)
                     z[u] = __fadd2_rn(z[u], __ldcs(reinterpret_cast<const float2 *>(from[u])));
                 else
                     z[u].x += __ldcs(from[u]);
-                from[u] += run;
+                from[u] += step;
             }
 #pragma unroll
         for (int u = 0; u < U; u++)
@@ -468,30 +468,31 @@ Operand operand(const Laid &l, const uint8_t *workspace, bool turned)
     return o;
 }
 
-// Tile width, CTAs of a tile and runs of a product, by an estimate in clocks of
+// Tile width, CTAs of a tile and parts of a product, by an estimate in clocks of
 // what was measured (19456 x 1024, 1024 and 4096 terms): a stage of 64 terms takes 590
 // on 256 columns of a pair of CTAs and 320 on 128, 650, 390 and 335 on 256, 128 and
-// 64 of one CTA; and the join of runs, which pays for long sums of few tiles (50000
-// pixels' gradient of a 64 x 64 weight: 211 us in one run, 18 in 32; of 32768 pixels'
+// 64 of one CTA; and the join of parts, which pays for long sums of few tiles (50000
+// pixels' gradient of a 64 x 64 weight: 211 us in one part, 18 in 32; of 32768 pixels'
 // 1024 x 1024 one: 162 and, in 4, 50).
 struct Cut {
-    int tile_n, pair, splits;
+    int tile_n, pair, parts, part_chunks, run_chunks;
     unsigned pitch;
     size_t bytes;
 };
 // through: a single run goes through the workspace as well.  A run is as long as its
 // accumulator's cut sums allow, n 1e-9 for n terms: float32 inputs 768 (8e-7, about
 // what float32 arithmetic leaves), 16-bit ones 2048 for a float32 result, else 16384.
+// Parts are several only where they are a few waves of tiles, so that their sums take
+// no more than 60 MB; else there is one, the size of the result.
 Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool through)
 {
     const long long chunks = (terms + 63) / 64;
     const int products = dtype == RZ_F32 ? 6 : 1;
     const long long longest = dtype == RZ_F32 ? 12 : out_dtype == RZ_F32 ? 32 : 256;
-    const int fewest = static_cast<int>((chunks + longest - 1) / longest);
     Cut best{};
     double least = 0.0;
     const unsigned pitch = static_cast<unsigned>(up(N, 8));
-    const double of_split = 170.0 + 4.0 * M * pitch / 2500.0;
+    const double of_part = 170.0 + 4.0 * M * pitch / 2500.0;
     for (int pair = 0; pair < 2; pair++)
         for (int tile = 256; tile >= (pair ? 128 : 64); tile /= 2) {
             const long long across = (N + tile - 1) / tile;
@@ -500,27 +501,27 @@ Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool t
             const int rows = pair ? 256 : 128, slots = pair ? kLinSms / 2 : kLinSms;
             const long long tiles = static_cast<long long>((M + rows - 1ull) / rows) * across;
             const auto consider = [&](long long want) {
-                want = std::min<long long>(std::max<long long>(want, fewest), chunks);
-                const long long run = (chunks + want - 1) / want;
-                const int splits = static_cast<int>((chunks + run - 1) / run);
-                const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
-                double t = waves * (run * products * stage + 300) + 8.0 * tile + (pair ? 1000 : 0);
-                const bool joined = splits > 1 || through;
-                if (joined) t += 4500 + of_split * splits + 4.0 * M * pitch / 2500.0;
+                const long long part = (chunks + want - 1) / want;
+                const int parts = static_cast<int>((chunks + part - 1) / part);
+                const long long runs = (part + longest - 1) / longest;
+                const double waves = static_cast<double>((tiles * parts + slots - 1) / slots);
+                double t = waves * (part * products * stage + 300 * runs) + 8.0 * tile + (pair ? 1000 : 0);
+                const bool joined = parts > 1 || runs > 1 || through;
+                if (joined) t += 4500 + of_part * parts + 4.0 * M * pitch / 2500.0;
                 if (!best.tile_n || t < least) {
                     least = t;
-                    best = {tile, pair, splits, pitch, joined ? sizeof(float) * splits * static_cast<size_t>(M) * pitch : 0};
+                    best = {tile, pair, parts, static_cast<int>(part), static_cast<int>((part + runs - 1) / runs), pitch,
+                            joined ? sizeof(float) * parts * static_cast<size_t>(M) * pitch : 0};
                 }
             };
-            consider(fewest);
-            consider(fewest + 1);
-            // of the runs that make one wave, two or three: as many as there can be, or those whose joins cost what they save
+            consider(1);
+            // of the parts that make one wave, two or three: as many as there can be, or those whose joins cost what they save
             for (int waves = 1; waves <= 3; waves++) {
-                const long long most = std::min<long long>(waves * static_cast<long long>(slots) / tiles, fewest + 63);
-                if (most <= fewest) continue;
+                const long long most = std::min<long long>({waves * static_cast<long long>(slots) / tiles, chunks, 64});
+                if (most <= 1) continue;
                 consider(most);
-                const long long even = std::lround(std::sqrt(waves * static_cast<double>(chunks) * products * stage / of_split));
-                if (even < most) consider(even);
+                const long long even = std::lround(std::sqrt(waves * static_cast<double>(chunks) * products * stage / of_part));
+                if (even > 1 && even < most) consider(even);
             }
         }
     return best;
@@ -612,7 +613,9 @@ cudaError_t product(const Operand &a, const Operand &b, const Finish &f, int out
     p.b = b;
     p.f = f;
     p.out_dtype = out_dtype;
-    p.splits = c.splits;
+    p.parts = c.parts;
+    p.part_chunks = c.part_chunks;
+    p.run_chunks = c.run_chunks;
     p.part = c.bytes ? part : nullptr;
     p.part_pitch = c.pitch;
     p.tile_n = c.tile_n;
@@ -620,7 +623,7 @@ cudaError_t product(const Operand &a, const Operand &b, const Finish &f, int out
     p.status = status;
     cudaError_t e = launch_product(p, stream);
     if (e != cudaSuccess || !c.bytes) return e;
-    const JoinArgs j{f, part, c.pitch, c.splits, 0, sums};
+    const JoinArgs j{f, part, c.pitch, c.parts, 0, sums};
     if (out_dtype == RZ_F32) return join_of<float>(j, stream);
     return out_dtype == RZ_BF16 ? join_of<__nv_bfloat16>(j, stream) : join_of<__half>(j, stream);
 }

@@ -170,14 +170,15 @@ struct Operand {
     int bf16;
 };
 
-// D = A B^T over the terms.  part: the terms are cut into `splits` runs, whose float32
-// sums go to part[run][M][part_pitch] for k_linear_join; else (one run) the kernel
-// itself finishes them, where direct_out says that it can.
+// D = A B^T over the terms.  part: the terms are cut into `parts`, whose float32 sums,
+// each added up in runs, go to part[i][M][part_pitch] for k_linear_join; else (one run)
+// the kernel itself finishes them, where direct_out says that it can.
 struct Product {
     Operand a, b;
     Finish f;
     int out_dtype;
-    int splits;
+    int parts;
+    int part_chunks, run_chunks;    // 64-term chunks of a part and of a run
     float *part;
     unsigned part_pitch;    // floats
     int tile_n;             // 64 (without a pair), 128 or 256

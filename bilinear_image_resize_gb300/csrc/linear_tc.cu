@@ -26,8 +26,11 @@
 // accumulator: the others are below 2^-23 of |a| |b|.
 //
 // The accumulator cuts what it adds (it does not round): a sum of n terms ends up
-// smaller by about n 1e-9 of its size.  So long sums are cut into runs, which
-// k_linear_join adds up in rounded arithmetic.
+// smaller by about n 1e-9 of its size.  So long sums are cut into runs, one after
+// another in the same CTA, each added to the tile's float32 sums as it leaves (TMA's
+// add, rounded): the sums of a tile lie in memory once, however long they are.  Only
+// where there are few tiles do several CTAs each take a part of a sum, with sums of
+// its own.  k_linear_join adds the parts up and finishes them.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -70,10 +73,10 @@ constexpr int kHead = (static_cast<int>(sizeof(Vars)) + kBias + 1023) / 1024 * 1
 
 struct TcArgs {
     Finish f;
-    unsigned tiles_m, tiles_n, tiles;   // tiles: of all runs
+    unsigned tiles_m, tiles_n, tiles;   // tiles: of all parts
     int tile_n, stages;
-    int chunks, run;                    // 64-term chunks, and of a run
-    int planes;
+    int chunks, part, run;              // 64-term chunks, and of a part and of a run
+    int products;                       // of planes, 1 or 6
     unsigned group;                     // rows of tiles that are walked together
     int a_turned, b_turned;
     int a_merged, b_merged;             // a turned operand's rows come in one box
@@ -226,16 +229,23 @@ __device__ __forceinline__ void block_add(const uint8_t *block, int sub, float2 
         for (int i = 0; i < VE / 2; i++) z[h * VE / 2 + i] = __fadd2_rn(z[h * VE / 2 + i], v[i]);
     }
 }
-// A filled block on its way to memory, clipped to the matrix.
-__device__ __forceinline__ void block_store(const CUtensorMap *map, const uint8_t *block, int n, int m, int run)
+// A filled block on its way to memory, clipped to the matrix; `add`: to what is there.
+template <bool MAY_ADD>
+__device__ __forceinline__ void block_store(const CUtensorMap *map, const uint8_t *block, int n, int m, int part, bool add)
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
-        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                         reinterpret_cast<uint64_t>(map)),
-                     "r"(n), "r"(m), "r"(run), "r"(smem_addr(block))
-                     : "memory");
+        if (MAY_ADD && add)
+            asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                             reinterpret_cast<uint64_t>(map)),
+                         "r"(n), "r"(m), "r"(part), "r"(smem_addr(block))
+                         : "memory");
+        else
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                             reinterpret_cast<uint64_t>(map)),
+                         "r"(n), "r"(m), "r"(part), "r"(smem_addr(block))
+                         : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
 }
@@ -246,29 +256,28 @@ __device__ __forceinline__ void blocks_read()
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
 }
 
-// A tile's place and the chunks of its run, each once for every product of planes.
+// A tile's place and the chunks of its part.
 struct Tile {
-    unsigned m, n, run;
-    int first, last, stages;
+    unsigned m, n, part;
+    int first, last;
 };
 __device__ __forceinline__ Tile tile_at(const TcArgs &a, unsigned t)
 {
     Tile r;
     const unsigned all = a.tiles_m * a.tiles_n, x = t % all, per = a.group * a.tiles_n;
     const unsigned g = x / per, y = x - g * per, rows = min(a.group, a.tiles_m - g * a.group);
-    r.run = t / all;
+    r.part = t / all;
     r.m = g * a.group + y % rows;
     r.n = y / rows;
-    r.first = static_cast<int>(r.run) * a.run;
-    r.last = min(a.chunks, r.first + a.run);
-    r.stages = (r.last - r.first) * (a.planes == 1 ? 1 : 6);
+    r.first = static_cast<int>(r.part) * a.part;
+    r.last = min(a.chunks, r.first + a.part);
     return r;
 }
 
 // The planes of the j-th product of planes, the smallest first.
-__device__ __forceinline__ void planes_of(int planes, int j, int &a, int &b)
+__device__ __forceinline__ void planes_of(int products, int j, int &a, int &b)
 {
-    if (planes == 1) {
+    if (products == 1) {
         a = b = 0;
         return;
     }
@@ -283,6 +292,8 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
             const __grid_constant__ CUtensorMap map_residual)
 {
+    // sums that go to the workspace may come in several runs
+    constexpr bool RUNS = sizeof(T) == 4 && ACT == RZ_ACT_NONE;
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ Vars vars;
     uint64_t *const full = vars.full, *const empty = vars.empty, *const done = vars.done, *const taken = vars.taken;
@@ -345,32 +356,36 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step) {
                 const Tile w = tile_at(a, t);
                 const int row = of_b ? static_cast<int>(w.n * a.tile_n + rank * rows_b) : static_cast<int>((w.m * CG + rank) * kTileM);
-                // (counted in chunks: past the last one's terms may lie 2^31)
-                int j = 0, chunk = w.first, pa, pb;
-                planes_of(a.planes, j, pa, pb);
-                for (int c = 0; c < w.stages; c++) {
-                    ok = __all_sync(0xffffffffu, wait_for(empty + s, phase ^ 1, a.status));
-                    if (!ok) break;
-                    const uint32_t at = to + s * stage_bytes, bar = bars + 8 * s;
-                    const int plane = of_b ? pb : pa, k0 = chunk * kTerms;
-                    if (elected()) {
-                        if (!of_b && rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
-                        if (!turned)
-                            load_box<CG>(map, at, bar, k0, row, 0, plane);
-                        else if (merged)
-                            load_box<CG>(map, at, bar, 0, k0, row / 64, plane);
-                        else
-                            for (int i = 0; i < rows; i += 64) load_box<CG>(map, at + i * 128, bar, row + i, k0, 0, plane);
-                    }
-                    __syncwarp();
-                    asked++;
-                    if (++s == a.stages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                    if (++chunk == w.last) {
-                        chunk = w.first;
-                        planes_of(a.planes, ++j, pa, pb);
+                for (int r0 = w.first, r1; r0 < w.last && ok; r0 = r1) {
+                    r1 = RUNS ? min(w.last, r0 + a.run) : w.last;
+                    // a run's chunks, once for every product of planes (counted in chunks: past the last one's terms may
+                    // lie 2^31)
+                    int j = 0, chunk = r0, pa, pb;
+                    planes_of(a.products, j, pa, pb);
+                    for (int c = (r1 - r0) * a.products; c > 0; c--) {
+                        ok = __all_sync(0xffffffffu, wait_for(empty + s, phase ^ 1, a.status));
+                        if (!ok) break;
+                        const uint32_t at = to + s * stage_bytes, bar = bars + 8 * s;
+                        const int plane = of_b ? pb : pa, k0 = chunk * kTerms;
+                        if (elected()) {
+                            if (!of_b && rank == 0) dev::mbar_arrive_expect_tx(full + s, CG * stage_bytes);
+                            if (!turned)
+                                load_box<CG>(map, at, bar, k0, row, 0, plane);
+                            else if (merged)
+                                load_box<CG>(map, at, bar, 0, k0, row / 64, plane);
+                            else
+                                for (int i = 0; i < rows; i += 64) load_box<CG>(map, at + i * 128, bar, row + i, k0, 0, plane);
+                        }
+                        __syncwarp();
+                        asked++;
+                        if (++s == a.stages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
+                        if (++chunk == r1) {
+                            chunk = r0;
+                            planes_of(a.products, ++j, pa, pb);
+                        }
                     }
                 }
             }
@@ -390,33 +405,37 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
             unsigned i = 0;
             const uint64_t desc_a = tile_desc(ring, a.a_turned), desc_b = tile_desc(ring + kBytesA, a.b_turned);
             const uint32_t step_a = (a.a_turned ? 2048 : 32) >> 4, step_b = (a.b_turned ? 2048 : 32) >> 4;
-            for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
+            for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step) {
                 const Tile w = tile_at(a, t);
-                const uint32_t acc = tmem + (i & 1) * 256;
-                ok = __all_sync(0xffffffffu, wait_for(taken + (i & 1), (i >> 1 & 1) ^ 1, a.status));
-                if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (int c = 0; c < w.stages; c++) {
-                    ok = __all_sync(0xffffffffu, wait_for(full + s, phase, a.status));
+                for (int r0 = w.first, r1; r0 < w.last && ok; r0 = r1, i++) {
+                    r1 = RUNS ? min(w.last, r0 + a.run) : w.last;
+                    const uint32_t acc = tmem + (i & 1) * 256;
+                    ok = __all_sync(0xffffffffu, wait_for(taken + (i & 1), (i >> 1 & 1) ^ 1, a.status));
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    // the ring lies below 2^18: no carry leaves the address
-                    const uint32_t at = static_cast<uint32_t>(s * stage_bytes) >> 4;
-                    const uint64_t da = desc_a + at, db = desc_b + at;
-                    if (elected()) {
+                    const int stages = (r1 - r0) * a.products;
+                    for (int c = 0; c < stages; c++) {
+                        ok = __all_sync(0xffffffffu, wait_for(full + s, phase, a.status));
+                        if (!ok) break;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        // the ring lies below 2^18: no carry leaves the address
+                        const uint32_t at = static_cast<uint32_t>(s * stage_bytes) >> 4;
+                        const uint64_t da = desc_a + at, db = desc_b + at;
+                        if (elected()) {
 #pragma unroll
-                        for (uint32_t k = 0; k < kTerms / 16; k++)
-                            mma<CG>(acc, da + k * step_a, db + k * step_b, a.idesc, c > 0 || k > 0);
-                        commit<CG>(empty + s);
+                            for (uint32_t k = 0; k < kTerms / 16; k++)
+                                mma<CG>(acc, da + k * step_a, db + k * step_b, a.idesc, c > 0 || k > 0);
+                            commit<CG>(empty + s);
+                        }
+                        __syncwarp();
+                        if (++s == a.stages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
                     }
+                    if (ok && elected()) commit<CG>(done + (i & 1));
                     __syncwarp();
-                    if (++s == a.stages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
                 }
-                if (ok && elected()) commit<CG>(done + (i & 1));
-                __syncwarp();
             }
         }
     } else if (warp >= 4) {
@@ -432,7 +451,7 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
         uint32_t phases = 0, coming = 0;        // a bit of each place: its barrier's phase, and whether a residual is on its way
         unsigned i = 0;
         bool ok = true;
-        for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step, i++) {
+        for (unsigned t = first_tile; t < a.tiles && ok; t += tile_step) {
             const Tile w = tile_at(a, t);
             const unsigned m0 = (w.m * CG + rank) * kTileM + 32 * quarter, n0 = w.n * a.tile_n + (e >> 2) * cols;
             const int live = m0 < a.f.M && n0 < a.f.N ? min(blocks, static_cast<int>((a.f.N - n0 + BC - 1) / BC)) : 0;
@@ -446,98 +465,103 @@ k_linear_tc(const __grid_constant__ TcArgs a, const __grid_constant__ CUtensorMa
                              "r"(static_cast<int>(m0)), "r"(0), "r"(smem_addr(bar))
                              : "memory");
             };
-            // what does not wait for the tile: its first residual, and bias, four columns a lane
-            if (a.f.has_residual && live && lane == 0) {
-                blocks_read<1>();
-                fetch(0, flip);
-            }
-            float bias[4] = {};
-            if (a.f.bias)
-#pragma unroll
-                for (int q = 0; q < 4; q++)
-                    if (4 * lane + q < cols && n0 + 4 * lane + q < a.f.N) bias[q] = __ldg(a.f.bias + n0 + 4 * lane + q);
-            ok = __all_sync(0xffffffffu, wait_for(done + (i & 1), i >> 1 & 1, a.status));
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            // the four warps of these columns write the same; none still reads what they held two tiles ago, which all had
-            // taken before this tile was begun
-            float4 *const columns = reinterpret_cast<float4 *>(raw) + (i & 1) * 64 + (e >> 2) * 32;
-            if (a.f.bias) {
-                columns[lane] = make_float4(bias[0], bias[1], bias[2], bias[3]);
-                __syncwarp();
-            }
-            const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + (e >> 2) * cols;
-            // a block's columns are asked for while the one before is worked on
-            uint32_t v[SUBS][16];
-#pragma unroll
-            for (int q = 0; q < SUBS; q++) tmem_load(acc + 16 * q, v[q]);
-            for (int b = 0; b < blocks; b++) {
-                float2 z[SUBS][8];
-#pragma unroll
-                for (int q = 0; q < SUBS; q++) {
-                    tmem_wait(v[q]);
-#pragma unroll
-                    for (int j = 0; j < 8; j++) z[q][j] = make_float2(__uint_as_float(v[q][2 * j]), __uint_as_float(v[q][2 * j + 1]));
+            for (int r0 = w.first; r0 < w.last && ok; r0 = RUNS ? r0 + a.run : w.last, i++) {
+                const bool more = RUNS && r0 > w.first;
+                // sums are added in their order: the run before is in memory
+                if (more && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                // what does not wait for the tile: its first residual, and bias, four columns a lane
+                if (a.f.has_residual && live && lane == 0) {
+                    blocks_read<1>();
+                    fetch(0, flip);
                 }
-                if (b + 1 < blocks)
+                float bias[4] = {};
+                if (a.f.bias)
 #pragma unroll
-                    for (int q = 0; q < SUBS; q++) tmem_load(acc + (b + 1) * BC + 16 * q, v[q]);
-                // (read by four columns: by shuffles, one a column, they took the data path of shared memory for 18 us of 368)
-                if (a.f.bias && b < live)
+                    for (int q = 0; q < 4; q++)
+                        if (4 * lane + q < cols && n0 + 4 * lane + q < a.f.N) bias[q] = __ldg(a.f.bias + n0 + 4 * lane + q);
+                ok = __all_sync(0xffffffffu, wait_for(done + (i & 1), i >> 1 & 1, a.status));
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                // the four warps of these columns write the same; none still reads what they held two tiles ago, which all had
+                // taken before this tile was begun
+                float4 *const columns = reinterpret_cast<float4 *>(raw) + (i & 1) * 64 + (e >> 2) * 32;
+                if (a.f.bias) {
+                    columns[lane] = make_float4(bias[0], bias[1], bias[2], bias[3]);
+                    __syncwarp();
+                }
+                const uint32_t acc = tmem + (i & 1) * 256 + (static_cast<uint32_t>(32 * quarter) << 16) + (e >> 2) * cols;
+                // a block's columns are asked for while the one before is worked on
+                uint32_t v[SUBS][16];
+#pragma unroll
+                for (int q = 0; q < SUBS; q++) tmem_load(acc + 16 * q, v[q]);
+                for (int b = 0; b < blocks; b++) {
+                    float2 z[SUBS][8];
+#pragma unroll
+                    for (int q = 0; q < SUBS; q++) {
+                        tmem_wait(v[q]);
+#pragma unroll
+                        for (int j = 0; j < 8; j++) z[q][j] = make_float2(__uint_as_float(v[q][2 * j]), __uint_as_float(v[q][2 * j + 1]));
+                    }
+                    if (b + 1 < blocks)
+#pragma unroll
+                        for (int q = 0; q < SUBS; q++) tmem_load(acc + (b + 1) * BC + 16 * q, v[q]);
+                    // (read by four columns: by shuffles, one a column, they took the data path of shared memory for 18 us of 368)
+                    if (a.f.bias && b < live)
+#pragma unroll
+                        for (int q = 0; q < SUBS; q++)
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2) {
+                                const float4 c = columns[(b * BC + 16 * q) / 4 + j / 2];
+                                z[q][j] = __fadd2_rn(z[q][j], make_float2(c.x, c.y));
+                                z[q][j + 1] = __fadd2_rn(z[q][j + 1], make_float2(c.z, c.w));
+                            }
+                    if (b + 1 == blocks) {
+                        // this warp's share of the tile is in registers, its bias read
+                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (CG == 1)
+                                dev::mbar_arrive(taken + (i & 1));
+                            else
+                                arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), 0));
+                        }
+                    }
+                    if (b >= live) continue;
+                    const int n = static_cast<int>(n0) + b * BC;
+                    if (a.f.has_residual && b + 1 < live && lane == 0) {
+                        blocks_read<0>();
+                        fetch(b + 1, flip ^ 1);
+                    }
+                    if (a.f.has_pre) {
+                        uint8_t *block = out + (a.f.has_residual ? 2 : flip) * kBlockBytes;
+                        if (lane == 0) blocks_read<1>();
+                        __syncwarp();
+#pragma unroll
+                        for (int q = 0; q < SUBS; q++) block_write<T>(block, q, z[q]);
+                        block_store<false>(&map_pre, block, n, static_cast<int>(m0), 0, false);
+                        if (!a.f.has_residual) flip ^= 1;
+                    }
 #pragma unroll
                     for (int q = 0; q < SUBS; q++)
 #pragma unroll
-                        for (int j = 0; j < 8; j += 2) {
-                            const float4 c = columns[(b * BC + 16 * q) / 4 + j / 2];
-                            z[q][j] = __fadd2_rn(z[q][j], make_float2(c.x, c.y));
-                            z[q][j + 1] = __fadd2_rn(z[q][j + 1], make_float2(c.z, c.w));
-                        }
-                if (b + 1 == blocks) {
-                    // this warp's share of the tile is in registers, its bias read
-                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CG == 1)
-                            dev::mbar_arrive(taken + (i & 1));
-                        else
-                            arrive_in_cluster(in_cta(smem_addr(taken + (i & 1)), 0));
+                        for (int j = 0; j < 8; j++) z[q][j] = activated<T, ACT>(z[q][j]);
+                    uint8_t *block = out + flip * kBlockBytes;
+                    if (a.f.has_residual) {
+                        ok = __all_sync(0xffffffffu, wait_for(&came[e][flip], phases >> flip & 1, a.status));
+                        if (!ok) break;
+                        phases ^= 1u << flip;
+                        coming &= ~(1u << flip);
+#pragma unroll
+                        for (int q = 0; q < SUBS; q++) block_add<T>(block, q, z[q]);
+                    } else {
+                        if (lane == 0) blocks_read<1>();
+                        __syncwarp();
                     }
-                }
-                if (b >= live) continue;
-                const int n = static_cast<int>(n0) + b * BC;
-                if (a.f.has_residual && b + 1 < live && lane == 0) {
-                    blocks_read<0>();
-                    fetch(b + 1, flip ^ 1);
-                }
-                if (a.f.has_pre) {
-                    uint8_t *block = out + (a.f.has_residual ? 2 : flip) * kBlockBytes;
-                    if (lane == 0) blocks_read<1>();
-                    __syncwarp();
 #pragma unroll
                     for (int q = 0; q < SUBS; q++) block_write<T>(block, q, z[q]);
-                    block_store(&map_pre, block, n, static_cast<int>(m0), 0);
-                    if (!a.f.has_residual) flip ^= 1;
+                    block_store<RUNS>(&map_out, block, n, static_cast<int>(m0), static_cast<int>(w.part), more);
+                    flip ^= 1;
                 }
-#pragma unroll
-                for (int q = 0; q < SUBS; q++)
-#pragma unroll
-                    for (int j = 0; j < 8; j++) z[q][j] = activated<T, ACT>(z[q][j]);
-                uint8_t *block = out + flip * kBlockBytes;
-                if (a.f.has_residual) {
-                    ok = __all_sync(0xffffffffu, wait_for(&came[e][flip], phases >> flip & 1, a.status));
-                    if (!ok) break;
-                    phases ^= 1u << flip;
-                    coming &= ~(1u << flip);
-#pragma unroll
-                    for (int q = 0; q < SUBS; q++) block_add<T>(block, q, z[q]);
-                } else {
-                    if (lane == 0) blocks_read<1>();
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int q = 0; q < SUBS; q++) block_write<T>(block, q, z[q]);
-                block_store(&map_out, block, n, static_cast<int>(m0), static_cast<int>(w.run));
-                flip ^= 1;
             }
         }
         if (lane == 0) {
@@ -598,13 +622,13 @@ bool encode(const Operand &o, unsigned share, CUtensorMap *map, int *merged)
 }
 
 // A result's (or residual's, or pre's) tensor map: blocks of 64 bytes by 32 rows, of
-// `runs` matrices one after another.
-bool encode_out(const Rows &r, unsigned M, unsigned N, int dtype, int runs, size_t run_bytes, CUtensorMap *map)
+// `parts` matrices one after another.
+bool encode_out(const Rows &r, unsigned M, unsigned N, int dtype, int parts, size_t part_bytes, CUtensorMap *map)
 {
     std::memset(map, 0, sizeof(*map));
     const size_t es = dtype_size(dtype), pitch = r.v.pitch % 16 ? N * es : static_cast<size_t>(r.v.pitch);    // of one row it is any
-    const cuuint64_t dims[3] = {N, M, static_cast<cuuint64_t>(runs)};
-    const cuuint64_t strides[2] = {pitch, runs > 1 ? run_bytes : pitch};
+    const cuuint64_t dims[3] = {N, M, static_cast<cuuint64_t>(parts)};
+    const cuuint64_t strides[2] = {pitch, parts > 1 ? part_bytes : pitch};
     const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(kBlockRow / es), 32, 1}, steps[3] = {1, 1, 1};
     const CUtensorMapDataType type = dtype == RZ_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                      : dtype == RZ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -672,14 +696,14 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     a.f = p.f;
     int dtype = p.out_dtype;
     if (p.part) {
-        // runs of a sum, and what TMA cannot write, leave as they are, float32; k_linear_join finishes them
+        // sums in parts or runs, and what TMA cannot write, leave as they are, float32; k_linear_join finishes them
         dtype = RZ_F32;
         a.f = Finish{};
         a.f.M = p.f.M;
         a.f.N = p.f.N;
         a.f.out.v = {reinterpret_cast<uint8_t *>(p.part), static_cast<long long>(p.part_pitch) * 4, 0};
     }
-    if (!encode_out(a.f.out, a.f.M, a.f.N, dtype, p.splits, static_cast<size_t>(p.part_pitch) * 4 * a.f.M, &m.out))
+    if (!encode_out(a.f.out, a.f.M, a.f.N, dtype, p.parts, static_cast<size_t>(p.part_pitch) * 4 * a.f.M, &m.out))
         return cudaErrorInvalidValue;
     m.pre = m.residual = m.out;     // where there is none
     if (a.f.has_pre && !encode_out(a.f.pre, a.f.M, a.f.N, dtype, 1, 0, &m.pre)) return cudaErrorInvalidValue;
@@ -688,14 +712,15 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     a.tile_n = p.tile_n;
     a.tiles_m = (p.f.M + cg * kTileM - 1) / (cg * kTileM);
     a.tiles_n = (p.f.N + p.tile_n - 1) / p.tile_n;
-    a.planes = p.a.planes;
+    a.products = p.a.planes == 1 ? 1 : 6;
     // Tiles of a row next to each other read its A at once, and B out of L2 where that holds it (65536 x 1024 x 4096: 341 us,
     // rows of tiles in groups of eight 373).  A larger B is read once for eight rows of tiles (8192 x 8192 x 8192: 611 us, by
     // single rows 650).
     a.group = 2.0 * p.f.N * p.b.terms * p.b.planes > 48e6 ? 8 : 1;
     a.chunks = static_cast<int>((p.a.terms + kTerms - 1) / kTerms);
-    a.run = (a.chunks + p.splits - 1) / p.splits;
-    const unsigned long long tiles = static_cast<unsigned long long>(a.tiles_m) * a.tiles_n * p.splits;
+    a.part = p.part_chunks;
+    a.run = p.run_chunks;
+    const unsigned long long tiles = static_cast<unsigned long long>(a.tiles_m) * a.tiles_n * p.parts;
     if (tiles > 0x7fffffffull) return cudaErrorInvalidConfiguration;
     a.tiles = static_cast<unsigned>(tiles);
     a.stages = std::min(kRing, (kSmem - kHead - kEpiWarps * a.places * kBlockBytes) / (kBytesA + p.tile_n / cg * kTerms * 2));

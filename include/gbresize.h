@@ -579,7 +579,9 @@ RZ_API int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_ma
  * data is not touched), 16-byte aligned, of any content, the call's own until the
  * stream has passed it; up to eight pixels need none.  Maps and weights whose rows
  * begin and end at multiples of 16 bytes, evenly apart, are read and written where
- * they lie; others pass through the workspace.  status: an int that the device can
+ * they lie; others pass through the workspace.  It holds at most a copy of each
+ * operand (6 bytes an element of float32, 2 of 16 bits) and, of the largest result, a
+ * float32 matrix of its size or 64 MB, whatever the sums' length.  status: an int that the device can
  * write (its own memory or pinned host memory) or NULL; a kernel whose bounded waits
  * (1 s of its own time: what it spends preempted does not count) run out writes
  * RZ_ERR_TIMEOUT there and leaves the result unfinished.  Asynchronous on `stream`;

@@ -211,3 +211,27 @@ def test_binding_names():
                  "map_qk_norm_grad_workspace", "map_position_bias", "map_position_bias_grad", "map_position_bias_grad_workspace",
                  "map_position_buckets"):
         assert name in rz.__all__ and getattr(rz, name).__doc__
+
+
+@pytest.mark.parametrize("pixels, C, K", [(65536, 1024, 4096), (1 << 18, 4096, 4096), (2_200_000, 4096, 4096), (1 << 24, 64, 64), (5000, 1000, 300),
+                                          ((1 << 31) - 1, 8, 8), (100, 65536, 65536), (300, 1030, 8)])
+@pytest.mark.parametrize("dtype, wtype", [(1, 1), (2, 2), (2, 1), (3, 1)])
+def test_workspaces_stay_of_the_size_of_the_maps(lib, nat, pixels, C, K, dtype, wtype):
+    """Whatever the sum's length: the operands' layouts (6 bytes an element of float32, 2 of 16 bits, rows rounded to 16 bytes),
+    one float32 matrix of each result's size or 64 MB, and a row of sums for every few pixels."""
+    es, ws = 4 if dtype == 1 else 2, 4 if wtype == 1 else 2
+    d = nat.RzLinear(1, 1, pixels, C, K, dtype, 1)
+    at = [1 << 48, 1 << 49, 1 << 50, 1 << 51, 1 << 52, 1 << 53]
+    x, y, pre, dx = (nat.RzMap(a, pixels * n * es, pixels * n * es) for a, n in zip(at, (C, K, K, C)))
+    n = ctypes.c_size_t(0)
+    up = lambda v: (v + 7) // 8 * 8       # noqa: E731
+    laid = 6 if dtype == 1 else 2
+    most = 64 << 20
+    assert lib.map_linear_workspace(d, x, at[4], C * es, None, None, y, ctypes.byref(n)) == 0
+    assert n.value <= laid * up(C) * (pixels + K) + max(4 * pixels * up(K), most) + 1024
+    assert lib.map_linear_grad_workspace(d, y, x, at[4], C * es, pre, dx, at[5], C * ws, wtype, ctypes.byref(n)) == 0
+    operands = laid * (up(C) * (pixels + K) + up(K) * pixels)
+    assert n.value <= operands + max(4 * pixels * up(C), 4 * K * up(C), most) + 4 * K * 700 + 4096
+    # towards the weight alone
+    assert lib.map_linear_grad_workspace(d, y, x, at[4], C * es, pre, None, at[5], C * ws, wtype, ctypes.byref(n)) == 0
+    assert n.value <= operands + max(4 * K * up(C), most) + 4 * K * 700 + 4096
