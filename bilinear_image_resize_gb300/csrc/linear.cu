@@ -480,15 +480,18 @@ struct Cut {
     size_t bytes;
 };
 // through: a single run goes through the workspace as well.  A run is as long as its
-// accumulator's cut sums allow, n 1e-9 for n terms: float32 inputs 768 (8e-7, about
-// what float32 arithmetic leaves), 16-bit ones 2048 for a float32 result, else 16384.
+// accumulator's cut sums allow (linear_tc.cu says by how much), and long enough that its
+// products hide its way out: float32 operands 512 terms (off by 1e-6; 768 terms 1.5e-6 at
+// the same speed, 256 terms 4e-7 and 7% slower), 16-bit ones 1024 for a float32 result
+// (65536 x 1024 x 4096: 498 us; 446 of 2048 terms, 686 of 512), else 8192 of float16 and
+// 16384 of bfloat16, where what is cut is a tenth and a hundredth of half a step.
 // Parts are several only where they are a few waves of tiles, so that their sums take
 // no more than 60 MB; else there is one, the size of the result.
 Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool through)
 {
     const long long chunks = (terms + 63) / 64;
     const int products = dtype == RZ_F32 ? 6 : 1;
-    const long long longest = dtype == RZ_F32 ? 12 : out_dtype == RZ_F32 ? 32 : 256;
+    const long long longest = dtype == RZ_F32 ? 8 : out_dtype == RZ_F32 ? 16 : dtype == RZ_F16 ? 128 : 256;
     Cut best{};
     double least = 0.0;
     const unsigned pitch = static_cast<unsigned>(up(N, 8));

@@ -23,10 +23,12 @@
 // which.  float32 operands come as three bfloat16 planes x = x0 + x1 + x2, each
 // the leading bits of what the ones before it leave; of the nine products of
 // planes the six with i + j <= 2 are summed, the smallest first, in the one
-// accumulator: the others are below 2^-23 of |a| |b|.
+// accumulator: the others are below 2^-21 of |a| |b| (2^-24 on the whole).
 //
-// The accumulator cuts what it adds (it does not round): a sum of n terms ends up
-// smaller by about n 1e-9 of its size.  So long sums are cut into runs, one after
+// The accumulator cuts what it adds (it does not round): a sum of n terms of one sign
+// ends up smaller by about n 2e-9 of its size, of float16 operands, whose products
+// have more bits to lose, by n 6e-9 (up to three times that where a few terms are most
+// of a sum).  So long sums are cut into runs, one after
 // another in the same CTA, each added to the tile's float32 sums as it leaves (TMA's
 // add, rounded): the sums of a tile lie in memory once, however long they are.  Only
 // where there are few tiles do several CTAs each take a part of a sum, with sums of

@@ -564,8 +564,9 @@ RZ_API int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_ma
  * bytes apart), b float[K] or NULL, act as in map_group_norm, residual a map
  * of y's shape or NULL.  pre: a map of y's shape that takes z, rounded, for the
  * gradient, or NULL.  x: C channels; y, residual and pre: K.  Products are
- * summed in float32; the result is rounded once.  float32 products are off by
- * about 1e-6 of the sum of their terms' magnitudes; GELU of 16-bit maps by
+ * summed in float32; the result is rounded once.  The tensor cores cut sums toward
+ * 0: those of float32 maps are off by about 1e-6 of the sum of their terms'
+ * magnitudes (3e-6 where a few terms are most of it); GELU of 16-bit maps by
  * (25 + 3 |z|) |z| / 2^26 before it is rounded, and below 0 by 3e-4 of itself where
  * that is less.  A value that is not finite
  * reaches the results of its own row or column alone; an infinity of float32 maps
@@ -606,7 +607,8 @@ RZ_API int map_linear(const rz_linear *d, const rz_map *x, const void *weight, s
  * dweight K rows of C elements of dweight_dtype (the map's dtype or RZ_F32),
  * dweight_pitch bytes apart, dbias device float[K]; each may be NULL, is written,
  * not added to, and overlaps no input; an empty map makes dweight and dbias 0.
- * Sums run in a fixed order, in float32; dz of 16-bit maps enters dx and dweight as
+ * Sums run in a fixed order, in float32 (a float32 dweight of bfloat16 maps is off by
+ * about 2.5e-6 of the sum of its terms' magnitudes, of float16 maps by 6e-6); dz of 16-bit maps enters dx and dweight as
  * a value of its type (rounded once where there is an activation), dbias as float32.
  * Workspace, status and the rest as map_linear.
  */

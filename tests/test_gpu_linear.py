@@ -383,3 +383,52 @@ def test_gelu_of_16_bit_maps_far_below_zero(rz, dtype):
                   torch.from_numpy(z).float().cuda(), act=ACTS["gelu"])
     want = z * sp.ndtr(z)
     check(y, want, ref.stored(want, 3e-4 * np.abs(want), dtype), "y")
+
+
+# The error of a float32 result of n terms, of the sum S of their magnitudes.  The tensor cores cut what they add: a run of
+# r terms of one sign and alike in size ends up short by 3e-9 r at most (float16 operands: 8e-9 r, their products have more
+# bits), the same way every time, runs being 512 terms of float32 operands and 1024 of 16-bit ones at most.  The products of
+# planes that are left out hold 2^-21 of a term at most.  Runs are added in float32, each rounding 2^-24 at most of what is
+# there, of random sign: six deviations of as many as there are runs.
+def held(n, dtype):
+    run = 512 if dtype == "f32" else 1024
+    cut = min(n, run) * (8e-9 if dtype == "f16" else 3e-9)
+    return cut + (2.0 ** -21 if dtype == "f32" else 0.0) + 6 * np.sqrt(np.ceil(n / run)) * 2.0 ** -24
+
+
+def near(got, a, b, bound):
+    """got against a @ b in float64, off by at most `bound` of the magnitudes' sums."""
+    want, S = a.double() @ b.double(), a.double().abs() @ b.double().abs()
+    return float(((got.double() - want).abs() / S).max()) <= bound
+
+
+@pytest.mark.parametrize("positive", [True, False])
+@pytest.mark.parametrize("P, C, K", [(300, 200, 64), (300, 1024, 72), (130, 4096, 40), (100, 65536, 8), (5000, 1536, 1000)])
+def test_float32_products_are_as_good_as_stated(rz, positive, P, C, K):
+    """All terms positive: what is cut adds up, and nothing hides in a cancelled sum."""
+    g = torch.Generator(device="cuda").manual_seed(C)
+    x, w = (torch.rand(s, generator=g, device="cuda") - (0.0 if positive else 0.5) for s in ((1, 1, P, C), (K, C)))
+    y = torch.empty((1, 1, P, K), device="cuda")
+    rz.map_linear(x, y, w)
+    assert near(y[0, 0], x[0, 0], w.T, held(C, "f32"))
+    dy = torch.rand((1, 1, P, K), generator=g, device="cuda") - (0.0 if positive else 0.5)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    rz.map_linear_grad(dy, x, w, dx, dw)
+    assert near(dx[0, 0], dy[0, 0], w, held(K, "f32"))
+    assert near(dw, dy[0, 0].T, x[0, 0], held(P, "f32"))
+
+
+@pytest.mark.parametrize("positive", [True, False])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("P, C, K", [(65536, 64, 64), (65536, 40, 264), (20000, 256, 512), (200000, 8, 16)])
+def test_float32_weight_gradients_are_as_good_as_stated(rz, positive, dtype, P, C, K):
+    g = torch.Generator(device="cuda").manual_seed(P + C)
+    t = getattr(torch, tok.TORCH[dtype])
+    x, dy = ((torch.rand((1, 1, P, n), generator=g, device="cuda") - (0.0 if positive else 0.5)).to(t) for n in (C, K))
+    dw, db = torch.empty((K, C), device="cuda"), torch.empty(K, device="cuda")
+    rz.map_linear_grad(dy, x, torch.zeros((K, C), dtype=t, device="cuda"), None, dw, db)
+    assert near(dw, dy[0, 0].T, x[0, 0], held(P, dtype))
+    assert near(db[:, None], dy[0, 0].T, torch.ones((P, 1), device="cuda"), tok.walk(min(P, 4096)) * 2.0 ** -24)
+    again = torch.empty_like(dw)
+    rz.map_linear_grad(dy, x, torch.zeros((K, C), dtype=t, device="cuda"), None, again)
+    assert torch.equal(dw, again)
