@@ -9,6 +9,7 @@
 // in order.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "linear.h"
 #include "rz_device.h"
@@ -29,6 +30,12 @@ constexpr int kPackWarps = kPackThreads / 32;
 // tensor cores: 16-bit rows of `pitch` bytes, float32 as three planes of bfloat16
 // (each the leading 8 bits of what is left: together all 24).  And their column
 // sums, by chunks of rows.
+//
+// dz = dy act'(pre) of 16-bit maps is rounded to their type here, which a result of that
+// type (dx, dweight) shows no more than its own rounding (2.3e-3 of a bf16 result's
+// size in the 2-norm, 1.7e-3 without it): a second plane would double their products, 90 of the 130 us
+// of 32768 x 1024 -> 1024.  A float32 dweight does take it: what the rounding left,
+// rounded in turn, is a second plane.  A float16 dz past 65504 is infinite.
 struct PackArgs {
     Rows in, slope;
     uint8_t *to;            // null: sums only
@@ -38,6 +45,7 @@ struct PackArgs {
     unsigned chunk;         // rows of a CTA
     int lanes;              // lanes side by side in a row, eight columns each
     int has_slope, act, wide;
+    int second;             // 16-bit: a second plane holds what the first one's rounding left
     unsigned blocks, across;    // CTAs, and of them along a row
 };
 // The matrices of a call in one launch, their CTAs one after another.
@@ -72,7 +80,7 @@ __device__ __forceinline__ float leading(float v)
     return v != v ? v : __uint_as_float(__float_as_uint(v) & 0xffff0000u);
 }
 
-template <class T, bool WIDE>
+template <class T, bool WIDE, bool SECOND>
 __device__ __forceinline__ void pack_block(const PackArgs &a, unsigned bx, unsigned by, float (&sh)[kPackWarps][256])
 {
     constexpr int U = sizeof(T) == 2 ? 4 : 2;       // rows read before the first is used
@@ -113,7 +121,15 @@ __device__ __forceinline__ void pack_block(const PackArgs &a, unsigned bx, unsig
                 if (!a.to) continue;
                 uint8_t *at = a.to + (r + u * step) * a.pitch + c * 2;
                 if constexpr (sizeof(T) == 2) {
-                    *reinterpret_cast<uint4 *>(at) = pack<T, 8>(f);
+                    const uint4 first = pack<T, 8>(f);
+                    *reinterpret_cast<uint4 *>(at) = first;
+                    if (SECOND && a.second) {
+                        float h[8];
+                        unpack<T, 8>(first, h);
+#pragma unroll
+                        for (int i = 0; i < 8; i++) f[i] = fabsf(h[i]) <= 3.4e38f ? f[i] - h[i] : 0.0f;
+                        *reinterpret_cast<uint4 *>(at + a.plane) = pack<T, 8>(f);
+                    }
                 } else {
 #pragma unroll
                     for (int p = 0; p < 3; p++) {
@@ -145,8 +161,9 @@ __device__ __forceinline__ void pack_block(const PackArgs &a, unsigned bx, unsig
 }
 
 // WIDE: of every job.  ONE: a single one, whose arguments need no index (32768 x 1024
-// with a slope: 34.5 us, 40 where they do).
-template <class T, bool WIDE, bool ONE>
+// with a slope: 34.5 us, 40 where they do).  SECOND: one has a second plane (with the
+// question asked at run time, those that have none took 41 us for 31).
+template <class T, bool WIDE, bool ONE, bool SECOND>
 __global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_constant__ PackJobs jobs)
 {
     __shared__ float sh[kPackWarps][256];
@@ -159,9 +176,9 @@ __global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_const
     const PackArgs &a = jobs.job[ONE ? 0 : j];
     const unsigned by = b / a.across, bx = b - by * a.across;
     if (WIDE || a.wide)
-        pack_block<T, true>(a, bx, by, sh);
+        pack_block<T, true, SECOND>(a, bx, by, sh);
     else
-        pack_block<T, false>(a, bx, by, sh);
+        pack_block<T, false, SECOND>(a, bx, by, sh);
 }
 
 // dbias: the chunks' sums, 32 columns a block, each of its warps a chunk in
@@ -430,18 +447,20 @@ size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 struct Laid {
     Rows in;
     unsigned rows, cols;
-    int dtype;
+    int dtype, planes;
     bool direct;
     size_t pitch, plane, bytes;     // of the layout in the workspace; bytes 0: direct
     size_t at = 0;
 };
-Laid lay(const Rows &in, unsigned rows, unsigned cols, int dtype, bool changed)
+// planes: of 16-bit rows that are changed on their way, 1 or 2.
+Laid lay(const Rows &in, unsigned rows, unsigned cols, int dtype, bool changed, int planes = 1)
 {
     Laid l{};
     l.in = in;
     l.rows = rows;
     l.cols = cols;
     l.dtype = dtype;
+    l.planes = dtype == RZ_F32 ? 3 : planes;
     l.direct = dtype != RZ_F32 && !changed && !in.HW && reinterpret_cast<uintptr_t>(in.v.p) % 16 == 0 &&
                (rows == 1 || in.v.pitch % 16 == 0);
     if (l.direct) {
@@ -450,11 +469,11 @@ Laid lay(const Rows &in, unsigned rows, unsigned cols, int dtype, bool changed)
     }
     l.pitch = up(cols, 8) * 2;
     l.plane = l.pitch * rows;
-    l.bytes = l.plane * (dtype == RZ_F32 ? 3 : 1);
+    l.bytes = l.plane * l.planes;
     return l;
 }
-// rows, terms: of the product; turned: the memory's rows are its terms.
-Operand operand(const Laid &l, const uint8_t *workspace, bool turned)
+// rows, terms: of the product; turned: the memory's rows are its terms; planes: the first so many.
+Operand operand(const Laid &l, const uint8_t *workspace, bool turned, int planes)
 {
     Operand o{};
     o.p = l.direct ? l.in.v.p : workspace + l.at;
@@ -462,7 +481,7 @@ Operand operand(const Laid &l, const uint8_t *workspace, bool turned)
     o.plane = l.plane;
     o.rows = turned ? l.cols : l.rows;
     o.terms = turned ? l.rows : l.cols;
-    o.planes = l.dtype == RZ_F32 ? 3 : 1;
+    o.planes = planes;
     o.turned = turned;
     o.bf16 = l.dtype != RZ_F16;
     return o;
@@ -487,10 +506,9 @@ struct Cut {
 // 16384 of bfloat16, where what is cut is a tenth and a hundredth of half a step.
 // Parts are several only where they are a few waves of tiles, so that their sums take
 // no more than 60 MB; else there is one, the size of the result.
-Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool through)
+Cut cut(unsigned M, unsigned N, unsigned terms, int dtype, int out_dtype, bool through, int products)
 {
     const long long chunks = (terms + 63) / 64;
-    const int products = dtype == RZ_F32 ? 6 : 1;
     const long long longest = dtype == RZ_F32 ? 8 : out_dtype == RZ_F32 ? 16 : dtype == RZ_F16 ? 128 : 256;
     Cut best{};
     double least = 0.0;
@@ -541,6 +559,7 @@ void add_job(PackJobs &jobs, const Laid &l, const Rows *slope, int act, float *s
     a.to = l.bytes ? workspace + l.at : nullptr;
     a.pitch = static_cast<long long>(l.pitch);
     a.plane = static_cast<long long>(l.plane);
+    a.second = l.planes == 2;
     a.sums = sums;
     a.M = l.rows;
     a.C = l.cols;
@@ -560,15 +579,22 @@ cudaError_t pack_launch(const PackJobs &jobs, int dtype, void *stream)
 {
     if (!jobs.count) return cudaSuccess;
     unsigned blocks = 0;
-    bool wide = true;
+    bool wide = true, second = false;
     for (int i = 0; i < jobs.count; i++) {
         blocks += jobs.job[i].blocks;
         wide = wide && jobs.job[i].wide;
+        second = second || jobs.job[i].second;
     }
     const auto of = [&](auto t) {
         using T = decltype(t);
-        if (!wide) return k_linear_pack<T, false, false>;
-        return jobs.count == 1 ? k_linear_pack<T, true, true> : k_linear_pack<T, true, false>;
+        const auto which = [&](auto s) {
+            constexpr bool S = decltype(s)::value;
+            if (!wide) return k_linear_pack<T, false, false, S>;
+            return jobs.count == 1 ? k_linear_pack<T, true, true, S> : k_linear_pack<T, true, false, S>;
+        };
+        if constexpr (sizeof(T) == 2)
+            if (second) return which(std::true_type{});
+        return which(std::false_type{});
     };
     const auto fn = dtype == RZ_F32 ? of(float{}) : dtype == RZ_BF16 ? of(__nv_bfloat16{}) : of(__half{});
     return launch(fn, dim3(blocks), kPackThreads, 0, stream, jobs);
@@ -721,7 +747,7 @@ Forward plan_forward(const rz_linear *d, const LinPlan &p, const rz_map *x, cons
     f.x = lay(rows_of(x, p.x), p.P, C, d->dtype, false);
     f.w = lay(rows_of(weight, weight_pitch), K, C, d->dtype, false);
     if (f.few) return f;
-    f.c = cut(p.P, K, C, d->dtype, d->dtype, !direct_out(f.out, d->dtype));
+    f.c = cut(p.P, K, C, d->dtype, d->dtype, !direct_out(f.out, d->dtype), products_of(f.x.planes, f.w.planes));
     f.w.at = up(f.x.bytes, 256);
     f.part = f.w.at + up(f.w.bytes, 256);
     f.total = f.part + f.c.bytes;
@@ -741,7 +767,8 @@ Backward plan_backward(const rz_linear *d, const LinPlan &p, const rz_map *dy, c
 {
     const unsigned C = static_cast<unsigned>(d->C), K = static_cast<unsigned>(d->K);
     Backward b{};
-    b.dz = lay(rows_of(dy, p.y), p.P, K, d->dtype, d->act != RZ_ACT_NONE);
+    const bool rounded = d->act != RZ_ACT_NONE;
+    b.dz = lay(rows_of(dy, p.y), p.P, K, d->dtype, rounded, rounded && dweight && dweight_dtype == RZ_F32 ? 2 : 1);
     if (!dx && !dweight) b.dz.bytes = 0;
     b.x = lay(rows_of(x, p.x), p.P, C, d->dtype, false);
     if (!dweight) b.x.bytes = 0;
@@ -749,11 +776,12 @@ Backward plan_backward(const rz_linear *d, const LinPlan &p, const rz_map *dy, c
     if (!dx) b.w.bytes = 0;
     if (dx) {
         b.dx = finish_of(rows_of(dx, p.x), p.P, C, d->dtype, nullptr, nullptr);
-        b.cx = cut(p.P, C, K, d->dtype, d->dtype, !direct_out(b.dx, d->dtype));
+        b.cx = cut(p.P, C, K, d->dtype, d->dtype, !direct_out(b.dx, d->dtype), products_of(b.w.planes, b.w.planes));
     }
     if (dweight) {
         b.dw = finish_of(rows_of(dweight, dweight_pitch), K, C, dweight_dtype, nullptr, nullptr);
-        b.cw = cut(K, C, p.P, d->dtype, dweight_dtype, !direct_out(b.dw, dweight_dtype));
+        b.cw = cut(K, C, p.P, d->dtype, dweight_dtype, !direct_out(b.dw, dweight_dtype),
+                   products_of(b.dz.planes, b.x.planes));
     }
     b.chunks = pack_chunks(p.P, K);
     b.x.at = up(b.dz.bytes, 256);
@@ -842,7 +870,7 @@ int map_linear(const rz_linear *d, const rz_map *x, const void *weight, size_t w
     for (const Laid *l : {&f.x, &f.w})
         if (l->bytes) add_job(jobs, *l, nullptr, 0, nullptr, pack_chunks(l->rows, l->cols), ws);
     if (const cudaError_t e = pack_launch(jobs, d->dtype, stream)) return lin_status(e);
-    return lin_status(product(operand(f.x, ws, false), operand(f.w, ws, false), f.out, d->dtype, f.c,
+    return lin_status(product(operand(f.x, ws, false, f.x.planes), operand(f.w, ws, false, f.w.planes), f.out, d->dtype, f.c,
                               reinterpret_cast<float *>(ws + f.part), status, stream));
 }
 
@@ -903,10 +931,10 @@ int map_linear_grad(const rz_linear *d, const rz_map *dy, const rz_map *x, const
     const Sums columns{sums, dbias, b.chunks, static_cast<unsigned>(d->K)};
     const bool with_w = dbias && dweight && b.cw.bytes, with_x = dbias && !with_w && dx && b.cx.bytes;
     if (dx && e == cudaSuccess)
-        e = product(operand(b.dz, ws, false), operand(b.w, ws, true), b.dx, d->dtype, b.cx, part, status, stream,
+        e = product(operand(b.dz, ws, false, b.w.planes), operand(b.w, ws, true, b.w.planes), b.dx, d->dtype, b.cx, part, status, stream,
                     with_x ? columns : Sums{});
     if (dweight && e == cudaSuccess)
-        e = product(operand(b.dz, ws, true), operand(b.x, ws, true), b.dw, dweight_dtype, b.cw, part, status, stream,
+        e = product(operand(b.dz, ws, true, b.dz.planes), operand(b.x, ws, true, b.x.planes), b.dw, dweight_dtype, b.cw, part, status, stream,
                     with_w ? columns : Sums{});
     if (dbias && !with_w && !with_x && e == cudaSuccess)
         e = maps::launch(k_linear_sums, dim3((columns.C + 31) / 32), 256, 0, stream, columns);

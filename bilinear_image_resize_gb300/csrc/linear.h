@@ -185,6 +185,9 @@ struct Product {
     int pair;               // two CTAs work on a tile of 256 rows, else one on 128
     int *status;
 };
+// Products of planes that an operand of `a` planes and one of `b` take: of three each
+// the six largest, of a second plane its own.
+inline int products_of(int a, int b) { return a == 3 && b == 3 ? 6 : a * b; }
 bool direct_out(const Finish &f, int dtype);
 cudaError_t launch_product(const Product &p, void *stream);
 

@@ -78,7 +78,7 @@ struct TcArgs {
     unsigned tiles_m, tiles_n, tiles;   // tiles: of all parts
     int tile_n, stages;
     int chunks, part, run;              // 64-term chunks, and of a part and of a run
-    int products;                       // of planes, 1 or 6
+    int products;                       // of planes, 1, 2 or 6
     unsigned group;                     // rows of tiles that are walked together
     int a_turned, b_turned;
     int a_merged, b_merged;             // a turned operand's rows come in one box
@@ -279,8 +279,9 @@ __device__ __forceinline__ Tile tile_at(const TcArgs &a, unsigned t)
 // The planes of the j-th product of planes, the smallest first.
 __device__ __forceinline__ void planes_of(int products, int j, int &a, int &b)
 {
-    if (products == 1) {
-        a = b = 0;
+    if (products <= 2) {
+        a = products == 2 && j == 0;
+        b = 0;
         return;
     }
     // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0); past the last, none
@@ -714,7 +715,7 @@ cudaError_t lin::launch_product(const Product &p, void *stream)
     a.tile_n = p.tile_n;
     a.tiles_m = (p.f.M + cg * kTileM - 1) / (cg * kTileM);
     a.tiles_n = (p.f.N + p.tile_n - 1) / p.tile_n;
-    a.products = p.a.planes == 1 ? 1 : 6;
+    a.products = products_of(p.a.planes, p.b.planes);
     // Tiles of a row next to each other read its A at once, and B out of L2 where that holds it (65536 x 1024 x 4096: 341 us,
     // rows of tiles in groups of eight 373).  A larger B is read once for eight rows of tiles (8192 x 8192 x 8192: 611 us, by
     // single rows 650).

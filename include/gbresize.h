@@ -581,8 +581,9 @@ RZ_API int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_ma
  * stream has passed it; up to eight pixels need none.  Maps and weights whose rows
  * begin and end at multiples of 16 bytes, evenly apart, are read and written where
  * they lie; others pass through the workspace.  It holds at most a copy of each
- * operand (6 bytes an element of float32, 2 of 16 bits) and, of the largest result, a
- * float32 matrix of its size or 64 MB, whatever the sums' length.  status: an int that the device can
+ * operand (6 bytes an element of float32, 2 of 16 bits; 4 of the gradient's dz where
+ * dweight is float32) and, of the largest result, a float32 matrix of its size or 64 MB,
+ * whatever the sums' length.  status: an int that the device can
  * write (its own memory or pinned host memory) or NULL; a kernel whose bounded waits
  * (1 s of its own time: what it spends preempted does not count) run out writes
  * RZ_ERR_TIMEOUT there and leaves the result unfinished.  Asynchronous on `stream`;
@@ -608,8 +609,10 @@ RZ_API int map_linear(const rz_linear *d, const rz_map *x, const void *weight, s
  * dweight_pitch bytes apart, dbias device float[K]; each may be NULL, is written,
  * not added to, and overlaps no input; an empty map makes dweight and dbias 0.
  * Sums run in a fixed order, in float32 (a float32 dweight of bfloat16 maps is off by
- * about 2.5e-6 of the sum of its terms' magnitudes, of float16 maps by 6e-6); dz of 16-bit maps enters dx and dweight as
- * a value of its type (rounded once where there is an activation), dbias as float32.
+ * about 2.5e-6 of the sum of its terms' magnitudes, of float16 maps by 6e-6).  dz of
+ * 16-bit maps with an activation enters dx, and a dweight of their type, as a value of
+ * that type (a float16 dz past 65504 is infinite); a float32 dweight as the sum of two,
+ * which takes half as long again; dbias as float32.
  * Workspace, status and the rest as map_linear.
  */
 RZ_API int map_linear_grad_workspace(const rz_linear *d, const rz_map *dy, const rz_map *x, const void *weight,

@@ -432,3 +432,41 @@ def test_float32_weight_gradients_are_as_good_as_stated(rz, positive, dtype, P, 
     again = torch.empty_like(dw)
     rz.map_linear_grad(dy, x, torch.zeros((K, C), dtype=t, device="cuda"), None, again)
     assert torch.equal(dw, again)
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype, left", [("bf16", 2.0 ** -16), ("f16", 2.0 ** -22)])
+@pytest.mark.parametrize("shape, K", [((2, 9, 15, 72), 136), ((1, 40, 50, 64), 128), ((1, 30, 70, 37), 51), ((1, 1, 5, 16), 24)])
+def test_float32_weight_gradients_see_dz_whole(rz, kind, dtype, left, shape, K):
+    """dz as the sum of two values of the type: half a step of the second is left of it (`left` of dz, and half a step of
+    float16's smallest), where a 16-bit dweight sees half a step of the first."""
+    C, P = shape[3], shape[0] * shape[1] * shape[2]
+    x, dy, pre = values(shape, dtype, 1), values((*shape[:3], K), dtype, 2), values((*shape[:3], K), dtype, 3, 1.5)
+    x, dy = np.abs(x), np.abs(dy)           # of one sign, so that nothing cancels
+    t = getattr(torch, tok.TORCH[dtype])
+    xv, dv, pv = (torch.from_numpy(a).to(t).cuda() for a in (x, dy, pre))
+    dx, dw, db = torch.empty_like(xv), torch.empty((K, C), device="cuda"), torch.empty(K, device="cuda")
+    w = values((K, C), dtype, 4, C ** -0.5)
+    wv = torch.from_numpy(w).to(t).cuda()
+    rz.map_linear_grad(dv, xv, wv, dx, dw, db, pre=pv, act=ACTS[kind])
+    want = tok.linear_grad(dy, x, w, pre, kind)
+    dz, xa = np.abs(want[3]).reshape(P, K), x.reshape(P, C)
+    slope = (dy * ref.slope_error(pre, 0, kind)).reshape(P, K) + 2.0 ** -24 * dz
+    bound = (slope + left * dz + (2.0 ** -25 if dtype == "f16" else 0.0)).T @ xa + held(P, dtype) * (dz.T @ xa)
+    check(dw, want[1], bound, "dweight")
+    # the same dx and dbias as beside a dweight of the type
+    other = [torch.empty_like(a) for a in (dx, wv, db)]
+    rz.map_linear_grad(dv, xv, wv, *other, pre=pv, act=ACTS[kind])
+    assert torch.equal(dx, other[0]) and torch.equal(db, other[2])
+
+
+@pytest.mark.parametrize("act", [1, 2])
+def test_float16_dz_past_its_range(rz, act):
+    """An infinite first value leaves no second one: the sum stays infinite."""
+    t = torch.float16
+    x, w = torch.ones((1, 1, 4, 8), dtype=t, device="cuda"), torch.ones((8, 8), dtype=t, device="cuda")
+    dy, pre = torch.ones((1, 1, 4, 8), dtype=t, device="cuda"), torch.full((1, 1, 4, 8), 2.0, dtype=t, device="cuda")
+    dy[0, 0, 1, 3] = 65000.0                                  # times a slope of 1.09
+    dw = torch.empty((8, 8), device="cuda")
+    rz.map_linear_grad(dy, x, w, None, dw, pre=pre, act=act)
+    assert bool(torch.isposinf(dw[3]).all()) and bool(torch.isfinite(dw[[0, 1, 2, 4, 5, 6, 7]]).all())

@@ -217,8 +217,8 @@ def test_binding_names():
                                           ((1 << 31) - 1, 8, 8), (100, 65536, 65536), (300, 1030, 8)])
 @pytest.mark.parametrize("dtype, wtype", [(1, 1), (2, 2), (2, 1), (3, 1)])
 def test_workspaces_stay_of_the_size_of_the_maps(lib, nat, pixels, C, K, dtype, wtype):
-    """Whatever the sum's length: the operands' layouts (6 bytes an element of float32, 2 of 16 bits, rows rounded to 16 bytes),
-    one float32 matrix of each result's size or 64 MB, and a row of sums for every few pixels."""
+    """Whatever the sum's length: the operands' layouts (6 bytes an element of float32, 2 of 16 bits, 4 of a dz for a float32 dweight,
+    rows rounded to 16 bytes), one float32 matrix of the largest result's size or 64 MB, and a row of sums for every few pixels."""
     es, ws = 4 if dtype == 1 else 2, 4 if wtype == 1 else 2
     d = nat.RzLinear(1, 1, pixels, C, K, dtype, 1)
     at = [1 << 48, 1 << 49, 1 << 50, 1 << 51, 1 << 52, 1 << 53]
@@ -230,7 +230,7 @@ def test_workspaces_stay_of_the_size_of_the_maps(lib, nat, pixels, C, K, dtype, 
     assert lib.map_linear_workspace(d, x, at[4], C * es, None, None, y, ctypes.byref(n)) == 0
     assert n.value <= laid * up(C) * (pixels + K) + max(4 * pixels * up(K), most) + 1024
     assert lib.map_linear_grad_workspace(d, y, x, at[4], C * es, pre, dx, at[5], C * ws, wtype, ctypes.byref(n)) == 0
-    operands = laid * (up(C) * (pixels + K) + up(K) * pixels)
+    operands = laid * (up(C) * (pixels + K)) + (4 if (dtype, wtype) in ((2, 1), (3, 1)) else laid) * up(K) * pixels
     assert n.value <= operands + max(4 * pixels * up(C), 4 * K * up(C), most) + 4 * K * 700 + 4096
     # towards the weight alone
     assert lib.map_linear_grad_workspace(d, y, x, at[4], C * es, pre, None, at[5], C * ws, wtype, ctypes.byref(n)) == 0
