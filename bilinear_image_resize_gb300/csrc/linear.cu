@@ -74,10 +74,12 @@ __device__ __forceinline__ void load8(const uint8_t *at, int left, Raw<T, 8> &r)
 }
 
 // The leading 8 bits of v, cut, so that what is left has its sign and no value
-// becomes infinite.
+// becomes infinite; 0 of one that is not finite.  Those go into the last plane whole,
+// which meets but the other operand's first: an infinity times a value is then the
+// infinity of its sign, where a lower plane of 0 would have made it NaN.
 __device__ __forceinline__ float leading(float v)
 {
-    return v != v ? v : __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+    return fabsf(v) <= 3.402823466e38f ? __uint_as_float(__float_as_uint(v) & 0xffff0000u) : 0.0f;
 }
 
 template <class T, bool WIDE, bool SECOND>
@@ -136,7 +138,7 @@ __device__ __forceinline__ void pack_block(const PackArgs &a, unsigned bx, unsig
                         float h[8];
 #pragma unroll
                         for (int i = 0; i < 8; i++) {
-                            h[i] = leading(f[i]);
+                            h[i] = p < 2 ? leading(f[i]) : f[i];    // (8 bits are left for the last)
                             f[i] -= h[i];
                         }
                         *reinterpret_cast<uint4 *>(at + p * a.plane) = pack<__nv_bfloat16, 8>(h);

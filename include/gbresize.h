@@ -568,9 +568,9 @@ RZ_API int resize_map_grad(const rz_resample *d, const rz_map *ddst, const rz_ma
  * 0: those of float32 maps are off by about 1e-6 of the sum of their terms'
  * magnitudes (3e-6 where a few terms are most of it); GELU of 16-bit maps by
  * (25 + 3 |z|) |z| / 2^26 before it is rounded, and below 0 by 3e-4 of itself where
- * that is less.  A value that is not finite
- * reaches the results of its own row or column alone; an infinity of float32 maps
- * may come out as NaN.
+ * that is less.  A value that is not finite reaches the results of its own row or
+ * column alone; of more than eight pixels of float32 maps, an infinity times another,
+ * or times less than 2^-133, is NaN.
  * y may be the residual itself, and overlaps no other map; weight and b lie
  * apart from y and pre.  K, C in [1, RZ_MAX_DIM], N * H * W < 2^31 (else
  * RZ_ERR_UNSUPPORTED).

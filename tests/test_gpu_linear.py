@@ -470,3 +470,35 @@ def test_float16_dz_past_its_range(rz, act):
     dw = torch.empty((8, 8), device="cuda")
     rz.map_linear_grad(dy, x, w, None, dw, pre=pre, act=act)
     assert bool(torch.isposinf(dw[3]).all()) and bool(torch.isfinite(dw[[0, 1, 2, 4, 5, 6, 7]]).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", [(1, 1, 3, 72), (1, 9, 17, 72)])
+def test_infinities_keep_their_sign(rz, dtype, shape):
+    """Of one infinity in a row the sums are infinite, of the sign of its product, however many rows there are; a zero's
+    product is NaN."""
+    K, P = 136, shape[1] * shape[2]
+    t = getattr(torch, tok.TORCH[dtype])
+    x, w = (torch.from_numpy(values(s, dtype, i)).to(t).cuda() for i, s in enumerate((shape, (K, 72))))
+    w[::3] = torch.sign(w[::3]) * 0.5                         # values whose lower bits are 0
+    w[5, 7] = 0.0
+    x[0, 0, 1, 7], x[0, 0, 2, 70] = float("inf"), -float("inf")
+    y = torch.empty((*shape[:3], K), dtype=t, device="cuda")
+    rz.map_linear(x, y, w)
+    want = x[0].double().cpu().view(P, 72) @ w.double().cpu().T
+    got = y.double().cpu().view(P, K)
+    assert bool(torch.isnan(want[1, 5])) and int(torch.isinf(want).sum()) == 2 * K - 1
+    finite = torch.isfinite(want)
+    assert torch.equal(torch.nan_to_num(got[~finite], nan=7.0), torch.nan_to_num(want[~finite], nan=7.0))
+    assert bool(torch.isfinite(got[finite]).all())
+    # backward: dy's infinity reaches its row of dx and its row of dweight alone
+    dy = torch.from_numpy(values((*shape[:3], K), dtype, 3)).to(t).cuda()
+    dy[0, 0, 2, 9] = -float("inf")
+    xb = torch.from_numpy(values(shape, dtype, 4)).to(t).cuda()
+    dx, dw, db = torch.empty_like(xb), torch.empty_like(w), torch.empty(K, device="cuda")
+    rz.map_linear_grad(dy, xb, w, dx, dw, db)
+    flat = dy.double().cpu().view(P, K)
+    for got, want in ((dx.view(P, 72), flat @ w.double().cpu()), (dw, flat.T @ xb.double().cpu().view(P, 72))):
+        got, odd = got.double().cpu(), ~torch.isfinite(want)
+        assert torch.equal(torch.nan_to_num(got[odd], nan=7.0), torch.nan_to_num(want[odd], nan=7.0)) and bool(torch.isfinite(got[~odd]).all())
+    assert float(db[9]) == -float("inf")
