@@ -502,3 +502,63 @@ def test_infinities_keep_their_sign(rz, dtype, shape):
         got, odd = got.double().cpu(), ~torch.isfinite(want)
         assert torch.equal(torch.nan_to_num(got[odd], nan=7.0), torch.nan_to_num(want[odd], nan=7.0)) and bool(torch.isfinite(got[~odd]).all())
     assert float(db[9]) == -float("inf")
+
+
+@pytest.mark.parametrize("pitch", [0, 2, 16, 1 << 12])
+@pytest.mark.parametrize("pixels", [5, 300])
+def test_weights_of_one_row_have_any_pitch(rz, pixels, pitch):
+    """By the C entry: the pitch of a single row leads nowhere."""
+    import ctypes
+
+    from bilinear_image_resize_gb300 import _native
+    lib, C = _native.load(), 64
+    x, dy = (torch.from_numpy(values((1, 1, pixels, n), "bf16", n)).bfloat16().cuda() for n in (C, 1))
+    w, y, dx = torch.from_numpy(values((1, C), "bf16", 3)).bfloat16().cuda(), torch.empty_like(dy), torch.empty_like(x)
+    dw, db = torch.full((1, C), 5.0, dtype=torch.bfloat16, device="cuda"), torch.empty(1, device="cuda")
+    d = _native.RzLinear(1, 1, pixels, C, 1, 2, 0)
+    m = lambda t: _native.RzMap(t.data_ptr(), pixels * t.shape[3] * 2, pixels * t.shape[3] * 2)      # noqa: E731
+    work = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    n = ctypes.c_size_t(0)
+    assert lib.map_linear_workspace(d, m(x), w.data_ptr(), pitch, None, None, m(y), ctypes.byref(n)) == 0 and n.value <= 1 << 24
+    assert lib.map_linear(d, m(x), w.data_ptr(), pitch, None, None, None, m(y), work.data_ptr(), 1 << 24, None, s) == 0
+    assert lib.map_linear_grad(d, m(dy), m(x), w.data_ptr(), pitch, None, m(dx), dw.data_ptr(), pitch, 2, db.data_ptr(), work.data_ptr(),
+                               1 << 24, None, s) == 0
+    torch.cuda.synchronize()
+    xa, wa, da = ref.host(x), ref.host(w), ref.host(dy)
+    check(y, tok.linear(xa, wa, None, "none")[0], tok.linear_bounds(xa, wa, None, "none", None, "bf16")[0], "y")
+    for got, want, bound in zip((dx, dw, db), tok.linear_grad(da, xa, wa, None, "none"),
+                                tok.linear_grad_bounds(da, xa, wa, None, "none", "bf16", "bf16")):
+        check(got, want, bound, "gradient")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("C, K, P", [(37, 40, 300), (321, 136, 400), (1, 64, 300), (63, 130, 513), (45, 1, 3000), (37, 40, 5)])
+def test_odd_weights_beside_values_that_are_not_finite(rz, dtype, C, K, P):
+    """Rows of odd widths, 16 bytes and more apart, read where they lie: nothing of what is between them is."""
+    x, w, dy = values((1, 1, P, C), dtype, 1), values((K, C), dtype, 2, C ** -0.5), values((1, 1, P, K), dtype, 3)
+    t = getattr(torch, tok.TORCH[dtype])
+    pad = (C + 7) // 8 * 8 + 8 - C
+    wv, _ = matrix(w, dtype, pad, 0, float("nan"))
+    xv, dv = (torch.from_numpy(a).to(t).cuda() for a in (x, dy))
+    y, dx, db = torch.empty_like(dv), torch.empty_like(xv), torch.empty(K, device="cuda")
+    gv, gflat = matrix(np.zeros((K, C)), dtype, pad, 0, -3.0)
+    rz.map_linear(xv, y, wv)
+    rz.map_linear_grad(dv, xv, wv, dx, gv, db)
+    check(y, tok.linear(x, w, None, "none")[0], tok.linear_bounds(x, w, None, "none", None, dtype)[0], "y")
+    for got, want, bound in zip((dx, gv, db), tok.linear_grad(dy, x, w, None, "none"),
+                                tok.linear_grad_bounds(dy, x, w, None, "none", dtype, dtype)):
+        check(got, want, bound, "gradient")
+    assert ref.outside_untouched(gflat, gv, -3.0)
+
+
+def test_first_call_on_a_given_stream(rz, monkeypatch):
+    """The binding's status word is made on any stream, the default's number among them."""
+    x, w = torch.ones((1, 4, 8, 16), device="cuda"), torch.ones((24, 16), device="cuda")
+    for stream in (0, torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        monkeypatch.setattr(rz, "_waits", {})
+        y = torch.empty((1, 4, 8, 24), device="cuda")
+        torch.cuda.synchronize()
+        rz.map_linear(x, y, w, stream=stream)
+        torch.cuda.synchronize()
+        assert 0 in rz._waits and bool((y == 16).all())

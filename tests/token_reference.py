@@ -21,7 +21,7 @@ def rounded(a, dtype):
 # summed so far, below the sum of magnitudes S: (n + 64) U S.  The tensor cores
 # round fewer times (once for sixteen terms), by up to 2 U where they cut.  float32
 # inputs as sums of three bfloat16 values take six passes, 6 n / 16 steps of 2 U,
-# and drop less than 4 U of S.
+# and drop less than 8 U of S.
 
 def sum_error(n, S):
     return (n + 64) * U * S
