@@ -759,7 +759,9 @@ def map_linear_grad(dy, x, weight, dx=None, dweight=None, dbias=None, pre=None, 
                     status=None, stream=None) -> None:
     """dx[:], dweight[:] and dbias[:] (each may be None) from dy, with the
     arguments of the map_linear call and the pre it wrote (None without an
-    activation).  dweight: (K, C), of the maps' dtype or float32."""
+    activation).  dweight: (K, C), of the maps' dtype, or float32, which sees dy
+    times the activation's slope whole where the others see it rounded to the
+    maps' dtype, and takes half as long again.  status: as in map_linear."""
     _with_torch()
     args = _linear_grad_args(dy, x, weight, dx, dweight, pre, act)
     _on_current_device(x, dy, weight, dx, dweight, dbias, pre)

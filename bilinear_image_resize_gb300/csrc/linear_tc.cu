@@ -28,11 +28,11 @@
 // The accumulator cuts what it adds (it does not round): a sum of n terms of one sign
 // ends up smaller by about n 2e-9 of its size, of float16 operands, whose products
 // have more bits to lose, by n 6e-9 (up to three times that where a few terms are most
-// of a sum).  So long sums are cut into runs, one after
-// another in the same CTA, each added to the tile's float32 sums as it leaves (TMA's
-// add, rounded): the sums of a tile lie in memory once, however long they are.  Only
-// where there are few tiles do several CTAs each take a part of a sum, with sums of
-// its own.  k_linear_join adds the parts up and finishes them.
+// of a sum).  So long sums are cut into runs, one after another in the same CTA, each
+// added to the tile's float32 sums as it leaves (TMA's add, rounded): the sums of a
+// tile lie in memory once, however long they are.  Only where there are few tiles do
+// several CTAs each take a part of a sum, with sums of its own.  k_linear_join adds the
+// parts up and finishes them.
 #include <cuda_runtime.h>
 
 #include <algorithm>
